@@ -25,9 +25,12 @@ Modules:
   eigen    -- the top-r eigenspace of a symmetric PSD metric (the basis V).
   svdquant -- the SVDQuant-style INT4 (group 64) W4A4 layer: quantiser, rank-r
               16-bit branch, residual, forward.
+  fp8      -- the 8-bit format with a scale for each block of 128, and the linear
+              layer on it, forward and backward.
+  norm     -- the gated norms around a transformer block, forward and backward.
 
 Every function here is pinned by tests under ``tests/test_oracle_*.py`` against
 closed forms, hand-derived vectors (``tests/golden/``), invariants and brute force.
 """
 
-from . import formats, hadamard, asp, smoothing, eigen, svdquant  # noqa: F401
+from . import formats, hadamard, asp, smoothing, eigen, svdquant, fp8, norm  # noqa: F401

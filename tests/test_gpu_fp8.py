@@ -1,0 +1,306 @@
+"""The 8-bit (block-128) quantisers, product and linear layer against the float64
+oracle, through the public Python layer and the C ABI.
+
+Gates (from the arithmetic):
+* codes and scales are bit-exact: S is a power of two and v / S is exact on both sides;
+* whole numbers whose sums stay below 2^24 (times one power of two) come out exact in
+  float32, whatever the order of the sums: any misplaced element, block or scale shows;
+* real data, float32 results: products are exact, and each of the K additions is off by
+  at most one unit of 2^-23 of the partial sum (rounded or truncated), so
+  |y - y64| <= K 2^-23 sum |a||b| + half a step of y's type;
+* bf16 results: beside that, a group of 8 products loses at most one unit of 2^-13 of
+  its largest for each of the others, 7 * 2^-13 max|a||b| <= 7 * 2^-13 * (sum over the
+  group), and a bound for y is 7 * 2^-13 of sum |a||b|; half a step of bf16 is added.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8 as O
+from wam_asp_w4a4_amd import binding as B
+from wam_asp_w4a4_amd.fp8 import Fp8Layer, Fp8Tensor, quantize
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def to_device(a, dtype="f32", ld=None):
+    """A float64 array as a device matrix of row stride ld, and its values as float64."""
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(TYPES[dtype])
+    if ld:
+        wide = torch.full((t.shape[0], ld), 77.0, dtype=t.dtype)
+        wide[:, :t.shape[1]] = t
+        return wide.to(DEV)[:, :t.shape[1]], t.double().numpy()
+    return t.to(DEV), t.double().numpy()
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+def check_codes(q, codes, bytes_):
+    np.testing.assert_array_equal(q.codes.cpu().numpy(), codes)
+    np.testing.assert_array_equal(q.scales.cpu().numpy(), O.layout_scales(bytes_))
+
+
+def data(rng, M, K):
+    """Magnitudes over 2^-30 .. 2^30, a block of zeros, and values at every border."""
+    v = rng.standard_normal((M, K)) * np.exp2(rng.integers(-30, 31, (M, -(-K // 128)))).repeat(128, 1)[:, :K]
+    v[-1, :min(K, 128)] = 0.0
+    special = [448.0, -17.0, 18.0, 19.0, 2.0 ** -10, -3 * 2.0 ** -10, -0.0, 2.0 ** -11]
+    v[0, :min(K, 8)] = special[:K]
+    if K > 8:
+        v[0, 8:128] = 0.25
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,ld", [(1, 1, None), (1, 128, None), (3, 127, None), (5, 129, 200),
+                                    (130, 640, None), (257, 1000, 1008), (64, 1001, 1001),
+                                    (300, 513, None)])
+def test_quantisers_are_bit_exact(M, K, ld, dtype):
+    print(f"quantise {M}x{K} ld={ld} {dtype}", flush=True)
+    x, v = to_device(data(np.random.default_rng(M + K), M, K), dtype, ld)
+    codes, s = O.quantize(v)
+    q = quantize(x)
+    check_codes(q, codes, s)
+    check_codes(quantize(x, transpose=True), *O.quantize(v.T))
+    layer = Fp8Layer.pack(x)
+    check_codes(layer, *O.quantize(v, square=True))
+    check_codes(Fp8Tensor(K, M, layer.codes_t, layer.scales_t), *O.quantize(v.T, square=True))
+    got = host(q.dequantize())
+    np.testing.assert_array_equal(got, O.values(codes, s, K))   # float32 holds every one here
+    np.testing.assert_array_equal(host(q.dequantize("bf16")), got)
+
+
+def test_values_without_a_code_and_extremes():
+    v = np.zeros((4, 256))
+    v[0, :4] = [np.nan, -np.inf, 3.0, np.inf]
+    v[1, :3] = [2.0 ** -149, -2.0 ** -126, 2.0 ** -130]
+    v[2, :2] = [3.4028234663852886e38, -1e30]
+    v[3, 128:] = np.nan
+    x, v = to_device(v)
+    q = quantize(x)
+    codes, s = O.quantize(v)
+    nan = np.isnan(v) | np.isinf(v)
+    got = q.codes.cpu().numpy()
+    assert ((got & 0x7F) == 0x7F)[nan].all()
+    np.testing.assert_array_equal(got[~nan], codes[~nan])
+    np.testing.assert_array_equal(q.scales.cpu().numpy(), O.layout_scales(s))
+    back = host(q.dequantize())
+    assert np.isnan(back[nan]).all()
+    np.testing.assert_array_equal(back[~nan], np.float32(O.values(codes, s, 256))[~nan])
+    # a row with a NaN or infinity spoils its own results only
+    w, _ = to_device(np.ones((20, 256)))
+    for rows in (4, 40):   # the few-row kernel and the tiles
+        y = Fp8Layer.pack(w).forward(torch.cat([x, torch.ones((rows - 4, 256), device=DEV)]))
+        assert torch.isnan(y[[0, 3]]).all() and torch.isfinite(y[1]).all()
+        assert torch.isfinite(y[4:]).all()
+
+
+# every kernel: few rows, 64-tiles whole and split, 128-tiles, 256-tiles
+SHAPES = [(1, 16, 1), (1, 33, 128), (5, 100, 129), (16, 4096, 1024), (16, 40, 4224), (17, 16, 640),
+          (33, 65, 127), (64, 64, 8192), (100, 130, 1537), (256, 1024, 1024), (777, 515, 300),
+          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product_of_whole_numbers_is_exact(M, N, K):
+    """|a|, |b| <= 4 times a power of two for each block: sums of K <= 8448 products stay
+    below 2^24 units of the smallest."""
+    print(f"product {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    nb = -(-K // 128)
+    ka = rng.integers(-2, 2, nb).repeat(128)[:K]
+
+    def matrix(rows):
+        return rng.integers(-4, 5, (rows, K))
+
+    a = matrix(M) * np.exp2(ka)
+    b = matrix(N) * np.exp2(-ka)        # so that every product is a whole number
+    x, _ = to_device(a, "bf16")
+    w, _ = to_device(b, "bf16")
+    bias = rng.integers(-50, 50, N)
+    xa = torch.from_numpy(a).to(DEV)
+    want = xa @ torch.from_numpy(b).to(DEV).t() + torch.from_numpy(bias).to(DEV).double()
+    layer = Fp8Layer.pack(w, torch.from_numpy(bias).float().to(DEV), backward=False)
+    y = layer.forward(x, "f32")
+    assert torch.equal(y.double(), want)
+    assert torch.equal(layer.forward(x, "bf16"), want.float().bfloat16())
+    assert torch.equal(layer.forward(quantize(x), "f32"), y)
+    assert torch.equal(Fp8Layer(N, K, layer.codes, layer.scales, None, None, None).forward(x, "f32").double(),
+                       want - torch.from_numpy(bias).to(DEV).double())
+
+
+@pytest.mark.parametrize("y_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,dtype,ld", [(1, 1030, 1024, "bf16", None), (7, 64, 1000, "f32", 1003),
+                                            (16, 256, 4096, "bf16", 4104), (200, 300, 2000, "f32", None),
+                                            (256, 1024, 4096, "bf16", None), (2000, 1700, 515, "bf16", 520)])
+def test_layer_against_the_oracle(M, N, K, dtype, ld, y_dtype):
+    print(f"layer {M}x{N}x{K} {dtype} -> {y_dtype}", flush=True)
+    rng = np.random.default_rng(K + M)
+    x, xv = to_device(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((1, K))), dtype, ld)
+    w, wv = to_device(rng.standard_normal((N, K)) / np.sqrt(K), dtype)
+    b = rng.standard_normal(N).astype(np.float32)
+    layer = Fp8Layer.pack(w, torch.from_numpy(b).to(DEV))
+    y = layer.forward(x, y_dtype)
+    qx, qw = O.held(xv), O.held(wv, square=True)
+    want = qx @ qw.T + b
+    half, window = (2.0 ** -8, 7 * 2.0 ** -13) if y_dtype == "bf16" else (2.0 ** -24, 0.0)
+    bound = (K * 2.0 ** -23 + window) * (np.abs(qx) @ np.abs(qw).T) + 2.0 ** -23 * np.abs(b)
+    assert (np.abs(host(y) - want) <= bound + half * (np.abs(want) + bound)).all()
+    # the row quantiser and the product in two calls: the same bits
+    assert torch.equal(layer.forward(quantize(x), y_dtype), y)
+    # and on every call, into the caller's buffers, whatever they held
+    out, ws = torch.full_like(y, 3.0), layer.workspace(M).fill_(255)
+    assert layer.forward(x, y_dtype, ws, out) is out and torch.equal(out, y)
+
+
+GRADS = [(1, 24, 16, "f32"), (130, 100, 200, "bf16"), (16, 1000, 33, "f32"), (300, 16, 130, "bf16"),
+         (257, 515, 640, "f32"), (1024, 256, 512, "bf16"), (2048, 2100, 1792, "bf16")]
+
+
+@pytest.mark.parametrize("M,N,K,dtype", GRADS)
+def test_gradients_against_the_oracle(M, N, K, dtype):
+    print(f"gradients {M}x{N}x{K} {dtype}", flush=True)
+    rng = np.random.default_rng(M + 2 * N + 3 * K)
+    x, xv = to_device(rng.standard_normal((M, K)) * 3, dtype, K + 8)
+    dy, dv = to_device(rng.standard_normal((M, N)) * 1e-3 * np.exp(rng.standard_normal((M, 1))), dtype, N + 3)
+    w, wv = to_device(rng.standard_normal((N, K)), dtype)
+    layer = Fp8Layer.pack(w, torch.zeros(N, device=DEV))
+    dx, dw, db = layer.backward(dy, x)
+    wx, ww, wb = O.backward(dv, xv, wv)
+    half, window = (2.0 ** -8, 7 * 2.0 ** -13) if dtype == "bf16" else (2.0 ** -24, 0.0)
+
+    def near(got, want, terms, mass, step):
+        bound = (terms * 2.0 ** -23 + (window if step > 1e-3 else 0.0)) * mass
+        assert (np.abs(host(got) - want) <= bound + step * (np.abs(want) + bound)).all()
+
+    near(dx, wx, N, np.abs(O.held(dv)) @ np.abs(O.held(wv, True)), half)
+    near(dw, ww, M, np.abs(O.held(dv.T)) @ np.abs(O.held(xv.T)).T, 2.0 ** -24)
+    near(db, wb, M, np.abs(dv).sum(axis=0), 2.0 ** -24)
+    assert dx.dtype == TYPES[dtype] and dw.dtype == db.dtype == torch.float32
+    # each alone is the same, and the ones that nobody asks for are absent
+    one = layer.backward(dy)
+    assert torch.equal(one[0], dx) and one[1] is None and torch.equal(one[2], db)
+    two = layer.backward(dy, x, need_dx=False, need_db=False, dw_dtype="bf16")
+    assert two[0] is None and two[2] is None and two[1].dtype == torch.bfloat16
+    near(two[1], ww, M, np.abs(O.held(dv.T)) @ np.abs(O.held(xv.T)).T * (1 + 7 * 2.0 ** -13 / (M * 2.0 ** -23)), 2.0 ** -8)
+    three = layer.backward(dy, need_dx=False, workspace=layer.workspace(M, backward=True).fill_(255))
+    assert three[0] is three[1] is None and torch.equal(three[2], db)
+
+
+def test_gradients_against_differences():
+    """Whole numbers: the layer is linear in them, so differences are exact."""
+    rng = np.random.default_rng(5)
+    M, N, K = 40, 70, 150
+    x, w, dy = (rng.integers(-4, 5, s).astype(float) for s in ((M, K), (N, K), (M, N)))
+    xt, wt, dt = (to_device(a)[0] for a in (x, w, dy))
+    layer = Fp8Layer.pack(wt)
+    dx, dw, _ = layer.backward(dt, xt)
+    d = rng.integers(-2, 3, x.shape)
+    dt_ = torch.from_numpy(d).float().to(DEV)
+    diff = (layer.forward(xt + dt_).double() - layer.forward(xt).double()) * dt.double()
+    assert diff.sum().item() == (dx.double() * dt_.double()).sum().item()
+    d = torch.from_numpy(rng.integers(-2, 3, w.shape)).float().to(DEV)
+    diff = (Fp8Layer.pack(wt + d).forward(xt).double() - layer.forward(xt).double()) * dt.double()
+    assert diff.sum().item() == (dw.double() * d.double()).sum().item()
+
+
+def test_empty_batches():
+    layer = Fp8Layer.pack(torch.ones((40, 200), device=DEV), torch.ones(40, device=DEV))
+    assert layer.forward(torch.empty((0, 200), device=DEV)).shape == (0, 40)
+    assert quantize(torch.empty((0, 200), device=DEV)).codes.shape == (0, 256)
+    dx, dw, db = layer.backward(torch.empty((0, 40), device=DEV), torch.empty((0, 200), device=DEV))
+    assert dx.shape == (0, 200) and not dw.any() and not db.any()
+
+
+def test_neighbouring_memory_is_untouched():
+    """Ragged outputs inside a larger buffer: nothing around them is written."""
+    for M, N, K in [(3, 19, 70), (70, 37, 200), (300, 261, 129)]:
+        print(f"neighbours {M}x{N}x{K}", flush=True)
+        layer = Fp8Layer.pack(torch.randn((N, K), device=DEV))
+        x = torch.randn((M, K), device=DEV)
+        buf = torch.full((M * N + 64,), 7.0, device=DEV)
+        y = layer.forward(x, y=buf[32:32 + M * N].view(M, N))   # 16-byte aligned, ragged rows
+        z = torch.full((M * N + 64,), 7.0, device=DEV)
+        layer.forward(x, y=z[3:3 + M * N].view(M, N))           # aligned to its elements only
+        assert torch.equal(z[3:3 + M * N].view(M, N), y)
+        assert (buf[:32] == 7).all() and (buf[32 + M * N:] == 7).all()
+        assert (z[:3] == 7).all() and (z[3 + M * N:] == 7).all()
+
+
+def test_captured_calls_replay_like_eager_ones():
+    layer = Fp8Layer.pack(torch.randn((512, 1024), device=DEV), torch.randn(512, device=DEV))
+    for M in (4, 256):
+        x, dy = torch.randn((M, 1024), device=DEV), torch.randn((M, 512), device=DEV)
+        ws, wb = layer.workspace(M), layer.workspace(M, backward=True)
+        y = torch.empty((M, 512), device=DEV)
+        layer.forward(x, workspace=ws, y=y)
+        layer.backward(dy, x, workspace=wb)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer.forward(x, workspace=ws, y=y)
+            grads = layer.backward(dy, x, workspace=wb)
+        for i in range(4):
+            x.copy_(torch.randn((M, 1024), device=DEV) * (i + 1))
+            dy.copy_(torch.randn((M, 512), device=DEV))
+            want_y, want = layer.forward(x), layer.backward(dy, x)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want_y)
+            assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+def test_calls_on_another_stream():
+    layer = Fp8Layer.pack(torch.randn((300, 700), device=DEV))
+    x = torch.randn((500, 700), device=DEV)
+    want = layer.forward(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [layer.forward(x, stream=side.cuda_stream) for _ in range(4)]
+    with torch.cuda.stream(side):
+        got.append(layer.forward(x))
+    side.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_the_c_calls_refuse_a_small_workspace():
+    layer = Fp8Layer.pack(torch.ones((64, 8192), device=DEV))
+    x = torch.ones((64, 8192), device=DEV)
+    need = B.asp_fp8_workspace_bytes(64, 64, 8192)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    y = torch.empty((64, 64), device=DEV)
+    with pytest.raises(B.ASPError) as ei:
+        B.asp_fp8_forward(x, 0, 8192, 64, 64, 8192, layer.codes, layer.scales, None, y, 0, ws, need - 1)
+    assert ei.value.status == 5
+
+
+def test_module_trains():
+    """Fp8Linear under autograd gives Fp8Layer.backward's gradients; frozen and trainable."""
+    from wam_asp_w4a4_amd.linear import Fp8Linear
+    lin = torch.nn.Linear(300, 130).to(DEV)
+    x = torch.randn((3, 40, 300), device=DEV, requires_grad=True)
+    dy = torch.randn((3, 40, 130), device=DEV)
+    layer = Fp8Layer.pack(lin.weight.detach(), lin.bias.detach())
+    want = layer.backward(dy.view(120, 130), x.detach().view(120, 300))
+    for trainable in (False, True):
+        m = Fp8Linear.from_linear(lin, trainable=trainable)
+        x.grad = lin.weight.grad = None
+        y = m(x)
+        assert torch.equal(y, layer.forward(x.detach().view(120, 300)).view(3, 40, 130))
+        y.backward(dy)
+        assert torch.equal(x.grad.view(120, 300), want[0])
+        if trainable:
+            assert torch.equal(lin.weight.grad, want[1]) and torch.equal(m.bias.grad, want[2])
+        with torch.no_grad():
+            assert torch.equal(m(x), y)
+    with pytest.raises(RuntimeError, match="capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            m(x)
+    torch.cuda.synchronize()
+    assert torch.equal(m(x), y)

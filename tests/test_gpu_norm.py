@@ -1,0 +1,352 @@
+"""The gated norms against the float64 oracle, forward and backward, through the
+public Python layer.
+
+Gates (from the arithmetic, u = 2^-24 the half step of float32):
+* a row's sum has at most 32 additions in a lane, 6 in a wave and 8 between waves one
+  after the other, so it is off by at most 46 u of the sum of magnitudes; with the few
+  roundings of each further step, a normed value v is off by 64 u (1 + |v| + r mean|h|):
+  r from the sum of squares, and for a layer norm the mean of the row.  Every later
+  factor and addition keeps that relative to the magnitudes that enter it;
+* h is rounded once to x's type (half a step); n is judged against the pre norm of the h
+  that the device stored, as it is defined, and rounded once to its own type;
+* column sums over M rows are off by M u of the sum of magnitudes, beside what enters.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8 as OF
+from oracle import norm as O
+from wam_asp_w4a4_amd import binding as B
+from wam_asp_w4a4_amd.fp8 import Fp8Layer, Fp8Tensor, quantize
+from wam_asp_w4a4_amd.norm import GatedNorm, gated_norm, gated_norm_backward
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+EPS = 1e-6
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def near(got, want, bound, half, live=None):
+    bound = np.broadcast_to(bound, want.shape)
+    off = np.abs(got - want) - (bound + half * (np.abs(want) + bound))
+    if live is not None:
+        off = off[live]
+    assert not off.size or off.max() <= 0, off.max()
+
+
+class Case:
+    def __init__(self, M, C, dtype, post, pre, tables, offsets, affine=True, alpha=0.7, ld=0):
+        g = torch.Generator(device=DEV).manual_seed(M * 131 + C)
+        rnd = lambda *s: torch.randn(s, generator=g, device=DEV)
+        t = TYPES[dtype]
+        self.M, self.C, self.dtype, self.t = M, C, dtype, t
+        self.seq = O.sequences(M, offsets)
+        self.live = self.seq >= 0
+        self.G = 1 if offsets is None else len(offsets) - 1
+        wide = lambda: torch.empty((M, C + ld), dtype=t, device=DEV)[:, :C].copy_(rnd(M, C) * 2 + 0.5)
+        self.x, self.y, self.dh, self.dn = wide(), wide(), wide(), wide()
+        table = rnd(self.G, 3, C) * 0.5
+        self.kw = dict(alpha=alpha, post=post, pre=pre, eps=EPS,
+                       post_weight=1 + 0.2 * rnd(C) if post != "none" else None,
+                       gate=table[:, 0] if tables else None,
+                       scale=table[:, 1] if tables and pre != "none" else None,
+                       shift=table[:, 2] if tables and pre != "none" else None,
+                       weight=1 + 0.2 * rnd(C) if affine and pre != "none" else None,
+                       bias=rnd(C) if affine and pre != "none" else None,
+                       offsets=None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device=DEV))
+
+    def host(self, name):
+        return host(self.kw[name])
+
+    def check_forward(self, h, n):
+        k, live = self.kw, self.live
+        x, y = host(self.x), host(self.y)
+        gate = np.abs(O._rows(k["gate"].double().cpu().numpy(), self.seq)) if k["gate"] is not None else 1.0
+        want = O.stream(x, y, self.seq, k["alpha"], k["post"], self.host("post_weight"), self.host("gate"), EPS)
+        q, r = (y, 1.0) if k["post"] == "none" else O.normed(y, k["post"], EPS)
+        pw = 1.0 if k["post_weight"] is None else np.abs(self.host("post_weight"))
+        bound = U * (4 * np.abs(k["alpha"] * x) + gate * pw * (8 * np.abs(q) if k["post"] == "none" else
+                     64 * (1 + np.abs(q) + r * np.abs(y).mean(axis=1, keepdims=True))))
+        got = host(h)
+        near(got, want, bound, HALF[self.dtype], live)
+        if n is None:
+            return
+        v, r = O.normed(got, k["pre"], EPS)
+        want = O.prenorm(got, self.seq, k["pre"], self.host("weight"), self.host("bias"), self.host("scale"),
+                         self.host("shift"), EPS)
+        w = 1.0 if k["weight"] is None else np.abs(self.host("weight"))
+        b = 0.0 if k["bias"] is None else np.abs(self.host("bias"))
+        m = 1.0 + (np.abs(O._rows(self.host("scale"), self.seq)) if k["scale"] is not None else 0.0)
+        s = np.abs(O._rows(self.host("shift"), self.seq)) if k["shift"] is not None else 0.0
+        bound = U * (64 * (1 + np.abs(v) + r * np.abs(got).mean(axis=1, keepdims=True)) * w * m + 8 * (b * m + s))
+        near(host(n), want, bound, HALF["bf16" if n.dtype == torch.bfloat16 else "f32"], live)
+
+
+SEQ = [0, 5, 5, 6, 29]            # an empty sequence, one of one row, padding behind
+SIZES = [(1, 1), (3, 7), (40, 128), (33, 512), (40, 1000), (33, 1024), (33, 1001), (30, 2048), (31, 4096),
+         (30, 5000), (30, 9001), (30, 16384)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,C", SIZES)
+def test_forward_sizes(M, C, dtype):
+    print(f"norm {M}x{C} {dtype}", flush=True)
+    c = Case(M, C, dtype, "rms", "layer", True, SEQ if M >= 30 else None)
+    h, n = gated_norm(c.x, c.y, **c.kw)
+    assert n.dtype == c.t
+    c.check_forward(h, n)
+    again = gated_norm(c.x, c.y, **c.kw)
+    live = torch.from_numpy(c.live).to(DEV)
+    assert torch.equal(again[0][live], h[live]) and torch.equal(again[1][live], n[live])
+
+
+@pytest.mark.parametrize("tables", [False, True])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+def test_forward_kinds(pre, post, tables):
+    for offsets, ld, affine, out in ((None, 0, True, None), (SEQ, 13, False, "f32"), ([2, 8, 20], 8, True, "bf16")):
+        c = Case(32, 328, "bf16", post, pre, tables, offsets, affine, ld=ld)
+        h, n = gated_norm(c.x, c.y, out=None if pre == "none" else out, **c.kw)
+        assert (n is None) == (pre == "none")
+        c.check_forward(h, n)
+
+
+def test_rows_of_no_sequence_are_left_and_buffers_are_used():
+    c = Case(40, 300, "bf16", "rms", "rms", True, [3, 9, 9, 30], ld=4)
+    h, n = torch.full_like(c.x, 5.0), torch.full((40, 320), 6.0, device=DEV)
+    got = gated_norm(c.x, c.y, h=h, n=n[:, :300], **c.kw)
+    assert got[0] is h
+    c.check_forward(h, got[1])
+    dead = torch.from_numpy(~c.live).to(DEV)
+    assert (h[dead] == 5).all() and (n[dead] == 6).all() and (n[:, 300:] == 6).all()
+    # padding may hold anything
+    c.x[dead], c.y[dead] = float("nan"), float("inf")
+    again = gated_norm(c.x, c.y, out="f32", **c.kw)
+    assert torch.equal(again[0][~dead], h[~dead]) and torch.equal(again[1][~dead], n[:, :300][~dead])
+    # h in place of x, and of y
+    for name in ("x", "y"):
+        x, y = c.x.clone(), c.y.clone()
+        out = {"x": x, "y": y}[name]
+        gated_norm(x, y, h=out, **c.kw)
+        assert torch.equal(out[~dead], h[~dead])
+
+
+def test_special_values():
+    c = Case(8, 256, "f32", "layer", "rms", False, None)
+    x, y = c.x.clone(), c.y.clone()
+    x[1], y[1] = 0.0, 0.0                       # an empty row: 0 / sqrt(eps)
+    y[2] = 3.0                                  # a constant row: its layer norm is 0
+    y[3, 7], x[4, 9] = float("nan"), float("inf")
+    h, n = gated_norm(x, y, alpha=1.0, post="layer", pre="rms")
+    assert not h[1].any() and not n[1].any() and torch.equal(h[2], x[2])
+    assert torch.isnan(n[[3, 4]]).any(dim=1).all()
+    assert torch.isfinite(n[[0, 1, 2, 5, 6, 7]]).all()
+    # a mean far above the deviation: no difference of large squares
+    big = torch.randn((4, 1024), device=DEV) + 4096.0
+    _, n = gated_norm(big, pre="layer")
+    near(host(n), O.normed(host(big), "layer", EPS)[0], 64 * U * 4100, U)
+
+
+@pytest.mark.parametrize("M,C", [(1, 1), (9, 100), (40, 128), (33, 640), (30, 1001), (40, 1536), (30, 5000)])
+def test_eight_bit_result(M, C):
+    """The codes are those of the row quantiser for the float32 n, bit for bit."""
+    print(f"eight bit {M}x{C}", flush=True)
+    c = Case(M, C, "bf16", "none", "layer", True, SEQ if M >= 30 else None)
+    _, n = gated_norm(c.x, c.y, out="f32", **c.kw)
+    h, q = gated_norm(c.x, c.y, out="fp8", **c.kw)
+    live = torch.from_numpy(c.live).to(DEV)
+    want = quantize(n)
+    assert torch.equal(q.codes[live], want.codes[live]) and torch.equal(q.scales[:, live], want.scales[:, live])
+    # into the caller's tensor: rows of no sequence keep their codes
+    mine = Fp8Tensor.empty(M, C, DEV)
+    mine.codes.fill_(9), mine.scales.fill_(8)
+    gated_norm(c.x, c.y, n=mine, **c.kw)
+    assert torch.equal(mine.codes[live], want.codes[live])
+    assert (mine.codes[~live] == 9).all() and (mine.scales[:, ~live] == 8).all()
+
+
+@pytest.mark.parametrize("M", [3, 200])
+def test_block_end_to_next_projection(M):
+    """A run as it is used: norms, 8-bit codes, the linear layer that reads them."""
+    C, N = 640, 300
+    c = Case(M, C, "bf16", "rms", "layer", True, None)
+    w = torch.randn((N, C), device=DEV) / C ** 0.5
+    layer = Fp8Layer.pack(w, torch.randn(N, device=DEV))
+    h, q = gated_norm(c.x, c.y, out="fp8", **c.kw)
+    y = layer.forward(q, "f32")
+    qv, wv = host(q.dequantize()), OF.held(host(w), square=True)
+    near(host(y), qv @ wv.T + host(layer.bias), C * 2 * U * (np.abs(qv) @ np.abs(wv).T + 1), U)
+    # against the unquantised n: half a step of E4M3 for each element
+    _, n = gated_norm(c.x, c.y, out="f32", **c.kw)
+    nv = host(n)
+    step = np.maximum(np.abs(nv) / 16, np.abs(nv).max() / 448 / 512)
+    assert (np.abs(host(y) - (nv @ wv.T + host(layer.bias))) <= step @ np.abs(wv).T + 1e-4).all()
+
+
+BACK = [(1, 1, "f32"), (5, 7, "f32"), (40, 128, "bf16"), (33, 512, "f32"), (70, 1000, "bf16"), (33, 1001, "f32"),
+        (30, 2048, "bf16"), (31, 4096, "bf16"), (30, 5000, "f32"), (30, 9001, "bf16"), (30, 16384, "bf16"),
+        (5000, 64, "f32"), (1500, 1100, "bf16")]
+
+
+def check_backward(c, y=True, dh=True):
+    k, C, M = c.kw, c.C, c.M
+    yt, dht = (c.y if y else None), (c.dh if dh else None)
+    dx0, dy0 = torch.full_like(c.x, 5.0), torch.full_like(c.x, 6.0) if y else None
+    dn = c.dn if k["pre"] != "none" else None
+    got = gated_norm_backward(dht, dn, c.x, yt, dx=dx0, dy=dy0, **k)
+    want = O.backward(host(dht), host(dn), host(c.x), host(yt), c.seq, c.G, k["alpha"], k["post"], c.host("post_weight"),
+                      c.host("gate"), k["pre"], c.host("weight"), c.host("bias"), c.host("scale"), EPS)
+    # magnitudes: of the gradient that reaches h through the pre norm, and onwards to y
+    h, d, e = host(c.x), host(dn), np.zeros((M, C)) if dht is None else np.abs(host(dht))
+    live = c.live
+    sums = {}
+    if dn is not None:
+        v, r = O.normed(h, k["pre"], EPS)
+        w = 1.0 if k["weight"] is None else np.abs(c.host("weight"))
+        m = 1.0 + (np.abs(O._rows(c.host("scale"), c.seq)) if k["scale"] is not None else 0.0)
+        g = np.abs(d) * w * m
+        spread = 1 + np.abs(v) + r * np.abs(h).mean(axis=1, keepdims=True)
+        mean = lambda a: a.mean(axis=1, keepdims=True)
+        e = e + r * (g + mean(g) + spread * mean(g * spread))
+        b = 0.0 if k["bias"] is None else np.abs(c.host("bias"))
+        sums["scale"], sums["shift"] = np.abs(d) * (spread * w + b), np.abs(d)
+        sums["weight"], sums["bias"] = np.abs(d) * m * spread, np.abs(d) * m
+    rows = 256 * U   # three row sums one after the other
+    near(host(got.dx), want["dx"], abs(k["alpha"]) * rows * e, HALF[c.dtype], live)
+    assert (got.dx[torch.from_numpy(~live).to(DEV)] == 5).all()
+    if y:
+        q, r = (np.abs(host(c.y)), 1.0) if k["post"] == "none" else O.normed(host(c.y), k["post"], EPS)
+        spread = np.abs(q) if k["post"] == "none" else 1 + np.abs(q) + r * np.abs(host(c.y)).mean(axis=1, keepdims=True)
+        gt = 1.0 if k["gate"] is None else np.abs(O._rows(c.host("gate"), c.seq))
+        pw = 1.0 if k["post_weight"] is None else np.abs(c.host("post_weight"))
+        sums["gate"], sums["post_weight"] = e * spread * pw, e * spread * gt
+        f = e * gt * pw
+        if k["post"] != "none":
+            f = r * (f + f.mean(axis=1, keepdims=True) + spread * (f * spread).mean(axis=1, keepdims=True))
+        near(host(got.dy), want["dy"], 3 * rows * f, HALF[c.dtype], live)
+        assert (got.dy[torch.from_numpy(~live).to(DEV)] == 6).all()
+    for name, mass in sums.items():
+        t = getattr(got, name)
+        if t is None:
+            assert k[name] is None
+            continue
+        assert t.dtype == torch.float32 and t.shape == k[name].shape
+        by = np.zeros((c.G, C))
+        np.add.at(by, c.seq[live], np.broadcast_to(mass, (M, C))[live])
+        bound = (rows * 3 + (M + 16) * U) * (by if t.dim() == 2 else by.sum(axis=0))
+        near(host(t), want[name], bound, U)
+    return got
+
+
+@pytest.mark.parametrize("M,C,dtype", BACK)
+def test_backward_sizes(M, C, dtype):
+    print(f"norm backward {M}x{C} {dtype}", flush=True)
+    c = Case(M, C, dtype, "layer", "rms", True, SEQ if M >= 30 else None)
+    first = check_backward(c)
+    again = gated_norm_backward(c.dh, c.dn, c.x, c.y, **c.kw)
+    assert all(torch.equal(a, b) for a, b in zip(first[2:], again[2:]))
+
+
+@pytest.mark.parametrize("tables", [False, True])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+def test_backward_kinds(pre, post, tables):
+    for offsets, ld, affine in ((None, 0, True), (SEQ, 13, False), ([2, 8, 20], 8, True)):
+        check_backward(Case(32, 328, "bf16", post, pre, tables, offsets, affine, ld=ld))
+    if pre != "none":
+        c = Case(32, 328, "f32", post, pre, tables, SEQ)
+        check_backward(c, dh=False)
+        c.dn = c.dn.bfloat16()
+        check_backward(c)
+        if post == "none" and not tables:
+            check_backward(c, y=False)
+
+
+def test_backward_against_differences():
+    """float32 differences over a step of 2^-6: off by its square times the third
+    derivative (below 1 in these units) and by 2^-24 of the loss's terms over the step."""
+    c = Case(24, 96, "f32", "rms", "layer", True, [0, 7, 7, 20])
+    live = torch.from_numpy(c.live).to(DEV)[:, None].double()
+
+    def loss(x, y, **over):
+        h, n = gated_norm(x, y, **{**c.kw, **over})
+        return ((h.double() * c.dh.double() + n.double() * c.dn.double()).nan_to_num() * live).sum().item()
+
+    h, _ = gated_norm(c.x, c.y, **c.kw)
+    g = gated_norm_backward(c.dh, c.dn, h, c.y, **c.kw)
+    step = 2.0 ** -6
+    for name in ("x", "y", "gate", "scale", "shift", "weight", "bias", "post_weight"):
+        v = {"x": c.x, "y": c.y}.get(name, c.kw.get(name))
+        grad = {"x": g.dx, "y": g.dy}.get(name)
+        grad = getattr(g, name) if grad is None else grad
+        d = torch.randn_like(v).contiguous()
+        if name in ("x", "y"):
+            d = d * live.float()
+            ends = [loss(*((v + s * step * d, c.y) if name == "x" else (c.x, v + s * step * d))) for s in (1, -1)]
+        else:
+            table = lambda s: torch.stack([v + s * step * d] * 3, 1)[:, 0] if v.dim() == 2 else v + s * step * d
+            ends = [loss(c.x, c.y, **{name: table(s)}) for s in (1, -1)]
+        diff = (ends[0] - ends[1]) / (2 * step)
+        want = ((grad * live.float() if name in ("x", "y") else grad).double() * d.double()).sum().item()
+        mass = (c.dn.abs().double() * live).sum().item()
+        assert abs(diff - want) <= mass * (step ** 2 + 2.0 ** -24 * 64 / step), (name, diff, want)
+
+
+def test_no_rows():
+    x = torch.empty((0, 64), device=DEV)
+    h, n = gated_norm(x, x, weight=torch.ones(64, device=DEV))
+    assert h.shape == n.shape == (0, 64)
+    g = gated_norm_backward(x, x, x, x, weight=torch.ones(64, device=DEV))
+    assert not g.weight.any()
+
+
+def test_captured_calls_replay_like_eager_ones():
+    c = Case(64, 1024, "bf16", "rms", "layer", True, [0, 20, 20, 60])
+    live = torch.from_numpy(c.live).to(DEV)
+    ws = torch.empty(B.asp_norm_gate_backward_workspace_bytes(64, 1024, 3), dtype=torch.uint8, device=DEV)
+    run = lambda: (*gated_norm(c.x, c.y, **c.kw), gated_norm_backward(c.dh, c.dn, c.x, c.y, workspace=ws, **c.kw))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, n, g = run()
+    for i in range(4):
+        for t in (c.x, c.y, c.dh, c.dn):
+            t.copy_(torch.randn_like(t) * (i + 1))
+        c.kw["offsets"].copy_(torch.tensor([0, 20 - i, 20 + i, 60], dtype=torch.int32))
+        wh, wn, wg = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h[live], wh[live]) and torch.equal(n[live], wn[live])
+        assert torch.equal(g.dx[live], wg.dx[live]) and torch.equal(g.dy[live], wg.dy[live])
+        assert all(torch.equal(a, b) for a, b in zip(g[2:], wg[2:]))
+
+
+def test_module_trains():
+    """GatedNorm under autograd gives gated_norm_backward's gradients."""
+    m = GatedNorm(160, post="rms", pre="layer").to(DEV)
+    with torch.no_grad():
+        for p in m.parameters():
+            p.add_(torch.randn_like(p) * 0.1)
+    x = torch.randn((2, 5, 160), device=DEV, requires_grad=True)
+    y = torch.randn((2, 5, 160), device=DEV, requires_grad=True)
+    gate = torch.randn((2, 160), device=DEV, requires_grad=True)
+    off = torch.tensor([0, 5, 10], dtype=torch.int32, device=DEV)
+    h, n = m(x, y, gate=gate, offsets=off)
+    dh, dn = torch.randn_like(h), torch.randn_like(n)
+    torch.autograd.backward([h, n], [dh, dn])
+    g = gated_norm_backward(dh.view(10, 160), dn.view(10, 160), h.detach().view(10, 160), y.detach().view(10, 160),
+                            post="rms", pre="layer", post_weight=m.post_weight.detach(), gate=gate.detach(),
+                            weight=m.weight.detach(), bias=m.bias.detach(), offsets=off)
+    assert torch.equal(x.grad.view(10, 160), g.dx) and torch.equal(y.grad.view(10, 160), g.dy)
+    assert torch.equal(gate.grad, g.gate) and torch.equal(m.weight.grad, g.weight)
+    assert torch.equal(m.bias.grad, g.bias) and torch.equal(m.post_weight.grad, g.post_weight)

@@ -22,11 +22,14 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasp.so")
 
 ASP_F32 = 0
 ASP_BF16 = 1
+ASP_E4M3 = 2          # asp_norm_gate's n in the 8-bit format
+ASP_NORM_NONE, ASP_NORM_RMS, ASP_NORM_LAYER = 0, 1, 2
 DTYPES = {"f32": ASP_F32, "bf16": ASP_BF16}
 
 # name -> (restype, argtypes); mirrors include/asp.h
 _i32, _i64, _sz, _p = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 _psz = ctypes.POINTER(ctypes.c_size_t)
+_f32 = ctypes.c_float
 SIGNATURES = {
     "asp_abi_version": (_i32, []),
     "asp_source_digest": (ctypes.c_char_p, []),
@@ -70,6 +73,26 @@ SIGNATURES = {
                                  _i32, _p, _p, _p]),
     "asp_forward_group_stages": (_i32, [_i32, _i32, _p, _i32, _i64, _i64, _i32, _p, _p, _p, _p,
                                         _p, _p, _p, _i32, _p, _p, _p]),
+    "asp_fp8_sizes": (_i32, [_i64, _i64, _psz, _psz]),
+    "asp_fp8_quantize": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
+    "asp_fp8_quantize_t": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
+    "asp_fp8_quantize_weight": (_i32, [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p]),
+    "asp_fp8_dequantize": (_i32, [_p, _p, _i64, _i64, _p, _i32, _p]),
+    "asp_fp8_gemm_workspace_bytes": (_i32, [_i64, _i64, _i64, _psz]),
+    "asp_fp8_gemm": (_i32, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _i32, _p, _sz, _p]),
+    "asp_fp8_workspace_bytes": (_i32, [_i64, _i64, _i64, _psz]),
+    "asp_fp8_forward": (_i32, [_p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i32, _p, _sz,
+                               _p]),
+    "asp_fp8_backward_workspace_bytes": (_i32, [_i64, _i64, _i64, _psz]),
+    "asp_fp8_backward": (_i32, [_p, _i32, _i64, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _i32,
+                                _p, _i32, _p, _p, _sz, _p]),
+    "asp_norm_gate": (_i32, [_p, _i64, _p, _i64, _i32, _i64, _i64, _f32, _i32, _p, _p, _i32, _p,
+                             _p, _p, _p, _i64, _i32, _p, _f32, _p, _i64, _p, _i32, _i64, _p, _p]),
+    "asp_norm_gate_backward_workspace_bytes": (_i32, [_i64, _i64, _i32, _psz]),
+    "asp_norm_gate_backward": (_i32, [_p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i32, _i64,
+                                      _i64, _f32, _i32, _p, _p, _i32, _p, _p, _p, _i64, _i32, _p,
+                                      _f32, _p, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p,
+                                      _sz, _p]),
 }
 
 _lib = None
@@ -377,3 +400,107 @@ def asp_forward(x, x_dtype, M, N, K, r, prep_pack, w_codes, w_scales, wv, bias, 
     _check(lib().asp_forward(_ptr(x), x_dtype, M, N, K, r, _ptr(prep_pack), _ptr(w_codes),
                              _ptr(w_scales), _ptr(wv), _ptr(bias), _ptr(y), y_dtype,
                              _ptr(workspace), workspace_bytes, _stream(stream, y)))
+
+
+# ------------------------------------------- 8-bit linear layer, gated norms
+#
+# Matrices and tables that the C entry points take with a row stride may be
+# strided tensors here (their rows contiguous); the stride is an argument.
+
+
+def _at(a):
+    """The address of a tensor of any strides (None: NULL)."""
+    return None if a is None else a.data_ptr()
+
+
+def _size(fn, *args):
+    out = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(out)))
+    return out.value
+
+
+def asp_fp8_sizes(rows, cols):
+    """(code bytes, scale bytes) of a rows x cols matrix in the 8-bit format."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().asp_fp8_sizes(rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def asp_fp8_quantize(inp, dtype, rows, cols, ld, codes, scales, stream=None):
+    _check(lib().asp_fp8_quantize(_at(inp), dtype, rows, cols, ld, _ptr(codes), _ptr(scales),
+                                  _stream(stream, inp)))
+
+
+def asp_fp8_quantize_t(inp, dtype, rows, cols, ld, codes_t, scales_t, stream=None):
+    _check(lib().asp_fp8_quantize_t(_at(inp), dtype, rows, cols, ld, _ptr(codes_t),
+                                    _ptr(scales_t), _stream(stream, inp)))
+
+
+def asp_fp8_quantize_weight(w, dtype, N, K, ld, codes, scales, codes_t=None, scales_t=None,
+                            stream=None):
+    _check(lib().asp_fp8_quantize_weight(_at(w), dtype, N, K, ld, _ptr(codes), _ptr(scales),
+                                         _ptr(codes_t), _ptr(scales_t), _stream(stream, w)))
+
+
+def asp_fp8_dequantize(codes, scales, rows, cols, out, dtype, stream=None):
+    _check(lib().asp_fp8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), dtype,
+                                    _stream(stream, out)))
+
+
+def asp_fp8_gemm_workspace_bytes(M, N, K) -> int:
+    return _size(lib().asp_fp8_gemm_workspace_bytes, M, N, K)
+
+
+def asp_fp8_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, bias, y, y_dtype, workspace=None,
+                 workspace_bytes=0, stream=None):
+    _check(lib().asp_fp8_gemm(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N,
+                              K, _ptr(bias), _ptr(y), y_dtype, _ptr(workspace), workspace_bytes,
+                              _stream(stream, y)))
+
+
+def asp_fp8_workspace_bytes(M, N, K) -> int:
+    return _size(lib().asp_fp8_workspace_bytes, M, N, K)
+
+
+def asp_fp8_forward(x, x_dtype, ldx, M, N, K, w_codes, w_scales, bias, y, y_dtype,
+                    workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().asp_fp8_forward(_at(x), x_dtype, ldx, M, N, K, _ptr(w_codes), _ptr(w_scales),
+                                 _ptr(bias), _ptr(y), y_dtype, _ptr(workspace), workspace_bytes,
+                                 _stream(stream, y)))
+
+
+def asp_fp8_backward_workspace_bytes(M, N, K) -> int:
+    return _size(lib().asp_fp8_backward_workspace_bytes, M, N, K)
+
+
+def asp_fp8_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, M, N, K, wt_codes, wt_scales, dx,
+                     dx_dtype, dw, dw_dtype, db, workspace, workspace_bytes, stream=None):
+    _check(lib().asp_fp8_backward(_at(dy), dy_dtype, lddy, _at(x), x_dtype, ldx, M, N, K,
+                                  _ptr(wt_codes), _ptr(wt_scales), _ptr(dx), dx_dtype, _ptr(dw),
+                                  dw_dtype, _ptr(db), _ptr(workspace), workspace_bytes,
+                                  _stream(stream, dy)))
+
+
+def asp_norm_gate(x, ldx, y, ldy, dtype, M, C, alpha, post, post_w, gate, pre, pre_w, pre_b, scale,
+                  shift, ldt, G, offsets, eps, h, ldh, n, n_dtype, ldn, n_scales=None,
+                  stream=None):
+    _check(lib().asp_norm_gate(_at(x), ldx, _at(y), ldy, dtype, M, C, alpha, post, _ptr(post_w),
+                               _at(gate), pre, _ptr(pre_w), _ptr(pre_b), _at(scale), _at(shift),
+                               ldt, G, _ptr(offsets), eps, _at(h), ldh, _at(n), n_dtype, ldn,
+                               _ptr(n_scales), _stream(stream, x)))
+
+
+def asp_norm_gate_backward_workspace_bytes(M, C, G) -> int:
+    return _size(lib().asp_norm_gate_backward_workspace_bytes, M, C, G)
+
+
+def asp_norm_gate_backward(dh, lddh, dn, lddn, dn_dtype, h, ldh, y, ldy, dtype, M, C, alpha, post,
+                           post_w, gate, pre, pre_w, pre_b, scale, ldt, G, offsets, eps, dx, lddx,
+                           dy, lddy, d_post_w, d_gate, d_pre_w, d_pre_b, d_scale, d_shift, ldd,
+                           workspace, workspace_bytes, stream=None):
+    _check(lib().asp_norm_gate_backward(
+        _at(dh), lddh, _at(dn), lddn, dn_dtype, _at(h), ldh, _at(y), ldy, dtype, M, C, alpha, post,
+        _ptr(post_w), _at(gate), pre, _ptr(pre_w), _ptr(pre_b), _at(scale), ldt, G, _ptr(offsets),
+        eps, _at(dx), lddx, _at(dy), lddy, _ptr(d_post_w), _at(d_gate), _ptr(d_pre_w),
+        _ptr(d_pre_b), _at(d_scale), _at(d_shift), ldd, _ptr(workspace), workspace_bytes,
+        _stream(stream, dh, dn)))

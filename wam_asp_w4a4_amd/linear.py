@@ -12,6 +12,8 @@ model with one call that refuses to swap only part of the targets.  Here:
   its bias is present exactly when the Linear has one, it sits on the model's
   device -- and only when all of them pass is any module swapped.  Otherwise
   ``InstallError`` lists every problem and the model is left unchanged.
+* ``Fp8Linear`` is the same around a layer in the 8-bit format (``fp8.Fp8Layer``),
+  for the projections that 4 bits hurt; ``install`` takes either kind.
 
 All arithmetic runs in libasp; this module only reshapes and dispatches.
 """
@@ -22,6 +24,7 @@ from typing import Mapping
 
 import torch
 
+from .fp8 import _NAMES, Fp8Layer, _no_capture
 from .layer import PackedLayer
 
 
@@ -71,6 +74,80 @@ class ASPLinear(torch.nn.Module):
                 f"rank={self.rank}, bias={self.packed.bias is not None}, NVFP4 W4A4")
 
 
+class _Fp8Apply(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, layer):
+        ctx.layer = layer
+        ctx.save_for_backward(x if weight is not None and ctx.needs_input_grad[1] else None, weight)
+        return layer.forward(x)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _no_capture()
+        x, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = ctx.layer.backward(dy.contiguous(), x, need_dx=need[0], need_db=need[2],
+                                        dw_dtype="f32" if weight is None else _NAMES[weight.dtype])
+        return dx, dw, db, None
+
+
+class Fp8Linear(torch.nn.Module):
+    """y = the 8-bit linear layer applied to x (..., in_features); y has x's type.
+
+    Around a packed ``Fp8Layer`` the weight is frozen, and x (and a bias that requires
+    it) has a gradient.  With ``weight`` (N x K, float32 or bf16, a parameter) every
+    forward packs the weight as it stands, and it has a gradient too: training in
+    8-bit products with the optimiser's weight kept in its own type.  Under a HIP
+    graph capture, gradients are refused: capture ``Fp8Layer.forward`` and
+    ``backward``, which keep no graph of their own."""
+
+    def __init__(self, packed: Fp8Layer | None = None, weight=None, bias=None):
+        super().__init__()
+        if (packed is None) == (weight is None):
+            raise ValueError("either a packed layer or a weight")
+        if packed is not None and bias is not None:
+            raise ValueError("a packed layer has its own bias")
+        self.packed = packed
+        self.weight = weight
+        self.bias = packed.bias if packed is not None else bias
+        self.out_features, self.in_features = ((packed.N, packed.K) if packed is not None
+                                               else weight.shape)
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear, trainable: bool = False):
+        """From an nn.Linear on the device: its weight packed once, or with ``trainable``
+        shared as the parameter that every forward packs.  The bias is kept in float32."""
+        bias = None if linear.bias is None else linear.bias.detach().float().contiguous()
+        if trainable:
+            return cls(weight=linear.weight,
+                       bias=None if bias is None else torch.nn.Parameter(bias.clone()))
+        return cls(Fp8Layer.pack(linear.weight.detach(), bias))
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[-1] != self.in_features:
+            raise ValueError(f"x has {x.shape[-1]} features, the layer {self.in_features}")
+        x2 = x.reshape(-1, self.in_features)
+        leaves = (x2, self.weight, self.bias)
+        grads = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in leaves)
+        if grads:
+            _no_capture()
+        layer = self.packed
+        if layer is None:
+            bias = None if self.bias is None else self.bias.detach()
+            layer = Fp8Layer.pack(self.weight.detach(), bias, backward=grads and x2.requires_grad)
+        if grads:
+            y = _Fp8Apply.apply(x2, self.weight, self.bias, layer)
+        else:
+            y = layer.forward(x2)
+        return y.reshape(*x.shape[:-1], self.out_features)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, E4M3 block 128, "
+                f"{'frozen' if self.weight is None else 'trainable'}")
+
+
 def _resolve(model: torch.nn.Module, name: str):
     """(parent module, attribute name, module) of a dotted submodule name."""
     parts = name.split(".")
@@ -82,9 +159,9 @@ def _resolve(model: torch.nn.Module, name: str):
     return parent, parts[-1], getattr(parent, parts[-1], None)
 
 
-def install(model: torch.nn.Module, layers: Mapping[str, PackedLayer]) -> list:
-    """Swap every named nn.Linear of ``model`` for an ASPLinear of its packed
-    layer, or none of them.  Returns the names swapped."""
+def install(model: torch.nn.Module, layers: Mapping[str, PackedLayer | Fp8Layer]) -> list:
+    """Swap every named nn.Linear of ``model`` for an ASPLinear (or Fp8Linear) of
+    its packed layer, or none of them.  Returns the names swapped."""
     problems = []
     plan = []
     for name, packed in layers.items():
@@ -95,7 +172,7 @@ def install(model: torch.nn.Module, layers: Mapping[str, PackedLayer]) -> list:
         if not isinstance(mod, torch.nn.Linear):
             problems.append(f"{name}: a {type(mod).__name__}, not an nn.Linear")
             continue
-        if not isinstance(packed, PackedLayer):
+        if not isinstance(packed, (PackedLayer, Fp8Layer)):
             problems.append(f"{name}: the packed layer is a {type(packed).__name__}")
             continue
         if (packed.K, packed.N) != (mod.in_features, mod.out_features):
@@ -110,5 +187,6 @@ def install(model: torch.nn.Module, layers: Mapping[str, PackedLayer]) -> list:
     if problems:
         raise InstallError(problems)
     for parent, attr, packed in plan:
-        setattr(parent, attr, ASPLinear(packed))
+        setattr(parent, attr, Fp8Linear(packed) if isinstance(packed, Fp8Layer)
+                else ASPLinear(packed))
     return list(layers)

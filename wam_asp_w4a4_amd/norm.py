@@ -1,0 +1,272 @@
+"""The norms after one transformer block and before the next, fused with the
+block's gate and the residual scale:
+
+    h = alpha x + gate[g] * post(y)
+    n = (pre(h) * weight + bias) * (1 + scale[g]) + shift[g]
+
+``gated_norm`` computes both in one pass (``include/asp.h``, ``asp_norm_gate``,
+has the definition); n may leave in the 8-bit format, ready for
+``fp8.Fp8Layer.forward``.  ``gated_norm_backward`` gives the gradients of all its
+inputs, and ``GatedNorm`` is both as a module.  All arithmetic happens inside
+libasp.
+"""
+
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import binding as B
+from .fp8 import (_CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture, _on,
+                  _stride)
+from .layer import _Y_DTYPES, _check_ws
+
+KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
+
+
+class NormGrads(NamedTuple):
+    """Gradients of gated_norm's inputs (None: the input was not given)."""
+    dx: torch.Tensor | None
+    dy: torch.Tensor | None
+    post_weight: torch.Tensor | None
+    gate: torch.Tensor | None
+    weight: torch.Tensor | None
+    bias: torch.Tensor | None
+    scale: torch.Tensor | None
+    shift: torch.Tensor | None
+
+
+def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, shift, offsets):
+    """Checks what x, y share and the tables; (post, pre, G, table row stride)."""
+    if post not in KINDS or pre not in KINDS:
+        raise ValueError(f"post and pre must be among {sorted(KINDS)}, not {post!r}, {pre!r}")
+    if not has_y and (post != "none" or gate is not None):
+        raise ValueError("a post norm or gate needs y")
+    if pre == "none" and not (weight is bias is scale is shift is None):
+        raise ValueError("weight, bias, scale and shift need a pre norm")
+    if post == "none" and post_weight is not None:
+        raise ValueError("post_weight needs a post norm")
+    for t, name in ((post_weight, "post_weight"), (weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _check_vector(t, name, C, device)
+    G = 1
+    if offsets is not None:
+        if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32:
+            raise TypeError("offsets must be an int32 tensor")
+        if offsets.dim() != 1 or offsets.numel() < 2 or offsets.device != device \
+                or not offsets.is_contiguous():
+            raise ValueError(f"offsets must be G + 1 >= 2 contiguous entries on {device}")
+        G = offsets.numel() - 1
+    ldt = None
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name} must be a float32 tensor")
+        if tuple(t.shape) != (G, C) and not (G == 1 and tuple(t.shape) == (C,)):
+            raise ValueError(f"{name} must be ({G}, {C}), got {tuple(t.shape)}")
+        if t.device != device or (C > 1 and t.stride(-1) != 1):
+            raise ValueError(f"the rows of {name} must be contiguous and on {device}")
+        ld = t.stride(0) if G > 1 else C
+        if ldt not in (None, ld) or ld < C:
+            raise ValueError("gate, scale and shift must have one row stride, of at least a row")
+        ldt = ld
+    return KINDS[post], KINDS[pre], G, C if ldt is None else ldt
+
+
+def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None, pre="rms",
+               weight=None, bias=None, scale=None, shift=None, offsets=None, eps=1e-6, out=None,
+               h=None, n=None, stream=None):
+    """(h, n) for the stream x and the block's output y (both M x C, float32 or bf16).
+
+    post, pre: 'none', 'rms' or 'layer' (pre 'none': n is None).  post_weight, weight,
+    bias: C float32.  gate, scale, shift: (G, C) float32 (C for one sequence).
+    offsets: G + 1 int32, the packed sequences' first rows and the end of the last;
+    rows of no sequence are left as they are.  out: 'f32', 'bf16' (None: x's type)
+    or 'fp8' for an ``Fp8Tensor``.  h, n: tensors to write (h may be x or y); without
+    y and with alpha 1, h is x itself and not written unless given."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D torch tensor")
+    M, C = x.shape
+    dev = x.device
+    _check_rows(x, "x", M, C, dev)
+    if y is not None:
+        _check_rows(y, "y", M, C, dev, (x.dtype,))
+    post, pre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
+                              scale, shift, offsets)
+    made = []
+    write = h
+    if h is not None:
+        _check_rows(h, "h", M, C, dev, (x.dtype,))
+    elif y is None and alpha == 1.0 and pre:
+        h = x
+    else:
+        write = h = torch.empty((M, C), dtype=x.dtype, device=dev)
+        made.append(h)
+    scales = None
+    if not pre:
+        if n is not None or out is not None:
+            raise ValueError("out and n need a pre norm")
+        values, code, ldn = None, B.ASP_F32, C
+    elif out == "fp8" or isinstance(n, Fp8Tensor):
+        if out not in (None, "fp8"):
+            raise ValueError(f"out {out!r} with an Fp8Tensor n")
+        if n is None:
+            n = Fp8Tensor.empty(M, C, dev)
+            made += [n.codes, n.scales]
+        else:
+            if not isinstance(n, Fp8Tensor):
+                raise TypeError("out 'fp8' needs an Fp8Tensor n")
+            n.check("n")
+            if (n.rows, n.cols) != (M, C) or n.codes.device != dev:
+                raise ValueError(f"n must be ({M}, {C}) on {dev}")
+        values, scales, code, ldn = n.codes, n.scales, B.ASP_E4M3, C
+    else:
+        if out is not None and out not in _Y_DTYPES:
+            raise ValueError(f"out must be 'f32', 'bf16' or 'fp8', not {out!r}")
+        if n is None:
+            n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
+            made.append(n)
+        else:
+            _check_rows(n, "n", M, C, dev, tuple(_CODES) if out is None else (_Y_DTYPES[out],))
+        values, code, ldn = n, _CODES[n.dtype], _stride(n)
+    with _on(dev):
+        B.asp_norm_gate(x, _stride(x), y, C if y is None else _stride(y), _CODES[x.dtype], M, C,
+                        alpha, post, post_weight, gate, pre, weight, bias, scale, shift, ldt, G,
+                        offsets, eps, write, _stride(h), values, code, ldn, scales, stream)
+    _lend(stream, *made)
+    return h, n
+
+
+def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None,
+                        pre="rms", weight=None, bias=None, scale=None, shift=None, offsets=None,
+                        eps=1e-6, dx=None, dy=None, workspace=None, stream=None):
+    """Gradients of ``gated_norm`` from dh (of h as it goes on; None: zeros) and dn (of
+    n, float32 or bf16; None without a pre norm).  h: the forward's; the options are
+    the forward's.  dx, dy: tensors to write (rows of no sequence are left as they
+    are).  Every given input of the forward has a gradient in the result, in its shape
+    (float32 but for dx and dy, which have the stream's type)."""
+    if not isinstance(h, torch.Tensor) or h.dim() != 2:
+        raise ValueError("h must be a 2-D torch tensor")
+    M, C = h.shape
+    dev = h.device
+    _check_rows(h, "h", M, C, dev)
+    if y is not None:
+        _check_rows(y, "y", M, C, dev, (h.dtype,))
+    if dh is not None:
+        _check_rows(dh, "dh", M, C, dev, (h.dtype,))
+    kpost, kpre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
+                                scale, shift, offsets)
+    if (dn is not None) != bool(kpre):
+        raise ValueError("dn belongs to the pre norm's result")
+    if dn is not None:
+        _check_rows(dn, "dn", M, C, dev)
+    if dh is None and dn is None:
+        raise ValueError("neither dh nor dn is given")
+    made = []
+
+    def new(shape, dtype=torch.float32):
+        made.append(torch.empty(shape, dtype=dtype, device=dev))
+        return made[-1]
+
+    def like(t):
+        return None if t is None else new(tuple(t.shape))
+
+    if dx is None:
+        dx = new((M, C), h.dtype)
+    else:
+        _check_rows(dx, "dx", M, C, dev, (h.dtype,))
+    if y is None:
+        if dy is not None:
+            raise ValueError("dy without y")
+    elif dy is None:
+        dy = new((M, C), h.dtype)
+    else:
+        _check_rows(dy, "dy", M, C, dev, (h.dtype,))
+    g = NormGrads(dx, dy, like(post_weight), like(gate), like(weight), like(bias), like(scale),
+                  like(shift))
+    need = 0
+    if any(t is not None for t in g[2:]):
+        need = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
+        if workspace is None:
+            workspace = new((need,), torch.uint8)
+    if workspace is not None:
+        _check_ws(workspace, need, dev)
+    with _on(dev):
+        B.asp_norm_gate_backward(
+            dh, C if dh is None else _stride(dh), dn, C if dn is None else _stride(dn),
+            B.ASP_F32 if dn is None else _CODES[dn.dtype], h, _stride(h), y,
+            C if y is None else _stride(y), _CODES[h.dtype], M, C, alpha, kpost, post_weight, gate,
+            kpre, weight, bias, scale, ldt, G, offsets, eps, dx, _stride(dx), dy,
+            C if dy is None else _stride(dy), g.post_weight, g.gate, g.weight, g.bias, g.scale,
+            g.shift, C, workspace, 0 if workspace is None else workspace.numel(), stream)
+    _lend(stream, *made)
+    return g
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, options):
+        given = dict(post_weight=post_weight, gate=gate, weight=weight, bias=bias, scale=scale,
+                     shift=shift)
+        # h is always written: a stream returned as it came would share its version
+        h, n = gated_norm(x, y, h=torch.empty_like(x, memory_format=torch.contiguous_format),
+                          **given, **options)
+        ctx.save_for_backward(h, y, *given.values())
+        ctx.options = options
+        return h, n
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh, dn):
+        _no_capture()
+        h, y, post_weight, gate, weight, bias, scale, shift = ctx.saved_tensors
+        g = gated_norm_backward(None if dh is None else dh.contiguous(),
+                                None if dn is None else dn.contiguous(), h, y,
+                                post_weight=post_weight, gate=gate, weight=weight, bias=bias,
+                                scale=scale, shift=shift, **ctx.options)
+        return (*g, None)
+
+
+class GatedNorm(torch.nn.Module):
+    """``gated_norm`` with its weights as parameters, differentiable in every input.
+
+    x, y: (..., C); gate, scale, shift: (G, C) or (C); returns (h, n) of x's shape
+    (n None for pre 'none').  Under a HIP graph capture, gradients are refused: capture
+    ``gated_norm`` and ``gated_norm_backward``, which keep no graph of their own."""
+
+    def __init__(self, channels, post="none", pre="rms", alpha=1.0, eps=1e-6, device=None):
+        super().__init__()
+        if post not in KINDS or pre not in KINDS:
+            raise ValueError(f"post and pre must be among {sorted(KINDS)}, not {post!r}, {pre!r}")
+        self.channels, self.post, self.pre, self.alpha, self.eps = channels, post, pre, alpha, eps
+
+        def parameter(used, value):
+            return torch.nn.Parameter(torch.full((channels,), value, device=device)) if used else None
+
+        self.post_weight = parameter(post != "none", 1.0)
+        self.weight = parameter(pre != "none", 1.0)
+        self.bias = parameter(pre == "layer", 0.0)
+
+    def forward(self, x, y=None, gate=None, scale=None, shift=None, offsets=None):
+        if x.shape[-1] != self.channels:
+            raise ValueError(f"x has {x.shape[-1]} channels, the norm {self.channels}")
+        if y is None and self.post != "none":
+            raise ValueError("a post norm needs y")
+        flat = [None if t is None else t.reshape(-1, self.channels) for t in (x, y)]
+        options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps,
+                       offsets=offsets)
+        tensors = (self.post_weight, gate, self.weight, self.bias, scale, shift)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                           for t in (*flat, *tensors)):
+            _no_capture()
+            h, n = _GatedNorm.apply(*flat, *tensors, options)
+        else:
+            names = ("post_weight", "gate", "weight", "bias", "scale", "shift")
+            h, n = gated_norm(*flat, **dict(zip(names, tensors)), **options)
+        return h.reshape(x.shape), None if n is None else n.reshape(x.shape)
+
+    def extra_repr(self) -> str:
+        return (f"{self.channels}, post={self.post!r}, pre={self.pre!r}, alpha={self.alpha}, "
+                f"eps={self.eps}")
