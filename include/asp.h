@@ -601,9 +601,9 @@ int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const v
  *              stride ldt, or NULL (ones, zeros, zeros)
  *   offsets    device int32, G + 1 entries, not decreasing: sequence g has the
  *              rows offsets[g] .. offsets[g + 1] - 1 (it may be empty).  Rows
- *              before the first and behind the last sequence are neither read
- *              nor written.  NULL: one sequence of all rows (G = 1)
- *   C 1..16384, G 1..65536, eps in [0, 1]
+ *              before the first and behind the last sequence count for
+ *              nothing and are not written.  NULL: one sequence of all rows (G = 1)
+ *   C 1..16384, G 1..65535, eps in [0, 1]
  */
 #define ASP_E4M3 2 /* n_dtype: the 8-bit format */
 #define ASP_NORM_NONE 0

@@ -13,10 +13,15 @@
 //
 // Everything is bound by memory: a row is read once, held in registers through
 // both norms (a layer norm's variance is summed around its mean, not as a
-// difference of squares), and written once.  A workgroup (or, up to 1024
-// columns, a wave) walks a strip of consecutive rows, so that the tables stay
-// in registers too: read anew for each row they would cost more cache traffic
-// than the row itself.
+// difference of squares), and written once.  A workgroup walks a strip of
+// consecutive rows, one row at a time with the next one's loads in flight; the
+// tables of the strip's sequence stay in registers (read anew for each row they
+// cost more cache traffic than the row: 653 against XXX us for the backward of
+// 16384 x 4096 bf16).  T threads share a row, 8 columns each (E = 2: 16, above 8192
+// columns): a thread's share of a row, its tables and its column sums are then
+// few enough registers for four waves a SIMD.
+#include <initializer_list>
+
 #include "asp_fp8.h"
 
 namespace asp {
@@ -30,7 +35,7 @@ struct NormArgs {
   uint8_t* n_scales;
   int64_t ldx, ldy, ldh, ldn, ldt;
   float alpha, eps;
-  int M, C, G, post, pre, n_dtype, rows;  // rows: of a strip
+  int M, C, G, post, pre, n_dtype, rows, tvec;  // rows: of a strip; tvec: 16-byte table loads
   // backward
   const void *dh, *dn;
   void *dx, *dy;
@@ -38,35 +43,43 @@ struct NormArgs {
   int64_t lddh, lddn, lddx, lddy;
 };
 
-// T: the lanes that share a row (64: one wave); E: 8-column chunks of a lane
-constexpr int threads_of(int T) { return T < 256 ? 256 : T; }
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// sum over the 16 lanes of a DPP row, in every lane
+__device__ __forceinline__ float row16_sum(float v) {
+  auto add = [](float a, auto ctrl) {
+    return a + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                             0, __builtin_bit_cast(int, a), decltype(ctrl)::value,
+                                             0xf, 0xf, false));
+  };
+  v = add(v, std::integral_constant<int, 0x128>{});
+  v = add(v, std::integral_constant<int, 0x124>{});
+  v = add(v, std::integral_constant<int, 0x122>{});
+  return add(v, std::integral_constant<int, 0x121>{});
 }
 
-// sums of two values over the row's lanes, in every lane; `slot` alternates, so
-// that one barrier separates a slot's reads from its next writes
-template <int T>
-__device__ __forceinline__ void row_sums(float& a, float& b, float (&lds)[2][2][16], int& slot) {
-  a = wave_sum(a);
-  b = wave_sum(b);
+__device__ __forceinline__ float wave_sum(float v) {
+  const int w = __builtin_bit_cast(int, row16_sum(v));
+  auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(w, l)); };
+  return (lane(0) + lane(16)) + (lane(32) + lane(48));
+}
+
+// sums of N values over the workgroup, in every lane; `slot` alternates, so that
+// the one barrier also separates a slot's reads from its next writes
+constexpr int kMaxSums = 4;
+typedef float SumsLds[2][kMaxSums][16];
+template <int T, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], SumsLds& lds, int& slot) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = wave_sum(s[i]);
   if constexpr (T > 64) {
     constexpr int W = T / 64;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-      lds[slot][0][wave] = a;
-      lds[slot][1][wave] = b;
-    }
-    __syncthreads();
-    a = b = 0.0f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane == 0)
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      a += lds[slot][0][w];
-      b += lds[slot][1][w];
-    }
+      for (int i = 0; i < N; ++i) lds[slot][i][wave] = s[i];
+    __syncthreads();
+    const int w = lane & 15;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = row16_sum(w < W ? lds[slot][i][w < W ? w : 0] : 0.0f);
     slot ^= 1;
   }
 }
@@ -84,25 +97,76 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int G, int ro
   return lo;
 }
 
-template <int E, int T>
-__device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, float other,
-                                      float (&v)[E][8]) {
+// 8 elements of a row as they lie in memory
+template <typename XT>
+struct Raw {
+  u32x4_t q[sizeof(XT) / 2];
+};
+
+template <typename XT, bool VEC>
+__device__ __forceinline__ void raw_load(const XT* p, int left, Raw<XT>& r) {
+  if constexpr (VEC) {
+    if (left > 0)
 #pragma unroll
-  for (int e = 0; e < E; ++e)
+      for (int i = 0; i < (int)sizeof(XT) / 2; ++i) r.q[i] = reinterpret_cast<const u32x4_t*>(p)[i];
+  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = (e * T + t) * 8 + k;
-      v[e][k] = p && c < C ? p[at + c] : other;
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(XT) == 2) {
+        const uint32_t w = e < left ? p[e] : 0u;
+        r.q[0][e >> 1] = e & 1 ? r.q[0][e >> 1] | w << 16 : w;
+      } else {
+        r.q[e >> 2][e & 3] = e < left ? __builtin_bit_cast(uint32_t, p[e]) : 0u;
+      }
     }
+  }
 }
 
+template <typename XT>
+__device__ __forceinline__ void unpack(const Raw<XT>& r, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t w = sizeof(XT) == 2 ? r.q[0][e >> 1] : r.q[(sizeof(XT) / 2 - 1) & (e >> 2)][e & 3];
+    if constexpr (sizeof(XT) == 2)
+      v[e] = e & 1 ? bf16_hi(w) : bf16_lo(w);
+    else
+      v[e] = __builtin_bit_cast(float, w);
+  }
+}
+
+// a thread's columns of a row: E chunks of 8, chunk e at column 8 (e T + t)
 template <typename XT, int E, int T, bool VEC>
 __device__ __forceinline__ void row_load(const void* p, int64_t row, int64_t ld, int C, int t,
-                                         float (&v)[E][8]) {
+                                         Raw<XT> (&r)[E]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = (e * T + t) * 8;
-    load8<VEC>(static_cast<const XT*>(p) + row * ld + c, C - c, v[e]);
+    raw_load<XT, VEC>(static_cast<const XT*>(p) + row * ld + c, C - c, r[e]);
+  }
+}
+
+template <int E, int T>
+__device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, bool vec,
+                                      float other, float (&v)[E][8]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = (e * T + t) * 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[e][k] = other;
+    if (!p || c >= C) continue;
+    if (vec) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + at + c);
+      const f32x4_t b = *reinterpret_cast<const f32x4_t*>(p + at + c + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[e][k] = a[k];
+        v[e][4 + k] = b[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < C) v[e][k] = p[at + c + k];
+    }
   }
 }
 
@@ -132,68 +196,59 @@ __device__ __forceinline__ void store8(void* p, int64_t at, bool bf16, int left,
   }
 }
 
+// f(e, k) for each of a thread's columns
+template <int E, typename F>
+__device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f(e, k);
+}
+
 // v - mean; columns past C become 0
 template <int E, int T>
 __device__ __forceinline__ void centre(float (&v)[E][8], float mean, int C, int t) {
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[e][k] = (e * T + t) * 8 + k < C ? v[e][k] - mean : 0.0f;
+  each<E>([&](int e, int k) { v[e][k] = (e * T + t) * 8 + k < C ? v[e][k] - mean : 0.0f; });
 }
 
-template <int E>
-__device__ __forceinline__ float sum_of(const float (&v)[E][8]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += v[e][k];
-  return s;
+// the row's one square root and division are IEEE ones: they cost nothing
+__device__ __forceinline__ float inverse_deviation(float squares, int C, float eps) {
+  return 1.0f / sqrtf(squares / (float)C + eps);
 }
 
-template <int E>
-__device__ __forceinline__ float dot_of(const float (&a)[E][8], const float (&b)[E][8]) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s = __builtin_fmaf(a[e][k], b[e][k], s);
-  return s;
-}
-
-// v -> the normed row; returns r.  (IEEE square root and division: the row's
-// one r costs nothing.)
+// v -> the normed row
 template <int E, int T>
-__device__ __forceinline__ float normalise(float (&v)[E][8], int kind, int C, float eps, int t,
-                                           float (&lds)[2][2][16], int& slot) {
-  float s, unused = 0.0f;
+__device__ __forceinline__ void normalise(float (&v)[E][8], int kind, int C, float eps, int t,
+                                          SumsLds& lds, int& slot) {
+  float s[1];
   if (kind == ASP_NORM_LAYER) {
-    s = sum_of<E>(v);
-    row_sums<T>(s, unused, lds, slot);
-    centre<E, T>(v, s / (float)C, C, t);
+    s[0] = 0.0f;
+    each<E>([&](int e, int k) { s[0] += v[e][k]; });
+    row_sums<T, 1>(s, lds, slot);
+    centre<E, T>(v, s[0] / (float)C, C, t);
   }
-  s = dot_of<E>(v, v);
-  unused = 0.0f;
-  row_sums<T>(s, unused, lds, slot);
-  const float r = 1.0f / sqrtf(s / (float)C + eps);
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[e][k] *= r;
-  return r;
+  s[0] = 0.0f;
+  each<E>([&](int e, int k) { s[0] = __builtin_fmaf(v[e][k], v[e][k], s[0]); });
+  row_sums<T, 1>(s, lds, slot);
+  const float r = inverse_deviation(s[0], C, eps);
+  each<E>([&](int e, int k) { v[e][k] *= r; });
 }
 
 template <typename XT, int T, int E, bool VEC>
-__global__ void __launch_bounds__(threads_of(T)) k_norm_gate(const NormArgs a) {
-  __shared__ float lds[2][2][16];
-  const int t = threadIdx.x % T;
+__global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
+  __shared__ SumsLds lds;
+  const int t = threadIdx.x;
   int slot = 0;
-  const int strip = blockIdx.x * (threads_of(T) / T) + threadIdx.x / T;
-  const int64_t r0 = (int64_t)strip * a.rows;
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows;
   const int64_t r1 = min(r0 + a.rows, (int64_t)a.M);
   const int pitch = (a.C + kFp8Block - 1) / kFp8Block * kFp8Block;
   float gp[E][8], pa[E][8], pc[E][8];
+  Raw<XT> nx[E] = {}, ny[E] = {};
+  auto fetch = [&](int64_t row) {
+    row_load<XT, E, T, VEC>(a.x, row, a.ldx, a.C, t, nx);
+    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, ny);
+  };
+  fetch(r0);
   int64_t begin = 0, end = 0;
   for (int64_t row = r0; row < r1; ++row) {
     if (row == r0 || row >= end) {
@@ -206,52 +261,33 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate(const NormArgs a) {
       } else {
         end = a.M;
       }
-      float u[E][8];
-      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
-      if (a.post != ASP_NORM_NONE) {
-        table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) gp[e][k] *= u[e][k];
-      }
-      // (v w + b) (1 + scale) + shift = v pa + pc
-      table<E, T>(a.pre_w, 0, a.C, t, 1.0f, pa);
-      table<E, T>(a.pre_b, 0, a.C, t, 0.0f, pc);
-      if (a.scale) {
-        table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            pa[e][k] *= 1.0f + u[e][k];
-            pc[e][k] *= 1.0f + u[e][k];
-          }
-      }
-      if (a.shift) {
-        table<E, T>(a.shift, g * a.ldt, a.C, t, 0.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) pc[e][k] += u[e][k];
-      }
+      const bool tv = a.tvec;
+      float u[E][8], w[E][8];
+      // v gate post_w, and (v w + b) (1 + scale) + shift = v pa + pc
+      table<E, T>(a.gate, g * a.ldt, a.C, t, tv, 1.0f, gp);
+      table<E, T>(a.post_w, 0, a.C, t, tv, 1.0f, u);
+      each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
+      table<E, T>(a.pre_w, 0, a.C, t, tv, 1.0f, pa);
+      table<E, T>(a.pre_b, 0, a.C, t, tv, 0.0f, pc);
+      table<E, T>(a.scale, g * a.ldt, a.C, t, tv, 0.0f, u);
+      table<E, T>(a.shift, g * a.ldt, a.C, t, tv, 0.0f, w);
+      each<E>([&](int e, int k) {
+        pa[e][k] *= 1.0f + u[e][k];
+        pc[e][k] = __builtin_fmaf(pc[e][k], 1.0f + u[e][k], w[e][k]);
+      });
     }
-    if (row < begin) continue;  // in front of the first sequence
     float v[E][8], p[E][8];
-    row_load<XT, E, T, VEC>(a.x, row, a.ldx, a.C, t, v);
-    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, p);
-    if (a.y) {
-      if (a.post != ASP_NORM_NONE) normalise<E, T>(p, a.post, a.C, a.eps, t, lds, slot);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[e][k] = __builtin_fmaf(p[e][k], gp[e][k], a.alpha * v[e][k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[e][k] *= a.alpha;
+    for (int e = 0; e < E; ++e) {
+      unpack(nx[e], v[e]);
+      unpack(ny[e], p[e]);
     }
+    if (row + 1 < r1) fetch(row + 1);
+    if (row < begin) continue;  // in front of the first sequence
+    if (a.post != ASP_NORM_NONE) normalise<E, T>(p, a.post, a.C, a.eps, t, lds, slot);
+    each<E>([&](int e, int k) {
+      v[e][k] = a.y ? __builtin_fmaf(p[e][k], gp[e][k], a.alpha * v[e][k]) : a.alpha * v[e][k];
+    });
     if constexpr (sizeof(XT) == 2)
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -269,10 +305,7 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate(const NormArgs a) {
       }
     if (a.pre == ASP_NORM_NONE) continue;
     normalise<E, T>(v, a.pre, a.C, a.eps, t, lds, slot);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[e][k] = __builtin_fmaf(v[e][k], pa[e][k], pc[e][k]);
+    each<E>([&](int e, int k) { v[e][k] = __builtin_fmaf(v[e][k], pa[e][k], pc[e][k]); });
     if (a.n_dtype != ASP_E4M3) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -287,7 +320,7 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate(const NormArgs a) {
       uint32_t u = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (c + k >= a.C) v[e][k] = 0.0f;  // pads the last block (pc may be anything there)
+        if (c + k >= a.C) v[e][k] = 0.0f;  // pads the block
         u = max(u, finite_bits(v[e][k]));
       }
       const uint32_t s = fp8_scale_byte(row16_max(u));
@@ -303,51 +336,59 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate(const NormArgs a) {
   }
 }
 
-// Backward.  With v the normed h (deviation 1/r), g = dn w (1 + scale):
+// Backward.  With m the mean that the pre norm takes off (0 for RMS), v = (h - m) r
+// and g = dn w (1 + scale):
 //   dh' = dh + r (g - [layer] mean g - v mean(g v)),   dx = alpha dh'
-// and the same form through the post norm for dy from dh' gate post_w.  Every
-// gradient of a table or weight follows from three column sums over each
+// and the same form through the post norm for dy from dh' gate post_w.  mean(g v)
+// is r mean(g (h - m)), so the sums of h's and y's squares and of g and g (h - m)
+// are taken together: three barriers a row (two without a layer norm).
+//
+// Every gradient of a table or weight follows from three column sums over each
 // sequence's rows, S1 = sum dn, S2 = sum dn v, S3 = sum dh' q (q the normed y, or
 // y): a strip keeps them in registers and writes them once for each sequence it
 // touches, to slot strip + g (strips and sequences both advance along the rows,
 // so no two pairs share one).  k_norm_sums adds the strips in order: the
 // results do not depend on scheduling.
 template <typename XT, typename NT, int T, int E, bool VEC>
-__global__ void __launch_bounds__(threads_of(T)) k_norm_gate_back(const NormArgs a) {
-  __shared__ float lds[2][2][16];
-  const int t = threadIdx.x % T;
+__global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
+  __shared__ SumsLds lds;
+  const int t = threadIdx.x;
   int slot = 0;
-  const int strip = blockIdx.x * (threads_of(T) / T) + threadIdx.x / T;
+  const int strip = blockIdx.x;
   const int64_t r0 = (int64_t)strip * a.rows;
   const int64_t r1 = min(r0 + a.rows, (int64_t)a.M);
-  float s1[E][8], s2[E][8], s3[E][8];
-  auto clear = [&]() {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s1[e][k] = s2[e][k] = s3[e][k] = 0.0f;
-  };
+  const float rc = 1.0f / (float)a.C;
+  const bool pre = a.pre != ASP_NORM_NONE, post = a.post != ASP_NORM_NONE;
+  const bool prel = a.pre == ASP_NORM_LAYER, postl = a.post == ASP_NORM_LAYER;
+  float gp[E][8], pa[E][8], s1[E][8], s2[E][8], s3[E][8];
   auto flush = [&](int g) {
     float* d = a.part + (int64_t)(strip + g) * 3 * a.C;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = (e * T + t) * 8 + k;
-        if (c < a.C) {
-          d[c] = s1[e][k];
-          d[a.C + c] = s2[e][k];
-          d[2 * (int64_t)a.C + c] = s3[e][k];
-        }
+    each<E>([&](int e, int k) {
+      const int c = (e * T + t) * 8 + k;
+      if (c < a.C) {
+        d[c] = s1[e][k];
+        d[a.C + c] = s2[e][k];
+        d[2 * (int64_t)a.C + c] = s3[e][k];
       }
+    });
   };
+  // dh and y not given, and h and dn without a pre norm, stay 0
+  Raw<XT> rd[E] = {}, ry[E] = {}, rh[E] = {};
+  Raw<NT> rn[E] = {};
+  auto fetch = [&](int64_t row) {
+    if (a.dh) row_load<XT, E, T, VEC>(a.dh, row, a.lddh, a.C, t, rd);
+    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, ry);
+    if (pre) {
+      row_load<XT, E, T, VEC>(a.h, row, a.ldh, a.C, t, rh);
+      row_load<NT, E, T, VEC>(a.dn, row, a.lddn, a.C, t, rn);
+    }
+  };
+  fetch(r0);
   int g = -1;
   int64_t begin = 0, end = 0;
-  clear();
   for (int64_t row = r0; row < r1; ++row) {
     if (row == r0 || row >= end) {
       if (g >= 0 && a.part) flush(g);
-      clear();
       g = 0;
       if (a.offsets) {
         g = sequence_of(a.offsets, a.G, (int)row);
@@ -360,50 +401,57 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate_back(const NormArgs
       } else {
         end = a.M;
       }
-    }
-    if (row < begin) continue;
-    float d[E][8], v[E][8], n[E][8], q[E][8];
-    if (a.dh) row_load<XT, E, T, VEC>(a.dh, row, a.lddh, a.C, t, d);
-    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, q);
-    if (!a.dh)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[e][k] = 0.0f;
-    if (a.pre != ASP_NORM_NONE) {
-      row_load<XT, E, T, VEC>(a.h, row, a.ldh, a.C, t, v);
-      row_load<NT, E, T, VEC>(a.dn, row, a.lddn, a.C, t, n);
-      const float r = normalise<E, T>(v, a.pre, a.C, a.eps, t, lds, slot);
+      const bool tv = a.tvec;
       float u[E][8];
+      table<E, T>(a.gate, g * a.ldt, a.C, t, tv, 1.0f, gp);
+      table<E, T>(a.post_w, 0, a.C, t, tv, 1.0f, u);
+      each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
+      table<E, T>(a.pre_w, 0, a.C, t, tv, 1.0f, pa);
+      table<E, T>(a.scale, g * a.ldt, a.C, t, tv, 0.0f, u);
+      each<E>([&](int e, int k) {
+        pa[e][k] *= 1.0f + u[e][k];
+        s1[e][k] = s2[e][k] = s3[e][k] = 0.0f;
+      });
+    }
+    float d[E][8], v[E][8], n[E][8], q[E][8];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s1[e][k] += n[e][k];
-          s2[e][k] = __builtin_fmaf(n[e][k], v[e][k], s2[e][k]);
-        }
-      if (a.pre_w) {
-        table<E, T>(a.pre_w, 0, a.C, t, 1.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) n[e][k] *= u[e][k];
-      }
-      if (a.scale) {
-        table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) n[e][k] *= 1.0f + u[e][k];
-      }
-      float c1 = a.pre == ASP_NORM_LAYER ? sum_of<E>(n) : 0.0f, c2 = dot_of<E>(n, v);
-      row_sums<T>(c1, c2, lds, slot);
-      c1 /= (float)a.C;
-      c2 /= (float)a.C;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[e][k] += r * (n[e][k] - c1 - v[e][k] * c2);
+    for (int e = 0; e < E; ++e) {
+      unpack(rd[e], d[e]);
+      unpack(ry[e], q[e]);
+      unpack(rh[e], v[e]);
+      unpack(rn[e], n[e]);
+    }
+    if (row + 1 < r1) fetch(row + 1);
+    if (row < begin) continue;
+    if (prel || postl) {
+      float s[2] = {0.0f, 0.0f};
+      each<E>([&](int e, int k) {
+        s[0] += v[e][k];
+        s[1] += q[e][k];
+      });
+      row_sums<T, 2>(s, lds, slot);
+      if (prel) centre<E, T>(v, s[0] * rc, a.C, t);
+      if (postl) centre<E, T>(q, s[1] * rc, a.C, t);
+    }
+    // squares of h - m and y - m, and of g = dn pa its sum and product with h - m
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    each<E>([&](int e, int k) {
+      const float gv = n[e][k] * pa[e][k];
+      s[0] = __builtin_fmaf(v[e][k], v[e][k], s[0]);
+      s[1] = __builtin_fmaf(q[e][k], q[e][k], s[1]);
+      s[2] = __builtin_fmaf(gv, v[e][k], s[2]);
+      s[3] += gv;
+    });
+    row_sums<T, 4>(s, lds, slot);
+    if (pre) {
+      const float r = inverse_deviation(s[0], a.C, a.eps);
+      const float c1 = prel ? s[3] * rc : 0.0f, c2 = r * s[2] * rc;
+      each<E>([&](int e, int k) {
+        const float vv = v[e][k] * r;
+        s1[e][k] += n[e][k];
+        s2[e][k] = __builtin_fmaf(n[e][k], vv, s2[e][k]);
+        d[e][k] += r * (__builtin_fmaf(n[e][k], pa[e][k], -c1) - vv * c2);
+      });
     }
     if (a.dx)
 #pragma unroll
@@ -416,37 +464,25 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate_back(const NormArgs
       }
     if (!a.y) continue;
     float r = 1.0f;
-    if (a.post != ASP_NORM_NONE) r = normalise<E, T>(q, a.post, a.C, a.eps, t, lds, slot);
-    float u[E][8];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s3[e][k] = __builtin_fmaf(d[e][k], q[e][k], s3[e][k]);
-    if (!a.dy) continue;
-    if (a.gate) {
-      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, u);
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[e][k] *= u[e][k];
+    if (post) {
+      r = inverse_deviation(s[1], a.C, a.eps);
+      each<E>([&](int e, int k) { q[e][k] *= r; });
     }
-    if (a.post != ASP_NORM_NONE) {
-      if (a.post_w) {
-        table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) d[e][k] *= u[e][k];
-      }
+    each<E>([&](int e, int k) {
+      s3[e][k] = __builtin_fmaf(d[e][k], q[e][k], s3[e][k]);
+      d[e][k] *= gp[e][k];
+    });
+    if (!a.dy) continue;
+    if (post) {
+      float z[2] = {0.0f, 0.0f};
       centre<E, T>(d, 0.0f, a.C, t);  // columns past C count as 0 in the sums
-      float c1 = a.post == ASP_NORM_LAYER ? sum_of<E>(d) : 0.0f, c2 = dot_of<E>(d, q);
-      row_sums<T>(c1, c2, lds, slot);
-      c1 /= (float)a.C;
-      c2 /= (float)a.C;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[e][k] = r * (d[e][k] - c1 - q[e][k] * c2);
+      each<E>([&](int e, int k) {
+        z[0] += d[e][k];
+        z[1] = __builtin_fmaf(d[e][k], q[e][k], z[1]);
+      });
+      row_sums<T, 2>(z, lds, slot);
+      const float c1 = postl ? z[0] * rc : 0.0f, c2 = z[1] * rc;
+      each<E>([&](int e, int k) { d[e][k] = r * (d[e][k] - c1 - q[e][k] * c2); });
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -458,70 +494,112 @@ __global__ void __launch_bounds__(threads_of(T)) k_norm_gate_back(const NormArgs
 }
 
 struct SumArgs {
-  const float* part;
+  float* part;
   const float *post_w, *gate, *pre_w, *pre_b, *scale;
   const int32_t* offsets;
   float *d_post_w, *d_gate, *d_pre_w, *d_pre_b, *d_scale, *d_shift;
-  int64_t ldt, ldd;
-  int M, C, G, rows, post;
+  int64_t ldt, ldd, slots;
+  int M, C, G, rows;
 };
 
-// 16 columns a workgroup; 16 lanes of a column take its strips in turn
+// The strips' column sums of sequence blockIdx.y, for 16 columns a workgroup: 16
+// threads of a column take its strips in turn, and the first adds them in order.
+// Their sequence's table gradients are written here; for the weights, which sum
+// over the sequences, S1 (1 + scale), S2 (1 + scale) and S3 gate go behind the
+// strips' slots, or are the results themselves when there is one sequence.
 __global__ void __launch_bounds__(256) k_norm_sums(const SumArgs a) {
   __shared__ float lds[3][16][17];
-  const int col = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int col = threadIdx.x & 15, lane = threadIdx.x >> 4, g = blockIdx.y;
   const int c = blockIdx.x * 16 + col;
   const bool in = c < a.C;
-  float w1 = 0.0f, w2 = 0.0f, w3 = 0.0f;  // sums over the sequences (first 16 threads)
-  for (int g = 0; g < a.G; ++g) {
-    int64_t o0 = 0, o1 = a.M;
-    if (a.offsets) {
-      o0 = max(a.offsets[g], 0);
-      o1 = min(a.offsets[g + 1], a.M);
-    }
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    if (in && o0 < o1)
-      for (int64_t k = o0 / a.rows + part; k <= (o1 - 1) / a.rows; k += 16) {
-        const float* p = a.part + (k + g) * 3 * a.C + c;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) s[i] += p[(int64_t)i * a.C];
-      }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) lds[i][part][col] = s[i];
-    __syncthreads();
-    if (part == 0 && in) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        s[i] = 0.0f;
-        for (int k = 0; k < 16; ++k) s[i] += lds[i][k][col];
-      }
-      const float w = a.pre_w ? a.pre_w[c] : 1.0f, b = a.pre_b ? a.pre_b[c] : 0.0f;
-      const float m = a.scale ? 1.0f + a.scale[g * a.ldt + c] : 1.0f;
-      const float gt = a.gate ? a.gate[g * a.ldt + c] : 1.0f;
-      const float pw = a.post != ASP_NORM_NONE && a.post_w ? a.post_w[c] : 1.0f;
-      if (a.d_shift) a.d_shift[g * a.ldd + c] = s[0];
-      if (a.d_scale) a.d_scale[g * a.ldd + c] = s[1] * w + s[0] * b;
-      if (a.d_gate) a.d_gate[g * a.ldd + c] = s[2] * pw;
-      w1 += s[0] * m;
-      w2 += s[1] * m;
-      w3 += s[2] * gt;
-    }
-    __syncthreads();
+  int64_t o0 = 0, o1 = a.M;
+  if (a.offsets) {
+    o0 = max(a.offsets[g], 0);
+    o1 = min(a.offsets[g + 1], a.M);
   }
-  if (part != 0 || !in) return;
-  if (a.d_pre_b) a.d_pre_b[c] = w1;
-  if (a.d_pre_w) a.d_pre_w[c] = w2;
-  if (a.d_post_w) a.d_post_w[c] = w3;
+  float s[3] = {0.0f, 0.0f, 0.0f};
+  if (in && o0 < o1) {
+    const int64_t k1 = (o1 - 1) / a.rows;
+    const float* p = a.part + (o0 / a.rows + lane + g) * 3 * a.C + c;
+#pragma unroll 4
+    for (int64_t k = o0 / a.rows + lane; k <= k1; k += 16) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) s[i] += p[(int64_t)i * a.C];
+      p += (int64_t)48 * a.C;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) lds[i][lane][col] = s[i];
+  __syncthreads();
+  if (lane != 0 || !in) return;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    s[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s[i] += lds[i][k][col];
+  }
+  const float w = a.pre_w ? a.pre_w[c] : 1.0f, b = a.pre_b ? a.pre_b[c] : 0.0f;
+  const float m = a.scale ? 1.0f + a.scale[g * a.ldt + c] : 1.0f;
+  const float gt = a.gate ? a.gate[g * a.ldt + c] : 1.0f;
+  const float pw = a.post_w ? a.post_w[c] : 1.0f;
+  if (a.d_shift) a.d_shift[g * a.ldd + c] = s[0];
+  if (a.d_scale) a.d_scale[g * a.ldd + c] = s[1] * w + s[0] * b;
+  if (a.d_gate) a.d_gate[g * a.ldd + c] = s[2] * pw;
+  if (a.G == 1) {
+    if (a.d_pre_b) a.d_pre_b[c] = s[0] * m;
+    if (a.d_pre_w) a.d_pre_w[c] = s[1] * m;
+    if (a.d_post_w) a.d_post_w[c] = s[2] * gt;
+  } else {
+    float* d = a.part + (a.slots + g) * 3 * a.C + c;
+    d[0] = s[0] * m;
+    d[a.C] = s[1] * m;
+    d[2 * (int64_t)a.C] = s[2] * gt;
+  }
+}
+
+// the weights' gradients: the sequences' sums in order
+__global__ void __launch_bounds__(64) k_norm_weight_sums(const SumArgs a) {
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (c >= a.C) return;
+  float s[3] = {0.0f, 0.0f, 0.0f};
+  const float* p = a.part + a.slots * 3 * a.C + c;
+#pragma unroll 4
+  for (int g = 0; g < a.G; ++g) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) s[i] += p[(int64_t)i * a.C];
+    p += 3 * (int64_t)a.C;
+  }
+  if (a.d_pre_b) a.d_pre_b[c] = s[0];
+  if (a.d_pre_w) a.d_pre_w[c] = s[1];
+  if (a.d_post_w) a.d_post_w[c] = s[2];
 }
 
 // ----------------------------------------------------------------- host side
 
 constexpr int kMaxNormC = 16384;
 
-int strips_wanted(int64_t C) { return C <= 1024 ? 4096 : 1024; }
+// threads of a row
+int row_threads(int64_t C) {
+  return C <= 512 ? 64 : C <= 1024 ? 128 : C <= 2048 ? 256 : C <= 4096 ? 512 : 1024;
+}
+
+// Rows of a strip: as many strips as four waves a SIMD make resident at once, so that
+// all of them run from the first row to the last; one row each where there are fewer.
 int strip_rows(int64_t M, int64_t C) {
-  const int64_t s = strips_wanted(C);
-  return (int)((M + s - 1) / s);
+  const int64_t s = 256 * 16 * 64 / row_threads(C);
+  return M > s ? (int)((M + s - 1) / s) : 1;
+}
+
+int64_t strip_count(int64_t M, int64_t C) {
+  const int64_t rows = strip_rows(M, C);
+  return (M + rows - 1) / rows;
+}
+
+// 16-byte loads of the tables
+bool tables_vec(int64_t C, int64_t ldt, std::initializer_list<const float*> tables) {
+  for (const float* p : tables)
+    if (!aligned16(p)) return false;
+  return C % 8 == 0 && ldt % 4 == 0;
 }
 
 int32_t check_norm(int32_t dtype, int64_t M, int64_t C, int32_t post, int32_t pre, int32_t G,
@@ -532,7 +610,7 @@ int32_t check_norm(int32_t dtype, int64_t M, int64_t C, int32_t post, int32_t pr
     return fail(ASP_ERR_SHAPE, "C=%lld outside [1, %d]", (long long)C, kMaxNormC);
   if (post < ASP_NORM_NONE || post > ASP_NORM_LAYER) return fail(ASP_ERR_ARG, "post=%d", post);
   if (pre < ASP_NORM_NONE || pre > ASP_NORM_LAYER) return fail(ASP_ERR_ARG, "pre=%d", pre);
-  if (G < 1 || G > 65536) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65536]", G);
+  if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
   if (!offsets && G != 1) return fail(ASP_ERR_ARG, "offsets is NULL with G=%d sequences", G);
   if (offsets && ((uintptr_t)offsets & 3)) return fail(ASP_ERR_ALIGN, "offsets is not 4-byte aligned");
   if (ldt < (G > 1 ? C : 0) || ldt > INT32_MAX)
@@ -547,27 +625,25 @@ int32_t check_vec(const float* p, const char* name) {
 
 template <typename XT, bool VEC>
 int32_t launch_norm(const NormArgs& a, hipStream_t st) {
-  const int64_t strips = (a.M + a.rows - 1) / a.rows;
-  const dim3 one((unsigned)strips), four((unsigned)((strips + 3) / 4));
-  if (a.C <= 512) k_norm_gate<XT, 64, 1, VEC><<<four, 256, 0, st>>>(a);
-  else if (a.C <= 1024) k_norm_gate<XT, 64, 2, VEC><<<four, 256, 0, st>>>(a);
-  else if (a.C <= 2048) k_norm_gate<XT, 256, 1, VEC><<<one, 256, 0, st>>>(a);
-  else if (a.C <= 4096) k_norm_gate<XT, 256, 2, VEC><<<one, 256, 0, st>>>(a);
-  else if (a.C <= 8192) k_norm_gate<XT, 512, 2, VEC><<<one, 512, 0, st>>>(a);
-  else k_norm_gate<XT, 512, 4, VEC><<<one, 512, 0, st>>>(a);
+  const dim3 grid((unsigned)strip_count(a.M, a.C));
+  if (a.C <= 512) k_norm_gate<XT, 64, 1, VEC><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 1024) k_norm_gate<XT, 128, 1, VEC><<<grid, 128, 0, st>>>(a);
+  else if (a.C <= 2048) k_norm_gate<XT, 256, 1, VEC><<<grid, 256, 0, st>>>(a);
+  else if (a.C <= 4096) k_norm_gate<XT, 512, 1, VEC><<<grid, 512, 0, st>>>(a);
+  else if (a.C <= 8192) k_norm_gate<XT, 1024, 1, VEC><<<grid, 1024, 0, st>>>(a);
+  else k_norm_gate<XT, 1024, 2, VEC><<<grid, 1024, 0, st>>>(a);
   return launch_status("norm");
 }
 
 template <typename XT, typename NT, bool VEC>
 int32_t launch_back(const NormArgs& a, hipStream_t st) {
-  const int64_t strips = (a.M + a.rows - 1) / a.rows;
-  const dim3 one((unsigned)strips), four((unsigned)((strips + 3) / 4));
-  if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1, VEC><<<four, 256, 0, st>>>(a);
-  else if (a.C <= 1024) k_norm_gate_back<XT, NT, 64, 2, VEC><<<four, 256, 0, st>>>(a);
-  else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1, VEC><<<one, 256, 0, st>>>(a);
-  else if (a.C <= 4096) k_norm_gate_back<XT, NT, 256, 2, VEC><<<one, 256, 0, st>>>(a);
-  else if (a.C <= 8192) k_norm_gate_back<XT, NT, 512, 2, VEC><<<one, 512, 0, st>>>(a);
-  else k_norm_gate_back<XT, NT, 512, 4, VEC><<<one, 512, 0, st>>>(a);
+  const dim3 grid((unsigned)strip_count(a.M, a.C));
+  if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1, VEC><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 1024) k_norm_gate_back<XT, NT, 128, 1, VEC><<<grid, 128, 0, st>>>(a);
+  else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1, VEC><<<grid, 256, 0, st>>>(a);
+  else if (a.C <= 4096) k_norm_gate_back<XT, NT, 512, 1, VEC><<<grid, 512, 0, st>>>(a);
+  else if (a.C <= 8192) k_norm_gate_back<XT, NT, 1024, 1, VEC><<<grid, 1024, 0, st>>>(a);
+  else k_norm_gate_back<XT, NT, 1024, 2, VEC><<<grid, 1024, 0, st>>>(a);
   return launch_status("norm backward");
 }
 
@@ -621,6 +697,7 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
   a.ldx = ldx; a.ldy = ldy; a.ldh = ldh; a.ldn = ldn; a.ldt = ldt; a.alpha = alpha; a.eps = eps;
   a.M = (int)M; a.C = (int)C; a.G = G; a.post = post; a.pre = pre; a.n_dtype = n_dtype;
   a.rows = strip_rows(M, C);
+  a.tvec = tables_vec(C, ldt, {post_w, gate, pre_w, pre_b, scale, shift});
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == ASP_BF16) return vec ? launch_norm<uint16_t, true>(a, st) : launch_norm<uint16_t, false>(a, st);
   return vec ? launch_norm<float, true>(a, st) : launch_norm<float, false>(a, st);
@@ -629,10 +706,10 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
 int32_t asp_norm_gate_backward_workspace_bytes(int64_t M, int64_t C, int32_t G, size_t* bytes) {
   clear_error();
   ASP_TRY(check_norm(ASP_F32, M, C, 0, 0, 1, nullptr, 0, 0.0f));
-  if (G < 1 || G > 65536) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65536]", G);
+  if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
   if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
-  const int64_t rows = M ? strip_rows(M, C) : 1;
-  *bytes = up256((size_t)((M + rows - 1) / rows + G) * 3 * C * 4);
+  // a slot for each pair of a strip and a sequence that it touches, and the sequences' sums
+  *bytes = up256((size_t)(strip_count(M, C) + G + (G > 1 ? G : 0)) * 3 * C * 4);
   return ASP_OK;
 }
 
@@ -691,7 +768,8 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   a.alpha = alpha; a.eps = eps; a.M = (int)M; a.C = (int)C; a.G = G; a.post = post; a.pre = pre;
   a.dh = dh; a.dn = dn; a.dx = dx; a.dy = dy; a.lddh = lddh; a.lddn = lddn; a.lddx = lddx;
   a.lddy = lddy; a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  a.rows = M ? strip_rows(M, C) : 1;
+  a.rows = strip_rows(M, C);
+  a.tvec = tables_vec(C, ldt, {post_w, gate, pre_w, scale});
   if (M > 0) {
     int32_t s;
     const bool n16 = dn_dtype == ASP_BF16;
@@ -705,12 +783,14 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   }
   if (!sums) return ASP_OK;
   SumArgs k = {};
-  k.part = static_cast<const float*>(workspace);
+  k.part = static_cast<float*>(workspace);
   k.post_w = post_w; k.gate = gate; k.pre_w = pre_w; k.pre_b = pre_b; k.scale = scale;
   k.offsets = offsets; k.d_post_w = d_post_w; k.d_gate = d_gate; k.d_pre_w = d_pre_w;
   k.d_pre_b = d_pre_b; k.d_scale = d_scale; k.d_shift = d_shift; k.ldt = ldt; k.ldd = ldd;
-  k.M = (int)M; k.C = (int)C; k.G = G; k.rows = a.rows; k.post = post;
-  k_norm_sums<<<dim3((unsigned)((C + 15) / 16)), 256, 0, st>>>(k);
+  k.M = (int)M; k.C = (int)C; k.G = G; k.rows = a.rows; k.slots = strip_count(M, C) + G;
+  k_norm_sums<<<dim3((unsigned)((C + 15) / 16), (unsigned)G), 256, 0, st>>>(k);
+  if (G > 1 && (d_pre_w || d_pre_b || d_post_w))
+    k_norm_weight_sums<<<dim3((unsigned)((C + 63) / 64)), 64, 0, st>>>(k);
   return launch_status("norm column sums");
 }
 
