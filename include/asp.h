@@ -505,9 +505,8 @@ int32_t asp_svdq_forward(const void* x, int32_t x_dtype, int64_t M, int64_t K, i
  *     the backward and the transposed form contract over rows, so they take
  *     at most 2^20 of them (and N at most 2^20);
  *   - float32 and bf16 matrices and float32 vectors need the alignment of their
- *     elements only, and input matrices any row stride ld >= their width
- *     (16-byte aligned rows of a multiple of 8 elements are read in 16-byte
- *     loads); outputs are contiguous.  Codes and scales are 16-byte aligned;
+ *     elements only, and input matrices any row stride ld >= their width;
+ *     outputs are contiguous.  Codes and scales are 16-byte aligned;
  *   - inputs need not be finite: a NaN or infinity makes NaN of the results
  *     that contract over it, and of no others;
  *   - results are the same bits on every call with the same arguments.

@@ -72,43 +72,60 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast
 __device__ __forceinline__ float bf16_hi(uint32_t w) {
   return __builtin_bit_cast(float, w & 0xFFFF0000u);
 }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_lo(v); }
 
-// eight consecutive elements at p, `left` of them inside the row (the rest read
-// as 0).  VEC: p is 16-byte aligned and left is >= 8 or <= 0.
-template <bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t left, float (&v)[8]) {
-  if constexpr (VEC) {
-    u32x4_t w = {0u, 0u, 0u, 0u};
-    if (left > 0) w = *reinterpret_cast<const u32x4_t*>(p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = bf16_lo(w[e]);
-      v[2 * e + 1] = bf16_hi(w[e]);
+// 16 bytes at an address aligned to an element only: the memory takes any, and an
+// aligned one costs the same as if it were known to be
+typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// eight consecutive elements as they lie in memory
+template <typename XT>
+struct Raw {
+  u32x4_t q[sizeof(XT) / 2];
+};
+
+// at p, `left` of them inside the row; the rest are 0 where left > 0, and r is left
+// as it is where left <= 0
+template <typename XT>
+__device__ __forceinline__ void raw_load(const XT* p, int left, Raw<XT>& r) {
+  if (left >= 8) {
+    if constexpr (sizeof(XT) == 2) {
+      r.q[0] = *reinterpret_cast<const u32x4_e2*>(p);
+    } else {
+      r.q[0] = *reinterpret_cast<const u32x4_e4*>(p);
+      r.q[1] = *reinterpret_cast<const u32x4_e4*>(p + 4);
     }
-  } else {
+  } else if (left > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? bf16_lo(p[e]) : 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(XT) == 2) {
+        const uint32_t w = e < left ? p[e] : 0u;
+        r.q[0][e >> 1] = e & 1 ? r.q[0][e >> 1] | w << 16 : w;
+      } else {
+        r.q[e >> 2][e & 3] = e < left ? __builtin_bit_cast(uint32_t, p[e]) : 0u;
+      }
+    }
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int64_t left, float (&v)[8]) {
-  if constexpr (VEC) {
-    f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
-    if (left > 0) {
-      a = *reinterpret_cast<const f32x4_t*>(p);
-      b = *reinterpret_cast<const f32x4_t*>(p + 4);
-    }
+
+template <typename XT>
+__device__ __forceinline__ void unpack(const Raw<XT>& r, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = a[e];
-      v[4 + e] = b[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.0f;
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t w = sizeof(XT) == 2 ? r.q[0][e >> 1] : r.q[(sizeof(XT) / 2 - 1) & (e >> 2)][e & 3];
+    if constexpr (sizeof(XT) == 2)
+      v[e] = e & 1 ? bf16_hi(w) : bf16_lo(w);
+    else
+      v[e] = __builtin_bit_cast(float, w);
   }
+}
+
+// eight elements, 0 from `left` on
+template <typename XT>
+__device__ __forceinline__ void load8(const XT* p, int left, float (&v)[8]) {
+  Raw<XT> r = {};
+  raw_load(p, left, r);
+  unpack(r, v);
 }
 
 // ------------------------------------------------------------- host helpers
@@ -128,11 +145,6 @@ inline int32_t check_matrix(const void* p, int32_t dtype, int64_t cols, int64_t 
     return fail(ASP_ERR_SHAPE, "row stride %lld of %s outside [%lld, 2^31)", (long long)ld, name,
                 (long long)cols);
   return ASP_OK;
-}
-
-// 8-element runs of every row are 16-byte aligned and lie wholly inside or past it
-inline bool vec8_ok(const void* p, int32_t dtype, int64_t cols, int64_t ld) {
-  return aligned16(p) && cols % 8 == 0 && ld % (dtype == ASP_BF16 ? 8 : 4) == 0;
 }
 
 // rows >= 0 and 1 <= cols <= 2^20 of a matrix in the 8-bit format

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(256) k_fp8_join(const GemmK g) {
 // 64 + 16 (l / 16).  XT = uint8_t reads x's codes; otherwise x itself is read and
 // quantised in registers, with the same arithmetic as the row quantiser: a row's
 // block is in the four lanes l % 16 + 16 q, two shuffles find its maximum.
-template <int W, typename XT, bool VEC, bool WIDE>
+template <int W, typename XT, bool WIDE>
 __global__ void __launch_bounds__(64 * W)
     k_fp8_few(const GemmK g, const XT* __restrict__ x, int64_t ldx, int K) {
   constexpr int U = 4;  // blocks of a wave in flight
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(64 * W)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int64_t at = (int64_t)kb * kFp8Block + 64 * (c >> 1) + 16 * q + 8 * (c & 1);
-          load8<VEC>(x + m * ldx + at, K - at, v[c]);
+          load8(x + m * ldx + at, K - at, v[c]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v[c][e]));
         }
@@ -408,18 +408,18 @@ int32_t launch_tiles(GemmK k, hipStream_t st) {
   return launch_status("fp8 gemm");
 }
 
-template <typename XT, bool VEC, bool WIDE>
+template <typename XT, bool WIDE>
 void launch_few_as(const GemmK& k, const XT* x, int64_t ldx, int64_t K, hipStream_t st) {
   const dim3 grid((unsigned)((k.N + 15) / 16));
-  if (k.KB >= 16) k_fp8_few<16, XT, VEC, WIDE><<<grid, 1024, 0, st>>>(k, x, ldx, (int)K);
-  else if (k.KB >= 8) k_fp8_few<8, XT, VEC, WIDE><<<grid, 512, 0, st>>>(k, x, ldx, (int)K);
-  else k_fp8_few<4, XT, VEC, WIDE><<<grid, 256, 0, st>>>(k, x, ldx, (int)K);
+  if (k.KB >= 16) k_fp8_few<16, XT, WIDE><<<grid, 1024, 0, st>>>(k, x, ldx, (int)K);
+  else if (k.KB >= 8) k_fp8_few<8, XT, WIDE><<<grid, 512, 0, st>>>(k, x, ldx, (int)K);
+  else k_fp8_few<4, XT, WIDE><<<grid, 256, 0, st>>>(k, x, ldx, (int)K);
 }
 
-template <typename XT, bool VEC>
+template <typename XT>
 int32_t launch_few(const GemmK& k, const XT* x, int64_t ldx, int64_t K, hipStream_t st) {
-  if (k.y_bf16) launch_few_as<XT, VEC, false>(k, x, ldx, K, st);
-  else launch_few_as<XT, VEC, true>(k, x, ldx, K, st);
+  if (k.y_bf16) launch_few_as<XT, false>(k, x, ldx, K, st);
+  else launch_few_as<XT, true>(k, x, ldx, K, st);
   return launch_status("fp8 few-row gemm");
 }
 
@@ -436,15 +436,9 @@ size_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
 int32_t fp8_gemm_fused(const Fp8Gemm& g, const void* x, int32_t x_dtype, int64_t ldx,
                        hipStream_t st) {
   const GemmK k = kernel_args(g, 1);
-  const bool vec = vec8_ok(x, x_dtype, g.K, ldx);
-  if (x_dtype == ASP_BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(x);
-    return vec ? launch_few<uint16_t, true>(k, p, ldx, g.K, st)
-               : launch_few<uint16_t, false>(k, p, ldx, g.K, st);
-  }
-  const float* p = static_cast<const float*>(x);
-  return vec ? launch_few<float, true>(k, p, ldx, g.K, st)
-             : launch_few<float, false>(k, p, ldx, g.K, st);
+  if (x_dtype == ASP_BF16)
+    return launch_few(k, static_cast<const uint16_t*>(x), ldx, g.K, st);
+  return launch_few(k, static_cast<const float*>(x), ldx, g.K, st);
 }
 
 namespace {
@@ -460,7 +454,7 @@ int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
 
 int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
   if (g.M <= kFewRows)
-    return launch_few<uint8_t, true>(kernel_args(g, 1), g.a, 0, g.K, st);
+    return launch_few(kernel_args(g, 1), g.a, 0, g.K, st);
   const Plan p = plan(g.M, g.N, g.K);
   const GemmK k = kernel_args(g, p.slices);
   ASP_TRY(k.y_bf16 ? launch_plan<false>(p, k, st) : launch_plan<true>(p, k, st));

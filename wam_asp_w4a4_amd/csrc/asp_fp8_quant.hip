@@ -11,7 +11,7 @@ namespace {
 // (16-byte loads in bf16), a block for each 16 lanes, whose maximum is four DPP
 // rotations, and the four blocks' scale bytes make the one dword that the
 // scale layout keeps together.
-template <typename XT, bool VEC>
+template <typename XT>
 __global__ void __launch_bounds__(256)
     k_fp8_rows(const XT* __restrict__ x, int64_t rows, int cols, int64_t ld, int groups,
                uint8_t* __restrict__ codes, uint32_t* __restrict__ scales) {
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256)
   const int c0 = 512 * g + 8 * lane;
   const int pitch = (cols + kFp8Block - 1) / kFp8Block * kFp8Block;
   float v[8];
-  load8<VEC>(x + row * ld + c0, cols - c0, v);
+  load8(x + row * ld + c0, cols - c0, v);
   uint32_t u = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) u = max(u, finite_bits(v[e]));
@@ -61,16 +61,11 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (
   const int rb = tile / ncb, cb = tile % ncb;
   const int64_t r0 = (int64_t)rb * 128 + 8 * rg, c0 = (int64_t)cb * 128 + 8 * cg;
   const XT* x = static_cast<const XT*>(j.in);
-  const bool vec = ((uintptr_t)x & 15) == 0 && j.cols % 8 == 0 && j.ld % (16 / sizeof(XT)) == 0;
   float v[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t left = r0 + i < j.rows ? j.cols - c0 : 0;
-    const XT* p = x + (r0 + i) * j.ld + c0;
-    if (vec)
-      load8<true>(p, left, v[i]);
-    else
-      load8<false>(p, left, v[i]);
+    load8(x + (r0 + i) * j.ld + c0, left, v[i]);
   }
   // magnitudes: per row (this thread's 8 columns) and per column (its 8 rows)
   uint32_t ru[8], cu[8];
@@ -227,16 +222,12 @@ int32_t fp8_quantize_rows(const void* in, int32_t dtype, int64_t rows, int64_t c
   if (blocks > INT32_MAX) return fail(ASP_ERR_SHAPE, "input too large for one launch");
   const dim3 grid((unsigned)blocks);
   uint32_t* sc = reinterpret_cast<uint32_t*>(scales);
-  const bool vec = vec8_ok(in, dtype, cols, ld);
-  if (dtype == ASP_BF16) {
-    const uint16_t* x = static_cast<const uint16_t*>(in);
-    if (vec) k_fp8_rows<uint16_t, true><<<grid, 256, 0, st>>>(x, rows, (int)cols, ld, groups, codes, sc);
-    else k_fp8_rows<uint16_t, false><<<grid, 256, 0, st>>>(x, rows, (int)cols, ld, groups, codes, sc);
-  } else {
-    const float* x = static_cast<const float*>(in);
-    if (vec) k_fp8_rows<float, true><<<grid, 256, 0, st>>>(x, rows, (int)cols, ld, groups, codes, sc);
-    else k_fp8_rows<float, false><<<grid, 256, 0, st>>>(x, rows, (int)cols, ld, groups, codes, sc);
-  }
+  if (dtype == ASP_BF16)
+    k_fp8_rows<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(in), rows, (int)cols, ld,
+                                               groups, codes, sc);
+  else
+    k_fp8_rows<float><<<grid, 256, 0, st>>>(static_cast<const float*>(in), rows, (int)cols, ld,
+                                            groups, codes, sc);
   return launch_status("fp8 row quantise");
 }
 

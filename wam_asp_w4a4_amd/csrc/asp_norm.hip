@@ -14,14 +14,10 @@
 // Everything is bound by memory: a row is read once, held in registers through
 // both norms (a layer norm's variance is summed around its mean, not as a
 // difference of squares), and written once.  A workgroup walks a strip of
-// consecutive rows, one row at a time with the next one's loads in flight; the
-// tables of the strip's sequence stay in registers (read anew for each row they
-// cost more cache traffic than the row: 653 against XXX us for the backward of
-// 16384 x 4096 bf16).  T threads share a row, 8 columns each (E = 2: 16, above 8192
+// consecutive rows; the tables of the strip's sequence stay in registers (read anew
+// for each row they cost more cache traffic than the row itself).  T threads share a row, 8 columns each (E = 2: 16, above 8192
 // columns): a thread's share of a row, its tables and its column sums are then
 // few enough registers for four waves a SIMD.
-#include <initializer_list>
-
 #include "asp_fp8.h"
 
 namespace asp {
@@ -35,7 +31,7 @@ struct NormArgs {
   uint8_t* n_scales;
   int64_t ldx, ldy, ldh, ldn, ldt;
   float alpha, eps;
-  int M, C, G, post, pre, n_dtype, rows, tvec;  // rows: of a strip; tvec: 16-byte table loads
+  int M, C, G, post, pre, n_dtype, rows;  // rows: of a strip
   // backward
   const void *dh, *dn;
   void *dx, *dy;
@@ -97,97 +93,52 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int G, int ro
   return lo;
 }
 
-// 8 elements of a row as they lie in memory
-template <typename XT>
-struct Raw {
-  u32x4_t q[sizeof(XT) / 2];
-};
-
-template <typename XT, bool VEC>
-__device__ __forceinline__ void raw_load(const XT* p, int left, Raw<XT>& r) {
-  if constexpr (VEC) {
-    if (left > 0)
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(XT) / 2; ++i) r.q[i] = reinterpret_cast<const u32x4_t*>(p)[i];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(XT) == 2) {
-        const uint32_t w = e < left ? p[e] : 0u;
-        r.q[0][e >> 1] = e & 1 ? r.q[0][e >> 1] | w << 16 : w;
-      } else {
-        r.q[e >> 2][e & 3] = e < left ? __builtin_bit_cast(uint32_t, p[e]) : 0u;
-      }
-    }
-  }
-}
-
-template <typename XT>
-__device__ __forceinline__ void unpack(const Raw<XT>& r, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t w = sizeof(XT) == 2 ? r.q[0][e >> 1] : r.q[(sizeof(XT) / 2 - 1) & (e >> 2)][e & 3];
-    if constexpr (sizeof(XT) == 2)
-      v[e] = e & 1 ? bf16_hi(w) : bf16_lo(w);
-    else
-      v[e] = __builtin_bit_cast(float, w);
-  }
-}
-
 // a thread's columns of a row: E chunks of 8, chunk e at column 8 (e T + t)
-template <typename XT, int E, int T, bool VEC>
+template <typename XT, int E, int T>
 __device__ __forceinline__ void row_load(const void* p, int64_t row, int64_t ld, int C, int t,
                                          Raw<XT> (&r)[E]) {
+  const XT* base = static_cast<const XT*>(p) + row * ld;  // uniform
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int c = (e * T + t) * 8;
-    raw_load<XT, VEC>(static_cast<const XT*>(p) + row * ld + c, C - c, r[e]);
+    const uint32_t c = (uint32_t)(e * T + t) * 8u;
+    raw_load(base + c, C - (int)c, r[e]);
   }
 }
 
 template <int E, int T>
-__device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, bool vec,
-                                      float other, float (&v)[E][8]) {
+__device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, float other,
+                                      float (&v)[E][8]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = (e * T + t) * 8;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[e][k] = other;
     if (!p || c >= C) continue;
-    if (vec) {
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + at + c);
-      const f32x4_t b = *reinterpret_cast<const f32x4_t*>(p + at + c + 4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[e][k] = a[k];
-        v[e][4 + k] = b[k];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < C) v[e][k] = p[at + c + k];
-    }
+    Raw<float> r = {};
+    raw_load(p + at + c, C - c, r);
+    unpack(r, v[e]);
   }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(void* p, int64_t at, bool bf16, int left, const float (&v)[8]) {
-  if (left <= 0) return;
+// 8 values to element c of a row that ends after `left` more
+__device__ __forceinline__ void store8(void* p, int64_t row, uint32_t c, bool bf16, int left,
+                                       const float (&v)[8]) {
   if (bf16) {
-    uint16_t* d = static_cast<uint16_t*>(p) + at;
-    if constexpr (VEC) {
-      *reinterpret_cast<u32x4_t*>(d) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
-                                               bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+    uint16_t* d = static_cast<uint16_t*>(p) + row + c;
+    if (left >= 8) {
+      *reinterpret_cast<u32x4_e2*>(d) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                                bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < left) d[k] = bf16_rne(v[k]);
     }
   } else {
-    float* d = static_cast<float*>(p) + at;
-    if constexpr (VEC) {
-      *reinterpret_cast<f32x4_t*>(d) = f32x4_t{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_t*>(d + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    float* d = static_cast<float*>(p) + row + c;
+    if (left >= 8) {
+      auto bits = [&](int k) { return __builtin_bit_cast(uint32_t, v[k]); };
+      *reinterpret_cast<u32x4_e4*>(d) = u32x4_t{bits(0), bits(1), bits(2), bits(3)};
+      *reinterpret_cast<u32x4_e4*>(d + 4) = u32x4_t{bits(4), bits(5), bits(6), bits(7)};
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -234,7 +185,7 @@ __device__ __forceinline__ void normalise(float (&v)[E][8], int kind, int C, flo
   each<E>([&](int e, int k) { v[e][k] *= r; });
 }
 
-template <typename XT, int T, int E, bool VEC>
+template <typename XT, int T, int E>
 __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
   __shared__ SumsLds lds;
   const int t = threadIdx.x;
@@ -245,8 +196,8 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
   float gp[E][8], pa[E][8], pc[E][8];
   Raw<XT> nx[E] = {}, ny[E] = {};
   auto fetch = [&](int64_t row) {
-    row_load<XT, E, T, VEC>(a.x, row, a.ldx, a.C, t, nx);
-    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, ny);
+    row_load<XT, E, T>(a.x, row, a.ldx, a.C, t, nx);
+    if (a.y) row_load<XT, E, T>(a.y, row, a.ldy, a.C, t, ny);
   };
   fetch(r0);
   int64_t begin = 0, end = 0;
@@ -261,16 +212,15 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
       } else {
         end = a.M;
       }
-      const bool tv = a.tvec;
       float u[E][8], w[E][8];
       // v gate post_w, and (v w + b) (1 + scale) + shift = v pa + pc
-      table<E, T>(a.gate, g * a.ldt, a.C, t, tv, 1.0f, gp);
-      table<E, T>(a.post_w, 0, a.C, t, tv, 1.0f, u);
+      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
+      table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
       each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
-      table<E, T>(a.pre_w, 0, a.C, t, tv, 1.0f, pa);
-      table<E, T>(a.pre_b, 0, a.C, t, tv, 0.0f, pc);
-      table<E, T>(a.scale, g * a.ldt, a.C, t, tv, 0.0f, u);
-      table<E, T>(a.shift, g * a.ldt, a.C, t, tv, 0.0f, w);
+      table<E, T>(a.pre_w, 0, a.C, t, 1.0f, pa);
+      table<E, T>(a.pre_b, 0, a.C, t, 0.0f, pc);
+      table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
+      table<E, T>(a.shift, g * a.ldt, a.C, t, 0.0f, w);
       each<E>([&](int e, int k) {
         pa[e][k] *= 1.0f + u[e][k];
         pc[e][k] = __builtin_fmaf(pc[e][k], 1.0f + u[e][k], w[e][k]);
@@ -301,7 +251,7 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = (e * T + t) * 8;
-        store8<VEC>(a.h, row * a.ldh + c, sizeof(XT) == 2, a.C - c, v[e]);
+        store8(a.h, row * a.ldh, c, sizeof(XT) == 2, a.C - c, v[e]);
       }
     if (a.pre == ASP_NORM_NONE) continue;
     normalise<E, T>(v, a.pre, a.C, a.eps, t, lds, slot);
@@ -310,7 +260,7 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int c = (e * T + t) * 8;
-        store8<VEC>(a.n, row * a.ldn + c, a.n_dtype == ASP_BF16, a.C - c, v[e]);
+        store8(a.n, row * a.ldn, c, a.n_dtype == ASP_BF16, a.C - c, v[e]);
       }
       continue;
     }
@@ -349,8 +299,12 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
 // touches, to slot strip + g (strips and sequences both advance along the rows,
 // so no two pairs share one).  k_norm_sums adds the strips in order: the
 // results do not depend on scheduling.
-template <typename XT, typename NT, int T, int E, bool VEC>
+template <typename XT, typename NT, int T, int E>
 __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
+  // the next row's loads in flight where a row is few enough registers (8192 x 8192 bf16,
+  // layer norms: 193 against 226 us); in float32 they cost registers that other waves
+  // need (16384 x 4096: 368 against 346 us)
+  constexpr bool kAhead = E == 1 && sizeof(XT) == 2;
   __shared__ SumsLds lds;
   const int t = threadIdx.x;
   int slot = 0;
@@ -362,28 +316,27 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
   const bool prel = a.pre == ASP_NORM_LAYER, postl = a.post == ASP_NORM_LAYER;
   float gp[E][8], pa[E][8], s1[E][8], s2[E][8], s3[E][8];
   auto flush = [&](int g) {
-    float* d = a.part + (int64_t)(strip + g) * 3 * a.C;
-    each<E>([&](int e, int k) {
-      const int c = (e * T + t) * 8 + k;
-      if (c < a.C) {
-        d[c] = s1[e][k];
-        d[a.C + c] = s2[e][k];
-        d[2 * (int64_t)a.C + c] = s3[e][k];
-      }
-    });
+    const int64_t at = (int64_t)(strip + g) * 3 * a.C;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t c = (uint32_t)(e * T + t) * 8u;
+      store8(a.part, at, c, false, a.C - (int)c, s1[e]);
+      store8(a.part, at + a.C, c, false, a.C - (int)c, s2[e]);
+      store8(a.part, at + 2 * (int64_t)a.C, c, false, a.C - (int)c, s3[e]);
+    }
   };
   // dh and y not given, and h and dn without a pre norm, stay 0
   Raw<XT> rd[E] = {}, ry[E] = {}, rh[E] = {};
   Raw<NT> rn[E] = {};
   auto fetch = [&](int64_t row) {
-    if (a.dh) row_load<XT, E, T, VEC>(a.dh, row, a.lddh, a.C, t, rd);
-    if (a.y) row_load<XT, E, T, VEC>(a.y, row, a.ldy, a.C, t, ry);
+    if (a.dh) row_load<XT, E, T>(a.dh, row, a.lddh, a.C, t, rd);
+    if (a.y) row_load<XT, E, T>(a.y, row, a.ldy, a.C, t, ry);
     if (pre) {
-      row_load<XT, E, T, VEC>(a.h, row, a.ldh, a.C, t, rh);
-      row_load<NT, E, T, VEC>(a.dn, row, a.lddn, a.C, t, rn);
+      row_load<XT, E, T>(a.h, row, a.ldh, a.C, t, rh);
+      row_load<NT, E, T>(a.dn, row, a.lddn, a.C, t, rn);
     }
   };
-  fetch(r0);
+  if constexpr (kAhead) fetch(r0);
   int g = -1;
   int64_t begin = 0, end = 0;
   for (int64_t row = r0; row < r1; ++row) {
@@ -401,18 +354,18 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
       } else {
         end = a.M;
       }
-      const bool tv = a.tvec;
       float u[E][8];
-      table<E, T>(a.gate, g * a.ldt, a.C, t, tv, 1.0f, gp);
-      table<E, T>(a.post_w, 0, a.C, t, tv, 1.0f, u);
+      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
+      table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
       each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
-      table<E, T>(a.pre_w, 0, a.C, t, tv, 1.0f, pa);
-      table<E, T>(a.scale, g * a.ldt, a.C, t, tv, 0.0f, u);
+      table<E, T>(a.pre_w, 0, a.C, t, 1.0f, pa);
+      table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
       each<E>([&](int e, int k) {
         pa[e][k] *= 1.0f + u[e][k];
         s1[e][k] = s2[e][k] = s3[e][k] = 0.0f;
       });
     }
+    if constexpr (!kAhead) fetch(row);
     float d[E][8], v[E][8], n[E][8], q[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -421,7 +374,7 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
       unpack(rh[e], v[e]);
       unpack(rn[e], n[e]);
     }
-    if (row + 1 < r1) fetch(row + 1);
+    if (kAhead && row + 1 < r1) fetch(row + 1);
     if (row < begin) continue;
     if (prel || postl) {
       float s[2] = {0.0f, 0.0f};
@@ -460,7 +413,7 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = a.alpha * d[e][k];
-        store8<VEC>(a.dx, row * a.lddx + c, sizeof(XT) == 2, a.C - c, o);
+        store8(a.dx, row * a.lddx, c, sizeof(XT) == 2, a.C - c, o);
       }
     if (!a.y) continue;
     float r = 1.0f;
@@ -487,7 +440,7 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = (e * T + t) * 8;
-      store8<VEC>(a.dy, row * a.lddy + c, sizeof(XT) == 2, a.C - c, d[e]);
+      store8(a.dy, row * a.lddy, c, sizeof(XT) == 2, a.C - c, d[e]);
     }
   }
   if (g >= 0 && a.part) flush(g);
@@ -595,13 +548,6 @@ int64_t strip_count(int64_t M, int64_t C) {
   return (M + rows - 1) / rows;
 }
 
-// 16-byte loads of the tables
-bool tables_vec(int64_t C, int64_t ldt, std::initializer_list<const float*> tables) {
-  for (const float* p : tables)
-    if (!aligned16(p)) return false;
-  return C % 8 == 0 && ldt % 4 == 0;
-}
-
 int32_t check_norm(int32_t dtype, int64_t M, int64_t C, int32_t post, int32_t pre, int32_t G,
                    const int32_t* offsets, int64_t ldt, float eps) {
   ASP_TRY(check_io_dtype(dtype, "dtype"));
@@ -623,27 +569,27 @@ int32_t check_vec(const float* p, const char* name) {
   return (uintptr_t)p & 3 ? fail(ASP_ERR_ALIGN, "%s is not aligned to its elements", name) : ASP_OK;
 }
 
-template <typename XT, bool VEC>
+template <typename XT>
 int32_t launch_norm(const NormArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)strip_count(a.M, a.C));
-  if (a.C <= 512) k_norm_gate<XT, 64, 1, VEC><<<grid, 64, 0, st>>>(a);
-  else if (a.C <= 1024) k_norm_gate<XT, 128, 1, VEC><<<grid, 128, 0, st>>>(a);
-  else if (a.C <= 2048) k_norm_gate<XT, 256, 1, VEC><<<grid, 256, 0, st>>>(a);
-  else if (a.C <= 4096) k_norm_gate<XT, 512, 1, VEC><<<grid, 512, 0, st>>>(a);
-  else if (a.C <= 8192) k_norm_gate<XT, 1024, 1, VEC><<<grid, 1024, 0, st>>>(a);
-  else k_norm_gate<XT, 1024, 2, VEC><<<grid, 1024, 0, st>>>(a);
+  if (a.C <= 512) k_norm_gate<XT, 64, 1><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 1024) k_norm_gate<XT, 128, 1><<<grid, 128, 0, st>>>(a);
+  else if (a.C <= 2048) k_norm_gate<XT, 256, 1><<<grid, 256, 0, st>>>(a);
+  else if (a.C <= 4096) k_norm_gate<XT, 512, 1><<<grid, 512, 0, st>>>(a);
+  else if (a.C <= 8192) k_norm_gate<XT, 1024, 1><<<grid, 1024, 0, st>>>(a);
+  else k_norm_gate<XT, 1024, 2><<<grid, 1024, 0, st>>>(a);
   return launch_status("norm");
 }
 
-template <typename XT, typename NT, bool VEC>
+template <typename XT, typename NT>
 int32_t launch_back(const NormArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)strip_count(a.M, a.C));
-  if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1, VEC><<<grid, 64, 0, st>>>(a);
-  else if (a.C <= 1024) k_norm_gate_back<XT, NT, 128, 1, VEC><<<grid, 128, 0, st>>>(a);
-  else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1, VEC><<<grid, 256, 0, st>>>(a);
-  else if (a.C <= 4096) k_norm_gate_back<XT, NT, 512, 1, VEC><<<grid, 512, 0, st>>>(a);
-  else if (a.C <= 8192) k_norm_gate_back<XT, NT, 1024, 1, VEC><<<grid, 1024, 0, st>>>(a);
-  else k_norm_gate_back<XT, NT, 1024, 2, VEC><<<grid, 1024, 0, st>>>(a);
+  if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 1024) k_norm_gate_back<XT, NT, 128, 1><<<grid, 128, 0, st>>>(a);
+  else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1><<<grid, 256, 0, st>>>(a);
+  else if (a.C <= 4096) k_norm_gate_back<XT, NT, 512, 1><<<grid, 512, 0, st>>>(a);
+  else if (a.C <= 8192) k_norm_gate_back<XT, NT, 1024, 1><<<grid, 1024, 0, st>>>(a);
+  else k_norm_gate_back<XT, NT, 1024, 2><<<grid, 1024, 0, st>>>(a);
   return launch_status("norm backward");
 }
 
@@ -674,15 +620,12 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
   ASP_TRY(check_matrix(x, dtype, C, ldx, "x"));
   if (y) ASP_TRY(check_matrix(y, dtype, C, ldy, "y"));
   if (h) ASP_TRY(check_matrix(h, dtype, C, ldh, "h"));
-  bool vec = vec8_ok(x, dtype, C, ldx) && (!y || vec8_ok(y, dtype, C, ldy)) &&
-             (!h || vec8_ok(h, dtype, C, ldh));
   if (pre != ASP_NORM_NONE) {
     if (n_dtype == ASP_E4M3) {
       ASP_TRY(check_ptr(n, "n", true));
       ASP_TRY(check_ptr(n_scales, "n_scales", true));
     } else {
       ASP_TRY(check_matrix(n, n_dtype, C, ldn, "n"));
-      vec = vec && vec8_ok(n, n_dtype, C, ldn);
     }
   }
   ASP_TRY(check_vec(post_w, "post_w"));
@@ -697,10 +640,8 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
   a.ldx = ldx; a.ldy = ldy; a.ldh = ldh; a.ldn = ldn; a.ldt = ldt; a.alpha = alpha; a.eps = eps;
   a.M = (int)M; a.C = (int)C; a.G = G; a.post = post; a.pre = pre; a.n_dtype = n_dtype;
   a.rows = strip_rows(M, C);
-  a.tvec = tables_vec(C, ldt, {post_w, gate, pre_w, pre_b, scale, shift});
   const hipStream_t st = (hipStream_t)stream;
-  if (dtype == ASP_BF16) return vec ? launch_norm<uint16_t, true>(a, st) : launch_norm<uint16_t, false>(a, st);
-  return vec ? launch_norm<float, true>(a, st) : launch_norm<float, false>(a, st);
+  return dtype == ASP_BF16 ? launch_norm<uint16_t>(a, st) : launch_norm<float>(a, st);
 }
 
 int32_t asp_norm_gate_backward_workspace_bytes(int64_t M, int64_t C, int32_t G, size_t* bytes) {
@@ -737,20 +678,14 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
     return fail(ASP_ERR_SHAPE, "table gradient stride %lld", (long long)ldd);
   const bool sums = d_post_w || d_gate || d_pre_w || d_pre_b || d_scale || d_shift;
   if (!sums && !dx && !dy) return ASP_OK;
-  bool vec = true;
   if (M > 0) {
-    auto mat = [&](const void* p, int32_t dt, int64_t ld, const char* name) -> int32_t {
-      ASP_TRY(check_matrix(p, dt, C, ld, name));
-      vec = vec && vec8_ok(p, dt, C, ld);
-      return ASP_OK;
-    };
-    if (dh) ASP_TRY(mat(dh, dtype, lddh, "dh"));
-    if (y) ASP_TRY(mat(y, dtype, ldy, "y"));
-    if (dx) ASP_TRY(mat(dx, dtype, lddx, "dx"));
-    if (dy) ASP_TRY(mat(dy, dtype, lddy, "dy"));
+    if (dh) ASP_TRY(check_matrix(dh, dtype, C, lddh, "dh"));
+    if (y) ASP_TRY(check_matrix(y, dtype, C, ldy, "y"));
+    if (dx) ASP_TRY(check_matrix(dx, dtype, C, lddx, "dx"));
+    if (dy) ASP_TRY(check_matrix(dy, dtype, C, lddy, "dy"));
     if (pre != ASP_NORM_NONE) {
-      ASP_TRY(mat(h, dtype, ldh, "h"));
-      ASP_TRY(mat(dn, dn_dtype, lddn, "dn"));
+      ASP_TRY(check_matrix(h, dtype, C, ldh, "h"));
+      ASP_TRY(check_matrix(dn, dn_dtype, C, lddn, "dn"));
     } else if (!dh) {
       return fail(ASP_ERR_ARG, "neither dh nor dn is given");
     }
@@ -769,17 +704,12 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   a.dh = dh; a.dn = dn; a.dx = dx; a.dy = dy; a.lddh = lddh; a.lddn = lddn; a.lddx = lddx;
   a.lddy = lddy; a.part = sums ? static_cast<float*>(workspace) : nullptr;
   a.rows = strip_rows(M, C);
-  a.tvec = tables_vec(C, ldt, {post_w, gate, pre_w, scale});
   if (M > 0) {
-    int32_t s;
     const bool n16 = dn_dtype == ASP_BF16;
     if (dtype == ASP_BF16)
-      s = n16 ? (vec ? launch_back<uint16_t, uint16_t, true>(a, st) : launch_back<uint16_t, uint16_t, false>(a, st))
-              : (vec ? launch_back<uint16_t, float, true>(a, st) : launch_back<uint16_t, float, false>(a, st));
+      ASP_TRY((n16 ? launch_back<uint16_t, uint16_t>(a, st) : launch_back<uint16_t, float>(a, st)));
     else
-      s = n16 ? (vec ? launch_back<float, uint16_t, true>(a, st) : launch_back<float, uint16_t, false>(a, st))
-              : (vec ? launch_back<float, float, true>(a, st) : launch_back<float, float, false>(a, st));
-    ASP_TRY(s);
+      ASP_TRY((n16 ? launch_back<float, uint16_t>(a, st) : launch_back<float, float>(a, st)));
   }
   if (!sums) return ASP_OK;
   SumArgs k = {};
