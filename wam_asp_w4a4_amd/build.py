@@ -29,10 +29,12 @@ HIP_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     # keep the compiler from forming packed fp32 VALU ops
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA results in ordinary VGPRs (no copies through the accumulation registers)
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I", INCLUDE, "-I", CSRC,
 ]
+# MFMA results in ordinary VGPRs (no copies through the accumulation registers)
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+# but here: a 128 x 128 tile for each wave fills the accumulation registers by itself
+AGPR_FORM = {"asp_fp8_gemm.hip"}
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-pthread",
               "-Wall", "-Wextra", "-I", INCLUDE, "-I", CSRC]
 
@@ -70,7 +72,8 @@ def build(verbose: bool = False) -> str:
             src = os.path.join(CSRC, name)
             obj = os.path.join(tmp, name + ".o")
             if name.endswith(".hip"):
-                jobs.append([HIPCC, *HIP_FLAGS, "-c", src, "-o", obj])
+                form = [] if name in AGPR_FORM else VGPR_FORM
+                jobs.append([HIPCC, *HIP_FLAGS, *form, "-c", src, "-o", obj])
             elif name.endswith(".cpp"):
                 jobs.append(["g++", *HOST_FLAGS, *digest, "-c", src, "-o", obj])
             else:

@@ -44,6 +44,16 @@ struct GemmK {
   int M, N, KB, y_bf16, slices, tiles_m, tiles_n;
 };
 
+// Bytes p .. p + n - 1 as a buffer, and the direct copy of 16 bytes a lane from it to
+// LDS: lane l's bytes, at offset v + s, land at lds_base (uniform) + 16 l.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const uint8_t* p, int64_t n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)n, 0x00020000);
+}
+__device__ __forceinline__ void buffer_copy16(__amdgpu_buffer_rsrc_t r, int v, int s, void* lds_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16,
+                                           v, s, 0, 0);
+}
+
 // XCD-aware tile order.  Workgroups go to the 8 XCDs (each with its own L2) in
 // turn; each XCD takes one contiguous run of tiles, walked in bands of 8 tile
 // rows, so that the operand rows its workgroups share stay in its L2.
@@ -83,65 +93,98 @@ __device__ __forceinline__ void store4(const GemmK& g, int64_t m, int n, f32x4_t
   }
 }
 
-// k_fp8_gemm: a workgroup of WGM x WGN waves owns a BM x BN tile of y, each wave
-// TM x TN MFMA tiles of 32 x 32.  A block of K (128 bytes of every operand row)
-// goes from memory straight to LDS (16 bytes a lane, no registers), the next
-// block's copies in flight while this one is multiplied.  Copy j of a stage
-// fills 8 rows; slot s of it holds row s / 8, piece (s % 8) ^ (row % 8) of that
-// row's eight 16-byte pieces, so that the MFMA reads (32 rows at one piece
-// index) fall in distinct banks.  The order of the K elements inside a block is
-// the same for both operands, and the scale is the same for all of them, so it
-// needs no care.  The operands are swapped (B's rows are the MFMA's rows): a
+// The order of half a block for the scheduler: after each MFMA its share of the
+// half's LDS reads and memory loads, so that no group of them holds the matrix unit
+// up (its MFMAs start one after the other, and a wave issues in order).
+template <int MFMAS, int READS, int LOADS, int M = 0>
+__device__ __forceinline__ void order() {
+  if constexpr (M < MFMAS) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS * (M + 1) / MFMAS - READS * M / MFMAS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x020, LOADS * (M + 1) / MFMAS - LOADS * M / MFMAS, 0);
+    order<MFMAS, READS, LOADS, M + 1>();
+  }
+}
+
+// k_fp8_gemm: a workgroup of 2 x 2 waves owns a BM x BN tile of y, each wave TM x TN
+// MFMA tiles of 32 x 32.  A block of K (128 bytes of every operand row) goes from
+// memory straight to LDS (16 bytes a lane, no registers) into one of two buffers.
+// Copy j of a block fills 8 rows; slot s of it holds row s / 8, piece (s % 8) ^
+// (row % 8) of that row's eight 16-byte pieces, so that the MFMA reads (32 rows at
+// one piece index) fall in distinct banks.  The order of the K elements inside a
+// block is the same for both operands, and the scale is the same for all of them,
+// so it needs no care.  The operands are swapped (B's rows are the MFMA's rows): a
 // lane then holds four consecutive columns of a row of y.
-// WIDE: the 16-bit arithmetic.
-template <int WGM, int WGN, int TM, int TN, bool WIDE>
-__global__ void __launch_bounds__(64 * WGM * WGN) k_fp8_gemm(const GemmK g) {
-  constexpr int NW = WGM * WGN, BM = 32 * TM * WGM, BN = 32 * TN * WGN;
+//
+// A block is multiplied in two halves of 64, each half's fragments read from LDS
+// while the other half is multiplied.  One barrier a block, between the halves: by
+// then every wave has the second half's fragments in registers, so the block's
+// buffer is free for the block after the next, and every wave's copies of the next
+// block have landed, so its first half can be read.
+template <int TM, int TN, bool WIDE>
+__global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
+  constexpr int BM = 64 * TM, BN = 64 * TN;
   constexpr int STAGE = (BM + BN) * kFp8Block;
-  constexpr int COPIES = (BM + BN) / 8 / NW;  // of this wave, for each stage
-  static_assert((BM + BN) % (8 * NW) == 0, "whole copies for every wave");
+  constexpr int COPIES = (BM + BN) / 32;  // of a wave, for each block
   __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
-  const int wm = wave / WGN, wn = wave % WGN;
+  const int wm = wave >> 1, wn = wave & 1;
   int tm, tn;
   tile_at(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  // the tile's last rows; rows past them re-read the last one, their results are not stored
+  const int mlast = (int)min((int64_t)BM, g.M - m0) - 1, nlast = (int)min((int64_t)BN, g.N - n0) - 1;
   // this slice's blocks of K
   const int kb0 = (int)((int64_t)g.KB * blockIdx.y / g.slices);
   const int kb1 = (int)((int64_t)g.KB * (blockIdx.y + 1) / g.slices);
 
-  // rows past the matrix re-read its last row; their results are not stored
-  const uint8_t* src[COPIES];
+  // Copies c < HALF are the wave's share of A's rows, the others of B's, through
+  // buffer descriptors that end with the tile's last row: one 32-bit offset a copy
+  // (a tile's rows span less than 2^28 bytes) and the block's offset in a scalar.
+  constexpr int HALF = COPIES / 2;
+  const __amdgpu_buffer_rsrc_t ra = descriptor(g.a + m0 * g.lda, (mlast + 1) * g.lda);
+  const __amdgpu_buffer_rsrc_t rb = descriptor(g.b + n0 * g.ldb, (nlast + 1) * g.ldb);
+  int offa[HALF], offb[HALF];
+  static_assert(BM == BN, "A and B have as many rows");
 #pragma unroll
-  for (int c = 0; c < COPIES; ++c) {
-    const int row = 8 * (wave * COPIES + c) + (lane >> 3);
-    const int piece = (lane & 7) ^ (row & 7);
-    src[c] = row < BM ? g.a + min(m0 + row, (int64_t)g.M - 1) * g.lda + 16 * piece
-                      : g.b + min(n0 + row - BM, (int64_t)g.N - 1) * g.ldb + 16 * piece;
+  for (int c = 0; c < HALF; ++c) {
+    const int row = 8 * (wave * HALF + c) + (lane >> 3);
+    const int piece = 16 * ((lane & 7) ^ (row & 7));
+    offa[c] = min(row, mlast) * (int)g.lda + piece;
+    offb[c] = min(row, nlast) * (int)g.ldb + piece;
   }
+  // block kb into buffer kb & 1 (past the last block: the last one again, which nobody
+  // reads, so that the loop has no branch)
   auto issue = [&](int kb) {
-    uint8_t* base = smem + (kb & 1) * STAGE + wave * COPIES * 1024;
+    uint8_t* base = smem + (kb & 1) * STAGE + wave * HALF * 1024;
+    const int at = min(kb, kb1 - 1) * kFp8Block;
 #pragma unroll
-    for (int c = 0; c < COPIES; ++c) lds_copy16(src[c] + (int64_t)kb * kFp8Block, base + 1024 * c);
+    for (int c = 0; c < HALF; ++c) {
+      buffer_copy16(ra, offa[c], at, base + 1024 * c);
+      buffer_copy16(rb, offb[c], at, base + BM * kFp8Block + 1024 * c);
+    }
   };
-  // scales: one dword holds a row's scales of four blocks
-  const uint32_t* sa[TM];
-  const uint32_t* sb[TN];
+  // a block's scale byte of each of the lane's rows
+  const uint8_t* sa = g.as + 4 * m0;
+  const uint8_t* sb = g.bs + 4 * n0;
+  uint32_t ca[TM], cb[TN], na[TM], nb[TN];
+  auto scales = [&](int kb) {
+    kb = min(kb, kb1 - 1);
+    const uint8_t* pa = sa + (int64_t)(kb >> 2) * g.M * 4 + (kb & 3);
+    const uint8_t* pb = sb + (int64_t)(kb >> 2) * g.N * 4 + (kb & 3);
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
-    sa[i] = reinterpret_cast<const uint32_t*>(g.as) +
-            min(m0 + 32 * (wm * TM + i) + l32, (int64_t)g.M - 1);
+    for (int i = 0; i < TM; ++i)
+      na[i] = pa[4u * (uint32_t)min(32 * (wm * TM + i) + l32, mlast)];
 #pragma unroll
-  for (int j = 0; j < TN; ++j)
-    sb[j] = reinterpret_cast<const uint32_t*>(g.bs) +
-            min(n0 + 32 * (wn * TN + j) + l32, (int64_t)g.N - 1);
-  uint32_t ca[TM], cb[TN];
-  auto scales = [&](int grp, uint32_t (&pa)[TM], uint32_t (&pb)[TN]) {
+    for (int j = 0; j < TN; ++j)
+      nb[j] = pb[4u * (uint32_t)min(32 * (wn * TN + j) + l32, nlast)];
+  };
+  auto next_scales = [&]() {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) pa[i] = sa[i][(int64_t)grp * g.M];
+    for (int i = 0; i < TM; ++i) ca[i] = na[i];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) pb[j] = sb[j][(int64_t)grp * g.N];
+    for (int j = 0; j < TN; ++j) cb[j] = nb[j];
   };
 
   f32x16_t acc[TM][TN];
@@ -160,63 +203,70 @@ __global__ void __launch_bounds__(64 * WGM * WGN) k_fp8_gemm(const GemmK g) {
     return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                    (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
-
-  if (kb0 < kb1) {
-    issue(kb0);
-    scales(kb0 >> 2, ca, cb);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) ca[i] >>= 8 * (kb0 & 3);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) cb[j] >>= 8 * (kb0 & 3);
-  }
-  for (int kb = kb0; kb < kb1; ++kb) {
-    // this wave's copies of block kb have landed; after the barrier everyone's
-    // have, and everyone has read block kb - 1, whose buffer is filled next
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const bool more = kb + 1 < kb1;
-    uint32_t na[TM], nb[TN];
-    const bool refill = more && ((kb + 1) & 3) == 0;
-    if (more) issue(kb + 1);
-    if (refill) scales((kb + 1) >> 2, na, nb);
+  i32x8_t fa[2][TM], fb[2][TN];
+  auto read = [&](int kb, int kk) {
     const uint8_t* base = smem + (kb & 1) * STAGE;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      i32x8_t fa[TM], fb[TN];
+    for (int j = 0; j < TN; ++j) fb[kk][j] = frag(base, rowb + 32 * j, kk);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag(base, rowa + 32 * i, kk);
+    for (int i = 0; i < TM; ++i) fa[kk][i] = frag(base, rowa + 32 * i, kk);
+  };
+  auto multiply = [&](int kk) {
+    if constexpr (WIDE) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = frag(base, rowb + 32 * j, kk);
-      if constexpr (WIDE) {
+      for (int s = 0; s < 4; ++s) {
+        bf16x8_t wa[TM], wb[TN];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          bf16x8_t wa[TM], wb[TN];
+        for (int j = 0; j < TN; ++j)
+          wb[j] = decode_bf16(fb[kk][j][2 * s], fb[kk][j][2 * s + 1], scale_f32(cb[j]));
 #pragma unroll
-          for (int i = 0; i < TM; ++i)
-            wa[i] = decode_bf16(fa[i][2 * s], fa[i][2 * s + 1], scale_f32(ca[i]));
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            wb[j] = decode_bf16(fb[j][2 * s], fb[j][2 * s + 1], scale_f32(cb[j]));
-#pragma unroll
-          for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
-        }
-      } else {
+        for (int i = 0; i < TM; ++i)
+          wa[i] = decode_bf16(fa[kk][i][2 * s], fa[kk][i][2 * s + 1], scale_f32(ca[i]));
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
           for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                fb[j], fa[i], acc[i][j], 0, 0, 0, (int)cb[j], 0, (int)ca[i]);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0, (int)cb[j], 0, (int)ca[i]);
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) ca[i] = refill ? na[i] : ca[i] >> 8;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) cb[j] = refill ? nb[j] : cb[j] >> 8;
+  };
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (kb0 < kb1) {
+    issue(kb0);
+    scales(kb0);
+    barrier();
+    issue(kb0 + 1);
+    read(kb0, 0);
+    next_scales();
+  }
+  for (int kb = kb0; kb < kb1; ++kb) {
+    read(kb, 1);
+    multiply(0);
+    if constexpr (!WIDE) order<TM * TN, 2 * (TM + TN), 0>();
+    barrier();
+    read(kb + 1, 0);
+    scales(kb + 1);
+    issue(kb + 2);
+    multiply(1);
+    if constexpr (!WIDE) {
+      order<TM * TN / 2, 2 * (TM + TN), 0>();
+      order<TM * TN - TM * TN / 2, 0, TM + TN + COPIES>();
+    }
+    next_scales();
   }
 
   // accumulator element v of lane l: column 8 (v / 4) + 4 (l / 32) + v % 4 of
@@ -396,15 +446,14 @@ GemmK kernel_args(const Fp8Gemm& g, int slices) {
   return k;
 }
 
-template <int WGM, int WGN, int TM, int TN, bool WIDE>
+template <int TM, int TN, bool WIDE>
 int32_t launch_tiles(GemmK k, hipStream_t st) {
-  constexpr int64_t BM = 32 * TM * WGM, BN = 32 * TN * WGN;
+  constexpr int64_t BM = 64 * TM, BN = 64 * TN;
   const int64_t tm = (k.M + BM - 1) / BM, tn = (k.N + BN - 1) / BN;
   if (tm * tn > INT32_MAX) return fail(ASP_ERR_SHAPE, "output too large for one launch");
   k.tiles_m = (int)tm;
   k.tiles_n = (int)tn;
-  k_fp8_gemm<WGM, WGN, TM, TN, WIDE>
-      <<<dim3((unsigned)(tm * tn), (unsigned)k.slices), 64 * WGM * WGN, 0, st>>>(k);
+  k_fp8_gemm<TM, TN, WIDE><<<dim3((unsigned)(tm * tn), (unsigned)k.slices), 256, 0, st>>>(k);
   return launch_status("fp8 gemm");
 }
 
@@ -445,9 +494,9 @@ namespace {
 template <bool WIDE>
 int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
   switch (p.tile) {
-    case 256: return launch_tiles<2, 4, 4, 2, WIDE>(k, st);
-    case 128: return launch_tiles<2, 2, 2, 2, WIDE>(k, st);
-    default: return launch_tiles<2, 2, 1, 1, WIDE>(k, st);
+    case 256: return launch_tiles<4, 4, WIDE>(k, st);
+    case 128: return launch_tiles<2, 2, WIDE>(k, st);
+    default: return launch_tiles<1, 1, WIDE>(k, st);
   }
 }
 }  // namespace
