@@ -53,6 +53,10 @@ __device__ __forceinline__ void buffer_copy16(__amdgpu_buffer_rsrc_t r, int v, i
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16,
                                            v, s, 0, 0);
 }
+__device__ __forceinline__ void buffer_copy4(__amdgpu_buffer_rsrc_t r, int v, void* lds_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 4,
+                                           v, 0, 0, 0);
+}
 
 // XCD-aware tile order.  Workgroups go to the 8 XCDs (each with its own L2) in
 // turn; each XCD takes one contiguous run of tiles, walked in bands of 8 tile
@@ -107,31 +111,43 @@ __device__ __forceinline__ void order() {
 }
 
 // k_fp8_gemm: a workgroup of 2 x 2 waves owns a BM x BN tile of y, each wave TM x TN
-// MFMA tiles of 32 x 32.  A block of K (128 bytes of every operand row) goes from
-// memory straight to LDS (16 bytes a lane, no registers) into one of two buffers.
-// Copy j of a block fills 8 rows; slot s of it holds row s / 8, piece (s % 8) ^
-// (row % 8) of that row's eight 16-byte pieces, so that the MFMA reads (32 rows at
-// one piece index) fall in distinct banks.  The order of the K elements inside a
-// block is the same for both operands, and the scale is the same for all of them,
-// so it needs no care.  The operands are swapped (B's rows are the MFMA's rows): a
-// lane then holds four consecutive columns of a row of y.
+// MFMA tiles of 32 x 32.  K goes by in stages of 64, straight from memory to LDS (16
+// bytes a lane, no registers).  Copy j of a stage fills 16 rows of 64 bytes; slot s
+// of it holds row s / 4, piece (s % 4) ^ (row / 4 % 4) of that row's four 16-byte
+// pieces, so that the MFMA reads (32 rows at one piece index) fall in distinct banks.
+// The order of the K elements inside a stage is the same for both operands, and
+// the scale is the same for all of them, so it needs no care.  The operands are
+// swapped (B's rows are the MFMA's rows): a lane then holds four consecutive
+// columns of a row of y.
 //
-// A block is multiplied in two halves of 64, each half's fragments read from LDS
-// while the other half is multiplied.  One barrier a block, between the halves: by
-// then every wave has the second half's fragments in registers, so the block's
-// buffer is free for the block after the next, and every wave's copies of the next
-// block have landed, so its first half can be read.
+// While a stage is multiplied from registers, the next one's fragments are read
+// from LDS, and three more stages are on their way into the four buffers: memory has
+// the time of three stages (one stage: 486 us at 8192^3, XXX now).  One barrier a
+// stage: by then every wave has the stage's fragments in registers, so its buffer
+// is free for the stage after the next three, and every wave's copies of the next
+// stage have landed.  The scales go the same way (the dword of a row's four blocks,
+// for each block anew): loaded to registers, their wait would be one for every older
+// copy, since loads are counted in order.
 template <int TM, int TN, bool WIDE>
 __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
-  constexpr int BM = 64 * TM, BN = 64 * TN;
-  constexpr int STAGE = (BM + BN) * kFp8Block;
-  constexpr int COPIES = (BM + BN) / 32;  // of a wave, for each block
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * STAGE];
+  constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64;
+  constexpr int STAGE = (BM + BN) * SK;
+  constexpr int CA = BM * SK / 4096, CB = BN * SK / 4096;  // a wave's copies of A and B for a stage
+  constexpr int SC = TM > 1 ? TM / 2 : 1;                  // and of 64 rows' scales for a block
+  constexpr int SCALES = 4 * (BM + BN);                    // bytes of a block's scales
+  constexpr int PITCH16 = 64 * TN + 16, PITCH32 = 128 * TN + 16;  // of a wave's result rows in LDS
+  constexpr int TP = TM > 1 ? TM / 2 : 1;                  // tile rows of a float32 result at a time
+  constexpr int OUT16 = 32 * TM * PITCH16, OUT32 = 32 * TP * PITCH32;
+  constexpr int OUT = OUT16 > OUT32 ? OUT16 : OUT32;       // a wave's result region
+  constexpr int STAGING = 4 * STAGE + 2 * SCALES;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[STAGING > 4 * OUT ? STAGING : 4 * OUT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave >> 1, wn = wave & 1;
   int tm, tn;
   tile_at(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   // the tile's last rows; rows past them re-read the last one, their results are not stored
   const int mlast = (int)min((int64_t)BM, g.M - m0) - 1, nlast = (int)min((int64_t)BN, g.N - n0) - 1;
@@ -139,46 +155,60 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   const int kb0 = (int)((int64_t)g.KB * blockIdx.y / g.slices);
   const int kb1 = (int)((int64_t)g.KB * (blockIdx.y + 1) / g.slices);
 
-  // Copies c < HALF are the wave's share of A's rows, the others of B's, through
-  // buffer descriptors that end with the tile's last row: one 32-bit offset a copy
-  // (a tile's rows span less than 2^28 bytes) and the block's offset in a scalar.
-  constexpr int HALF = COPIES / 2;
+  // The copies go through buffer descriptors that end with the tile's last row: one
+  // 32-bit offset a copy (a tile's rows span less than 2^28 bytes) and the stage's
+  // offset in a scalar.
   const __amdgpu_buffer_rsrc_t ra = descriptor(g.a + m0 * g.lda, (mlast + 1) * g.lda);
   const __amdgpu_buffer_rsrc_t rb = descriptor(g.b + n0 * g.ldb, (nlast + 1) * g.ldb);
-  int offa[HALF], offb[HALF];
-  static_assert(BM == BN, "A and B have as many rows");
-#pragma unroll
-  for (int c = 0; c < HALF; ++c) {
-    const int row = 8 * (wave * HALF + c) + (lane >> 3);
-    const int piece = 16 * ((lane & 7) ^ (row & 7));
-    offa[c] = min(row, mlast) * (int)g.lda + piece;
-    offb[c] = min(row, nlast) * (int)g.ldb + piece;
-  }
-  // block kb into buffer kb & 1 (past the last block: the last one again, which nobody
-  // reads, so that the loop has no branch)
-  auto issue = [&](int kb) {
-    uint8_t* base = smem + (kb & 1) * STAGE + wave * HALF * 1024;
-    const int at = min(kb, kb1 - 1) * kFp8Block;
-#pragma unroll
-    for (int c = 0; c < HALF; ++c) {
-      buffer_copy16(ra, offa[c], at, base + 1024 * c);
-      buffer_copy16(rb, offb[c], at, base + BM * kFp8Block + 1024 * c);
-    }
+  int offa[CA], offb[CB];
+  auto source = [&](int copy, int last, int64_t ld) {
+    const int row = 16 * copy + (lane >> 2);
+    return min(row, last) * (int)ld + 16 * ((lane & 3) ^ (row >> 2 & 3));
   };
-  // a block's scale byte of each of the lane's rows
-  const uint8_t* sa = g.as + 4 * m0;
-  const uint8_t* sb = g.bs + 4 * n0;
+#pragma unroll
+  for (int c = 0; c < CA; ++c) offa[c] = source(wave * CA + c, mlast, g.lda);
+#pragma unroll
+  for (int c = 0; c < CB; ++c) offb[c] = source(wave * CB + c, nlast, g.ldb);
+  // stage s (half s % 2 of block s / 2) into buffer s % 4; past the last one the last
+  // again, which nobody reads, so that the loop has no branch
+  auto issue = [&](int s) {
+    uint8_t* base = smem + (s & 3) * STAGE;
+    const int at = min(s, 2 * kb1 - 1) * SK;
+#pragma unroll
+    for (int c = 0; c < CA; ++c) buffer_copy16(ra, offa[c], at, base + (wave * CA + c) * 1024);
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      buffer_copy16(rb, offb[c], at, base + BM * SK + (wave * CB + c) * 1024);
+  };
+  // block kb's scales into scale buffer kb % 2: copy i has 64 rows of A, then of B (a
+  // 64 x 64 tile has two for four waves: the others repeat them)
+  const uint8_t* scale_base[SC];
+  int64_t scale_group[SC];
+  int scale_bytes[SC], scale_off[SC];
+#pragma unroll
+  for (int c = 0; c < SC; ++c) {
+    const int i = (wave * SC + c) % (2 * TM);
+    const bool is_a = i < TM;
+    scale_base[c] = is_a ? g.as + 4 * m0 : g.bs + 4 * n0;
+    scale_group[c] = 4 * (int64_t)(is_a ? g.M : g.N);
+    scale_bytes[c] = 4 * ((is_a ? mlast : nlast) + 1);
+    scale_off[c] = 4 * min(64 * (i % TM) + lane, is_a ? mlast : nlast);
+  }
+  auto issue_scales = [&](int kb) {
+    const int64_t grp = min(kb, kb1 - 1) >> 2;
+    uint8_t* base = smem + 4 * STAGE + (kb & 1) * SCALES;
+#pragma unroll
+    for (int c = 0; c < SC; ++c)
+      buffer_copy4(descriptor(scale_base[c] + grp * scale_group[c], scale_bytes[c]), scale_off[c],
+                   base + 256 * ((wave * SC + c) % (2 * TM)));
+  };
   uint32_t ca[TM], cb[TN], na[TM], nb[TN];
-  auto scales = [&](int kb) {
-    kb = min(kb, kb1 - 1);
-    const uint8_t* pa = sa + (int64_t)(kb >> 2) * g.M * 4 + (kb & 3);
-    const uint8_t* pb = sb + (int64_t)(kb >> 2) * g.N * 4 + (kb & 3);
+  auto read_scales = [&](int kb) {
+    const uint8_t* base = smem + 4 * STAGE + (kb & 1) * SCALES + (min(kb, kb1 - 1) & 3);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      na[i] = pa[4u * (uint32_t)min(32 * (wm * TM + i) + l32, mlast)];
+    for (int j = 0; j < TN; ++j) nb[j] = base[4 * (BM + 32 * (wn * TN + j) + l32)];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      nb[j] = pb[4u * (uint32_t)min(32 * (wn * TN + j) + l32, nlast)];
+    for (int i = 0; i < TM; ++i) na[i] = base[4 * (32 * (wm * TM + i) + l32)];
   };
   auto next_scales = [&]() {
 #pragma unroll
@@ -195,33 +225,34 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  const int rowa = 32 * TM * wm + l32, rowb = BM + 32 * TN * wn + l32, key = l32 & 7;
-  auto frag = [&](const uint8_t* base, int row, int kk) {
-    const uint8_t* p = base + row * kFp8Block;
-    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * kk + 2 * half) ^ key));
-    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(p + 16 * ((4 * kk + 2 * half + 1) ^ key));
-    return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                   (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  const int key = l32 >> 2 & 3;
+  const int lo = 16 * ((2 * half) ^ key), hi = 16 * ((2 * half + 1) ^ key);
+  const int rowa = (32 * TM * wm + l32) * SK, rowb = (BM + 32 * TN * wn + l32) * SK;
+  auto frag = [&](const uint8_t* p) {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p + lo);
+    const u32x4_t b = *reinterpret_cast<const u32x4_t*>(p + hi);
+    return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3],
+                   (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
   };
   i32x8_t fa[2][TM], fb[2][TN];
-  auto read = [&](int kb, int kk) {
-    const uint8_t* base = smem + (kb & 1) * STAGE;
+  auto read = [&](int s, int set) {
+    const uint8_t* base = smem + (s & 3) * STAGE;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[kk][j] = frag(base, rowb + 32 * j, kk);
+    for (int j = 0; j < TN; ++j) fb[set][j] = frag(base + rowb + 32 * SK * j);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[kk][i] = frag(base, rowa + 32 * i, kk);
+    for (int i = 0; i < TM; ++i) fa[set][i] = frag(base + rowa + 32 * SK * i);
   };
-  auto multiply = [&](int kk) {
+  auto multiply = [&](int set) {
     if constexpr (WIDE) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         bf16x8_t wa[TM], wb[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-          wb[j] = decode_bf16(fb[kk][j][2 * s], fb[kk][j][2 * s + 1], scale_f32(cb[j]));
+          wb[j] = decode_bf16(fb[set][j][2 * s], fb[set][j][2 * s + 1], scale_f32(cb[j]));
 #pragma unroll
         for (int i = 0; i < TM; ++i)
-          wa[i] = decode_bf16(fa[kk][i][2 * s], fa[kk][i][2 * s + 1], scale_f32(ca[i]));
+          wa[i] = decode_bf16(fa[set][i][2 * s], fa[set][i][2 * s + 1], scale_f32(ca[i]));
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -234,60 +265,140 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
         for (int j = 0; j < TN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0, (int)cb[j], 0, (int)ca[i]);
+              fb[set][j], fa[set][i], acc[i][j], 0, 0, 0, (int)cb[j], 0, (int)ca[i]);
     }
   };
-  auto barrier = [&]() {
+  // The copies behind stage s + 1's when the barrier of stage s is reached: those of two
+  // stages and of one block's scales (which go in front of an even stage's).
+  constexpr int FLIGHT = 2 * (CA + CB) + SC;
+  auto barrier = [&](auto flight) {
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flight)::value) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
+  using Flight = std::integral_constant<int, FLIGHT>;
+  constexpr int FIRST = TM * TN / 2, REST = TM * TN - FIRST;
 
   if (kb0 < kb1) {
-    issue(kb0);
-    scales(kb0);
-    barrier();
-    issue(kb0 + 1);
-    read(kb0, 0);
+    issue_scales(kb0);
+    issue(2 * kb0);
+    issue(2 * kb0 + 1);
+    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
+    issue_scales(kb0 + 1);
+    issue(2 * kb0 + 2);
+    issue(2 * kb0 + 3);
+    barrier(std::integral_constant<int, FLIGHT + CA + CB>{});
+    read(2 * kb0, 0);
+    read_scales(kb0);
     next_scales();
   }
   for (int kb = kb0; kb < kb1; ++kb) {
-    read(kb, 1);
+    barrier(Flight{});
+    read(2 * kb + 1, 1);
+    issue_scales(kb + 2);
+    issue(2 * kb + 4);
     multiply(0);
-    if constexpr (!WIDE) order<TM * TN, 2 * (TM + TN), 0>();
-    barrier();
-    read(kb + 1, 0);
-    scales(kb + 1);
-    issue(kb + 2);
+    if constexpr (!WIDE) {
+      order<FIRST, 2 * (TM + TN), 0>();
+      order<REST, 0, SC + CA + CB>();
+    }
+    barrier(Flight{});
+    read(2 * kb + 2, 0);
+    read_scales(kb + 1);
+    issue(2 * kb + 5);
     multiply(1);
     if constexpr (!WIDE) {
-      order<TM * TN / 2, 2 * (TM + TN), 0>();
-      order<TM * TN - TM * TN / 2, 0, TM + TN + COPIES>();
+      order<FIRST, 3 * (TM + TN), 0>();
+      order<REST, 0, CA + CB>();
     }
     next_scales();
   }
+  // every copy has landed and every read is done: the buffers become the results' rows
+  barrier(std::integral_constant<int, 0>{});
 
-  // accumulator element v of lane l: column 8 (v / 4) + 4 (l / 32) + v % 4 of
-  // row l % 32 of y's 32 x 32 tile
-  GemmK o = g;
-  if (g.slices > 1) {
-    o.y = g.part + (int64_t)blockIdx.y * g.M * g.N;
-    o.y_bf16 = 0;
-    o.bias = nullptr;
+  // Accumulator element v of lane l: column 8 (v / 4) + 4 (l / 32) + v % 4 of row
+  // l % 32 of y's 32 x 32 tile.  Each wave turns its part in its own region of LDS
+  // (rows padded by 16 bytes against bank conflicts) and stores whole 16-byte pieces of
+  // its rows.
+  const bool split = g.slices > 1;
+  const bool y16 = g.y_bf16 && !split;
+  uint8_t* mine = smem + wave * OUT;
+  const int64_t mw = m0 + 32 * TM * wm;
+  const int nw = (int)n0 + 32 * TN * wn;
+  auto values = [&](int i, int j, int v) {
+    const int n = nw + 32 * j + 8 * v + 4 * half;
+    f32x4_t r = {acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+    if (g.bias && !split)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] += n + e < g.N ? g.bias[n + e] : 0.0f;
+    return r;
+  };
+  auto settle = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+  if (y16) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const f32x4_t r = values(i, j, v);
+          *reinterpret_cast<u32x2_t*>(mine + (32 * i + l32) * PITCH16 + 64 * j + 16 * v + 8 * half) =
+              u32x2_t{bf16x2_rne(r[0], r[1]), bf16x2_rne(r[2], r[3])};
+        }
+    settle();
+    constexpr int PIECES = 4 * TN;  // of 8 values a row
+    const int col = 8 * (lane % PIECES), left = g.N - nw - col;
+#pragma unroll
+    for (int r = 0; r < 32 * TM; r += 64 / PIECES) {
+      const int row = r + lane / PIECES;
+      if (mw + row >= g.M) continue;
+      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(mine + row * PITCH16 + 2 * col);
+      uint16_t* y = static_cast<uint16_t*>(g.y) + (mw + row) * g.N + nw + col;
+      if (left >= 8) {
+        *reinterpret_cast<u32x4_e2*>(y) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < left) y[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+    return;
   }
-  const bool vec = g.N % 4 == 0 && ((uintptr_t)o.y & 15) == 0;
+  float* out = split ? g.part + (int64_t)blockIdx.y * g.M * g.N : static_cast<float*>(g.y);
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i0 = 0; i0 < TM; i0 += TP) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
+    for (int i = 0; i < TP; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        store4(o, m0 + 32 * (wm * TM + i) + l32, (int)(n0 + 32 * (wn * TN + j)) + 8 * v + 4 * half,
-               f32x4_t{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2],
-                       acc[i][j][4 * v + 3]},
-               vec);
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          *reinterpret_cast<f32x4_t*>(mine + (32 * i + l32) * PITCH32 + 128 * j + 32 * v + 16 * half) =
+              values(i0 + i, j, v);
+    settle();
+    constexpr int PIECES = 8 * TN;  // of 4 values a row
+    const int col = 4 * (lane % PIECES), left = g.N - nw - col;
+#pragma unroll
+    for (int r = 0; r < 32 * TP; r += 64 / PIECES) {
+      const int row = r + lane / PIECES;
+      const int64_t m = mw + 32 * i0 + row;
+      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(mine + row * PITCH32 + 4 * col);
+      if (m >= g.M) continue;
+      float* y = out + m * g.N + nw + col;
+      if (left >= 4) {
+        *reinterpret_cast<u32x4_e4*>(y) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t b = w[e];
+          if (e < left) y[e] = __builtin_bit_cast(float, b);
+        }
+      }
+    }
+    settle();
+  }
 }
 
 // the slices' partial sums, added in slice order, plus bias
