@@ -59,15 +59,15 @@ __device__ __forceinline__ void buffer_copy4(__amdgpu_buffer_rsrc_t r, int v, vo
 }
 
 // XCD-aware tile order.  Workgroups go to the 8 XCDs (each with its own L2) in
-// turn; each XCD takes one contiguous run of tiles, walked in bands of 8 tile
+// turn; each XCD takes one contiguous run of tiles, walked in bands of 4 tile
 // rows, so that the operand rows its workgroups share stay in its L2.
 __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int total = tiles_m * tiles_n, per = total / 8, extra = total % 8;
   const int xcd = id % 8, k = id / 8;
   const int t = xcd * per + min(xcd, extra) + k;
-  const int band = 8 * tiles_n, b = t / band, r = t % band;
-  const int rows = min(8, tiles_m - 8 * b);
-  tm = 8 * b + r % rows;
+  const int band = 4 * tiles_n, b = t / band, r = t % band;
+  const int rows = min(4, tiles_m - 4 * b);
+  tm = 4 * b + r % rows;
   tn = r / rows;
 }
 
@@ -103,9 +103,11 @@ __device__ __forceinline__ void store4(const GemmK& g, int64_t m, int n, f32x4_t
 template <int MFMAS, int READS, int LOADS, int M = 0>
 __device__ __forceinline__ void order() {
   if constexpr (M < MFMAS) {
+    constexpr int R = READS * (M + 1) / MFMAS - READS * M / MFMAS;
+    constexpr int L = LOADS * (M + 1) / MFMAS - LOADS * M / MFMAS;
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, READS * (M + 1) / MFMAS - READS * M / MFMAS, 0);
-    __builtin_amdgcn_sched_group_barrier(0x020, LOADS * (M + 1) / MFMAS - LOADS * M / MFMAS, 0);
+    if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    if constexpr (L > 0) __builtin_amdgcn_sched_group_barrier(0x020, L, 0);
     order<MFMAS, READS, LOADS, M + 1>();
   }
 }
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64;
   constexpr int STAGE = (BM + BN) * SK;
   constexpr int CA = BM * SK / 4096, CB = BN * SK / 4096;  // a wave's copies of A and B for a stage
-  constexpr int SC = TM > 1 ? TM / 2 : 1;                  // and of 64 rows' scales for a block
+  constexpr int SC = (TM + TN + 3) / 4;                    // and of 64 rows' scales for a block
   constexpr int SCALES = 4 * (BM + BN);                    // bytes of a block's scales
   constexpr int PITCH16 = 64 * TN + 16, PITCH32 = 128 * TN + 16;  // of a wave's result rows in LDS
   constexpr int TP = TM > 1 ? TM / 2 : 1;                  // tile rows of a float32 result at a time
@@ -169,25 +171,28 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   for (int c = 0; c < CA; ++c) offa[c] = source(wave * CA + c, mlast, g.lda);
 #pragma unroll
   for (int c = 0; c < CB; ++c) offb[c] = source(wave * CB + c, nlast, g.ldb);
-  // stage s (half s % 2 of block s / 2) into buffer s % 4; past the last one the last
-  // again, which nobody reads, so that the loop has no branch
-  auto issue = [&](int s) {
+  // copy c of stage s (half s % 2 of block s / 2) into buffer s % 4; past the last stage the
+  // last again, which nobody reads, so that the loop has no branch
+  auto copy = [&](int s, int c) {
     uint8_t* base = smem + (s & 3) * STAGE;
     const int at = min(s, 2 * kb1 - 1) * SK;
-#pragma unroll
-    for (int c = 0; c < CA; ++c) buffer_copy16(ra, offa[c], at, base + (wave * CA + c) * 1024);
-#pragma unroll
-    for (int c = 0; c < CB; ++c)
-      buffer_copy16(rb, offb[c], at, base + BM * SK + (wave * CB + c) * 1024);
+    if (c < CA)
+      buffer_copy16(ra, offa[c < CA ? c : 0], at, base + (wave * CA + c) * 1024);
+    else
+      buffer_copy16(rb, offb[c < CA ? 0 : c - CA], at, base + BM * SK + (wave * CB + c - CA) * 1024);
   };
-  // block kb's scales into scale buffer kb % 2: copy i has 64 rows of A, then of B (a
-  // 64 x 64 tile has two for four waves: the others repeat them)
+  auto issue = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < CA + CB; ++c) copy(s, c);
+  };
+  // block kb's scales into scale buffer kb % 2: copy i has 64 rows of A, then of B (where
+  // the waves have more copies than there are, the first ones are made again)
   const uint8_t* scale_base[SC];
   int64_t scale_group[SC];
   int scale_bytes[SC], scale_off[SC];
 #pragma unroll
   for (int c = 0; c < SC; ++c) {
-    const int i = (wave * SC + c) % (2 * TM);
+    const int i = (wave * SC + c) % (TM + TN);
     const bool is_a = i < TM;
     scale_base[c] = is_a ? g.as + 4 * m0 : g.bs + 4 * n0;
     scale_group[c] = 4 * (int64_t)(is_a ? g.M : g.N);
@@ -200,15 +205,15 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
     for (int c = 0; c < SC; ++c)
       buffer_copy4(descriptor(scale_base[c] + grp * scale_group[c], scale_bytes[c]), scale_off[c],
-                   base + 256 * ((wave * SC + c) % (2 * TM)));
+                   base + 256 * ((wave * SC + c) % (TM + TN)));
   };
   uint32_t ca[TM], cb[TN], na[TM], nb[TN];
-  auto read_scales = [&](int kb) {
+  auto read_scale = [&](int kb, int f) {
     const uint8_t* base = smem + 4 * STAGE + (kb & 1) * SCALES + (min(kb, kb1 - 1) & 3);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) nb[j] = base[4 * (BM + 32 * (wn * TN + j) + l32)];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) na[i] = base[4 * (32 * (wm * TM + i) + l32)];
+    if (f < TN)
+      nb[f < TN ? f : 0] = base[4 * (BM + 32 * (wn * TN + f) + l32)];
+    else
+      na[f < TN ? 0 : f - TN] = base[4 * (32 * (wm * TM + f - TN) + l32)];
   };
   auto next_scales = [&]() {
 #pragma unroll
@@ -235,12 +240,13 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
                    (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
   };
   i32x8_t fa[2][TM], fb[2][TN];
-  auto read = [&](int s, int set) {
+  // fragment f of stage s: the columns' first
+  auto read = [&](int s, int set, int f) {
     const uint8_t* base = smem + (s & 3) * STAGE;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fb[set][j] = frag(base + rowb + 32 * SK * j);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) fa[set][i] = frag(base + rowa + 32 * SK * i);
+    if (f < TN)
+      fb[set][f < TN ? f : 0] = frag(base + rowb + 32 * SK * f);
+    else
+      fa[set][f < TN ? 0 : f - TN] = frag(base + rowa + 32 * SK * (f - TN));
   };
   auto multiply = [&](int set) {
     if constexpr (WIDE) {
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
     }
   };
   // The copies behind stage s + 1's when the barrier of stage s is reached: those of two
-  // stages and of one block's scales (which go in front of an even stage's).
+  // stages and of one block's scales (which go behind an even stage's).
   constexpr int FLIGHT = 2 * (CA + CB) + SC;
   auto barrier = [&](auto flight) {
     __builtin_amdgcn_sched_barrier(0);
@@ -279,7 +285,8 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
     __builtin_amdgcn_sched_barrier(0);
   };
   using Flight = std::integral_constant<int, FLIGHT>;
-  constexpr int FIRST = TM * TN / 2, REST = TM * TN - FIRST;
+  constexpr int F = TM + TN;  // fragments of a stage, and as many copies
+  static_assert(CA + CB == F, "a copy for each fragment");
 
   if (kb0 < kb1) {
     issue_scales(kb0);
@@ -290,29 +297,37 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
     issue(2 * kb0 + 2);
     issue(2 * kb0 + 3);
     barrier(std::integral_constant<int, FLIGHT + CA + CB>{});
-    read(2 * kb0, 0);
-    read_scales(kb0);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      read(2 * kb0, 0, f);
+      read_scale(kb0, f);
+    }
     next_scales();
   }
+  // In each half the reads and copies alternate, spread evenly over the MFMAs: the four
+  // waves' copies keep the load path busy half the time, and none waits for it.
   for (int kb = kb0; kb < kb1; ++kb) {
     barrier(Flight{});
-    read(2 * kb + 1, 1);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      read(2 * kb + 1, 1, f);
+      copy(2 * kb + 4, f);
+    }
     issue_scales(kb + 2);
-    issue(2 * kb + 4);
     multiply(0);
     if constexpr (!WIDE) {
-      order<FIRST, 2 * (TM + TN), 0>();
-      order<REST, 0, SC + CA + CB>();
+      order<TM * TN, 2 * F, F>();
+      __builtin_amdgcn_sched_group_barrier(0x020, SC, 0);
     }
     barrier(Flight{});
-    read(2 * kb + 2, 0);
-    read_scales(kb + 1);
-    issue(2 * kb + 5);
-    multiply(1);
-    if constexpr (!WIDE) {
-      order<FIRST, 3 * (TM + TN), 0>();
-      order<REST, 0, CA + CB>();
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      read(2 * kb + 2, 0, f);
+      read_scale(kb + 1, f);
+      copy(2 * kb + 5, f);
     }
+    multiply(1);
+    if constexpr (!WIDE) order<TM * TN, 3 * F, F>();
     next_scales();
   }
   // every copy has landed and every read is done: the buffers become the results' rows
