@@ -342,26 +342,38 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   uint8_t* mine = smem + wave * OUT;
   const int64_t mw = m0 + 32 * TM * wm;
   const int nw = (int)n0 + 32 * TN * wn;
-  auto values = [&](int i, int j, int v) {
+  // the four columns (j, v): their bias, and their values of tile row i
+  auto bias_of = [&](int j, int v) {
+    f32x4_t b = {0.0f, 0.0f, 0.0f, 0.0f};
     const int n = nw + 32 * j + 8 * v + 4 * half;
-    f32x4_t r = {acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
-    if (g.bias && !split)
+    if (g.bias && !split) {
+      if (n + 4 <= g.N)
+        b = __builtin_bit_cast(f32x4_t, (u32x4_t) * reinterpret_cast<const u32x4_e4*>(g.bias + n));
+      else
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] += n + e < g.N ? g.bias[n + e] : 0.0f;
-    return r;
+        for (int e = 0; e < 4; ++e)
+          if (n + e < g.N) b[e] = g.bias[n + e];
+    }
+    return b;
+  };
+  auto values = [&](int i, int j, int v, f32x4_t b) {
+    return f32x4_t{acc[i][j][4 * v] + b[0], acc[i][j][4 * v + 1] + b[1], acc[i][j][4 * v + 2] + b[2],
+                   acc[i][j][4 * v + 3] + b[3]};
   };
   auto settle = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
   if (y16) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+      for (int v = 0; v < 4; ++v) {
+        const f32x4_t b = bias_of(j, v);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const f32x4_t r = values(i, j, v);
+        for (int i = 0; i < TM; ++i) {
+          const f32x4_t r = values(i, j, v, b);
           *reinterpret_cast<u32x2_t*>(mine + (32 * i + l32) * PITCH16 + 64 * j + 16 * v + 8 * half) =
               u32x2_t{bf16x2_rne(r[0], r[1]), bf16x2_rne(r[2], r[3])};
         }
+      }
     settle();
     constexpr int PIECES = 4 * TN;  // of 8 values a row
     const int col = 8 * (lane % PIECES), left = g.N - nw - col;
@@ -385,13 +397,15 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
   for (int i0 = 0; i0 < TM; i0 += TP) {
 #pragma unroll
-    for (int i = 0; i < TP; ++i)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+      for (int v = 0; v < 4; ++v) {
+        const f32x4_t b = bias_of(j, v);
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
+        for (int i = 0; i < TP; ++i)
           *reinterpret_cast<f32x4_t*>(mine + (32 * i + l32) * PITCH32 + 128 * j + 32 * v + 16 * half) =
-              values(i0 + i, j, v);
+              values(i0 + i, j, v, b);
+      }
     settle();
     constexpr int PIECES = 8 * TN;  // of 4 values a row
     const int col = 4 * (lane % PIECES), left = g.N - nw - col;
