@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(64 * W)
     uint32_t bsc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = min(k0 + u * W, g.KB - 1);
+      const int kb = k0 + u * W;
+      if (kb >= g.KB) break;
       b[u][0] = *reinterpret_cast<const u32x4_t*>(bp + (int64_t)kb * kFp8Block);
       b[u][1] = *reinterpret_cast<const u32x4_t*>(bp + (int64_t)kb * kFp8Block + 64);
       bsc[u] = g.bs[((int64_t)(kb >> 2) * g.N + n) * 4 + (kb & 3)];
@@ -545,13 +546,22 @@ __global__ void __launch_bounds__(64 * W)
     static_cast<float*>(g.y)[at] = s;
 }
 
-// column sums from the tile quantiser's partials, in row order
-__global__ void __launch_bounds__(64) k_fp8_colsum(const float* __restrict__ part, int nrb, int64_t N,
-                                                   float* __restrict__ out) {
-  const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (n >= N) return;
+// column sums from the tile quantiser's partials: 16 columns a workgroup, whose 16
+// threads of a column take the row blocks in turn; the first adds them in order
+__global__ void __launch_bounds__(256) k_fp8_colsum(const float* __restrict__ part, int nrb, int N,
+                                                    float* __restrict__ out) {
+  __shared__ float lds[16][17];
+  const int col = threadIdx.x & 15, lane = threadIdx.x >> 4, n = blockIdx.x * 16 + col;
   float s = 0.0f;
-  for (int r = 0; r < nrb; ++r) s += part[(int64_t)r * N + n];
+  if (n < N)
+#pragma unroll 4
+    for (int r = lane; r < nrb; r += 16) s += part[(int64_t)r * N + n];
+  lds[lane][col] = s;
+  __syncthreads();
+  if (lane != 0 || n >= N) return;
+  s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s += lds[k][col];
   out[n] = s;
 }
 
@@ -817,8 +827,8 @@ int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const v
       {x, M, K, ldx, nullptr, nullptr, base + L.xtc, base + L.xts, nullptr, x_dtype, 0}};
   ASP_TRY(fp8_quantize_tiles(dw ? 2 : 1, jobs, st));
   if (db) {
-    k_fp8_colsum<<<dim3((unsigned)((N + 63) / 64)), 64, 0, st>>>(
-        reinterpret_cast<const float*>(base + L.sums), (int)fp8_blocks(M), N, db);
+    k_fp8_colsum<<<dim3((unsigned)((N + 15) / 16)), 256, 0, st>>>(
+        reinterpret_cast<const float*>(base + L.sums), (int)fp8_blocks(M), (int)N, db);
     ASP_TRY(launch_status("fp8 column sums"));
   }
   if (dx && M > 0) {

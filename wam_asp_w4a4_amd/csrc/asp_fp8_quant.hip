@@ -45,30 +45,33 @@ struct TileArgs {
   int tiles0;  // workgroups of the first job
 };
 
-// Tile form: a workgroup reads a 128 x 128 tile once and writes from it the row
-// form, the transposed form and the tile's column sums.  Thread t holds columns
-// 8 (t % 16) .. +7 of rows 8 (t / 16) .. +7: a row's 128 columns are one DPP row
-// of lanes, and a column's 8 rows make 8 consecutive bytes of the transposed
-// codes, which turn through LDS in 8-byte chunks (chunk index XOR column / 8,
-// so that a wave's writes spread over the banks).  Rows and columns past the
-// matrix count as zeros: they pad the last block.
+// Tile form: a workgroup of 512 reads a 128 x 128 tile once and writes from it the
+// row form, the transposed form and the tile's column sums.  Thread t holds columns
+// 8 (t % 16) .. +7 of rows 4 (t / 16) .. +3, as they lie in memory: a row's 128
+// columns are one DPP row of lanes, and a column's 4 rows make 4 consecutive bytes of
+// the transposed codes, which turn through LDS (dword index XOR 2 (column / 8), so that
+// a wave's writes spread over the banks).  Rows and columns past the matrix count
+// as zeros: they pad the last block.  Half as many rows for a thread as a workgroup
+// of 256 would give it: XXX
+constexpr int kTileWaves = 8;
+
 template <typename XT>
-__device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (&cmax)[4][128],
-                                          float (&csum)[4][128], uint8_t (&turn)[128 * 128]) {
+__device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile,
+                                          uint32_t (&cmax)[kTileWaves][128],
+                                          float (&csum)[kTileWaves][128],
+                                          uint8_t (&turn)[128 * 128]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
   const int ncb = (int)((j.cols + 127) / 128);
   const int rb = tile / ncb, cb = tile % ncb;
-  const int64_t r0 = (int64_t)rb * 128 + 8 * rg, c0 = (int64_t)cb * 128 + 8 * cg;
-  const XT* x = static_cast<const XT*>(j.in);
-  float v[8][8];
+  const int64_t r0 = (int64_t)rb * 128 + 4 * rg, c0 = (int64_t)cb * 128 + 8 * cg;
+  const XT* x = static_cast<const XT*>(j.in) + r0 * j.ld + c0;
+  Raw<XT> raw[4] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t left = r0 + i < j.rows ? j.cols - c0 : 0;
-    load8(x + (r0 + i) * j.ld + c0, left, v[i]);
-  }
-  // magnitudes: per row (this thread's 8 columns) and per column (its 8 rows)
-  uint32_t ru[8], cu[8];
+  for (int i = 0; i < 4; ++i)
+    if (r0 + i < j.rows) raw_load(x + i * j.ld, (int)min(j.cols - c0, (int64_t)8), raw[i]);
+  // magnitudes: per row (this thread's 8 columns) and per column (its 4 rows)
+  uint32_t ru[4], cu[8];
   float cs[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -76,58 +79,77 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (
     cs[e] = 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float v[8];
+    unpack(raw[i], v);
     ru[i] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t u = finite_bits(v[i][e]);
+      const uint32_t u = finite_bits(v[e]);
       ru[i] = max(ru[i], u);
       cu[e] = max(cu[e], u);
-      cs[e] += v[i][e];
+      cs[e] += v[e];
     }
     ru[i] = row16_max(ru[i]);
   }
-  // the column results of the wave's four row groups, then of the four waves
+  if (j.codes_t || j.sums || j.square) {
+    // the column results of the wave's four row groups, then of the waves
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cu[e] = max(cu[e], (uint32_t)__shfl_xor((int)cu[e], 16));
-    cu[e] = max(cu[e], (uint32_t)__shfl_xor((int)cu[e], 32));
-    cs[e] += __shfl_xor(cs[e], 16);
-    cs[e] += __shfl_xor(cs[e], 32);
-    if (lane < 16) {
-      cmax[wave][8 * cg + e] = __builtin_bit_cast(float, cu[e]);
-      csum[wave][8 * cg + e] = cs[e];
+    for (int e = 0; e < 8; ++e) {
+      cu[e] = max(cu[e], (uint32_t)__shfl_xor((int)cu[e], 16));
+      cu[e] = max(cu[e], (uint32_t)__shfl_xor((int)cu[e], 32));
+      if (j.sums) {
+        cs[e] += __shfl_xor(cs[e], 16);
+        cs[e] += __shfl_xor(cs[e], 32);
+      }
+      if (lane < 16) {
+        cmax[wave][8 * cg + e] = cu[e];
+        csum[wave][8 * cg + e] = cs[e];
+      }
+    }
+    __syncthreads();
+    if (tid < 128) {
+      uint32_t u = 0;
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kTileWaves; ++w) {
+        u = max(u, cmax[w][tid]);
+        s += csum[w][tid];
+      }
+      cmax[0][tid] = u;
+      if (j.sums && (int64_t)cb * 128 + tid < j.cols)
+        j.sums[rb * j.cols + (int64_t)cb * 128 + tid] = s;
+    }
+    __syncthreads();
+    const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(&cmax[0][8 * cg]);
+    const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(&cmax[0][8 * cg + 4]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cu[e] = lo[e];
+      cu[4 + e] = hi[e];
     }
   }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cu[e] = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      cu[e] = max(cu[e], __builtin_bit_cast(uint32_t, cmax[w][8 * cg + e]));
-  }
-  if (j.square) {  // one scale for the tile: every thread sees every column group of a DPP row
+  if (j.square) {  // one scale for the tile: a DPP row's lanes hold every column group
     uint32_t u = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) u = max(u, cu[e]);
     u = row16_max(u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ru[e] = cu[e] = u;
+    for (int e = 0; e < 8; ++e) cu[e] = u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ru[i] = u;
   }
-  if (j.sums && tid < 128 && (int64_t)cb * 128 + tid < j.cols)
-    j.sums[rb * j.cols + (int64_t)cb * 128 + tid] =
-        (csum[0][tid] + csum[1][tid]) + (csum[2][tid] + csum[3][tid]);
   if (j.codes) {
     const int64_t pitch = (int64_t)ncb * 128;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (r0 + i >= j.rows) continue;
       const uint32_t s = fp8_scale_byte(ru[i]);
       const float inv = fp8_inverse(s);
+      float v[8];
+      unpack(raw[i], v);
       *reinterpret_cast<u32x2_t*>(j.codes + (r0 + i) * pitch + c0) =
-          u32x2_t{fp8_pack4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                  fp8_pack4(v[i][4], v[i][5], v[i][6], v[i][7], inv)};
+          u32x2_t{fp8_pack4(v[0], v[1], v[2], v[3], inv), fp8_pack4(v[4], v[5], v[6], v[7], inv)};
       if (cg == 0) {
         uint8_t* d = j.scales + ((int64_t)(cb >> 2) * j.rows + r0 + i) * 4;
         d[cb & 3] = (uint8_t)s;
@@ -138,13 +160,15 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (
   }
   if (!j.codes_t) return;
   const int nrb = (int)((j.rows + 127) / 128);
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack(raw[i], v[i]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const uint32_t s = fp8_scale_byte(cu[e]);
     const float inv = fp8_inverse(s);
-    *reinterpret_cast<u32x2_t*>(&turn[(8 * cg + e) * 128 + 8 * (rg ^ cg)]) =
-        u32x2_t{fp8_pack4(v[0][e], v[1][e], v[2][e], v[3][e], inv),
-                fp8_pack4(v[4][e], v[5][e], v[6][e], v[7][e], inv)};
+    *reinterpret_cast<uint32_t*>(&turn[(8 * cg + e) * 128 + 4 * (rg ^ 2 * cg)]) =
+        fp8_pack4(v[0][e], v[1][e], v[2][e], v[3][e], inv);
     if (rg == 0 && c0 + e < j.cols) {
       uint8_t* d = j.scales_t + ((int64_t)(rb >> 2) * j.cols + c0 + e) * 4;
       d[rb & 3] = (uint8_t)s;
@@ -154,8 +178,8 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int col = rg + 16 * i;  // 16 lanes write one column's 128 bytes
+  for (int i = 0; i < 4; ++i) {
+    const int col = rg + 32 * i;  // 16 lanes write one column's 128 bytes
     const int64_t c = (int64_t)cb * 128 + col;
     if (c < j.cols)
       *reinterpret_cast<u32x2_t*>(j.codes_t + c * ((int64_t)nrb * 128) + (int64_t)rb * 128 + 8 * cg) =
@@ -163,8 +187,9 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile, float (
   }
 }
 
-__global__ void __launch_bounds__(256) k_fp8_tiles(const TileArgs a) {
-  __shared__ float cmax[4][128], csum[4][128];
+__global__ void __launch_bounds__(64 * kTileWaves) k_fp8_tiles(const TileArgs a) {
+  __shared__ __attribute__((aligned(16))) uint32_t cmax[kTileWaves][128];
+  __shared__ float csum[kTileWaves][128];
   __shared__ __attribute__((aligned(16))) uint8_t turn[128 * 128];
   const bool second = (int)blockIdx.x >= a.tiles0;
   const Fp8TileJob& j = a.j[second ? 1 : 0];
@@ -242,7 +267,7 @@ int32_t fp8_quantize_tiles(int n, const Fp8TileJob* jobs, hipStream_t st) {
     if (total > INT32_MAX) return fail(ASP_ERR_SHAPE, "input too large for one launch");
   }
   if (total == 0) return ASP_OK;
-  k_fp8_tiles<<<dim3((unsigned)total), 256, 0, st>>>(a);
+  k_fp8_tiles<<<dim3((unsigned)total), 64 * kTileWaves, 0, st>>>(a);
   return launch_status("fp8 tile quantise");
 }
 
