@@ -100,15 +100,16 @@ def test_values_without_a_code_and_extremes():
         assert torch.isfinite(y[4:]).all()
 
 
-# every kernel: few rows, 64-tiles whole and split, 128-tiles, 256-tiles
+# every kernel: few rows, 32 x 32 tiles, tiles of 64, 128 (whole and split) and 256
 SHAPES = [(1, 16, 1), (1, 33, 128), (5, 100, 129), (16, 4096, 1024), (16, 40, 4224), (17, 16, 640),
           (33, 65, 127), (64, 64, 8192), (100, 130, 1537), (256, 1024, 1024), (777, 515, 300),
-          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130)]
+          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130),
+          (1000, 1003, 385), (520, 515, 33000)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_product_of_whole_numbers_is_exact(M, N, K):
-    """|a|, |b| <= 4 times a power of two for each block: sums of K <= 8448 products stay
+    """|a|, |b| <= 4 times a power of two for each block: sums of K <= 33000 products stay
     below 2^24 units of the smallest."""
     print(f"product {M}x{N}x{K}", flush=True)
     rng = np.random.default_rng(M * 7 + N * 3 + K)

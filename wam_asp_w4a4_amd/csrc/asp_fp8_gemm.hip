@@ -123,16 +123,16 @@ __device__ __forceinline__ void order() {
 // columns of a row of y.
 //
 // While a stage is multiplied from registers, the next one's fragments are read
-// from LDS, and three more stages are on their way into the four buffers: memory has
-// the time of three stages (one stage: 486 us at 8192^3, XXX now).  One barrier a
-// stage: by then every wave has the stage's fragments in registers, so its buffer
-// is free for the stage after the next three, and every wave's copies of the next
-// stage have landed.  The scales go the same way (the dword of a row's four blocks,
+// from LDS, and NB - 1 more stages are on their way into the NB buffers: at 8192^3
+// 436 us with three of them against 486 us with one of twice the size.  One barrier
+// a stage: by then every wave has the stage's fragments in registers, so its buffer
+// is free for the stage NB later, and every wave's copies of the next stage have
+// landed.  The scales go the same way (the dword of a row's four blocks,
 // for each block anew): loaded to registers, their wait would be one for every older
 // copy, since loads are counted in order.
 template <int TM, int TN, bool WIDE>
 __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
-  constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64;
+  constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64, NB = 4;
   constexpr int STAGE = (BM + BN) * SK;
   constexpr int CA = BM * SK / 4096, CB = BN * SK / 4096;  // a wave's copies of A and B for a stage
   constexpr int SC = (TM + TN + 3) / 4;                    // and of 64 rows' scales for a block
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   constexpr int TP = TM > 1 ? TM / 2 : 1;                  // tile rows of a float32 result at a time
   constexpr int OUT16 = 32 * TM * PITCH16, OUT32 = 32 * TP * PITCH32;
   constexpr int OUT = OUT16 > OUT32 ? OUT16 : OUT32;       // a wave's result region
-  constexpr int STAGING = 4 * STAGE + 2 * SCALES;
+  constexpr int STAGING = NB * STAGE + NB / 2 * SCALES;
   __shared__ __attribute__((aligned(16))) uint8_t smem[STAGING > 4 * OUT ? STAGING : 4 * OUT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   for (int c = 0; c < CA; ++c) offa[c] = source(wave * CA + c, mlast, g.lda);
 #pragma unroll
   for (int c = 0; c < CB; ++c) offb[c] = source(wave * CB + c, nlast, g.ldb);
-  // copy c of stage s (half s % 2 of block s / 2) into buffer s % 4; past the last stage the
+  // copy c of stage s (half s % 2 of block s / 2) into buffer s % NB; past the last stage the
   // last again, which nobody reads, so that the loop has no branch
   auto copy = [&](int s, int c) {
-    uint8_t* base = smem + (s & 3) * STAGE;
+    uint8_t* base = smem + (s & (NB - 1)) * STAGE;
     const int at = min(s, 2 * kb1 - 1) * SK;
     if (c < CA)
       buffer_copy16(ra, offa[c < CA ? c : 0], at, base + (wave * CA + c) * 1024);
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
     for (int c = 0; c < CA + CB; ++c) copy(s, c);
   };
-  // block kb's scales into scale buffer kb % 2: copy i has 64 rows of A, then of B (where
+  // block kb's scales into scale buffer kb % (NB / 2): copy i has 64 rows of A, then of B (where
   // the waves have more copies than there are, the first ones are made again)
   const uint8_t* scale_base[SC];
   int64_t scale_group[SC];
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   }
   auto issue_scales = [&](int kb) {
     const int64_t grp = min(kb, kb1 - 1) >> 2;
-    uint8_t* base = smem + 4 * STAGE + (kb & 1) * SCALES;
+    uint8_t* base = smem + NB * STAGE + (kb & (NB / 2 - 1)) * SCALES;
 #pragma unroll
     for (int c = 0; c < SC; ++c)
       buffer_copy4(descriptor(scale_base[c] + grp * scale_group[c], scale_bytes[c]), scale_off[c],
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   };
   uint32_t ca[TM], cb[TN], na[TM], nb[TN];
   auto read_scale = [&](int kb, int f) {
-    const uint8_t* base = smem + 4 * STAGE + (kb & 1) * SCALES + (min(kb, kb1 - 1) & 3);
+    const uint8_t* base = smem + NB * STAGE + (kb & (NB / 2 - 1)) * SCALES + (min(kb, kb1 - 1) & 3);
     if (f < TN)
       nb[f < TN ? f : 0] = base[4 * (BM + 32 * (wn * TN + f) + l32)];
     else
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   i32x8_t fa[2][TM], fb[2][TN];
   // fragment f of stage s: the columns' first
   auto read = [&](int s, int set, int f) {
-    const uint8_t* base = smem + (s & 3) * STAGE;
+    const uint8_t* base = smem + (s & (NB - 1)) * STAGE;
     if (f < TN)
       fb[set][f < TN ? f : 0] = frag(base + rowb + 32 * SK * f);
     else
@@ -274,9 +274,10 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
               fb[set][j], fa[set][i], acc[i][j], 0, 0, 0, (int)cb[j], 0, (int)ca[i]);
     }
   };
-  // The copies behind stage s + 1's when the barrier of stage s is reached: those of two
-  // stages and of one block's scales (which go behind an even stage's).
-  constexpr int FLIGHT = 2 * (CA + CB) + SC;
+  // The copies behind stage s + 1's when the barrier of stage s is reached: those of
+  // NB - 2 stages and of (NB - 2) / 2 blocks' scales (which go behind an even stage's).
+  constexpr int FLIGHT = (NB - 2) * (CA + CB) + (NB - 2) / 2 * SC;
+  static_assert(FLIGHT + CA + CB < 64, "the wait counts up to 63 loads");
   auto barrier = [&](auto flight) {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(decltype(flight)::value) : "memory");
@@ -289,13 +290,15 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   static_assert(CA + CB == F, "a copy for each fragment");
 
   if (kb0 < kb1) {
+    // in the order of the loop, which the waits count on
     issue_scales(kb0);
-    issue(2 * kb0);
-    issue(2 * kb0 + 1);
-    __builtin_amdgcn_sched_barrier(0);  // the waits count on this order
-    issue_scales(kb0 + 1);
-    issue(2 * kb0 + 2);
-    issue(2 * kb0 + 3);
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (s >= 2 && s % 2 == 0) issue_scales(kb0 + s / 2);
+      __builtin_amdgcn_sched_barrier(0);
+      issue(2 * kb0 + s);
+    }
     barrier(std::integral_constant<int, FLIGHT + CA + CB>{});
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -311,9 +314,9 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       read(2 * kb + 1, 1, f);
-      copy(2 * kb + 4, f);
+      copy(2 * kb + NB, f);
     }
-    issue_scales(kb + 2);
+    issue_scales(kb + NB / 2);
     multiply(0);
     if constexpr (!WIDE) {
       order<TM * TN, 2 * F, F>();
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
     for (int f = 0; f < F; ++f) {
       read(2 * kb + 2, 0, f);
       read_scale(kb + 1, f);
-      copy(2 * kb + 5, f);
+      copy(2 * kb + NB + 1, f);
     }
     multiply(1);
     if constexpr (!WIDE) order<TM * TN, 3 * F, F>();
@@ -452,6 +455,112 @@ __global__ void __launch_bounds__(256) k_fp8_join(const GemmK g) {
   store4(g, m, n, s, vec && ((uintptr_t)g.y & 15) == 0);
 }
 
+// k_fp8_mid: few tiles.  A workgroup owns a 32 x 32 tile of y, and its waves take
+// every kMidWaves-th block of K, each through two slots of LDS of its own: whole
+// rows of 128 bytes are copied (read straight into MFMA registers, 32 lines a load,
+// the same bytes take the load path twice as long: 11.7 against 6.6 us at 256 x 1024 x
+// 4096), and no wave waits for another until their partial tiles meet in LDS and are
+// added in wave order.  Bound by the latency of a wave's chain of blocks.  (Tiles of
+// 32 x 64 and 64 x 64 leave fewer workgroups: 8.2 and 10.5 us; eight waves: 6.7.)  Copy
+// j of a fragment fills 8 rows; slot s of it holds row s / 8, piece (s % 8) ^ (row % 8)
+// of that row's eight.
+constexpr int kMidWaves = 4;
+
+template <bool WIDE>
+__global__ void __launch_bounds__(64 * kMidWaves) k_fp8_mid(const GemmK g) {
+  constexpr int LD = 36;                     // floats of a partial tile's row
+  constexpr int SLOT = 8192 + 256;           // B's 32 rows, A's, and their scale dwords
+  constexpr int OPS = 9;                     // copies of a block
+  static_assert(32 * LD * 4 <= 2 * SLOT, "a partial tile fits a wave's slots");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kMidWaves * 2 * SLOT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  int tm, tn;
+  tile_at(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
+  const int64_t m0 = 32 * (int64_t)tm, n0 = 32 * (int64_t)tn;
+  const int mlast = (int)min((int64_t)32, g.M - m0) - 1, nlast = (int)min((int64_t)32, g.N - n0) - 1;
+  const __amdgpu_buffer_rsrc_t ra = descriptor(g.a + m0 * g.lda, (mlast + 1) * g.lda);
+  const __amdgpu_buffer_rsrc_t rb = descriptor(g.b + n0 * g.ldb, (nlast + 1) * g.ldb);
+  int offa[4], offb[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int row = 8 * c + (lane >> 3), piece = 16 * ((lane & 7) ^ (row & 7));
+    offa[c] = min(row, mlast) * (int)g.lda + piece;
+    offb[c] = min(row, nlast) * (int)g.ldb + piece;
+  }
+  // the scale dword of B's row l32 (lower lanes) or A's
+  const uint8_t* sp = half ? g.as + 4 * (m0 + min(l32, mlast)) : g.bs + 4 * (n0 + min(l32, nlast));
+  const int64_t sg = 4 * (int64_t)(half ? g.M : g.N);
+  uint8_t* mine = smem + wave * 2 * SLOT;
+  auto issue = [&](int kb, int slot) {
+    uint8_t* base = mine + slot * SLOT;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      buffer_copy16(rb, offb[c], kb * kFp8Block, base + 1024 * c);
+      buffer_copy16(ra, offa[c], kb * kFp8Block, base + 4096 + 1024 * c);
+    }
+    __builtin_amdgcn_global_load_lds(sp + (kb >> 2) * sg, base + 8192, 4, 0, 0);
+  };
+  f32x16_t acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+  auto piece = [&](const uint8_t* base, int p) {
+    return *reinterpret_cast<const u32x4_t*>(base + 128 * l32 + 16 * (p ^ (l32 & 7)));
+  };
+  auto frag = [&](const uint8_t* base, int kk) {
+    const u32x4_t a = piece(base, 4 * kk + 2 * half), b = piece(base, 4 * kk + 2 * half + 1);
+    return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3],
+                   (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+  };
+  if (wave < g.KB) issue(wave, 0);
+  int slot = 0;
+  for (int kb = wave; kb < g.KB; kb += kMidWaves, slot ^= 1) {
+    // the next block's slot was read to the end before this point
+    if (kb + kMidWaves < g.KB) {
+      issue(kb + kMidWaves, slot ^ 1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(OPS) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const uint8_t* base = mine + slot * SLOT;
+    const i32x8_t fb[2] = {frag(base, 0), frag(base, 1)};
+    const i32x8_t fa[2] = {frag(base + 4096, 0), frag(base + 4096, 1)};
+    const uint32_t cb = base[8192 + 4 * l32 + (kb & 3)], ca = base[8192 + 128 + 4 * l32 + (kb & 3)];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              decode_bf16(fb[kk][2 * s], fb[kk][2 * s + 1], scale_f32(cb)),
+              decode_bf16(fa[kk][2 * s], fa[kk][2 * s + 1], scale_f32(ca)), acc, 0, 0, 0);
+      } else {
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[kk], fa[kk], acc, 0, 0, 0, (int)cb,
+                                                              0, (int)ca);
+      }
+    }
+  }
+  __syncthreads();  // every wave is done with its slots: they become the partial tiles
+  // accumulator element v of lane l: column 8 (v / 4) + 4 (l / 32) + v % 4 of row l % 32
+  auto part = [&](int w, int row, int col) {
+    return reinterpret_cast<f32x4_t*>(smem + w * 2 * SLOT + (row * LD + col) * 4);
+  };
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    *part(wave, l32, 8 * v + 4 * half) =
+        f32x4_t{acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]};
+  __syncthreads();
+  static_assert(64 * kMidWaves == 256, "four columns of the tile for each thread");
+  const int row = tid / 8, col = 4 * (tid % 8);
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < kMidWaves; ++w) s += *part(w, row, col);
+  store4(g, m0 + row, (int)n0 + col, s, g.N % 4 == 0 && ((uintptr_t)g.y & 15) == 0);
+}
+
 // k_fp8_few: at most 16 rows of x.  Bound by the weight's bytes, so a workgroup
 // owns 16 columns of y over all of K, its W waves taking every W-th block
 // straight from memory into registers: lane l holds row l % 16 of each operand
@@ -569,19 +678,30 @@ __global__ void __launch_bounds__(256) k_fp8_colsum(const float* __restrict__ pa
 
 constexpr int kFewRows = 16;
 
+enum Kernel { kTiles256, kTiles128, kTiles64, kMid };
+
 struct Plan {
-  int tile;  // 256, 128 or 64: the square tile's side
-  int slices;
+  Kernel kernel;
+  int slices;  // of K
 };
 
+// The kernel for more than kFewRows rows.  A larger tile reads fewer bytes for its
+// products: 256 x 256 tiles reach 2560 TFLOP/s at 8192^3, 128 x 128 ones (two a CU)
+// 1780.  But a tile is one CU's work: beyond half a round of 256-tiles (128) they are
+// faster (2048 x 4096 x 4096, exactly 128: 59 against 43 us with 512 tiles of 128),
+// below that 128-tiles while they fill three quarters of the CUs.  A long K over
+// fewer of them is split into slices whose float32 partial sums a second kernel adds.
+// What is left is bound by latency: up to 768 tiles of 32 x 32 are k_fp8_mid's (256 x
+// 1024 x 4096: 6.6 us, against 11.6 with 64-tiles in four slices), more are 64-tiles
+// (256 x 4096 x 1024, 1024 tiles of 32: 6.0 us against 7.6).
 Plan plan(int64_t M, int64_t N, int64_t K) {
   auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   const int64_t KB = fp8_blocks(K);
-  if (tiles(256) >= 192) return {256, 1};
-  if (tiles(128) >= 192) return {128, 1};
-  Plan p = {64, 1};
-  while (p.slices < 8 && tiles(64) * p.slices < 256 && KB / (2 * p.slices) >= 4) p.slices *= 2;
-  return p;
+  if (tiles(256) > 128) return {kTiles256, 1};
+  if (tiles(128) >= 192) return {kTiles128, 1};
+  for (int s = 2; s <= 16; s *= 2)
+    if (KB / s >= 32 && tiles(128) * s >= 192 && tiles(128) >= 16) return {kTiles128, s};
+  return {tiles(32) <= 768 ? kMid : kTiles64, 1};
 }
 
 GemmK kernel_args(const Fp8Gemm& g, int slices) {
@@ -605,6 +725,15 @@ int32_t launch_tiles(GemmK k, hipStream_t st) {
   k.tiles_n = (int)tn;
   k_fp8_gemm<TM, TN, WIDE><<<dim3((unsigned)(tm * tn), (unsigned)k.slices), 256, 0, st>>>(k);
   return launch_status("fp8 gemm");
+}
+
+template <bool WIDE>
+int32_t launch_mid(GemmK k, hipStream_t st) {
+  const int64_t tm = (k.M + 31) / 32, tn = (k.N + 31) / 32;
+  k.tiles_m = (int)tm;
+  k.tiles_n = (int)tn;
+  k_fp8_mid<WIDE><<<dim3((unsigned)(tm * tn)), 64 * kMidWaves, 0, st>>>(k);
+  return launch_status("fp8 mid gemm");
 }
 
 template <typename XT, bool WIDE>
@@ -643,10 +772,11 @@ int32_t fp8_gemm_fused(const Fp8Gemm& g, const void* x, int32_t x_dtype, int64_t
 namespace {
 template <bool WIDE>
 int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
-  switch (p.tile) {
-    case 256: return launch_tiles<4, 4, WIDE>(k, st);
-    case 128: return launch_tiles<2, 2, WIDE>(k, st);
-    default: return launch_tiles<1, 1, WIDE>(k, st);
+  switch (p.kernel) {
+    case kTiles256: return launch_tiles<4, 4, WIDE>(k, st);
+    case kTiles128: return launch_tiles<2, 2, WIDE>(k, st);
+    case kTiles64: return launch_tiles<1, 1, WIDE>(k, st);
+    default: return launch_mid<WIDE>(k, st);
   }
 }
 }  // namespace
