@@ -71,9 +71,12 @@ def test_c_calls_validate_before_any_launch():
     assert b(dy=None) == 1 and b(x=None) == 1 and b(wt=None) == 1 and b(nb=need - 1) == 5
     assert b(dw=FAKE + 2) == 3
     assert b(dx=None, dw=None, db=None) == 0      # nothing is asked for
-    g = lambda a=FAKE, ws=FAKE, nb=1 << 30: _status(
-        "asp_fp8_gemm", a, FAKE, FAKE, FAKE, 64, 64, 8192, None, FAKE, 0, ws, nb, None)
-    assert g(a=None) == 1 and g(a=FAKE + 4) == 3 and g(nb=0) == 5 and g(ws=None) == 1
+    # few tiles of a long K: slices, whose sums need a workspace
+    need = B.asp_fp8_gemm_workspace_bytes(512, 512, 65536)
+    assert need > 0 and B.asp_fp8_gemm_workspace_bytes(64, 64, 8192) == 0
+    g = lambda a=FAKE, ws=FAKE, nb=need - 1: _status(
+        "asp_fp8_gemm", a, FAKE, FAKE, FAKE, 512, 512, 65536, None, FAKE, 0, ws, nb, None)
+    assert g(a=None) == 1 and g(a=FAKE + 4) == 3 and g() == 5 and g(ws=None) == 1
 
 
 def _norm(**o):

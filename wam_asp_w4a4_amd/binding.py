@@ -13,6 +13,7 @@ no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -413,9 +414,32 @@ def _at(a):
     return None if a is None else a.data_ptr()
 
 
-def _size(fn, *args):
+def stream_on(stream, device):
+    """The stream handle for a launch on `device`: the caller's, else torch's current one."""
+    if stream is not None or device.type != "cuda":
+        return stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def launch(device, fn, *args):
+    """fn(*args) with `device` current, raising the library's error.  For callers that
+    have checked their tensors and pass addresses."""
+    import torch
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        _check(status)
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(name, *args):
+    """A size that depends on the numbers alone."""
     out = ctypes.c_size_t(0)
-    _check(fn(*args, ctypes.byref(out)))
+    _check(getattr(lib(), name)(*args, ctypes.byref(out)))
     return out.value
 
 
@@ -448,7 +472,7 @@ def asp_fp8_dequantize(codes, scales, rows, cols, out, dtype, stream=None):
 
 
 def asp_fp8_gemm_workspace_bytes(M, N, K) -> int:
-    return _size(lib().asp_fp8_gemm_workspace_bytes, M, N, K)
+    return _size("asp_fp8_gemm_workspace_bytes", M, N, K)
 
 
 def asp_fp8_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, bias, y, y_dtype, workspace=None,
@@ -459,7 +483,7 @@ def asp_fp8_gemm(a_codes, a_scales, b_codes, b_scales, M, N, K, bias, y, y_dtype
 
 
 def asp_fp8_workspace_bytes(M, N, K) -> int:
-    return _size(lib().asp_fp8_workspace_bytes, M, N, K)
+    return _size("asp_fp8_workspace_bytes", M, N, K)
 
 
 def asp_fp8_forward(x, x_dtype, ldx, M, N, K, w_codes, w_scales, bias, y, y_dtype,
@@ -470,7 +494,7 @@ def asp_fp8_forward(x, x_dtype, ldx, M, N, K, w_codes, w_scales, bias, y, y_dtyp
 
 
 def asp_fp8_backward_workspace_bytes(M, N, K) -> int:
-    return _size(lib().asp_fp8_backward_workspace_bytes, M, N, K)
+    return _size("asp_fp8_backward_workspace_bytes", M, N, K)
 
 
 def asp_fp8_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, M, N, K, wt_codes, wt_scales, dx,
@@ -491,7 +515,7 @@ def asp_norm_gate(x, ldx, y, ldy, dtype, M, C, alpha, post, post_w, gate, pre, p
 
 
 def asp_norm_gate_backward_workspace_bytes(M, C, G) -> int:
-    return _size(lib().asp_norm_gate_backward_workspace_bytes, M, C, G)
+    return _size("asp_norm_gate_backward_workspace_bytes", M, C, G)
 
 
 def asp_norm_gate_backward(dh, lddh, dn, lddn, dn_dtype, h, ldh, y, ldy, dtype, M, C, alpha, post,

@@ -10,7 +10,6 @@ All arithmetic happens inside libasp.
 
 from __future__ import annotations
 
-import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -21,14 +20,6 @@ from .layer import _Y_DTYPES, _check_ws, _check_y
 BLOCK = 128
 _NAMES = {torch.float32: "f32", torch.bfloat16: "bf16"}
 _CODES = {torch.float32: B.ASP_F32, torch.bfloat16: B.ASP_BF16}
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """The device made current for a launch, where it is not already."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
 
 
 def _lend(stream, *tensors):
@@ -53,8 +44,17 @@ def _stride(t):
     return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
 
 
-def _check_rows(t, name, rows, cols, device, dtypes=tuple(_NAMES)):
-    """t must be a (rows, cols) matrix with contiguous rows that do not overlap."""
+def _check_rows(t, name, rows, cols, device, dtypes=_CODES):
+    """t must be a (rows, cols) matrix with contiguous rows that do not overlap (rows
+    None: any number).  Returns its row stride."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device:
+        shape = t.shape
+        if len(shape) == 2 and shape[1] == cols and (rows is None or shape[0] == rows):
+            if t.is_contiguous():
+                return cols
+            ld = _stride(t)
+            if (cols == 1 or t.stride(1) == 1) and ld >= cols:
+                return ld
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
@@ -64,17 +64,17 @@ def _check_rows(t, name, rows, cols, device, dtypes=tuple(_NAMES)):
                          f"got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.numel() and ((cols > 1 and t.stride(1) != 1) or _stride(t) < cols):
-        raise ValueError(f"the rows of {name} must be contiguous and apart, "
-                         f"got strides {t.stride()}")
+    raise ValueError(f"the rows of {name} must be contiguous and apart, got strides {t.stride()}")
 
 
 def _check_vector(t, name, size, device):
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == (size,) \
+            and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
         raise TypeError(f"{name} must be a float32 tensor")
-    if tuple(t.shape) != (size,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be {size} contiguous entries on {device}, "
-                         f"got {tuple(t.shape)} on {t.device}")
+    raise ValueError(f"{name} must be {size} contiguous entries on {device}, "
+                     f"got {tuple(t.shape)} on {t.device}")
 
 
 def _groups(cols):
@@ -83,6 +83,17 @@ def _groups(cols):
 
 def _pitch(cols):
     return (cols + BLOCK - 1) // BLOCK * BLOCK
+
+
+def _check_format(rows, cols, codes, scales, name):
+    for t, shape in ((codes, (rows, _pitch(cols))), (scales, (_groups(cols), rows, 4))):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+            raise TypeError(f"{name}: codes and scales must be uint8 tensors")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: a {rows} x {cols} matrix needs contiguous {shape}, "
+                             f"got {tuple(t.shape)}")
+    if codes.device != scales.device:
+        raise ValueError(f"{name}: codes on {codes.device}, scales on {scales.device}")
 
 
 @dataclass
@@ -101,16 +112,7 @@ class Fp8Tensor:
 
     def check(self, name="the 8-bit tensor"):
         """Codes and scales are what rows and cols say (the C ABI sees only pointers)."""
-        for t, shape in ((self.codes, (self.rows, _pitch(self.cols))),
-                         (self.scales, (_groups(self.cols), self.rows, 4))):
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
-                raise TypeError(f"{name}: codes and scales must be uint8 tensors")
-            if tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name}: a {self.rows} x {self.cols} matrix needs contiguous "
-                                 f"{shape}, got {tuple(t.shape)}")
-        if self.codes.device != self.scales.device:
-            raise ValueError(f"{name}: codes on {self.codes.device}, scales on "
-                             f"{self.scales.device}")
+        _check_format(self.rows, self.cols, self.codes, self.scales, name)
 
     def dequantize(self, dtype="f32", stream=None):
         """The values as a float32 or bf16 matrix."""
@@ -119,9 +121,9 @@ class Fp8Tensor:
             raise ValueError(f"dtype must be 'f32' or 'bf16', not {dtype!r}")
         out = torch.empty((self.rows, self.cols), dtype=_Y_DTYPES[dtype],
                           device=self.codes.device)
-        with _on(out.device):
-            B.asp_fp8_dequantize(self.codes, self.scales, self.rows, self.cols, out,
-                                 B.DTYPES[dtype], stream)
+        dev = out.device
+        B.launch(dev, B.lib().asp_fp8_dequantize, self.codes.data_ptr(), self.scales.data_ptr(),
+                 self.rows, self.cols, out.data_ptr(), B.DTYPES[dtype], B.stream_on(stream, dev))
         _lend(stream, out)
         return out
 
@@ -131,12 +133,13 @@ def quantize(x, transpose=False, stream=None):
     ``transpose`` its transpose (K x M, blocks of 128 of x's rows)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor")
-    _check_rows(x, "x", None, x.shape[1], x.device)
     M, K = x.shape
-    q = Fp8Tensor.empty(K, M, x.device) if transpose else Fp8Tensor.empty(M, K, x.device)
-    call = B.asp_fp8_quantize_t if transpose else B.asp_fp8_quantize
-    with _on(x.device):
-        call(x, _CODES[x.dtype], M, K, _stride(x), q.codes, q.scales, stream)
+    dev = x.device
+    ld = _check_rows(x, "x", M, K, dev)
+    q = Fp8Tensor.empty(K, M, dev) if transpose else Fp8Tensor.empty(M, K, dev)
+    fn = B.lib().asp_fp8_quantize_t if transpose else B.lib().asp_fp8_quantize
+    B.launch(dev, fn, x.data_ptr(), _CODES[x.dtype], M, K, ld, q.codes.data_ptr(),
+             q.scales.data_ptr(), B.stream_on(stream, dev))
     _lend(stream, q.codes, q.scales)
     return q
 
@@ -158,25 +161,26 @@ class Fp8Layer:
         transposed codes too, which dx needs."""
         if not isinstance(w, torch.Tensor) or w.dim() != 2:
             raise ValueError("w must be a 2-D torch tensor")
-        _check_rows(w, "w", None, w.shape[1], w.device)
         N, K = w.shape
+        dev = w.device
+        ld = _check_rows(w, "w", N, K, dev)
         if bias is not None:
             _check_vector(bias, "bias", N, w.device)
-        q = Fp8Tensor.empty(N, K, w.device)
-        t = Fp8Tensor.empty(K, N, w.device) if backward else None
+        q = Fp8Tensor.empty(N, K, dev)
+        t = Fp8Tensor.empty(K, N, dev) if backward else None
         ct, st = (t.codes, t.scales) if backward else (None, None)
-        with _on(w.device):
-            B.asp_fp8_quantize_weight(w, _CODES[w.dtype], N, K, _stride(w), q.codes, q.scales,
-                                      ct, st, stream)
+        B.launch(dev, B.lib().asp_fp8_quantize_weight, w.data_ptr(), _CODES[w.dtype], N, K, ld,
+                 q.codes.data_ptr(), q.scales.data_ptr(), B._at(ct), B._at(st),
+                 B.stream_on(stream, dev))
         _lend(stream, q.codes, q.scales, ct, st)
         return cls(N, K, q.codes, q.scales, ct, st, bias)
 
     def __post_init__(self):
-        Fp8Tensor(self.N, self.K, self.codes, self.scales).check("the weight")
+        _check_format(self.N, self.K, self.codes, self.scales, "the weight")
         if (self.codes_t is None) != (self.scales_t is None):
             raise ValueError("codes_t and scales_t belong together")
         if self.codes_t is not None:
-            Fp8Tensor(self.K, self.N, self.codes_t, self.scales_t).check("the transposed weight")
+            _check_format(self.K, self.N, self.codes_t, self.scales_t, "the transposed weight")
             if self.codes_t.device != self.codes.device:
                 raise ValueError("the transposed weight is on another device")
         if self.bias is not None:
@@ -195,38 +199,41 @@ class Fp8Layer:
     def forward(self, x, y_dtype=None, workspace=None, y=None, stream=None):
         """y = Q(x) W^T + bias for x (M x K, float32 or bf16, any row stride) or an
         ``Fp8Tensor``; y_dtype 'f32' or 'bf16' (None: x's; 'bf16' for codes)."""
+        dev, N, K = self.codes.device, self.N, self.K
         quantised = isinstance(x, Fp8Tensor)
         if quantised:
             x.check("x")
-            if x.cols != self.K:
-                raise ValueError(f"x must be (M, {self.K}), got ({x.rows}, {x.cols})")
-            if x.codes.device != self.device:
-                raise ValueError(f"x is on {x.codes.device}, the layer on {self.device}")
+            if x.cols != K:
+                raise ValueError(f"x must be (M, {K}), got ({x.rows}, {x.cols})")
+            if x.codes.device != dev:
+                raise ValueError(f"x is on {x.codes.device}, the layer on {dev}")
             M, y_dtype = x.rows, y_dtype or "bf16"
         else:
-            _check_rows(x, "x", None, self.K, self.device)
+            ld = _check_rows(x, "x", None, K, dev)
             M, y_dtype = x.shape[0], y_dtype or _NAMES[x.dtype]
-        _check_y(y, M, self.N, y_dtype, self.device)
+        _check_y(y, M, N, y_dtype, dev)
         size = B.asp_fp8_gemm_workspace_bytes if quantised else B.asp_fp8_workspace_bytes
-        need = size(M, self.N, self.K)
+        need = have = size(M, N, K)
         made = []
         if y is None:
-            y = torch.empty((M, self.N), dtype=_Y_DTYPES[y_dtype], device=self.device)
+            y = torch.empty((M, N), dtype=_Y_DTYPES[y_dtype], device=dev)
             made.append(y)
         if workspace is not None:
-            _check_ws(workspace, need, self.device)
+            _check_ws(workspace, need, dev)
+            have = workspace.numel()
         elif need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             made.append(workspace)
-        have = 0 if workspace is None else workspace.numel()
-        with _on(self.device):
-            if quantised:
-                B.asp_fp8_gemm(x.codes, x.scales, self.codes, self.scales, M, self.N, self.K,
-                               self.bias, y, B.DTYPES[y_dtype], workspace, have, stream)
-            else:
-                B.asp_fp8_forward(x, _CODES[x.dtype], _stride(x), M, self.N, self.K, self.codes,
-                                  self.scales, self.bias, y, B.DTYPES[y_dtype], workspace, have,
-                                  stream)
+        at = B._at
+        tail = (self.codes.data_ptr(), self.scales.data_ptr())
+        out = (at(self.bias), y.data_ptr(), B.DTYPES[y_dtype], at(workspace), have,
+               B.stream_on(stream, dev))
+        if quantised:
+            B.launch(dev, B.lib().asp_fp8_gemm, x.codes.data_ptr(), x.scales.data_ptr(), *tail, M, N,
+                     K, *out)
+        else:
+            B.launch(dev, B.lib().asp_fp8_forward, x.data_ptr(), _CODES[x.dtype], ld, M, N, K, *tail,
+                     *out)
         _lend(stream, *made)
         return y
 
@@ -235,36 +242,37 @@ class Fp8Layer:
         """(dx, dw, db) for dy (M x N): dx in dy's type where ``need_dx``, dw (N x K, of
         ``dw_dtype``) where x is given, db float32 where ``need_db`` (None: where the
         layer has a bias); the others are None."""
-        _check_rows(dy, "dy", None, self.N, self.device)
+        dev, N, K = self.codes.device, self.N, self.K
+        lddy, ldx = _check_rows(dy, "dy", None, N, dev), K
         M = dy.shape[0]
         if x is not None:
-            _check_rows(x, "x", M, self.K, self.device)
+            ldx = _check_rows(x, "x", M, K, dev)
         if dw_dtype not in _Y_DTYPES:
             raise ValueError(f"dw_dtype must be 'f32' or 'bf16', not {dw_dtype!r}")
         if need_dx and self.codes_t is None:
             raise ValueError("dx needs the transposed weight: pack the layer with backward=True")
-        dev, made = self.device, []
+        made = []
 
         def new(shape, dtype):
             made.append(torch.empty(shape, dtype=dtype, device=dev))
             return made[-1]
 
-        dx = new((M, self.K), dy.dtype) if need_dx else None
-        dw = new((self.N, self.K), _Y_DTYPES[dw_dtype]) if x is not None else None
-        db = new((self.N,), torch.float32) if (self.bias is not None if need_db is None
-                                              else need_db) else None
-        if dx is None and dw is None and db is None:
+        if need_db is None:
+            need_db = self.bias is not None
+        dx = new((M, K), dy.dtype) if need_dx else None
+        dw = new((N, K), _Y_DTYPES[dw_dtype]) if x is not None else None
+        db = new((N,), torch.float32) if need_db else None
+        if not made:
             return None, None, None
-        need = B.asp_fp8_backward_workspace_bytes(M, self.N, self.K)
+        need = B.asp_fp8_backward_workspace_bytes(M, N, K)
         if workspace is not None:
             _check_ws(workspace, need, dev)
         else:
-            workspace = new((max(need, 256),), torch.uint8)
-        with _on(dev):
-            B.asp_fp8_backward(dy, _CODES[dy.dtype], _stride(dy), x,
-                               B.ASP_F32 if x is None else _CODES[x.dtype],
-                               self.K if x is None else _stride(x), M, self.N, self.K,
-                               self.codes_t, self.scales_t, dx, _CODES[dy.dtype], dw,
-                               B.DTYPES[dw_dtype], db, workspace, workspace.numel(), stream)
+            workspace = new((need,), torch.uint8)
+        at, code = B._at, _CODES[dy.dtype]
+        B.launch(dev, B.lib().asp_fp8_backward, dy.data_ptr(), code, lddy, at(x),
+                 B.ASP_F32 if x is None else _CODES[x.dtype], ldx, M, N, K, at(self.codes_t),
+                 at(self.scales_t), at(dx), code, at(dw), B.DTYPES[dw_dtype], at(db),
+                 workspace.data_ptr(), workspace.numel(), B.stream_on(stream, dev))
         _lend(stream, *made)
         return dx, dw, db

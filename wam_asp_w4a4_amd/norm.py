@@ -18,8 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import binding as B
-from .fp8 import (_CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture, _on,
-                  _stride)
+from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture
 from .layer import _Y_DTYPES, _check_ws
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
@@ -64,7 +63,7 @@ def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, s
             continue
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
             raise TypeError(f"{name} must be a float32 tensor")
-        if tuple(t.shape) != (G, C) and not (G == 1 and tuple(t.shape) == (C,)):
+        if t.shape != (G, C) and not (G == 1 and t.shape == (C,)):
             raise ValueError(f"{name} must be ({G}, {C}), got {tuple(t.shape)}")
         if t.device != device or (C > 1 and t.stride(-1) != 1):
             raise ValueError(f"the rows of {name} must be contiguous and on {device}")
@@ -90,15 +89,15 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         raise ValueError("x must be a 2-D torch tensor")
     M, C = x.shape
     dev = x.device
-    _check_rows(x, "x", M, C, dev)
+    ldx, ldy, same = _check_rows(x, "x", M, C, dev), C, (x.dtype,)
     if y is not None:
-        _check_rows(y, "y", M, C, dev, (x.dtype,))
+        ldy = _check_rows(y, "y", M, C, dev, same)
     post, pre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
                               scale, shift, offsets)
     made = []
-    write = h
+    write, ldh = h, C
     if h is not None:
-        _check_rows(h, "h", M, C, dev, (x.dtype,))
+        ldh = _check_rows(h, "h", M, C, dev, same)
     elif y is None and alpha == 1.0 and pre:
         h = x
     else:
@@ -125,16 +124,18 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     else:
         if out is not None and out not in _Y_DTYPES:
             raise ValueError(f"out must be 'f32', 'bf16' or 'fp8', not {out!r}")
+        ldn = C
         if n is None:
             n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
             made.append(n)
         else:
-            _check_rows(n, "n", M, C, dev, tuple(_CODES) if out is None else (_Y_DTYPES[out],))
-        values, code, ldn = n, _CODES[n.dtype], _stride(n)
-    with _on(dev):
-        B.asp_norm_gate(x, _stride(x), y, C if y is None else _stride(y), _CODES[x.dtype], M, C,
-                        alpha, post, post_weight, gate, pre, weight, bias, scale, shift, ldt, G,
-                        offsets, eps, write, _stride(h), values, code, ldn, scales, stream)
+            ldn = _check_rows(n, "n", M, C, dev, _CODES if out is None else (_Y_DTYPES[out],))
+        values, code = n, _CODES[n.dtype]
+    at = B._at
+    B.launch(dev, B.lib().asp_norm_gate, x.data_ptr(), ldx, at(y), ldy, _CODES[x.dtype], M, C, alpha,
+             post, at(post_weight), at(gate), pre, at(weight), at(bias), at(scale), at(shift), ldt, G,
+             at(offsets), eps, at(write), ldh, at(values), code, ldn, at(scales),
+             B.stream_on(stream, dev))
     _lend(stream, *made)
     return h, n
 
@@ -151,17 +152,18 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         raise ValueError("h must be a 2-D torch tensor")
     M, C = h.shape
     dev = h.device
-    _check_rows(h, "h", M, C, dev)
+    ldh, ldy, lddh, lddn, lddx, lddy = _check_rows(h, "h", M, C, dev), C, C, C, C, C
+    same = (h.dtype,)
     if y is not None:
-        _check_rows(y, "y", M, C, dev, (h.dtype,))
+        ldy = _check_rows(y, "y", M, C, dev, same)
     if dh is not None:
-        _check_rows(dh, "dh", M, C, dev, (h.dtype,))
+        lddh = _check_rows(dh, "dh", M, C, dev, same)
     kpost, kpre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
                                 scale, shift, offsets)
     if (dn is not None) != bool(kpre):
         raise ValueError("dn belongs to the pre norm's result")
     if dn is not None:
-        _check_rows(dn, "dn", M, C, dev)
+        lddn = _check_rows(dn, "dn", M, C, dev)
     if dh is None and dn is None:
         raise ValueError("neither dh nor dn is given")
     made = []
@@ -171,19 +173,19 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         return made[-1]
 
     def like(t):
-        return None if t is None else new(tuple(t.shape))
+        return None if t is None else new(t.shape)
 
     if dx is None:
         dx = new((M, C), h.dtype)
     else:
-        _check_rows(dx, "dx", M, C, dev, (h.dtype,))
+        lddx = _check_rows(dx, "dx", M, C, dev, same)
     if y is None:
         if dy is not None:
             raise ValueError("dy without y")
     elif dy is None:
         dy = new((M, C), h.dtype)
     else:
-        _check_rows(dy, "dy", M, C, dev, (h.dtype,))
+        lddy = _check_rows(dy, "dy", M, C, dev, same)
     g = NormGrads(dx, dy, like(post_weight), like(gate), like(weight), like(bias), like(scale),
                   like(shift))
     need = 0
@@ -193,14 +195,13 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
             workspace = new((need,), torch.uint8)
     if workspace is not None:
         _check_ws(workspace, need, dev)
-    with _on(dev):
-        B.asp_norm_gate_backward(
-            dh, C if dh is None else _stride(dh), dn, C if dn is None else _stride(dn),
-            B.ASP_F32 if dn is None else _CODES[dn.dtype], h, _stride(h), y,
-            C if y is None else _stride(y), _CODES[h.dtype], M, C, alpha, kpost, post_weight, gate,
-            kpre, weight, bias, scale, ldt, G, offsets, eps, dx, _stride(dx), dy,
-            C if dy is None else _stride(dy), g.post_weight, g.gate, g.weight, g.bias, g.scale,
-            g.shift, C, workspace, 0 if workspace is None else workspace.numel(), stream)
+    at = B._at
+    B.launch(dev, B.lib().asp_norm_gate_backward, at(dh), lddh, at(dn), lddn,
+             B.ASP_F32 if dn is None else _CODES[dn.dtype], h.data_ptr(), ldh, at(y), ldy,
+             _CODES[h.dtype], M, C, alpha, kpost, at(post_weight), at(gate), kpre, at(weight),
+             at(bias), at(scale), ldt, G, at(offsets), eps, at(dx), lddx, at(dy), lddy,
+             at(g.post_weight), at(g.gate), at(g.weight), at(g.bias), at(g.scale), at(g.shift), C,
+             at(workspace), 0 if workspace is None else workspace.numel(), B.stream_on(stream, dev))
     _lend(stream, *made)
     return g
 
