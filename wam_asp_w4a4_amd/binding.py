@@ -17,6 +17,7 @@ import functools
 import os
 
 import numpy as np
+import torch
 
 ABI_VERSION = 8
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasp.so")
@@ -418,14 +419,12 @@ def stream_on(stream, device):
     """The stream handle for a launch on `device`: the caller's, else torch's current one."""
     if stream is not None or device.type != "cuda":
         return stream
-    import torch
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def launch(device, fn, *args):
     """fn(*args) with `device` current, raising the library's error.  For callers that
     have checked their tensors and pass addresses."""
-    import torch
     if device.type != "cuda" or device.index == torch.cuda.current_device():
         status = fn(*args)
     else:

@@ -68,7 +68,7 @@ def _check_rows(t, name, rows, cols, device, dtypes=_CODES):
 
 
 def _check_vector(t, name, size, device):
-    if isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == (size,) \
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == (size,) \
             and t.device == device and t.is_contiguous():
         return
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
@@ -77,23 +77,23 @@ def _check_vector(t, name, size, device):
                      f"got {tuple(t.shape)} on {t.device}")
 
 
-def _groups(cols):
-    return (cols + 4 * BLOCK - 1) // (4 * BLOCK)
-
-
-def _pitch(cols):
-    return (cols + BLOCK - 1) // BLOCK * BLOCK
-
-
 def _check_format(rows, cols, codes, scales, name):
-    for t, shape in ((codes, (rows, _pitch(cols))), (scales, (_groups(cols), rows, 4))):
+    """Codes and scales of a rows x cols matrix (the C ABI sees only pointers)."""
+    blocks = (cols + BLOCK - 1) // BLOCK
+    want = ((rows, blocks * BLOCK), ((blocks + 3) // 4, rows, 4))
+    if isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) \
+            and codes.dtype is torch.uint8 and scales.dtype is torch.uint8 \
+            and codes.shape == want[0] and scales.shape == want[1] \
+            and codes.is_contiguous() and scales.is_contiguous() \
+            and codes.device == scales.device:
+        return
+    for t, shape in zip((codes, scales), want):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
             raise TypeError(f"{name}: codes and scales must be uint8 tensors")
         if t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: a {rows} x {cols} matrix needs contiguous {shape}, "
                              f"got {tuple(t.shape)}")
-    if codes.device != scales.device:
-        raise ValueError(f"{name}: codes on {codes.device}, scales on {scales.device}")
+    raise ValueError(f"{name}: codes on {codes.device}, scales on {scales.device}")
 
 
 @dataclass
@@ -106,12 +106,14 @@ class Fp8Tensor:
 
     @staticmethod
     def empty(rows, cols, device):
+        blocks = (cols + BLOCK - 1) // BLOCK
         return Fp8Tensor(rows, cols,
-                         torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=device),
-                         torch.empty((_groups(cols), rows, 4), dtype=torch.uint8, device=device))
+                         torch.empty((rows, blocks * BLOCK), dtype=torch.uint8, device=device),
+                         torch.empty(((blocks + 3) // 4, rows, 4), dtype=torch.uint8,
+                                     device=device))
 
     def check(self, name="the 8-bit tensor"):
-        """Codes and scales are what rows and cols say (the C ABI sees only pointers)."""
+        """Codes and scales are what rows and cols say."""
         _check_format(self.rows, self.cols, self.codes, self.scales, name)
 
     def dequantize(self, dtype="f32", stream=None):
@@ -208,33 +210,36 @@ class Fp8Layer:
             if x.codes.device != dev:
                 raise ValueError(f"x is on {x.codes.device}, the layer on {dev}")
             M, y_dtype = x.rows, y_dtype or "bf16"
+            need = B.asp_fp8_gemm_workspace_bytes(M, N, K)
         else:
             ld = _check_rows(x, "x", None, K, dev)
             M, y_dtype = x.shape[0], y_dtype or _NAMES[x.dtype]
-        _check_y(y, M, N, y_dtype, dev)
-        size = B.asp_fp8_gemm_workspace_bytes if quantised else B.asp_fp8_workspace_bytes
-        need = have = size(M, N, K)
+            need = B.asp_fp8_workspace_bytes(M, N, K)
         made = []
-        if y is None:
+        if y is not None or y_dtype not in _Y_DTYPES:
+            _check_y(y, M, N, y_dtype, dev)
+        else:
             y = torch.empty((M, N), dtype=_Y_DTYPES[y_dtype], device=dev)
             made.append(y)
+        have, ws = need, None
         if workspace is not None:
             _check_ws(workspace, need, dev)
-            have = workspace.numel()
+            have, ws = workspace.numel(), workspace.data_ptr()
         elif need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             made.append(workspace)
-        at = B._at
-        tail = (self.codes.data_ptr(), self.scales.data_ptr())
-        out = (at(self.bias), y.data_ptr(), B.DTYPES[y_dtype], at(workspace), have,
-               B.stream_on(stream, dev))
+            ws = workspace.data_ptr()
+        bias = self.bias
+        bias = None if bias is None else bias.data_ptr()
+        wc, wsc, to = self.codes.data_ptr(), self.scales.data_ptr(), B.stream_on(stream, dev)
         if quantised:
-            B.launch(dev, B.lib().asp_fp8_gemm, x.codes.data_ptr(), x.scales.data_ptr(), *tail, M, N,
-                     K, *out)
+            B.launch(dev, B.lib().asp_fp8_gemm, x.codes.data_ptr(), x.scales.data_ptr(), wc, wsc, M,
+                     N, K, bias, y.data_ptr(), B.DTYPES[y_dtype], ws, have, to)
         else:
-            B.launch(dev, B.lib().asp_fp8_forward, x.data_ptr(), _CODES[x.dtype], ld, M, N, K, *tail,
-                     *out)
-        _lend(stream, *made)
+            B.launch(dev, B.lib().asp_fp8_forward, x.data_ptr(), _CODES[x.dtype], ld, M, N, K, wc,
+                     wsc, bias, y.data_ptr(), B.DTYPES[y_dtype], ws, have, to)
+        if stream is not None:
+            _lend(stream, *made)
         return y
 
     def backward(self, dy, x=None, need_dx=True, need_db=None, dw_dtype="f32", workspace=None,

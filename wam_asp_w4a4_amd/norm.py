@@ -46,9 +46,12 @@ def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, s
         raise ValueError("weight, bias, scale and shift need a pre norm")
     if post == "none" and post_weight is not None:
         raise ValueError("post_weight needs a post norm")
-    for t, name in ((post_weight, "post_weight"), (weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _check_vector(t, name, C, device)
+    if post_weight is not None:
+        _check_vector(post_weight, "post_weight", C, device)
+    if weight is not None:
+        _check_vector(weight, "weight", C, device)
+    if bias is not None:
+        _check_vector(bias, "bias", C, device)
     G = 1
     if offsets is not None:
         if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32:
@@ -60,6 +63,11 @@ def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, s
     ldt = None
     for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
         if t is None:
+            continue
+        if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and G == 1 \
+                and t.numel() == C == t.shape[-1] and t.dim() <= 2 and t.is_contiguous() \
+                and t.device == device and ldt in (None, C):
+            ldt = C
             continue
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
             raise TypeError(f"{name} must be a float32 tensor")
