@@ -100,10 +100,11 @@ def test_values_without_a_code_and_extremes():
         assert torch.isfinite(y[4:]).all()
 
 
-# every kernel: few rows, 32 x 32 tiles, tiles of 64, 128 (whole and split) and 256
+# every kernel: few rows, 32 x 32 tiles, tiles of 64, 128 (whole and split) and 256 (whole, the
+# last ones in quarters or halves)
 SHAPES = [(1, 16, 1), (1, 33, 128), (5, 100, 129), (16, 4096, 1024), (16, 40, 4224), (17, 16, 640),
           (33, 65, 127), (64, 64, 8192), (100, 130, 1537), (256, 1024, 1024), (777, 515, 300),
-          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130),
+          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130), (4100, 4700, 200),
           (1000, 1003, 385), (520, 515, 33000)]
 
 

@@ -42,6 +42,7 @@ struct GemmK {
   float* part;  // [slices][M][N] partial sums when slices > 1
   int64_t lda, ldb;  // code pitches: KB * 128
   int M, N, KB, y_bf16, slices, tiles_m, tiles_n;
+  int whole, parts;  // of k_fp8_gemm_tail: the tiles computed whole, the parts of each other
 };
 
 // Bytes p .. p + n - 1 as a buffer, and the direct copy of 16 bytes a lane from it to
@@ -59,16 +60,17 @@ __device__ __forceinline__ void buffer_copy4(__amdgpu_buffer_rsrc_t r, int v, vo
 }
 
 // XCD-aware tile order.  Workgroups go to the 8 XCDs (each with its own L2) in
-// turn; each XCD takes one contiguous run of tiles, walked in bands of 4 tile
-// rows, so that the operand rows its workgroups share stay in its L2.
-__device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int total = tiles_m * tiles_n, per = total / 8, extra = total % 8;
-  const int xcd = id % 8, k = id / 8;
-  const int t = xcd * per + min(xcd, extra) + k;
+// turn; each XCD takes one contiguous run of tiles (xcd_run), walked in bands of 4 tile
+// rows (tile_at), so that the operand rows its workgroups share stay in its L2.
+__device__ __forceinline__ int xcd_run(int id, int total) {
+  const int xcd = id % 8;
+  return xcd * (total / 8) + min(xcd, total % 8) + id / 8;
+}
+__device__ __forceinline__ void tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int band = 4 * tiles_n, b = t / band, r = t % band;
   const int rows = min(4, tiles_m - 4 * b);
-  tm = 4 * b + r % rows;
-  tn = r / rows;
+  tm = __builtin_amdgcn_readfirstlane(4 * b + r % rows);
+  tn = __builtin_amdgcn_readfirstlane(r / rows);
 }
 
 // four consecutive results of one row, n .. n + 3 (bounds checked)
@@ -130,27 +132,30 @@ __device__ __forceinline__ void order() {
 // landed.  The scales go the same way (the dword of a row's four blocks,
 // for each block anew): loaded to registers, their wait would be one for every older
 // copy, since loads are counted in order.
+template <int TM, int TN>
+struct Tile {
+  static constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64, NB = 4;
+  static constexpr int STAGE = (BM + BN) * SK;
+  static constexpr int SCALES = 4 * (BM + BN);  // bytes of a block's scales
+  static constexpr int PITCH16 = 64 * TN + 16, PITCH32 = 128 * TN + 16;  // of a wave's result rows in LDS
+  static constexpr int TP = TM > 1 ? TM / 2 : 1;  // tile rows of a float32 result at a time
+  static constexpr int OUT16 = 32 * TM * PITCH16, OUT32 = 32 * TP * PITCH32;
+  static constexpr int OUT = OUT16 > OUT32 ? OUT16 : OUT32;  // a wave's result region
+  static constexpr int STAGING = NB * STAGE + NB / 2 * SCALES;
+  static constexpr int LDS = STAGING > 4 * OUT ? STAGING : 4 * OUT;
+};
+
 template <int TM, int TN, bool WIDE>
-__global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
-  constexpr int BM = 64 * TM, BN = 64 * TN, SK = 64, NB = 4;
-  constexpr int STAGE = (BM + BN) * SK;
+__device__ __forceinline__ void gemm_tile(const GemmK& g, const int64_t m0, const int64_t n0,
+                                          uint8_t* smem) {
+  using T = Tile<TM, TN>;
+  constexpr int BM = T::BM, BN = T::BN, SK = T::SK, NB = T::NB, STAGE = T::STAGE, SCALES = T::SCALES;
+  constexpr int PITCH16 = T::PITCH16, PITCH32 = T::PITCH32, TP = T::TP, OUT = T::OUT;
   constexpr int CA = BM * SK / 4096, CB = BN * SK / 4096;  // a wave's copies of A and B for a stage
   constexpr int SC = (TM + TN + 3) / 4;                    // and of 64 rows' scales for a block
-  constexpr int SCALES = 4 * (BM + BN);                    // bytes of a block's scales
-  constexpr int PITCH16 = 64 * TN + 16, PITCH32 = 128 * TN + 16;  // of a wave's result rows in LDS
-  constexpr int TP = TM > 1 ? TM / 2 : 1;                  // tile rows of a float32 result at a time
-  constexpr int OUT16 = 32 * TM * PITCH16, OUT32 = 32 * TP * PITCH32;
-  constexpr int OUT = OUT16 > OUT32 ? OUT16 : OUT32;       // a wave's result region
-  constexpr int STAGING = NB * STAGE + NB / 2 * SCALES;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[STAGING > 4 * OUT ? STAGING : 4 * OUT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave >> 1, wn = wave & 1;
-  int tm, tn;
-  tile_at(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-  tm = __builtin_amdgcn_readfirstlane(tm);
-  tn = __builtin_amdgcn_readfirstlane(tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   // the tile's last rows; rows past them re-read the last one, their results are not stored
   const int mlast = (int)min((int64_t)BM, g.M - m0) - 1, nlast = (int)min((int64_t)BN, g.N - n0) - 1;
   // this slice's blocks of K
@@ -433,6 +438,43 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   }
 }
 
+template <int TM, int TN, bool WIDE>
+__global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
+  using T = Tile<TM, TN>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
+  int tm, tn;
+  tile_at(xcd_run(blockIdx.x, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
+  gemm_tile<TM, TN, WIDE>(g, (int64_t)tm * T::BM, (int64_t)tn * T::BN, smem);
+}
+
+// 256 x 256 tiles, the last of them in parts: g.whole tiles (whole rounds of the CUs),
+// then each of the others as two of 256 x 128 or four of 128 x 128, a CU's work each.
+// 4096 x 14336 x 4096 (3.5 rounds) 248 -> 238 us, 4352 x 4352 x 4096 (1.13) 103 -> 83;
+// float32 results 421 -> 395 and 185 -> 141.
+template <bool WIDE>
+__global__ void __launch_bounds__(256, 1) k_fp8_gemm_tail(const GemmK g) {
+  using T = Tile<4, 4>;
+  static_assert(Tile<4, 2>::LDS <= T::LDS && Tile<2, 2>::LDS <= T::LDS, "one region for all");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
+  const int id = blockIdx.x;
+  int tm, tn;
+  if (id < g.whole) {
+    tile_at(xcd_run(id, g.whole), g.tiles_m, g.tiles_n, tm, tn);
+    gemm_tile<4, 4, WIDE>(g, (int64_t)tm * T::BM, (int64_t)tn * T::BN, smem);
+    return;
+  }
+  const int t = xcd_run(id - g.whole, gridDim.x - g.whole);
+  tile_at(g.whole + t / g.parts, g.tiles_m, g.tiles_n, tm, tn);
+  const int part = __builtin_amdgcn_readfirstlane(t % g.parts);
+  const int64_t m0 = (int64_t)tm * T::BM + 128 * (part >> 1);
+  const int64_t n0 = (int64_t)tn * T::BN + 128 * (part & 1);
+  if (m0 >= g.M || n0 >= g.N) return;
+  if (g.parts == 2)
+    gemm_tile<4, 2, WIDE>(g, m0, n0, smem);
+  else
+    gemm_tile<2, 2, WIDE>(g, m0, n0, smem);
+}
+
 // the slices' partial sums, added in slice order, plus bias
 __global__ void __launch_bounds__(256) k_fp8_join(const GemmK g) {
   const int64_t n4 = (g.N + 3) / 4;
@@ -476,9 +518,7 @@ __global__ void __launch_bounds__(64 * kMidWaves) k_fp8_mid(const GemmK g) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   int tm, tn;
-  tile_at(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-  tm = __builtin_amdgcn_readfirstlane(tm);
-  tn = __builtin_amdgcn_readfirstlane(tn);
+  tile_at(xcd_run(blockIdx.x, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t m0 = 32 * (int64_t)tm, n0 = 32 * (int64_t)tn;
   const int mlast = (int)min((int64_t)32, g.M - m0) - 1, nlast = (int)min((int64_t)32, g.N - n0) - 1;
   const __amdgpu_buffer_rsrc_t ra = descriptor(g.a + m0 * g.lda, (mlast + 1) * g.lda);
@@ -678,12 +718,22 @@ __global__ void __launch_bounds__(256) k_fp8_colsum(const float* __restrict__ pa
 
 constexpr int kFewRows = 16;
 
-enum Kernel { kTiles256, kTiles128, kTiles64, kMid };
+constexpr int kCUs = 256;
+
+enum Kernel { kTiles256, kTiles256Tail, kTiles128, kTiles64, kMid };
 
 struct Plan {
   Kernel kernel;
   int slices;  // of K
 };
+
+// The parts of each 256-tile left over by whole rounds of the CUs: as many as keep every
+// part on a CU of its own.
+int tail_parts(int64_t tiles) {
+  const int64_t left = tiles % kCUs;
+  if (tiles < kCUs || left == 0) return 1;
+  return left <= kCUs / 4 ? 4 : left <= kCUs / 2 ? 2 : 1;
+}
 
 // The kernel for more than kFewRows rows.  A larger tile reads fewer bytes for its
 // products: 256 x 256 tiles reach 2560 TFLOP/s at 8192^3, 128 x 128 ones (two a CU)
@@ -697,7 +747,7 @@ struct Plan {
 Plan plan(int64_t M, int64_t N, int64_t K) {
   auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   const int64_t KB = fp8_blocks(K);
-  if (tiles(256) > 128) return {kTiles256, 1};
+  if (tiles(256) > kCUs / 2) return {tail_parts(tiles(256)) > 1 ? kTiles256Tail : kTiles256, 1};
   if (tiles(128) >= 192) return {kTiles128, 1};
   for (int s = 2; s <= 16; s *= 2)
     if (KB / s >= 32 && tiles(128) * s >= 192 && tiles(128) >= 16) return {kTiles128, s};
@@ -724,6 +774,19 @@ int32_t launch_tiles(GemmK k, hipStream_t st) {
   k.tiles_m = (int)tm;
   k.tiles_n = (int)tn;
   k_fp8_gemm<TM, TN, WIDE><<<dim3((unsigned)(tm * tn), (unsigned)k.slices), 256, 0, st>>>(k);
+  return launch_status("fp8 gemm");
+}
+
+template <bool WIDE>
+int32_t launch_tail(GemmK k, hipStream_t st) {
+  k.tiles_m = (k.M + 255) / 256;
+  k.tiles_n = (k.N + 255) / 256;
+  const int64_t tiles = (int64_t)k.tiles_m * k.tiles_n;
+  if (tiles > INT32_MAX - kCUs) return fail(ASP_ERR_SHAPE, "output too large for one launch");
+  const int64_t left = tiles % kCUs;
+  k.whole = (int)(tiles - left);
+  k.parts = tail_parts(tiles);
+  k_fp8_gemm_tail<WIDE><<<dim3((unsigned)(k.whole + k.parts * left)), 256, 0, st>>>(k);
   return launch_status("fp8 gemm");
 }
 
@@ -774,6 +837,7 @@ template <bool WIDE>
 int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
   switch (p.kernel) {
     case kTiles256: return launch_tiles<4, 4, WIDE>(k, st);
+    case kTiles256Tail: return launch_tail<WIDE>(k, st);
     case kTiles128: return launch_tiles<2, 2, WIDE>(k, st);
     case kTiles64: return launch_tiles<1, 1, WIDE>(k, st);
     default: return launch_mid<WIDE>(k, st);
