@@ -161,7 +161,9 @@ def test_layer_against_the_oracle(M, N, K, dtype, ld, y_dtype):
 
 
 GRADS = [(1, 24, 16, "f32"), (130, 100, 200, "bf16"), (16, 1000, 33, "f32"), (300, 16, 130, "bf16"),
-         (257, 515, 640, "f32"), (1024, 256, 512, "bf16"), (2048, 2100, 1792, "bf16")]
+         (257, 515, 640, "f32"), (1024, 256, 512, "bf16"), (2048, 2100, 1792, "bf16"),
+         # small products of one launch: 32 x 32 tiles with 64 x 64 ones, 64 x 64 ones only
+         (300, 2000, 1300, "bf16"), (1200, 2000, 1300, "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,dtype", GRADS)

@@ -438,13 +438,18 @@ __device__ __forceinline__ void gemm_tile(const GemmK& g, const int64_t m0, cons
   }
 }
 
+// tile id of g's
+template <int TM, int TN, bool WIDE>
+__device__ __forceinline__ void gemm_tile_of(const GemmK& g, int id, uint8_t* smem) {
+  int tm, tn;
+  tile_at(xcd_run(id, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
+  gemm_tile<TM, TN, WIDE>(g, (int64_t)tm * 64 * TM, (int64_t)tn * 64 * TN, smem);
+}
+
 template <int TM, int TN, bool WIDE>
 __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const GemmK g) {
-  using T = Tile<TM, TN>;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
-  int tm, tn;
-  tile_at(xcd_run(blockIdx.x, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
-  gemm_tile<TM, TN, WIDE>(g, (int64_t)tm * T::BM, (int64_t)tn * T::BN, smem);
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Tile<TM, TN>::LDS];
+  gemm_tile_of<TM, TN, WIDE>(g, blockIdx.x, smem);
 }
 
 // 256 x 256 tiles, the last of them in parts: g.whole tiles (whole rounds of the CUs),
@@ -508,17 +513,19 @@ __global__ void __launch_bounds__(256) k_fp8_join(const GemmK g) {
 // of that row's eight.
 constexpr int kMidWaves = 4;
 
+constexpr int kMidSlot = 8192 + 256;  // B's 32 rows, A's, and their scale dwords
+constexpr int kMidLds = kMidWaves * 2 * kMidSlot;
+
 template <bool WIDE>
-__global__ void __launch_bounds__(64 * kMidWaves) k_fp8_mid(const GemmK g) {
+__device__ __forceinline__ void mid_tile(const GemmK& g, int id, uint8_t* smem) {
   constexpr int LD = 36;                     // floats of a partial tile's row
-  constexpr int SLOT = 8192 + 256;           // B's 32 rows, A's, and their scale dwords
+  constexpr int SLOT = kMidSlot;
   constexpr int OPS = 9;                     // copies of a block
   static_assert(32 * LD * 4 <= 2 * SLOT, "a partial tile fits a wave's slots");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kMidWaves * 2 * SLOT];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   int tm, tn;
-  tile_at(xcd_run(blockIdx.x, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
+  tile_at(xcd_run(id, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, tm, tn);
   const int64_t m0 = 32 * (int64_t)tm, n0 = 32 * (int64_t)tn;
   const int mlast = (int)min((int64_t)32, g.M - m0) - 1, nlast = (int)min((int64_t)32, g.N - n0) - 1;
   const __amdgpu_buffer_rsrc_t ra = descriptor(g.a + m0 * g.lda, (mlast + 1) * g.lda);
@@ -599,6 +606,12 @@ __global__ void __launch_bounds__(64 * kMidWaves) k_fp8_mid(const GemmK g) {
 #pragma unroll
   for (int w = 0; w < kMidWaves; ++w) s += *part(w, row, col);
   store4(g, m0 + row, (int)n0 + col, s, g.N % 4 == 0 && ((uintptr_t)g.y & 15) == 0);
+}
+
+template <bool WIDE>
+__global__ void __launch_bounds__(64 * kMidWaves) k_fp8_mid(const GemmK g) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kMidLds];
+  mid_tile<WIDE>(g, blockIdx.x, smem);
 }
 
 // k_fp8_few: at most 16 rows of x.  Bound by the weight's bytes, so a workgroup
@@ -697,21 +710,55 @@ __global__ void __launch_bounds__(64 * W)
 
 // column sums from the tile quantiser's partials: 16 columns a workgroup, whose 16
 // threads of a column take the row blocks in turn; the first adds them in order
-__global__ void __launch_bounds__(256) k_fp8_colsum(const float* __restrict__ part, int nrb, int N,
-                                                    float* __restrict__ out) {
-  __shared__ float lds[16][17];
-  const int col = threadIdx.x & 15, lane = threadIdx.x >> 4, n = blockIdx.x * 16 + col;
+struct ColSum {
+  const float* part;  // [nrb][N]
+  float* out;
+  int nrb, N;
+};
+__device__ __forceinline__ void column_sums(const ColSum& c, int id, float (&lds)[16][17]) {
+  const int col = threadIdx.x & 15, lane = threadIdx.x >> 4, n = id * 16 + col;
   float s = 0.0f;
-  if (n < N)
+  if (n < c.N)
 #pragma unroll 4
-    for (int r = lane; r < nrb; r += 16) s += part[(int64_t)r * N + n];
+    for (int r = lane; r < c.nrb; r += 16) s += c.part[(int64_t)r * c.N + n];
   lds[lane][col] = s;
   __syncthreads();
-  if (lane != 0 || n >= N) return;
+  if (lane != 0 || n >= c.N) return;
   s = 0.0f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) s += lds[k][col];
-  out[n] = s;
+  c.out[n] = s;
+}
+__global__ void __launch_bounds__(256) k_fp8_colsum(const ColSum c) {
+  __shared__ float lds[16][17];
+  column_sums(c, blockIdx.x, lds);
+}
+
+// k_fp8_back: what a small layer's backward computes from the quantised operands, in one
+// launch: g[0]'s tiles (count[0] workgroups), g[1]'s, then the column sums.  Each alone
+// is a few microseconds of latency on part of the CUs.
+struct BackK {
+  GemmK g[2];
+  int count[2], mid[2];
+  ColSum sums;
+};
+template <bool MID>
+__global__ void __launch_bounds__(256, 2) k_fp8_back(const BackK b) {
+  constexpr int TILE = Tile<1, 1>::LDS;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[MID && kMidLds > TILE ? kMidLds : TILE];
+  int id = blockIdx.x;
+  const int second = id >= b.count[0];
+  if (second) id -= b.count[0];
+  if (second && id >= b.count[1])
+    return column_sums(b.sums, id - b.count[1], *reinterpret_cast<float(*)[16][17]>(smem));
+  const GemmK& g = b.g[second];
+  if (MID && b.mid[second]) {
+    if (g.y_bf16) mid_tile<false>(g, id, smem);
+    else mid_tile<true>(g, id, smem);
+  } else {
+    if (g.y_bf16) gemm_tile_of<1, 1, false>(g, id, smem);
+    else gemm_tile_of<1, 1, true>(g, id, smem);
+  }
 }
 
 // ----------------------------------------------------------------- host side
@@ -858,6 +905,31 @@ int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
 }
 
 namespace {
+
+// Latency-bound products, which share a launch with others (k_fp8_back).
+bool small(const Fp8Gemm& g) {
+  const Plan p = plan(g.M, g.N, g.K);
+  return p.slices == 1 && (p.kernel == kMid || p.kernel == kTiles64);
+}
+
+// up to two small products, and column sums where c.out is given
+int32_t launch_back(int n, const Fp8Gemm* g, const ColSum& c, hipStream_t st) {
+  BackK b = {};
+  b.sums = c;
+  int64_t blocks = c.out ? (c.N + 15) / 16 : 0;
+  for (int i = 0; i < n; ++i) {
+    GemmK& k = b.g[i] = kernel_args(g[i], 1);
+    b.mid[i] = plan(g[i].M, g[i].N, g[i].K).kernel == kMid;
+    const int t = b.mid[i] ? 32 : 64;
+    k.tiles_m = (k.M + t - 1) / t;
+    k.tiles_n = (k.N + t - 1) / t;
+    b.count[i] = k.tiles_m * k.tiles_n;
+    blocks += b.count[i];
+  }
+  if (b.mid[0] || b.mid[1]) k_fp8_back<true><<<dim3((unsigned)blocks), 256, 0, st>>>(b);
+  else k_fp8_back<false><<<dim3((unsigned)blocks), 256, 0, st>>>(b);
+  return launch_status("fp8 backward");
+}
 
 int32_t check_gemm(int64_t M, int64_t N, int64_t K) {
   ASP_TRY(check_fp8_dims(M, K, "M", "K"));
@@ -1020,20 +1092,22 @@ int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const v
        base + L.dyts, db ? reinterpret_cast<float*>(base + L.sums) : nullptr, dy_dtype, 0},
       {x, M, K, ldx, nullptr, nullptr, base + L.xtc, base + L.xts, nullptr, x_dtype, 0}};
   ASP_TRY(fp8_quantize_tiles(dw ? 2 : 1, jobs, st));
+  const ColSum sums = {reinterpret_cast<const float*>(base + L.sums), db, (int)fp8_blocks(M), (int)N};
+  Fp8Gemm g[2];
+  int n = 0;
+  if (dx && M > 0)
+    g[n++] = {base + L.dyc, base + L.dys, wt_codes, wt_scales, M, K, N, nullptr,
+              dx, dx_dtype, base + L.gemm};
+  if (dw)
+    g[n++] = {base + L.dytc, base + L.dyts, base + L.xtc, base + L.xts, N, K, M, nullptr,
+              dw, dw_dtype, base + L.gemm};
+  if (n > 0 && small(g[0]) && small(g[n - 1])) return launch_back(n, g, sums, st);
   if (db) {
-    k_fp8_colsum<<<dim3((unsigned)((N + 15) / 16)), 256, 0, st>>>(
-        reinterpret_cast<const float*>(base + L.sums), (int)fp8_blocks(M), (int)N, db);
+    k_fp8_colsum<<<dim3((unsigned)((N + 15) / 16)), 256, 0, st>>>(sums);
     ASP_TRY(launch_status("fp8 column sums"));
   }
-  if (dx && M > 0) {
-    const Fp8Gemm g = {base + L.dyc, base + L.dys, wt_codes, wt_scales, M, K, N, nullptr,
-                       dx, dx_dtype, base + L.gemm};
-    ASP_TRY(fp8_gemm_impl(g, st));
-  }
-  if (!dw) return ASP_OK;
-  const Fp8Gemm g = {base + L.dytc, base + L.dyts, base + L.xtc, base + L.xts, N, K, M, nullptr,
-                     dw, dw_dtype, base + L.gemm};
-  return fp8_gemm_impl(g, st);
+  for (int i = 0; i < n; ++i) ASP_TRY(fp8_gemm_impl(g[i], st));
+  return ASP_OK;
 }
 
 }  // extern "C"
