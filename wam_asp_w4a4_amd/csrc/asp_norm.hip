@@ -543,10 +543,14 @@ int strip_rows(int64_t M, int64_t C) {
   return M > s ? (int)((M + s - 1) / s) : 1;
 }
 
-int64_t strip_count(int64_t M, int64_t C) {
-  const int64_t rows = strip_rows(M, C);
-  return (M + rows - 1) / rows;
+// The backward's: two at least where the strips' column sums, 12 bytes a column, are
+// what it waits for (a replayed call, float32: 2000 x 1024 38 -> 31 us, 4000 x 500 37 -> 31;
+// below half a million columns the second row costs more: 256 x 1024 19 against 20.5).
+int back_rows(int64_t M, int64_t C) {
+  return M * C < (1 << 19) ? strip_rows(M, C) : std::max(strip_rows(M, C), 2);
 }
+
+int64_t strips(int64_t M, int64_t rows) { return (M + rows - 1) / rows; }
 
 int32_t check_norm(int32_t dtype, int64_t M, int64_t C, int32_t post, int32_t pre, int32_t G,
                    const int32_t* offsets, int64_t ldt, float eps) {
@@ -571,7 +575,7 @@ int32_t check_vec(const float* p, const char* name) {
 
 template <typename XT>
 int32_t launch_norm(const NormArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)strip_count(a.M, a.C));
+  const dim3 grid((unsigned)strips(a.M, a.rows));
   if (a.C <= 512) k_norm_gate<XT, 64, 1><<<grid, 64, 0, st>>>(a);
   else if (a.C <= 1024) k_norm_gate<XT, 128, 1><<<grid, 128, 0, st>>>(a);
   else if (a.C <= 2048) k_norm_gate<XT, 256, 1><<<grid, 256, 0, st>>>(a);
@@ -583,7 +587,7 @@ int32_t launch_norm(const NormArgs& a, hipStream_t st) {
 
 template <typename XT, typename NT>
 int32_t launch_back(const NormArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)strip_count(a.M, a.C));
+  const dim3 grid((unsigned)strips(a.M, a.rows));
   if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1><<<grid, 64, 0, st>>>(a);
   else if (a.C <= 1024) k_norm_gate_back<XT, NT, 128, 1><<<grid, 128, 0, st>>>(a);
   else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1><<<grid, 256, 0, st>>>(a);
@@ -650,7 +654,7 @@ int32_t asp_norm_gate_backward_workspace_bytes(int64_t M, int64_t C, int32_t G, 
   if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
   if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
   // a slot for each pair of a strip and a sequence that it touches, and the sequences' sums
-  *bytes = up256((size_t)(strip_count(M, C) + G + (G > 1 ? G : 0)) * 3 * C * 4);
+  *bytes = up256((size_t)(strips(M, back_rows(M, C)) + G + (G > 1 ? G : 0)) * 3 * C * 4);
   return ASP_OK;
 }
 
@@ -703,7 +707,7 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   a.alpha = alpha; a.eps = eps; a.M = (int)M; a.C = (int)C; a.G = G; a.post = post; a.pre = pre;
   a.dh = dh; a.dn = dn; a.dx = dx; a.dy = dy; a.lddh = lddh; a.lddn = lddn; a.lddx = lddx;
   a.lddy = lddy; a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  a.rows = strip_rows(M, C);
+  a.rows = back_rows(M, C);
   if (M > 0) {
     const bool n16 = dn_dtype == ASP_BF16;
     if (dtype == ASP_BF16)
@@ -717,7 +721,7 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   k.post_w = post_w; k.gate = gate; k.pre_w = pre_w; k.pre_b = pre_b; k.scale = scale;
   k.offsets = offsets; k.d_post_w = d_post_w; k.d_gate = d_gate; k.d_pre_w = d_pre_w;
   k.d_pre_b = d_pre_b; k.d_scale = d_scale; k.d_shift = d_shift; k.ldt = ldt; k.ldd = ldd;
-  k.M = (int)M; k.C = (int)C; k.G = G; k.rows = a.rows; k.slots = strip_count(M, C) + G;
+  k.M = (int)M; k.C = (int)C; k.G = G; k.rows = a.rows; k.slots = strips(M, a.rows) + G;
   k_norm_sums<<<dim3((unsigned)((C + 15) / 16), (unsigned)G), 256, 0, st>>>(k);
   if (G > 1 && (d_pre_w || d_pre_b || d_post_w))
     k_norm_weight_sums<<<dim3((unsigned)((C + 63) / 64)), 64, 0, st>>>(k);
