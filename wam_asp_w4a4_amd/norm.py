@@ -180,8 +180,13 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         made.append(torch.empty(shape, dtype=dtype, device=dev))
         return made[-1]
 
-    def like(t):
-        return None if t is None else new(t.shape)
+    def like(*inputs):
+        # one allocation for those of one shape
+        given = [t for t in inputs if t is not None]
+        if any(t.shape != given[0].shape for t in given):
+            return [None if t is None else new(t.shape) for t in inputs]
+        rows = iter(new((len(given), *given[0].shape)).unbind(0) if given else ())
+        return [None if t is None else next(rows) for t in inputs]
 
     if dx is None:
         dx = new((M, C), h.dtype)
@@ -194,10 +199,10 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         dy = new((M, C), h.dtype)
     else:
         lddy = _check_rows(dy, "dy", M, C, dev, same)
-    g = NormGrads(dx, dy, like(post_weight), like(gate), like(weight), like(bias), like(scale),
-                  like(shift))
+    d_post_weight, d_weight, d_bias = like(post_weight, weight, bias)
+    d_gate, d_scale, d_shift = like(gate, scale, shift)
     need = 0
-    if any(t is not None for t in g[2:]):
+    if not (post_weight is weight is bias is gate is scale is shift is None):
         need = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
         if workspace is None:
             workspace = new((need,), torch.uint8)
@@ -208,10 +213,10 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
              B.ASP_F32 if dn is None else _CODES[dn.dtype], h.data_ptr(), ldh, at(y), ldy,
              _CODES[h.dtype], M, C, alpha, kpost, at(post_weight), at(gate), kpre, at(weight),
              at(bias), at(scale), ldt, G, at(offsets), eps, at(dx), lddx, at(dy), lddy,
-             at(g.post_weight), at(g.gate), at(g.weight), at(g.bias), at(g.scale), at(g.shift), C,
+             at(d_post_weight), at(d_gate), at(d_weight), at(d_bias), at(d_scale), at(d_shift), C,
              at(workspace), 0 if workspace is None else workspace.numel(), B.stream_on(stream, dev))
     _lend(stream, *made)
-    return g
+    return NormGrads(dx, dy, d_post_weight, d_gate, d_weight, d_bias, d_scale, d_shift)
 
 
 class _GatedNorm(torch.autograd.Function):
