@@ -104,7 +104,7 @@ def test_values_without_a_code_and_extremes():
 # last ones in quarters or halves)
 SHAPES = [(1, 16, 1), (1, 33, 128), (5, 100, 129), (16, 4096, 1024), (16, 40, 4224), (17, 16, 640),
           (33, 65, 127), (64, 64, 8192), (100, 130, 1537), (256, 1024, 1024), (777, 515, 300),
-          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130), (4100, 4700, 200),
+          (1920, 1793, 256), (3500, 3330, 640), (4100, 3900, 130), (4100, 4700, 200), (1500, 3500, 2050),
           (1000, 1003, 385), (520, 515, 33000)]
 
 

@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(256, TM * TN > 4 ? 1 : 2) k_fp8_gemm(const Gem
   gemm_tile_of<TM, TN, WIDE>(g, blockIdx.x, smem);
 }
 
-// 256 x 256 tiles, the last of them in parts: g.whole tiles (whole rounds of the CUs),
-// then each of the others as two of 256 x 128 or four of 128 x 128, a CU's work each.
+// 256 x 256 tiles, the last of them in parts: g.whole tiles (whole rounds of the CUs, or
+// none), then each of the others as two of 256 x 128 or four of 128 x 128, a CU's work each.
 // 4096 x 14336 x 4096 (3.5 rounds) 248 -> 238 us, 4352 x 4352 x 4096 (1.13) 103 -> 83;
 // float32 results 421 -> 395 and 185 -> 141.
 template <bool WIDE>
@@ -774,27 +774,31 @@ struct Plan {
   int slices;  // of K
 };
 
-// The parts of each 256-tile left over by whole rounds of the CUs: as many as keep every
-// part on a CU of its own.
+// The parts of each 256-tile left over by whole rounds of the CUs (all tiles, if there is
+// no whole round): as many as keep every part on a CU of its own.
 int tail_parts(int64_t tiles) {
   const int64_t left = tiles % kCUs;
-  if (tiles < kCUs || left == 0) return 1;
+  if (left == 0) return 1;
   return left <= kCUs / 4 ? 4 : left <= kCUs / 2 ? 2 : 1;
 }
 
 // The kernel for more than kFewRows rows.  A larger tile reads fewer bytes for its
 // products: 256 x 256 tiles reach 2560 TFLOP/s at 8192^3, 128 x 128 ones (two a CU)
 // 1780.  But a tile is one CU's work: beyond half a round of 256-tiles (128) they are
-// faster (2048 x 4096 x 4096, exactly 128: 59 against 43 us with 512 tiles of 128),
-// below that 128-tiles while they fill three quarters of the CUs.  A long K over
-// fewer of them is split into slices whose float32 partial sums a second kernel adds.
-// What is left is bound by latency: up to 768 tiles of 32 x 32 are k_fp8_mid's (256 x
-// 1024 x 4096: 6.6 us, against 11.6 with 64-tiles in four slices), more are 64-tiles
-// (256 x 4096 x 1024, 1024 tiles of 32: 6.0 us against 7.6).
-Plan plan(int64_t M, int64_t N, int64_t K) {
+// faster.  A quarter to half a round is one round of their 256 x 128 halves, faster than
+// 128-tiles where 8-bit products last (2048 x 4096 x 4096 47 -> 42 us, 700 x 6000 x
+// 4096 39 -> 32; even at K = 1024, and float32 results at any: 65 against 67).  Below that
+// 128-tiles while they fill three quarters of the CUs.  A long K over fewer of them
+// is split into slices whose float32 partial sums a second kernel adds.  What is left
+// is bound by latency: up to 768 tiles of 32 x 32 are k_fp8_mid's (256 x 1024 x 4096:
+// 6.6 us, against 11.6 with 64-tiles in four slices), more are 64-tiles (256 x 4096 x
+// 1024, 1024 tiles of 32: 6.0 us against 7.6).  `wide` never changes the slices.
+Plan plan(int64_t M, int64_t N, int64_t K, bool wide) {
   auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   const int64_t KB = fp8_blocks(K);
-  if (tiles(256) > kCUs / 2) return {tail_parts(tiles(256)) > 1 ? kTiles256Tail : kTiles256, 1};
+  if (tiles(256) > kCUs / 2 ||
+      (tiles(256) > kCUs / 4 && tiles(128) > kCUs && KB >= 16 && !wide))
+    return {tail_parts(tiles(256)) > 1 ? kTiles256Tail : kTiles256, 1};
   if (tiles(128) >= 192) return {kTiles128, 1};
   for (int s = 2; s <= 16; s *= 2)
     if (KB / s >= 32 && tiles(128) * s >= 192 && tiles(128) >= 16) return {kTiles128, s};
@@ -867,7 +871,7 @@ bool fp8_fuses(int64_t M) { return M <= kFewRows; }
 
 size_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
   if (M <= kFewRows) return 0;
-  const Plan p = plan(M, N, K);
+  const Plan p = plan(M, N, K, false);
   return p.slices > 1 ? up256((size_t)p.slices * M * N * 4) : 0;
 }
 
@@ -895,7 +899,7 @@ int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
 int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
   if (g.M <= kFewRows)
     return launch_few(kernel_args(g, 1), g.a, 0, g.K, st);
-  const Plan p = plan(g.M, g.N, g.K);
+  const Plan p = plan(g.M, g.N, g.K, g.y_dtype != ASP_BF16);
   const GemmK k = kernel_args(g, p.slices);
   ASP_TRY(k.y_bf16 ? launch_plan<false>(p, k, st) : launch_plan<true>(p, k, st));
   if (p.slices == 1) return ASP_OK;
@@ -908,7 +912,7 @@ namespace {
 
 // Latency-bound products, which share a launch with others (k_fp8_back).
 bool small(const Fp8Gemm& g) {
-  const Plan p = plan(g.M, g.N, g.K);
+  const Plan p = plan(g.M, g.N, g.K, g.y_dtype != ASP_BF16);
   return p.slices == 1 && (p.kernel == kMid || p.kernel == kTiles64);
 }
 
@@ -919,7 +923,7 @@ int32_t launch_back(int n, const Fp8Gemm* g, const ColSum& c, hipStream_t st) {
   int64_t blocks = c.out ? (c.N + 15) / 16 : 0;
   for (int i = 0; i < n; ++i) {
     GemmK& k = b.g[i] = kernel_args(g[i], 1);
-    b.mid[i] = plan(g[i].M, g[i].N, g[i].K).kernel == kMid;
+    b.mid[i] = plan(g[i].M, g[i].N, g[i].K, !k.y_bf16).kernel == kMid;
     const int t = b.mid[i] ? 32 : 64;
     k.tiles_m = (k.M + t - 1) / t;
     k.tiles_n = (k.N + t - 1) / t;
