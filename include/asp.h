@@ -509,7 +509,10 @@ int32_t asp_svdq_forward(const void* x, int32_t x_dtype, int64_t M, int64_t K, i
  *     outputs are contiguous.  Codes and scales are 16-byte aligned;
  *   - inputs need not be finite: a NaN or infinity makes NaN of the results
  *     that contract over it, and of no others;
- *   - results are the same bits on every call with the same arguments.
+ *   - results are the same bits on every call with the same arguments;
+ *   - outputs overlap no input (but where it says so) and no other output, and a
+ *     workspace belongs to one call in flight: two streams, or two captured graphs
+ *     that may replay at once, need one each.
  *
  * asp_fp8_sizes: bytes of the codes and scales of a rows x cols matrix (host).
  * asp_fp8_quantize: in (device, rows x cols) -> codes, scales, blocks along
@@ -600,8 +603,9 @@ int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const v
  *              stride ldt, or NULL (ones, zeros, zeros)
  *   offsets    device int32, G + 1 entries, not decreasing: sequence g has the
  *              rows offsets[g] .. offsets[g + 1] - 1 (it may be empty).  Rows
- *              before the first and behind the last sequence count for
- *              nothing and are not written.  NULL: one sequence of all rows (G = 1)
+ *              before the first and behind the last sequence count for nothing;
+ *              they are zeros in h where `zero` has bit 0 set and in n where it
+ *              has bit 1, else not written.  NULL: one sequence of all rows (G = 1)
  *   C 1..16384, G 1..65535, eps in [0, 1]
  */
 #define ASP_E4M3 2 /* n_dtype: the 8-bit format */
@@ -613,14 +617,16 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
                       const float* gate, int32_t pre, const float* pre_w, const float* pre_b,
                       const float* scale, const float* shift, int64_t ldt, int32_t G,
                       const int32_t* offsets, float eps, void* h, int64_t ldh, void* n,
-                      int32_t n_dtype, int64_t ldn, uint8_t* n_scales, void* stream);
+                      int32_t n_dtype, int64_t ldn, uint8_t* n_scales, int32_t zero,
+                      void* stream);
 
 /*
  * Its gradients, from dh (of h as the residual stream goes on; NULL: zeros) and
  * dn (of n, float32 or bf16; the 8-bit format counts as the identity).  h is the
  * forward's, read where there is a pre norm; the statistics are computed anew.
  *   dx, dy     device out, M x C of `dtype`, or NULL; rows of no sequence are
- *              not written
+ *              zeros in dx where `zero` has bit 0 set and in dy where it has
+ *              bit 1, else not written
  *   d_post_w, d_pre_w, d_pre_b, d_gate, d_scale, d_shift   float32 out or NULL;
  *              the tables' with the row stride ldd.  An empty sequence's are 0
  *   workspace  device, asp_norm_gate_backward_workspace_bytes bytes, 256-byte
@@ -634,9 +640,9 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
                                int32_t post, const float* post_w, const float* gate, int32_t pre,
                                const float* pre_w, const float* pre_b, const float* scale,
                                int64_t ldt, int32_t G, const int32_t* offsets, float eps, void* dx,
-                               int64_t lddx, void* dy, int64_t lddy, float* d_post_w,
-                               float* d_gate, float* d_pre_w, float* d_pre_b, float* d_scale,
-                               float* d_shift, int64_t ldd, void* workspace,
+                               int64_t lddx, void* dy, int64_t lddy, int32_t zero,
+                               float* d_post_w, float* d_gate, float* d_pre_w, float* d_pre_b,
+                               float* d_scale, float* d_shift, int64_t ldd, void* workspace,
                                size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

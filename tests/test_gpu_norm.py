@@ -350,3 +350,55 @@ def test_module_trains():
     assert torch.equal(x.grad.view(10, 160), g.dx) and torch.equal(y.grad.view(10, 160), g.dy)
     assert torch.equal(gate.grad, g.gate) and torch.equal(m.weight.grad, g.weight)
     assert torch.equal(m.bias.grad, g.bias) and torch.equal(m.post_weight.grad, g.post_weight)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,C,offsets", [(9, 40, [2, 2, 5]), (40, 200, [0, 11, 33]), (7, 1100, [7, 7, 7]),
+                                         (5000, 130, [700, 1300, 4200]), (6, 8300, [1, 4, 5])])
+def test_rows_of_no_sequence_are_zeros_in_tensors_made_here(M, C, offsets, dtype):
+    print(f"zeros {M}x{C} {dtype} {offsets}", flush=True)
+    c = Case(M, C, dtype, "rms", "layer", True, offsets)
+    dead = torch.from_numpy(~c.live).to(DEV)
+    for out in ("f32", "bf16", "fp8"):
+        trash = [torch.full((M, C), float("nan"), device=DEV) for _ in range(4)]
+        del trash                                            # what the allocator hands out next
+        h, n = gated_norm(c.x, c.y, out=out, **c.kw)
+        if out == "fp8":
+            assert (n.scales[:, dead] == 127).all() and not n.codes[dead].any()
+            n = n.dequantize()
+        assert not h[dead].any() and not n[dead].any()
+        given = torch.full((M, C), 5.0, dtype=c.t, device=DEV)
+        assert gated_norm(c.x, c.y, h=given, **c.kw)[0] is given
+        assert (given[dead] == 5).all() and torch.equal(given[~dead], h[~dead])
+    g = gated_norm_backward(c.dh, c.dn, h, c.y, **c.kw)
+    assert not g.dx[dead].any() and not g.dy[dead].any()
+    mine = torch.full((M, C), 5.0, dtype=c.t, device=DEV)
+    assert torch.equal(gated_norm_backward(c.dh, c.dn, h, c.y, dy=mine, **c.kw).dx, g.dx)
+    assert (mine[dead] == 5).all() and torch.equal(mine[~dead], g.dy[~dead])
+
+
+def test_module_takes_padded_broadcast_and_strided_inputs():
+    """A packed batch with padding behind it, the stream broadcast, the tables of
+    different strides: the gradients of the same values laid out plainly."""
+    torch.manual_seed(3)
+    m = GatedNorm(96, post="rms", pre="layer", device=DEV)
+    offsets = torch.tensor([0, 7, 20], dtype=torch.int32, device=DEV)
+    x = torch.randn(1, 96, device=DEV, requires_grad=True)
+    y = torch.randn(96, 24, device=DEV, requires_grad=True)
+    gate = torch.randn(96, device=DEV, requires_grad=True)
+    scale = torch.randn(2, 192, device=DEV, requires_grad=True)
+    dh, dn = torch.randn(2, 24, 96, device=DEV)
+    h, n = m(x.expand(24, 96), y.t(), gate.expand(2, 96), scale[:, ::2], offsets=offsets)
+    got = torch.autograd.grad((h, n), (x, y, gate, scale, *m.parameters()), (dh, dn))
+    flat = [t.detach().contiguous() for t in (x.expand(24, 96), y.t(), gate.expand(2, 96), scale[:, ::2])]
+    want = gated_norm_backward(dh, dn, h.detach(), flat[1], post="rms", post_weight=m.post_weight.detach(),
+                               gate=flat[2], weight=m.weight.detach(), bias=m.bias.detach(), scale=flat[3],
+                               pre="layer", offsets=offsets)
+    assert not h[20:].any() and not n[20:].any()
+    # sums of 24 and 2 rows by torch: its own order
+    assert torch.allclose(got[0], want.dx.sum(0, keepdim=True), rtol=1e-5, atol=1e-5)
+    assert torch.equal(got[1], want.dy.t()) and not got[1][:, 20:].any()
+    assert torch.allclose(got[2], want.gate.sum(0), rtol=1e-5, atol=1e-5)
+    assert torch.equal(got[3][:, ::2], want.scale) and not got[3][:, 1::2].any()
+    for a, b in zip(got[4:], (want.post_weight, want.weight, want.bias)):
+        assert torch.equal(a, b)

@@ -32,6 +32,7 @@ struct NormArgs {
   int64_t ldx, ldy, ldh, ldn, ldt;
   float alpha, eps;
   int M, C, G, post, pre, n_dtype, rows;  // rows: of a strip
+  int zero;  // bits: the first, the second output's rows of no sequence become zeros
   // backward
   const void *dh, *dn;
   void *dx, *dy;
@@ -147,6 +148,17 @@ __device__ __forceinline__ void store8(void* p, int64_t row, uint32_t c, bool bf
   }
 }
 
+// a row of no sequence becomes zeros
+template <int E, int T>
+__device__ __forceinline__ void zero_row(void* p, int64_t row, bool bf16, int C, int t) {
+  const float v[8] = {};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = (e * T + t) * 8;
+    store8(p, row, c, bf16, C - c, v);
+  }
+}
+
 // f(e, k) for each of a thread's columns
 template <int E, typename F>
 __device__ __forceinline__ void each(F&& f) {
@@ -199,15 +211,15 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
     row_load<XT, E, T>(a.x, row, a.ldx, a.C, t, nx);
     if (a.y) row_load<XT, E, T>(a.y, row, a.ldy, a.C, t, ny);
   };
-  fetch(r0);
-  int64_t begin = 0, end = 0;
-  for (int64_t row = r0; row < r1; ++row) {
-    if (row == r0 || row >= end) {
+  const int64_t first = a.offsets ? max(r0, (int64_t)a.offsets[0]) : r0;
+  if (first < r1) fetch(first);
+  int64_t row = first, end = 0;
+  for (; row < r1; ++row) {
+    if (row == first || row >= end) {
       int g = 0;
       if (a.offsets) {
         g = sequence_of(a.offsets, a.G, (int)row);
         if (g >= a.G) break;  // behind the last sequence
-        begin = a.offsets[g];
         end = a.offsets[g + 1];
       } else {
         end = a.M;
@@ -233,7 +245,6 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
       unpack(ny[e], p[e]);
     }
     if (row + 1 < r1) fetch(row + 1);
-    if (row < begin) continue;  // in front of the first sequence
     if (a.post != ASP_NORM_NONE) normalise<E, T>(p, a.post, a.C, a.eps, t, lds, slot);
     each<E>([&](int e, int k) {
       v[e][k] = a.y ? __builtin_fmaf(p[e][k], gp[e][k], a.alpha * v[e][k]) : a.alpha * v[e][k];
@@ -282,6 +293,24 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
       if ((t & 15) == 0 && c < (pitch + 511) / 512 * 512)
         a.n_scales[((int64_t)(c >> 9) * a.M + row) * 4 + ((c >> 7) & 3)] =
             (uint8_t)(c < pitch ? s : kFp8PadScale);
+    }
+  }
+  if (!a.zero) return;
+  // the strip's rows in front of the first sequence, then those behind the last
+  for (int64_t z = r0 < first ? r0 : row; z < r1; z = z + 1 == first ? max(row, first) : z + 1) {
+    if (a.zero & 1) zero_row<E, T>(a.h, z * a.ldh, sizeof(XT) == 2, a.C, t);
+    if (!(a.zero & 2)) continue;
+    if (a.n_dtype != ASP_E4M3) {
+      zero_row<E, T>(a.n, z * a.ldn, a.n_dtype == ASP_BF16, a.C, t);
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = (e * T + t) * 8;
+      if (c < pitch)
+        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(a.n) + z * pitch + c) = u32x2_t{0u, 0u};
+      if ((t & 15) == 0 && c < (pitch + 511) / 512 * 512)
+        a.n_scales[((int64_t)(c >> 9) * a.M + z) * 4 + ((c >> 7) & 3)] = (uint8_t)kFp8PadScale;
     }
   }
 }
@@ -336,11 +365,13 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
       row_load<NT, E, T>(a.dn, row, a.lddn, a.C, t, rn);
     }
   };
-  if constexpr (kAhead) fetch(r0);
+  const int64_t first = a.offsets ? max(r0, (int64_t)a.offsets[0]) : r0;
+  if constexpr (kAhead)
+    if (first < r1) fetch(first);
   int g = -1;
-  int64_t begin = 0, end = 0;
-  for (int64_t row = r0; row < r1; ++row) {
-    if (row == r0 || row >= end) {
+  int64_t row = first, end = 0;
+  for (; row < r1; ++row) {
+    if (row == first || row >= end) {
       if (g >= 0 && a.part) flush(g);
       g = 0;
       if (a.offsets) {
@@ -349,7 +380,6 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
           g = -1;
           break;
         }
-        begin = a.offsets[g];
         end = a.offsets[g + 1];
       } else {
         end = a.M;
@@ -375,7 +405,6 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
       unpack(rn[e], n[e]);
     }
     if (kAhead && row + 1 < r1) fetch(row + 1);
-    if (row < begin) continue;
     if (prel || postl) {
       float s[2] = {0.0f, 0.0f};
       each<E>([&](int e, int k) {
@@ -444,6 +473,11 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
     }
   }
   if (g >= 0 && a.part) flush(g);
+  if (!a.zero) return;
+  for (int64_t z = r0 < first ? r0 : row; z < r1; z = z + 1 == first ? max(row, first) : z + 1) {
+    if (a.zero & 1) zero_row<E, T>(a.dx, z * a.lddx, sizeof(XT) == 2, a.C, t);
+    if (a.zero & 2) zero_row<E, T>(a.dy, z * a.lddy, sizeof(XT) == 2, a.C, t);
+  }
 }
 
 struct SumArgs {
@@ -609,7 +643,8 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
                       const float* gate, int32_t pre, const float* pre_w, const float* pre_b,
                       const float* scale, const float* shift, int64_t ldt, int32_t G,
                       const int32_t* offsets, float eps, void* h, int64_t ldh, void* n,
-                      int32_t n_dtype, int64_t ldn, uint8_t* n_scales, void* stream) {
+                      int32_t n_dtype, int64_t ldn, uint8_t* n_scales, int32_t zero,
+                      void* stream) {
   clear_error();
   ASP_TRY(check_norm(dtype, M, C, post, pre, G, offsets, ldt, eps));
   if (!y && (post != ASP_NORM_NONE || gate))
@@ -618,6 +653,8 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
     return fail(ASP_ERR_ARG, "pre norm arguments without a pre norm");
   if (pre == ASP_NORM_NONE && !h) return fail(ASP_ERR_ARG, "neither h nor n is asked for");
   if (post == ASP_NORM_NONE && post_w) return fail(ASP_ERR_ARG, "post_w without a post norm");
+  if (zero < 0 || zero > 3 || (M > 0 && ((zero & 1 && !h) || (zero & 2 && !n))))
+    return fail(ASP_ERR_ARG, "zero=%d", zero);
   if (n_dtype != ASP_F32 && n_dtype != ASP_BF16 && n_dtype != ASP_E4M3)
     return fail(ASP_ERR_ARG, "n_dtype=%d", n_dtype);
   if (M == 0) return ASP_OK;
@@ -644,6 +681,7 @@ int32_t asp_norm_gate(const void* x, int64_t ldx, const void* y, int64_t ldy, in
   a.ldx = ldx; a.ldy = ldy; a.ldh = ldh; a.ldn = ldn; a.ldt = ldt; a.alpha = alpha; a.eps = eps;
   a.M = (int)M; a.C = (int)C; a.G = G; a.post = post; a.pre = pre; a.n_dtype = n_dtype;
   a.rows = strip_rows(M, C);
+  a.zero = zero;
   const hipStream_t st = (hipStream_t)stream;
   return dtype == ASP_BF16 ? launch_norm<uint16_t>(a, st) : launch_norm<float>(a, st);
 }
@@ -664,9 +702,9 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
                                int32_t post, const float* post_w, const float* gate, int32_t pre,
                                const float* pre_w, const float* pre_b, const float* scale,
                                int64_t ldt, int32_t G, const int32_t* offsets, float eps, void* dx,
-                               int64_t lddx, void* dy, int64_t lddy, float* d_post_w,
-                               float* d_gate, float* d_pre_w, float* d_pre_b, float* d_scale,
-                               float* d_shift, int64_t ldd, void* workspace,
+                               int64_t lddx, void* dy, int64_t lddy, int32_t zero,
+                               float* d_post_w, float* d_gate, float* d_pre_w, float* d_pre_b,
+                               float* d_scale, float* d_shift, int64_t ldd, void* workspace,
                                size_t workspace_bytes, void* stream) {
   clear_error();
   ASP_TRY(check_norm(dtype, M, C, post, pre, G, offsets, ldt, eps));
@@ -680,6 +718,8 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
     return fail(ASP_ERR_ARG, "pre norm arguments without a pre norm");
   if (ldd < (G > 1 ? C : 0) || ldd > INT32_MAX)
     return fail(ASP_ERR_SHAPE, "table gradient stride %lld", (long long)ldd);
+  if (zero < 0 || zero > 3 || (M > 0 && ((zero & 1 && !dx) || (zero & 2 && !dy))))
+    return fail(ASP_ERR_ARG, "zero=%d", zero);
   const bool sums = d_post_w || d_gate || d_pre_w || d_pre_b || d_scale || d_shift;
   if (!sums && !dx && !dy) return ASP_OK;
   if (M > 0) {
@@ -708,6 +748,7 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
   a.dh = dh; a.dn = dn; a.dx = dx; a.dy = dy; a.lddh = lddh; a.lddn = lddn; a.lddx = lddx;
   a.lddy = lddy; a.part = sums ? static_cast<float*>(workspace) : nullptr;
   a.rows = back_rows(M, C);
+  a.zero = zero;
   if (M > 0) {
     const bool n16 = dn_dtype == ASP_BF16;
     if (dtype == ASP_BF16)

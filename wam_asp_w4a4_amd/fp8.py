@@ -44,6 +44,13 @@ def _stride(t):
     return t.shape[1] if t.shape[0] <= 1 else t.stride(0)
 
 
+def _row_major(t):
+    """t itself, or a copy where its rows overlap (a broadcast) or are not contiguous."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1 or t.dim() == 2 and _stride(t) < t.shape[1]:
+        return t.contiguous()
+    return t
+
+
 def _check_rows(t, name, rows, cols, device, dtypes=_CODES):
     """t must be a (rows, cols) matrix with contiguous rows that do not overlap (rows
     None: any number).  Returns its row stride."""

@@ -18,7 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import binding as B
-from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture
+from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture, _row_major
 from .layer import _Y_DTYPES, _check_ws
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
@@ -90,7 +90,8 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     post, pre: 'none', 'rms' or 'layer' (pre 'none': n is None).  post_weight, weight,
     bias: C float32.  gate, scale, shift: (G, C) float32 (C for one sequence).
     offsets: G + 1 int32, the packed sequences' first rows and the end of the last;
-    rows of no sequence are left as they are.  out: 'f32', 'bf16' (None: x's type)
+    rows of no sequence are left as they are in h and n where given, and are zeros in
+    tensors made here.  out: 'f32', 'bf16' (None: x's type)
     or 'fp8' for an ``Fp8Tensor``.  h, n: tensors to write (h may be x or y); without
     y and with alpha 1, h is x itself and not written unless given."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
@@ -102,7 +103,7 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         ldy = _check_rows(y, "y", M, C, dev, same)
     post, pre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
                               scale, shift, offsets)
-    made = []
+    made, zero = [], 0   # bits of the outputs made here: h, n
     write, ldh = h, C
     if h is not None:
         ldh = _check_rows(h, "h", M, C, dev, same)
@@ -111,6 +112,7 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     else:
         write = h = torch.empty((M, C), dtype=x.dtype, device=dev)
         made.append(h)
+        zero = 1
     scales = None
     if not pre:
         if n is not None or out is not None:
@@ -122,6 +124,7 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         if n is None:
             n = Fp8Tensor.empty(M, C, dev)
             made += [n.codes, n.scales]
+            zero |= 2
         else:
             if not isinstance(n, Fp8Tensor):
                 raise TypeError("out 'fp8' needs an Fp8Tensor n")
@@ -136,13 +139,14 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         if n is None:
             n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
             made.append(n)
+            zero |= 2
         else:
             ldn = _check_rows(n, "n", M, C, dev, _CODES if out is None else (_Y_DTYPES[out],))
         values, code = n, _CODES[n.dtype]
     at = B._at
     B.launch(dev, B.lib().asp_norm_gate, x.data_ptr(), ldx, at(y), ldy, _CODES[x.dtype], M, C, alpha,
              post, at(post_weight), at(gate), pre, at(weight), at(bias), at(scale), at(shift), ldt, G,
-             at(offsets), eps, at(write), ldh, at(values), code, ldn, at(scales),
+             at(offsets), eps, at(write), ldh, at(values), code, ldn, at(scales), zero,
              B.stream_on(stream, dev))
     _lend(stream, *made)
     return h, n
@@ -154,7 +158,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     """Gradients of ``gated_norm`` from dh (of h as it goes on; None: zeros) and dn (of
     n, float32 or bf16; None without a pre norm).  h: the forward's; the options are
     the forward's.  dx, dy: tensors to write (rows of no sequence are left as they
-    are).  Every given input of the forward has a gradient in the result, in its shape
+    are; they are zeros in tensors made here).  Every given input of the forward has a gradient in the result, in its shape
     (float32 but for dx and dy, which have the stream's type)."""
     if not isinstance(h, torch.Tensor) or h.dim() != 2:
         raise ValueError("h must be a 2-D torch tensor")
@@ -174,7 +178,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         lddn = _check_rows(dn, "dn", M, C, dev)
     if dh is None and dn is None:
         raise ValueError("neither dh nor dn is given")
-    made = []
+    made, zero = [], 0   # bits of the outputs made here: dx, dy
 
     def new(shape, dtype=torch.float32):
         made.append(torch.empty(shape, dtype=dtype, device=dev))
@@ -190,6 +194,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
 
     if dx is None:
         dx = new((M, C), h.dtype)
+        zero = 1
     else:
         lddx = _check_rows(dx, "dx", M, C, dev, same)
     if y is None:
@@ -197,6 +202,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
             raise ValueError("dy without y")
     elif dy is None:
         dy = new((M, C), h.dtype)
+        zero |= 2
     else:
         lddy = _check_rows(dy, "dy", M, C, dev, same)
     d_post_weight, d_weight, d_bias = like(post_weight, weight, bias)
@@ -212,7 +218,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     B.launch(dev, B.lib().asp_norm_gate_backward, at(dh), lddh, at(dn), lddn,
              B.ASP_F32 if dn is None else _CODES[dn.dtype], h.data_ptr(), ldh, at(y), ldy,
              _CODES[h.dtype], M, C, alpha, kpost, at(post_weight), at(gate), kpre, at(weight),
-             at(bias), at(scale), ldt, G, at(offsets), eps, at(dx), lddx, at(dy), lddy,
+             at(bias), at(scale), ldt, G, at(offsets), eps, at(dx), lddx, at(dy), lddy, zero,
              at(d_post_weight), at(d_gate), at(d_weight), at(d_bias), at(d_scale), at(d_shift), C,
              at(workspace), 0 if workspace is None else workspace.numel(), B.stream_on(stream, dev))
     _lend(stream, *made)
@@ -224,9 +230,12 @@ class _GatedNorm(torch.autograd.Function):
     def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, options):
         given = dict(post_weight=post_weight, gate=gate, weight=weight, bias=bias, scale=scale,
                      shift=shift)
-        # h is always written: a stream returned as it came would share its version
-        h, n = gated_norm(x, y, h=torch.empty_like(x, memory_format=torch.contiguous_format),
-                          **given, **options)
+        h = None
+        if y is None and options["alpha"] == 1.0:
+            # written all the same: a stream returned as it came would share its version
+            make = torch.empty if options["offsets"] is None else torch.zeros
+            h = make(x.shape, dtype=x.dtype, device=x.device)
+        h, n = gated_norm(x, y, h=h, **given, **options)
         ctx.save_for_backward(h, y, *given.values())
         ctx.options = options
         return h, n
@@ -247,7 +256,8 @@ class GatedNorm(torch.nn.Module):
     """``gated_norm`` with its weights as parameters, differentiable in every input.
 
     x, y: (..., C); gate, scale, shift: (G, C) or (C); returns (h, n) of x's shape
-    (n None for pre 'none').  Under a HIP graph capture, gradients are refused: capture
+    (n None for pre 'none'; rows of no sequence are zeros; without gradients, y and a
+    factor alpha, h is x itself).  Under a HIP graph capture, gradients are refused: capture
     ``gated_norm`` and ``gated_norm_backward``, which keep no graph of their own."""
 
     def __init__(self, channels, post="none", pre="rms", alpha=1.0, eps=1e-6, device=None):
@@ -268,7 +278,10 @@ class GatedNorm(torch.nn.Module):
             raise ValueError(f"x has {x.shape[-1]} channels, the norm {self.channels}")
         if y is None and self.post != "none":
             raise ValueError("a post norm needs y")
-        flat = [None if t is None else t.reshape(-1, self.channels) for t in (x, y)]
+        flat = [None if t is None else _row_major(t.reshape(-1, self.channels)) for t in (x, y)]
+        tables = [t for t in (gate, scale, shift) if t is not None]
+        if len({(t.dim(), t.stride()) for t in tables}) > 1 or any(_row_major(t) is not t for t in tables):
+            gate, scale, shift = (None if t is None else t.contiguous() for t in (gate, scale, shift))
         options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps,
                        offsets=offsets)
         tensors = (self.post_weight, gate, self.weight, self.bias, scale, shift)
