@@ -55,6 +55,7 @@ def test_c_calls_validate_before_any_launch():
     assert q(ld=99) == 2 and q(rows=-1) == 2 and q(cols=0) == 2
     assert q(x=FAKE + 2) == 3 and q(c=FAKE + 8) == 3 and q(s=FAKE + 4) == 3
     assert q(rows=0, x=None, c=None, s=None) == 0
+    assert q(rows=1 << 27, cols=4096, ld=4096) == 2        # 2^28 workgroups: no launch takes them
     t = lambda **o: _status("asp_fp8_quantize_t", FAKE, 1, o.get("rows", 4), 100, 100, o.get("c", FAKE), FAKE, None)
     assert t(c=None) == 1 and t(rows=(1 << 20) + 1) == 2 and t(rows=0) == 0
     w = lambda ct=FAKE, st=FAKE, N=4: _status("asp_fp8_quantize_weight", FAKE, 0, N, 100, 100, FAKE, FAKE, ct, st, None)
@@ -82,7 +83,7 @@ def test_c_calls_validate_before_any_launch():
 def _norm(**o):
     a = dict(x=FAKE, ldx=96, y=FAKE, ldy=96, dtype=0, M=8, C=96, alpha=1.0, post=1, pw=None, gate=None, pre=1,
              w=None, b=None, sc=None, sh=None, ldt=96, G=1, off=None, eps=1e-6, h=FAKE, ldh=96, n=FAKE, ndt=0,
-             ldn=96, ns=None)
+             ldn=96, ns=None, zero=0)
     a.update(o)
     return _status("asp_norm_gate", *a.values(), None)
 
@@ -97,13 +98,14 @@ def test_norm_refusals():
     assert _norm(G=0) == 2 and _norm(G=2, off=FAKE, ldt=95) == 2 and _norm(ldn=95) == 2
     assert _norm(x=FAKE + 2) == 3 and _norm(off=FAKE + 2) == 3 and _norm(w=FAKE + 1) == 3
     assert _norm(ndt=2, n=FAKE + 8, ns=FAKE) == 3
+    assert _norm(zero=4) == 1 and _norm(zero=-1) == 1 and _norm(zero=1, h=None) == 1
     assert _norm(M=0, x=None, n=None) == 0
     need = B.asp_norm_gate_backward_workspace_bytes(8, 96, 1)
 
     def back(**o):
         a = dict(dh=FAKE, lddh=96, dn=FAKE, lddn=96, dndt=0, h=FAKE, ldh=96, y=FAKE, ldy=96, dtype=0, M=8, C=96,
                  alpha=1.0, post=1, pw=None, gate=None, pre=1, w=None, b=None, sc=None, ldt=96, G=1, off=None,
-                 eps=1e-6, dx=FAKE, lddx=96, dy=FAKE, lddy=96, dpw=None, dg=None, dw=FAKE, db=None, dsc=None,
+                 eps=1e-6, dx=FAKE, lddx=96, dy=FAKE, lddy=96, zero=0, dpw=None, dg=None, dw=FAKE, db=None, dsc=None,
                  dsh=None, ldd=96, ws=FAKE, nb=need)
         a.update(o)
         return _status("asp_norm_gate_backward", *a.values(), None)
@@ -111,6 +113,7 @@ def test_norm_refusals():
     assert back(dn=None) == 1 and back(h=None) == 1 and back(y=None) == 1 and back(ws=None) == 1
     assert back(pre=0) == 1 and back(pre=0, dn=None, dw=None, dh=None) == 1 and back(post=0, dpw=FAKE) == 1
     assert back(lddn=95) == 2 and back(dx=FAKE + 2) == 3 and back(nb=need - 1) == 5
+    assert back(zero=4) == 1 and back(zero=1, dx=None) == 1 and back(zero=2, dy=None) == 1
     assert back(dx=None, dy=None, dw=None) == 0
 
 

@@ -219,6 +219,10 @@ def test_empty_batches():
     assert quantize(torch.empty((0, 200), device=DEV)).codes.shape == (0, 256)
     dx, dw, db = layer.backward(torch.empty((0, 40), device=DEV), torch.empty((0, 200), device=DEV))
     assert dx.shape == (0, 200) and not dw.any() and not db.any()
+    for N, K in ((2000, 1300), (4000, 2000)):   # the tiled kernels
+        layer = Fp8Layer.pack(torch.ones((N, K), device=DEV), torch.ones(N, device=DEV))
+        dx, dw, db = layer.backward(torch.empty((0, N), device=DEV), torch.empty((0, K), device=DEV))
+        assert dx.shape == (0, K) and not dw.any() and not db.any()
 
 
 def test_neighbouring_memory_is_untouched():
@@ -308,3 +312,18 @@ def test_module_trains():
             m(x)
     torch.cuda.synchronize()
     assert torch.equal(m(x), y)
+
+
+def test_module_takes_broadcast_and_transposed_inputs():
+    from wam_asp_w4a4_amd.linear import Fp8Linear
+    m = Fp8Linear.from_linear(torch.nn.Linear(200, 70).to(DEV), trainable=True)
+    x = torch.randn((1, 200), device=DEV, requires_grad=True)
+    plain = x.detach().expand(40, 200).contiguous().requires_grad_()
+    y = m(x.expand(40, 200))
+    assert torch.equal(y, m(plain))
+    dy = torch.randn((40, 70), device=DEV)
+    y.backward(dy)
+    m(plain).backward(dy)
+    assert torch.allclose(x.grad, plain.grad.sum(0, keepdim=True), rtol=1e-5, atol=1e-5)
+    z = torch.randn((200, 40), device=DEV)
+    assert torch.equal(m(z.t()), m(z.t().contiguous()))

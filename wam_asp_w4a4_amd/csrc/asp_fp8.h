@@ -27,6 +27,8 @@ inline size_t fp8_code_bytes(int64_t rows, int64_t cols) { return (size_t)rows *
 inline size_t fp8_scale_bytes(int64_t rows, int64_t cols) {
   return (size_t)((fp8_blocks(cols) + 3) / 4) * rows * 4;
 }
+// a launch has fewer than 2^32 lanes
+constexpr int64_t kMaxLanes = UINT32_MAX;
 inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // ------------------------------------------------------------------- device

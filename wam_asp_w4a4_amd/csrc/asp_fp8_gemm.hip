@@ -821,7 +821,7 @@ template <int TM, int TN, bool WIDE>
 int32_t launch_tiles(GemmK k, hipStream_t st) {
   constexpr int64_t BM = 64 * TM, BN = 64 * TN;
   const int64_t tm = (k.M + BM - 1) / BM, tn = (k.N + BN - 1) / BN;
-  if (tm * tn > INT32_MAX) return fail(ASP_ERR_SHAPE, "output too large for one launch");
+  if (tm * tn > kMaxLanes / 256) return fail(ASP_ERR_SHAPE, "output too large for one launch");
   k.tiles_m = (int)tm;
   k.tiles_n = (int)tn;
   k_fp8_gemm<TM, TN, WIDE><<<dim3((unsigned)(tm * tn), (unsigned)k.slices), 256, 0, st>>>(k);
@@ -833,7 +833,7 @@ int32_t launch_tail(GemmK k, hipStream_t st) {
   k.tiles_m = (k.M + 255) / 256;
   k.tiles_n = (k.N + 255) / 256;
   const int64_t tiles = (int64_t)k.tiles_m * k.tiles_n;
-  if (tiles > INT32_MAX - kCUs) return fail(ASP_ERR_SHAPE, "output too large for one launch");
+  if (tiles > kMaxLanes / 256 - kCUs) return fail(ASP_ERR_SHAPE, "output too large for one launch");
   const int64_t left = tiles % kCUs;
   k.whole = (int)(tiles - left);
   k.parts = tail_parts(tiles);
@@ -850,16 +850,21 @@ int32_t launch_mid(GemmK k, hipStream_t st) {
   return launch_status("fp8 mid gemm");
 }
 
+int few_waves(int KB) { return KB >= 16 ? 16 : KB >= 8 ? 8 : 4; }
+
 template <typename XT, bool WIDE>
 void launch_few_as(const GemmK& k, const XT* x, int64_t ldx, int64_t K, hipStream_t st) {
-  const dim3 grid((unsigned)((k.N + 15) / 16));
-  if (k.KB >= 16) k_fp8_few<16, XT, WIDE><<<grid, 1024, 0, st>>>(k, x, ldx, (int)K);
-  else if (k.KB >= 8) k_fp8_few<8, XT, WIDE><<<grid, 512, 0, st>>>(k, x, ldx, (int)K);
+  const dim3 grid((unsigned)(((int64_t)k.N + 15) / 16));
+  const int waves = few_waves(k.KB);
+  if (waves == 16) k_fp8_few<16, XT, WIDE><<<grid, 1024, 0, st>>>(k, x, ldx, (int)K);
+  else if (waves == 8) k_fp8_few<8, XT, WIDE><<<grid, 512, 0, st>>>(k, x, ldx, (int)K);
   else k_fp8_few<4, XT, WIDE><<<grid, 256, 0, st>>>(k, x, ldx, (int)K);
 }
 
 template <typename XT>
 int32_t launch_few(const GemmK& k, const XT* x, int64_t ldx, int64_t K, hipStream_t st) {
+  if (((int64_t)k.N + 15) / 16 > kMaxLanes / (64 * few_waves(k.KB)))
+    return fail(ASP_ERR_SHAPE, "output too large for one launch");
   if (k.y_bf16) launch_few_as<XT, false>(k, x, ldx, K, st);
   else launch_few_as<XT, true>(k, x, ldx, K, st);
   return launch_status("fp8 few-row gemm");

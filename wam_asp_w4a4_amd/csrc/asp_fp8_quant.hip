@@ -245,7 +245,7 @@ int32_t fp8_quantize_rows(const void* in, int32_t dtype, int64_t rows, int64_t c
                           uint8_t* codes, uint8_t* scales, hipStream_t st) {
   const int groups = (int)((fp8_blocks(cols) + 3) / 4);
   const int64_t blocks = (rows * groups + 3) / 4;
-  if (blocks > INT32_MAX) return fail(ASP_ERR_SHAPE, "input too large for one launch");
+  if (blocks > kMaxLanes / 256) return fail(ASP_ERR_SHAPE, "input too large for one launch");
   const dim3 grid((unsigned)blocks);
   uint32_t* sc = reinterpret_cast<uint32_t*>(scales);
   if (dtype == ASP_BF16)
@@ -263,11 +263,11 @@ int32_t fp8_quantize_tiles(int n, const Fp8TileJob* jobs, hipStream_t st) {
   for (int i = 0; i < n; ++i) {
     a.j[i] = jobs[i];
     const int64_t t = fp8_blocks(jobs[i].rows) * fp8_blocks(jobs[i].cols);
-    if (i == 0) a.tiles0 = (int)t;
     total += t;
-    if (total > INT32_MAX) return fail(ASP_ERR_SHAPE, "input too large for one launch");
+    if (total > kMaxLanes / (64 * kTileWaves)) return fail(ASP_ERR_SHAPE, "input too large for one launch");
   }
   if (total == 0) return ASP_OK;
+  a.tiles0 = (int)(fp8_blocks(jobs[0].rows) * fp8_blocks(jobs[0].cols));
   k_fp8_tiles<<<dim3((unsigned)total), 64 * kTileWaves, 0, st>>>(a);
   return launch_status("fp8 tile quantise");
 }
@@ -335,7 +335,7 @@ int32_t asp_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
   ASP_TRY(check_ptr(scales, "scales", true));
   ASP_TRY(check_matrix(out, dtype, cols, cols, "out"));
   const int64_t blocks = (rows * (fp8_pitch(cols) / 8) + 255) / 256;
-  if (blocks > INT32_MAX) return fail(ASP_ERR_SHAPE, "input too large for one launch");
+  if (blocks > kMaxLanes / 256) return fail(ASP_ERR_SHAPE, "input too large for one launch");
   const dim3 grid((unsigned)blocks);
   if (dtype == ASP_BF16)
     k_fp8_dequantize<uint16_t><<<grid, 256, 0, (hipStream_t)stream>>>(

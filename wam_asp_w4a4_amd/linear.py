@@ -24,7 +24,7 @@ from typing import Mapping
 
 import torch
 
-from .fp8 import _NAMES, Fp8Layer, _no_capture
+from .fp8 import _NAMES, Fp8Layer, _no_capture, _row_major
 from .layer import PackedLayer
 
 
@@ -127,7 +127,7 @@ class Fp8Linear(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.shape[-1] != self.in_features:
             raise ValueError(f"x has {x.shape[-1]} features, the layer {self.in_features}")
-        x2 = x.reshape(-1, self.in_features)
+        x2 = _row_major(x.reshape(-1, self.in_features))
         leaves = (x2, self.weight, self.bias)
         grads = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in leaves)
         if grads:
