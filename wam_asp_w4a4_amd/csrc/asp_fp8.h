@@ -86,27 +86,54 @@ struct Raw {
   u32x4_t q[sizeof(XT) / 2];
 };
 
-// at p, `left` of them inside the row; the rest are 0 where left > 0, and r is left
-// as it is where left <= 0
-template <typename XT>
-__device__ __forceinline__ void raw_load(const XT* p, int left, Raw<XT>& r) {
-  if (left >= 8) {
-    if constexpr (sizeof(XT) == 2) {
-      r.q[0] = *reinterpret_cast<const u32x4_e2*>(p);
-    } else {
-      r.q[0] = *reinterpret_cast<const u32x4_e4*>(p);
-      r.q[1] = *reinterpret_cast<const u32x4_e4*>(p + 4);
-    }
-  } else if (left > 0) {
+// From element c of a row of `cols`; past its end r is not touched, its zeros stay.
+// Where the row ends inside the eight, float32 is loaded element by element.  16-bit
+// elements would have to be waited for to be paired: there the eight before the row's end
+// are loaded, as every other lane does, and raw_settle puts them in place where they are
+// used (element by element 16384 x 4094 took 298 us in the norms' backward, where 4096
+// columns take 185; so 203.  The same in float32 costs registers: 640 x 3023 29 us for
+// 24).  SHORT: a row of fewer than eight.
+template <bool SHORT, typename XT>
+__device__ __forceinline__ void raw_load(const XT* row, int c, int cols, Raw<XT>& r) {
+  if (c >= cols) return;
+  if constexpr (sizeof(XT) == 2 && !SHORT) {
+    r.q[0] = *reinterpret_cast<const u32x4_e2*>(row + (uint32_t)min(c, cols - 8));
+  } else if constexpr (sizeof(XT) == 2) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(XT) == 2) {
-        const uint32_t w = e < left ? p[e] : 0u;
-        r.q[0][e >> 1] = e & 1 ? r.q[0][e >> 1] | w << 16 : w;
-      } else {
-        r.q[e >> 2][e & 3] = e < left ? __builtin_bit_cast(uint32_t, p[e]) : 0u;
-      }
+      const uint32_t w = e < cols ? row[e] : 0u;
+      r.q[0][e >> 1] = e & 1 ? r.q[0][e >> 1] | w << 16 : w;
     }
+  } else {
+    const XT* p = row + (uint32_t)c;
+    const int left = cols - c;
+    if (left >= 8) {
+      r.q[0] = *reinterpret_cast<const u32x4_e4*>(p);
+      r.q[1] = *reinterpret_cast<const u32x4_e4*>(p + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        r.q[e >> 2][e & 3] = e < left ? __builtin_bit_cast(uint32_t, p[e]) : 0u;
+    }
+  }
+}
+
+template <bool SHORT, typename XT>
+__device__ __forceinline__ void raw_settle(int c, int cols, Raw<XT>& r) {
+  if constexpr (sizeof(XT) == 2 && !SHORT) {
+    const int over = -cols & 7;  // uniform: the elements before the row's last piece
+    if (over == 0 || c + 8 <= cols) return;
+    uint32_t w[5] = {r.q[0][0], r.q[0][1], r.q[0][2], r.q[0][3], 0u};
+    auto move = [&](int n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = i + n < 4 ? w[i + n < 4 ? i + n : 4] : 0u;
+    };
+    if (over & 4) move(2);
+    if (over & 2) move(1);
+    if (over & 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(w[i + 1], w[i], 16);
+    r.q[0] = u32x4_t{w[0], w[1], w[2], w[3]};
   }
 }
 
@@ -122,11 +149,22 @@ __device__ __forceinline__ void unpack(const Raw<XT>& r, float (&v)[8]) {
   }
 }
 
-// eight elements, 0 from `left` on
+// both, for any row
 template <typename XT>
-__device__ __forceinline__ void load8(const XT* p, int left, float (&v)[8]) {
+__device__ __forceinline__ void raw_get(const XT* row, int c, int cols, Raw<XT>& r) {
+  if (cols >= 8) {
+    raw_load<false>(row, c, cols, r);
+    raw_settle<false>(c, cols, r);
+  } else {
+    raw_load<true>(row, c, cols, r);
+  }
+}
+
+// eight elements from element c of a row of `cols`, 0 past its end
+template <typename XT>
+__device__ __forceinline__ void load8(const XT* row, int c, int cols, float (&v)[8]) {
   Raw<XT> r = {};
-  raw_load(p, left, r);
+  raw_get(row, c, cols, r);
   unpack(r, v);
 }
 

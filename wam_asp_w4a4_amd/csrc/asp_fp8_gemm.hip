@@ -662,8 +662,8 @@ __global__ void __launch_bounds__(64 * W)
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int64_t at = (int64_t)kb * kFp8Block + 64 * (c >> 1) + 16 * q + 8 * (c & 1);
-          load8(x + m * ldx + at, K - at, v[c]);
+          const int at = kb * kFp8Block + 64 * (c >> 1) + 16 * q + 8 * (c & 1);
+          load8(x + m * ldx, at, K, v[c]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = max(top, finite_bits(v[c][e]));
         }

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(256)
   const int c0 = 512 * g + 8 * lane;
   const int pitch = (cols + kFp8Block - 1) / kFp8Block * kFp8Block;
   float v[8];
-  load8(x + row * ld + c0, cols - c0, v);
+  load8(x + row * ld, c0, cols, v);
   uint32_t u = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) u = max(u, finite_bits(v[e]));
@@ -66,11 +66,17 @@ __device__ __forceinline__ void tile_body(const Fp8TileJob& j, int tile,
   const int ncb = (int)((j.cols + 127) / 128);
   const int rb = tile / ncb, cb = tile % ncb;
   const int64_t r0 = (int64_t)rb * 128 + 4 * rg, c0 = (int64_t)cb * 128 + 8 * cg;
-  const XT* x = static_cast<const XT*>(j.in) + r0 * j.ld + c0;
+  const XT* x = static_cast<const XT*>(j.in) + r0 * j.ld;
   Raw<XT> raw[4] = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (r0 + i < j.rows) raw_load(x + i * j.ld, (int)min(j.cols - c0, (int64_t)8), raw[i]);
+    if (r0 + i < j.rows) {
+      if (j.cols >= 8) raw_load<false>(x + i * j.ld, (int)c0, (int)j.cols, raw[i]);
+      else raw_load<true>(x + i * j.ld, (int)c0, (int)j.cols, raw[i]);
+    }
+  if (j.cols >= 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw_settle<false>((int)c0, (int)j.cols, raw[i]);
   // magnitudes: per row (this thread's 8 columns) and per column (its 4 rows)
   uint32_t ru[4], cu[8];
   float cs[8];

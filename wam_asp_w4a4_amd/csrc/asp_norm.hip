@@ -95,18 +95,17 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int G, int ro
 }
 
 // a thread's columns of a row: E chunks of 8, chunk e at column 8 (e T + t)
-template <typename XT, int E, int T>
+template <typename XT, int E, int T, bool SHORT>
 __device__ __forceinline__ void row_load(const void* p, int64_t row, int64_t ld, int C, int t,
                                          Raw<XT> (&r)[E]) {
   const XT* base = static_cast<const XT*>(p) + row * ld;  // uniform
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const uint32_t c = (uint32_t)(e * T + t) * 8u;
-    raw_load(base + c, C - (int)c, r[e]);
+    raw_load<SHORT>(base, (e * T + t) * 8, C, r[e]);
   }
 }
 
-template <int E, int T>
+template <int E, int T, bool SHORT>
 __device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, float other,
                                       float (&v)[E][8]) {
 #pragma unroll
@@ -116,7 +115,8 @@ __device__ __forceinline__ void table(const float* p, int64_t at, int C, int t, 
     for (int k = 0; k < 8; ++k) v[e][k] = other;
     if (!p || c >= C) continue;
     Raw<float> r = {};
-    raw_load(p + at + c, C - c, r);
+    raw_load<SHORT>(p + at, c, C, r);
+    raw_settle<SHORT>(c, C, r);
     unpack(r, v[e]);
   }
 }
@@ -197,7 +197,7 @@ __device__ __forceinline__ void normalise(float (&v)[E][8], int kind, int C, flo
   each<E>([&](int e, int k) { v[e][k] *= r; });
 }
 
-template <typename XT, int T, int E>
+template <typename XT, int T, int E, bool SHORT = false>
 __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
   __shared__ SumsLds lds;
   const int t = threadIdx.x;
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
   float gp[E][8], pa[E][8], pc[E][8];
   Raw<XT> nx[E] = {}, ny[E] = {};
   auto fetch = [&](int64_t row) {
-    row_load<XT, E, T>(a.x, row, a.ldx, a.C, t, nx);
-    if (a.y) row_load<XT, E, T>(a.y, row, a.ldy, a.C, t, ny);
+    row_load<XT, E, T, SHORT>(a.x, row, a.ldx, a.C, t, nx);
+    if (a.y) row_load<XT, E, T, SHORT>(a.y, row, a.ldy, a.C, t, ny);
   };
   const int64_t first = a.offsets ? max(r0, (int64_t)a.offsets[0]) : r0;
   if (first < r1) fetch(first);
@@ -226,13 +226,13 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
       }
       float u[E][8], w[E][8];
       // v gate post_w, and (v w + b) (1 + scale) + shift = v pa + pc
-      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
-      table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
+      table<E, T, SHORT>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
+      table<E, T, SHORT>(a.post_w, 0, a.C, t, 1.0f, u);
       each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
-      table<E, T>(a.pre_w, 0, a.C, t, 1.0f, pa);
-      table<E, T>(a.pre_b, 0, a.C, t, 0.0f, pc);
-      table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
-      table<E, T>(a.shift, g * a.ldt, a.C, t, 0.0f, w);
+      table<E, T, SHORT>(a.pre_w, 0, a.C, t, 1.0f, pa);
+      table<E, T, SHORT>(a.pre_b, 0, a.C, t, 0.0f, pc);
+      table<E, T, SHORT>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
+      table<E, T, SHORT>(a.shift, g * a.ldt, a.C, t, 0.0f, w);
       each<E>([&](int e, int k) {
         pa[e][k] *= 1.0f + u[e][k];
         pc[e][k] = __builtin_fmaf(pc[e][k], 1.0f + u[e][k], w[e][k]);
@@ -241,6 +241,8 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
     float v[E][8], p[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      raw_settle<SHORT>((e * T + t) * 8, a.C, nx[e]);
+      raw_settle<SHORT>((e * T + t) * 8, a.C, ny[e]);
       unpack(nx[e], v[e]);
       unpack(ny[e], p[e]);
     }
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(T) k_norm_gate(const NormArgs a) {
 // touches, to slot strip + g (strips and sequences both advance along the rows,
 // so no two pairs share one).  k_norm_sums adds the strips in order: the
 // results do not depend on scheduling.
-template <typename XT, typename NT, int T, int E>
+template <typename XT, typename NT, int T, int E, bool SHORT = false>
 __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
   // the next row's loads in flight where a row is few enough registers (8192 x 8192 bf16,
   // layer norms: 193 against 226 us); in float32 they cost registers that other waves
@@ -358,11 +360,11 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
   Raw<XT> rd[E] = {}, ry[E] = {}, rh[E] = {};
   Raw<NT> rn[E] = {};
   auto fetch = [&](int64_t row) {
-    if (a.dh) row_load<XT, E, T>(a.dh, row, a.lddh, a.C, t, rd);
-    if (a.y) row_load<XT, E, T>(a.y, row, a.ldy, a.C, t, ry);
+    if (a.dh) row_load<XT, E, T, SHORT>(a.dh, row, a.lddh, a.C, t, rd);
+    if (a.y) row_load<XT, E, T, SHORT>(a.y, row, a.ldy, a.C, t, ry);
     if (pre) {
-      row_load<XT, E, T>(a.h, row, a.ldh, a.C, t, rh);
-      row_load<NT, E, T>(a.dn, row, a.lddn, a.C, t, rn);
+      row_load<XT, E, T, SHORT>(a.h, row, a.ldh, a.C, t, rh);
+      row_load<NT, E, T, SHORT>(a.dn, row, a.lddn, a.C, t, rn);
     }
   };
   const int64_t first = a.offsets ? max(r0, (int64_t)a.offsets[0]) : r0;
@@ -385,11 +387,11 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
         end = a.M;
       }
       float u[E][8];
-      table<E, T>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
-      table<E, T>(a.post_w, 0, a.C, t, 1.0f, u);
+      table<E, T, SHORT>(a.gate, g * a.ldt, a.C, t, 1.0f, gp);
+      table<E, T, SHORT>(a.post_w, 0, a.C, t, 1.0f, u);
       each<E>([&](int e, int k) { gp[e][k] *= u[e][k]; });
-      table<E, T>(a.pre_w, 0, a.C, t, 1.0f, pa);
-      table<E, T>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
+      table<E, T, SHORT>(a.pre_w, 0, a.C, t, 1.0f, pa);
+      table<E, T, SHORT>(a.scale, g * a.ldt, a.C, t, 0.0f, u);
       each<E>([&](int e, int k) {
         pa[e][k] *= 1.0f + u[e][k];
         s1[e][k] = s2[e][k] = s3[e][k] = 0.0f;
@@ -399,6 +401,11 @@ __global__ void __launch_bounds__(T, 4) k_norm_gate_back(const NormArgs a) {
     float d[E][8], v[E][8], n[E][8], q[E][8];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      const int c = (e * T + t) * 8;
+      raw_settle<SHORT>(c, a.C, rd[e]);
+      raw_settle<SHORT>(c, a.C, ry[e]);
+      raw_settle<SHORT>(c, a.C, rh[e]);
+      raw_settle<SHORT>(c, a.C, rn[e]);
       unpack(rd[e], d[e]);
       unpack(ry[e], q[e]);
       unpack(rh[e], v[e]);
@@ -610,7 +617,8 @@ int32_t check_vec(const float* p, const char* name) {
 template <typename XT>
 int32_t launch_norm(const NormArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)strips(a.M, a.rows));
-  if (a.C <= 512) k_norm_gate<XT, 64, 1><<<grid, 64, 0, st>>>(a);
+  if (a.C < 8) k_norm_gate<XT, 64, 1, true><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 512) k_norm_gate<XT, 64, 1><<<grid, 64, 0, st>>>(a);
   else if (a.C <= 1024) k_norm_gate<XT, 128, 1><<<grid, 128, 0, st>>>(a);
   else if (a.C <= 2048) k_norm_gate<XT, 256, 1><<<grid, 256, 0, st>>>(a);
   else if (a.C <= 4096) k_norm_gate<XT, 512, 1><<<grid, 512, 0, st>>>(a);
@@ -622,7 +630,8 @@ int32_t launch_norm(const NormArgs& a, hipStream_t st) {
 template <typename XT, typename NT>
 int32_t launch_back(const NormArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)strips(a.M, a.rows));
-  if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1><<<grid, 64, 0, st>>>(a);
+  if (a.C < 8) k_norm_gate_back<XT, NT, 64, 1, true><<<grid, 64, 0, st>>>(a);
+  else if (a.C <= 512) k_norm_gate_back<XT, NT, 64, 1><<<grid, 64, 0, st>>>(a);
   else if (a.C <= 1024) k_norm_gate_back<XT, NT, 128, 1><<<grid, 128, 0, st>>>(a);
   else if (a.C <= 2048) k_norm_gate_back<XT, NT, 256, 1><<<grid, 256, 0, st>>>(a);
   else if (a.C <= 4096) k_norm_gate_back<XT, NT, 512, 1><<<grid, 512, 0, st>>>(a);
