@@ -402,3 +402,50 @@ def test_module_takes_padded_broadcast_and_strided_inputs():
     assert torch.equal(got[3][:, ::2], want.scale) and not got[3][:, 1::2].any()
     for a, b in zip(got[4:], (want.post_weight, want.weight, want.bias)):
         assert torch.equal(a, b)
+
+
+def test_binding_calls_give_the_layers_results():
+    """The wrappers of the C calls, one by one, against fp8.py and norm.py."""
+    M, N, K = 40, 130, 200
+    w, x, dy = (torch.randn(s, device=DEV) for s in ((N, K), (M, K), (M, N)))
+    bias = torch.randn(N, device=DEV)
+    layer = Fp8Layer.pack(w, bias)
+    q, qt = Fp8Tensor.empty(M, K, DEV), Fp8Tensor.empty(K, M, DEV)
+    B.asp_fp8_quantize(x, B.ASP_F32, M, K, K, q.codes, q.scales)
+    B.asp_fp8_quantize_t(x, B.ASP_F32, M, K, K, qt.codes, qt.scales)
+    for got, want in ((q, quantize(x)), (qt, quantize(x, transpose=True))):
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    a, b = Fp8Tensor.empty(N, K, DEV), Fp8Tensor.empty(K, N, DEV)
+    B.asp_fp8_quantize_weight(w, B.ASP_F32, N, K, K, a.codes, a.scales, b.codes, b.scales)
+    assert torch.equal(a.codes, layer.codes) and torch.equal(b.codes, layer.codes_t)
+    v = torch.empty_like(x)
+    B.asp_fp8_dequantize(q.codes, q.scales, M, K, v, B.ASP_F32)
+    assert torch.equal(v, q.dequantize())
+    want, y, z = layer.forward(x), *(torch.empty((M, N), device=DEV) for _ in range(2))
+    ws = layer.workspace(M)
+    B.asp_fp8_gemm(q.codes, q.scales, a.codes, a.scales, M, N, K, bias, y, B.ASP_F32)
+    B.asp_fp8_forward(x, B.ASP_F32, K, M, N, K, a.codes, a.scales, bias, z, B.ASP_F32, ws, ws.numel())
+    assert torch.equal(y, want) and torch.equal(z, want)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(bias)
+    ws = layer.workspace(M, backward=True)
+    B.asp_fp8_backward(dy, B.ASP_F32, N, x, B.ASP_F32, K, M, N, K, b.codes, b.scales, dx, B.ASP_F32,
+                       dw, B.ASP_F32, db, ws, ws.numel())
+    assert all(torch.equal(s, t) for s, t in zip((dx, dw, db), layer.backward(dy, x)))
+
+    c = Case(M, K, "f32", "rms", "layer", True, [3, 20, 33])
+    h, n = gated_norm(c.x, c.y, **c.kw)
+    g = gated_norm_backward(c.dh, c.dn, h, c.y, **c.kw)
+    k = c.kw
+    h2, n2, dx2, dy2 = (torch.full_like(h, 9.0) for _ in range(4))
+    ldt = k["gate"].stride(0)
+    B.asp_norm_gate(c.x, c.x.stride(0), c.y, c.y.stride(0), B.ASP_F32, M, K, k["alpha"], B.ASP_NORM_RMS,
+                    k["post_weight"], k["gate"], B.ASP_NORM_LAYER, k["weight"], k["bias"], k["scale"],
+                    k["shift"], ldt, 2, k["offsets"], EPS, h2, K, n2, B.ASP_F32, K, zero=3)
+    assert torch.equal(h2, h) and torch.equal(n2, n)
+    made = [torch.full((2, K) if i in (1, 4, 5) else (K,), 9.0, device=DEV) for i in range(6)]
+    ws = torch.empty(B.asp_norm_gate_backward_workspace_bytes(M, K, 2), dtype=torch.uint8, device=DEV)
+    B.asp_norm_gate_backward(c.dh, c.dh.stride(0), c.dn, c.dn.stride(0), B.ASP_F32, h, K, c.y,
+                             c.y.stride(0), B.ASP_F32, M, K, k["alpha"], B.ASP_NORM_RMS, k["post_weight"],
+                             k["gate"], B.ASP_NORM_LAYER, k["weight"], k["bias"], k["scale"], ldt, 2,
+                             k["offsets"], EPS, dx2, K, dy2, K, 3, *made, K, ws, ws.numel())
+    assert all(torch.equal(s, t) for s, t in zip((dx2, dy2, *made), g))

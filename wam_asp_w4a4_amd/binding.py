@@ -89,7 +89,8 @@ SIGNATURES = {
     "asp_fp8_backward": (_i32, [_p, _i32, _i64, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _i32,
                                 _p, _i32, _p, _p, _sz, _p]),
     "asp_norm_gate": (_i32, [_p, _i64, _p, _i64, _i32, _i64, _i64, _f32, _i32, _p, _p, _i32, _p,
-                             _p, _p, _p, _i64, _i32, _p, _f32, _p, _i64, _p, _i32, _i64, _p, _i32, _p]),
+                             _p, _p, _p, _i64, _i32, _p, _f32, _p, _i64, _p, _i32, _i64, _p,
+                             _i32, _p]),
     "asp_norm_gate_backward_workspace_bytes": (_i32, [_i64, _i64, _i32, _psz]),
     "asp_norm_gate_backward": (_i32, [_p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i32, _i64,
                                       _i64, _f32, _i32, _p, _p, _i32, _p, _p, _p, _i64, _i32, _p,
@@ -449,6 +450,27 @@ def asp_fp8_sizes(rows, cols):
     return c.value, s.value
 
 
+def asp_fp8_quantize(inp, dtype, rows, cols, ld, codes, scales, stream=None):
+    _check(lib().asp_fp8_quantize(_at(inp), dtype, rows, cols, ld, _ptr(codes), _ptr(scales),
+                                  _stream(stream, inp)))
+
+
+def asp_fp8_quantize_t(inp, dtype, rows, cols, ld, codes_t, scales_t, stream=None):
+    _check(lib().asp_fp8_quantize_t(_at(inp), dtype, rows, cols, ld, _ptr(codes_t),
+                                    _ptr(scales_t), _stream(stream, inp)))
+
+
+def asp_fp8_quantize_weight(w, dtype, N, K, ld, codes, scales, codes_t=None, scales_t=None,
+                            stream=None):
+    _check(lib().asp_fp8_quantize_weight(_at(w), dtype, N, K, ld, _ptr(codes), _ptr(scales),
+                                         _ptr(codes_t), _ptr(scales_t), _stream(stream, w)))
+
+
+def asp_fp8_dequantize(codes, scales, rows, cols, out, dtype, stream=None):
+    _check(lib().asp_fp8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out), dtype,
+                                    _stream(stream, out)))
+
+
 def asp_fp8_gemm_workspace_bytes(M, N, K) -> int:
     return _size("asp_fp8_gemm_workspace_bytes", M, N, K)
 
@@ -475,5 +497,34 @@ def asp_fp8_backward_workspace_bytes(M, N, K) -> int:
     return _size("asp_fp8_backward_workspace_bytes", M, N, K)
 
 
+def asp_fp8_backward(dy, dy_dtype, lddy, x, x_dtype, ldx, M, N, K, wt_codes, wt_scales, dx,
+                     dx_dtype, dw, dw_dtype, db, workspace, workspace_bytes, stream=None):
+    _check(lib().asp_fp8_backward(_at(dy), dy_dtype, lddy, _at(x), x_dtype, ldx, M, N, K,
+                                  _ptr(wt_codes), _ptr(wt_scales), _ptr(dx), dx_dtype, _ptr(dw),
+                                  dw_dtype, _ptr(db), _ptr(workspace), workspace_bytes,
+                                  _stream(stream, dy)))
+
+
+def asp_norm_gate(x, ldx, y, ldy, dtype, M, C, alpha, post, post_w, gate, pre, pre_w, pre_b, scale,
+                  shift, ldt, G, offsets, eps, h, ldh, n, n_dtype, ldn, n_scales=None, zero=0,
+                  stream=None):
+    _check(lib().asp_norm_gate(_at(x), ldx, _at(y), ldy, dtype, M, C, alpha, post, _ptr(post_w),
+                               _at(gate), pre, _ptr(pre_w), _ptr(pre_b), _at(scale), _at(shift),
+                               ldt, G, _ptr(offsets), eps, _at(h), ldh, _at(n), n_dtype, ldn,
+                               _ptr(n_scales), zero, _stream(stream, x)))
+
+
 def asp_norm_gate_backward_workspace_bytes(M, C, G) -> int:
     return _size("asp_norm_gate_backward_workspace_bytes", M, C, G)
+
+
+def asp_norm_gate_backward(dh, lddh, dn, lddn, dn_dtype, h, ldh, y, ldy, dtype, M, C, alpha, post,
+                           post_w, gate, pre, pre_w, pre_b, scale, ldt, G, offsets, eps, dx, lddx,
+                           dy, lddy, zero, d_post_w, d_gate, d_pre_w, d_pre_b, d_scale, d_shift, ldd,
+                           workspace, workspace_bytes, stream=None):
+    _check(lib().asp_norm_gate_backward(
+        _at(dh), lddh, _at(dn), lddn, dn_dtype, _at(h), ldh, _at(y), ldy, dtype, M, C, alpha, post,
+        _ptr(post_w), _at(gate), pre, _ptr(pre_w), _ptr(pre_b), _at(scale), ldt, G, _ptr(offsets),
+        eps, _at(dx), lddx, _at(dy), lddy, zero, _ptr(d_post_w), _at(d_gate), _ptr(d_pre_w),
+        _ptr(d_pre_b), _at(d_scale), _at(d_shift), ldd, _ptr(workspace), workspace_bytes,
+        _stream(stream, dh, dn)))
