@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(256) k_fp8_colsum(const ColSum c) {
 
 // k_fp8_back: what a small layer's backward computes from the quantised operands, in one
 // launch: g[0]'s tiles (count[0] workgroups), g[1]'s, then the column sums.  Each alone
-// is a few microseconds of latency on part of the CUs.
+// is a few microseconds of latency on part of the CUs: 256 x 1024 x 1024, the whole
+// backward, 17.8 us with a launch for each, 13.5 so.
 struct BackK {
   GemmK g[2];
   int count[2], mid[2];
