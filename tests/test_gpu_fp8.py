@@ -327,3 +327,73 @@ def test_module_takes_broadcast_and_transposed_inputs():
     assert torch.allclose(x.grad, plain.grad.sum(0, keepdim=True), rtol=1e-5, atol=1e-5)
     z = torch.randn((200, 40), device=DEV)
     assert torch.equal(m(z.t()), m(z.t().contiguous()))
+
+
+def test_offsets_past_32_bits():
+    """Whole numbers, whose sums are exact: the far rows of a large call and the same rows alone."""
+    def whole(M, K):
+        return torch.randint(-4, 5, (M, K), dtype=torch.int8, device=DEV).bfloat16()
+
+    M, N, K = 600_000, 130, 4000        # x and its codes past 2^31 elements
+    x, dy = whole(M, K), whole(M, N)
+    layer = Fp8Layer.pack(whole(N, K))
+    y = layer.forward(x, "f32")
+    assert torch.equal(y[-300:], layer.forward(x[-300:].contiguous(), "f32"))
+    dx, dw, _ = layer.backward(dy, x)
+    assert torch.equal(dx[-300:], layer.backward(dy[-300:].contiguous())[0])
+    want = torch.zeros((N, K), device=DEV, dtype=torch.float64)
+    for i in range(0, M, 100_000):
+        want += (dy[i:i + 100_000].float().t() @ x[i:i + 100_000].float()).double()   # below 2^24
+    assert torch.equal(dw.double(), want)
+    assert torch.equal(quantize(x).dequantize("bf16")[-300:], x[-300:])
+    del x, dy, y, dx, dw, want
+
+    M, N, K = 70_000, 40_000, 130       # y past 2^31 elements
+    x = whole(M, K)
+    layer = Fp8Layer.pack(whole(N, K), backward=False)
+    y = layer.forward(x, "f32")
+    assert torch.equal(y[-300:], layer.forward(x[-300:].contiguous(), "f32"))
+    y = layer.forward(x)
+    assert torch.equal(y[-300:], layer.forward(x[-300:].contiguous()))
+
+
+def test_one_row_of_the_longest_k():
+    K = 1 << 20
+    x = torch.randint(-2, 3, (40, K), dtype=torch.int8, device=DEV).bfloat16()
+    w = torch.randint(-2, 3, (20, K), dtype=torch.int8, device=DEV).bfloat16()
+    layer = Fp8Layer.pack(w, backward=False)
+    want = x.float() @ w.float().t()     # whole numbers up to 2^22: exact in any order
+    assert torch.equal(layer.forward(x, "f32"), want)
+    assert torch.equal(layer.forward(x[:1], "f32"), want[:1])
+
+
+def test_two_captured_calls_and_two_streams_share_a_layer():
+    """Each call has a workspace of its own: graphs replayed at once and eager calls on two
+    streams do not disturb each other."""
+    layer = Fp8Layer.pack(torch.randn((1024, 1024), device=DEV), torch.randn(1024, device=DEV))
+    xs = [torch.randn((M, 1024), device=DEV) for M in (200, 700)]
+    want = [(layer.forward(x), layer.backward(x, x)) for x in xs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in xs]
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append((layer.forward(x), layer.backward(x, x)))
+        graphs.append(graph)
+
+    def same(a, b):
+        return torch.equal(a[0], b[0]) and all(torch.equal(s, t) for s, t in zip(a[1], b[1]))
+
+    for _ in range(5):
+        torch.cuda.synchronize()
+        eager = []
+        for x, graph, stream in zip(xs, graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(outs, want))
+        for x, stream in zip(xs, streams):
+            with torch.cuda.stream(stream):
+                eager.append((layer.forward(x), layer.backward(x, x)))
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(eager, want))

@@ -449,3 +449,72 @@ def test_binding_calls_give_the_layers_results():
                              k["gate"], B.ASP_NORM_LAYER, k["weight"], k["bias"], k["scale"], ldt, 2,
                              k["offsets"], EPS, dx2, K, dy2, K, 3, *made, K, ws, ws.numel())
     assert all(torch.equal(s, t) for s, t in zip((dx2, dy2, *made), g))
+
+
+def test_offsets_past_32_bits():
+    """The far rows of a large call and the same rows alone: the same bits."""
+    M, C = 140_000, 16_384
+    x, y = (torch.randn((M, C), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    w = torch.rand(C, device=DEV) + 0.5
+    kw = dict(post="rms", post_weight=w, pre="layer", weight=w)
+    h, n = gated_norm(x, y, **kw)
+    far = slice(M - 50, M)
+    for a, b in zip((h, n), gated_norm(x[far].contiguous(), y[far].contiguous(), **kw)):
+        assert torch.equal(a[far], b)
+    g = gated_norm_backward(x, n, h, y, **kw)
+    s = gated_norm_backward(*(t[far].contiguous() for t in (x, n, h, y)), **kw)
+    assert torch.equal(g.dx[far], s.dx) and torch.equal(g.dy[far], s.dy)
+    del g, s
+    _, q = gated_norm(x, y, out="fp8", **kw)
+    far = slice(M - 300, M)
+    assert torch.equal(q.codes[far], gated_norm(x[far].contiguous(), y[far].contiguous(), out="fp8", **kw)[1].codes)
+
+
+def test_module_without_a_pre_norm_and_under_capture():
+    m = GatedNorm(200, post="layer", pre="none", alpha=0.5, device=DEV)
+    x, y = (torch.randn((2, 30, 200), device=DEV, requires_grad=True) for _ in range(2))
+    h, n = m(x, y)
+    assert n is None
+    dh = torch.randn_like(h)
+    got = torch.autograd.grad(h, (x, y, m.post_weight), dh)
+    want = gated_norm_backward(dh.view(60, 200), None, h.detach().view(60, 200), y.detach().view(60, 200),
+                               alpha=0.5, post="layer", post_weight=m.post_weight.detach(), pre="none")
+    assert torch.equal(got[0].view(60, 200), want.dx) and torch.equal(got[1].view(60, 200), want.dy)
+    assert torch.equal(got[2], want.post_weight)
+    with pytest.raises(RuntimeError, match="capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            m(x, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(graph):
+        k = m(x, y)[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(k, h)
+
+
+def test_modules_of_a_bf16_model():
+    """Parameters and tables in bf16 are used as their float32 values; gradients come back in
+    their types."""
+    from wam_asp_w4a4_amd.linear import Fp8Linear
+    norm = GatedNorm(96, pre="layer", device=DEV).bfloat16()
+    lin = Fp8Linear.from_linear(torch.nn.Linear(96, 70).to(DEV), trainable=True).bfloat16()
+    x = torch.randn((20, 96), dtype=torch.bfloat16, device=DEV)
+    tab = torch.randn((1, 192), dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    scale, shift = tab.chunk(2, dim=1)
+    h, n = norm(x, scale=scale, shift=shift)
+    z = lin(n)
+    want = gated_norm(x, pre="layer", weight=norm.weight.detach().float(), bias=norm.bias.detach().float(),
+                      scale=scale.detach().float(), shift=shift.detach().float())[1]
+    assert torch.equal(n, want) and z.dtype == torch.bfloat16
+    layer = Fp8Layer.pack(lin.weight.detach(), lin.bias.detach().float())
+    assert torch.equal(z, layer.forward(want))
+    dz = torch.randn_like(z)
+    z.backward(dz)
+    dn, dw, db = layer.backward(dz, want, dw_dtype="bf16")
+    assert torch.equal(lin.weight.grad, dw) and torch.equal(lin.bias.grad, db.bfloat16())
+    g = gated_norm_backward(torch.zeros_like(x), dn, h.detach(), pre="layer", weight=norm.weight.detach().float(),
+                            bias=norm.bias.detach().float(), scale=scale.detach().float(),
+                            shift=shift.detach().float())
+    assert torch.equal(tab.grad, torch.cat((g.scale, g.shift), dim=1).bfloat16())
+    assert torch.equal(norm.weight.grad, g.weight.bfloat16())

@@ -51,6 +51,10 @@ def _row_major(t):
     return t
 
 
+def _float32(t):
+    return t if t is None or t.dtype is torch.float32 else t.float()
+
+
 def _check_rows(t, name, rows, cols, device, dtypes=_CODES):
     """t must be a (rows, cols) matrix with contiguous rows that do not overlap (rows
     None: any number).  Returns its row stride."""

@@ -24,7 +24,7 @@ from typing import Mapping
 
 import torch
 
-from .fp8 import _NAMES, Fp8Layer, _no_capture, _row_major
+from .fp8 import _NAMES, Fp8Layer, _float32, _no_capture, _row_major
 from .layer import PackedLayer
 
 
@@ -134,7 +134,7 @@ class Fp8Linear(torch.nn.Module):
             _no_capture()
         layer = self.packed
         if layer is None:
-            bias = None if self.bias is None else self.bias.detach()
+            bias = None if self.bias is None else _float32(self.bias.detach())
             layer = Fp8Layer.pack(self.weight.detach(), bias, backward=grads and x2.requires_grad)
         if grads:
             y = _Fp8Apply.apply(x2, self.weight, self.bias, layer)

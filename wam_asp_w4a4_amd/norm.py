@@ -18,7 +18,8 @@ from typing import NamedTuple
 import torch
 
 from . import binding as B
-from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _lend, _no_capture, _row_major
+from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _lend, _no_capture, \
+    _row_major
 from .layer import _Y_DTYPES, _check_ws
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
@@ -255,7 +256,8 @@ class _GatedNorm(torch.autograd.Function):
 class GatedNorm(torch.nn.Module):
     """``gated_norm`` with its weights as parameters, differentiable in every input.
 
-    x, y: (..., C); gate, scale, shift: (G, C) or (C); returns (h, n) of x's shape
+    x, y: (..., C); gate, scale, shift: (G, C) or (C), taken as float32 like the weights;
+    returns (h, n) of x's shape
     (n None for pre 'none'; rows of no sequence are zeros; without gradients, y and a
     factor alpha, h is x itself).  Under a HIP graph capture, gradients are refused: capture
     ``gated_norm`` and ``gated_norm_backward``, which keep no graph of their own."""
@@ -279,12 +281,14 @@ class GatedNorm(torch.nn.Module):
         if y is None and self.post != "none":
             raise ValueError("a post norm needs y")
         flat = [None if t is None else _row_major(t.reshape(-1, self.channels)) for t in (x, y)]
+        post_weight, weight, bias, gate, scale, shift = map(
+            _float32, (self.post_weight, self.weight, self.bias, gate, scale, shift))
         tables = [t for t in (gate, scale, shift) if t is not None]
         if len({(t.dim(), t.stride()) for t in tables}) > 1 or any(_row_major(t) is not t for t in tables):
             gate, scale, shift = (None if t is None else t.contiguous() for t in (gate, scale, shift))
         options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps,
                        offsets=offsets)
-        tensors = (self.post_weight, gate, self.weight, self.bias, scale, shift)
+        tensors = (post_weight, gate, weight, bias, scale, shift)
         if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                            for t in (*flat, *tensors)):
             _no_capture()
