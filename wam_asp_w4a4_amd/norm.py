@@ -159,8 +159,9 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     """Gradients of ``gated_norm`` from dh (of h as it goes on; None: zeros) and dn (of
     n, float32 or bf16; None without a pre norm).  h: the forward's; the options are
     the forward's.  dx, dy: tensors to write (rows of no sequence are left as they
-    are; they are zeros in tensors made here).  Every given input of the forward has a gradient in the result, in its shape
-    (float32 but for dx and dy, which have the stream's type)."""
+    are; they are zeros in tensors made here).  Every given input of the forward has a
+    gradient in the result, in its shape (float32 but for dx and dy, which have the
+    stream's type)."""
     if not isinstance(h, torch.Tensor) or h.dim() != 2:
         raise ValueError("h must be a 2-D torch tensor")
     M, C = h.shape
