@@ -209,6 +209,37 @@ def test_gated_norm_backward_rejects_before_launch():
             norm.gated_norm_backward(*args, **kw)
 
 
+CPU_CALLS = {
+    "quantize": lambda x: fp8.quantize(x),
+    "quantize transposed": lambda x: fp8.quantize(x, transpose=True),
+    "dequantize": lambda x: fp8.Fp8Tensor.empty(40, 200, "cpu").dequantize(),
+    "pack": lambda x: fp8.Fp8Layer.pack(x),
+    "forward": lambda x: layer().forward(x),
+    "forward of codes": lambda x: layer().forward(fp8.Fp8Tensor.empty(40, 200, "cpu")),
+    "backward": lambda x: layer().backward(torch.zeros((40, 64)), x),
+    "norm": lambda x: norm.gated_norm(x, x, post="rms"),
+    "norm to codes": lambda x: norm.gated_norm(x, out="fp8"),
+    "norm backward": lambda x: norm.gated_norm_backward(x, x, x, x, weight=torch.ones(200)),
+    "norm module": lambda x: norm.GatedNorm(200)(x),
+    "norm module, frozen": lambda x: norm.GatedNorm(200).requires_grad_(False)(x),
+    "linear": lambda x: Fp8Linear(layer())(x),
+    "linear, trainable": lambda x: Fp8Linear.from_linear(torch.nn.Linear(200, 64), trainable=True)(x),
+    "from_linear": lambda x: Fp8Linear.from_linear(torch.nn.Linear(200, 64)),
+}
+
+
+@pytest.mark.parametrize("call", list(CPU_CALLS))
+def test_cpu_tensors_never_reach_the_library(call, monkeypatch):
+    """Every other argument is right: only the device is not."""
+    reached = []
+    for name in B.SIGNATURES:
+        if name.startswith(("asp_fp8", "asp_norm")) and not name.endswith(("_bytes", "_sizes")):
+            monkeypatch.setattr(B.lib(), name, lambda *a, name=name: reached.append(name) or 0)
+    with pytest.raises(ValueError, match="GPU"):
+        CPU_CALLS[call](torch.zeros((40, 200)))
+    assert not reached
+
+
 def test_install_takes_either_kind():
     m = torch.nn.Sequential(torch.nn.Linear(200, 64), torch.nn.GELU(), torch.nn.Linear(64, 200, bias=False))
     assert install(m, {"0": layer(64, 200), "2": layer(200, 64, bias=False)}) == ["0", "2"]

@@ -425,8 +425,11 @@ def stream_on(stream, device):
 
 def launch(device, fn, *args):
     """fn(*args) with `device` current, raising the library's error.  For callers that
-    have checked their tensors and pass addresses."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
+    have checked their tensors, which lie on `device`, and pass addresses: a kernel given
+    the host's would fault."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}, not on a GPU")
+    if device.index == torch.cuda.current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(device):
