@@ -121,3 +121,16 @@ def test_group_rejects_mixed_shapes(layer):
         forward_group([layer, other], torch.zeros((2, 256)))
     with pytest.raises(ValueError):
         forward_group([layer, layer], torch.zeros((2, 256)), ys=[torch.empty((2, 64))])
+
+
+def test_a_layer_on_the_cpu_is_refused_before_launch(layer, monkeypatch):
+    from wam_asp_w4a4_amd import binding as B
+    from wam_asp_w4a4_amd.layer import forward_group
+    x = torch.zeros((4, 256))
+    reached = []
+    for name in ("asp_forward", "asp_forward_group"):
+        monkeypatch.setattr(B.lib(), name, lambda *a, name=name: reached.append(name) or 0)
+    for call in (lambda: layer.forward(x), lambda: ASPLinear(layer)(x), lambda: forward_group([layer], x)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    assert not reached

@@ -18,7 +18,8 @@ _Y_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
 def _check_x(x, K, device):
-    """x must be a 2-D (M, K) float32 or bfloat16 tensor on the weights' device."""
+    """x must be a 2-D (M, K) float32 or bfloat16 tensor on the weights' device, a GPU
+    (a kernel given the host's addresses would fault)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch tensor")
     if x.dtype not in (torch.bfloat16, torch.float32):
@@ -29,6 +30,8 @@ def _check_x(x, K, device):
         raise ValueError(f"x is on {x.device}, the layer on {device}")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
+    if x.device.type != "cuda":
+        raise ValueError(f"x and the layer are on {x.device}, not on a GPU")
 
 
 def _check_y(y, M, N, y_dtype, device):
