@@ -277,6 +277,57 @@ def test_calls_on_another_stream():
     assert all(torch.equal(g, want) for g in got)
 
 
+def _busy():
+    """Some milliseconds of work on the current stream."""
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
+    b = torch.empty_like(a)
+    for _ in range(12):
+        torch.mm(a, a, out=b)
+
+
+def test_memory_of_calls_on_another_stream():
+    """The current stream is behind: blocks that it freed are still to be written by it, and a
+    result is still to be read.  Neither may be handed to a call on another stream."""
+    from wam_asp_w4a4_amd.norm import gated_norm, gated_norm_backward
+    M, N, K = 500, 300, 700
+    w, bias = torch.randn((N, K), device=DEV), torch.randn(N, device=DEV)
+    x, x2, dy = (torch.randn((M, k), device=DEV) for k in (K, K, N))
+    layer = Fp8Layer.pack(w, bias)
+
+    def calls(x, stream=None):
+        q = quantize(x, stream=stream)
+        p = Fp8Layer.pack(w, bias, stream=stream)
+        h, n = gated_norm(x, x, post="rms", stream=stream)
+        _, c = gated_norm(x, out="fp8", stream=stream)
+        g = gated_norm_backward(x, x, x, x, post="rms", weight=w[0], stream=stream)
+        return [layer.forward(x, stream=stream), *layer.backward(dy, x, stream=stream), q.codes, q.scales,
+                q.dequantize(stream=stream), p.codes, p.scales, p.codes_t, p.scales_t, h, n, c.codes, c.scales,
+                g.dx, g.dy, g.weight]
+
+    want, want2 = calls(x), calls(x2)
+    torch.cuda.synchronize()
+    side, cur = torch.cuda.Stream(), torch.cuda.current_stream()
+    assert side.cuda_stream != cur.cuda_stream
+    side.wait_stream(cur)
+    _busy()
+    for _ in range(2):
+        trash = [torch.empty_like(t) for t in want for _ in range(2)]
+        for t in trash:
+            t.fill_(3)
+        del trash, t
+    got = calls(x, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # read late, on the current stream, and freed before that
+    _busy()
+    late = [t.clone() for t in got]
+    del got
+    again = calls(x2, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(late, want))
+    assert all(torch.equal(a, b) for a, b in zip(again, want2))
+
+
 def test_the_c_calls_refuse_a_small_workspace():
     layer = Fp8Layer.pack(torch.ones((64, 8192), device=DEV))
     x = torch.ones((64, 8192), device=DEV)

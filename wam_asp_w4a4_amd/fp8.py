@@ -6,6 +6,10 @@ block of 128, for the projections that 4 bits hurt.
 are the format itself (``include/asp.h`` describes its bytes): what
 ``norm.gated_norm`` hands over with ``out="fp8"`` enters ``forward`` as it is.
 All arithmetic happens inside libasp.
+
+Calls run on torch's current stream, or on ``stream`` (a handle): inputs, and outputs
+and workspaces that are given, must be ready for it.  What such a call makes belongs to
+``stream``: the current one waits for it before it reads them.
 """
 
 from __future__ import annotations
@@ -15,21 +19,11 @@ from dataclasses import dataclass
 import torch
 
 from . import binding as B
-from .layer import _Y_DTYPES, _check_ws, _check_y
+from .layer import _Y_DTYPES, _check_ws, _check_y, _lend, _made_for
 
 BLOCK = 128
 _NAMES = {torch.float32: "f32", torch.bfloat16: "bf16"}
 _CODES = {torch.float32: B.ASP_F32, torch.bfloat16: B.ASP_BF16}
-
-
-def _lend(stream, *tensors):
-    """Tensors made here (on torch's current stream) are used on `stream`: the
-    allocator is told, so that their memory is not given away too early."""
-    if stream is None:
-        return
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            t.record_stream(torch.cuda.ExternalStream(stream, t.device))
 
 
 def _no_capture():
@@ -132,9 +126,9 @@ class Fp8Tensor:
         self.check()
         if dtype not in _Y_DTYPES:
             raise ValueError(f"dtype must be 'f32' or 'bf16', not {dtype!r}")
-        out = torch.empty((self.rows, self.cols), dtype=_Y_DTYPES[dtype],
-                          device=self.codes.device)
-        dev = out.device
+        dev = self.codes.device
+        with _made_for(stream, dev):
+            out = torch.empty((self.rows, self.cols), dtype=_Y_DTYPES[dtype], device=dev)
         B.launch(dev, B.lib().asp_fp8_dequantize, self.codes.data_ptr(), self.scales.data_ptr(),
                  self.rows, self.cols, out.data_ptr(), B.DTYPES[dtype], B.stream_on(stream, dev))
         _lend(stream, out)
@@ -149,7 +143,8 @@ def quantize(x, transpose=False, stream=None):
     M, K = x.shape
     dev = x.device
     ld = _check_rows(x, "x", M, K, dev)
-    q = Fp8Tensor.empty(K, M, dev) if transpose else Fp8Tensor.empty(M, K, dev)
+    with _made_for(stream, dev):
+        q = Fp8Tensor.empty(K, M, dev) if transpose else Fp8Tensor.empty(M, K, dev)
     fn = B.lib().asp_fp8_quantize_t if transpose else B.lib().asp_fp8_quantize
     B.launch(dev, fn, x.data_ptr(), _CODES[x.dtype], M, K, ld, q.codes.data_ptr(),
              q.scales.data_ptr(), B.stream_on(stream, dev))
@@ -179,8 +174,9 @@ class Fp8Layer:
         ld = _check_rows(w, "w", N, K, dev)
         if bias is not None:
             _check_vector(bias, "bias", N, w.device)
-        q = Fp8Tensor.empty(N, K, dev)
-        t = Fp8Tensor.empty(K, N, dev) if backward else None
+        with _made_for(stream, dev):
+            q = Fp8Tensor.empty(N, K, dev)
+            t = Fp8Tensor.empty(K, N, dev) if backward else None
         ct, st = (t.codes, t.scales) if backward else (None, None)
         B.launch(dev, B.lib().asp_fp8_quantize_weight, w.data_ptr(), _CODES[w.dtype], N, K, ld,
                  q.codes.data_ptr(), q.scales.data_ptr(), B._at(ct), B._at(st),
@@ -226,19 +222,19 @@ class Fp8Layer:
             ld = _check_rows(x, "x", None, K, dev)
             M, y_dtype = x.shape[0], y_dtype or _NAMES[x.dtype]
             need = B.asp_fp8_workspace_bytes(M, N, K)
-        made = []
+        made = None
         if y is not None or y_dtype not in _Y_DTYPES:
             _check_y(y, M, N, y_dtype, dev)
         else:
-            y = torch.empty((M, N), dtype=_Y_DTYPES[y_dtype], device=dev)
-            made.append(y)
+            with _made_for(stream, dev):
+                made = y = torch.empty((M, N), dtype=_Y_DTYPES[y_dtype], device=dev)
         have, ws = need, None
         if workspace is not None:
             _check_ws(workspace, need, dev)
             have, ws = workspace.numel(), workspace.data_ptr()
         elif need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            made.append(workspace)
+            with _made_for(stream, dev):
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             ws = workspace.data_ptr()
         bias = self.bias
         bias = None if bias is None else bias.data_ptr()
@@ -249,8 +245,7 @@ class Fp8Layer:
         else:
             B.launch(dev, B.lib().asp_fp8_forward, x.data_ptr(), _CODES[x.dtype], ld, M, N, K, wc,
                      wsc, bias, y.data_ptr(), B.DTYPES[y_dtype], ws, have, to)
-        if stream is not None:
-            _lend(stream, *made)
+        _lend(stream, made)
         return y
 
     def backward(self, dy, x=None, need_dx=True, need_db=None, dw_dtype="f32", workspace=None,
@@ -267,28 +262,23 @@ class Fp8Layer:
             raise ValueError(f"dw_dtype must be 'f32' or 'bf16', not {dw_dtype!r}")
         if need_dx and self.codes_t is None:
             raise ValueError("dx needs the transposed weight: pack the layer with backward=True")
-        made = []
-
-        def new(shape, dtype):
-            made.append(torch.empty(shape, dtype=dtype, device=dev))
-            return made[-1]
-
         if need_db is None:
             need_db = self.bias is not None
-        dx = new((M, K), dy.dtype) if need_dx else None
-        dw = new((N, K), _Y_DTYPES[dw_dtype]) if x is not None else None
-        db = new((N,), torch.float32) if need_db else None
-        if not made:
+        if not need_dx and x is None and not need_db:
             return None, None, None
         need = B.asp_fp8_backward_workspace_bytes(M, N, K)
         if workspace is not None:
             _check_ws(workspace, need, dev)
-        else:
-            workspace = new((need,), torch.uint8)
+        with _made_for(stream, dev):
+            dx = torch.empty((M, K), dtype=dy.dtype, device=dev) if need_dx else None
+            dw = None if x is None else torch.empty((N, K), dtype=_Y_DTYPES[dw_dtype], device=dev)
+            db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
+            if workspace is None:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         at, code = B._at, _CODES[dy.dtype]
         B.launch(dev, B.lib().asp_fp8_backward, dy.data_ptr(), code, lddy, at(x),
                  B.ASP_F32 if x is None else _CODES[x.dtype], ldx, M, N, K, at(self.codes_t),
                  at(self.scales_t), at(dx), code, at(dw), B.DTYPES[dw_dtype], at(db),
                  workspace.data_ptr(), workspace.numel(), B.stream_on(stream, dev))
-        _lend(stream, *made)
+        _lend(stream, dx, dw, db)
         return dx, dw, db

@@ -7,6 +7,7 @@ torch and calls ``asp_forward``.  All arithmetic happens inside libasp.
 
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import numpy as np
@@ -15,6 +16,27 @@ import torch
 from . import binding as B
 
 _Y_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+_HERE = nullcontext()
+
+
+def _made_for(stream, device):
+    """The context in which tensors for a call on the stream handle `stream` are made.
+    They come from that stream's memory: a block of the current stream's may still have
+    work pending there, which the call's stream does not wait for."""
+    if stream is None or device.type != "cuda" \
+            or stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return _HERE
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device))
+
+
+def _lend(stream, *tensors):
+    """Results made for a call on `stream` will be used on the current stream too: the
+    allocator is told, so that their memory is not given away too early."""
+    if stream is None:
+        return
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(torch.cuda.current_stream(t.device))
 
 
 def _check_x(x, K, device):

@@ -18,9 +18,8 @@ from typing import NamedTuple
 import torch
 
 from . import binding as B
-from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _lend, _no_capture, \
-    _row_major
-from .layer import _Y_DTYPES, _check_ws
+from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _no_capture, _row_major
+from .layer import _Y_DTYPES, _check_ws, _lend, _made_for
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
 
@@ -94,7 +93,8 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     rows of no sequence are left as they are in h and n where given, and are zeros in
     tensors made here.  out: 'f32', 'bf16' (None: x's type)
     or 'fp8' for an ``Fp8Tensor``.  h, n: tensors to write (h may be x or y); without
-    y and with alpha 1, h is x itself and not written unless given."""
+    y and with alpha 1, h is x itself and not written unless given.  stream: as in
+    ``fp8``, for which everything given must be ready."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D torch tensor")
     M, C = x.shape
@@ -105,13 +105,15 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     post, pre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
                               scale, shift, offsets)
     made, zero = [], 0   # bits of the outputs made here: h, n
+    own = _made_for(stream, dev)
     write, ldh = h, C
     if h is not None:
         ldh = _check_rows(h, "h", M, C, dev, same)
     elif y is None and alpha == 1.0 and pre:
         h = x
     else:
-        write = h = torch.empty((M, C), dtype=x.dtype, device=dev)
+        with own:
+            write = h = torch.empty((M, C), dtype=x.dtype, device=dev)
         made.append(h)
         zero = 1
     scales = None
@@ -123,7 +125,8 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         if out not in (None, "fp8"):
             raise ValueError(f"out {out!r} with an Fp8Tensor n")
         if n is None:
-            n = Fp8Tensor.empty(M, C, dev)
+            with own:
+                n = Fp8Tensor.empty(M, C, dev)
             made += [n.codes, n.scales]
             zero |= 2
         else:
@@ -138,7 +141,8 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
             raise ValueError(f"out must be 'f32', 'bf16' or 'fp8', not {out!r}")
         ldn = C
         if n is None:
-            n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
+            with own:
+                n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
             made.append(n)
             zero |= 2
         else:
@@ -182,8 +186,11 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         raise ValueError("neither dh nor dn is given")
     made, zero = [], 0   # bits of the outputs made here: dx, dy
 
+    own = _made_for(stream, dev)
+
     def new(shape, dtype=torch.float32):
-        made.append(torch.empty(shape, dtype=dtype, device=dev))
+        with own:
+            made.append(torch.empty(shape, dtype=dtype, device=dev))
         return made[-1]
 
     def like(*inputs):
@@ -213,7 +220,8 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     if not (post_weight is weight is bias is gate is scale is shift is None):
         need = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
         if workspace is None:
-            workspace = new((need,), torch.uint8)
+            with own:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     if workspace is not None:
         _check_ws(workspace, need, dev)
     at = B._at
