@@ -1,0 +1,59 @@
+"""The 4-bit layers and the basis solve on a stream that is not torch's current one: the
+memory of what they make, while the current stream is behind."""
+
+import numpy as np
+import pytest
+import torch
+
+from wam_asp_w4a4_amd import synth
+from wam_asp_w4a4_amd.layer import PackedLayer, SvdqLayer, forward_group, top_eigenspace
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _busy():
+    """Some milliseconds of work on the current stream."""
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
+    b = torch.empty_like(a)
+    for _ in range(12):
+        torch.mm(a, a, out=b)
+
+
+def test_memory_of_calls_on_another_stream():
+    """Blocks that the current stream freed are still to be written by it, and a result is
+    still to be read.  Neither may be handed to a call on another stream."""
+    lay = synth.make_layer("s", 80, 256, 384, 32, seed=1, dtype="f32")
+    packed = [PackedLayer.pack(lay.w, lay.s, lay.v, b, DEV) for b in (lay.b, None)]
+    int4 = SvdqLayer.pack_host(lay.w, lay.s, 0, None).to(DEV)
+    a = torch.randn((256, 256), device=DEV)
+    g, v0 = a @ a.t() / 256, torch.randn((256, 16), device=DEV)
+    x = torch.from_numpy(np.ascontiguousarray(lay.x)).to(DEV)
+    x2 = torch.randn_like(x)
+
+    def calls(x, stream=None):
+        return [packed[0].forward(x, stream=stream), packed[0].forward(x, "bf16", stream=stream),
+                *forward_group(packed, x, stream=stream), int4.forward(x, stream=stream),
+                *top_eigenspace(g, v0, 8, 4, stream=stream)]
+
+    want, want2 = calls(x), calls(x2)
+    torch.cuda.synchronize()
+    side, cur = torch.cuda.Stream(), torch.cuda.current_stream()
+    assert side.cuda_stream != cur.cuda_stream
+    side.wait_stream(cur)
+    _busy()
+    trash = [torch.empty_like(t) for t in want for _ in range(2)]
+    for t in trash:
+        t.fill_(3)
+    del trash, t
+    got = calls(x, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # read late, on the current stream, and freed before that
+    _busy()
+    late = [t.clone() for t in got]
+    del got
+    again = calls(x2, side.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(late, want))
+    assert all(torch.equal(a, b) for a, b in zip(again, want2))

@@ -153,19 +153,23 @@ class PackedLayer:
                 stream=None) -> torch.Tensor:
         """y = the layer applied to x (M x K, float32 or bfloat16, on the layer's
         device); y_dtype 'f32' or 'bf16'.  Shapes, dtypes and devices are
-        checked here: the C ABI sees only pointers."""
+        checked here: the C ABI sees only pointers.  stream: a handle to run on (None:
+        torch's current one), for which everything given must be ready."""
         _check_x(x, self.K, self.device)
         M = x.shape[0]
         _check_y(y, M, self.N, y_dtype, self.device)
         x_dtype = B.ASP_BF16 if x.dtype == torch.bfloat16 else B.ASP_F32
-        if y is None:
-            y = torch.empty((M, self.N), device=x.device, dtype=_Y_DTYPES[y_dtype])
+        made = y is None
+        with _made_for(stream, self.device):
+            if made:
+                y = torch.empty((M, self.N), device=x.device, dtype=_Y_DTYPES[y_dtype])
+            ws = self.workspace(M) if workspace is None else workspace
         need = B.asp_workspace_bytes(M, self.N, self.K, self.r)
-        ws = self.workspace(M) if workspace is None else workspace
         _check_ws(ws, need, self.device)
         B.asp_forward(x, x_dtype, M, self.N, self.K, self.r, self.prep, self.w_codes,
                       self.w_scales, self.wv, self.bias, y, B.DTYPES[y_dtype], ws, ws.numel(),
                       stream)
+        _lend(stream, y if made else None)
         return y
 
 
@@ -180,15 +184,18 @@ def forward_group(layers, x, y_dtype: str = "f32", workspaces=None, ys=None, str
     _check_x(x, K, layers[0].device)
     M = x.shape[0]
     x_dtype = B.ASP_BF16 if x.dtype == torch.bfloat16 else B.ASP_F32
-    if ys is None:
-        ys = [torch.empty((M, l.N), device=x.device, dtype=_Y_DTYPES.get(y_dtype, torch.float32))
-              for l in layers]
+    made = ys is None
+    if made:
+        with _made_for(stream, x.device):
+            ys = [torch.empty((M, l.N), device=x.device,
+                              dtype=_Y_DTYPES.get(y_dtype, torch.float32)) for l in layers]
     if len(ys) != len(layers):
         raise ValueError("one y per layer")
     for l, y in zip(layers, ys):
         _check_y(y, M, l.N, y_dtype, l.device)
     if workspaces is None:
-        workspaces = [l.workspace(M) for l in layers]
+        with _made_for(stream, x.device):
+            workspaces = [l.workspace(M) for l in layers]
     if len(workspaces) != len(layers):
         raise ValueError("one workspace per layer")
     for l, w in zip(layers, workspaces):
@@ -198,6 +205,8 @@ def forward_group(layers, x, y_dtype: str = "f32", workspaces=None, ys=None, str
                         [l.wv for l in layers] if r else None,
                         [l.bias for l in layers], [l.N for l in layers], ys, B.DTYPES[y_dtype],
                         workspaces, [w.numel() for w in workspaces], stream)
+    if made:
+        _lend(stream, *ys)
     return ys
 
 
@@ -217,7 +226,8 @@ def smoothing_search(x, w, bias, v, candidates=None, stream=None):
     r = 0 if v is None else v.shape[1]
     x_dtype = B.ASP_BF16 if x.dtype == torch.bfloat16 else B.ASP_F32
     nbytes = B.asp_smoothing_search_workspace_bytes(M, N, K, r, len(cands))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    with _made_for(stream, x.device):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     mse, best = B.asp_smoothing_search(x, x_dtype, M, K, w, bias, N, v, r,
                                        [a for a, _ in cands], [b for _, b in cands], ws,
                                        nbytes, stream)
@@ -233,12 +243,14 @@ def top_eigenspace(g, v0, r, iters, workspace=None, stream=None):
     if tuple(g.shape) != (K, K):
         raise ValueError("g must be K x K with K = v0.shape[0]")
     nbytes = B.asp_top_eigenspace_workspace_bytes(K, p, r)
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
-    v = torch.empty((K, r), dtype=torch.float32, device=g.device)
-    evals = torch.empty(r, dtype=torch.float32, device=g.device)
-    resid = torch.empty(r, dtype=torch.float32, device=g.device)
+    with _made_for(stream, g.device):
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        v = torch.empty((K, r), dtype=torch.float32, device=g.device)
+        evals = torch.empty(r, dtype=torch.float32, device=g.device)
+        resid = torch.empty(r, dtype=torch.float32, device=g.device)
     B.asp_top_eigenspace(g, K, v0, p, r, iters, v, evals, resid, workspace, nbytes, stream)
+    _lend(stream, v, evals, resid)
     return v, evals, resid
 
 
@@ -319,12 +331,15 @@ class SvdqLayer:
         _check_y(y, M, self.N, y_dtype, dev)
         x_dtype = B.ASP_BF16 if x.dtype == torch.bfloat16 else B.ASP_F32
         nbytes = B.asp_svdq_workspace_bytes(M, self.N, self.K, self.r)
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        made = y is None
+        with _made_for(stream, dev):
+            if workspace is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+            if made:
+                y = torch.empty((M, self.N), dtype=_Y_DTYPES[y_dtype], device=x.device)
         _check_ws(workspace, nbytes, dev)
-        if y is None:
-            y = torch.empty((M, self.N), dtype=_Y_DTYPES[y_dtype], device=x.device)
         B.asp_svdq_forward(x, x_dtype, M, self.K, self.r, self.prep, self.codes, self.scales,
                            self.l1 if self.r else None, self.bias, self.N, y, B.DTYPES[y_dtype],
                            workspace, nbytes, stream)
+        _lend(stream, y if made else None)
         return y
