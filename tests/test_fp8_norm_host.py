@@ -252,3 +252,16 @@ def test_install_takes_either_kind():
         Fp8Linear()
     with pytest.raises(ValueError):
         Fp8Linear(layer(), bias=torch.zeros(64))
+
+
+@pytest.mark.parametrize("xs,ys,fits", [((4, 96), (8, 48), False), ((4, 96), (96, 4), False), ((4, 96), (384,), False),
+                                        ((2, 6, 96), (3, 4, 96), False), ((2, 6, 96), (6, 2, 96), False),
+                                        ((4, 96), (1, 96), False), ((2, 6, 96), (2, 1, 96), False),
+                                        ((4, 96), (4, 96), True), ((2, 6, 96), (12, 96), True),
+                                        ((12, 96), (3, 4, 96), True), ((96,), (1, 96), True)])
+def test_module_takes_a_y_of_the_streams_rows_only(xs, ys, fits):
+    """What fits gets as far as the refusal of CPU tensors."""
+    m = norm.GatedNorm(96, post="rms")
+    for frozen in (False, True):
+        with pytest.raises(ValueError, match="GPU" if fits else "y must have the shape"):
+            m.requires_grad_(not frozen)(torch.zeros(xs), torch.zeros(ys))

@@ -265,10 +265,10 @@ class _GatedNorm(torch.autograd.Function):
 class GatedNorm(torch.nn.Module):
     """``gated_norm`` with its weights as parameters, differentiable in every input.
 
-    x, y: (..., C); gate, scale, shift: (G, C) or (C), taken as float32 like the weights;
-    returns (h, n) of x's shape
-    (n None for pre 'none'; rows of no sequence are zeros; without gradients, y and a
-    factor alpha, h is x itself).  Under a HIP graph capture, gradients are refused: capture
+    x, y: (..., C) of one shape, or either as its rows (M, C); gate, scale, shift: (G, C) or
+    (C), taken as float32 like the weights; returns (h, n) of x's shape (n None for pre
+    'none'; rows of no sequence are zeros; without gradients, y and a factor alpha, h is x
+    itself).  Under a HIP graph capture, gradients are refused: capture
     ``gated_norm`` and ``gated_norm_backward``, which keep no graph of their own."""
 
     def __init__(self, channels, post="none", pre="rms", alpha=1.0, eps=1e-6, device=None):
@@ -289,6 +289,11 @@ class GatedNorm(torch.nn.Module):
             raise ValueError(f"x has {x.shape[-1]} channels, the norm {self.channels}")
         if y is None and self.post != "none":
             raise ValueError("a post norm needs y")
+        if y is not None and y.shape != x.shape and not (
+                2 in (x.dim(), y.dim()) and y.shape[-1] == self.channels
+                and y.numel() == x.numel()):
+            raise ValueError(f"y must have the shape of x or of its rows, {tuple(x.shape)}, "
+                             f"got {tuple(y.shape)}")
         flat = [None if t is None else _row_major(t.reshape(-1, self.channels)) for t in (x, y)]
         post_weight, weight, bias, gate, scale, shift = map(
             _float32, (self.post_weight, self.weight, self.bias, gate, scale, shift))
