@@ -4,6 +4,7 @@ the modules that hold them."""
 
 import pytest
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from wam_asp_w4a4_amd import binding as B
 from wam_asp_w4a4_amd import fp8, norm
@@ -265,3 +266,28 @@ def test_module_takes_a_y_of_the_streams_rows_only(xs, ys, fits):
     for frozen in (False, True):
         with pytest.raises(ValueError, match="GPU" if fits else "y must have the shape"):
             m.requires_grad_(not frozen)(torch.zeros(xs), torch.zeros(ys))
+
+
+@pytest.mark.parametrize("frozen", [False, True])
+def test_forward_mode_is_refused(frozen, monkeypatch):
+    """The library's calls are replaced: a tangent must not get that far, wherever it rides."""
+    monkeypatch.setattr(B, "launch", lambda *a: None)
+    m = norm.GatedNorm(200, post="rms", pre="layer").requires_grad_(not frozen)
+    packed = Fp8Linear(layer())
+    trained = Fp8Linear.from_linear(torch.nn.Linear(200, 64), trainable=True).requires_grad_(not frozen)
+    x, table = torch.ones((6, 200)), torch.ones(200)
+    with forward_ad.dual_level():
+        dx, dt = (forward_ad.make_dual(t, t.clone()) for t in (x, table))
+        weight = forward_ad.make_dual(trained.weight.detach(), torch.ones((64, 200)))
+        calls = [lambda: m(dx, x), lambda: m(x, dx), lambda: m(x, x, gate=dt), lambda: m(x, x, shift=dt),
+                 lambda: packed(dx), lambda: trained(dx),
+                 lambda: torch.func.functional_call(m, {"weight": dt}, (x, x)),
+                 lambda: torch.func.functional_call(trained, {"weight": weight}, (x,))]
+        for i, call in enumerate(calls):
+            with pytest.raises(RuntimeError, match="forward-mode"):
+                call()
+                print("no error:", i)
+        for m_, args in ((m, (x, x)), (packed, (x,)), (trained, (x,))):
+            m_(*args)                         # none of its tensors has a tangent
+    with pytest.raises(RuntimeError, match="forward-mode"):
+        torch.func.jvp(packed, (x,), (x,))

@@ -17,6 +17,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 from .layer import _Y_DTYPES, _check_ws, _check_y, _lend, _made_for
@@ -31,6 +32,13 @@ def _no_capture():
     if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("gradients under a graph capture: capture the explicit forward and "
                            "backward calls instead of autograd")
+
+
+def _no_forward_mode(*tensors):
+    """The modules' derivatives are reverse mode: a tangent would be lost without a word."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError("no forward-mode derivative: the layer's gradients are reverse mode only")
 
 
 def _stride(t):

@@ -24,7 +24,7 @@ from typing import Mapping
 
 import torch
 
-from .fp8 import _NAMES, Fp8Layer, _float32, _no_capture, _row_major
+from .fp8 import _NAMES, Fp8Layer, _float32, _no_capture, _no_forward_mode, _row_major
 from .layer import PackedLayer
 
 
@@ -98,9 +98,10 @@ class Fp8Linear(torch.nn.Module):
     Around a packed ``Fp8Layer`` the weight is frozen, and x (and a bias that requires
     it) has a gradient.  With ``weight`` (N x K, float32 or bf16, a parameter) every
     forward packs the weight as it stands, and it has a gradient too: training in
-    8-bit products with the optimiser's weight kept in its own type.  Under a HIP
-    graph capture, gradients are refused: capture ``Fp8Layer.forward`` and
-    ``backward``, which keep no graph of their own."""
+    8-bit products with the optimiser's weight kept in its own type.  Gradients are
+    reverse mode; forward-mode tangents are refused.  Under a HIP graph capture, gradients
+    are refused: capture ``Fp8Layer.forward`` and ``backward``, which keep no graph of
+    their own."""
 
     def __init__(self, packed: Fp8Layer | None = None, weight=None, bias=None):
         super().__init__()
@@ -129,6 +130,7 @@ class Fp8Linear(torch.nn.Module):
             raise ValueError(f"x has {x.shape[-1]} features, the layer {self.in_features}")
         x2 = _row_major(x.reshape(-1, self.in_features))
         leaves = (x2, self.weight, self.bias)
+        _no_forward_mode(*leaves)
         grads = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in leaves)
         if grads:
             _no_capture()

@@ -18,7 +18,8 @@ from typing import NamedTuple
 import torch
 
 from . import binding as B
-from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _no_capture, _row_major
+from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _no_capture, \
+    _no_forward_mode, _row_major
 from .layer import _Y_DTYPES, _check_ws, _lend, _made_for
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
@@ -268,8 +269,9 @@ class GatedNorm(torch.nn.Module):
     x, y: (..., C) of one shape, or either as its rows (M, C); gate, scale, shift: (G, C) or
     (C), taken as float32 like the weights; returns (h, n) of x's shape (n None for pre
     'none'; rows of no sequence are zeros; without gradients, y and a factor alpha, h is x
-    itself).  Under a HIP graph capture, gradients are refused: capture
-    ``gated_norm`` and ``gated_norm_backward``, which keep no graph of their own."""
+    itself).  Gradients are reverse mode; forward-mode tangents are refused.  Under a HIP
+    graph capture, gradients are refused: capture ``gated_norm`` and
+    ``gated_norm_backward``, which keep no graph of their own."""
 
     def __init__(self, channels, post="none", pre="rms", alpha=1.0, eps=1e-6, device=None):
         super().__init__()
@@ -303,6 +305,7 @@ class GatedNorm(torch.nn.Module):
         options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps,
                        offsets=offsets)
         tensors = (post_weight, gate, weight, bias, scale, shift)
+        _no_forward_mode(*flat, *tensors)
         if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                            for t in (*flat, *tensors)):
             _no_capture()
