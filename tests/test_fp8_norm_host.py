@@ -2,6 +2,8 @@
 kernel; pointers that reach the C ABI are fake and rejected before any use), and
 the modules that hold them."""
 
+import ctypes
+
 import pytest
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -291,3 +293,36 @@ def test_forward_mode_is_refused(frozen, monkeypatch):
             m_(*args)                         # none of its tensors has a tangent
     with pytest.raises(RuntimeError, match="forward-mode"):
         torch.func.jvp(packed, (x,), (x,))
+
+
+def test_a_bias_that_was_converted_is_not_read_as_float32(monkeypatch):
+    """A bias parameter follows the module's type; the kernels read float32 of N entries."""
+    seen = []
+
+    def launch(device, fn, x, dtype, ld, M, N, K, codes, scales, bias, *rest):
+        seen.append((bias, [] if bias is None else list((ctypes.c_float * N).from_address(bias))))
+
+    monkeypatch.setattr(B, "launch", launch)
+    l = layer(bias=False)
+    l = fp8.Fp8Layer(l.N, l.K, l.codes, l.scales, l.codes_t, l.scales_t, torch.nn.Parameter(torch.arange(64.0)))
+    m, x = Fp8Linear(l), torch.zeros((4, 200))
+    values = list(range(64))
+    m(x)
+    assert seen[-1] == (l.bias.data_ptr(), values)
+    m.bfloat16()
+    assert l.bias.dtype == torch.bfloat16
+    with pytest.raises(TypeError, match="bias must be a float32 tensor"):
+        l.forward(x)
+    for grad in (True, False):                 # the module uses its values
+        m.bias.requires_grad_(grad)
+        m(x)
+        assert seen[-1][1] == values
+    m.bias = torch.nn.Parameter(torch.ones(64))     # another one in its place
+    m(x)
+    assert seen[-1] == (m.bias.data_ptr(), [1.0] * 64)
+    m.bias = None
+    m(x)
+    assert seen[-1][0] is None
+    m.bias = torch.nn.Parameter(torch.ones(64, device="meta"))
+    with pytest.raises(ValueError, match="bias"):
+        m(x)

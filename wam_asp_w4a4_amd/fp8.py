@@ -245,7 +245,9 @@ class Fp8Layer:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             ws = workspace.data_ptr()
         bias = self.bias
-        bias = None if bias is None else bias.data_ptr()
+        if bias is not None:   # a parameter may have been converted since it was checked
+            _check_vector(bias, "bias", N, dev)
+            bias = bias.data_ptr()
         wc, wsc, to = self.codes.data_ptr(), self.scales.data_ptr(), B.stream_on(stream, dev)
         if quantised:
             B.launch(dev, B.lib().asp_fp8_gemm, x.codes.data_ptr(), x.scales.data_ptr(), wc, wsc, M,

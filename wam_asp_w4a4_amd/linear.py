@@ -20,6 +20,7 @@ All arithmetic runs in libasp; this module only reshapes and dispatches.
 
 from __future__ import annotations
 
+from dataclasses import replace
 from typing import Mapping
 
 import torch
@@ -138,6 +139,8 @@ class Fp8Linear(torch.nn.Module):
         if layer is None:
             bias = None if self.bias is None else _float32(self.bias.detach())
             layer = Fp8Layer.pack(self.weight.detach(), bias, backward=grads and x2.requires_grad)
+        elif self.bias is not layer.bias or self.bias is not None and self.bias.dtype != torch.float32:
+            layer = replace(layer, bias=None if self.bias is None else _float32(self.bias.detach()))
         if grads:
             y = _Fp8Apply.apply(x2, self.weight, self.bias, layer)
         else:
