@@ -326,3 +326,17 @@ def test_a_bias_that_was_converted_is_not_read_as_float32(monkeypatch):
     m.bias = torch.nn.Parameter(torch.ones(64, device="meta"))
     with pytest.raises(ValueError, match="bias"):
         m(x)
+
+
+def test_offsets_changed_before_the_backward_are_noticed(monkeypatch):
+    monkeypatch.setattr(B, "launch", lambda *a: None)
+    m = norm.GatedNorm(32)
+    off = torch.tensor([0, 3, 6], dtype=torch.int32)
+    for change in (False, True):
+        n = m(torch.zeros((6, 32)), offsets=off)[1]
+        if change:
+            off[1] = 4                      # the next batch's, in the same buffer
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                n.sum().backward()
+        else:
+            n.sum().backward()

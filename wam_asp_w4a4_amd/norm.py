@@ -238,16 +238,16 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
 
 class _GatedNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, options):
+    def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, offsets, options):
         given = dict(post_weight=post_weight, gate=gate, weight=weight, bias=bias, scale=scale,
                      shift=shift)
         h = None
         if y is None and options["alpha"] == 1.0:
             # written all the same: a stream returned as it came would share its version
-            make = torch.empty if options["offsets"] is None else torch.zeros
+            make = torch.empty if offsets is None else torch.zeros
             h = make(x.shape, dtype=x.dtype, device=x.device)
-        h, n = gated_norm(x, y, h=h, **given, **options)
-        ctx.save_for_backward(h, y, *given.values())
+        h, n = gated_norm(x, y, h=h, offsets=offsets, **given, **options)
+        ctx.save_for_backward(h, y, *given.values(), offsets)
         ctx.options = options
         return h, n
 
@@ -255,12 +255,12 @@ class _GatedNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dn):
         _no_capture()
-        h, y, post_weight, gate, weight, bias, scale, shift = ctx.saved_tensors
+        h, y, post_weight, gate, weight, bias, scale, shift, offsets = ctx.saved_tensors
         g = gated_norm_backward(None if dh is None else dh.contiguous(),
                                 None if dn is None else dn.contiguous(), h, y,
                                 post_weight=post_weight, gate=gate, weight=weight, bias=bias,
-                                scale=scale, shift=shift, **ctx.options)
-        return (*g, None)
+                                scale=scale, shift=shift, offsets=offsets, **ctx.options)
+        return (*g, None, None)
 
 
 class GatedNorm(torch.nn.Module):
@@ -302,17 +302,16 @@ class GatedNorm(torch.nn.Module):
         tables = [t for t in (gate, scale, shift) if t is not None]
         if len({(t.dim(), t.stride()) for t in tables}) > 1 or any(_row_major(t) is not t for t in tables):
             gate, scale, shift = (None if t is None else t.contiguous() for t in (gate, scale, shift))
-        options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps,
-                       offsets=offsets)
+        options = dict(post=self.post, pre=self.pre, alpha=self.alpha, eps=self.eps)
         tensors = (post_weight, gate, weight, bias, scale, shift)
         _no_forward_mode(*flat, *tensors)
         if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                            for t in (*flat, *tensors)):
             _no_capture()
-            h, n = _GatedNorm.apply(*flat, *tensors, options)
+            h, n = _GatedNorm.apply(*flat, *tensors, offsets, options)
         else:
             names = ("post_weight", "gate", "weight", "bias", "scale", "shift")
-            h, n = gated_norm(*flat, **dict(zip(names, tensors)), **options)
+            h, n = gated_norm(*flat, **dict(zip(names, tensors)), offsets=offsets, **options)
         return h.reshape(x.shape), None if n is None else n.reshape(x.shape)
 
     def extra_repr(self) -> str:
