@@ -572,9 +572,9 @@ int32_t asp_fp8_forward(const void* x, int32_t x_dtype, int64_t ldx, int64_t M, 
  *   dx (M x K) = Q(dy) W                  blocks of dy along N
  *   dw (N x K) = Qt(dy)^T Qt(x)           blocks of both along M
  *   db (N)     = the sum of dy's rows, float32
- * Each of dx, dw, db may be NULL: it is not computed, and x is read for dw alone,
- * wt_codes and wt_scales (the transposed weight) for dx alone.  M == 0 gives
- * zero dw and db.
+ * Each of dx, dw, db may be NULL: it is not computed, which does not change the bits
+ * of the others, and x is read for dw alone, wt_codes and wt_scales (the transposed
+ * weight) for dx alone.  M == 0 gives zero dw and db.
  */
 int32_t asp_fp8_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x,

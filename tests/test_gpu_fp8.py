@@ -196,6 +196,27 @@ def test_gradients_against_the_oracle(M, N, K, dtype):
     assert three[0] is three[1] is None and torch.equal(three[2], db)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 1024), (16, 14336, 4096), (3, 130, 200), (20000, 16, 1300), (5000, 9, 70),
+                                   (256, 1024, 1024), (700, 2000, 1300)])
+def test_each_gradient_alone_has_the_same_bits(M, N, K, dtype):
+    """Which kernel a product takes depends on its own sizes, not on what else is asked for."""
+    print(f"alone {M}x{N}x{K} {dtype}", flush=True)
+    torch.manual_seed(M + N + K)
+    layer = Fp8Layer.pack(torch.randn((N, K), device=DEV), torch.zeros(N, device=DEV))
+    x, dy = torch.randn((M, K), device=DEV).to(TYPES[dtype]), torch.randn((M, N), device=DEV).to(TYPES[dtype])
+    for dw_dtype in ("f32", "bf16"):
+        dx, dw, db = layer.backward(dy, x, dw_dtype=dw_dtype)
+        for need_dx, need_dw, need_db in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1), (1, 1, 0)):
+            got = layer.backward(dy, x if need_dw else None, need_dx=need_dx, need_db=need_db, dw_dtype=dw_dtype)
+            for name, g, want, need in zip(("dx", "dw", "db"), got, (dx, dw, db), (need_dx, need_dw, need_db)):
+                assert (g is not None) == bool(need)
+                assert g is None or torch.equal(g, want), (name, dw_dtype, need_dx, need_dw, need_db)
+    if M > 16:     # above the few-row kernel's rows, the product of the same operands
+        back = Fp8Layer(K, N, layer.codes_t, layer.scales_t, None, None, None)
+        assert torch.equal(back.forward(quantize(dy), dtype), dx)
+
+
 def test_gradients_against_differences():
     """Whole numbers: the layer is linear in them, so differences are exact."""
     rng = np.random.default_rng(5)

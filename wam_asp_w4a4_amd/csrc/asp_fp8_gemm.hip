@@ -734,8 +734,8 @@ __global__ void __launch_bounds__(256) k_fp8_colsum(const ColSum c) {
   column_sums(c, blockIdx.x, lds);
 }
 
-// k_fp8_back: what a small layer's backward computes from the quantised operands, in one
-// launch: g[0]'s tiles (count[0] workgroups), g[1]'s, then the column sums.  Each alone
+// k_fp8_back: the small products of a layer's backward and its column sums, in one
+// launch: g[0]'s tiles (count[0] workgroups), g[1]'s, then the sums.  Each alone
 // is a few microseconds of latency on part of the CUs: 256 x 1024 x 1024, the whole
 // backward, 17.8 us with a launch for each, 13.5 so.
 struct BackK {
@@ -916,7 +916,10 @@ int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
 
 namespace {
 
-// Latency-bound products, which share a launch with others (k_fp8_back).
+// Latency-bound products, which share a launch with others (k_fp8_back): the backward asks
+// this of each by itself, so that a gradient's bits do not depend on which others are
+// wanted.  Up to kFewRows rows too: k_fp8_few would be a launch beside the column sums'
+// (dx and db of 16 x 14336 x 4096: 18.3 us, with it 24.7; 1 x 4096 x 1024: 10.1 and 11.6).
 bool small(const Fp8Gemm& g) {
   const Plan p = plan(g.M, g.N, g.K, g.y_dtype != ASP_BF16);
   return p.slices == 1 && (p.kernel == kMid || p.kernel == kTiles64);
@@ -1111,12 +1114,16 @@ int32_t asp_fp8_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const v
   if (dw)
     g[n++] = {base + L.dytc, base + L.dyts, base + L.xtc, base + L.xts, N, K, M, nullptr,
               dw, dw_dtype, base + L.gemm};
-  if (n > 0 && small(g[0]) && small(g[n - 1])) return launch_back(n, g, sums, st);
-  if (db) {
+  Fp8Gemm joint[2], alone[2];
+  int nj = 0, na = 0;
+  for (int i = 0; i < n; ++i) (small(g[i]) ? joint[nj++] : alone[na++]) = g[i];
+  if (nj > 0) {
+    ASP_TRY(launch_back(nj, joint, sums, st));
+  } else if (db) {
     k_fp8_colsum<<<dim3((unsigned)((N + 15) / 16)), 256, 0, st>>>(sums);
     ASP_TRY(launch_status("fp8 column sums"));
   }
-  for (int i = 0; i < n; ++i) ASP_TRY(fp8_gemm_impl(g[i], st));
+  for (int i = 0; i < na; ++i) ASP_TRY(fp8_gemm_impl(alone[i], st));
   return ASP_OK;
 }
 
