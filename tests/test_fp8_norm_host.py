@@ -340,3 +340,52 @@ def test_offsets_changed_before_the_backward_are_noticed(monkeypatch):
                 n.sum().backward()
         else:
             n.sum().backward()
+
+
+BACKWARD_ARGS = ("dh lddh dn lddn dn_dtype h ldh y ldy dtype M C alpha post post_weight_in gate_in pre weight_in bias_in "
+                 "scale_in ldt G offsets eps dx lddx dy lddy zero post_weight gate weight bias scale shift ldd ws "
+                 "ws_bytes stream").split()
+
+
+@pytest.mark.parametrize("used", ["h and n", "h", "n"])
+@pytest.mark.parametrize("trained", [("x",), ("y",), ("x", "y", "weight"), ("gate",), ("y", "shift"), ("post_weight",)])
+def test_backward_asks_the_library_for_the_wanted_gradients_only(trained, used, monkeypatch):
+    """By the pointers that the call passes: NULL for what nobody wants, and for a result
+    that nothing uses."""
+    calls = []
+    monkeypatch.setattr(B, "launch", lambda device, fn, *args: calls.append(args))
+    m = norm.GatedNorm(32, post="rms", pre="layer").requires_grad_(False)
+    t = {"x": torch.ones((6, 32)), "y": torch.ones((6, 32)), "gate": torch.ones(32), "scale": torch.ones(32),
+         "shift": torch.ones(32)}
+    for name in trained:
+        (t[name] if name in t else getattr(m, name)).requires_grad_()
+    h, n = m(**t)
+    wanted = [t[name] if name in t else getattr(m, name) for name in trained]
+    loss = {"h and n": (h, n), "h": (h,), "n": (n,)}[used]
+    del calls[:]
+    got = torch.autograd.grad(loss, wanted, [torch.ones_like(o) for o in loss])
+    assert all(g.shape == w.shape for g, w in zip(got, wanted))
+    names = {"x": "dx", "y": "dy"}
+    n_only = {"weight", "bias", "scale", "shift"}
+    asked = {names.get(k, k) for k in trained if used != "h" or k not in n_only}
+    for name, g in zip(trained, got):
+        assert names.get(name, name) in asked or not g.any()
+    if not asked:
+        assert not calls
+        return
+    a = dict(zip(BACKWARD_ARGS, calls[0]))
+    assert len(calls) == 1 and len(calls[0]) == len(BACKWARD_ARGS)
+    given = {k for k in norm.NormGrads._fields if a[k] is not None}
+    assert given == asked
+    assert (a["dh"] is None) == (used == "n") and (a["dn"] is None) == (used == "h")
+    assert (a["ws"] is None) == (asked <= {"dx", "dy"})
+    assert a["zero"] == ("dx" in asked) + 2 * ("dy" in asked)
+
+
+def test_need_is_checked():
+    x, w = torch.zeros((6, 32)), torch.ones(32)
+    for kw, why in ((dict(need=["dz"]), "dz"), (dict(need=["dy"]), "dy"), (dict(need=["weight", "gate"], weight=w), "gate"),
+                    (dict(need=["weight"], weight=w, dx=x), "does not name"), (dict(dy=x), "dy without y")):
+        with pytest.raises(ValueError, match=why):
+            norm.gated_norm_backward(x, x, x, **kw)
+    assert norm.gated_norm_backward(x, x, x, need=[]) == (None,) * 8

@@ -518,3 +518,53 @@ def test_modules_of_a_bf16_model():
                             shift=shift.detach().float())
     assert torch.equal(tab.grad, torch.cat((g.scale, g.shift), dim=1).bfloat16())
     assert torch.equal(norm.weight.grad, g.weight.bfloat16())
+
+
+@pytest.mark.parametrize("M,C,dtype,post,pre,offsets", [(40, 1000, "bf16", "rms", "layer", SEQ), (33, 7, "f32", "layer", "rms", None),
+                                                        (30, 9001, "bf16", "layer", "layer", SEQ), (700, 1100, "f32", "none", "rms", SEQ),
+                                                        (40, 328, "bf16", "rms", "none", [2, 8, 20])])
+def test_each_gradient_alone_has_the_same_bits(M, C, dtype, post, pre, offsets):
+    print(f"alone {M}x{C} {dtype} {post} {pre}", flush=True)
+    c = Case(M, C, dtype, post, pre, True, offsets)
+    dn = c.dn if pre != "none" else None
+    full = gated_norm_backward(c.dh, dn, c.x, c.y, **c.kw)
+    given = [name for name, t in full._asdict().items() if t is not None]
+    for need in [[name] for name in given] + [["dx", "gate"], ["dx", "dy"], given[2:], given]:
+        got = gated_norm_backward(c.dh, dn, c.x, c.y, need=need, **c.kw)._asdict()
+        assert [k for k, v in got.items() if v is not None] == sorted(need, key=given.index)
+        assert all(torch.equal(got[k], getattr(full, k)) for k in need), need
+    mine = torch.full_like(c.x, 5.0)
+    live = torch.from_numpy(c.live).to(DEV)
+    assert gated_norm_backward(c.dh, dn, c.x, c.y, dy=mine, need=["dy"], **c.kw).dx is None
+    assert torch.equal(mine[live], full.dy[live]) and (mine[~live] == 5).all()
+
+
+@pytest.mark.parametrize("offsets", [None, [1, 9, 9, 30]])
+def test_module_with_frozen_weights_or_an_unused_result(offsets):
+    """The gradients are those of the whole call, of a loss in which the unused result has
+    the weight 0."""
+    c = Case(40, 200, "bf16", "rms", "layer", True, offsets)
+    m = GatedNorm(200, post="rms", pre="layer", alpha=0.7, device=DEV)
+    tables = {k: c.kw[k].clone() for k in ("gate", "scale", "shift")}
+    leaves = [c.x.clone(), c.y.clone(), *tables.values(), *m.parameters()]
+    for t in leaves:
+        t.requires_grad_()
+    x, y, *_ = leaves
+    run = lambda: m(x, y, offsets=c.kw["offsets"], **tables)
+    for weights in ((1.0, 0.0), (0.0, 1.0)):
+        h, n = run()
+        want = torch.autograd.grad((h, n), leaves, (c.dh * weights[0], c.dn * weights[1]))
+        h, n = run()
+        out, d = (h, c.dh) if weights[0] else (n, c.dn)
+        got = torch.autograd.grad(out, leaves, d)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    h, n = run()
+    want = torch.autograd.grad((h, n), leaves, (c.dh, c.dn))
+    m.requires_grad_(False)
+    for k in range(1, 5):
+        kept = leaves[:k]
+        for i, t in enumerate(leaves[:5]):
+            t.requires_grad_(i < k)
+        h, n = run()
+        got = torch.autograd.grad((h, n), kept, (c.dh, c.dn))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

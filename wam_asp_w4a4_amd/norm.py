@@ -26,7 +26,7 @@ KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAY
 
 
 class NormGrads(NamedTuple):
-    """Gradients of gated_norm's inputs (None: the input was not given)."""
+    """Gradients of gated_norm's inputs (None: not given, or not wanted)."""
     dx: torch.Tensor | None
     dy: torch.Tensor | None
     post_weight: torch.Tensor | None
@@ -35,6 +35,9 @@ class NormGrads(NamedTuple):
     bias: torch.Tensor | None
     scale: torch.Tensor | None
     shift: torch.Tensor | None
+
+
+_WANT_ALL = dict.fromkeys(NormGrads._fields, True)
 
 
 def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, shift, offsets):
@@ -160,13 +163,14 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
 
 def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None,
                         pre="rms", weight=None, bias=None, scale=None, shift=None, offsets=None,
-                        eps=1e-6, dx=None, dy=None, workspace=None, stream=None):
+                        eps=1e-6, dx=None, dy=None, need=None, workspace=None, stream=None):
     """Gradients of ``gated_norm`` from dh (of h as it goes on; None: zeros) and dn (of
     n, float32 or bf16; None without a pre norm).  h: the forward's; the options are
     the forward's.  dx, dy: tensors to write (rows of no sequence are left as they
-    are; they are zeros in tensors made here).  Every given input of the forward has a
-    gradient in the result, in its shape (float32 but for dx and dy, which have the
-    stream's type)."""
+    are; they are zeros in tensors made here).  need: the names of the wanted gradients
+    (fields of ``NormGrads``; None: of every given input); the others are not computed, and
+    dx and dy alone need no workspace.  A gradient has its input's shape (float32 but for dx
+    and dy, which have the stream's type)."""
     if not isinstance(h, torch.Tensor) or h.dim() != 2:
         raise ValueError("h must be a 2-D torch tensor")
     M, C = h.shape
@@ -185,6 +189,19 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         lddn = _check_rows(dn, "dn", M, C, dev)
     if dh is None and dn is None:
         raise ValueError("neither dh nor dn is given")
+    if y is None and dy is not None:
+        raise ValueError("dy without y")
+    want = _WANT_ALL if need is None else {name: name in need for name in NormGrads._fields}
+    if need is not None:
+        given = dict(dx=h, dy=y, post_weight=post_weight, gate=gate, weight=weight, bias=bias,
+                     scale=scale, shift=shift)
+        for name in need:
+            if given.get(name) is None:
+                raise ValueError(f"need names {name!r}: no gradient of a given input")
+        if dx is not None and not want["dx"] or dy is not None and not want["dy"]:
+            raise ValueError("a tensor for a gradient that need does not name")
+        if not need:
+            return NormGrads(*8 * (None,))
     made, zero = [], 0   # bits of the outputs made here: dx, dy
 
     own = _made_for(stream, dev)
@@ -194,37 +211,36 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
             made.append(torch.empty(shape, dtype=dtype, device=dev))
         return made[-1]
 
-    def like(*inputs):
+    def like(**inputs):
         # one allocation for those of one shape
+        inputs = [t if want[name] else None for name, t in inputs.items()]
         given = [t for t in inputs if t is not None]
         if any(t.shape != given[0].shape for t in given):
             return [None if t is None else new(t.shape) for t in inputs]
         rows = iter(new((len(given), *given[0].shape)).unbind(0) if given else ())
         return [None if t is None else next(rows) for t in inputs]
 
-    if dx is None:
+    if dx is not None:
+        lddx = _check_rows(dx, "dx", M, C, dev, same)
+    elif want["dx"]:
         dx = new((M, C), h.dtype)
         zero = 1
-    else:
-        lddx = _check_rows(dx, "dx", M, C, dev, same)
-    if y is None:
-        if dy is not None:
-            raise ValueError("dy without y")
-    elif dy is None:
+    if dy is not None:
+        lddy = _check_rows(dy, "dy", M, C, dev, same)
+    elif y is not None and want["dy"]:
         dy = new((M, C), h.dtype)
         zero |= 2
-    else:
-        lddy = _check_rows(dy, "dy", M, C, dev, same)
-    d_post_weight, d_weight, d_bias = like(post_weight, weight, bias)
-    d_gate, d_scale, d_shift = like(gate, scale, shift)
-    need = 0
-    if not (post_weight is weight is bias is gate is scale is shift is None):
-        need = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
+    sums = [*like(post_weight=post_weight, weight=weight, bias=bias),
+            *like(gate=gate, scale=scale, shift=shift)]
+    d_post_weight, d_weight, d_bias, d_gate, d_scale, d_shift = sums
+    size = 0
+    if any(t is not None for t in sums):
+        size = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
         if workspace is None:
             with own:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+                workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
     if workspace is not None:
-        _check_ws(workspace, need, dev)
+        _check_ws(workspace, size, dev)
     at = B._at
     B.launch(dev, B.lib().asp_norm_gate_backward, at(dh), lddh, at(dn), lddn,
              B.ASP_F32 if dn is None else _CODES[dn.dtype], h.data_ptr(), ldh, at(y), ldy,
@@ -239,6 +255,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
 class _GatedNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, offsets, options):
+        ctx.set_materialize_grads(False)
         given = dict(post_weight=post_weight, gate=gate, weight=weight, bias=bias, scale=scale,
                      shift=shift)
         h = None
@@ -255,12 +272,25 @@ class _GatedNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dn):
         _no_capture()
-        h, y, post_weight, gate, weight, bias, scale, shift, offsets = ctx.saved_tensors
+        h, y, *tensors, offsets = ctx.saved_tensors
+        given = dict(zip(NormGrads._fields[2:], tensors))
+        need = [name for name, n in zip(NormGrads._fields, ctx.needs_input_grad) if n]
+        options = ctx.options
+        if dh is None and dn is None or not need:
+            return 10 * (None,)
+        zeros = {}
+        if dn is None and options["pre"] != "none":
+            # n is not used: h alone goes on, and what only n reads has zero gradients
+            options = {**options, "pre": "none"}
+            for name in ("weight", "bias", "scale", "shift"):
+                t = given.pop(name)
+                if name in need:
+                    zeros[name] = torch.zeros_like(t)
+            need = [name for name in need if name not in zeros]
         g = gated_norm_backward(None if dh is None else dh.contiguous(),
-                                None if dn is None else dn.contiguous(), h, y,
-                                post_weight=post_weight, gate=gate, weight=weight, bias=bias,
-                                scale=scale, shift=shift, offsets=offsets, **ctx.options)
-        return (*g, None, None)
+                                None if dn is None else dn.contiguous(), h, y, need=need,
+                                offsets=offsets, **given, **options)
+        return (*g._replace(**zeros), None, None)
 
 
 class GatedNorm(torch.nn.Module):
