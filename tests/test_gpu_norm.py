@@ -568,3 +568,21 @@ def test_module_with_frozen_weights_or_an_unused_result(offsets):
         h, n = run()
         got = torch.autograd.grad((h, n), kept, (c.dh, c.dn))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("pre", ["rms", "layer", "none"])
+@pytest.mark.parametrize("with_y", [False, True])
+@pytest.mark.parametrize("offsets", [None, [2, 9, 9, 30]])
+def test_module_gives_the_same_with_and_without_gradients(offsets, with_y, pre):
+    """The rows of no sequence too: zeros, where offsets are given."""
+    c = Case(40, 200, "bf16", "none", pre, False, offsets, affine=False)
+    m = GatedNorm(200, pre=pre, device=DEV)
+    c.x.requires_grad_()
+    kw = dict(y=c.y if with_y else None, offsets=c.kw["offsets"])
+    train = m(c.x, **kw)
+    assert train[0].requires_grad
+    with torch.no_grad():
+        plain = m(c.x, **kw)
+    for a, b in zip(train, plain):
+        assert (a is None) == (b is None)
+        assert a is None or torch.equal(a, b) and not b[torch.from_numpy(~c.live).to(DEV)].any()

@@ -252,6 +252,13 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     return NormGrads(dx, dy, d_post_weight, d_gate, d_weight, d_bias, d_scale, d_shift)
 
 
+def _module_norm(x, y, offsets, h=None, **options):
+    """``gated_norm`` with zeros in h's rows of no sequence also where h would be x itself."""
+    if y is None and options["alpha"] == 1.0 and offsets is not None:
+        h = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+    return gated_norm(x, y, h=h, offsets=offsets, **options)
+
+
 class _GatedNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, post_weight, gate, weight, bias, scale, shift, offsets, options):
@@ -259,11 +266,10 @@ class _GatedNorm(torch.autograd.Function):
         given = dict(post_weight=post_weight, gate=gate, weight=weight, bias=bias, scale=scale,
                      shift=shift)
         h = None
-        if y is None and options["alpha"] == 1.0:
+        if y is None and options["alpha"] == 1.0 and offsets is None:
             # written all the same: a stream returned as it came would share its version
-            make = torch.empty if offsets is None else torch.zeros
-            h = make(x.shape, dtype=x.dtype, device=x.device)
-        h, n = gated_norm(x, y, h=h, offsets=offsets, **given, **options)
+            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        h, n = _module_norm(x, y, h=h, offsets=offsets, **given, **options)
         ctx.save_for_backward(h, y, *given.values(), offsets)
         ctx.options = options
         return h, n
@@ -298,8 +304,8 @@ class GatedNorm(torch.nn.Module):
 
     x, y: (..., C) of one shape, or either as its rows (M, C); gate, scale, shift: (G, C) or
     (C), taken as float32 like the weights; returns (h, n) of x's shape (n None for pre
-    'none'; rows of no sequence are zeros; without gradients, y and a factor alpha, h is x
-    itself).  Gradients are reverse mode; forward-mode tangents are refused.  Under a HIP
+    'none'; rows of no sequence are zeros; without gradients, offsets, y and a factor alpha,
+    h is x itself).  Gradients are reverse mode; forward-mode tangents are refused.  Under a HIP
     graph capture, gradients are refused: capture ``gated_norm`` and
     ``gated_norm_backward``, which keep no graph of their own."""
 
@@ -341,7 +347,7 @@ class GatedNorm(torch.nn.Module):
             h, n = _GatedNorm.apply(*flat, *tensors, offsets, options)
         else:
             names = ("post_weight", "gate", "weight", "bias", "scale", "shift")
-            h, n = gated_norm(*flat, **dict(zip(names, tensors)), offsets=offsets, **options)
+            h, n = _module_norm(*flat, offsets, **dict(zip(names, tensors)), **options)
         return h.reshape(x.shape), None if n is None else n.reshape(x.shape)
 
     def extra_repr(self) -> str:
