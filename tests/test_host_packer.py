@@ -9,6 +9,10 @@
   may move a value by one unit in the last place on rare elements).
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -183,3 +187,17 @@ def test_prep_pack_constants(K, r):
     from oracle import asp as OAsp
     act = OAsp.activation_side(lay.x, lay.s, lay.v)
     assert np.abs(x @ got - act["u"]).max() <= 1e-6 * np.abs(act["u"]).max()
+
+
+def test_the_binding_packs_without_torch():
+    """A process that only packs on the host takes NumPy arrays and loads NumPy alone."""
+    code = ("import sys, numpy as np\n"
+            "from wam_asp_w4a4_amd import binding as B\n"
+            "w = np.ones((4, 128), np.float32)\n"
+            "codes, scales = np.empty((4, 64), np.uint8), np.empty((4, 8), np.uint8)\n"
+            "B.asp_pack_weight(4, 128, 0, w, np.ones(128, np.float32), None, codes, scales, None, None, 1)\n"
+            "assert (scales == scales[0, 0]).all()\n"
+            "sys.exit('torch' in sys.modules)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr

@@ -15,9 +15,9 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import sys
 
 import numpy as np
-import torch
 
 ABI_VERSION = 8
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasp.so")
@@ -420,7 +420,7 @@ def stream_on(stream, device):
     """The stream handle for a launch on `device`: the caller's, else torch's current one."""
     if stream is not None or device.type != "cuda":
         return stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return sys.modules["torch"]._C._cuda_getCurrentRawStream(device.index)
 
 
 def launch(device, fn, *args):
@@ -429,6 +429,7 @@ def launch(device, fn, *args):
     the host's would fault."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, not on a GPU")
+    torch = sys.modules["torch"]   # there, since `device` is one of its
     if device.index == torch.cuda.current_device():
         status = fn(*args)
     else:
