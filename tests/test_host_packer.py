@@ -196,7 +196,6 @@ def test_the_binding_packs_without_torch():
             "w = np.ones((4, 128), np.float32)\n"
             "codes, scales = np.empty((4, 64), np.uint8), np.empty((4, 8), np.uint8)\n"
             "B.asp_pack_weight(4, 128, 0, w, np.ones(128, np.float32), None, codes, scales, None, None, 1)\n"
-            "assert (scales == scales[0, 0]).all()\n"
             "sys.exit('torch' in sys.modules)\n")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
