@@ -389,3 +389,11 @@ def test_need_is_checked():
         with pytest.raises(ValueError, match=why):
             norm.gated_norm_backward(x, x, x, **kw)
     assert norm.gated_norm_backward(x, x, x, need=[]) == (None,) * 8
+
+
+def test_result_types_are_checked():
+    for call in (lambda: Fp8Linear(layer(), y_dtype="f16"), lambda: layer().forward(torch.zeros((4, 200)), "f16"),
+                 lambda: layer().backward(torch.zeros((4, 64)), dx_dtype="f16"),
+                 lambda: layer().backward(torch.zeros((4, 64)), torch.zeros((4, 200)), dw_dtype="f16")):
+        with pytest.raises(ValueError, match="must be 'f32'"):
+            call()

@@ -386,6 +386,33 @@ def test_module_trains():
     assert torch.equal(m(x), y)
 
 
+@pytest.mark.parametrize("M", [5, 150, 3000])
+def test_float32_sums_are_a_choice_in_every_direction(M):
+    """bf16 activations with a float32 y and dx: the sums of the float32 call on the same values."""
+    from wam_asp_w4a4_amd.linear import Fp8Linear
+    lin = torch.nn.Linear(1000, 700).to(DEV)
+    x = torch.randn((M, 1000), device=DEV).bfloat16().requires_grad_()
+    dy = torch.randn((M, 700), device=DEV).bfloat16()
+    layer = Fp8Layer.pack(lin.weight.detach(), lin.bias.detach())
+    want = layer.backward(dy.float(), x.detach().float())
+    got = layer.backward(dy, x.detach(), dx_dtype="f32")
+    assert got[0].dtype == torch.float32 and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(layer.backward(dy.float(), dx_dtype="bf16")[0], layer.backward(dy)[0])
+    for trainable in (False, True):
+        m = Fp8Linear.from_linear(lin, trainable=trainable, y_dtype="f32")
+        x.grad = None
+        y = m(x)
+        assert y.dtype == torch.float32 and torch.equal(y, layer.forward(x.detach().float()))
+        with torch.no_grad():
+            assert torch.equal(m(x), y)
+        y.backward(dy.float())
+        assert torch.equal(x.grad, want[0].bfloat16())
+    m = Fp8Linear(weight=torch.nn.Parameter(lin.weight.detach().bfloat16()), y_dtype="f32")
+    m(x).backward(dy.float())
+    want = Fp8Layer.pack(m.weight.detach()).backward(dy.float(), x.detach().float())
+    assert torch.equal(m.weight.grad, want[1].bfloat16())
+
+
 def test_module_takes_broadcast_and_transposed_inputs():
     from wam_asp_w4a4_amd.linear import Fp8Linear
     m = Fp8Linear.from_linear(torch.nn.Linear(200, 70).to(DEV), trainable=True)

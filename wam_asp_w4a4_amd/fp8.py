@@ -215,7 +215,9 @@ class Fp8Layer:
 
     def forward(self, x, y_dtype=None, workspace=None, y=None, stream=None):
         """y = Q(x) W^T + bias for x (M x K, float32 or bf16, any row stride) or an
-        ``Fp8Tensor``; y_dtype 'f32' or 'bf16' (None: x's; 'bf16' for codes)."""
+        ``Fp8Tensor``; y_dtype 'f32' or 'bf16' (None: x's; 'bf16' for codes).  A float32 y
+        has float32 sums; a bf16 one is computed at twice the rate, with each 8 consecutive
+        products added in 14 bits below their largest (1.5e-5 of y's 2-norm)."""
         dev, N, K = self.codes.device, self.N, self.K
         quantised = isinstance(x, Fp8Tensor)
         if quantised:
@@ -259,17 +261,20 @@ class Fp8Layer:
         return y
 
     def backward(self, dy, x=None, need_dx=True, need_db=None, dw_dtype="f32", workspace=None,
-                 stream=None):
-        """(dx, dw, db) for dy (M x N): dx in dy's type where ``need_dx``, dw (N x K, of
-        ``dw_dtype``) where x is given, db float32 where ``need_db`` (None: where the
-        layer has a bias); the others are None."""
+                 stream=None, dx_dtype=None):
+        """(dx, dw, db) for dy (M x N): dx of ``dx_dtype`` (None: dy's type) where
+        ``need_dx``, dw (N x K, of ``dw_dtype``) where x is given, db float32 where
+        ``need_db`` (None: where the layer has a bias); the others are None.  The types
+        choose the arithmetic, as in ``forward``."""
         dev, N, K = self.codes.device, self.N, self.K
         lddy, ldx = _check_rows(dy, "dy", None, N, dev), K
         M = dy.shape[0]
         if x is not None:
             ldx = _check_rows(x, "x", M, K, dev)
-        if dw_dtype not in _Y_DTYPES:
-            raise ValueError(f"dw_dtype must be 'f32' or 'bf16', not {dw_dtype!r}")
+        dx_dtype = dx_dtype or _NAMES[dy.dtype]
+        if dw_dtype not in _Y_DTYPES or dx_dtype not in _Y_DTYPES:
+            raise ValueError(f"dx_dtype and dw_dtype must be 'f32' or 'bf16', not {dx_dtype!r}, "
+                             f"{dw_dtype!r}")
         if need_dx and self.codes_t is None:
             raise ValueError("dx needs the transposed weight: pack the layer with backward=True")
         if need_db is None:
@@ -280,15 +285,15 @@ class Fp8Layer:
         if workspace is not None:
             _check_ws(workspace, need, dev)
         with _made_for(stream, dev):
-            dx = torch.empty((M, K), dtype=dy.dtype, device=dev) if need_dx else None
+            dx = torch.empty((M, K), dtype=_Y_DTYPES[dx_dtype], device=dev) if need_dx else None
             dw = None if x is None else torch.empty((N, K), dtype=_Y_DTYPES[dw_dtype], device=dev)
             db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
             if workspace is None:
                 workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        at, code = B._at, _CODES[dy.dtype]
-        B.launch(dev, B.lib().asp_fp8_backward, dy.data_ptr(), code, lddy, at(x),
+        at = B._at
+        B.launch(dev, B.lib().asp_fp8_backward, dy.data_ptr(), _CODES[dy.dtype], lddy, at(x),
                  B.ASP_F32 if x is None else _CODES[x.dtype], ldx, M, N, K, at(self.codes_t),
-                 at(self.scales_t), at(dx), code, at(dw), B.DTYPES[dw_dtype], at(db),
+                 at(self.scales_t), at(dx), B.DTYPES[dx_dtype], at(dw), B.DTYPES[dw_dtype], at(db),
                  workspace.data_ptr(), workspace.numel(), B.stream_on(stream, dev))
         _lend(stream, dx, dw, db)
         return dx, dw, db

@@ -77,24 +77,28 @@ class ASPLinear(torch.nn.Module):
 
 class _Fp8Apply(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, layer):
+    def forward(ctx, x, weight, bias, layer, y_dtype):
         ctx.layer = layer
-        ctx.save_for_backward(x if weight is not None and ctx.needs_input_grad[1] else None, weight)
-        return layer.forward(x)
+        # autograd rounds gradients that have more bits than their inputs
+        ctx.dw_dtype = "f32" if weight is None or y_dtype == "f32" else _NAMES[weight.dtype]
+        ctx.save_for_backward(x if weight is not None and ctx.needs_input_grad[1] else None)
+        return layer.forward(x, y_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         _no_capture()
-        x, weight = ctx.saved_tensors
+        x, = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx, dw, db = ctx.layer.backward(dy.contiguous(), x, need_dx=need[0], need_db=need[2],
-                                        dw_dtype="f32" if weight is None else _NAMES[weight.dtype])
-        return dx, dw, db, None
+                                        dw_dtype=ctx.dw_dtype)
+        return dx, dw, db, None, None
 
 
 class Fp8Linear(torch.nn.Module):
-    """y = the 8-bit linear layer applied to x (..., in_features); y has x's type.
+    """y = the 8-bit linear layer applied to x (..., in_features), in x's type or the given
+    ``y_dtype``: 'f32' has float32 sums in y and all gradients, also for a bf16 x or weight,
+    at half the rate (``Fp8Layer.forward`` has the arithmetic).
 
     Around a packed ``Fp8Layer`` the weight is frozen, and x (and a bias that requires
     it) has a gradient.  With ``weight`` (N x K, float32 or bf16, a parameter) every
@@ -104,27 +108,30 @@ class Fp8Linear(torch.nn.Module):
     are refused: capture ``Fp8Layer.forward`` and ``backward``, which keep no graph of
     their own."""
 
-    def __init__(self, packed: Fp8Layer | None = None, weight=None, bias=None):
+    def __init__(self, packed: Fp8Layer | None = None, weight=None, bias=None, y_dtype=None):
         super().__init__()
         if (packed is None) == (weight is None):
             raise ValueError("either a packed layer or a weight")
         if packed is not None and bias is not None:
             raise ValueError("a packed layer has its own bias")
+        if y_dtype not in (None, "f32", "bf16"):
+            raise ValueError(f"y_dtype must be 'f32', 'bf16' or None, not {y_dtype!r}")
         self.packed = packed
+        self.y_dtype = y_dtype
         self.weight = weight
         self.bias = packed.bias if packed is not None else bias
         self.out_features, self.in_features = ((packed.N, packed.K) if packed is not None
                                                else weight.shape)
 
     @classmethod
-    def from_linear(cls, linear: torch.nn.Linear, trainable: bool = False):
+    def from_linear(cls, linear: torch.nn.Linear, trainable: bool = False, y_dtype=None):
         """From an nn.Linear on the device: its weight packed once, or with ``trainable``
         shared as the parameter that every forward packs.  The bias is kept in float32."""
         bias = None if linear.bias is None else linear.bias.detach().float().contiguous()
         if trainable:
-            return cls(weight=linear.weight,
+            return cls(weight=linear.weight, y_dtype=y_dtype,
                        bias=None if bias is None else torch.nn.Parameter(bias.clone()))
-        return cls(Fp8Layer.pack(linear.weight.detach(), bias))
+        return cls(Fp8Layer.pack(linear.weight.detach(), bias), y_dtype=y_dtype)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.shape[-1] != self.in_features:
@@ -142,9 +149,9 @@ class Fp8Linear(torch.nn.Module):
         elif self.bias is not layer.bias or self.bias is not None and self.bias.dtype != torch.float32:
             layer = replace(layer, bias=None if self.bias is None else _float32(self.bias.detach()))
         if grads:
-            y = _Fp8Apply.apply(x2, self.weight, self.bias, layer)
+            y = _Fp8Apply.apply(x2, self.weight, self.bias, layer, self.y_dtype)
         else:
-            y = layer.forward(x2)
+            y = layer.forward(x2, self.y_dtype)
         return y.reshape(*x.shape[:-1], self.out_features)
 
     def extra_repr(self) -> str:
