@@ -136,6 +136,35 @@ def test_product_of_whole_numbers_is_exact(M, N, K):
                        want - torch.from_numpy(bias).to(DEV).double())
 
 
+def far_apart(rng, K):
+    """The columns, one of a block of 128 and at most 200 of them, at which both operands
+    hold +-256 beside the +-1 of all others: products of 2^16 next to ones of 1."""
+    blocks = np.linspace(0, -(-K // 128) - 1, min(200, -(-K // 128))).astype(int)
+    return np.unique(np.minimum(128 * blocks + rng.integers(0, 128, blocks.size), K - 1))
+
+
+def signs(rng, rows, cols):
+    return (rng.integers(0, 2, (rows, cols), dtype=np.int8) * 2 - 1).astype(np.float32)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_float32_results_are_summed_in_float32(M, N, K):
+    """Products 16 bits apart within eight consecutive ones, which the 8-bit instruction's
+    14-bit window would drop.  All magnitudes together are below 200 * 2^16 + 33000 < 2^24:
+    float32 sums of any order are exact."""
+    print(f"float32 sums {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(M + N + K)
+    big = far_apart(rng, K)
+    a, b = signs(rng, M, K), signs(rng, N, K)
+    a[:, big] *= 256
+    b[:, big] *= 256
+    x, w = (torch.from_numpy(v).to(DEV) for v in (a, b))
+    want = x.double() @ w.double().t()
+    layer = Fp8Layer.pack(w, backward=False)
+    for xt in (x, x.bfloat16(), quantize(x)):
+        assert torch.equal(layer.forward(xt, "f32").double(), want)
+
+
 @pytest.mark.parametrize("y_dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K,dtype,ld", [(1, 1030, 1024, "bf16", None), (7, 64, 1000, "f32", 1003),
                                             (16, 256, 4096, "bf16", 4104), (200, 300, 2000, "f32", None),
@@ -194,6 +223,24 @@ def test_gradients_against_the_oracle(M, N, K, dtype):
     near(two[1], ww, M, np.abs(O.held(dv.T)) @ np.abs(O.held(xv.T)).T * (1 + 7 * 2.0 ** -13 / (M * 2.0 ** -23)), 2.0 ** -8)
     three = layer.backward(dy, need_dx=False, workspace=layer.workspace(M, backward=True).fill_(255))
     assert three[0] is three[1] is None and torch.equal(three[2], db)
+
+
+@pytest.mark.parametrize("M,N,K", [shape[:3] for shape in GRADS])
+def test_float32_gradients_are_summed_in_float32(M, N, K):
+    """As in the forward: dx sums over N and dw over M, at most 200 * 2^16 + 2100 * 2^8 < 2^24."""
+    print(f"float32 gradients {M}x{N}x{K}", flush=True)
+    rng = np.random.default_rng(M + N + K)
+    x, dy, w = signs(rng, M, K), signs(rng, M, N), signs(rng, N, K)
+    m, n = far_apart(rng, M), far_apart(rng, N)
+    dy[m] = signs(rng, m.size, N) * 256
+    x[m] *= 256
+    dy[:, n] = signs(rng, M, n.size) * 256
+    w[n] *= 256
+    x, dy, w = (torch.from_numpy(v).to(DEV) for v in (x, dy, w))
+    dx, dw, db = Fp8Layer.pack(w, torch.zeros(N, device=DEV)).backward(dy, x)
+    assert torch.equal(dx.double(), dy.double() @ w.double())
+    assert torch.equal(dw.double(), dy.double().t().contiguous() @ x.double())
+    assert torch.equal(db.double(), dy.double().sum(0))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

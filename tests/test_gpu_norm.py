@@ -586,3 +586,28 @@ def test_module_gives_the_same_with_and_without_gradients(offsets, with_y, pre):
     for a, b in zip(train, plain):
         assert (a is None) == (b is None)
         assert a is None or torch.equal(a, b) and not b[torch.from_numpy(~c.live).to(DEV)].any()
+
+
+@pytest.mark.parametrize("M,C", [(5, 7), (33, 1000), (40, 1001), (30, 5001), (30, 9001)])
+def test_backward_of_a_bf16_stream_with_a_float32_result(M, C):
+    """gated_norm(bf16, out='f32') and its backward: dn in float32 beside bf16 rows."""
+    print(f"bf16 stream, float32 dn {M}x{C}", flush=True)
+    for post, pre, ld in (("layer", "rms", 0), ("rms", "layer", 3)):
+        c = Case(M, C, "bf16", post, pre, True, SEQ if M >= 30 else None, ld=ld)
+        h, n = gated_norm(c.x, c.y, out="f32", **c.kw)
+        c.check_forward(h, n)
+        c.dn = torch.randn((M, C + 5), device=DEV)[:, :C]
+        check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,C", [(3, 129), (33, 1001), (30, 8300), (30, 16384)])
+def test_eight_bit_result_of_either_stream_and_of_wide_rows(M, C, dtype):
+    print(f"eight bit {M}x{C} {dtype}", flush=True)
+    c = Case(M, C, dtype, "rms", "rms", True, SEQ if M >= 30 else None)
+    _, n = gated_norm(c.x, c.y, out="f32", **c.kw)
+    _, q = gated_norm(c.x, c.y, out="fp8", **c.kw)
+    live = torch.from_numpy(c.live).to(DEV)
+    codes, s = OF.quantize(host(n))
+    np.testing.assert_array_equal(q.codes[live].cpu().numpy(), codes[c.live])
+    np.testing.assert_array_equal(q.scales[:, live].cpu().numpy(), OF.layout_scales(s)[:, c.live])
