@@ -1,6 +1,5 @@
 // Shared pieces of the 8-bit (block-128) units: the format's arithmetic on the
-// device, element access with any stride, buffer sizes and the launchers that
-// more than one translation unit calls.
+// device, element access with any stride, buffer sizes and the quantisers' launchers.
 //
 // Format.  128 consecutive elements along the contracted axis share a scale
 // S = 2^k, the smallest with k >= -126 and amax / S <= 448, amax taken over the
@@ -220,21 +219,5 @@ struct Fp8TileJob {
   int32_t dtype, square;
 };
 int32_t fp8_quantize_tiles(int n, const Fp8TileJob* jobs, hipStream_t st);
-
-size_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K);
-// y = A B^T + bias from codes, or from x itself where M is small enough for
-// fp8_fuses(M) (x quantised inside)
-struct Fp8Gemm {
-  const uint8_t *a, *as, *b, *bs;
-  int64_t M, N, K;  // K >= 0
-  const float* bias;
-  void* y;
-  int32_t y_dtype;
-  void* ws;
-};
-int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st);
-bool fp8_fuses(int64_t M);
-int32_t fp8_gemm_fused(const Fp8Gemm& g, const void* x, int32_t x_dtype, int64_t ldx,
-                       hipStream_t st);
 
 }  // namespace asp

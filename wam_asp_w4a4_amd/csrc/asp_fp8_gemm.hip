@@ -764,6 +764,16 @@ __global__ void __launch_bounds__(256, 2) k_fp8_back(const BackK b) {
 
 // ----------------------------------------------------------------- host side
 
+// y = A B^T + bias, from A's codes
+struct Fp8Gemm {
+  const uint8_t *a, *as, *b, *bs;
+  int64_t M, N, K;  // K >= 0
+  const float* bias;
+  void* y;
+  int32_t y_dtype;
+  void* ws;
+};
+
 constexpr int kFewRows = 16;
 
 constexpr int kCUs = 256;
@@ -871,8 +881,7 @@ int32_t launch_few(const GemmK& k, const XT* x, int64_t ldx, int64_t K, hipStrea
   return launch_status("fp8 few-row gemm");
 }
 
-}  // namespace
-
+// x itself is taken where M is small enough, and quantised inside
 bool fp8_fuses(int64_t M) { return M <= kFewRows; }
 
 size_t fp8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
@@ -889,7 +898,6 @@ int32_t fp8_gemm_fused(const Fp8Gemm& g, const void* x, int32_t x_dtype, int64_t
   return launch_few(k, static_cast<const float*>(x), ldx, g.K, st);
 }
 
-namespace {
 template <bool WIDE>
 int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
   switch (p.kernel) {
@@ -900,7 +908,6 @@ int32_t launch_plan(const Plan& p, const GemmK& k, hipStream_t st) {
     default: return launch_mid<WIDE>(k, st);
   }
 }
-}  // namespace
 
 int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
   if (g.M <= kFewRows)
@@ -913,8 +920,6 @@ int32_t fp8_gemm_impl(const Fp8Gemm& g, hipStream_t st) {
   k_fp8_join<<<dim3((unsigned)blocks), 256, 0, st>>>(k);
   return launch_status("fp8 join");
 }
-
-namespace {
 
 // Latency-bound products, which share a launch with others (k_fp8_back): the backward asks
 // this of each by itself, so that a gradient's bits do not depend on which others are
