@@ -794,16 +794,33 @@ int tail_parts(int64_t tiles) {
 }
 
 // The kernel for more than kFewRows rows.  A larger tile reads fewer bytes for its
-// products: 256 x 256 tiles reach 2560 TFLOP/s at 8192^3, 128 x 128 ones (two a CU)
-// 1780.  But a tile is one CU's work: beyond half a round of 256-tiles (128) they are
-// faster.  A quarter to half a round is one round of their 256 x 128 halves, faster than
-// 128-tiles where 8-bit products last (2048 x 4096 x 4096 47 -> 42 us, 700 x 6000 x
-// 4096 39 -> 32; even at K = 1024, and float32 results at any: 65 against 67).  Below that
-// 128-tiles while they fill three quarters of the CUs.  A long K over fewer of them
-// is split into slices whose float32 partial sums a second kernel adds.  What is left
-// is bound by latency: up to 768 tiles of 32 x 32 are k_fp8_mid's (256 x 1024 x 4096:
-// 6.6 us, against 11.6 with 64-tiles in four slices), more are 64-tiles (256 x 4096 x
-// 1024, 1024 tiles of 32: 6.0 us against 7.6).  `wide` never changes the slices.
+// products (256 x 256 reach 2560 TFLOP/s at 8192^3, 128 x 128, two a CU, 1780), but a tile
+// is one CU's work.  The product alone, us, bf16 result (float32 result), by the number of
+// tiles; the kernel of the rule first:
+//  - 256-tiles beyond half a round of them, against 128-tiles: 256 of them, 4096 x 4096 x
+//    4096 63 and 88 (112, 123), K = 512 21.4 and 23.3; 144 of them, 2304 x 4096 x 4096 50 and
+//    57 (87, 85), where a short K would have been as fast in 128-tiles (K = 512: 18.8, 18.1).
+//  - A quarter to half a round as one round of their 256 x 128 halves, against 128-tiles:
+//    2048 x 4096 x 4096 41 and 44, 700 x 6000 x 4096 32 and 39, K = 2048 20.5 and 22.4.  A
+//    shorter K gains nothing (K = 1024: 15.5 and 15.1) and a float32 result nothing at any
+//    (64 and 65; K = 1024 22.5 and 20.6): they take 128-tiles.
+//  - 128-tiles from three quarters of the CUs on, against 64-tiles: 195 of them, 1664 x 1920 x
+//    4096 23 and 37 (32, 47), K = 512 8.1 and 9.2 (11.6, 11.4).  120 of them, on the rule's
+//    other side: 64-tiles 20.8, 128-tiles 21.3 (26, 31), K = 512 6.5 and 7.5.  In between, once
+//    64-tiles are more than two a CU, it depends on K: 169 of them, 64-tiles 8.1 and
+//    128-tiles 7.8 at K = 512 (9.7, 11.2), 29.4 and 22.5 at K = 4096 (37, 32).
+//  - Slices of a long K over fewer 128-tiles, whose float32 partial sums a second kernel
+//    adds: as many as fill those three quarters, of 32 blocks at least.  1280 x 1280 (100
+//    tiles), K = 8192 in two: 30 and 36 unsliced, 37 in 64-tiles (38, 51, 45); K = 32768 80
+//    and 126 (110, 183).  512 x 1024 (32 tiles), K = 32768 in eight: 35 and 46 in k_fp8_mid
+//    (44, 52).  K = 4096, which is not sliced: 64-tiles 19.8, two slices 21.4 (24.8, 26.1).
+//    Below 16 tiles k_fp8_mid has the workgroups to do without (256 x 512 x 16384: 13.5,
+//    eight slices 19).
+//  - What is left is bound by latency.  Up to 768 tiles of 32 x 32 k_fp8_mid, against
+//    64-tiles: 256 x 1024 x 4096 5.9 and 10.7 (7.2, 16.8), 512 x 1536 x 1024 6.4 and 5.8
+//    (7.0, 7.6), K = 4096 12.6 and 13.0 (14.3, 17.7); more are 64-tiles: 1024 of them, 256 x
+//    4096 x 1024, 6.0 and 7.3 (7.8, 8.6).
+// `wide`, a float32 result, never changes the slices.
 Plan plan(int64_t M, int64_t N, int64_t K, bool wide) {
   auto tiles = [&](int64_t t) { return ((M + t - 1) / t) * ((N + t - 1) / t); };
   const int64_t KB = fp8_blocks(K);
@@ -861,6 +878,10 @@ int32_t launch_mid(GemmK k, hipStream_t st) {
   return launch_status("fp8 mid gemm");
 }
 
+// Waves over which k_fp8_few splits K, by its blocks (4, 8, 16 waves, M = 1, bf16, us): N =
+// 1024, K = 512 4.2 4.2 4.2, 1024 5.3 4.8 4.9, 2048 8.0 6.6 5.9, 16384 46 32 27.  At N =
+// 14336, 896 workgroups, fewer waves lose less or nothing (K = 1024 9.1 9.6 13.1, 4096 28.5
+// 27.5 31.3): the rule is for the columns of one round of the CUs.
 int few_waves(int KB) { return KB >= 16 ? 16 : KB >= 8 ? 8 : 4; }
 
 template <typename XT, bool WIDE>
