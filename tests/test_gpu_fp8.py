@@ -353,7 +353,8 @@ def _busy():
         torch.mm(a, a, out=b)
 
 
-def test_memory_of_calls_on_another_stream():
+@pytest.mark.parametrize("other", ["a side stream", "the default stream"])
+def test_memory_of_calls_on_another_stream(other):
     """The current stream is behind: blocks that it freed are still to be written by it, and a
     result is still to be read.  Neither may be handed to a call on another stream."""
     from wam_asp_w4a4_amd.norm import gated_norm, gated_norm_backward
@@ -374,26 +375,29 @@ def test_memory_of_calls_on_another_stream():
 
     want, want2 = calls(x), calls(x2)
     torch.cuda.synchronize()
-    side, cur = torch.cuda.Stream(), torch.cuda.current_stream()
-    assert side.cuda_stream != cur.cuda_stream
-    side.wait_stream(cur)
-    _busy()
-    for _ in range(2):
-        trash = [torch.empty_like(t) for t in want for _ in range(2)]
-        for t in trash:
-            t.fill_(3)
-        del trash, t
-    got = calls(x, side.cuda_stream)
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(got, want))
-    # read late, on the current stream, and freed before that
-    _busy()
-    late = [t.clone() for t in got]
-    del got
-    again = calls(x2, side.cuda_stream)
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(late, want))
-    assert all(torch.equal(a, b) for a, b in zip(again, want2))
+    side, cur = torch.cuda.Stream(), torch.cuda.default_stream()
+    if other == "the default stream":
+        side, cur = cur, side
+        assert side.cuda_stream == 0
+    cur.wait_stream(side)
+    with torch.cuda.stream(cur):
+        _busy()
+        for _ in range(2):
+            trash = [torch.empty_like(t) for t in want for _ in range(2)]
+            for t in trash:
+                t.fill_(3)
+            del trash, t
+        got = calls(x, side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # read late, on the current stream, and freed before that
+        _busy()
+        late = [t.clone() for t in got]
+        del got
+        again = calls(x2, side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(late, want))
+        assert all(torch.equal(a, b) for a, b in zip(again, want2))
 
 
 def test_the_c_calls_refuse_a_small_workspace():

@@ -20,7 +20,8 @@ def _busy():
         torch.mm(a, a, out=b)
 
 
-def test_memory_of_calls_on_another_stream():
+@pytest.mark.parametrize("other", ["a side stream", "the default stream"])
+def test_memory_of_calls_on_another_stream(other):
     """Blocks that the current stream freed are still to be written by it, and a result is
     still to be read.  Neither may be handed to a call on another stream."""
     lay = synth.make_layer("s", 80, 256, 384, 32, seed=1, dtype="f32")
@@ -38,22 +39,36 @@ def test_memory_of_calls_on_another_stream():
 
     want, want2 = calls(x), calls(x2)
     torch.cuda.synchronize()
-    side, cur = torch.cuda.Stream(), torch.cuda.current_stream()
-    assert side.cuda_stream != cur.cuda_stream
-    side.wait_stream(cur)
-    _busy()
-    trash = [torch.empty_like(t) for t in want for _ in range(2)]
-    for t in trash:
-        t.fill_(3)
-    del trash, t
-    got = calls(x, side.cuda_stream)
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(got, want))
-    # read late, on the current stream, and freed before that
-    _busy()
-    late = [t.clone() for t in got]
-    del got
-    again = calls(x2, side.cuda_stream)
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(late, want))
-    assert all(torch.equal(a, b) for a, b in zip(again, want2))
+    side, cur = torch.cuda.Stream(), torch.cuda.default_stream()
+    if other == "the default stream":
+        side, cur = cur, side
+        assert side.cuda_stream == 0
+    cur.wait_stream(side)
+    with torch.cuda.stream(cur):
+        _busy()
+        trash = [torch.empty_like(t) for t in want for _ in range(2)]
+        for t in trash:
+            t.fill_(3)
+        del trash, t
+        got = calls(x, side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # read late, on the current stream, and freed before that
+        _busy()
+        late = [t.clone() for t in got]
+        del got
+        again = calls(x2, side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(late, want))
+        assert all(torch.equal(a, b) for a, b in zip(again, want2))
+
+
+def test_the_stream_that_a_handle_stands_for():
+    from wam_asp_w4a4_amd.layer import _made_for
+    dev, side = torch.device("cuda:0"), torch.cuda.Stream()
+    for cur, other in ((torch.cuda.default_stream(), side), (side, torch.cuda.default_stream())):
+        with torch.cuda.stream(cur):
+            for handle, want in ((None, cur), (cur.cuda_stream, cur), (other.cuda_stream, other)):
+                with _made_for(handle, dev):
+                    assert torch.cuda.current_stream().cuda_stream == want.cuda_stream
+            assert torch.cuda.current_stream() == cur

@@ -26,7 +26,9 @@ def _made_for(stream, device):
     if stream is None or device.type != "cuda" \
             or stream == torch._C._cuda_getCurrentRawStream(device.index):
         return _HERE
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device))
+    # the handle 0 is the default stream's; ExternalStream would make a new one of it
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if stream
+                             else torch.cuda.default_stream(device))
 
 
 def _lend(stream, *tensors):
