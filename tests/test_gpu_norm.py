@@ -611,3 +611,46 @@ def test_eight_bit_result_of_either_stream_and_of_wide_rows(M, C, dtype):
     codes, s = OF.quantize(host(n))
     np.testing.assert_array_equal(q.codes[live].cpu().numpy(), codes[c.live])
     np.testing.assert_array_equal(q.scales[:, live].cpu().numpy(), OF.layout_scales(s)[:, c.live])
+
+
+@pytest.mark.parametrize("C", [64, 8192])
+def test_the_most_sequences(C):
+    """65535 of them, most of one row: the gradients of a few of them alone."""
+    G, M = 65535, 66000
+    print(f"many sequences {M}x{C}", flush=True)
+    torch.manual_seed(C)
+    size = torch.ones(G, dtype=torch.int64)
+    size[::2000], size[1::2000] = 12, 0
+    offsets = torch.cat([torch.tensor([3]), 3 + size.cumsum(0)]).clamp(max=M).to(torch.int32)
+    x, y, dh, dn = (torch.randn((M, C), dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    table = torch.randn((G, 3, C), device=DEV) * 0.5
+    w = 1 + 0.2 * torch.randn(C, device=DEV)
+    kw = dict(post="rms", pre="layer", post_weight=w, weight=w, bias=w)
+    tables = dict(gate=table[:, 0], scale=table[:, 1], shift=table[:, 2])
+    at = offsets.to(DEV)
+    h, n = gated_norm(x, y, offsets=at, **tables, **kw)
+    g = gated_norm_backward(dh, dn, h, y, offsets=at, **tables, **kw)
+    for k in (0, 1, 2, 1999, 2000, 40000, 40001, G - 2, G - 1):
+        a, b = offsets[k].item(), offsets[k + 1].item()
+        one = {name: t[k:k + 1] for name, t in tables.items()}
+        if a == b:
+            assert not g.gate[k].any() and not g.scale[k].any() and not g.shift[k].any()
+            continue
+        part = slice(a, b)
+        want = gated_norm(x[part], y[part], **one, **kw)
+        assert torch.equal(h[part], want[0]) and torch.equal(n[part], want[1])
+        want = gated_norm_backward(dh[part], dn[part], h[part], y[part], **one, **kw)
+        assert torch.equal(g.dx[part], want.dx) and torch.equal(g.dy[part], want.dy)
+        for name in tables:   # up to 12 terms below 50 in two orders: 2 * 12 * U * 600 < 1e-3
+            assert torch.allclose(getattr(g, name)[k], getattr(want, name)[0], rtol=0, atol=1e-3), (name, k)
+    live = slice(offsets[0].item(), offsets[-1].item())
+    rows = torch.repeat_interleave(torch.arange(G), offsets.diff()).to(DEV)
+    m = torch.zeros(C, dtype=torch.float64, device=DEV)
+    mass = torch.zeros(C, dtype=torch.float64, device=DEV)
+    for i in range(0, rows.numel(), 8192):
+        r = slice(i, min(i + 8192, rows.numel()))
+        t = dn[live][r].double() * (1 + table[rows[r], 1].double())
+        m += t.sum(0)
+        mass += t.abs().sum(0)
+    # d bias = the sum of dn (1 + scale): each of the rows' and sequences' additions is off by at most U
+    assert ((g.bias.double() - m).abs() <= (M + G) * U * mass).all()

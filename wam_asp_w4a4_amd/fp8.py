@@ -28,7 +28,9 @@ _CODES = {torch.float32: B.ASP_F32, torch.bfloat16: B.ASP_BF16}
 
 
 def _no_capture():
-    """Autograd's own bookkeeping of eager leaves does not survive a capture."""
+    """Refused, since one case ends the process: a backward pass captured while an eager
+    graph of the same leaves still lives (their gradients are accumulated on the stream
+    that the eager graph noted, which is not being captured)."""
     if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
         raise RuntimeError("gradients under a graph capture: capture the explicit forward and "
                            "backward calls instead of autograd")
