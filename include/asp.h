@@ -523,7 +523,8 @@ int32_t asp_svdq_forward(const void* x, int32_t x_dtype, int64_t M, int64_t K, i
  *   scales, and those of its transpose (K x N), which the backward reads
  *   (codes_t and scales_t may both be NULL).
  * asp_fp8_dequantize: out (rows x cols, float32 or bf16) = the codes' values;
- *   exact but where a value is below the type's normal range.
+ *   exact but where a value is outside the type's normal range (the largest
+ *   float32 values round to 2^128, an infinity there and in the products).
  */
 #define ASP_FP8_BLOCK 128
 int32_t asp_fp8_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);

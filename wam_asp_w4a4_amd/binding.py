@@ -430,7 +430,7 @@ def launch(device, fn, *args):
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}, not on a GPU")
     torch = sys.modules["torch"]   # there, since `device` is one of its
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         status = fn(*args)
     else:
         with torch.cuda.device(device):

@@ -20,7 +20,7 @@ import torch
 from torch.autograd import forward_ad
 
 from . import binding as B
-from .layer import _Y_DTYPES, _check_ws, _check_y, _lend, _made_for
+from .layer import _Y_DTYPES, _check_ws, _check_y, _lend, _made_for, _new
 
 BLOCK = 128
 _NAMES = {torch.float32: "f32", torch.bfloat16: "bf16"}
@@ -137,8 +137,7 @@ class Fp8Tensor:
         if dtype not in _Y_DTYPES:
             raise ValueError(f"dtype must be 'f32' or 'bf16', not {dtype!r}")
         dev = self.codes.device
-        with _made_for(stream, dev):
-            out = torch.empty((self.rows, self.cols), dtype=_Y_DTYPES[dtype], device=dev)
+        out = _new(stream, dev, (self.rows, self.cols), _Y_DTYPES[dtype])
         B.launch(dev, B.lib().asp_fp8_dequantize, self.codes.data_ptr(), self.scales.data_ptr(),
                  self.rows, self.cols, out.data_ptr(), B.DTYPES[dtype], B.stream_on(stream, dev))
         _lend(stream, out)
@@ -238,19 +237,19 @@ class Fp8Layer:
         if y is not None or y_dtype not in _Y_DTYPES:
             _check_y(y, M, N, y_dtype, dev)
         else:
-            with _made_for(stream, dev):
-                made = y = torch.empty((M, N), dtype=_Y_DTYPES[y_dtype], device=dev)
+            made = y = _new(stream, dev, (M, N), _Y_DTYPES[y_dtype])
         have, ws = need, None
         if workspace is not None:
             _check_ws(workspace, need, dev)
             have, ws = workspace.numel(), workspace.data_ptr()
         elif need:
-            with _made_for(stream, dev):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _new(stream, dev, need, torch.uint8)
             ws = workspace.data_ptr()
         bias = self.bias
-        if bias is not None:   # a parameter may have been converted since it was checked
-            _check_vector(bias, "bias", N, dev)
+        if bias is not None:
+            # a parameter may have been converted since it was checked
+            if bias.dtype is not torch.float32 or bias.device != dev or bias.numel() != N:
+                _check_vector(bias, "bias", N, dev)
             bias = bias.data_ptr()
         wc, wsc, to = self.codes.data_ptr(), self.scales.data_ptr(), B.stream_on(stream, dev)
         if quantised:
@@ -259,7 +258,8 @@ class Fp8Layer:
         else:
             B.launch(dev, B.lib().asp_fp8_forward, x.data_ptr(), _CODES[x.dtype], ld, M, N, K, wc,
                      wsc, bias, y.data_ptr(), B.DTYPES[y_dtype], ws, have, to)
-        _lend(stream, made)
+        if stream is not None:
+            _lend(stream, made)
         return y
 
     def backward(self, dy, x=None, need_dx=True, need_db=None, dw_dtype="f32", workspace=None,
@@ -286,12 +286,11 @@ class Fp8Layer:
         need = B.asp_fp8_backward_workspace_bytes(M, N, K)
         if workspace is not None:
             _check_ws(workspace, need, dev)
-        with _made_for(stream, dev):
-            dx = torch.empty((M, K), dtype=_Y_DTYPES[dx_dtype], device=dev) if need_dx else None
-            dw = None if x is None else torch.empty((N, K), dtype=_Y_DTYPES[dw_dtype], device=dev)
-            db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
-            if workspace is None:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        else:
+            workspace = _new(stream, dev, need, torch.uint8)
+        dx = _new(stream, dev, (M, K), _Y_DTYPES[dx_dtype]) if need_dx else None
+        dw = None if x is None else _new(stream, dev, (N, K), _Y_DTYPES[dw_dtype])
+        db = _new(stream, dev, N) if need_db else None
         at = B._at
         B.launch(dev, B.lib().asp_fp8_backward, dy.data_ptr(), _CODES[dy.dtype], lddy, at(x),
                  B.ASP_F32 if x is None else _CODES[x.dtype], ldx, M, N, K, at(self.codes_t),

@@ -31,6 +31,14 @@ def _made_for(stream, device):
                              else torch.cuda.default_stream(device))
 
 
+def _new(stream, device, shape, dtype=torch.float32):
+    """An empty tensor for a call on `stream` (``_made_for``)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _made_for(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _lend(stream, *tensors):
     """Results made for a call on `stream` will be used on the current stream too: the
     allocator is told, so that their memory is not given away too early."""

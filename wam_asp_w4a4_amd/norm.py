@@ -20,7 +20,7 @@ import torch
 from . import binding as B
 from .fp8 import _CODES, Fp8Tensor, _check_rows, _check_vector, _float32, _no_capture, \
     _no_forward_mode, _row_major
-from .layer import _Y_DTYPES, _check_ws, _lend, _made_for
+from .layer import _Y_DTYPES, _check_ws, _lend, _made_for, _new
 
 KINDS = {"none": B.ASP_NORM_NONE, "rms": B.ASP_NORM_RMS, "layer": B.ASP_NORM_LAYER}
 
@@ -35,9 +35,6 @@ class NormGrads(NamedTuple):
     bias: torch.Tensor | None
     scale: torch.Tensor | None
     shift: torch.Tensor | None
-
-
-_WANT_ALL = dict.fromkeys(NormGrads._fields, True)
 
 
 def _spec(C, device, has_y, post, post_weight, gate, pre, weight, bias, scale, shift, offsets):
@@ -109,15 +106,13 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
     post, pre, G, ldt = _spec(C, dev, y is not None, post, post_weight, gate, pre, weight, bias,
                               scale, shift, offsets)
     made, zero = [], 0   # bits of the outputs made here: h, n
-    own = _made_for(stream, dev)
     write, ldh = h, C
     if h is not None:
         ldh = _check_rows(h, "h", M, C, dev, same)
     elif y is None and alpha == 1.0 and pre:
         h = x
     else:
-        with own:
-            write = h = torch.empty((M, C), dtype=x.dtype, device=dev)
+        write = h = _new(stream, dev, (M, C), x.dtype)
         made.append(h)
         zero = 1
     scales = None
@@ -129,7 +124,7 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
         if out not in (None, "fp8"):
             raise ValueError(f"out {out!r} with an Fp8Tensor n")
         if n is None:
-            with own:
+            with _made_for(stream, dev):
                 n = Fp8Tensor.empty(M, C, dev)
             made += [n.codes, n.scales]
             zero |= 2
@@ -145,8 +140,7 @@ def gated_norm(x, y=None, *, alpha=1.0, post="none", post_weight=None, gate=None
             raise ValueError(f"out must be 'f32', 'bf16' or 'fp8', not {out!r}")
         ldn = C
         if n is None:
-            with own:
-                n = torch.empty((M, C), dtype=x.dtype if out is None else _Y_DTYPES[out], device=dev)
+            n = _new(stream, dev, (M, C), x.dtype if out is None else _Y_DTYPES[out])
             made.append(n)
             zero |= 2
         else:
@@ -191,29 +185,25 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
         raise ValueError("neither dh nor dn is given")
     if y is None and dy is not None:
         raise ValueError("dy without y")
-    want = _WANT_ALL if need is None else {name: name in need for name in NormGrads._fields}
+    # the inputs whose gradients are wanted
+    wanted = NormGrads(h, y, post_weight, gate, weight, bias, scale, shift)
     if need is not None:
-        given = dict(dx=h, dy=y, post_weight=post_weight, gate=gate, weight=weight, bias=bias,
-                     scale=scale, shift=shift)
         for name in need:
-            if given.get(name) is None:
+            if name not in NormGrads._fields or getattr(wanted, name) is None:
                 raise ValueError(f"need names {name!r}: no gradient of a given input")
-        if dx is not None and not want["dx"] or dy is not None and not want["dy"]:
+        if dx is not None and "dx" not in need or dy is not None and "dy" not in need:
             raise ValueError("a tensor for a gradient that need does not name")
         if not need:
             return NormGrads(*8 * (None,))
+        wanted = NormGrads(*(t if name in need else None for name, t in wanted._asdict().items()))
     made, zero = [], 0   # bits of the outputs made here: dx, dy
 
-    own = _made_for(stream, dev)
-
     def new(shape, dtype=torch.float32):
-        with own:
-            made.append(torch.empty(shape, dtype=dtype, device=dev))
+        made.append(_new(stream, dev, shape, dtype))
         return made[-1]
 
-    def like(**inputs):
+    def like(*inputs):
         # one allocation for those of one shape
-        inputs = [t if want[name] else None for name, t in inputs.items()]
         given = [t for t in inputs if t is not None]
         if any(t.shape != given[0].shape for t in given):
             return [None if t is None else new(t.shape) for t in inputs]
@@ -222,23 +212,21 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
 
     if dx is not None:
         lddx = _check_rows(dx, "dx", M, C, dev, same)
-    elif want["dx"]:
+    elif wanted.dx is not None:
         dx = new((M, C), h.dtype)
         zero = 1
     if dy is not None:
         lddy = _check_rows(dy, "dy", M, C, dev, same)
-    elif y is not None and want["dy"]:
+    elif wanted.dy is not None:
         dy = new((M, C), h.dtype)
         zero |= 2
-    sums = [*like(post_weight=post_weight, weight=weight, bias=bias),
-            *like(gate=gate, scale=scale, shift=shift)]
-    d_post_weight, d_weight, d_bias, d_gate, d_scale, d_shift = sums
+    d_post_weight, d_weight, d_bias = like(wanted.post_weight, wanted.weight, wanted.bias)
+    d_gate, d_scale, d_shift = like(wanted.gate, wanted.scale, wanted.shift)
     size = 0
-    if any(t is not None for t in sums):
+    if not (d_post_weight is d_weight is d_bias is d_gate is d_scale is d_shift is None):
         size = B.asp_norm_gate_backward_workspace_bytes(M, C, G)
         if workspace is None:
-            with own:
-                workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+            workspace = _new(stream, dev, size, torch.uint8)
     if workspace is not None:
         _check_ws(workspace, size, dev)
     at = B._at
