@@ -2,7 +2,8 @@
 //
 // All are bound by memory: a bf16 matrix is read once (2 bytes an element) and
 // its codes written once (1 byte).  4096 x 4096 bf16 rows 11 us (4.6 TB/s); 8192 x 4096
-// dy and x, transposed codes of both and rows and column sums of dy, 53 us (4.4 TB/s).
+// dy and x, transposed codes of both and rows and column sums of dy, 53 us (4.4 TB/s); a
+// 4096 x 14336 bf16 weight, both forms, 47 us (5.0 TB/s).
 #include "asp_fp8.h"
 
 namespace asp {
@@ -209,7 +210,8 @@ __global__ void __launch_bounds__(64 * kTileWaves) k_fp8_tiles(const TileArgs a)
 
 // One lane for each 8 codes.  An E4M3 value times a power of two is exact in
 // float32 and in bf16 (four significant bits) but where it leaves the type's
-// range: below it the product rounds once, into the type's subnormals.
+// range: below it the product rounds once, into the type's subnormals.  Its stores are
+// an element each: 4096 x 14336 to bf16 72 us (2.4 TB/s).
 template <typename YT>
 __global__ void __launch_bounds__(256)
     k_fp8_dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
