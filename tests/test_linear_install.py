@@ -134,3 +134,16 @@ def test_a_layer_on_the_cpu_is_refused_before_launch(layer, monkeypatch):
         with pytest.raises(ValueError, match="GPU"):
             call()
     assert not reached
+
+
+def test_the_solve_and_the_search_refuse_cpu_tensors(monkeypatch):
+    from wam_asp_w4a4_amd import binding as B
+    from wam_asp_w4a4_amd.layer import smoothing_search, top_eigenspace
+    reached = []
+    for name in ("asp_top_eigenspace", "asp_smoothing_search"):
+        monkeypatch.setattr(B.lib(), name, lambda *a, name=name: reached.append(name) or 0)
+    for call in (lambda: top_eigenspace(torch.eye(256), torch.ones((256, 16)), 8, 4),
+                 lambda: smoothing_search(torch.ones((8, 256)), np.ones((64, 256), np.float32), None, None)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    assert not reached

@@ -230,6 +230,8 @@ def smoothing_grid():
 def smoothing_search(x, w, bias, v, candidates=None, stream=None):
     """Pick the layer's smoothing exponents by its own quantised output error on the
     calibration activations x (device, M x K).  Returns (alpha, beta, mse array, index)."""
+    if x.device.type != "cuda":
+        raise ValueError(f"x is on {x.device}, not on a GPU")
     cands = smoothing_grid() if candidates is None else list(candidates)
     M, K = x.shape
     N = w.shape[0]
@@ -252,6 +254,8 @@ def top_eigenspace(g, v0, r, iters, workspace=None, stream=None):
     K, p = v0.shape
     if tuple(g.shape) != (K, K):
         raise ValueError("g must be K x K with K = v0.shape[0]")
+    if g.device.type != "cuda" or v0.device != g.device:
+        raise ValueError(f"g is on {g.device}, v0 on {v0.device}, not on one GPU")
     nbytes = B.asp_top_eigenspace_workspace_bytes(K, p, r)
     with _made_for(stream, g.device):
         if workspace is None:
