@@ -391,6 +391,24 @@ def test_need_is_checked():
     assert norm.gated_norm_backward(x, x, x, need=[]) == (None,) * 8
 
 
+@pytest.mark.parametrize("x_type,y_dtype,dx,dw", [(torch.float32, None, 0, 0), (torch.bfloat16, None, 1, 1),
+                                                  (torch.float32, "bf16", 0, 1), (torch.bfloat16, "bf16", 1, 1),
+                                                  (torch.float32, "f32", 0, 0), (torch.bfloat16, "f32", 0, 0)])
+def test_gradients_have_the_bits_of_their_inputs(x_type, y_dtype, dx, dw, monkeypatch):
+    """The types that the module's backward asks the library for (0 float32, 1 bf16): a
+    gradient of a float32 x is not computed in bf16 because y is."""
+    calls = []
+    monkeypatch.setattr(B, "launch", lambda device, fn, *args: calls.append(args))
+    weight = torch.nn.Parameter(torch.zeros((64, 200), dtype=torch.bfloat16 if dw else torch.float32))
+    m = Fp8Linear(weight=weight, y_dtype=y_dtype)
+    x = torch.zeros((6, 200), dtype=x_type, requires_grad=True)
+    y = m(x)
+    assert y.dtype == {"f32": torch.float32, "bf16": torch.bfloat16, None: x_type}[y_dtype]
+    y.sum().backward()
+    assert calls[-1][12] == dx and calls[-1][14] == dw
+    assert x.grad.dtype == x_type and weight.grad.dtype == weight.dtype
+
+
 def test_result_types_are_checked():
     for call in (lambda: Fp8Linear(layer(), y_dtype="f16"), lambda: layer().forward(torch.zeros((4, 200)), "f16"),
                  lambda: layer().backward(torch.zeros((4, 64)), dx_dtype="f16"),

@@ -79,7 +79,8 @@ class _Fp8Apply(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, layer, y_dtype):
         ctx.layer = layer
-        # autograd rounds gradients that have more bits than their inputs
+        # the inputs' types; autograd rounds gradients that have more bits
+        ctx.dx_dtype = "f32" if y_dtype == "f32" else _NAMES[x.dtype]
         ctx.dw_dtype = "f32" if weight is None or y_dtype == "f32" else _NAMES[weight.dtype]
         ctx.save_for_backward(x if weight is not None and ctx.needs_input_grad[1] else None)
         return layer.forward(x, y_dtype)
@@ -91,7 +92,7 @@ class _Fp8Apply(torch.autograd.Function):
         x, = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx, dw, db = ctx.layer.backward(dy.contiguous(), x, need_dx=need[0], need_db=need[2],
-                                        dw_dtype=ctx.dw_dtype)
+                                        dw_dtype=ctx.dw_dtype, dx_dtype=ctx.dx_dtype)
         return dx, dw, db, None, None
 
 
