@@ -389,6 +389,15 @@ def test_need_is_checked():
         with pytest.raises(ValueError, match=why):
             norm.gated_norm_backward(x, x, x, **kw)
     assert norm.gated_norm_backward(x, x, x, need=[]) == (None,) * 8
+    assert norm.gated_norm_backward(x, x, x, need=iter(())) == (None,) * 8
+
+
+def test_need_may_be_read_once(monkeypatch):
+    monkeypatch.setattr(B, "launch", lambda *a: None)
+    x, w = torch.zeros((6, 32)), torch.ones(32)
+    g = norm.gated_norm_backward(x, x, x, weight=w, need=(name for name in ("dx", "weight")))
+    assert g.dx.shape == x.shape and g.weight.shape == w.shape
+    assert norm.gated_norm_backward(x, x, x, weight=w, need={"weight"}).dx is None
 
 
 @pytest.mark.parametrize("x_type,y_dtype,dx,dw", [(torch.float32, None, 0, 0), (torch.bfloat16, None, 1, 1),

@@ -188,6 +188,7 @@ def gated_norm_backward(dh, dn, h, y=None, *, alpha=1.0, post="none", post_weigh
     # the inputs whose gradients are wanted
     wanted = NormGrads(h, y, post_weight, gate, weight, bias, scale, shift)
     if need is not None:
+        need = tuple(need)
         for name in need:
             if name not in NormGrads._fields or getattr(wanted, name) is None:
                 raise ValueError(f"need names {name!r}: no gradient of a given input")
