@@ -72,3 +72,38 @@ def test_the_stream_that_a_handle_stands_for():
                 with _made_for(handle, dev):
                     assert torch.cuda.current_stream().cuda_stream == want.cuda_stream
             assert torch.cuda.current_stream() == cur
+
+
+def test_a_forked_stream_inside_a_capture():
+    """Calls on a stream that joined a capture make their tensors in the graph's memory:
+    replays give the eager results, with eager work in between."""
+    from wam_asp_w4a4_amd.fp8 import Fp8Layer
+    from wam_asp_w4a4_amd.norm import gated_norm, gated_norm_backward
+    torch.manual_seed(7)
+    layer = Fp8Layer.pack(torch.randn((300, 640), device=DEV), torch.randn(300, device=DEV))
+    x, dy = torch.randn((200, 640), device=DEV), torch.randn((200, 300), device=DEV)
+    w = torch.randn(640, device=DEV)
+
+    def calls(stream=None):
+        h, n = gated_norm(x, x, post="rms", weight=w, stream=stream)
+        return [h, n, layer.forward(n, stream=stream), *layer.backward(dy, n, stream=stream),
+                *gated_norm_backward(x, n, h, x, post="rms", weight=w, need=("dx", "weight"), stream=stream)[::4]]
+
+    calls()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        got = calls(side.cuda_stream)
+        cur.wait_stream(side)
+    for i in range(4):
+        x.copy_(torch.randn_like(x) * (i + 1))
+        dy.copy_(torch.randn_like(dy))
+        want = calls()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        trash = [torch.full_like(t, 9.0) for t in want for _ in range(3)]
+        del trash, want
