@@ -646,6 +646,168 @@ int32_t asp_norm_gate_backward(const void* dh, int64_t lddh, const void* dn, int
                                float* d_scale, float* d_shift, int64_t ldd, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* --------------------------------------------------- a block's attention */
+
+/*
+ * The norm of each head of the queries and keys, with the rotation by their
+ * positions, in one pass.  For a head's D elements v of token t:
+ *   u = norm(v) * w      ASP_NORM_RMS, ASP_NORM_LAYER (as in asp_norm_gate, over
+ *                        the D elements), or v itself (ASP_NORM_NONE)
+ *   y: the pairs (a, b) of u's first `rot` elements become
+ *      (a c - b s, a s + b c), c = cosine[p][i], s = sine[p][i] for pair i
+ *      and the token's position p; the others stay
+ *   ASP_ROTATE_PAIRS: pair i is (2i, 2i + 1); ASP_ROTATE_HALVES: (i, i + rot / 2)
+ *
+ *   q, k       device, T x Hq x D and T x Hk x D of `dtype`, heads contiguous,
+ *              token strides ldq, ldk and head strides hsq, hsk (elements, from
+ *              0).  k NULL with Hk = 0: queries alone
+ *   q_w, k_w   float32 of D entries, or NULL (ones)
+ *   cosine, sine   float32, P x rot / 2 (both or, with rot = 0, neither)
+ *   positions  int32 of T entries; NULL: token t has position t (P >= T).  A token
+ *              whose position is not in 0..P - 1 counts for nothing: its heads
+ *              are zeros in q_out where `zero` has bit 0 set and in k_out where
+ *              it has bit 1, else not written
+ *   q_out, k_out   of out_dtype, with strides of their own that keep heads
+ *              apart; q_out may be q itself and k_out k itself (same type and
+ *              strides)
+ *   D even, 2..256; rot even, 0..D; eps in [0, 1]; Hq, Hk up to 65535
+ * Any element alignment.  Inputs need not be finite: a NaN or infinity reaches
+ * its own head only.  Arithmetic is float32, rounded once.
+ */
+#define ASP_ROTATE_PAIRS 0
+#define ASP_ROTATE_HALVES 1
+int32_t asp_head_norm(const void* q, int64_t ldq, int64_t hsq, int32_t Hq, const void* k,
+                      int64_t ldk, int64_t hsk, int32_t Hk, int32_t dtype, int64_t T, int32_t D,
+                      int32_t norm, const float* q_w, const float* k_w, float eps,
+                      const float* cosine, const float* sine, int64_t P, int32_t rot,
+                      int32_t layout, const int32_t* positions, void* q_out, int64_t ldqo,
+                      int64_t hsqo, void* k_out, int64_t ldko, int64_t hsko, int32_t out_dtype,
+                      int32_t zero, void* stream);
+
+/*
+ * Its gradients from those of its results, dq and dk (d_dtype; strides of their
+ * own), and its inputs q and k.
+ *   dq_in, dk_in   device out of `dtype`, the gradients of q and k, or NULL; heads of
+ *              tokens that count for nothing are zeros or not written, by `zero`;
+ *              dq_in may be dq itself and dk_in dk itself (same type and strides)
+ *   d_q_w, d_k_w   float32 out of D entries, or NULL
+ * A tensor is read only where one of its two gradients is wanted, and which others are
+ * wanted does not change a gradient's bits.  The weights' sums have a fixed order: the
+ * same bits on every call.  T == 0 gives zero d_q_w and d_k_w.
+ *   workspace  device, asp_head_norm_backward_workspace_bytes bytes, 256-byte
+ *              aligned (not needed without d_q_w and d_k_w)
+ */
+int32_t asp_head_norm_backward_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                               size_t* bytes);
+int32_t asp_head_norm_backward(const void* dq, int64_t lddq, int64_t hsdq, const void* dk,
+                               int64_t lddk, int64_t hsdk, int32_t d_dtype, const void* q,
+                               int64_t ldq, int64_t hsq, int32_t Hq, const void* k, int64_t ldk,
+                               int64_t hsk, int32_t Hk, int32_t dtype, int64_t T, int32_t D,
+                               int32_t norm, const float* q_w, const float* k_w, float eps,
+                               const float* cosine, const float* sine, int64_t P, int32_t rot,
+                               int32_t layout, const int32_t* positions, void* dq_in,
+                               int64_t lddqi, int64_t hsdqi, void* dk_in, int64_t lddki,
+                               int64_t hsdki, int32_t zero, float* d_q_w, float* d_k_w,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of packed sequences whose queries and keys differ in number:
+ *   s = scale q k^T,  lse = log(sum exp(s)),  o = sum exp(s - lse) v
+ * over the keys of the query's sequence that count, with Hq / Hk consecutive query
+ * heads for each key head.  A query without such a key (or with none above
+ * -infinity) has o = 0 and lse = -infinity.
+ *   q, o       device, Tq x Hq x D of `dtype`; k, v: Tk x Hk x D.  Heads are
+ *              contiguous; token strides (ld, D to 2^22 elements) and head strides
+ *              (hs) are multiples of 16 bytes.  o may be q itself (same strides)
+ *   scale      above 0
+ *   q_offsets, kv_offsets   device int32, G + 1 entries, not decreasing: sequence g
+ *              has the queries q_offsets[g] .. q_offsets[g + 1] - 1 and the keys
+ *              kv_offsets[g] .. (either may be none).  NULL (G = 1): all of them.
+ *              Queries before the first and behind the last sequence count for
+ *              nothing: they are zeros in o where `zero` has bit 0 set and
+ *              -infinity in lse where it has bit 1, else not written
+ *   kv_lengths device int32, G entries, or NULL: only the first kv_lengths[g] keys
+ *              of sequence g count (at most those it has)
+ *   key_mask   device, Tk bytes, or NULL: a key whose byte is 0 does not count; its
+ *              elements reach no result, whatever they are
+ *   lse        device out float32 Tq x Hq, or NULL
+ *   D a multiple of 8, 8..128; Hq, Hk up to 65535
+ * Inputs need not be finite: a NaN reaches the queries that read it.  bf16: products
+ * of bf16 with float32 sums; exp(s - lse) is rounded to bf16 for its product with v.
+ * float32: float32 throughout.  The same bits on every call.
+ *   workspace  device, asp_attention_workspace_bytes bytes (may be 0), 256-byte
+ *              aligned: partial results where few queries have many keys
+ */
+int32_t asp_attention_workspace_bytes(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D,
+                                      int32_t G, size_t* bytes);
+int32_t asp_attention(const void* q, int64_t ldq, int64_t hsq, const void* k, int64_t ldk,
+                      int64_t hsk, const void* v, int64_t ldv, int64_t hsv, int32_t dtype,
+                      int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, float scale,
+                      int32_t G, const int32_t* q_offsets, const int32_t* kv_offsets,
+                      const int32_t* kv_lengths, const uint8_t* key_mask, void* o, int64_t ldo,
+                      int64_t hso, float* lse, int32_t zero, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients from that of o, with the forward's o and lse:
+ *   p = exp(s - lse),  ds = p (do v^T - sum(do o)),
+ *   dq = scale ds k,  dk = scale ds^T q,  dv = p^T do
+ * The heads that share keys add up in dk and dv.
+ *   dq, dk, dv device out of `dtype`, or NULL: not computed, which does not change
+ *              the bits of the others.  Queries of no sequence are zeros in dq where
+ *              `zero` has bit 0 set, keys of none in dk (bit 1) and dv (bit 2),
+ *              else not written; keys that do not count have zeros
+ * bf16: p and ds are rounded to bf16 for their products.  Sums have a fixed order:
+ * the same bits on every call.
+ *   workspace  device, asp_attention_backward_workspace_bytes bytes, 256-byte aligned
+ */
+int32_t asp_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk,
+                                               int32_t D, int32_t G, size_t* bytes);
+int32_t asp_attention_backward(const void* dout, int64_t lddo, int64_t hsdo, const void* q,
+                               int64_t ldq, int64_t hsq, const void* k, int64_t ldk, int64_t hsk,
+                               const void* v, int64_t ldv, int64_t hsv, const void* o, int64_t ldo,
+                               int64_t hso, const float* lse, int32_t dtype, int64_t Tq, int64_t Tk,
+                               int32_t Hq, int32_t Hk, int32_t D, float scale, int32_t G,
+                               const int32_t* q_offsets, const int32_t* kv_offsets,
+                               const int32_t* kv_lengths, const uint8_t* key_mask, void* dq,
+                               int64_t lddq, int64_t hsdq, void* dk, int64_t lddk, int64_t hsdk,
+                               void* dv, int64_t lddv, int64_t hsdv, int32_t zero, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * Keys and values held in 4 bits: `rows` rows of Hk heads of D elements (a multiple
+ * of 16, 16..128), each in the packed codes and block scales of the head of this file
+ * (blocks of 16 along a head): codes rows x Hk x D / 2 bytes, scales rows x Hk x D / 16.
+ * A block with a NaN or an infinity has the scale 0x7F and stands for NaN.
+ *
+ * asp_kv_store: k and v (device, T x Hk x D, any strides and element alignment) into a
+ *   cache.  The tokens offsets[g] .. offsets[g + 1] - 1 go to rows kv_offsets[g] +
+ *   kv_lengths[g] and on, up to row kv_offsets[g + 1] - 1: what has no room there is
+ *   dropped, and tokens of no sequence are not stored.  NULL (G = 1): all tokens,
+ *   rows 0 to rows - 1; kv_lengths NULL: 0.  No length is changed here.
+ * asp_kv_load: a cache's values (exact in both types) as rows x Hk x D of `dtype`;
+ *   k or v may be NULL.
+ * asp_attention_cache: asp_attention over a cache's values, which are exact in its
+ *   products; bf16 q: they are fp16 products, with exp(s - lse) rounded to fp16.
+ *   asp_attention_workspace_bytes has its workspace.
+ */
+int32_t asp_kv_store(const void* k, int64_t ldk, int64_t hsk, const void* v, int64_t ldv,
+                     int64_t hsv, int32_t dtype, int64_t T, int32_t Hk, int32_t D, int32_t G,
+                     const int32_t* offsets, const int32_t* kv_offsets, const int32_t* kv_lengths,
+                     int64_t rows, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                     uint8_t* v_scales, void* stream);
+int32_t asp_kv_load(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                    const uint8_t* v_scales, int64_t rows, int32_t Hk, int32_t D, void* k, void* v,
+                    int32_t dtype, void* stream);
+int32_t asp_attention_cache(const void* q, int64_t ldq, int64_t hsq, int32_t dtype,
+                            const uint8_t* k_codes, const uint8_t* k_scales,
+                            const uint8_t* v_codes, const uint8_t* v_scales, int64_t Tq, int64_t Tk,
+                            int32_t Hq, int32_t Hk, int32_t D, float scale, int32_t G,
+                            const int32_t* q_offsets, const int32_t* kv_offsets,
+                            const int32_t* kv_lengths, const uint8_t* key_mask, void* o,
+                            int64_t ldo, int64_t hso, float* lse, int32_t zero, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,9 +28,13 @@ Modules:
   fp8      -- the 8-bit format with a scale for each block of 128, and the linear
               layer on it, forward and backward.
   norm     -- the gated norms around a transformer block, forward and backward.
+  heads    -- the norms of queries and keys with the rotation by positions, forward and
+              backward.
+  attention -- attention of packed sequences, forward and backward.
 
 Every function here is pinned by tests under ``tests/test_oracle_*.py`` against
 closed forms, hand-derived vectors (``tests/golden/``), invariants and brute force.
 """
 
-from . import formats, hadamard, asp, smoothing, eigen, svdquant, fp8, norm  # noqa: F401
+from . import formats, hadamard, asp, smoothing, eigen, svdquant, fp8, norm, heads, \
+    attention  # noqa: F401

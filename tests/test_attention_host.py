@@ -1,0 +1,269 @@
+"""Refusals of the head norms, attention and the 4-bit cache (CPU: no call reaches a GPU)."""
+
+import ctypes
+
+import pytest
+import torch
+
+from wam_asp_w4a4_amd import binding as B
+from wam_asp_w4a4_amd.attention import Attention, Nvfp4Cache, attention, attention_backward
+from wam_asp_w4a4_amd.heads import HeadNorm, head_norm, head_norm_backward
+
+P = 4096   # an address that no check reads
+SHAPE, ARG, ALIGN, WORKSPACE = 2, 1, 3, 5
+
+
+def status(call, want):
+    with pytest.raises(B.ASPError) as e:
+        call()
+    assert e.value.status == want, (e.value.status, str(e.value))
+    assert str(e.value)
+
+
+def heads(**kw):
+    a = dict(q=P, ldq=128, hsq=64, Hq=2, k=P, ldk=128, hsk=64, Hk=2, dtype=1, T=4, D=64, norm=1, q_w=P, k_w=P,
+             eps=1e-6, cosine=P, sine=P, P=4, rot=64, layout=0, positions=None, q_out=P, ldqo=128, hsqo=64,
+             k_out=P, ldko=128, hsko=64, out_dtype=1, zero=0, stream=None)
+    a.update(kw)
+    B._check(B.lib().asp_head_norm(*a.values()))
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(dtype=7), ARG), (dict(out_dtype=2), ARG), (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE),
+    (dict(D=63), SHAPE), (dict(D=0), SHAPE), (dict(D=258), SHAPE), (dict(Hq=0), SHAPE), (dict(Hq=65536), SHAPE),
+    (dict(Hk=-1), SHAPE), (dict(Hk=0), ARG), (dict(norm=3), ARG), (dict(norm=0), ARG), (dict(eps=-1.0), ARG),
+    (dict(eps=float("nan")), ARG), (dict(layout=2), ARG), (dict(rot=66), SHAPE), (dict(rot=63), SHAPE),
+    (dict(rot=-2), SHAPE), (dict(rot=0), ARG), (dict(sine=None), ARG), (dict(P=3), SHAPE), (dict(P=1 << 31), SHAPE),
+    (dict(cosine=P + 2), ALIGN), (dict(positions=P + 1), ALIGN), (dict(q_w=P + 1), ALIGN), (dict(zero=4), ARG),
+    (dict(q=None), ARG), (dict(k_out=None), ARG), (dict(q=P + 1), ALIGN), (dict(ldq=-1), SHAPE),
+    (dict(hsqo=32), SHAPE), (dict(ldqo=64), SHAPE), (dict(ldko=1 << 31), SHAPE)])
+def test_head_norm_arguments(kw, want):
+    status(lambda: heads(**kw), want)
+
+
+def heads_back(**kw):
+    a = dict(dq=P, lddq=128, hsdq=64, dk=P, lddk=128, hsdk=64, d_dtype=1, q=P, ldq=128, hsq=64, Hq=2, k=P, ldk=128,
+             hsk=64, Hk=2, dtype=1, T=4, D=64, norm=1, q_w=P, k_w=P, eps=1e-6, cosine=P, sine=P, P=4, rot=64,
+             layout=0, positions=None, dq_in=P, lddqi=128, hsdqi=64, dk_in=P, lddki=128, hsdki=64, zero=0,
+             d_q_w=P, d_k_w=P, workspace=P, workspace_bytes=1 << 20, stream=None)
+    a.update(kw)
+    B._check(B.lib().asp_head_norm_backward(*a.values()))
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(d_dtype=2), ARG), (dict(norm=0), ARG), (dict(dq=None), ARG), (dict(dk=P + 1), ALIGN),
+    (dict(zero=1, dq_in=None), ARG), (dict(zero=8), ARG), (dict(hsdqi=8), SHAPE), (dict(workspace=None), ARG),
+    (dict(workspace=P + 8), ALIGN), (dict(workspace_bytes=16), WORKSPACE), (dict(Hk=0), ARG),
+    (dict(d_q_w=P + 2), ALIGN)])
+def test_head_norm_backward_arguments(kw, want):
+    status(lambda: heads_back(**kw), want)
+
+
+def attend(**kw):
+    a = dict(q=P, ldq=128, hsq=64, k=P, ldk=128, hsk=64, v=P, ldv=128, hsv=64, dtype=1, Tq=4, Tk=5, Hq=2, Hk=2, D=64,
+             scale=0.125, G=1, q_offsets=None, kv_offsets=None, kv_lengths=None, key_mask=None, o=P, ldo=128, hso=64,
+             lse=P, zero=0, workspace=None, workspace_bytes=0, stream=None)
+    a.update(kw)
+    B._check(B.lib().asp_attention(*a.values()))
+
+
+BOTH = [(dict(dtype=2), ARG), (dict(Tq=-1), SHAPE), (dict(Tk=1 << 31), SHAPE), (dict(Hq=3), SHAPE), (dict(Hk=0), SHAPE),
+        (dict(Hq=65536, Hk=1), SHAPE), (dict(D=60), SHAPE), (dict(D=136), SHAPE), (dict(D=0), SHAPE),
+        (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG),
+        (dict(scale=float("inf")), ARG), (dict(G=0), SHAPE), (dict(G=65536, q_offsets=P, kv_offsets=P), SHAPE),
+        (dict(G=2), ARG), (dict(G=2, q_offsets=P), ARG), (dict(q_offsets=P + 2), ALIGN), (dict(kv_lengths=P + 1), ALIGN),
+        (dict(q=None), ARG), (dict(q=P + 2), ALIGN), (dict(ldq=132), ALIGN), (dict(hsq=4), ALIGN),
+        (dict(ldq=1 << 23), SHAPE), (dict(ldq=56), SHAPE), (dict(lse=P + 2), ALIGN)]
+
+
+@pytest.mark.parametrize("kw, want", BOTH + [
+    (dict(zero=4), ARG), (dict(zero=2, lse=None), ARG), (dict(o=None), ARG), (dict(v=None), ARG), (dict(k=P + 8), ALIGN),
+    (dict(ldo=64), SHAPE), (dict(ldk=1 << 23), SHAPE), (dict(ldv=0), SHAPE),
+    # few queries of many keys are split: partial results in a workspace
+    (dict(Tq=1, Tk=1 << 16), ARG), (dict(Tq=1, Tk=1 << 16, workspace=P, workspace_bytes=256), WORKSPACE)])
+def test_attention_arguments(kw, want):
+    status(lambda: attend(**kw), want)
+
+
+def cached(**kw):
+    a = dict(q=P, ldq=128, hsq=64, dtype=1, k_codes=P, k_scales=P, v_codes=P, v_scales=P, Tq=4, Tk=5, Hq=2, Hk=2, D=64,
+             scale=0.125, G=1, q_offsets=None, kv_offsets=None, kv_lengths=None, key_mask=None, o=P, ldo=128, hso=64,
+             lse=P, zero=0, workspace=None, workspace_bytes=0, stream=None)
+    a.update(kw)
+    B._check(B.lib().asp_attention_cache(*a.values()))
+
+
+@pytest.mark.parametrize("kw, want", BOTH + [
+    (dict(D=72, ldq=144, hsq=72, ldo=144, hso=72), SHAPE), (dict(k_codes=None), ARG), (dict(v_scales=P + 8), ALIGN)])
+def test_cached_attention_arguments(kw, want):
+    status(lambda: cached(**kw), want)
+
+
+def attend_back(**kw):
+    a = dict(dout=P, lddo=128, hsdo=64, q=P, ldq=128, hsq=64, k=P, ldk=128, hsk=64, v=P, ldv=128, hsv=64, o=P, ldo=128,
+             hso=64, lse=P, dtype=1, Tq=4, Tk=5, Hq=2, Hk=2, D=64, scale=0.125, G=1, q_offsets=None, kv_offsets=None,
+             kv_lengths=None, key_mask=None, dq=P, lddq=128, hsdq=64, dk=P, lddk=128, hsdk=64, dv=P, lddv=128, hsdv=64,
+             zero=0, workspace=P, workspace_bytes=1 << 20, stream=None)
+    a.update(kw)
+    B._check(B.lib().asp_attention_backward(*a.values()))
+
+
+@pytest.mark.parametrize("kw, want", BOTH + [
+    (dict(lse=None), ARG), (dict(zero=8), ARG), (dict(zero=4, dv=None), ARG), (dict(dout=None), ARG), (dict(o=P + 4), ALIGN),
+    (dict(dk=P + 4), ALIGN), (dict(lddk=64), SHAPE), (dict(workspace=None), ARG), (dict(workspace_bytes=8), WORKSPACE)])
+def test_attention_backward_arguments(kw, want):
+    status(lambda: attend_back(**kw), want)
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(dtype=2), ARG), (dict(T=-1), SHAPE), (dict(Hk=0), SHAPE), (dict(D=24), SHAPE), (dict(D=144), SHAPE), (dict(G=0), SHAPE),
+    (dict(G=2), ARG), (dict(offsets=P + 1), ALIGN), (dict(rows=-1), SHAPE), (dict(k=None), ARG), (dict(v=P + 1), ALIGN),
+    (dict(ldk=-1), SHAPE), (dict(v_codes=P + 8), ALIGN), (dict(k_scales=None), ARG)])
+def test_store_arguments(kw, want):
+    a = dict(k=P, ldk=128, hsk=64, v=P, ldv=128, hsv=64, dtype=1, T=4, Hk=2, D=64, G=1, offsets=None, kv_offsets=None,
+             kv_lengths=None, rows=9, k_codes=P, k_scales=P, v_codes=P, v_scales=P, stream=None)
+    a.update(kw)
+    status(lambda: B._check(B.lib().asp_kv_store(*a.values())), want)
+
+
+@pytest.mark.parametrize("kw, want", [(dict(dtype=2), ARG), (dict(D=8), SHAPE), (dict(Hk=0), SHAPE), (dict(rows=1 << 31), SHAPE),
+                                      (dict(k=P + 8), ALIGN), (dict(v_codes=None), ARG)])
+def test_load_arguments(kw, want):
+    a = dict(k_codes=P, k_scales=P, v_codes=P, v_scales=P, rows=3, Hk=2, D=64, k=P, v=P, dtype=1, stream=None)
+    a.update(kw)
+    status(lambda: B._check(B.lib().asp_kv_load(*a.values())), want)
+
+
+def test_calls_without_work_need_nothing():
+    heads(T=0, q=None, k=None, q_out=None, k_out=None)
+    heads_back(dq_in=None, dk_in=None, d_q_w=None, d_k_w=None, q=None)
+    attend(Tq=0, q=None, o=None)
+    cached(Tq=0, q=None, o=None)
+    attend_back(dq=None, dk=None, dv=None, q=None)
+    b = B.lib()
+    assert b.asp_kv_store(None, 0, 0, None, 0, 0, 1, 0, 1, 64, 1, None, None, None, 4, None, None, None, None, None) == 0
+    assert b.asp_kv_load(None, None, None, None, 4, 1, 64, None, None, 1, None) == 0
+
+
+def test_workspace_sizes():
+    assert B.asp_attention_workspace_bytes(4096, 4096, 16, 16, 128, 1) == 0
+    one = B.asp_attention_workspace_bytes(1, 1 << 16, 2, 2, 64, 1)
+    assert one > 0 and one % 256 == 0
+    assert B.asp_attention_backward_workspace_bytes(10, 10, 4, 2, 64, 1) >= 10 * 4 * 8
+    assert B.asp_head_norm_backward_workspace_bytes(100, 4, 2, 64) >= 2 * 64 * 4
+    for fn, args in (("asp_attention_workspace_bytes", (1, 1, 1, 1, 64, 1)), ("asp_attention_backward_workspace_bytes", (1, 1, 1, 1, 64, 1)),
+                     ("asp_head_norm_backward_workspace_bytes", (1, 1, 1, 64))):
+        status(lambda: B._check(getattr(B.lib(), fn)(*args, None)), ARG)
+        status(lambda: B._check(getattr(B.lib(), fn)(-1, *args[1:], ctypes.byref(ctypes.c_size_t()))), SHAPE)
+
+
+# --------------------------------------------------------------- the Python layer
+
+
+def t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def refused(kind, match, call):
+    with pytest.raises(kind, match=match):
+        call()
+
+
+def test_tensors_on_the_cpu_are_refused():
+    q, k, f = t(4, 2, 64), t(5, 2, 64), t(4, 2, dtype=torch.float32)
+    tab = t(4, 32, dtype=torch.float32)
+    for call in (lambda: head_norm(q, cos=tab, sin=tab), lambda: head_norm_backward(q, None, q), lambda: attention(q, k, k),
+                 lambda: attention_backward(q, q, k, k, q, f), lambda: Nvfp4Cache.empty(4, 2, 64, "cpu").store(q, q),
+                 lambda: Nvfp4Cache.empty(4, 2, 64, "cpu").dequantize(), lambda: attention(q, Nvfp4Cache.empty(4, 2, 64, "cpu")),
+                 lambda: HeadNorm(64)(q), lambda: Attention()(q, k, k)):
+        refused(ValueError, "not on a GPU", call)
+
+
+def test_head_norm_refusals():
+    q, k, w = t(4, 2, 64), t(4, 1, 64), t(64, dtype=torch.float32)
+    tab, pos = t(9, 16, dtype=torch.float32), ints(0, 1, 2, 3)
+    for kind, match, args, kw in [
+            (ValueError, "3-D", (t(4, 64),), {}), (ValueError, "k must be", (q, t(3, 1, 64)), {}),
+            (TypeError, "k must be", (q, k.float()), {}), (ValueError, "contiguous", (t(4, 64, 2).transpose(1, 2),), {}),
+            (TypeError, "q must be", (q.half(),), {}), (ValueError, "norm must", (q,), dict(norm="l2")),
+            (ValueError, "layout must", (q,), dict(layout="x")), (ValueError, "need a norm", (q,), dict(norm="none", q_weight=w)),
+            (ValueError, "without k", (q,), dict(k_weight=w)), (TypeError, "float32", (q,), dict(q_weight=w.double())),
+            (ValueError, "q_weight", (q,), dict(q_weight=w[:32])), (ValueError, "belong", (q,), dict(cos=tab)),
+            (ValueError, "positions without", (q,), dict(positions=pos)), (TypeError, "cos must", (q,), dict(cos=tab.double(), sin=tab)),
+            (ValueError, "sin must", (q,), dict(cos=tab, sin=tab[:4])), (ValueError, "1 to 32", (q,), dict(cos=t(9, 33, dtype=torch.float32), sin=tab)),
+            (ValueError, "tables of 3", (q,), dict(cos=tab[:3], sin=tab[:3])), (TypeError, "int32", (q,), dict(cos=tab, sin=tab, positions=pos.long())),
+            (ValueError, "4 contiguous", (q,), dict(cos=tab, sin=tab, positions=pos[:3])), (ValueError, "out must", (q,), dict(out="fp8")),
+            (ValueError, "k_out without", (q,), dict(k_out=k)), (ValueError, "q_out must", (q,), dict(q_out=t(4, 1, 64))),
+            (TypeError, "q_out must", (q,), dict(q_out=q, out="f32")), (TypeError, "q_out must", (q,), dict(q_out=q.half())),
+            (TypeError, "torch tensor", (q,), dict(q_out=3))]:
+        refused(kind, match, lambda: head_norm(*args, **kw))
+    for kind, match, kw in [(ValueError, "need names", dict(need=["x"])), (ValueError, "need names", dict(need=["dk"])),
+                            (ValueError, "not wanted", dict(need=["q_weight"], q_weight=w, dq_in=q)),
+                            (TypeError, "dq_in must", dict(dq_in=q.float())), (TypeError, "uint8", dict(q_weight=w, workspace=w)),
+                            (ValueError, "workspace holds", dict(q_weight=w, workspace=torch.zeros(1, dtype=torch.uint8)))]:
+        refused(kind, match, lambda: head_norm_backward(q, None, q, **kw))
+    refused(TypeError, "dq must", lambda: head_norm_backward(None, None, q))
+    refused(TypeError, "dk must", lambda: head_norm_backward(q, k.float(), q, k))
+    assert head_norm_backward(q, None, q, need=()) == (None, None, None, None)
+    m = HeadNorm(64)
+    refused(ValueError, "q must be", lambda: m(t(4, 2, 32)))
+    refused(ValueError, "same tokens", lambda: m(q, t(3, 1, 64)))
+    refused(ValueError, "positions must", lambda: m(t(2, 4, 2, 64), cos=tab, sin=tab, positions=ints(1, 2)))
+    refused(ValueError, "no gradient", lambda: m(q, cos=tab.clone().requires_grad_(), sin=tab))
+    refused(ValueError, "norm must", lambda: HeadNorm(64, norm="x"))
+    refused(ValueError, "layout must", lambda: HeadNorm(64, layout="x"))
+
+
+def test_attention_refusals():
+    q, k, f = t(4, 2, 64), t(5, 2, 64), t(4, 2, dtype=torch.float32)
+    o2 = ints(0, 2, 4)
+    for kind, match, args, kw in [
+            (ValueError, "3-D", (t(4, 64), k, k), {}), (TypeError, "k must be", (q, k.float(), k), {}), (TypeError, "v must be", (q, k), {}),
+            (ValueError, "v must be", (q, k, t(4, 2, 64)), {}), (ValueError, "multiple of", (q, t(5, 3, 64), t(5, 3, 64)), {}),
+            (ValueError, "aligned", (t(4, 2, 66)[..., 1:65], k, k), {}), (ValueError, "aligned", (q, t(5, 2, 68)[..., :64], k), {}),
+            (ValueError, "overlap", (q, t(1, 2, 64).expand(5, 2, 64), k), {}), (ValueError, "belong", (q, k, k), dict(q_offsets=o2)),
+            (TypeError, "int32", (q, k, k), dict(q_offsets=o2.long(), kv_offsets=o2)), (ValueError, "kv_offsets", (q, k, k), dict(q_offsets=o2, kv_offsets=o2[:2])),
+            (ValueError, "q_offsets", (q, k, k), dict(q_offsets=o2[:1], kv_offsets=o2)), (ValueError, "kv_lengths", (q, k, k), dict(kv_lengths=o2)),
+            (TypeError, "key_mask", (q, k, k), dict(key_mask=o2)), (ValueError, "key_mask", (q, k, k), dict(key_mask=torch.ones(4, dtype=torch.bool))),
+            (ValueError, "scale", (q, k, k), dict(scale=0.0)), (ValueError, "scale", (q, k, k), dict(scale=float("nan"))),
+            (TypeError, "o must be", (q, k, k), dict(o=q.float())), (TypeError, "lse", (q, k, k), dict(lse=q)), (ValueError, "lse", (q, k, k), dict(lse=f[:3])),
+            (TypeError, "uint8", (q, k, k), dict(workspace=f))]:
+        refused(kind, match, lambda: attention(*args, **kw))
+    for kind, match, kw in [(ValueError, "need names", dict(need=["dx"])), (ValueError, "does not name", dict(need=["dq"], dk=k)),
+                            (TypeError, "dv must", dict(dv=k.float())), (ValueError, "workspace holds", dict(workspace=torch.zeros(8, dtype=torch.uint8)))]:
+        refused(kind, match, lambda: attention_backward(q, q, k, k, q, f, **kw))
+    refused(TypeError, "do must", lambda: attention_backward(q.float(), q, k, k, q, f))
+    refused(ValueError, "lse", lambda: attention_backward(q, q, k, k, q, f[:2]))
+    assert attention_backward(q, q, k, k, q, f, need=()) == (None, None, None)
+    m = Attention()
+    refused(ValueError, "must be", lambda: m(t(64), k, k))
+    refused(ValueError, "k and v must", lambda: m(t(2, 4, 2, 64), t(1, 4, 2, 64), t(1, 4, 2, 64)))
+    refused(ValueError, "v must", lambda: m(t(2, 4, 2, 64), t(2, 4, 2, 64), t(2, 5, 2, 64)))
+    refused(ValueError, "key_mask must", lambda: m(t(2, 4, 2, 64), t(2, 4, 2, 64), t(2, 4, 2, 64), key_mask=torch.ones(4)))
+    refused(ValueError, "packed", lambda: m(t(2, 4, 2, 64), t(2, 4, 2, 64), t(2, 4, 2, 64), q_offsets=o2, kv_offsets=o2))
+    refused(ValueError, "scale", lambda: Attention(scale=-1.0))
+
+
+def test_cache_refusals():
+    c = Nvfp4Cache.empty(6, 2, 64, "cpu")
+    assert (c.rows, c.heads, c.head_dim) == (6, 2, 64)
+    refused(ValueError, "multiple of 16", lambda: Nvfp4Cache.empty(6, 2, 24, "cpu"))
+    refused(TypeError, "uint8", lambda: Nvfp4Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales.int()))
+    refused(ValueError, "needs contiguous", lambda: Nvfp4Cache(c.k_codes, c.k_scales[:5], c.v_codes, c.v_scales))
+    refused(ValueError, "codes must", lambda: Nvfp4Cache(c.k_codes[..., :4], c.k_scales, c.v_codes, c.v_scales))
+    k = t(4, 2, 64)
+    for kind, match, args, kw in [(ValueError, "k must be", (t(4, 1, 64), k), {}), (ValueError, "v must be", (k, t(3, 2, 64)), {}),
+                                  (TypeError, "v must be", (k, k.float()), {}), (ValueError, "belong", (k, k), dict(offsets=ints(0, 4))),
+                                  (ValueError, "kv_offsets", (k, k), dict(offsets=ints(0, 4), kv_offsets=ints(0, 2, 6))),
+                                  (ValueError, "kv_lengths", (k, k), dict(kv_lengths=ints(0, 4)))]:
+        refused(kind, match, lambda: c.store(*args, **kw))
+    refused(ValueError, "dtype", lambda: c.dequantize("fp8"))
+    refused(ValueError, "v with a cache", lambda: attention(k, c, k))
+    refused(ValueError, "heads of 64", lambda: attention(t(4, 2, 32), c))
+    refused(TypeError, "no gradients", lambda: attention_backward(k, k, c, k, k, t(4, 2, dtype=torch.float32)))
+    refused(ValueError, "cache and offsets", lambda: Attention()(t(1, 4, 2, 64), c))
+    refused(RuntimeError, "no gradients", lambda: Attention()(k.float().requires_grad_(), c))

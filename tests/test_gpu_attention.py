@@ -1,0 +1,613 @@
+"""Attention, its gradients and the 4-bit cache against the float64 oracle, through the public
+Python layer.
+
+Gates (from the arithmetic; u = 2^-24 the half step of float32, h that of the products' type:
+2^-8 for bf16, 2^-11 for fp16 over a cache, and no rounding beside u in float32):
+* a score is a sum of D products, off by (D + 8) u of scale sum|q||k|; its exponent's argument is
+  rounded on the way to base 2, 4 u of |s| + |lse|; 2^x itself is off by 4 u.  So p is off by
+  e p, e = (D + 8) u scale sum|q||k| + 4 u (|s| + |lse| + 1), of the row's largest such sum;
+* o: p is rounded by h for its product but not in its sum, and sums of n keys are off by n u of their
+  magnitudes: (h + 2 e + (n + 8) u) sum p|v|, and the result's own half step.  lse: e + 8 u;
+* ds = p (dp - delta) is off by e|ds| + D u p (sum|do||v| + sum|do||o|) + h|ds|, dq by the sum of
+  that with scale|k| (+ n u of magnitudes); dk likewise over the rows, dv as o.
+* what is below 2^-126 counts as zero (float32's and bf16's smallest normal number): each p, ds and
+  result may lose as much, and p's loss meets the same factors as p.
+A cache's fp16 queries are scaled to 2^13 and more, so rounding them costs less than u of
+the row's largest element: D u of scale max|q| sum|k| more.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as O
+from oracle import formats as F
+from wam_asp_w4a4_amd.attention import Attention, Nvfp4Cache, attention, attention_backward
+from wam_asp_w4a4_amd.heads import HeadNorm, head_norm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+TINY = 2.0 ** -126
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def ints(v):
+    return None if v is None else torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def near(got, want, bound, step, what=""):
+    assert np.isfinite(got).all(), what
+    off = np.abs(got - want) - (bound + step * (np.abs(want) + bound))
+    assert not off.size or off.max() <= 0, (what, off.max())
+
+
+class Case:
+    def __init__(self, Tq, Tk, Hq, Hk, D, dtype="bf16", qo=None, ko=None, kl=None, mask=None, scale=None, layout="fused", sharp=1.0,
+                 seed=0, cache=False):
+        g = torch.Generator(device=DEV).manual_seed(Tq * 7919 + Tk * 31 + D + seed)
+        rnd = lambda *s: torch.randn(s, generator=g, device=DEV)
+        t = TYPES[dtype]
+        self.dtype, self.t, self.D, self.Hq, self.Hk = dtype, t, D, Hq, Hk
+        self.scale = D ** -0.5 if scale is None else scale
+        self.q = (rnd(Tq, Hq, D) * sharp).to(t)
+        self.do = rnd(Tq, Hq, D).to(t)
+        kv = rnd(Tk, 2, Hk, D).to(t)
+        self.k, self.v = kv[:, 0], kv[:, 1]
+        if layout == "heads":        # by head first
+            self.q, self.k, self.v, self.do = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (self.q, self.k, self.v, self.do))
+        elif layout == "padded":     # rows and heads apart
+            def apart(x):
+                e = 16 // x.element_size()
+                y = torch.full((x.shape[0], x.shape[1] + 1, x.shape[2] + e), float("nan"), dtype=t, device=DEV)
+                y = y[:, :x.shape[1], :x.shape[2]]
+                return y.copy_(x)
+            self.q, self.k, self.v, self.do = map(apart, (self.q, self.k, self.v, self.do))
+        if isinstance(mask, float):
+            mask = torch.rand((Tk,), generator=g, device=DEV) < mask
+        self.lists = dict(q_offsets=qo, kv_offsets=ko, kv_lengths=kl)
+        self.mask = None if mask is None else torch.as_tensor(mask, device=DEV).bool()
+        self.kw = dict(scale=scale, key_mask=self.mask, **{n: ints(v) for n, v in self.lists.items()})
+        self.ok = O.allowed(Tq, Tk, key_mask=None if mask is None else self.mask.cpu().numpy(), **self.lists)
+        self.owned = np.zeros(Tq, bool)
+        self.owned[slice(0, Tq) if qo is None else slice(qo[0], qo[-1])] = True
+        self.cache = None
+        if cache:
+            self.cache = Nvfp4Cache.empty(Tk, Hk, D, DEV)
+            self.cache.store(self.k, self.v)
+            self.k, self.v = self.cache.dequantize("f32")
+
+    def errors(self):
+        """(s, |s| bounds' e by head, query and key)"""
+        q, k = host(self.q), host(self.k)
+        keep = self.ok.any(axis=0)[:, None, None]
+        k = np.where(keep, k, 0.0)
+        mag = np.stack([np.abs(q[:, h]) @ np.abs(k[:, h // (self.Hq // self.Hk)]).T for h in range(self.Hq)]) * self.scale
+        if self.cache is not None and self.dtype == "bf16":
+            mag = mag + np.stack([np.abs(q[:, h]).max(1, keepdims=True) * np.abs(k[:, h // (self.Hq // self.Hk)]).sum(1)[None]
+                                  for h in range(self.Hq)]) * self.scale
+        return mag
+
+    def check_forward(self, result=None):
+        o, lse = result or attention(self.q, *((self.cache,) if self.cache is not None else (self.k, self.v)), **self.kw)
+        torch.cuda.synchronize()
+        q, k, v = host(self.q), host(self.k), host(self.v)
+        want, wlse = O.forward(q, k, v, self.ok, self.scale)
+        mag = self.errors()
+        s = O.scores(q, k, self.ok, self.scale)
+        p = O.weights(s, wlse)
+        n = self.ok.sum(axis=1).max(initial=0)
+        h = 0.0 if self.dtype == "f32" else 2.0 ** -11 if self.cache is not None else 2.0 ** -8
+        dead = np.where(self.ok, 0.0, -np.inf)
+        for head in range(self.Hq):
+            l = np.where(np.isfinite(wlse[:, head]), wlse[:, head], 0.0)
+            e = (self.D + 8) * U * mag[head].max(axis=1, initial=0.0) + 4 * U * (2 * np.abs(l) + 20 + mag[head].max(axis=1, initial=0.0))
+            vals = np.where(self.ok.any(axis=0)[:, None], np.abs(v[:, head // (self.Hq // self.Hk)]), 0.0)
+            bound = (h + 2 * e[:, None] + (n + 8) * U) * (p[head] @ vals) + TINY * (1 + vals.sum(axis=0))
+            live = self.owned
+            near(host(o)[live, head], want[live, head], bound[live], STEP[self.dtype], f"o of head {head}")
+            got = host(lse)[:, head]
+            some = np.isfinite(wlse[:, head])
+            assert (got[~some] == -np.inf).all()
+            near(got[some], wlse[some, head], (e + 8 * U * (1 + np.abs(l)))[some], 0.0, "lse")
+        none = ~self.ok.any(axis=1)
+        assert not host(o)[none].any()
+        self.o, self.lse = o, lse
+        return o, lse
+
+    def check_backward(self, result=None):
+        if not hasattr(self, "o"):
+            self.o, self.lse = attention(self.q, self.k, self.v, **self.kw)
+        g = result or attention_backward(self.do, self.q, self.k, self.v, self.o, self.lse, **self.kw)
+        torch.cuda.synchronize()
+        q, k, v, o, do, lse = map(host, (self.q, self.k, self.v, self.o, self.do, self.lse))
+        want = O.backward(do, q, k, v, o, lse, self.ok, self.scale)
+        Hq, group = self.Hq, self.Hq // self.Hk
+        mag, s = self.errors(), O.scores(q, k, self.ok, self.scale)
+        p = O.weights(s, lse)
+        keep = self.ok.any(axis=0)[:, None]
+        n = max(self.ok.sum(axis=1).max(initial=0), self.ok.sum(axis=0).max(initial=0) * group)
+        h = 0.0 if self.dtype == "f32" else 2.0 ** -8
+        bounds = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)]
+        for head in range(Hq):
+            kh, vh = (np.where(keep, np.abs(t[:, head // group]), 0.0) for t in (k, v))
+            l = np.where(np.isfinite(lse[:, head]), np.abs(lse[:, head]), 0.0)[:, None]
+            e = (self.D + 8) * U * mag[head] + 4 * U * (2 * l + 20 + mag[head])
+            ad, ao = np.abs(do[:, head]), np.abs(o[:, head])
+            raw = ad @ vh.T + (ad * ao).sum(axis=1, keepdims=True)
+            ds = np.abs(p[head]) * raw
+            eds = ds * (e + (self.D + 8) * U + h + (n + 8) * U) + TINY * (1 + raw) * self.ok
+            bounds[0][:, head] = self.scale * eds @ kh
+            bounds[1][:, head // group] += self.scale * eds.T @ np.abs(q[:, head])
+            bounds[2][:, head // group] += (p[head] * (e + h + (n + 8) * U) + TINY * self.ok).T @ ad
+        for name, a, b, c in zip(g._fields, g, want, bounds):
+            if a is not None:
+                near(host(a), b, c + TINY, STEP[self.dtype], name)
+        return g
+
+
+LENGTHS = [  # Tq, Tk, Hq, Hk, D
+    (1, 1, 1, 1, 8), (1, 70, 8, 2, 64), (31, 33, 2, 2, 40), (32, 64, 4, 1, 128), (65, 63, 3, 1, 72), (128, 127, 2, 2, 96),
+    (130, 129, 6, 2, 80), (3, 1500, 4, 2, 128), (300, 40, 8, 8, 16), (257, 515, 4, 4, 64), (1, 3000, 8, 1, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, Hq, Hk, D", LENGTHS)
+def test_parity(Tq, Tk, Hq, Hk, D, dtype):
+    print(f"attention {Tq} {Tk} {Hq} {Hk} {D} {dtype}", flush=True)
+    case = Case(Tq, Tk, Hq, Hk, D, dtype)
+    case.check_forward()
+    case.check_backward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, Hq, Hk, D", [(129, 200, 128, 128, 64), (130, 131, 256, 64, 128), (520, 330, 64, 64, 32), (1, 190, 512, 256, 96)])
+def test_many_heads(Tq, Tk, Hq, Hk, D, dtype):
+    """Enough rows for the forms whose waves have rows of their own."""
+    print(f"attention {Tq} {Tk} {Hq} {Hk} {D} {dtype}", flush=True)
+    case = Case(Tq, Tk, Hq, Hk, D, dtype)
+    case.check_forward()
+    case.check_backward()
+
+
+RAGGED = [  # q offsets, key offsets, lengths
+    ([0, 5, 5, 40, 77], [0, 30, 60, 60, 200], None),          # no queries, no keys
+    ([3, 70, 71, 72], [2, 66, 131, 150], [64, 0, 100]),       # padding at both ends, lengths past the end and zero
+    ([0, 33, 66, 99], [0, 64, 128, 256], [1, 64, -3]),
+    ([0, 0, 0], [0, 0, 9], None),
+    ([0] + [i + 1 for i in range(100)], [3 * i for i in range(101)], None)]   # a hundred sequences of one token
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mask", [None, 0.6])
+@pytest.mark.parametrize("which", range(len(RAGGED)))
+@pytest.mark.parametrize("Hq, Hk, D", [(4, 2, 64), (2, 2, 128), (96, 32, 24)])
+def test_ragged(Hq, Hk, D, which, mask, dtype):
+    qo, ko, kl = RAGGED[which]
+    print(f"ragged {which} {Hq} {Hk} {D} {mask} {dtype}", flush=True)
+    case = Case(qo[-1] + 4, ko[-1] + 5, Hq, Hk, D, dtype, qo, ko, kl, mask)
+    case.check_forward()
+    g = case.check_backward()
+    assert not host(case.o)[~case.owned].any() and (host(case.lse)[~case.owned] == -np.inf).all()
+    dead = ~case.ok.any(axis=0)
+    assert not host(g.dk)[dead].any() and not host(g.dv)[dead].any() and not host(g.dq)[~case.owned].any()
+
+
+@pytest.mark.parametrize("layout", ["heads", "padded"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides(layout, dtype):
+    case = Case(70, 100, 4, 2, 48, dtype, layout=layout, mask=0.8)
+    case.check_forward()
+    case.check_backward()
+    # results into given tensors of the same strides
+    outs = [torch.full_like(t, 5.0) if layout == "heads" else t.clone() for t in (case.q, case.k, case.v)]
+    o = outs[0].clone() if layout == "padded" else torch.empty_like(case.q)
+    lse = torch.empty((70, 4), device=DEV)
+    got = attention(case.q, case.k, case.v, o=o, lse=lse, **case.kw)
+    assert got[0] is o and torch.equal(o, case.o) and torch.equal(lse, case.lse)
+    g = attention_backward(case.do, case.q, case.k, case.v, o, lse, dq=outs[0], dk=outs[1], dv=outs[2], **case.kw)
+    for a, b in zip(g, attention_backward(case.do, case.q, case.k, case.v, o, lse, **case.kw)):
+        assert torch.equal(a, b)
+    # o over q itself
+    q = case.q.clone(memory_format=torch.preserve_format)
+    attention(q, case.k, case.v, o=q, **case.kw)
+    assert torch.equal(q, o)
+
+
+def test_given_outputs_keep_rows_of_no_sequence():
+    for Hq, Hk in ((4, 2), (128, 64)):
+        case = Case(90, 120, Hq, Hk, 64, "bf16", [7, 40, 80], [4, 100, 101])
+        o, lse = torch.full_like(case.q, 3.0), torch.full((90, Hq), 3.0, device=DEV)
+        attention(case.q, case.k, case.v, o=o, lse=lse, **case.kw)
+        out = [torch.full_like(t, 3.0) for t in (case.q, case.k.contiguous(), case.v.contiguous())]
+        attention_backward(case.do, case.q, case.k, case.v, o, lse, dq=out[0], dk=out[1], dv=out[2], **case.kw)
+        for t in (o, lse, out[0]):
+            assert (t[:7] == 3.0).all() and (t[80:] == 3.0).all() and not (t[7:80] == 3.0).all(-1).any()
+        for t in out[1:]:
+            assert (t[:4] == 3.0).all() and (t[101:] == 3.0).all() and not (t[4:101] == 3.0).all(-1).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_places_hold_anything(dtype):
+    for Hq, Tk in ((4, 150), (4, 2000), (128, 150)):
+        case = Case(140, Tk, Hq, Hq, 64, dtype, [5, 100, 130], [3, 70, Tk - 9], [60, Tk - 90], 0.7)
+        want = (*attention(case.q, case.k, case.v, **case.kw), *case.check_backward())
+        dead = torch.from_numpy(~case.ok.any(axis=0)).to(DEV)
+        for i, bad in enumerate((float("nan"), float("inf"), torch.finfo(case.t).min)):
+            case.k[dead] = bad
+            case.v[dead] = -bad
+            pad = torch.from_numpy(~case.owned).to(DEV)
+            for t in (case.q, case.do, case.o):
+                t[pad] = bad
+            got = (*attention(case.q, case.k, case.v, **case.kw),
+                   *attention_backward(case.do, case.q, case.k, case.v, case.o, case.lse, **case.kw))
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+
+
+def test_a_mask_that_leaves_nothing():
+    case = Case(40, 130, 4, 2, 64, "bf16", mask=[False] * 130)
+    o, lse = case.check_forward()
+    assert not o.any() and (lse == -torch.inf).all()
+    g = case.check_backward()
+    assert not any(t.any() for t in g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_keys_and_no_queries(dtype):
+    for Tq, Tk in ((0, 20), (20, 0), (0, 0)):
+        case = Case(Tq, Tk, 4, 2, 64, dtype)
+        o, lse = attention(case.q, case.k, case.v)
+        assert o.shape == case.q.shape and not o.any() and (lse == -torch.inf).all()
+        g = attention_backward(case.do, case.q, case.k, case.v, o, lse)
+        assert g.dk.shape == (Tk, 2, 64) and not any(t.any() for t in g)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_and_small_scores(dtype):
+    """Scores up to +-thousands: the maximum is raised over the tiles, in rising and falling order."""
+    for order in (1, -1):
+        case = Case(64, 700, 2, 2, 64, dtype, scale=1.0)
+        ramp = torch.linspace(-30, 30, 700, device=DEV)[::1].flip(0) if order < 0 else torch.linspace(-30, 30, 700, device=DEV)
+        case.k.copy_((case.k.float() * 0.05 + ramp[:, None, None]).to(case.t))
+        case.q.copy_((case.q.float() * 0.1 + 1.0).to(case.t))
+        case.check_forward()
+        case.check_backward()
+    for scale in (1e-20, 1e-38):     # and factors next to zero
+        case = Case(20, 300, 2, 1, 64, dtype, scale=scale)
+        case.check_forward()
+    # a key at minus infinity has no weight, and a row that has no other key has no result
+    case = Case(4, 3, 1, 1, 8, dtype)
+    case.q.fill_(1.0)
+    case.k[1] = -torch.inf
+    o, lse = attention(case.q, case.k, case.v)
+    two = torch.tensor([True, False, True], device=DEV)
+    o2, lse2 = attention(case.q, case.k, case.v, key_mask=two)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    o, lse = attention(case.q, case.k, case.v, key_mask=~two)
+    assert not o.any() and (lse == -torch.inf).all()
+    # a NaN in a key that counts is the queries' that read it
+    case.k[1] = torch.nan
+    o, lse = attention(case.q, case.k, case.v)
+    assert o.isnan().all() and lse.isnan().all()
+
+
+def test_a_nan_query_stays_in_its_row():
+    for Hq, Tk in ((4, 100), (2, 3000), (128, 100)):
+        case = Case(70, Tk, Hq, Hq, 64, "bf16")
+        want = attention(case.q, case.k, case.v)
+        case.q[33, 1, 5] = torch.nan
+        got = attention(case.q, case.k, case.v)
+        for a, b in zip(got, want):
+            assert a[33, 1].isnan().all()
+            a[33, 1] = b[33, 1] = 0
+            assert torch.equal(a, b)
+
+
+def test_same_bits_and_wanted_gradients_alone():
+    for Tq, Tk, Hq, Hk in ((300, 4000, 4, 2), (300, 300, 128, 64), (3000, 77, 2, 1)):
+        case = Case(Tq, Tk, Hq, Hk, 64, "bf16", mask=0.9)
+        first = attention(case.q, case.k, case.v, **case.kw)
+        for a, b in zip(attention(case.q, case.k, case.v, **case.kw), first):
+            assert torch.equal(a, b)
+        args = (case.do, case.q, case.k, case.v, *first)
+        want = attention_backward(*args, **case.kw)
+        for need in (("dq", "dk", "dv"), ("dq",), ("dk",), ("dv",), ("dv", "dk"), ("dq", "dv")):
+            got = attention_backward(*args, need=iter(need), **case.kw)
+            for name, a, b in zip(want._fields, got, want):
+                assert (a is None) == (name not in need)
+                assert a is None or torch.equal(a, b), (name, need)
+
+
+def test_gradients_are_differences():
+    case = Case(9, 20, 4, 2, 16, "f32", mask=0.7)
+    o, lse = attention(case.q, case.k, case.v, **case.kw)
+    g = attention_backward(case.do, case.q, case.k, case.v, o, lse, **case.kw)
+    x, do, r, h = [host(t) for t in (case.q, case.k, case.v)], host(case.do), np.random.default_rng(1), 1e-6
+    for n in range(3):
+        d = r.normal(size=x[n].shape)
+        f = []
+        for sign in (h, -h):
+            y = list(x)
+            y[n] = x[n] + sign * d
+            f.append((O.forward(*y, case.ok, case.scale)[0] * do).sum())
+        a = host(g[n])
+        assert abs((a * d).sum() - (f[0] - f[1]) / (2 * h)) <= 1e-5 * (np.abs(a) * np.abs(d)).sum()
+
+
+def test_keys_past_2_to_the_32_bytes():
+    Tk, H, D = 300_000, 64, 128   # 4.9 GB each
+    k, v = (torch.empty((Tk, H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    small = Case(3, 90, H, H, D)
+    k[-90:], v[-90:] = small.k, small.v
+    kw = dict(q_offsets=ints([0, 3]), kv_offsets=ints([Tk - 90, Tk]))
+    o, lse = small.check_forward(attention(small.q, k, v, **kw))
+    dk, dv = torch.full_like(k, 2.0), torch.full_like(v, 2.0)
+    g = attention_backward(small.do, small.q, k, v, o, lse, dk=dk, dv=dv, **kw)
+    small.check_backward(g._replace(dk=dk[-90:], dv=dv[-90:]))
+    assert (dk[:-90] == 2.0).all() and (dv[:-90] == 2.0).all()
+
+
+def test_offsets_out_of_order_stay_inside():
+    """What no call should hand over is read inside the tensors all the same."""
+    case = Case(40, 60, 4, 2, 64)
+    for qo, ko, kl in (([50, -7, 99], [70, -4, 10], None), ([0, 40, 20], [60, 0, 30], [2 ** 31 - 1, -2 ** 31]), ([-2 ** 31, 2 ** 31 - 1, 0], [-5, 2 ** 31 - 1, 3], [9, 9])):
+        kw = dict(q_offsets=ints(qo), kv_offsets=ints(ko), kv_lengths=ints(kl))
+        o, lse = attention(case.q, case.k, case.v, **kw)
+        attention_backward(case.do, case.q, case.k, case.v, o, lse, **kw)
+        c = Nvfp4Cache.empty(60, 2, 64, DEV)
+        c.store(case.k, case.v, offsets=ints(qo), kv_offsets=ints(ko), kv_lengths=ints(kl))
+        attention(case.q, c, **kw)
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ the module
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_module(dtype):
+    B, Tq, Tk, Hq, Hk, D = 3, 37, 50, 4, 2, 64
+    t = TYPES[dtype]
+    torch.manual_seed(5)
+    q = torch.randn((B, Tq, Hq, D), device=DEV).to(t).requires_grad_()
+    k = torch.randn((1, Tk, Hk, D), device=DEV).to(t).requires_grad_()   # one encoder's states for all
+    v = torch.randn((B, Tk, Hk, D), device=DEV).to(t).requires_grad_()
+    mask = torch.rand((B, Tk), device=DEV) < 0.8
+    lengths = ints([50, 20, 0])
+    do = torch.randn_like(q).transpose(1, 2).contiguous().transpose(1, 2)
+    m = Attention()
+    o = m(q, k.expand(B, -1, -1, -1), v, kv_lengths=lengths, key_mask=mask)
+    got = torch.autograd.grad(o, [q, k, v], do)
+    flat = [x.detach().expand(B, *x.shape[1:]).reshape(-1, *x.shape[2:]).contiguous() for x in (q, k, v)]
+    kw = dict(q_offsets=ints([0, Tq, 2 * Tq, 3 * Tq]), kv_offsets=ints([0, Tk, 2 * Tk, 3 * Tk]), kv_lengths=lengths, key_mask=mask.flatten())
+    o2, lse = attention(*flat, **kw)
+    assert o.shape == q.shape and torch.equal(o.flatten(0, 1), o2)
+    want = attention_backward(do.reshape(-1, Hq, D).contiguous(), *flat, o2, lse, **kw)
+    assert torch.equal(got[0].flatten(0, 1), want.dq) and torch.equal(got[2].flatten(0, 1), want.dv)
+    assert torch.equal(got[1], want.dk.reshape(B, Tk, Hk, D).sum(0, keepdim=True))
+    # packed, no gradients, tensors that the kernels cannot read as they lie
+    with torch.no_grad():
+        odd = torch.empty((Tk * B * Hk * D + 1,), dtype=t, device=DEV)[1:].view(B * Tk, Hk, D).copy_(flat[2])
+        assert torch.equal(m(flat[0], flat[1], odd, **kw), o2)
+        assert torch.equal(m(q, k.expand(B, -1, -1, -1), v, kv_lengths=lengths, key_mask=mask), o)
+        assert m(q[:0], k[:0], v[:0]).shape == (0, Tq, Hq, D)
+        assert not m(q, k.expand(B, -1, -1, -1)[:, :0], v[:, :0]).any()
+    g = torch.autograd.grad(m(q, k.expand(B, -1, -1, -1), v).float().sum(), [v])   # only one is wanted
+    assert g[0].shape == v.shape
+
+
+def test_a_block_of_them():
+    """Norms and rotation of one projection's queries and keys, then attention: the gradients of
+    the projection against torch's own in 64 bits.  Each step is off by 2^-24 times the sums of
+    magnitudes that its own tests count (at most some hundreds): 1e-4 of the largest gradient."""
+    T, H, Hk, D = 150, 4, 2, 64
+    torch.manual_seed(11)
+    x = torch.randn((T, H + 2 * Hk, D), device=DEV)
+    a = torch.arange(T, device=DEV).double()[:, None] * torch.exp2(-torch.arange(D // 2, device=DEV).double() / 4)
+    cos, sin = torch.cos(a).float(), torch.sin(a).float()
+    m, att = HeadNorm(D, device=DEV), Attention()
+    leaf = x.clone().requires_grad_()
+    q, k = m(leaf[:, :H], leaf[:, H:H + Hk], cos, sin)
+    o = att(q, k, leaf[:, H + Hk:])
+    do = torch.randn_like(o)
+    got = torch.autograd.grad(o, [leaf, m.q_weight, m.k_weight], do)
+
+    y = x.double().cpu().requires_grad_()
+    wq, wk = (torch.ones(D, dtype=torch.float64).requires_grad_() for _ in range(2))
+    c, s = cos.double().cpu()[:, None], sin.double().cpu()[:, None]
+
+    def turn(v, w):
+        v = v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1e-6) * w
+        return torch.stack([v[..., ::2] * c - v[..., 1::2] * s, v[..., ::2] * s + v[..., 1::2] * c], -1).flatten(-2)
+
+    q, k, v = turn(y[:, :H], wq), turn(y[:, H:H + Hk], wk), y[:, H + Hk:]
+    k, v = (z.repeat_interleave(H // Hk, 1).transpose(0, 1) for z in (k, v))
+    p = torch.softmax(q.transpose(0, 1) @ k.transpose(1, 2) / D ** 0.5, -1)
+    want = torch.autograd.grad((p @ v).transpose(0, 1), [y, wq, wk], do.double().cpu())
+    for a, b in zip(got, want):
+        assert (a.double().cpu() - b).abs().max() <= 1e-4 * b.abs().max()
+
+
+def test_streams_graphs_and_captures():
+    case = Case(5, 3000, 8, 2, 128, "bf16", mask=0.9)     # split: a workspace
+    calls = lambda stream=None: [*(r := attention(case.q, case.k, case.v, stream=stream, **case.kw)),
+                                 *attention_backward(case.do, case.q, case.k, case.v, *r, stream=stream, **case.kw)]
+    want = calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = calls(side.cuda_stream)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for _ in range(2):     # each with its own workspaces
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(calls())
+        graphs.append(g)
+    for i in range(4):
+        case.q.copy_(torch.randn_like(case.q) * (i + 1))
+        want = calls()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, want))
+    m = Attention()
+    with pytest.raises(RuntimeError, match="capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            m(case.q.detach().requires_grad_(), case.k, case.v)
+    with pytest.raises(RuntimeError, match="forward-mode"):
+        with torch.autograd.forward_ad.dual_level():
+            m(torch.autograd.forward_ad.make_dual(case.q, case.q), case.k, case.v)
+
+
+# ------------------------------------------------------------- the 4-bit cache
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T, H, D", [(1, 1, 16), (7, 3, 80), (50, 8, 128), (33, 2, 64)])
+def test_store_has_the_format(T, H, D, dtype):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn((T, 2 * H + 1, D + 1), generator=g, device=DEV)
+    x[0, 0] = 0.0
+    x[T // 2] *= 1e4     # scales at 448
+    x[T - 1, H] *= 1e-4  # and below the smallest
+    x = x.to(TYPES[dtype])
+    k, v = x[:, :H, :D], x[:, H:2 * H, 1:]    # elements at odd places
+    cache = Nvfp4Cache.empty(T + 3, H, D, DEV)
+    cache.store(k, v)
+    for t, codes, scales, values in zip((k, v), (cache.k_codes, cache.v_codes), (cache.k_scales, cache.v_scales), cache.dequantize()):
+        want_c, want_s = F.quantize_nvfp4(t.float().cpu().numpy().reshape(T, -1))
+        assert np.array_equal(codes[:T].cpu().numpy().reshape(T, -1), want_c)
+        assert np.array_equal(scales[:T].cpu().numpy().reshape(T, -1), want_s)
+        assert not codes[T:].any() and not scales[T:].any()
+        assert np.array_equal(host(values[:T]).reshape(T, -1), F.dequantize_nvfp4(want_c, want_s))
+    for a, b in zip(cache.dequantize("bf16"), cache.dequantize()):
+        assert torch.equal(a.float(), b)
+
+
+def test_store_goes_behind_the_used_rows():
+    H, D = 2, 32
+    k, v = torch.randn((2, 14, H, D), device=DEV)
+    every = Nvfp4Cache.empty(14, H, D, DEV)
+    every.store(k, v)
+    cache = Nvfp4Cache.empty(20, H, D, DEV)
+    for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales):
+        t.fill_(9)
+    # 3 tokens behind 2, none, 6 of which 4 fit, 2 behind none; one token before and two after them are nobody's
+    cache.store(k, v, offsets=ints([1, 4, 4, 10, 12]), kv_offsets=ints([1, 7, 9, 14, 19]), kv_lengths=ints([2, 1, 1, 0]))
+    to = {3: 1, 4: 2, 5: 3, 10: 4, 11: 5, 12: 6, 13: 7, 14: 10, 15: 11}
+    for a, b in ((cache.k_codes, every.k_codes), (cache.k_scales, every.k_scales), (cache.v_codes, every.v_codes), (cache.v_scales, every.v_scales)):
+        for row in range(20):
+            if row in to:
+                assert torch.equal(a[row], b[to[row]]), row
+            else:
+                assert (a[row] == 9).all(), row
+    cache.store(k[:0], v[:0])
+    Nvfp4Cache.empty(0, H, D, DEV).store(k, v)
+    assert Nvfp4Cache.empty(0, H, D, DEV).dequantize()[0].shape == (0, H, D)
+    full = Nvfp4Cache.empty(5, H, D, DEV)
+    full.store(k, v, kv_lengths=ints([3]))     # one sequence: two fit
+    assert torch.equal(full.k_codes[3:], every.k_codes[:2]) and not full.k_codes[:3].any()
+
+
+def test_a_nan_in_a_block():
+    k, v = torch.randn((2, 5, 2, 64), device=DEV)
+    k[1, 0, 20] = torch.nan
+    v[3, 1, 63] = torch.inf
+    c = Nvfp4Cache.empty(5, 2, 64, DEV)
+    c.store(k, v)
+    a, b = c.dequantize()
+    bad = [torch.zeros_like(k, dtype=torch.bool) for _ in range(2)]
+    bad[0][1, 0, 16:32] = bad[1][3, 1, 48:] = True
+    assert torch.equal(a.isnan(), bad[0]) and torch.equal(b.isnan(), bad[1])
+    q = torch.randn((3, 2, 64), device=DEV)
+    for x in (q, q.bfloat16()):
+        o = attention(x, c)[0]
+        assert o[:, 0].isnan().all() and torch.equal(o[:, 1].isnan(), bad[1][3, 1].expand(3, 64))
+        o, _ = attention(x, c, key_mask=torch.tensor([1, 0, 1, 0, 1], device=DEV).bool())
+        assert not o.isnan().any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, Hq, Hk, D", [(1, 1, 1, 1, 16), (1, 700, 8, 2, 128), (8, 3000, 4, 1, 64), (65, 130, 3, 3, 96), (130, 200, 128, 128, 64),
+                                               (129, 260, 256, 64, 128), (40, 333, 6, 2, 80)])
+def test_cache_parity(Tq, Tk, Hq, Hk, D, dtype):
+    print(f"cache {Tq} {Tk} {Hq} {Hk} {D} {dtype}", flush=True)
+    Case(Tq, Tk, Hq, Hk, D, dtype, cache=True).check_forward()
+    qo, ko = [0, Tq // 2, Tq], [0, Tk // 3, Tk]
+    Case(Tq, Tk, Hq, Hk, D, dtype, qo, ko, [Tk // 4, Tk], 0.7, cache=True).check_forward()
+
+
+def test_cache_queries_of_any_size():
+    """fp16 products: queries far outside its range are scaled."""
+    for f in (1e-30, 1e-6, 1.0, 3e4, 1e30):
+        case = Case(20, 100, 4, 2, 64, "bf16", scale=0.125 / f, cache=True)
+        case.q.copy_((case.q.float() * f).bfloat16())
+        case.check_forward()
+    case.q.zero_()
+    case.check_forward()
+
+
+def test_a_long_cache():
+    rows, H, D = 1 << 20, 64, 128     # 4.3 GB of codes
+    big = Nvfp4Cache.empty(rows, H, D, DEV)
+    case = Case(2, 80, H, H, D, cache=True)
+    q, k, v, small = case.q, case.k, case.v, case.cache
+    big.store(k, v, offsets=ints([0, 80]), kv_offsets=ints([rows - 100, rows]), kv_lengths=ints([20]))
+    assert torch.equal(big.k_codes[-80:], small.k_codes) and torch.equal(big.v_scales[-80:], small.v_scales)
+    case.check_forward(attention(q, big, q_offsets=ints([0, 2]), kv_offsets=ints([rows - 80, rows])))
+    assert not big.k_codes[:-80].any()
+
+
+def test_serving_steps():
+    """Prompts, then token by token: norms and rotation, into the cache, attention over it.  Each step
+    against the oracle on the cache's values; a captured step replays."""
+    Hq, Hk, D, G, room = 8, 2, 64, 3, 40
+    torch.manual_seed(2)
+    kv_offsets = ints([g * room for g in range(G + 1)])
+    cache = Nvfp4Cache.empty(G * room, Hk, D, DEV)
+    lengths = ints([0] * G)
+    a = torch.arange(room, device=DEV).float()[:, None] * torch.exp2(-torch.arange(D // 2, device=DEV).float() / 3)
+    cos, sin, w = torch.cos(a), torch.sin(a), torch.rand(D, device=DEV) + 0.5
+    att = Attention()
+
+    def step(x, offsets, positions):
+        q, k = head_norm(x[:, :Hq], x[:, Hq:Hq + Hk], q_weight=w, k_weight=w, cos=cos, sin=sin, positions=positions)
+        cache.store(k, x[:, Hq + Hk:], offsets=offsets, kv_offsets=kv_offsets, kv_lengths=lengths)
+        lengths.add_(offsets[1:] - offsets[:-1])
+        return q, att(q, cache, q_offsets=offsets, kv_offsets=kv_offsets, kv_lengths=lengths)
+
+    def check(q, o, offsets):
+        k, v = (host(t) for t in cache.dequantize())
+        ok = O.allowed(q.shape[0], G * room, offsets.tolist(), kv_offsets.tolist(), lengths.tolist())
+        want, lse = O.forward(host(q), k, v, ok, D ** -0.5)
+        p = O.weights(O.scores(host(q), k, ok, D ** -0.5), lse)
+        for h in range(Hq):
+            near(host(o)[:, h], want[:, h], (2.0 ** -11 + 1e-4) * p[h] @ np.abs(v[:, h // (Hq // Hk)]), 2.0 ** -8)
+
+    prompts = [5, 17, 1]
+    offsets = ints([0, 5, 22, 23])
+    x = torch.randn((23, Hq + 2 * Hk, D), device=DEV).bfloat16()
+    positions = torch.cat([torch.arange(n) for n in prompts]).int().to(DEV)
+    check(*step(x, offsets, positions), offsets)
+    one, x1, pos = ints([0, 1, 2, 3]), torch.randn((G, Hq + 2 * Hk, D), device=DEV).bfloat16(), ints(prompts)
+    check(*step(x1, one, pos), one)
+    start = lengths.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pos.add_(1)
+        q, o = step(x1, one, pos)
+    for i in range(4):
+        x1.copy_(torch.randn_like(x1))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lengths.tolist() == (start + i + 1).tolist() and pos.tolist() == [n + i + 1 for n in prompts]
+        check(q, o, one)

@@ -1,0 +1,410 @@
+"""Attention between a block's queries and keys of another number: an encoder's states,
+the other expert's tokens, or its own.
+
+    o = softmax(scale q k^T) v
+
+``attention`` computes it over packed sequences (``include/asp.h``, ``asp_attention``, has
+the definition), ``attention_backward`` gives the gradients, and ``Attention`` is both as a
+module.  ``Nvfp4Cache`` holds keys and values in 4 bits, for those that many steps read:
+``attention`` takes it in place of k and v.  All arithmetic happens inside libasp.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import NamedTuple
+
+import torch
+
+from . import binding as B
+from .fp8 import _CODES, _no_capture, _no_forward_mode
+from .heads import _check_heads
+from .layer import _Y_DTYPES, _check_ws, _lend, _made_for, _new
+
+
+class AttentionGrads(NamedTuple):
+    """Gradients of attention's inputs (None: not wanted)."""
+    dq: torch.Tensor | None
+    dk: torch.Tensor | None
+    dv: torch.Tensor | None
+
+
+def _check_ints(t, name, size, device):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be an int32 tensor")
+    if t.dim() != 1 or (t.shape[0] != size if size else t.shape[0] < 2) or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be {size or 'G + 1 >= 2'} contiguous entries on {device}, "
+                         f"got {tuple(t.shape)} on {t.device}")
+
+
+def _aligned(t, name, st, sh):
+    """The kernels read 16 bytes at a time."""
+    if (st | sh) * t.element_size() % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned, its token and head strides too; got "
+                         f"strides {t.stride()}")
+    if t.shape[0] > 1 and st < t.shape[2]:
+        raise ValueError(f"the tokens of {name} must not overlap, got strides {t.stride()}")
+
+
+def _check_pair(first, second, device):
+    """Offsets of the two sides: both or neither, G."""
+    if (first is None) != (second is None):
+        raise ValueError("the offsets of both sides belong together")
+    if first is None:
+        return 1
+    _check_ints(first, "q_offsets", 0, device)
+    _check_ints(second, "kv_offsets", first.shape[0], device)
+    return first.shape[0] - 1
+
+
+def _check_keys(Tk, G, device, kv_lengths, key_mask):
+    if kv_lengths is not None:
+        _check_ints(kv_lengths, "kv_lengths", G, device)
+    if key_mask is not None:
+        if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("key_mask must be a bool or uint8 tensor")
+        if key_mask.shape != (Tk,) or key_mask.device != device or not key_mask.is_contiguous():
+            raise ValueError(f"key_mask must be {Tk} contiguous entries on {device}")
+
+
+def _scale(scale, D):
+    scale = D ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < 3.0e38:
+        raise ValueError(f"scale must be above 0, not {scale}")
+    return scale
+
+
+@dataclass
+class Nvfp4Cache:
+    """Keys and values in the framework's 4-bit format: rows of Hk heads of D elements (a
+    multiple of 16, up to 128), blocks of 16 along a head.  4.5 bits a value."""
+    k_codes: torch.Tensor    # rows x Hk x D / 2 uint8
+    k_scales: torch.Tensor   # rows x Hk x D / 16 uint8 (E4M3)
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+
+    @classmethod
+    def empty(cls, rows, heads, head_dim, device):
+        """A cache of zeros."""
+        if head_dim < 16 or head_dim > 128 or head_dim % 16:
+            raise ValueError(f"head_dim must be a multiple of 16 up to 128, not {head_dim}")
+        return cls(*(torch.zeros((rows, heads, head_dim // n), dtype=torch.uint8, device=device)
+                     for n in (2, 16, 2, 16)))
+
+    def __post_init__(self):
+        self.check()
+
+    def check(self):
+        """The four tensors belong together."""
+        kc = self.k_codes
+        for t in (kc, self.k_scales, self.v_codes, self.v_scales):
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
+                raise TypeError("codes and scales must be uint8 tensors")
+        if kc.dim() != 3 or kc.shape[2] % 8 or not 8 <= kc.shape[2] <= 64 or kc.shape[1] < 1:
+            raise ValueError("codes must be (rows, heads, D / 2), D a multiple of 16 up to 128, got "
+                             f"{tuple(kc.shape)}")
+        codes, scales = kc.shape, (*kc.shape[:2], kc.shape[2] // 8)
+        for t, shape in ((kc, codes), (self.k_scales, scales), (self.v_codes, codes),
+                         (self.v_scales, scales)):
+            if t.shape != shape or not t.is_contiguous() or t.device != kc.device:
+                raise ValueError(f"a cache of {tuple(codes)} codes needs contiguous {tuple(shape)} on "
+                                 f"{kc.device}, got {tuple(t.shape)} on {t.device}")
+
+    @property
+    def device(self) -> torch.device:
+        return self.k_codes.device
+
+    @property
+    def rows(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def head_dim(self) -> int:
+        return 2 * self.k_codes.shape[2]
+
+    def store(self, k, v, *, offsets=None, kv_offsets=None, kv_lengths=None, stream=None):
+        """New tokens' k and v (T, Hk, D; float32 or bf16, any strides) into the cache.
+
+        offsets: G + 1 int32, the new tokens of each sequence; kv_offsets: G + 1 int32, the
+        cache rows of each; kv_lengths: G int32, how many of them it has used.  The tokens
+        of a sequence go behind those; what has no room in its rows is dropped.  Without
+        offsets: one sequence of all tokens and rows.  The lengths are the caller's to
+        advance (and then say ``attention`` how many keys count)."""
+        self.check()
+        dev, Hk, D = self.device, self.heads, self.head_dim
+        ldk, hsk = _check_heads(k, "k", (None, Hk, D), dev)
+        ldv, hsv = _check_heads(v, "v", (k.shape[0], Hk, D), dev, (k.dtype,))
+        if (offsets is None) != (kv_offsets is None):
+            raise ValueError("offsets and kv_offsets belong together")
+        G = 1
+        if offsets is not None:
+            _check_ints(offsets, "offsets", 0, dev)
+            G = offsets.shape[0] - 1
+            _check_ints(kv_offsets, "kv_offsets", G + 1, dev)
+        if kv_lengths is not None:
+            _check_ints(kv_lengths, "kv_lengths", G, dev)
+        at = B._at
+        B.launch(dev, B.lib().asp_kv_store, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv,
+                 _CODES[k.dtype], k.shape[0], Hk, D, G, at(offsets), at(kv_offsets), at(kv_lengths),
+                 self.rows, at(self.k_codes), at(self.k_scales), at(self.v_codes),
+                 at(self.v_scales), B.stream_on(stream, dev))
+
+    def dequantize(self, dtype="f32", stream=None):
+        """(k, v): the cache's values, (rows, Hk, D) float32 or bf16, which hold them exactly."""
+        self.check()
+        if dtype not in _Y_DTYPES:
+            raise ValueError(f"dtype must be 'f32' or 'bf16', not {dtype!r}")
+        dev = self.device
+        k, v = (_new(stream, dev, (self.rows, self.heads, self.head_dim), _Y_DTYPES[dtype])
+                for _ in range(2))
+        at = B._at
+        B.launch(dev, B.lib().asp_kv_load, at(self.k_codes), at(self.k_scales), at(self.v_codes),
+                 at(self.v_scales), self.rows, self.heads, self.head_dim, at(k), at(v),
+                 B.DTYPES[dtype], B.stream_on(stream, dev))
+        _lend(stream, k, v)
+        return k, v
+
+
+def attention(q, k, v=None, *, scale=None, q_offsets=None, kv_offsets=None, kv_lengths=None,
+              key_mask=None, o=None, lse=None, workspace=None, stream=None):
+    """(o, lse) of q (Tq, Hq, D) over k and v (Tk, Hk, D), float32 or bf16, or over an
+    ``Nvfp4Cache`` k; Hq a multiple of Hk, each Hq / Hk consecutive heads share one.  o has q's
+    type, lse (Tq, Hq) float32 is the logarithm of each softmax's sum.
+
+    scale: 1 / sqrt(D) by default.  q_offsets, kv_offsets: G + 1 int32, the first rows of the
+    packed sequences and the end of the last; queries see the keys of their sequence.
+    kv_lengths: G int32, how many of a sequence's keys count, from its first.  key_mask: Tk
+    bool, which keys count.  A query without a key has o 0 and lse -infinity.  Queries of no
+    sequence are left as they are in o and lse where given; in tensors made here they are 0
+    and -infinity.  D: a multiple of 8 up to 128; tensors and strides 16-byte aligned.
+    stream: as in ``fp8``."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D torch tensor, (T, H, D)")
+    Tq, Hq, D = q.shape
+    dev = q.device
+    ldq, hsq = _check_heads(q, "q", (Tq, Hq, D), dev)
+    _aligned(q, "q", ldq, hsq)
+    cached = isinstance(k, Nvfp4Cache)
+    if cached:
+        if v is not None:
+            raise ValueError("v with a cache")
+        k.check()
+        if k.device != dev or k.head_dim != D:
+            raise ValueError(f"the cache has heads of {k.head_dim} on {k.device}, q of {D} on {dev}")
+        Tk, Hk = k.rows, k.heads
+    else:
+        ldk, hsk = _check_heads(k, "k", (None, None, D), dev, (q.dtype,))
+        Tk, Hk = k.shape[:2]
+        ldv, hsv = _check_heads(v, "v", (Tk, Hk, D), dev, (q.dtype,))
+        _aligned(k, "k", ldk, hsk)
+        _aligned(v, "v", ldv, hsv)
+    if Hk < 1 or Hq < 1 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
+    G = _check_pair(q_offsets, kv_offsets, dev)
+    _check_keys(Tk, G, dev, kv_lengths, key_mask)
+    scale = _scale(scale, D)
+    made, zero = [], 0
+    if o is None:
+        o = _new(stream, dev, (Tq, Hq, D), q.dtype)
+        made.append(o)
+        zero, ldo, hso = 1, Hq * D, D
+    else:
+        ldo, hso = _check_heads(o, "o", (Tq, Hq, D), dev, (q.dtype,))
+        _aligned(o, "o", ldo, hso)
+    if lse is None:
+        lse = _new(stream, dev, (Tq, Hq))
+        made.append(lse)
+        zero |= 2
+    elif not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
+        raise TypeError("lse must be a float32 tensor")
+    elif lse.shape != (Tq, Hq) or lse.device != dev or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous ({Tq}, {Hq}) on {dev}")
+    need = B.asp_attention_workspace_bytes(Tq, Tk, Hq, Hk, D, G)
+    if workspace is not None:
+        _check_ws(workspace, need, dev)
+    elif need:
+        workspace = _new(stream, dev, need, torch.uint8)
+    at = B._at
+    ws, have = at(workspace), 0 if workspace is None else workspace.numel()
+    tail = (at(q_offsets), at(kv_offsets), at(kv_lengths), at(key_mask), o.data_ptr(), ldo, hso,
+            lse.data_ptr(), zero, ws, have, B.stream_on(stream, dev))
+    if cached:
+        B.launch(dev, B.lib().asp_attention_cache, q.data_ptr(), ldq, hsq, _CODES[q.dtype],
+                 at(k.k_codes), at(k.k_scales), at(k.v_codes), at(k.v_scales), Tq, Tk, Hq, Hk, D,
+                 scale, G, *tail)
+    else:
+        B.launch(dev, B.lib().asp_attention, q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk,
+                 v.data_ptr(), ldv, hsv, _CODES[q.dtype], Tq, Tk, Hq, Hk, D, scale, G, *tail)
+    _lend(stream, *made)
+    return o, lse
+
+
+def attention_backward(do, q, k, v, o, lse, *, scale=None, q_offsets=None, kv_offsets=None,
+                       kv_lengths=None, key_mask=None, need=None, dq=None, dk=None, dv=None,
+                       workspace=None, stream=None):
+    """Gradients of ``attention`` from that of o, with its inputs, o and lse; the options are the
+    forward's.  need: the names of the wanted gradients (fields of ``AttentionGrads``; None:
+    all); the others are not computed.  dq, dk, dv: tensors to write (rows of no sequence are
+    left as they are there and are zeros in tensors made here)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D torch tensor, (T, H, D)")
+    Tq, Hq, D = q.shape
+    dev, same = q.device, (q.dtype,)
+    if isinstance(k, Nvfp4Cache):
+        raise TypeError("a cache has no gradients")
+
+    def strides(t, name, shape, dtypes=same):
+        s = _check_heads(t, name, shape, dev, dtypes)
+        _aligned(t, name, *s)
+        return s
+
+    sq = strides(q, "q", (Tq, Hq, D), _CODES)
+    sk = strides(k, "k", (None, None, D))
+    Tk, Hk = k.shape[:2]
+    sv = strides(v, "v", (Tk, Hk, D))
+    so = strides(o, "o", (Tq, Hq, D))
+    sdo = strides(do, "do", (Tq, Hq, D))
+    if Hk < 1 or Hq < 1 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
+        raise TypeError("lse must be a float32 tensor")
+    if lse.shape != (Tq, Hq) or lse.device != dev or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous ({Tq}, {Hq}) on {dev}")
+    G = _check_pair(q_offsets, kv_offsets, dev)
+    _check_keys(Tk, G, dev, kv_lengths, key_mask)
+    scale = _scale(scale, D)
+    names = AttentionGrads._fields
+    need = names if need is None else tuple(need)
+    for name in need:
+        if name not in names:
+            raise ValueError(f"need names {name!r}: no gradient")
+    given = dict(dq=dq, dk=dk, dv=dv)
+    for name, t in given.items():
+        if t is not None and name not in need:
+            raise ValueError("a tensor for a gradient that need does not name")
+    if not need:
+        return AttentionGrads(None, None, None)
+    made, zero, out = [], 0, []
+    for bit, (name, shape) in enumerate(zip(names, ((Tq, Hq, D), (Tk, Hk, D), (Tk, Hk, D)))):
+        t = given[name]
+        if name not in need:
+            out += [None, 0, 0]
+        elif t is None:
+            given[name] = t = _new(stream, dev, shape, q.dtype)
+            made.append(t)
+            zero |= 1 << bit
+            out += [t.data_ptr(), shape[1] * D, D]
+        else:
+            out += [t.data_ptr(), *strides(t, name, shape)]
+    size = B.asp_attention_backward_workspace_bytes(Tq, Tk, Hq, Hk, D, G)
+    if workspace is None:
+        workspace = _new(stream, dev, size, torch.uint8)
+    _check_ws(workspace, size, dev)
+    at = B._at
+    B.launch(dev, B.lib().asp_attention_backward, do.data_ptr(), *sdo, q.data_ptr(), *sq, k.data_ptr(),
+             *sk, v.data_ptr(), *sv, o.data_ptr(), *so, lse.data_ptr(), _CODES[q.dtype], Tq, Tk, Hq, Hk,
+             D, scale, G, at(q_offsets), at(kv_offsets), at(kv_lengths), at(key_mask), *out, zero,
+             workspace.data_ptr(), workspace.numel(), B.stream_on(stream, dev))
+    _lend(stream, *made)
+    return AttentionGrads(*given.values())
+
+
+def _readable(t):
+    """t, or a copy where the kernels cannot read it as it lies."""
+    st, sh, sd = t.stride()
+    T, H, D = t.shape
+    e = t.element_size()
+    good = (D == 1 or sd == 1) and (T == 1 or st >= D and st * e % 16 == 0 and st <= 1 << 22) \
+        and (H == 1 or sh * e % 16 == 0) and t.data_ptr() % 16 == 0
+    return t if good else t.contiguous().clone() if t.is_contiguous() else t.contiguous()
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, q_offsets, kv_offsets, kv_lengths, key_mask, scale):
+        options = (q_offsets, kv_offsets, kv_lengths, key_mask)
+        o, lse = attention(q, k, v, scale=scale, q_offsets=q_offsets, kv_offsets=kv_offsets,
+                           kv_lengths=kv_lengths, key_mask=key_mask)
+        ctx.save_for_backward(q, k, v, o, lse, *options)
+        ctx.scale = scale
+        ctx.mark_non_differentiable(lse)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, _):
+        _no_capture()
+        q, k, v, o, lse, q_offsets, kv_offsets, kv_lengths, key_mask = ctx.saved_tensors
+        need = [n for n, w in zip(AttentionGrads._fields, ctx.needs_input_grad) if w]
+        g = attention_backward(_readable(do), q, k, v, o, lse, scale=ctx.scale, need=need,
+                               q_offsets=q_offsets, kv_offsets=kv_offsets, kv_lengths=kv_lengths,
+                               key_mask=key_mask)
+        return (*g, None, None, None, None, None)
+
+
+class Attention(torch.nn.Module):
+    """``attention`` as a module, differentiable in q, k and v.
+
+    q: (B, Tq, Hq, D), k and v: (B, Tk, Hk, D) with key_mask (B, Tk) and kv_lengths (B); or
+    packed, (T, H, D) with q_offsets and kv_offsets, key_mask (Tk) and kv_lengths (G).  k may be
+    an ``Nvfp4Cache`` (packed form; no gradients).  Returns o of q's shape.  Gradients are
+    reverse mode; forward-mode tangents are refused.  Under a HIP graph capture, gradients are
+    refused: capture ``attention`` and ``attention_backward``, which keep no graph of their
+    own."""
+
+    def __init__(self, scale=None):
+        super().__init__()
+        if scale is not None:
+            _scale(scale, 1)
+        self.scale = scale
+
+    def forward(self, q, k, v=None, q_offsets=None, kv_offsets=None, kv_lengths=None, key_mask=None):
+        shape = q.shape
+        cached = isinstance(k, Nvfp4Cache)
+        if q.dim() == 4:
+            if cached or q_offsets is not None or kv_offsets is not None:
+                raise ValueError("a cache and offsets go with packed sequences, (T, H, D)")
+            if v is None or k.dim() != 4 or k.shape[0] != shape[0]:
+                raise ValueError(f"k and v must be (B, Tk, Hk, D) with B = {shape[0]}")
+            n, Tq, Tk = shape[0], shape[1], k.shape[1]
+            if v.shape != k.shape:
+                raise ValueError(f"v must have the shape of k, {tuple(k.shape)}, got {tuple(v.shape)}")
+            if key_mask is not None:
+                if key_mask.shape != (n, Tk):
+                    raise ValueError(f"key_mask must be ({n}, {Tk}), got {tuple(key_mask.shape)}")
+                key_mask = key_mask.reshape(-1)
+            if n == 0 or Tq == 0:
+                return q.clone()
+            if n > 1:
+                q_offsets, kv_offsets = (torch.arange(n + 1, dtype=torch.int32, device=q.device) * T
+                                         for T in (Tq, Tk))
+            q, k, v = (t.reshape(-1, *t.shape[2:]) for t in (q, k, v))
+        elif q.dim() != 3:
+            raise ValueError(f"q must be (B, T, H, D) or (T, H, D), got {tuple(shape)}")
+        if key_mask is not None:
+            key_mask = key_mask.contiguous()
+        options = dict(q_offsets=q_offsets, kv_offsets=kv_offsets, kv_lengths=kv_lengths,
+                       key_mask=key_mask)
+        scale = _scale(self.scale, shape[-1])
+        leaves = (q,) if cached else (q, k, v)
+        _no_forward_mode(*leaves)
+        grads = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in leaves)
+        if cached:
+            if grads:
+                raise RuntimeError("no gradients through a cache")
+            return attention(_readable(q), k, v, scale=scale, **options)[0].reshape(shape)
+        q, k, v = (_readable(t) for t in (q, k, v))
+        if grads:
+            _no_capture()
+            o, _ = _Attention.apply(q, k, v, *options.values(), scale)
+        else:
+            o, _ = attention(q, k, v, scale=scale, **options)
+        return o.reshape(shape)
+
+    def extra_repr(self) -> str:
+        return f"scale={self.scale}"

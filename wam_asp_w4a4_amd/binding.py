@@ -26,6 +26,7 @@ ASP_F32 = 0
 ASP_BF16 = 1
 ASP_E4M3 = 2          # asp_norm_gate's n in the 8-bit format
 ASP_NORM_NONE, ASP_NORM_RMS, ASP_NORM_LAYER = 0, 1, 2
+ASP_ROTATE_PAIRS, ASP_ROTATE_HALVES = 0, 1
 DTYPES = {"f32": ASP_F32, "bf16": ASP_BF16}
 
 # name -> (restype, argtypes); mirrors include/asp.h
@@ -96,6 +97,29 @@ SIGNATURES = {
                                       _i64, _f32, _i32, _p, _p, _i32, _p, _p, _p, _i64, _i32, _p,
                                       _f32, _p, _i64, _p, _i64, _i32, _p, _p, _p, _p, _p, _p,
                                       _i64, _p, _sz, _p]),
+    "asp_head_norm": (_i32, [_p, _i64, _i64, _i32, _p, _i64, _i64, _i32, _i32, _i64, _i32, _i32,
+                             _p, _p, _f32, _p, _p, _i64, _i32, _i32, _p, _p, _i64, _i64, _p, _i64,
+                             _i64, _i32, _i32, _p]),
+    "asp_head_norm_backward_workspace_bytes": (_i32, [_i64, _i32, _i32, _i32, _psz]),
+    "asp_head_norm_backward": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _i32, _p, _i64, _i64, _i32,
+                                      _p, _i64, _i64, _i32, _i32, _i64, _i32, _i32, _p, _p, _f32,
+                                      _p, _p, _i64, _i32, _i32, _p, _p, _i64, _i64, _p, _i64, _i64,
+                                      _i32, _p, _p, _p, _sz, _p]),
+    "asp_attention_workspace_bytes": (_i32, [_i64, _i64, _i32, _i32, _i32, _i32, _psz]),
+    "asp_attention": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i32, _i64, _i64, _i32,
+                             _i32, _i32, _f32, _i32, _p, _p, _p, _p, _p, _i64, _i64, _p, _i32, _p,
+                             _sz, _p]),
+    "asp_attention_backward_workspace_bytes": (_i32, [_i64, _i64, _i32, _i32, _i32, _i32, _psz]),
+    "asp_attention_backward": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64,
+                                      _p, _i64, _i64, _p, _i32, _i64, _i64, _i32, _i32, _i32, _f32,
+                                      _i32, _p, _p, _p, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64,
+                                      _i64, _i32, _p, _sz, _p]),
+    "asp_kv_store": (_i32, [_p, _i64, _i64, _p, _i64, _i64, _i32, _i64, _i32, _i32, _i32, _p, _p, _p,
+                            _i64, _p, _p, _p, _p, _p]),
+    "asp_kv_load": (_i32, [_p, _p, _p, _p, _i64, _i32, _i32, _p, _p, _i32, _p]),
+    "asp_attention_cache": (_i32, [_p, _i64, _i64, _i32, _p, _p, _p, _p, _i64, _i64, _i32, _i32, _i32,
+                                   _f32, _i32, _p, _p, _p, _p, _p, _i64, _i64, _p, _i32, _p, _sz,
+                                   _p]),
 }
 
 _lib = None
@@ -532,3 +556,79 @@ def asp_norm_gate_backward(dh, lddh, dn, lddn, dn_dtype, h, ldh, y, ldy, dtype, 
         eps, _at(dx), lddx, _at(dy), lddy, zero, _ptr(d_post_w), _at(d_gate), _ptr(d_pre_w),
         _ptr(d_pre_b), _at(d_scale), _at(d_shift), ldd, _ptr(workspace), workspace_bytes,
         _stream(stream, dh, dn)))
+
+
+# ------------------------------------------------------- a block's attention
+
+
+def asp_head_norm(q, ldq, hsq, Hq, k, ldk, hsk, Hk, dtype, T, D, norm, q_w, k_w, eps, cosine, sine,
+                  P, rot, layout, positions, q_out, ldqo, hsqo, k_out, ldko, hsko, out_dtype, zero=0,
+                  stream=None):
+    _check(lib().asp_head_norm(_at(q), ldq, hsq, Hq, _at(k), ldk, hsk, Hk, dtype, T, D, norm,
+                               _ptr(q_w), _ptr(k_w), eps, _ptr(cosine), _ptr(sine), P, rot, layout,
+                               _ptr(positions), _at(q_out), ldqo, hsqo, _at(k_out), ldko, hsko,
+                               out_dtype, zero, _stream(stream, q)))
+
+
+def asp_head_norm_backward_workspace_bytes(T, Hq, Hk, D) -> int:
+    return _size("asp_head_norm_backward_workspace_bytes", T, Hq, Hk, D)
+
+
+def asp_head_norm_backward(dq, lddq, hsdq, dk, lddk, hsdk, d_dtype, q, ldq, hsq, Hq, k, ldk, hsk, Hk,
+                           dtype, T, D, norm, q_w, k_w, eps, cosine, sine, P, rot, layout, positions,
+                           dq_in, lddqi, hsdqi, dk_in, lddki, hsdki, zero, d_q_w, d_k_w, workspace,
+                           workspace_bytes, stream=None):
+    _check(lib().asp_head_norm_backward(
+        _at(dq), lddq, hsdq, _at(dk), lddk, hsdk, d_dtype, _at(q), ldq, hsq, Hq, _at(k), ldk, hsk, Hk,
+        dtype, T, D, norm, _ptr(q_w), _ptr(k_w), eps, _ptr(cosine), _ptr(sine), P, rot, layout,
+        _ptr(positions), _at(dq_in), lddqi, hsdqi, _at(dk_in), lddki, hsdki, zero, _ptr(d_q_w),
+        _ptr(d_k_w), _ptr(workspace), workspace_bytes, _stream(stream, dq, dk)))
+
+
+def asp_attention_workspace_bytes(Tq, Tk, Hq, Hk, D, G) -> int:
+    return _size("asp_attention_workspace_bytes", Tq, Tk, Hq, Hk, D, G)
+
+
+def asp_attention(q, ldq, hsq, k, ldk, hsk, v, ldv, hsv, dtype, Tq, Tk, Hq, Hk, D, scale, G, q_offsets,
+                  kv_offsets, kv_lengths, key_mask, o, ldo, hso, lse, zero=0, workspace=None,
+                  workspace_bytes=0, stream=None):
+    _check(lib().asp_attention(
+        _at(q), ldq, hsq, _at(k), ldk, hsk, _at(v), ldv, hsv, dtype, Tq, Tk, Hq, Hk, D, scale, G,
+        _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_lengths), _ptr(key_mask), _at(o), ldo, hso,
+        _ptr(lse), zero, _ptr(workspace), workspace_bytes, _stream(stream, q)))
+
+
+def asp_attention_backward_workspace_bytes(Tq, Tk, Hq, Hk, D, G) -> int:
+    return _size("asp_attention_backward_workspace_bytes", Tq, Tk, Hq, Hk, D, G)
+
+
+def asp_attention_backward(dout, lddo, hsdo, q, ldq, hsq, k, ldk, hsk, v, ldv, hsv, o, ldo, hso, lse,
+                           dtype, Tq, Tk, Hq, Hk, D, scale, G, q_offsets, kv_offsets, kv_lengths,
+                           key_mask, dq, lddq, hsdq, dk, lddk, hsdk, dv, lddv, hsdv, zero, workspace,
+                           workspace_bytes, stream=None):
+    _check(lib().asp_attention_backward(
+        _at(dout), lddo, hsdo, _at(q), ldq, hsq, _at(k), ldk, hsk, _at(v), ldv, hsv, _at(o), ldo, hso,
+        _ptr(lse), dtype, Tq, Tk, Hq, Hk, D, scale, G, _ptr(q_offsets), _ptr(kv_offsets),
+        _ptr(kv_lengths), _ptr(key_mask), _at(dq), lddq, hsdq, _at(dk), lddk, hsdk, _at(dv), lddv,
+        hsdv, zero, _ptr(workspace), workspace_bytes, _stream(stream, dout, k)))
+
+
+def asp_kv_store(k, ldk, hsk, v, ldv, hsv, dtype, T, Hk, D, G, offsets, kv_offsets, kv_lengths, rows,
+                 k_codes, k_scales, v_codes, v_scales, stream=None):
+    _check(lib().asp_kv_store(_at(k), ldk, hsk, _at(v), ldv, hsv, dtype, T, Hk, D, G, _ptr(offsets),
+                              _ptr(kv_offsets), _ptr(kv_lengths), rows, _ptr(k_codes),
+                              _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream, k)))
+
+
+def asp_kv_load(k_codes, k_scales, v_codes, v_scales, rows, Hk, D, k, v, dtype, stream=None):
+    _check(lib().asp_kv_load(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), rows, Hk, D,
+                             _ptr(k), _ptr(v), dtype, _stream(stream, k, v)))
+
+
+def asp_attention_cache(q, ldq, hsq, dtype, k_codes, k_scales, v_codes, v_scales, Tq, Tk, Hq, Hk, D,
+                        scale, G, q_offsets, kv_offsets, kv_lengths, key_mask, o, ldo, hso, lse, zero=0,
+                        workspace=None, workspace_bytes=0, stream=None):
+    _check(lib().asp_attention_cache(
+        _at(q), ldq, hsq, dtype, _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), Tq, Tk,
+        Hq, Hk, D, scale, G, _ptr(q_offsets), _ptr(kv_offsets), _ptr(kv_lengths), _ptr(key_mask),
+        _at(o), ldo, hso, _ptr(lse), zero, _ptr(workspace), workspace_bytes, _stream(stream, q)))

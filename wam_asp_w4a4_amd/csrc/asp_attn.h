@@ -1,0 +1,383 @@
+// Shared pieces of the attention kernels, forward and backward.
+//
+//   o = softmax(scale q k^T) v      for the queries and keys of each packed sequence
+//
+// Matrices in registers.  The 32 x 32 MFMA's accumulator has, in lane l, column l % 32 and
+// the 16 rows 8 (v / 4) + 4 (l / 32) + v % 4.  Scores are computed transposed (keys are
+// the rows, queries the columns; in the backward for dk and dv the other way round), so
+// that a lane holds 16 keys of one query: a softmax's sums run inside a lane, and the
+// rounded weights are, as they lie, the right operand of the next product, whose
+// contraction runs over the same keys.  That operand wants, for each 16 keys, eight of
+// them in each half of the wave; which eight is free, as long as the left operand has the
+// same: keys 4 h + {0..3} and 8 + 4 h + {0..3} for half h.  The left operand (a transposed
+// tile of rows) comes from LDS by transposing reads.
+//
+// Tiles of rows in LDS.  A row of D elements is 16-byte pieces; piece c of row r lies at
+// place c ^ swizzle(r) of its row, so that both the reads of 32 rows at one piece and the
+// transposing reads of 4 rows by 64 bytes fall in distinct banks.  Rows go from memory
+// to LDS without registers (16 bytes a lane; the swizzle is in the lanes' addresses).
+// They are read through buffer descriptors: an offset past the end gives zeros, and that
+// is how rows behind the sequence, masked rows and elements past D become zeros.
+#pragma once
+
+#include <algorithm>
+
+#include "asp_fp8.h"
+
+namespace asp {
+
+constexpr int kMaxAttnD = 128;
+constexpr int64_t kMaxAttnStride = (int64_t)1 << 22;  // of tokens, elements: 64 rows span less than 2^31 bytes
+constexpr int kFar = 0x7FFFFFF0;                      // an offset past every descriptor's end
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+struct AttnArgs {
+  const void *q, *k, *v;
+  void* o;
+  int64_t qt, qh, kt, kh, vt, vh, ot, oh;  // token and head strides, elements
+  const uint8_t *kc, *ks, *vc, *vs;        // a cache's codes [Tk][Hk][D / 2] and scales [Tk][Hk][D / 16]
+  float* lse;                              // [Tq][Hq]
+  const int32_t *qo, *ko, *kl;             // offsets of the sequences, and how many of a sequence's keys count
+  const uint8_t* mask;                     // [Tk]
+  int64_t Tq, Tk;
+  int Hq, Hk, group, D, G, splits, slots, zero;
+  float scale;
+  float* part;    // [splits][Tq][Hq][D]
+  float* part_l;  // [splits][Tq][Hq]
+  // backward
+  const void* dout;
+  int64_t gt, gh;
+  void *dq, *dk, *dv;
+  int64_t dqt, dqh, dkt, dkh, dvt, dvh;
+  float2* rows;  // [Tq][Hq]: the logarithm (base 2) of a query's sum and do . o
+  float *part_dq, *part_dk, *part_dv;
+};
+
+// ------------------------------------------------------------------- device
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rows(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ void attn_copy(__amdgpu_buffer_rsrc_t r, int offset, void* lds_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16,
+                                           offset, 0, 0, 0);
+}
+// What takes a score to the exponent of 2.  It never becomes 0: minus infinity, a key that does not
+// count, has to stay that.
+constexpr float kLeast = 1.17549435e-38f;
+__device__ __forceinline__ float attn_factor(float scale) { return fmaxf(scale * kLog2e, kLeast); }
+
+// every copy of this wave has landed and every LDS read is done; with WG, of the workgroup's
+template <bool WG>
+__device__ __forceinline__ void attn_settle() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  if constexpr (WG) __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// f of the two halves of the wave, in both
+template <typename F>
+__device__ __forceinline__ float both_halves(float x, F&& f) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  return f(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
+// A tile of rows in LDS: DT * 32 elements of ES bytes
+template <int ES, int DT>
+struct Rows {
+  static constexpr int BYTES = DT * 32 * ES, PIECES = BYTES / 16;
+  static_assert(PIECES % 8 == 0, "the swizzle permutes eight or sixteen pieces");
+  static __device__ __forceinline__ int swizzle(int row) {
+    return PIECES == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : (row & 3) << 2 | (row >> 2 & 3);
+  }
+  // the row and piece of memory that a lane's copy `i` (of 64 pieces) has in its place
+  static __device__ __forceinline__ int row_of(int i, int lane) { return (64 * i + lane) / PIECES; }
+  static __device__ __forceinline__ int piece_of(int i, int lane) {
+    return (64 * i + lane) % PIECES ^ swizzle(row_of(i, lane));
+  }
+};
+
+// the left operand's 16 bytes: piece 2 s + half of row `lane % 32`
+template <int ES, int DT>
+__device__ __forceinline__ u32x4_t row_frag(const uint8_t* tile, int s, int half, int l32) {
+  using R = Rows<ES, DT>;
+  return *reinterpret_cast<const u32x4_t*>(tile + l32 * R::BYTES +
+                                           16 * ((2 * s) ^ (half ^ R::swizzle(l32))));
+}
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+// The left operand of 16-bit elements for the transposed tile: lane l has column
+// 32 dt + l % 32 of rows 16 s + 4 h + {0..3} and 8 more.  One transposing read has 16 lanes
+// fetch 4 rows of 16 elements, lane i element 4 (i % 4) on of row i / 4, and hands
+// lane i column i.
+template <int DT>
+__device__ __forceinline__ s16x8_t column_frag(const uint8_t* tile, int s, int dt, int lane) {
+  using R = Rows<2, DT>;
+  const int half = lane >> 5, i = lane & 15;
+  s16x8_t out;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int row = 16 * s + 8 * b + 4 * half + (i >> 2);
+    const int piece = (4 * dt + 2 * (lane >> 4 & 1) + (i >> 1 & 1)) ^ R::swizzle(row & 15);
+    const auto* p = reinterpret_cast<const s16x4_t*>(tile + row * R::BYTES + 16 * piece + 8 * (i & 1));
+    const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4_t*)p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[4 * b + k] = v[k];
+  }
+  return out;
+}
+
+// and of float32 elements: column 32 dt + l % 32 of row 8 i + 4 h + e
+template <int DT>
+__device__ __forceinline__ float column_value(const uint8_t* tile, int i, int e, int dt, int lane) {
+  using R = Rows<4, DT>;
+  const int row = 8 * i + 4 * (lane >> 5) + e, l32 = lane & 31;
+  const int piece = (8 * dt + (l32 >> 2)) ^ R::swizzle(row & 15);
+  return *reinterpret_cast<const float*>(tile + row * R::BYTES + 16 * piece + 4 * (l32 & 3));
+}
+
+// How products are computed.  Half: fp16, which holds the 4-bit format's values exactly.
+struct Bf16 {
+  static constexpr int ES = 2;
+  static __device__ __forceinline__ f32x16_t mfma(s16x8_t a, s16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) { return bf16x2_rne(a, b); }
+};
+struct Half {
+  static constexpr int ES = 2;
+  static __device__ __forceinline__ f32x16_t mfma(s16x8_t a, s16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                                  __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {
+    const half2_t v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+};
+struct Full {
+  static constexpr int ES = 4;
+};
+
+// acc += rows (one piece of the left operand) times the right operand's piece
+template <typename P>
+__device__ __forceinline__ void piece_mfma(u32x4_t a, u32x4_t b, f32x16_t& acc) {
+  if constexpr (P::ES == 2)
+    acc = P::mfma(__builtin_bit_cast(s16x8_t, a), __builtin_bit_cast(s16x8_t, b), acc);
+  else
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__builtin_bit_cast(float, (uint32_t)a[e]),
+                                                 __builtin_bit_cast(float, (uint32_t)b[e]), acc, 0, 0, 0);
+}
+
+// The accumulator `w` (32 rows of weights) as the right operand of products over those rows
+template <typename P>
+struct Weights {
+  s16x8_t half[2];
+  __device__ __forceinline__ void set(const f32x16_t& w) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4_t u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = P::pair(w[8 * s + 2 * e], w[8 * s + 2 * e + 1]);
+      half[s] = __builtin_bit_cast(s16x8_t, u);
+    }
+  }
+};
+template <>
+struct Weights<Full> {
+  f32x16_t w;
+  __device__ __forceinline__ void set(const f32x16_t& x) { w = x; }
+};
+
+// acc[dt] += (the tile's columns) times the weights of its 32 rows
+template <typename P, int DT>
+__device__ __forceinline__ void columns_mfma(const uint8_t* tile, const Weights<P>& w,
+                                             f32x16_t (&acc)[DT], int lane) {
+  if constexpr (P::ES == 2) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+        acc[dt] = P::mfma(column_frag<DT>(tile, s, dt, lane), w.half[s], acc[dt]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+          acc[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(column_value<DT>(tile, i, e, dt, lane),
+                                                         w.w[4 * i + e], acc[dt], 0, 0, 0);
+  }
+}
+
+// A lane's row of accumulators, elements of a transposed 32-column tile, to memory: `row` is the
+// lane's output row, D its elements; XT float or uint16_t (bf16).
+template <typename XT, int DT>
+__device__ __forceinline__ void store_row(XT* row, const f32x16_t (&acc)[DT], float factor, int D,
+                                          int half) {
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {
+    if constexpr (sizeof(XT) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = 32 * dt + 8 * i + 4 * half;
+        if (d < D)
+          *reinterpret_cast<f32x4_t*>(row + d) =
+              f32x4_t{acc[dt][4 * i] * factor, acc[dt][4 * i + 1] * factor,
+                      acc[dt][4 * i + 2] * factor, acc[dt][4 * i + 3] * factor};
+      }
+    } else {
+      // the halves of the wave exchange four elements: each has eight consecutive ones
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t a = bf16x2_rne(acc[dt][4 * i + 2 * e] * factor, acc[dt][4 * i + 2 * e + 1] * factor);
+          const uint32_t b = bf16x2_rne(acc[dt][4 * i + 4 + 2 * e] * factor, acc[dt][4 * i + 5 + 2 * e] * factor);
+          const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+          w[e] = r[0];
+          w[2 + e] = r[1];
+        }
+        const int d = 32 * dt + 8 * (i + half);
+        if (d < D) *reinterpret_cast<u32x4_t*>(row + d) = u32x4_t{w[0], w[1], w[2], w[3]};
+      }
+    }
+  }
+}
+
+// One sequence's rows and keys
+struct AttnSeq {
+  int64_t q0, k0;
+  int64_t rows;  // tokens
+  int64_t keys;  // that count
+  int64_t all;   // keys
+  int64_t tile;  // the block's tile of the sequence
+  bool any;
+};
+
+__device__ __forceinline__ int64_t attn_offset(const int32_t* o, int g, int64_t total) {
+  return min(max((int64_t)o[g], (int64_t)0), total);
+}
+
+// Which sequence and tile a slot stands for.  Rows of `per` tiles: a sequence's first slot is
+// (its first row) / tile + g, which leaves each sequence enough slots and none to two.  The
+// wave searches 64 sequences at a time.  Offsets that are out of range or decrease give
+// sequences inside the tensors all the same.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* offsets, int64_t total,
+                                            int group, int tile_rows, int slot) {
+  AttnSeq s = {};
+  int g = 0;
+  s.tile = slot;
+  s.any = true;
+  if (offsets) {
+    auto first = [&](int i) {
+      return (int64_t)((uint64_t)(attn_offset(offsets, i, total) * group) / (uint32_t)tile_rows) + i;
+    };
+    const int lane = threadIdx.x & 63;
+    int n = a.G;
+    while (n > 0) {
+      const int step = (n + 63) / 64, i = g + lane * step;
+      const bool before = lane * step < n && first(i) <= slot;
+      const int count = __builtin_popcountll(__ballot(before));
+      if (count == 0) {
+        s.any = false;
+        break;
+      }
+      g += (count - 1) * step;
+      n = step > 1 ? min(step, n - (count - 1) * step) : 0;
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    if (s.any) s.tile = slot - first(g);
+  }
+  s.q0 = a.qo ? attn_offset(a.qo, g, a.Tq) : 0;
+  s.rows = (a.qo ? attn_offset(a.qo, g + 1, a.Tq) : a.Tq) - s.q0;
+  s.k0 = a.ko ? attn_offset(a.ko, g, a.Tk) : 0;
+  s.all = max((a.ko ? attn_offset(a.ko, g + 1, a.Tk) : a.Tk) - s.k0, (int64_t)0);
+  s.keys = a.kl ? min(s.all, max((int64_t)a.kl[g], (int64_t)0)) : s.all;
+  s.rows = max(s.rows, (int64_t)0);
+  return s;
+}
+
+// XCD-aware order: consecutive workgroups go to the 8 XCDs in turn; each takes one contiguous
+// run, so that the tiles of a head, which read the same keys, share an L2.
+__device__ __forceinline__ int64_t attn_run(uint32_t id, uint32_t total) {
+  const uint32_t xcd = id % 8;
+  return (int64_t)xcd * (total / 8) + min(xcd, total % 8) + id / 8;
+}
+
+// Rows of no sequence: f(token) for the tokens outside the offsets, a share for each slot
+template <typename F>
+__device__ __forceinline__ void attn_outside(const int32_t* offsets, int G, int64_t total, int slot,
+                                             int slots, F&& f) {
+  const int64_t share = (total + slots - 1) / slots, t0 = slot * share, t1 = min(t0 + share, total);
+  const int64_t in0 = attn_offset(offsets, 0, total), in1 = attn_offset(offsets, G, total);
+  for (int64_t t = t0; t < t1; ++t) {
+    if (t >= in0 && t < in1)
+      t = in1 - 1;  // to the sequences' end
+    else
+      f(t);
+  }
+}
+
+// ------------------------------------------------------------- host helpers
+
+// slots of tiles of `tile` rows out of `rows` in G sequences
+inline int64_t attn_slots(int64_t rows, int64_t tile, int G, bool ragged) {
+  return ragged ? rows / tile + G : (rows + tile - 1) / tile;
+}
+
+// (T, H, D) rows that the kernels read in 16-byte pieces
+inline int32_t check_attn_rows(const void* p, int32_t dtype, int64_t T, int H, int D, int64_t st,
+                               int64_t sh, bool out, const char* name) {
+  const int per = dtype == ASP_BF16 ? 8 : 4;  // elements of 16 bytes
+  ASP_TRY(check_ptr(p, name, true));
+  if (st % per || sh % per)
+    return fail(ASP_ERR_ALIGN, "strides %lld, %lld of %s are not multiples of %d elements",
+                (long long)st, (long long)sh, name, per);
+  if ((T > 1 && st < D) || st < 0 || st > kMaxAttnStride || sh < 0 || sh > ((int64_t)1 << 40))
+    return fail(ASP_ERR_SHAPE, "strides %lld, %lld of %s", (long long)st, (long long)sh, name);
+  if (!out) return ASP_OK;
+  const bool by_token = (H <= 1 || sh >= D) && (T <= 1 || st >= (H - 1) * sh + D);
+  const bool by_head = (T <= 1 || st >= D) && (H <= 1 || sh >= (T - 1) * st + D);
+  if (!by_token && !by_head)
+    return fail(ASP_ERR_SHAPE, "strides %lld, %lld of %s let heads overlap", (long long)st,
+                (long long)sh, name);
+  return ASP_OK;
+}
+
+inline int32_t check_attn(int32_t dtype, int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D,
+                          int32_t G, float scale, const int32_t* qo, const int32_t* ko,
+                          const int32_t* kl) {
+  ASP_TRY(check_io_dtype(dtype, "dtype"));
+  if (Tq < 0 || Tq > INT32_MAX || Tk < 0 || Tk > INT32_MAX)
+    return fail(ASP_ERR_SHAPE, "Tq=%lld, Tk=%lld outside [0, 2^31)", (long long)Tq, (long long)Tk);
+  if (Hq < 1 || Hk < 1 || Hq > 65535 || Hq % Hk)
+    return fail(ASP_ERR_SHAPE, "Hq=%d is not a multiple of Hk=%d in [1, 65535]", Hq, Hk);
+  if (D < 8 || D > kMaxAttnD || D % 8)
+    return fail(ASP_ERR_SHAPE, "D=%d is not a multiple of 8 in [8, %d]", D, kMaxAttnD);
+  if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
+  if (!(scale > 0.0f) || !(scale < 3.0e38f)) return fail(ASP_ERR_ARG, "scale=%g", scale);
+  if ((!qo || !ko) && G != 1)
+    return fail(ASP_ERR_ARG, "offsets are NULL with G=%d sequences", G);
+  if ((uintptr_t)qo & 3 || (uintptr_t)ko & 3 || (uintptr_t)kl & 3)
+    return fail(ASP_ERR_ALIGN, "offsets or lengths are not 4-byte aligned");
+  return ASP_OK;
+}
+
+inline int32_t check_attn_grid(int64_t blocks, int threads) {
+  if (blocks * threads > kMaxLanes)
+    return fail(ASP_ERR_SHAPE, "%lld workgroups are more than one launch has", (long long)blocks);
+  return ASP_OK;
+}
+
+}  // namespace asp

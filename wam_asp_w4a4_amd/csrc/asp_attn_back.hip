@@ -1,0 +1,616 @@
+// Attention, backward.  With p = exp(scale q k^T - lse), computed anew from the forward's
+// logarithms, and delta = do . o of each query:
+//
+//   ds = p (do v^T - delta),   dq = scale ds k,   dk = scale ds^T q,   dv = p^T do
+//
+// Two passes, each with its sums in registers and in a fixed order, so that the results
+// are the same bits on every call: k_attn_dq holds queries and goes over the keys
+// (three products), k_attn_dkv holds keys and goes over the queries of all heads that
+// share them (four).  That is two products more than one pass would need, whose dq would
+// have to be added to memory by atomics in any order, or kept in parts for each tile of
+// keys.  asp_attn.h has the layouts: as in the forward, the accumulators of p and ds are,
+// rounded to bf16 (half a step each, signs averaging out over the sums), the right
+// operands of the products that contract over them.
+#include "asp_attn.h"
+
+namespace asp {
+namespace {
+
+template <typename XT>
+using Product = std::conditional_t<sizeof(XT) == 4, Full, Bf16>;
+
+// a lane's pieces of one row of a matrix: D elements, zeros where `valid` is false
+template <typename XT, int QS>
+__device__ __forceinline__ void row_pieces(const XT* row, bool valid, int D, int half,
+                                           u32x4_t (&f)[QS]) {
+#pragma unroll
+  for (int s = 0; s < QS; ++s) {
+    const int d = (2 * s + half) * (16 / (int)sizeof(XT));
+    f[s] = valid && d < D ? *reinterpret_cast<const u32x4_t*>(row + d) : u32x4_t{0, 0, 0, 0};
+  }
+}
+
+template <typename XT>
+__device__ __forceinline__ float piece_dot(u32x4_t a, u32x4_t b, float sum) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(XT) == 2) {
+      sum = __builtin_fmaf(bf16_lo(a[e]), bf16_lo(b[e]), sum);
+      sum = __builtin_fmaf(bf16_hi(a[e]), bf16_hi(b[e]), sum);
+    } else {
+      sum = __builtin_fmaf(__builtin_bit_cast(float, (uint32_t)a[e]),
+                           __builtin_bit_cast(float, (uint32_t)b[e]), sum);
+    }
+  }
+  return sum;
+}
+
+// A query's logarithm to base 2, made +infinity where the row has no key: its p are then 0
+__device__ __forceinline__ float row_log(float lse) {
+  return lse == kNegInf ? -kNegInf : lse * kLog2e;
+}
+
+// Zeros to the heads [h0, h0 + heads) of token t
+template <typename XT>
+__device__ __forceinline__ void zero_heads(void* p, int64_t t, int64_t st, int64_t sh, int h0,
+                                           int heads, int D, int threads) {
+  const int pieces = D * (int)sizeof(XT) / 16;
+  for (int i = threadIdx.x; i < heads * pieces; i += threads)
+    *reinterpret_cast<u32x4_t*>(static_cast<XT*>(p) + t * st + (h0 + i / pieces) * sh +
+                                i % pieces * (16 / sizeof(XT))) = u32x4_t{0, 0, 0, 0};
+}
+
+// Joins the accumulators of W columns of waves in LDS: column 0 has the sums (false: another's
+// wave, which is done).  `wave` counts the waves of a column.
+template <int W, int WAVES, int N>
+__device__ __forceinline__ bool join_columns(uint8_t* smem, int column, int wave, int lane,
+                                             f32x16_t (&acc)[N]) {
+  if constexpr (W > 1) {
+    float* at = reinterpret_cast<float*>(smem) + lane;
+    __syncthreads();
+    if (column > 0) {
+      float* to = at + ((column - 1) * WAVES + wave) * N * 16 * 64;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) to[(16 * n + v) * 64] = acc[n][v];
+    }
+    __syncthreads();
+    if (column > 0) return false;
+#pragma unroll
+    for (int w = 0; w < W - 1; ++w) {
+      const float* from = at + (w * WAVES + wave) * N * 16 * 64;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[n][v] += from[(16 * n + v) * 64];
+    }
+  }
+  return true;
+}
+
+template <typename XT, int DT, int WM, int WK, int KT>
+struct BackQ {
+  using P = Product<XT>;
+  using R = Rows<P::ES, DT>;
+  static constexpr int THREADS = 64 * WM * WK, BM = 32 * WM, BN = 32 * KT;
+  static constexpr int TILE = BN * R::BYTES, GROUP = 4 * TILE;
+  static constexpr int JOIN = (WK - 1) * WM * DT * 16 * 64 * 4;
+  static constexpr int LDS = WK * GROUP > JOIN ? WK * GROUP : JOIN;
+  static_assert(LDS <= 160 * 1024, "a CU has 160 KB of LDS");
+};
+
+// dq of 32 WM rows (a token's shared heads follow one another); WK columns of waves take
+// every WK-th tile of 32 KT keys.  Also writes each row's logarithm and delta for k_attn_dkv.
+template <typename XT, int DT, int WM, int WK, int KT>
+__global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS)) k_attn_dq(const AttnArgs a) {
+  using B = BackQ<XT, DT, WM, WK, KT>;
+  using P = typename B::P;
+  using R = typename B::R;
+  constexpr int BM = B::BM, BN = B::BN, TILE = B::TILE, QS = R::PIECES / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[B::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wm = wave % WM, wk = wave / WM;
+  const int64_t run = attn_run(blockIdx.x, gridDim.x);
+  const int slot = (int)(run % a.slots), split = (int)(run / a.slots % a.splits);
+  const int hk = (int)(run / a.slots / a.splits);
+  const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
+  if (a.zero & 1 && a.qo && split == 0)
+    attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
+      zero_heads<XT>(a.dq, t, a.dqt, a.dqh, hk * a.group, a.group, a.D, B::THREADS);
+    });
+  const int64_t row0 = seq.tile * BM, rows = seq.rows * a.group;
+  if (!seq.any || row0 >= rows) return;
+
+  const int64_t r = row0 + 32 * wm + l32;
+  const bool valid = r < rows;
+  const int64_t t_of = a.group == 1 ? r : r / a.group;
+  const int64_t token = seq.q0 + t_of;
+  const int head = hk * a.group + (int)(r - t_of * a.group);
+  const int64_t at = token * a.Hq + head;
+  u32x4_t qf[QS], df[QS];
+  row_pieces(static_cast<const XT*>(a.q) + token * a.qt + head * a.qh, valid, a.D, half, qf);
+  row_pieces(static_cast<const XT*>(a.dout) + token * a.gt + head * a.gh, valid, a.D, half, df);
+  float delta = 0.0f;
+  {
+    u32x4_t of[QS];
+    row_pieces(static_cast<const XT*>(a.o) + token * a.ot + head * a.oh, valid, a.D, half, of);
+#pragma unroll
+    for (int s = 0; s < QS; ++s) delta = piece_dot<XT>(df[s], of[s], delta);
+    delta = both_halves(delta, [](float x, float y) { return x + y; });
+  }
+  const float lg = valid ? row_log(a.lse[at]) : -kNegInf;
+  if (valid && half == 0 && wk == 0 && split == 0) a.rows[at] = make_float2(lg, delta);
+  const float c = attn_factor(a.scale);
+
+  f32x16_t acc[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
+
+  const int64_t tiles = (seq.keys + BN - 1) / BN;
+  const int64_t first = tiles * split / a.splits, last = tiles * (split + 1) / a.splits;
+  const int turns = (int)((last - first + WK - 1) / WK);
+  uint8_t* mine = smem + wk * B::GROUP;
+  auto key0 = [&](int t) { return (first + (int64_t)t * WK + wk) * BN; };
+  auto keys_of = [&](int t) -> uint64_t {
+    const int64_t k = key0(t) + lane;
+    bool on = lane < BN && t < turns && first + (int64_t)t * WK + wk < last && k < seq.keys;
+    if (on && a.mask) on = a.mask[seq.k0 + k] != 0;
+    return __ballot(on);
+  };
+  constexpr int COPIES = TILE / 1024 / WM;
+  static_assert(TILE % (1024 * WM) == 0, "whole copies for each wave");
+  int offk[COPIES], offv[COPIES];
+#pragma unroll
+  for (int i = 0; i < COPIES; ++i) {
+    const int row = R::row_of(wm * COPIES + i, lane), d = R::piece_of(wm * COPIES + i, lane) * (16 / P::ES);
+    offk[i] = d < a.D ? (row * (int)a.kt + d) * P::ES : kFar;
+    offv[i] = d < a.D ? (row * (int)a.vt + d) * P::ES : kFar;
+  }
+  auto issue = [&](int t, uint64_t live) {
+    uint8_t* to = mine + (t & 1) * 2 * TILE;
+    const int64_t k = seq.k0 + key0(t), n = min((int64_t)BN, seq.keys - key0(t));
+    const auto rk = attn_rows(static_cast<const XT*>(a.k) + (n > 0 ? k * a.kt + hk * a.kh : 0),
+                              n > 0 ? ((n - 1) * a.kt + a.D) * P::ES : 0);
+    const auto rv = attn_rows(static_cast<const XT*>(a.v) + (n > 0 ? k * a.vt + hk * a.vh : 0),
+                              n > 0 ? ((n - 1) * a.vt + a.D) * P::ES : 0);
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      // a masked key's elements would meet a weight of 0, and make NaN of NaN or infinity
+      const bool off = a.mask && !(live >> R::row_of(wm * COPIES + i, lane) & 1);
+      attn_copy(rk, off ? kFar : offk[i], to + (wm * COPIES + i) * 1024);
+      attn_copy(rv, off ? kFar : offv[i], to + TILE + (wm * COPIES + i) * 1024);
+    }
+  };
+
+  uint64_t live = keys_of(0);
+  issue(0, live);
+  for (int t = 0; t < turns; ++t) {
+    const uint64_t next = keys_of(t + 1);
+    const uint8_t* tile = mine + (t & 1) * 2 * TILE;
+    attn_settle<(WM > 1)>();
+    if (t + 1 < turns) issue(t + 1, next);
+    if (live != 0) {
+      f32x16_t s[KT], d[KT];
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[k][v] = d[k][v] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < QS; ++i)
+          piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * k * R::BYTES, i, half, l32), qf[i], s[k]);
+#pragma unroll
+        for (int i = 0; i < QS; ++i)
+          piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * k * R::BYTES, i, half, l32), df[i], d[k]);
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          d[k][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][v], c, -lg)) * (d[k][v] - delta);
+      }
+      constexpr uint64_t ALL = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
+      if (live != ALL)
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          const uint32_t bits = (uint32_t)(live >> (32 * k)) >> (4 * half);
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            if (!(bits >> (8 * (v >> 2) + (v & 3)) & 1)) d[k][v] = 0.0f;
+        }
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        Weights<P> w;
+        w.set(d[k]);
+        columns_mfma<P, DT>(tile + 32 * k * R::BYTES, w, acc, lane);
+      }
+    }
+    live = next;
+  }
+  if (!join_columns<WK, WM>(smem, wk, wm, lane, acc) || !valid) return;
+  if (a.splits > 1)
+    store_row<float, DT>(a.part_dq + ((int64_t)split * a.Tq * a.Hq + at) * a.D, acc, a.scale, a.D, half);
+  else
+    store_row<XT, DT>(static_cast<XT*>(a.dq) + token * a.dqt + head * a.dqh, acc, a.scale, a.D, half);
+}
+
+// Each row's logarithm and delta alone, where dq is not wanted.  Two lanes a row, which add as the
+// halves of a wave in k_attn_dq do: the same bits.
+template <typename XT>
+__global__ void __launch_bounds__(256) k_attn_rows(const AttnArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 128 + (threadIdx.x >> 1);
+  if (row >= a.Tq * a.Hq) return;
+  const int64_t t = row / a.Hq;
+  const int h = (int)(row - t * a.Hq);
+  if (a.qo && (t < attn_offset(a.qo, 0, a.Tq) || t >= attn_offset(a.qo, a.G, a.Tq))) return;
+  const XT* g = static_cast<const XT*>(a.dout) + t * a.gt + h * a.gh;
+  const XT* o = static_cast<const XT*>(a.o) + t * a.ot + h * a.oh;
+  constexpr int PER = 16 / sizeof(XT);
+  float delta = 0.0f;
+  for (int d = PER * (threadIdx.x & 1); d < a.D; d += 2 * PER)
+    delta = piece_dot<XT>(*reinterpret_cast<const u32x4_t*>(g + d),
+                          *reinterpret_cast<const u32x4_t*>(o + d), delta);
+  delta += __shfl_xor(delta, 1);
+  if ((threadIdx.x & 1) == 0) a.rows[row] = make_float2(row_log(a.lse[row]), delta);
+}
+
+template <typename XT, int DT, int WN, int WQ, int QT>
+struct BackKV {
+  using P = Product<XT>;
+  using R = Rows<P::ES, DT>;
+  static constexpr int THREADS = 64 * WN * WQ, BN = 32 * WN, BQ = 32 * QT;
+  static constexpr int TILE = BQ * R::BYTES;                 // queries or do
+  static constexpr int GROUP = 4 * TILE + 2 * 2 * BQ * 4;    // two buffers, and two of the rows' two values
+  static constexpr int JOIN = (WQ - 1) * WN * 2 * DT * 16 * 64 * 4;
+  static constexpr int LDS = WQ * GROUP > JOIN ? WQ * GROUP : JOIN;
+  static_assert(LDS <= 160 * 1024, "a CU has 160 KB of LDS");
+};
+
+// dk and dv of 32 WN keys of one head; WQ columns of waves take every WQ-th tile of 32 QT
+// queries, head by head of those that share the keys.
+template <typename XT, int DT, int WN, int WQ, int QT>
+__global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_dkv(const AttnArgs a) {
+  using B = BackKV<XT, DT, WN, WQ, QT>;
+  using P = typename B::P;
+  using R = typename B::R;
+  constexpr int BN = B::BN, BQ = B::BQ, TILE = B::TILE, QS = R::PIECES / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[B::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int wn = wave % WN, wq = wave / WN;
+  const int64_t run = attn_run(blockIdx.x, gridDim.x);
+  const int slot = (int)(run % a.slots), split = (int)(run / a.slots % a.splits);
+  const int hk = (int)(run / a.slots / a.splits);
+  const AttnSeq seq = attn_seq(a, a.ko, a.Tk, 1, BN, slot);
+  if (a.zero & 6 && a.ko && split == 0)
+    attn_outside(a.ko, a.G, a.Tk, slot, a.slots, [&](int64_t t) {
+      if (a.zero & 2) zero_heads<XT>(a.dk, t, a.dkt, a.dkh, hk, 1, a.D, B::THREADS);
+      if (a.zero & 4) zero_heads<XT>(a.dv, t, a.dvt, a.dvh, hk, 1, a.D, B::THREADS);
+    });
+  const int64_t key0 = seq.tile * BN;
+  if (!seq.any || key0 >= seq.all) return;
+
+  const int64_t key = key0 + 32 * wn + l32, krow = seq.k0 + key;
+  const bool stored = key < seq.all;
+  bool counts = key < seq.keys;
+  if (counts && a.mask) counts = a.mask[krow] != 0;
+  u32x4_t kf[QS], vf[QS];
+  row_pieces(static_cast<const XT*>(a.k) + krow * a.kt + hk * a.kh, counts, a.D, half, kf);
+  row_pieces(static_cast<const XT*>(a.v) + krow * a.vt + hk * a.vh, counts, a.D, half, vf);
+  const float c = attn_factor(a.scale);
+
+  f32x16_t acc[2 * DT];  // dv, dk
+#pragma unroll
+  for (int dt = 0; dt < 2 * DT; ++dt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
+  f32x16_t(&dv)[DT] = reinterpret_cast<f32x16_t(&)[DT]>(acc);
+  f32x16_t(&dk)[DT] = reinterpret_cast<f32x16_t(&)[DT]>(acc[DT]);
+
+  const int64_t per_head = (seq.rows + BQ - 1) / BQ;
+  // a workgroup without a key that counts has nothing to sum
+  const int64_t tiles = key0 < seq.keys ? per_head * a.group : 0;
+  const int64_t first = tiles * split / a.splits, last = tiles * (split + 1) / a.splits;
+  const int turns = (int)((last - first + WQ - 1) / WQ);
+  uint8_t* mine = smem + wq * B::GROUP;
+  float* row_log2 = reinterpret_cast<float*>(mine + 4 * TILE);  // [buffer][BQ], then the deltas
+  float* row_delta = row_log2 + 2 * BQ;
+  constexpr int COPIES = TILE / 1024 / WN;
+  static_assert(TILE % (1024 * WN) == 0, "whole copies for each wave");
+  int offq[COPIES], offd[COPIES];
+#pragma unroll
+  for (int i = 0; i < COPIES; ++i) {
+    const int row = R::row_of(wn * COPIES + i, lane), d = R::piece_of(wn * COPIES + i, lane) * (16 / P::ES);
+    offq[i] = d < a.D ? (row * (int)a.qt + d) * P::ES : kFar;
+    offd[i] = d < a.D ? (row * (int)a.gt + d) * P::ES : kFar;
+  }
+  float2 mine_row = make_float2(0.0f, 0.0f);
+  auto issue = [&](int t) {
+    uint8_t* to = mine + (t & 1) * 2 * TILE;
+    const int64_t tile = first + (int64_t)t * WQ + wq;
+    const int64_t h = per_head ? tile / per_head : 0, row = (tile - h * per_head) * BQ;
+    const int64_t n = tile < last ? min((int64_t)BQ, seq.rows - row) : 0;
+    const int head = hk * a.group + (int)h;
+    const int64_t q = seq.q0 + row;
+    const auto rq = attn_rows(static_cast<const XT*>(a.q) + (n > 0 ? q * a.qt + head * a.qh : 0),
+                              n > 0 ? ((n - 1) * a.qt + a.D) * P::ES : 0);
+    const auto rd = attn_rows(static_cast<const XT*>(a.dout) + (n > 0 ? q * a.gt + head * a.gh : 0),
+                              n > 0 ? ((n - 1) * a.gt + a.D) * P::ES : 0);
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i) {
+      attn_copy(rq, offq[i], to + (wn * COPIES + i) * 1024);
+      attn_copy(rd, offd[i], to + TILE + (wn * COPIES + i) * 1024);
+    }
+    // rows past the end: weights of 0
+    mine_row = make_float2(-kNegInf, 0.0f);
+    if (wn == 0 && lane < n) mine_row = a.rows[(q + lane) * a.Hq + head];
+  };
+
+  if (turns > 0) issue(0);
+  for (int t = 0; t < turns; ++t) {
+    const int b = t & 1;
+    const uint8_t* tile = mine + b * 2 * TILE;
+    if (wn == 0 && lane < BQ) {
+      row_log2[b * BQ + lane] = mine_row.x;
+      row_delta[b * BQ + lane] = mine_row.y;
+    }
+    attn_settle<(WN > 1)>();
+    if (t + 1 < turns) issue(t + 1);
+#pragma unroll
+    for (int j = 0; j < QT; ++j) {
+      f32x16_t s, d;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) s[v] = d[v] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < QS; ++i)
+        piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * j * R::BYTES, i, half, l32), kf[i], s);
+#pragma unroll
+      for (int i = 0; i < QS; ++i)
+        piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * j * R::BYTES, i, half, l32), vf[i], d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = b * BQ + 32 * j + 8 * i + 4 * half;
+        const f32x4_t lg = *reinterpret_cast<const f32x4_t*>(row_log2 + row);
+        const f32x4_t de = *reinterpret_cast<const f32x4_t*>(row_delta + row);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + e], c, -lg[e]));
+          s[4 * i + e] = p;
+          d[4 * i + e] = p * (d[4 * i + e] - de[e]);
+        }
+      }
+      Weights<P> wp, ws;
+      wp.set(s);
+      ws.set(d);
+      columns_mfma<P, DT>(tile + TILE + 32 * j * R::BYTES, wp, dv, lane);
+      columns_mfma<P, DT>(tile + 32 * j * R::BYTES, ws, dk, lane);
+    }
+  }
+  if (!join_columns<WQ, WN>(smem, wq, wn, lane, acc) || !stored) return;
+  // a key that does not count has gradients of 0
+  if (!counts)
+#pragma unroll
+    for (int dt = 0; dt < 2 * DT; ++dt)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
+  const int64_t at = krow * a.Hk + hk;
+  if (a.splits > 1) {
+    const int64_t part = ((int64_t)split * a.Tk * a.Hk + at) * a.D;
+    if (a.dv) store_row<float, DT>(a.part_dv + part, dv, 1.0f, a.D, half);
+    if (a.dk) store_row<float, DT>(a.part_dk + part, dk, a.scale, a.D, half);
+  } else {
+    if (a.dv) store_row<XT, DT>(static_cast<XT*>(a.dv) + krow * a.dvt + hk * a.dvh, dv, 1.0f, a.D, half);
+    if (a.dk) store_row<XT, DT>(static_cast<XT*>(a.dk) + krow * a.dkt + hk * a.dkh, dk, a.scale, a.D, half);
+  }
+}
+
+// The splits' sums of one or two tensors (blockIdx.y) of T x H heads, in order; 16 lanes a head
+struct SumArgs {
+  const float* part[2];
+  void* out[2];
+  int64_t st[2], sh[2];
+  const int32_t* offsets;
+  int64_t T;
+  int H, D, G, splits;
+};
+
+template <typename XT>
+__global__ void __launch_bounds__(256) k_attn_sum(const SumArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), rows = a.T * a.H;
+  const int d = 8 * (threadIdx.x & 15), which = blockIdx.y;
+  if (row >= rows || d >= a.D || !a.out[which]) return;
+  const int64_t t = row / a.H, h = row - t * a.H;
+  if (a.offsets && (t < attn_offset(a.offsets, 0, a.T) || t >= attn_offset(a.offsets, a.G, a.T))) return;
+  float v[8] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part[which] + (s * rows + row) * a.D + d);
+    const f32x4_t x = p[0], y = p[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] += x[e];
+      v[4 + e] += y[e];
+    }
+  }
+  XT* o = static_cast<XT*>(a.out[which]) + t * a.st[which] + h * a.sh[which] + d;
+  if constexpr (sizeof(XT) == 2) {
+    *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                             bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+  } else {
+    *reinterpret_cast<f32x4_t*>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+  }
+}
+
+// -------------------------------------------------------------------- host
+
+// The form of one of the two passes, by sizes alone: `held` rows in registers (queries with their
+// shared heads, or keys) of Hk heads, `passed` rows in all that go by.  wide: four waves of
+// different rows share the tiles; else a workgroup has 32 rows and its waves share the tiles.
+struct Plan {
+  bool wide;
+  int slots, splits;
+};
+
+Plan plan_of(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged) {
+  Plan p;
+  p.wide = attn_slots(held, 128, 1, false) * Hk >= 256;
+  const int tile = p.wide ? 128 : 32;
+  p.slots = (int)attn_slots(held, tile, G, ragged);
+  const int64_t blocks = std::max<int64_t>(1, (held + tile - 1) / tile) * Hk;
+  const int64_t tiles = (passed / G + 127) / 128;
+  int64_t splits = 1;
+  if (!p.wide && blocks < 256) splits = std::min<int64_t>((511 + blocks) / blocks, tiles / 2);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
+  return p;
+}
+
+struct Sizes {
+  Plan q, kv;
+  size_t rows, dq, dk;  // bytes of the parts of the workspace; dv's are dk's
+};
+
+Sizes sizes_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, int32_t G, bool rq, bool rk) {
+  Sizes s;
+  const int64_t group = Hq / Hk;
+  s.q = plan_of(Tq * group, Tk, Hk, G, rq);
+  s.kv = plan_of(Tk, Tq * group, Hk, G, rk);
+  s.rows = up256((size_t)Tq * Hq * 8);
+  s.dq = s.q.splits > 1 ? up256((size_t)s.q.splits * Tq * Hq * D * 4) : 0;
+  s.dk = s.kv.splits > 1 ? up256((size_t)s.kv.splits * Tk * Hk * D * 4) : 0;
+  return s;
+}
+
+template <typename XT, int DT, int WM, int WK, int KT>
+int32_t launch_dq(const AttnArgs& a, hipStream_t st) {
+  using B = BackQ<XT, DT, WM, WK, KT>;
+  const int64_t blocks = (int64_t)a.slots * a.splits * a.Hk;
+  ASP_TRY(check_attn_grid(blocks, B::THREADS));
+  k_attn_dq<XT, DT, WM, WK, KT><<<dim3((unsigned)blocks), B::THREADS, 0, st>>>(a);
+  return launch_status("attention dq");
+}
+
+template <typename XT, int DT, int WN, int WQ, int QT>
+int32_t launch_dkv(const AttnArgs& a, hipStream_t st) {
+  using B = BackKV<XT, DT, WN, WQ, QT>;
+  const int64_t blocks = (int64_t)a.slots * a.splits * a.Hk;
+  ASP_TRY(check_attn_grid(blocks, B::THREADS));
+  k_attn_dkv<XT, DT, WN, WQ, QT><<<dim3((unsigned)blocks), B::THREADS, 0, st>>>(a);
+  return launch_status("attention dk, dv");
+}
+
+template <typename XT>
+int32_t launch_sum(const SumArgs& s, int tensors, hipStream_t st) {
+  const int64_t blocks = (s.T * s.H + 15) / 16;
+  ASP_TRY(check_attn_grid(blocks * tensors, 256));
+  k_attn_sum<XT><<<dim3((unsigned)blocks, tensors), 256, 0, st>>>(s);
+  return launch_status("attention sums");
+}
+
+template <typename XT, int DT>
+int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
+  // rows of 512 bytes: half the tile, and two columns of waves, for LDS's sake
+  constexpr bool LONG = sizeof(XT) == 4 && DT == 4;
+  constexpr int COLUMNS = LONG ? 2 : 4, DEEP = LONG ? 1 : 2;
+  if (a.Tq > 0 && a.dq) {
+    a.slots = z.q.slots;
+    a.splits = z.q.splits;
+    ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, COLUMNS, 1>(a, st)));
+    if (a.splits > 1) {
+      SumArgs s = {};
+      s.part[0] = a.part_dq; s.out[0] = a.dq; s.st[0] = a.dqt; s.sh[0] = a.dqh;
+      s.offsets = a.qo; s.T = a.Tq; s.H = a.Hq; s.D = a.D; s.G = a.G; s.splits = a.splits;
+      ASP_TRY(launch_sum<XT>(s, 1, st));
+    }
+  } else if (a.Tq > 0 && a.Tk > 0) {
+    const int64_t blocks = (a.Tq * a.Hq + 127) / 128;
+    ASP_TRY(check_attn_grid(blocks, 256));
+    k_attn_rows<XT><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+    ASP_TRY(launch_status("attention rows"));
+  }
+  if (a.Tk == 0 || (!a.dk && !a.dv)) return ASP_OK;
+  a.slots = z.kv.slots;
+  a.splits = z.kv.splits;
+  ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, COLUMNS, 1>(a, st)));
+  if (a.splits == 1) return ASP_OK;
+  SumArgs s = {};
+  s.part[0] = a.part_dk; s.out[0] = a.dk; s.st[0] = a.dkt; s.sh[0] = a.dkh;
+  s.part[1] = a.part_dv; s.out[1] = a.dv; s.st[1] = a.dvt; s.sh[1] = a.dvh;
+  s.offsets = a.ko; s.T = a.Tk; s.H = a.Hk; s.D = a.D; s.G = a.G; s.splits = a.splits;
+  return launch_sum<XT>(s, 2, st);
+}
+
+}  // namespace
+}  // namespace asp
+
+using namespace asp;
+
+extern "C" {
+
+int32_t asp_attention_backward_workspace_bytes(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk,
+                                               int32_t D, int32_t G, size_t* bytes) {
+  clear_error();
+  const int32_t some = 0;
+  ASP_TRY(check_attn(ASP_F32, Tq, Tk, Hq, Hk, D, G, 1.0f, &some, &some, nullptr));
+  if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
+  const Sizes z = sizes_of(Tq, Tk, Hq, Hk, D, G, true, true);
+  *bytes = z.rows + z.dq + 2 * z.dk;
+  return ASP_OK;
+}
+
+int32_t asp_attention_backward(const void* dout, int64_t lddo, int64_t hsdo, const void* q,
+                               int64_t ldq, int64_t hsq, const void* k, int64_t ldk, int64_t hsk,
+                               const void* v, int64_t ldv, int64_t hsv, const void* o, int64_t ldo,
+                               int64_t hso, const float* lse, int32_t dtype, int64_t Tq, int64_t Tk,
+                               int32_t Hq, int32_t Hk, int32_t D, float scale, int32_t G,
+                               const int32_t* q_offsets, const int32_t* kv_offsets,
+                               const int32_t* kv_lengths, const uint8_t* key_mask, void* dq,
+                               int64_t lddq, int64_t hsdq, void* dk, int64_t lddk, int64_t hsdk,
+                               void* dv, int64_t lddv, int64_t hsdv, int32_t zero, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  clear_error();
+  ASP_TRY(check_attn(dtype, Tq, Tk, Hq, Hk, D, G, scale, q_offsets, kv_offsets, kv_lengths));
+  if (zero < 0 || zero > 7 || (Tq > 0 && zero & 1 && !dq) ||
+      (Tk > 0 && ((zero & 2 && !dk) || (zero & 4 && !dv))))
+    return fail(ASP_ERR_ARG, "zero=%d", zero);
+  if (!dq && !dk && !dv) return ASP_OK;
+  if (Tq > 0) {
+    ASP_TRY(check_attn_rows(dout, dtype, Tq, Hq, D, lddo, hsdo, false, "do"));
+    ASP_TRY(check_attn_rows(q, dtype, Tq, Hq, D, ldq, hsq, false, "q"));
+    ASP_TRY(check_attn_rows(o, dtype, Tq, Hq, D, ldo, hso, false, "o"));
+    if (!lse) return fail(ASP_ERR_ARG, "lse is NULL");
+    if ((uintptr_t)lse & 3) return fail(ASP_ERR_ALIGN, "lse is not 4-byte aligned");
+    if (dq) ASP_TRY(check_attn_rows(dq, dtype, Tq, Hq, D, lddq, hsdq, true, "dq"));
+  }
+  if (Tk > 0) {
+    ASP_TRY(check_attn_rows(k, dtype, Tk, Hk, D, ldk, hsk, false, "k"));
+    ASP_TRY(check_attn_rows(v, dtype, Tk, Hk, D, ldv, hsv, false, "v"));
+    if (dk) ASP_TRY(check_attn_rows(dk, dtype, Tk, Hk, D, lddk, hsdk, true, "dk"));
+    if (dv) ASP_TRY(check_attn_rows(dv, dtype, Tk, Hk, D, lddv, hsdv, true, "dv"));
+  }
+  const Sizes z = sizes_of(Tq, Tk, Hq, Hk, D, G, q_offsets != nullptr, kv_offsets != nullptr);
+  const size_t need = z.rows + z.dq + 2 * z.dk;
+  if (need) ASP_TRY(check_ptr(workspace, "workspace", true));
+  if (workspace_bytes < need)
+    return fail(ASP_ERR_WORKSPACE, "the workspace holds %zu bytes, the call needs %zu",
+                workspace_bytes, need);
+  AttnArgs a = {};
+  a.q = q; a.k = k; a.v = v; a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse);
+  a.qt = ldq; a.qh = hsq; a.kt = ldk; a.kh = hsk; a.vt = ldv; a.vh = hsv; a.ot = ldo; a.oh = hso;
+  a.qo = q_offsets; a.ko = kv_offsets; a.kl = kv_lengths; a.mask = key_mask;
+  a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hk = Hk; a.group = Hq / Hk; a.D = D; a.G = G;
+  a.zero = zero; a.scale = scale;
+  a.dout = dout; a.gt = lddo; a.gh = hsdo;
+  a.dq = dq; a.dqt = lddq; a.dqh = hsdq; a.dk = dk; a.dkt = lddk; a.dkh = hsdk;
+  a.dv = dv; a.dvt = lddv; a.dvh = hsdv;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.rows = reinterpret_cast<float2*>(w);
+  a.part_dq = reinterpret_cast<float*>(w + z.rows);
+  a.part_dk = reinterpret_cast<float*>(w + z.rows + z.dq);
+  a.part_dv = reinterpret_cast<float*>(w + z.rows + z.dq + z.dk);
+  const hipStream_t st = (hipStream_t)stream;
+  if (dtype == ASP_BF16)
+    return D <= 64 ? run_back<uint16_t, 2>(a, z, st) : run_back<uint16_t, 4>(a, z, st);
+  return D <= 64 ? run_back<float, 2>(a, z, st) : run_back<float, 4>(a, z, st);
+}
+
+}  // extern "C"

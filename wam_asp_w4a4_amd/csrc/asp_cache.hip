@@ -1,0 +1,188 @@
+// A cache of keys and values in NVFP4 blocks of 16 along a head: storing new tokens' rows,
+// and reading rows back.  Both are bound by memory: a lane has one block, 16 elements in
+// and 8 bytes of codes and one scale byte out, so that neighbouring lanes write whole
+// cache lines of a token's heads.  Keys and values go in one launch.
+#include "asp_attn.h"
+
+namespace asp {
+namespace {
+
+constexpr uint32_t kNanScale = 0x7F;  // of a block with a NaN or an infinity
+
+struct StoreArgs {
+  const void* x[2];
+  int64_t xt[2], xh[2];
+  uint8_t *codes[2], *scales[2];
+  const int32_t *offsets, *ko, *kl;
+  int64_t T, rows;
+  int H, per, G;  // per: blocks of a head
+};
+
+template <typename XT>
+__global__ void __launch_bounds__(256) k_kv_store(const StoreArgs a) {
+  const int64_t each = a.T * a.H * a.per;
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int which = i >= each;
+  if (which) i -= each;
+  if (i >= each) return;
+  const int64_t head_of = i / a.per, t = head_of / a.H;
+  const int blk = (int)(i - head_of * a.per), h = (int)(head_of - t * a.H);
+  // the token's sequence: the last that begins at or before it
+  int g = 0;
+  int64_t t0 = 0;
+  if (a.offsets) {
+    if (t < a.offsets[0] || t >= a.offsets[a.G]) return;
+    int lo = 0, hi = a.G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.offsets[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    g = lo;
+    t0 = a.offsets[g];
+  }
+  const int64_t k0 = a.ko ? attn_offset(a.ko, g, a.rows) : 0;
+  const int64_t k1 = a.ko ? attn_offset(a.ko, g + 1, a.rows) : a.rows;
+  const int64_t row = k0 + (a.kl ? max((int64_t)a.kl[g], (int64_t)0) : 0) + (t - t0);
+  if (row < k0 || row >= k1) return;  // no room in the sequence's rows
+
+  float v[16];
+  const XT* x = static_cast<const XT*>(a.x[which]) + t * a.xt[which] + h * a.xh[which] + 16 * blk;
+  uint32_t bad = 0;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    float u[8];
+    load8(x + 8 * p, 0, 8, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[8 * p + e] = u[e];
+      bad |= !(__builtin_fabsf(u[e]) < __builtin_inff());
+    }
+  }
+  uint32_t scale;
+  uint2 w = quantize_block(v, scale);
+  if (bad) {
+    w = make_uint2(0, 0);
+    scale = kNanScale;
+  }
+  const int64_t at = (row * a.H + h) * a.per + blk;
+  *reinterpret_cast<uint2*>(a.codes[which] + 8 * at) = w;
+  a.scales[which][at] = (uint8_t)scale;
+}
+
+struct LoadArgs {
+  const uint8_t *codes[2], *scales[2];
+  void* out[2];
+  int64_t blocks;
+};
+
+template <typename XT>
+__global__ void __launch_bounds__(256) k_kv_load(const LoadArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int which = blockIdx.y;
+  if (i >= a.blocks || !a.out[which]) return;
+  const u32x2_t w = *reinterpret_cast<const u32x2_t*>(a.codes[which] + 8 * i);
+  const float s = __builtin_amdgcn_cvt_f32_fp8((int)a.scales[which][i], 0);
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = e2m1_decode(w[e >> 3] >> (4 * (e & 7)) & 15u) * s;
+  XT* o = static_cast<XT*>(a.out[which]) + 16 * i;
+  if constexpr (sizeof(XT) == 2) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      reinterpret_cast<u32x4_t*>(o)[p] =
+          u32x4_t{bf16x2_rne(v[8 * p], v[8 * p + 1]), bf16x2_rne(v[8 * p + 2], v[8 * p + 3]),
+                  bf16x2_rne(v[8 * p + 4], v[8 * p + 5]), bf16x2_rne(v[8 * p + 6], v[8 * p + 7])};
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      reinterpret_cast<f32x4_t*>(o)[p] = f32x4_t{v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]};
+  }
+}
+
+int32_t check_cache(int64_t rows, int32_t Hk, int32_t D) {
+  if (rows < 0 || rows > INT32_MAX)
+    return fail(ASP_ERR_SHAPE, "rows=%lld outside [0, 2^31)", (long long)rows);
+  if (Hk < 1 || Hk > 65535) return fail(ASP_ERR_SHAPE, "Hk=%d outside [1, 65535]", Hk);
+  if (D < 16 || D > kMaxAttnD || D % 16)
+    return fail(ASP_ERR_SHAPE, "D=%d is not a multiple of 16 in [16, %d]", D, kMaxAttnD);
+  return ASP_OK;
+}
+
+}  // namespace
+}  // namespace asp
+
+using namespace asp;
+
+extern "C" {
+
+int32_t asp_kv_store(const void* k, int64_t ldk, int64_t hsk, const void* v, int64_t ldv,
+                     int64_t hsv, int32_t dtype, int64_t T, int32_t Hk, int32_t D, int32_t G,
+                     const int32_t* offsets, const int32_t* kv_offsets, const int32_t* kv_lengths,
+                     int64_t rows, uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                     uint8_t* v_scales, void* stream) {
+  clear_error();
+  ASP_TRY(check_io_dtype(dtype, "dtype"));
+  ASP_TRY(check_cache(rows, Hk, D));
+  if (T < 0 || T > INT32_MAX) return fail(ASP_ERR_SHAPE, "T=%lld outside [0, 2^31)", (long long)T);
+  if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
+  if ((!offsets || !kv_offsets) && G != 1)
+    return fail(ASP_ERR_ARG, "offsets are NULL with G=%d sequences", G);
+  if ((uintptr_t)offsets & 3 || (uintptr_t)kv_offsets & 3 || (uintptr_t)kv_lengths & 3)
+    return fail(ASP_ERR_ALIGN, "offsets or lengths are not 4-byte aligned");
+  if (T == 0 || rows == 0) return ASP_OK;
+  const struct { const void* p; int64_t st, sh; const char* name; } in[] = {{k, ldk, hsk, "k"}, {v, ldv, hsv, "v"}};
+  for (const auto& i : in) {
+    if (!i.p) return fail(ASP_ERR_ARG, "%s is NULL", i.name);
+    if ((uintptr_t)i.p % (dtype == ASP_BF16 ? 2 : 4))
+      return fail(ASP_ERR_ALIGN, "%s is not aligned to its elements", i.name);
+    if (i.st < 0 || i.sh < 0 || i.st > INT32_MAX || i.sh > ((int64_t)1 << 40))
+      return fail(ASP_ERR_SHAPE, "strides %lld, %lld of %s", (long long)i.st, (long long)i.sh, i.name);
+  }
+  ASP_TRY(check_ptr(k_codes, "k_codes", true));
+  ASP_TRY(check_ptr(k_scales, "k_scales", true));
+  ASP_TRY(check_ptr(v_codes, "v_codes", true));
+  ASP_TRY(check_ptr(v_scales, "v_scales", true));
+  StoreArgs a = {};
+  a.x[0] = k; a.xt[0] = ldk; a.xh[0] = hsk; a.codes[0] = k_codes; a.scales[0] = k_scales;
+  a.x[1] = v; a.xt[1] = ldv; a.xh[1] = hsv; a.codes[1] = v_codes; a.scales[1] = v_scales;
+  a.offsets = offsets; a.ko = kv_offsets; a.kl = kv_lengths;
+  a.T = T; a.rows = rows; a.H = Hk; a.per = D / 16; a.G = G;
+  const int64_t blocks = (2 * T * Hk * a.per + 255) / 256;
+  ASP_TRY(check_attn_grid(blocks, 256));
+  const hipStream_t st = (hipStream_t)stream;
+  if (dtype == ASP_BF16) k_kv_store<uint16_t><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  else k_kv_store<float><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  return launch_status("cache store");
+}
+
+int32_t asp_kv_load(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                    const uint8_t* v_scales, int64_t rows, int32_t Hk, int32_t D, void* k, void* v,
+                    int32_t dtype, void* stream) {
+  clear_error();
+  ASP_TRY(check_io_dtype(dtype, "dtype"));
+  ASP_TRY(check_cache(rows, Hk, D));
+  if (rows == 0 || (!k && !v)) return ASP_OK;
+  LoadArgs a = {};
+  a.blocks = rows * Hk * (D / 16);
+  if (k) {
+    ASP_TRY(check_ptr(k, "k", true));
+    ASP_TRY(check_ptr(k_codes, "k_codes", true));
+    ASP_TRY(check_ptr(k_scales, "k_scales", true));
+  }
+  if (v) {
+    ASP_TRY(check_ptr(v, "v", true));
+    ASP_TRY(check_ptr(v_codes, "v_codes", true));
+    ASP_TRY(check_ptr(v_scales, "v_scales", true));
+  }
+  a.codes[0] = k_codes; a.scales[0] = k_scales; a.out[0] = k;
+  a.codes[1] = v_codes; a.scales[1] = v_scales; a.out[1] = v;
+  const int64_t blocks = (a.blocks + 255) / 256;
+  ASP_TRY(check_attn_grid(2 * blocks, 256));
+  const hipStream_t st = (hipStream_t)stream;
+  if (dtype == ASP_BF16) k_kv_load<uint16_t><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(a);
+  else k_kv_load<float><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(a);
+  return launch_status("cache load");
+}
+
+}  // extern "C"

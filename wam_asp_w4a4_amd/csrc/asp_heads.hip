@@ -1,0 +1,622 @@
+// Norms of each head of the queries and keys with the position rotation, forward and
+// backward.  A head's D elements v of token t become
+//
+//   u = norm(v) w                      none, RMS or layer norm over the D elements
+//   y = u turned by the angles of the token's position, pair by pair:
+//       (a, b) -> (a c - b s, a s + b c),  c, s = cosine, sine[position][pair]
+//
+// for the pairs of the first `rot` elements; the others stay u.  Backward: a rotation's
+// transpose is the rotation by the negative angle, so with g the turned-back dy and
+// x^ = norm(v), r its inverse deviation:
+//
+//   dw = sum over tokens and heads of g x^,   dv = r (g w - x^ mean(g w x^) [- mean(g w)])
+//
+// Both directions are bound by memory: every value is read once and written once, and
+// a token's row of the tables serves all of its heads from registers.  L lanes hold one
+// head, 8 elements (4 pairs) each; S groups of L lanes share a token and take its heads
+// in turn, with the next head's loads in flight.  A launch has the blocks of the
+// queries, then those of the keys.
+#include "asp_fp8.h"
+
+namespace asp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeadD = 256;
+constexpr int kMaxGradBlocks = 1024;  // of each of the two tensors: rows of partial sums of dw
+
+// one of the two tensors; strides in elements
+struct Side {
+  const void *x, *dy;
+  void* y;  // backward: dv
+  const float* w;
+  float *dw, *part;
+  int64_t xt, xh, yt, yh, gt, gh;  // token and head strides of x, y and dy
+  int H, S, shift, blocks;  // S groups share a token (a power of two, 2^shift)
+};
+
+struct HeadArgs {
+  Side side[2];
+  const float *cosine, *sine;
+  const int32_t* positions;
+  int64_t P;
+  float eps;
+  int T, D, rot, norm, zero;
+};
+
+// the sum over the L lanes of a group, in every lane of it
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  auto add = [](float a, auto ctrl) {
+    return a + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                             0, __builtin_bit_cast(int, a), decltype(ctrl)::value,
+                                             0xf, 0xf, false));
+  };
+  if constexpr (L > 1) v = add(v, std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  if constexpr (L > 2) v = add(v, std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  if constexpr (L > 4) v = add(v, std::integral_constant<int, 0x141>{});  // the other four of 8
+  if constexpr (L > 8) v = add(v, std::integral_constant<int, 0x140>{});  // the other eight of 16
+  if constexpr (L > 16) v += __shfl_xor(v, 16);
+  return v;
+}
+
+// Where a lane's 8 elements lie in a head.  HALVES: pair p < rot / 2 is (p, p + rot / 2), and
+// elements past rot make pairs of neighbours (never turned); else pair p is (2p, 2p + 1).
+// Element j of a lane belongs to its pair pair_of(j).  VEC: D and rot are multiples of 8, so
+// that the eight are one or two runs inside the head.
+template <bool HALVES, bool VEC>
+struct Lane {
+  int at[VEC ? (HALVES ? 2 : 1) : 8];  // first elements of the runs; -1: none
+  static constexpr int RUNS = VEC ? (HALVES ? 2 : 1) : 8, RUN = 8 / RUNS;
+  __device__ __forceinline__ Lane(int l, int D, int rot) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = 4 * l + (HALVES ? j & 3 : j >> 1);
+        int e = HALVES ? 2 * p + (j >> 2) : 8 * l + j;
+        if (HALVES && p < rot / 2) e = j < 4 ? p : p + rot / 2;
+        at[j] = p < D / 2 ? e : -1;
+      }
+    } else if constexpr (HALVES) {
+      const bool turned = 8 * l < rot;
+      at[0] = 8 * l >= D ? -1 : turned ? 4 * l : 8 * l;
+      at[1] = 8 * l >= D ? -1 : turned ? 4 * l + rot / 2 : 8 * l + 4;
+    } else {
+      at[0] = 8 * l < D ? 8 * l : -1;
+    }
+  }
+  static __device__ __forceinline__ constexpr int first(int pair) { return HALVES ? pair : 2 * pair; }
+  static __device__ __forceinline__ constexpr int second(int pair) {
+    return HALVES ? pair + 4 : 2 * pair + 1;
+  }
+};
+
+typedef uint32_t u32x2_e2 __attribute__((ext_vector_type(2), aligned(2)));
+
+// a lane's elements as they lie in memory: bf16 two a dword where a run has two
+template <typename XT, bool HALVES, bool VEC>
+struct Eight {
+  using Where = Lane<HALVES, VEC>;
+  static constexpr int WORDS = sizeof(XT) == 2 && VEC ? 4 : 8;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void load(const void* base, int64_t row, const Where& where) {
+    const XT* p = static_cast<const XT*>(base) + row;
+#pragma unroll
+    for (int r = 0; r < Where::RUNS; ++r) {
+      if (where.at[r] < 0) continue;
+      const XT* q = p + where.at[r];
+      if constexpr (!VEC) {
+        if constexpr (sizeof(XT) == 2) w[r] = *q;
+        else w[r] = __builtin_bit_cast(uint32_t, *q);
+      } else if constexpr (sizeof(XT) == 2 && HALVES) {
+        const u32x2_t v = *reinterpret_cast<const u32x2_e2*>(q);
+        w[2 * r] = v[0];
+        w[2 * r + 1] = v[1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < (sizeof(XT) == 2 ? 1 : Where::RUN / 4); ++i) {
+          u32x4_t v;
+          if constexpr (sizeof(XT) == 2) v = *reinterpret_cast<const u32x4_e2*>(q + 8 * i);
+          else v = *reinterpret_cast<const u32x4_e4*>(q + 4 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[(Where::RUN / 4 * r + i) * 4 + k] = v[k];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (sizeof(XT) == 4) v[j] = __builtin_bit_cast(float, w[j]);
+      else if constexpr (VEC) v[j] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+      else v[j] = bf16_lo(w[j]);
+    }
+  }
+};
+
+template <typename YT, bool HALVES, bool VEC>
+__device__ __forceinline__ void store_eight(void* base, int64_t row, const Lane<HALVES, VEC>& where,
+                                            const float (&v)[8]) {
+  using Where = Lane<HALVES, VEC>;
+  YT* p = static_cast<YT*>(base) + row;
+#pragma unroll
+  for (int r = 0; r < Where::RUNS; ++r) {
+    if (where.at[r] < 0) continue;
+    YT* q = p + where.at[r];
+    if constexpr (!VEC) {
+      if constexpr (sizeof(YT) == 2) *q = bf16_rne(v[r]);
+      else *q = v[r];
+    } else if constexpr (sizeof(YT) == 2 && HALVES) {
+      *reinterpret_cast<u32x2_e2*>(q) =
+          u32x2_t{bf16x2_rne(v[4 * r], v[4 * r + 1]), bf16x2_rne(v[4 * r + 2], v[4 * r + 3])};
+    } else if constexpr (sizeof(YT) == 2) {
+      *reinterpret_cast<u32x4_e2*>(q) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                                bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+    } else {
+      auto bits = [&](int k) { return __builtin_bit_cast(uint32_t, v[k]); };
+#pragma unroll
+      for (int i = 0; i < Where::RUN / 4; ++i) {
+        const int k = Where::RUN * r + 4 * i;
+        *reinterpret_cast<u32x4_e4*>(q + 4 * i) =
+            u32x4_t{bits(k), bits(k + 1), bits(k + 2), bits(k + 3)};
+      }
+    }
+  }
+}
+
+// A token's cosines and sines for a lane's pairs (1 and 0 past `rot`); false: the token's
+// position is outside the tables, it counts for nothing.
+template <bool VEC>
+__device__ __forceinline__ bool angles(const HeadArgs& a, int64_t token, int l, float (&c)[4],
+                                       float (&s)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = 1.0f;
+    s[i] = 0.0f;
+  }
+  if (!a.rot) return true;
+  const int64_t pos = a.positions ? a.positions[token] : token;
+  if (pos < 0 || pos >= a.P) return false;
+  const int half = a.rot / 2;
+  const float *pc = a.cosine + pos * half + 4 * l, *ps = a.sine + pos * half + 4 * l;
+  if constexpr (VEC) {
+    if (8 * l < a.rot) {
+      const u32x4_t u = *reinterpret_cast<const u32x4_e4*>(pc), w = *reinterpret_cast<const u32x4_e4*>(ps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = __builtin_bit_cast(float, (uint32_t)u[i]);
+        s[i] = __builtin_bit_cast(float, (uint32_t)w[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * l + i < half) {
+        c[i] = pc[i];
+        s[i] = ps[i];
+      }
+  }
+  return true;
+}
+
+// v -> the normed head; r: its inverse deviation.  The root and the division are IEEE ones.
+template <int L, typename Where>
+__device__ __forceinline__ float head_normed(float (&v)[8], int norm, float rd, float eps,
+                                             const Where& where) {
+  if (norm == ASP_NORM_NONE) return 1.0f;
+  if (norm == ASP_NORM_LAYER) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j];
+    const float mean = group_sum<L>(sum) * rd;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = where.at[j / Where::RUN] < 0 ? 0.0f : v[j] - mean;
+  }
+  float sq = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
+  const float r = 1.0f / sqrtf(group_sum<L>(sq) * rd + eps);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= r;
+  return r;
+}
+
+template <typename Where>
+__device__ __forceinline__ void head_weights(const float* p, const Where& where, float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int at = where.at[j / Where::RUN];
+    w[j] = p && at >= 0 ? p[at + j % Where::RUN] : 1.0f;
+  }
+}
+
+template <typename XT, typename YT, int L, bool HALVES, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_head_norm(const HeadArgs a) {
+  using Where = Lane<HALVES, VEC>;
+  const bool second = (int)blockIdx.x >= a.side[0].blocks;
+  const Side& s = a.side[second];
+  const int block = blockIdx.x - (second ? a.side[0].blocks : 0);
+  const int l = threadIdx.x % L, group = threadIdx.x / L;
+  const int64_t token = (int64_t)block * ((kThreads / L) >> s.shift) + (group >> s.shift);
+  if (token >= a.T) return;
+  const Where where(l, a.D, a.rot);
+  int h = group & (s.S - 1);
+  if (h >= s.H) return;
+  Eight<XT, HALVES, VEC> next;
+  next.clear();
+  next.load(s.x, token * s.xt + h * s.xh, where);
+  float c[4], n[4], w[8];
+  const bool live = angles<VEC>(a, token, l, c, n);
+  if (!live) {
+    const float none[8] = {};
+    if (a.zero & (second ? 2 : 1))
+      for (; h < s.H; h += s.S) store_eight<YT>(s.y, token * s.yt + h * s.yh, where, none);
+    return;
+  }
+  head_weights(s.w, where, w);
+  const float rd = 1.0f / (float)a.D;
+  for (; h < s.H; h += s.S) {
+    float v[8], y[8];
+    next.get(v);
+    if (h + s.S < s.H) next.load(s.x, token * s.xt + (h + s.S) * s.xh, where);
+    head_normed<L>(v, a.norm, rd, a.eps, where);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = Where::first(i), f = Where::second(i);
+      const float p = v[e] * w[e], q = v[f] * w[f];
+      y[e] = __builtin_fmaf(p, c[i], -(q * n[i]));
+      y[f] = __builtin_fmaf(p, n[i], q * c[i]);
+    }
+    store_eight<YT>(s.y, token * s.yt + h * s.yh, where, y);
+  }
+}
+
+// The weights' gradients are summed over the block's tokens in registers, over its groups in
+// LDS, and over the blocks by k_head_sums, each in a fixed order.
+template <typename XT, typename GT, int L, bool HALVES, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_head_norm_back(const HeadArgs a) {
+  using Where = Lane<HALVES, VEC>;
+  __shared__ float sums[kThreads * 8];
+  const bool second = (int)blockIdx.x >= a.side[0].blocks;
+  const Side& s = a.side[second];
+  const int block = blockIdx.x - (second ? a.side[0].blocks : 0);
+  const int l = threadIdx.x % L, group = threadIdx.x / L;
+  const Where where(l, a.D, a.rot);
+  const float rd = 1.0f / (float)a.D;
+  float w[8], dw[8] = {};
+  head_weights(s.w, where, w);
+  const int tokens = (kThreads / L) >> s.shift;  // of a block at a time
+  for (int64_t token = (int64_t)block * tokens + (group >> s.shift); token < a.T;
+       token += (int64_t)s.blocks * tokens) {
+    int h = group & (s.S - 1);
+    if (h >= s.H) break;
+    Eight<XT, HALVES, VEC> nx;
+    Eight<GT, HALVES, VEC> ng;
+    nx.clear();
+    ng.clear();
+    auto fetch = [&](int head) {
+      nx.load(s.x, token * s.xt + head * s.xh, where);
+      ng.load(s.dy, token * s.gt + head * s.gh, where);
+    };
+    fetch(h);
+    float c[4], n[4];
+    if (!angles<VEC>(a, token, l, c, n)) {
+      const float none[8] = {};
+      if (s.y && a.zero & (second ? 2 : 1))
+        for (; h < s.H; h += s.S) store_eight<XT>(s.y, token * s.yt + h * s.yh, where, none);
+      continue;
+    }
+    for (; h < s.H; h += s.S) {
+      float v[8], d[8], g[8];
+      nx.get(v);
+      ng.get(d);
+      if (h + s.S < s.H) fetch(h + s.S);
+      const float r = head_normed<L>(v, a.norm, rd, a.eps, where);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = Where::first(i), f = Where::second(i);
+        g[e] = __builtin_fmaf(d[e], c[i], d[f] * n[i]);
+        g[f] = __builtin_fmaf(d[f], c[i], -(d[e] * n[i]));
+      }
+      float m[2] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[j] = __builtin_fmaf(g[j], v[j], dw[j]);
+        g[j] *= w[j];
+        m[0] = __builtin_fmaf(g[j], v[j], m[0]);
+        m[1] += g[j];
+      }
+      if (!s.y) continue;
+      if (a.norm != ASP_NORM_NONE) {
+        m[0] = group_sum<L>(m[0]) * rd;
+        m[1] = a.norm == ASP_NORM_LAYER ? group_sum<L>(m[1]) * rd : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = r * (__builtin_fmaf(-v[j], m[0], g[j]) - m[1]);
+      }
+      store_eight<XT>(s.y, token * s.yt + h * s.yh, where, g);
+    }
+  }
+  if (!s.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[(group * L + l) * 8 + j] = dw[j];
+  __syncthreads();
+  // element i of a lane's eight: L * 8 sums over the groups
+  for (int i = threadIdx.x; i < L * 8; i += kThreads) {
+    float sum = 0.0f;
+    for (int g = 0; g < kThreads / L; ++g) sum += sums[g * L * 8 + i];
+    const Where mine(i / 8, a.D, a.rot);
+    const int at = mine.at[(i & 7) / Where::RUN];
+    if (at >= 0) s.part[(int64_t)block * a.D + at + (i & 7) % Where::RUN] = sum;
+  }
+}
+
+// dw = the sum of the blocks' rows: 16 columns a block, 64 threads a column
+__global__ void __launch_bounds__(1024) k_head_sums(const HeadArgs a) {
+  __shared__ float sums[64][17];
+  const Side& s = a.side[blockIdx.y];
+  if (!s.dw) return;
+  const int col = blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
+  float sum = 0.0f;
+  if (col < a.D)
+    for (int b = row; b < s.blocks; b += 64) sum += s.part[(int64_t)b * a.D + col];
+  sums[row][threadIdx.x & 15] = sum;
+  __syncthreads();
+  if (row || col >= a.D) return;
+  for (int r = 1; r < 64; ++r) sum += sums[r][threadIdx.x & 15];
+  s.dw[col] = sum;
+}
+
+// -------------------------------------------------------------------- host
+
+int lanes_of(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+
+// The groups that share a token, and the blocks of a tensor.  One token's heads are spread
+// over as many groups as there are while that does not fill the card; with many tokens a
+// group takes several heads, for which it reads the tables once.
+void spread(Side& s, int64_t T, int D, bool backward) {
+  const int groups = kThreads / lanes_of(D);
+  s.S = 1;
+  s.shift = 0;
+  if (s.H <= 0 || T <= 0) {
+    s.H = 0;
+    s.blocks = 0;
+    return;
+  }
+  // waves of 64 lanes while each group takes one head; 4096 of them fill the card twice over
+  while (s.S < groups && s.S < s.H && (s.S * T * lanes_of(D) / 64 < 4096 || s.H > 8 * s.S)) {
+    s.S *= 2;
+    ++s.shift;
+  }
+  const int64_t tokens = groups >> s.shift;
+  int64_t blocks = (T + tokens - 1) / tokens;
+  if (backward && blocks > kMaxGradBlocks) blocks = kMaxGradBlocks;
+  s.blocks = (int)blocks;
+}
+
+int32_t check_heads(int32_t dtype, int64_t T, int32_t D, int32_t Hq, int32_t Hk, int32_t norm,
+                    float eps, const float* cosine, const float* sine, int64_t P, int32_t rot,
+                    int32_t layout, const int32_t* positions) {
+  ASP_TRY(check_io_dtype(dtype, "dtype"));
+  if (T < 0 || T > INT32_MAX) return fail(ASP_ERR_SHAPE, "T=%lld outside [0, 2^31)", (long long)T);
+  if (D < 2 || D > kMaxHeadD || D % 2)
+    return fail(ASP_ERR_SHAPE, "D=%d is not an even number in [2, %d]", D, kMaxHeadD);
+  if (Hq < 1 || Hq > 65535) return fail(ASP_ERR_SHAPE, "Hq=%d outside [1, 65535]", Hq);
+  if (Hk < 0 || Hk > 65535) return fail(ASP_ERR_SHAPE, "Hk=%d outside [0, 65535]", Hk);
+  if (norm < ASP_NORM_NONE || norm > ASP_NORM_LAYER) return fail(ASP_ERR_ARG, "norm=%d", norm);
+  if (!(eps >= 0.0f) || eps > 1.0f) return fail(ASP_ERR_ARG, "eps=%g outside [0, 1]", eps);
+  if (layout != ASP_ROTATE_PAIRS && layout != ASP_ROTATE_HALVES)
+    return fail(ASP_ERR_ARG, "layout=%d", layout);
+  if (rot < 0 || rot > D || rot % 2) return fail(ASP_ERR_SHAPE, "rot=%d of D=%d", rot, D);
+  if (rot == 0) {
+    if (cosine || sine || positions) return fail(ASP_ERR_ARG, "tables or positions with rot=0");
+    return ASP_OK;
+  }
+  if (!cosine || !sine) return fail(ASP_ERR_ARG, "a rotation without its tables");
+  if ((uintptr_t)cosine & 3 || (uintptr_t)sine & 3 || (uintptr_t)positions & 3)
+    return fail(ASP_ERR_ALIGN, "tables or positions are not 4-byte aligned");
+  if (P < (positions ? 1 : T) || P > INT32_MAX)
+    return fail(ASP_ERR_SHAPE, "tables of %lld positions", (long long)P);
+  return ASP_OK;
+}
+
+// strides of (T, H, D) with contiguous heads; of outputs no two heads may overlap
+int32_t check_strides(const void* p, int32_t dtype, int64_t T, int H, int D, int64_t st, int64_t sh,
+                      bool out, const char* name) {
+  if (!p) return fail(ASP_ERR_ARG, "%s is NULL", name);
+  if ((uintptr_t)p % (dtype == ASP_BF16 ? 2 : 4))
+    return fail(ASP_ERR_ALIGN, "%s is not aligned to its elements", name);
+  if (st < 0 || sh < 0 || st > INT32_MAX || sh > ((int64_t)1 << 40))
+    return fail(ASP_ERR_SHAPE, "strides %lld, %lld of %s", (long long)st, (long long)sh, name);
+  if (!out) return ASP_OK;
+  const bool by_token = (H <= 1 || sh >= D) && (T <= 1 || st >= (H - 1) * sh + D);
+  const bool by_head = (T <= 1 || st >= D) && (H <= 1 || sh >= (T - 1) * st + D);
+  if (!by_token && !by_head)
+    return fail(ASP_ERR_SHAPE, "strides %lld, %lld of %s let heads overlap", (long long)st,
+                (long long)sh, name);
+  return ASP_OK;
+}
+
+struct Forward {
+  template <typename XT, typename YT, int L, bool HALVES, bool VEC>
+  static void launch(const HeadArgs& a, dim3 grid, hipStream_t st) {
+    k_head_norm<XT, YT, L, HALVES, VEC><<<grid, kThreads, 0, st>>>(a);
+  }
+};
+struct Backward {
+  template <typename XT, typename YT, int L, bool HALVES, bool VEC>
+  static void launch(const HeadArgs& a, dim3 grid, hipStream_t st) {
+    k_head_norm_back<XT, YT, L, HALVES, VEC><<<grid, kThreads, 0, st>>>(a);
+  }
+};
+
+template <typename K, typename XT, typename YT, int L>
+void launch_layout(const HeadArgs& a, int layout, dim3 grid, hipStream_t st) {
+  const bool vec = a.D % 8 == 0 && a.rot % 8 == 0;
+  if (layout == ASP_ROTATE_HALVES)
+    vec ? K::template launch<XT, YT, L, true, true>(a, grid, st)
+        : K::template launch<XT, YT, L, true, false>(a, grid, st);
+  else
+    vec ? K::template launch<XT, YT, L, false, true>(a, grid, st)
+        : K::template launch<XT, YT, L, false, false>(a, grid, st);
+}
+
+template <typename K, typename XT, typename YT>
+void launch_lanes(const HeadArgs& a, int layout, dim3 grid, hipStream_t st) {
+  switch (lanes_of(a.D)) {
+    case 4: return launch_layout<K, XT, YT, 4>(a, layout, grid, st);
+    case 8: return launch_layout<K, XT, YT, 8>(a, layout, grid, st);
+    case 16: return launch_layout<K, XT, YT, 16>(a, layout, grid, st);
+    default: return launch_layout<K, XT, YT, 32>(a, layout, grid, st);
+  }
+}
+
+template <typename K>
+int32_t launch_heads(const HeadArgs& a, int x_dtype, int y_dtype, int layout, hipStream_t st) {
+  const int64_t blocks = (int64_t)a.side[0].blocks + a.side[1].blocks;
+  if (blocks * kThreads > kMaxLanes)
+    return fail(ASP_ERR_SHAPE, "T=%d needs more than one launch", a.T);
+  const dim3 grid((unsigned)blocks);
+  const bool xb = x_dtype == ASP_BF16, yb = y_dtype == ASP_BF16;
+  if (xb) yb ? launch_lanes<K, uint16_t, uint16_t>(a, layout, grid, st)
+             : launch_lanes<K, uint16_t, float>(a, layout, grid, st);
+  else yb ? launch_lanes<K, float, uint16_t>(a, layout, grid, st)
+          : launch_lanes<K, float, float>(a, layout, grid, st);
+  return launch_status("head norm");
+}
+
+HeadArgs head_args(int64_t T, int32_t D, int32_t norm, float eps, const float* cosine,
+                   const float* sine, int64_t P, int32_t rot, const int32_t* positions,
+                   int32_t zero) {
+  HeadArgs a = {};
+  a.cosine = cosine;
+  a.sine = sine;
+  a.positions = positions;
+  a.P = P;
+  a.eps = eps;
+  a.T = (int)T;
+  a.D = D;
+  a.rot = rot;
+  a.norm = norm;
+  a.zero = zero;
+  return a;
+}
+
+}  // namespace
+}  // namespace asp
+
+using namespace asp;
+
+extern "C" {
+
+int32_t asp_head_norm(const void* q, int64_t ldq, int64_t hsq, int32_t Hq, const void* k,
+                      int64_t ldk, int64_t hsk, int32_t Hk, int32_t dtype, int64_t T, int32_t D,
+                      int32_t norm, const float* q_w, const float* k_w, float eps,
+                      const float* cosine, const float* sine, int64_t P, int32_t rot,
+                      int32_t layout, const int32_t* positions, void* q_out, int64_t ldqo,
+                      int64_t hsqo, void* k_out, int64_t ldko, int64_t hsko, int32_t out_dtype,
+                      int32_t zero, void* stream) {
+  clear_error();
+  ASP_TRY(check_heads(dtype, T, D, Hq, Hk, norm, eps, cosine, sine, P, rot, layout, positions));
+  ASP_TRY(check_io_dtype(out_dtype, "out_dtype"));
+  if (norm == ASP_NORM_NONE && (q_w || k_w)) return fail(ASP_ERR_ARG, "weights without a norm");
+  if ((uintptr_t)q_w & 3 || (uintptr_t)k_w & 3)
+    return fail(ASP_ERR_ALIGN, "weights are not 4-byte aligned");
+  if (zero < 0 || zero > 3) return fail(ASP_ERR_ARG, "zero=%d", zero);
+  if (Hk == 0 && (k || k_w || k_out)) return fail(ASP_ERR_ARG, "keys with Hk=0");
+  if (T == 0) return ASP_OK;
+  ASP_TRY(check_strides(q, dtype, T, Hq, D, ldq, hsq, false, "q"));
+  ASP_TRY(check_strides(q_out, out_dtype, T, Hq, D, ldqo, hsqo, true, "q_out"));
+  if (Hk) {
+    ASP_TRY(check_strides(k, dtype, T, Hk, D, ldk, hsk, false, "k"));
+    ASP_TRY(check_strides(k_out, out_dtype, T, Hk, D, ldko, hsko, true, "k_out"));
+  }
+  HeadArgs a = head_args(T, D, norm, eps, cosine, sine, P, rot, positions, zero);
+  a.side[0].x = q; a.side[0].y = q_out; a.side[0].w = q_w; a.side[0].H = Hq;
+  a.side[0].xt = ldq; a.side[0].xh = hsq; a.side[0].yt = ldqo; a.side[0].yh = hsqo;
+  a.side[1].x = k; a.side[1].y = k_out; a.side[1].w = k_w; a.side[1].H = Hk;
+  a.side[1].xt = ldk; a.side[1].xh = hsk; a.side[1].yt = ldko; a.side[1].yh = hsko;
+  for (Side& s : a.side) spread(s, T, D, false);
+  return launch_heads<Forward>(a, dtype, out_dtype, layout, (hipStream_t)stream);
+}
+
+int32_t asp_head_norm_backward_workspace_bytes(int64_t T, int32_t Hq, int32_t Hk, int32_t D,
+                                               size_t* bytes) {
+  clear_error();
+  ASP_TRY(check_heads(ASP_F32, T, D, Hq, Hk, 0, 0.0f, nullptr, nullptr, 0, 0, 0, nullptr));
+  if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
+  Side q = {}, k = {};
+  q.H = Hq;
+  k.H = Hk;
+  spread(q, T, D, true);
+  spread(k, T, D, true);
+  *bytes = up256((size_t)(q.blocks + k.blocks) * D * 4);
+  return ASP_OK;
+}
+
+int32_t asp_head_norm_backward(const void* dq, int64_t lddq, int64_t hsdq, const void* dk,
+                               int64_t lddk, int64_t hsdk, int32_t d_dtype, const void* q,
+                               int64_t ldq, int64_t hsq, int32_t Hq, const void* k, int64_t ldk,
+                               int64_t hsk, int32_t Hk, int32_t dtype, int64_t T, int32_t D,
+                               int32_t norm, const float* q_w, const float* k_w, float eps,
+                               const float* cosine, const float* sine, int64_t P, int32_t rot,
+                               int32_t layout, const int32_t* positions, void* dq_in,
+                               int64_t lddqi, int64_t hsdqi, void* dk_in, int64_t lddki,
+                               int64_t hsdki, int32_t zero, float* d_q_w, float* d_k_w,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  ASP_TRY(check_heads(dtype, T, D, Hq, Hk, norm, eps, cosine, sine, P, rot, layout, positions));
+  ASP_TRY(check_io_dtype(d_dtype, "d_dtype"));
+  if (norm == ASP_NORM_NONE && (q_w || k_w || d_q_w || d_k_w))
+    return fail(ASP_ERR_ARG, "weights without a norm");
+  for (const float* w : {q_w, k_w, (const float*)d_q_w, (const float*)d_k_w})
+    if ((uintptr_t)w & 3) return fail(ASP_ERR_ALIGN, "weights are not 4-byte aligned");
+  if (zero < 0 || zero > 3 || (T > 0 && ((zero & 1 && !dq_in) || (zero & 2 && !dk_in))))
+    return fail(ASP_ERR_ARG, "zero=%d", zero);
+  if (Hk == 0 && (dk || k || k_w || dk_in || d_k_w)) return fail(ASP_ERR_ARG, "keys with Hk=0");
+  HeadArgs a = head_args(T, D, norm, eps, cosine, sine, P, rot, positions, zero);
+  Side &sq = a.side[0], &sk = a.side[1];
+  // a tensor without a wanted gradient is not read
+  sq.H = dq_in || d_q_w ? Hq : 0;
+  sk.H = dk_in || d_k_w ? Hk : 0;
+  if (!sq.H && !sk.H) return ASP_OK;
+  if (T > 0) {
+    if (sq.H) {
+      ASP_TRY(check_strides(q, dtype, T, Hq, D, ldq, hsq, false, "q"));
+      ASP_TRY(check_strides(dq, d_dtype, T, Hq, D, lddq, hsdq, false, "dq"));
+      if (dq_in) ASP_TRY(check_strides(dq_in, dtype, T, Hq, D, lddqi, hsdqi, true, "dq_in"));
+    }
+    if (sk.H) {
+      ASP_TRY(check_strides(k, dtype, T, Hk, D, ldk, hsk, false, "k"));
+      ASP_TRY(check_strides(dk, d_dtype, T, Hk, D, lddk, hsdk, false, "dk"));
+      if (dk_in) ASP_TRY(check_strides(dk_in, dtype, T, Hk, D, lddki, hsdki, true, "dk_in"));
+    }
+  }
+  spread(sq, T, D, true);
+  spread(sk, T, D, true);
+  const bool sums = d_q_w || d_k_w;
+  if (sums) {
+    const size_t need = (size_t)(sq.blocks + sk.blocks) * D * 4;
+    if (need) ASP_TRY(check_ptr(workspace, "workspace", true));
+    if (workspace_bytes < need)
+      return fail(ASP_ERR_WORKSPACE, "the workspace holds %zu bytes, the call needs %zu",
+                  workspace_bytes, need);
+  }
+  sq.x = q; sq.dy = dq; sq.y = dq_in; sq.w = q_w; sq.dw = d_q_w;
+  sq.xt = ldq; sq.xh = hsq; sq.gt = lddq; sq.gh = hsdq; sq.yt = lddqi; sq.yh = hsdqi;
+  sk.x = k; sk.dy = dk; sk.y = dk_in; sk.w = k_w; sk.dw = d_k_w;
+  sk.xt = ldk; sk.xh = hsk; sk.gt = lddk; sk.gh = hsdk; sk.yt = lddki; sk.yh = hsdki;
+  float* part = static_cast<float*>(workspace);
+  sq.part = d_q_w ? part : nullptr;
+  sk.part = d_k_w ? part + (size_t)sq.blocks * D : nullptr;
+  const hipStream_t st = (hipStream_t)stream;
+  if (sq.blocks + sk.blocks) ASP_TRY(launch_heads<Backward>(a, dtype, d_dtype, layout, st));
+  if (!sums) return ASP_OK;
+  k_head_sums<<<dim3((D + 15) / 16, 2), 1024, 0, st>>>(a);
+  return launch_status("head norm sums");
+}
+
+}  // extern "C"
