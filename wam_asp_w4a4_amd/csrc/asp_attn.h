@@ -41,7 +41,9 @@ struct AttnArgs {
   const int32_t *qo, *ko, *kl;             // offsets of the sequences, and how many of a sequence's keys count
   const uint8_t* mask;                     // [Tk]
   int64_t Tq, Tk;
-  int Hq, Hk, group, D, G, splits, slots, zero;
+  int Hq, Hk, group, D, G, slots, zero;
+  int splits;     // workgroups that may share one range of rows that go by,
+  int64_t chunk;  // which is split from so many on
   float scale;
   float* part;    // [splits][Tq][Hq][D]
   float* part_l;  // [splits][Tq][Hq]
@@ -308,11 +310,42 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* of
   return s;
 }
 
-// XCD-aware order: consecutive workgroups go to the 8 XCDs in turn; each takes one contiguous
-// run, so that the tiles of a head, which read the same keys, share an L2.
-__device__ __forceinline__ int64_t attn_run(uint32_t id, uint32_t total) {
-  const uint32_t xcd = id % 8;
-  return (int64_t)xcd * (total / 8) + min(xcd, total % 8) + id / 8;
+// How many workgroups share `passed` rows
+__device__ __forceinline__ int attn_parts(const AttnArgs& a, int64_t passed) {
+  return a.splits == 1 ? 1 : (int)min(max((passed + a.chunk - 1) / a.chunk, (int64_t)1), (int64_t)a.splits);
+}
+
+// The sequence of a token inside the offsets: the last that begins at or before it.  A wave looks at
+// 64 of them at a time.
+__device__ __forceinline__ int attn_owner(const int32_t* offsets, int G, int64_t token) {
+  int g = 0, n = G;
+  while (n > 0) {
+    const int step = (n + 63) / 64, i = (threadIdx.x & 63) * step;
+    const int count = __builtin_popcountll(__ballot(i < n && offsets[g + min(i, n - 1)] <= token));
+    const int at = max(count - 1, 0) * step;
+    g += at;
+    n = step > 1 ? min(step, n - at) : 0;
+  }
+  return __builtin_amdgcn_readfirstlane(g);
+}
+
+// the keys of sequence g that count
+__device__ __forceinline__ int64_t attn_keys(const AttnArgs& a, int g) {
+  const int64_t all = a.ko ? attn_offset(a.ko, g + 1, a.Tk) - attn_offset(a.ko, g, a.Tk) : a.Tk;
+  return max(a.kl ? min(all, (int64_t)a.kl[g]) : all, (int64_t)0);
+}
+
+// XCD-aware order: consecutive workgroups go to the 8 XCDs in turn.  Sequences of one length: each
+// XCD takes one contiguous run, so that the tiles of a head, which read the same keys, share an
+// L2.  Ragged ones: runs of kRaggedRun in turn, since the long sequences of a head would all be one
+// XCD's (the backward of 8192 queries in 4 sequences of 878 to 5506, 16 heads of 128, 4 of the
+// keys: 962 us, so 639).  The grid is then a multiple of 8 runs, and ids past the last
+// have no work.
+constexpr int kRaggedRun = 8;
+__device__ __forceinline__ int64_t attn_run(uint32_t id, uint32_t total, bool ragged) {
+  const uint32_t xcd = id % 8, at = id / 8;
+  if (ragged) return ((int64_t)(at / kRaggedRun) * 8 + xcd) * kRaggedRun + at % kRaggedRun;
+  return (int64_t)xcd * (total / 8) + min(xcd, total % 8) + at;
 }
 
 // Rows of no sequence: f(token) for the tokens outside the offsets, a share for each slot
@@ -378,6 +411,43 @@ inline int32_t check_attn_grid(int64_t blocks, int threads) {
   if (blocks * threads > kMaxLanes)
     return fail(ASP_ERR_SHAPE, "%lld workgroups are more than one launch has", (long long)blocks);
   return ASP_OK;
+}
+
+// workgroups of a launch: see attn_run
+inline int64_t attn_grid(const AttnArgs& a, bool ragged) {
+  const int64_t total = (int64_t)a.slots * a.splits * a.Hk, step = 8 * kRaggedRun;
+  return ragged ? (total + step - 1) / step * step : total;
+}
+
+// The form of a pass, by sizes alone: `held` rows in registers (queries with their shared heads, or
+// keys) of each of Hk heads, `passed` rows that go by.  wide: four waves of different rows
+// share the tiles that go by; else a workgroup has 32 rows and its waves share the tiles.
+struct AttnPlan {
+  bool wide;
+  int tile, slots, splits;
+  int64_t chunk;
+};
+
+inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged) {
+  AttnPlan p;
+  p.wide = attn_slots(held, 128, 1, false) * Hk >= 256;
+  p.tile = p.wide ? 128 : 32;
+  p.slots = (int)attn_slots(held, p.tile, G, ragged);
+  // workgroups without splits and rows that go by, as if the sequences were alike
+  const int64_t each = (held / G + p.tile - 1) / p.tile, blocks = std::max<int64_t>(1, each) * G * Hk;
+  const int64_t by = std::max<int64_t>(1, passed / G);
+  // A range is split where that makes so many workgroups, and ragged sequences more, since the longest
+  // would be alone at the end; but from `least` rows on only, since a part's result is written
+  // and read again in float32.
+  const int64_t target = G > 1 ? 1024 : p.wide ? 0 : 512, least = p.wide ? 1024 : 256;
+  const int64_t most = p.wide ? 8 : std::min<int64_t>(64, 4 * target / blocks);
+  p.splits = 1;
+  p.chunk = passed + 1;
+  if (blocks < target && (p.wide || blocks < 256)) {
+    p.chunk = std::max(least, (by * blocks + target - 1) / target);
+    p.splits = (int)std::max<int64_t>(1, std::min((passed + p.chunk - 1) / p.chunk, most));
+  }
+  return p;
 }
 
 }  // namespace asp

@@ -54,9 +54,11 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave % WM, wk = wave / WM;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x);
-  const int slot = (int)(run % a.slots), split = (int)(run / a.slots % a.splits);
-  const int hk = (int)(run / a.slots / a.splits);
+  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.qo != nullptr);
+  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
+  // the later parts, which shorter sequences do not have, come last
+  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
+  const int split = (int)(run / a.slots / a.Hk);
   const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
 
   if (a.zero && a.qo && split == 0)
@@ -71,7 +73,8 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
       }
     });
   const int64_t row0 = seq.tile * BM, rows = seq.rows * a.group;
-  if (!seq.any || row0 >= rows) return;
+  const int parts = attn_parts(a, seq.keys);
+  if (!seq.any || row0 >= rows || split >= parts) return;
 
   // the lane's queries
   int64_t token[NQ];
@@ -132,17 +135,16 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
 
   // this workgroup's tiles of keys; each of its WK columns makes `turns`
   const int64_t tiles = (seq.keys + BN - 1) / BN;
-  const int64_t first = tiles * split / a.splits, last = tiles * (split + 1) / a.splits;
+  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
   const int turns = (int)((last - first + WK - 1) / WK);
   uint8_t* mine = smem + wk * F::GROUP;
   const int64_t base_row = seq.k0;
   auto key0 = [&](int t) { return (first + (int64_t)t * WK + wk) * BN; };
-  // which of a tile's keys count, one bit a key
-  auto keys_of = [&](int t) -> uint64_t {
+  // whether the lane's key of a tile counts; the tiles' 64 lanes together are one bit a key
+  auto key_on = [&](int t) -> int {
     const int64_t at = key0(t) + lane;
-    bool on = lane < BN && t < turns && first + (int64_t)t * WK + wk < last && at < seq.keys;
-    if (on && a.mask) on = a.mask[base_row + at] != 0;
-    return __ballot(on);
+    const bool on = lane < BN && t < turns && first + (int64_t)t * WK + wk < last && at < seq.keys;
+    return on ? (a.mask ? a.mask[base_row + at] : 1) : 0;
   };
 
   // ---- copies of bf16 and float32 tiles
@@ -227,19 +229,24 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
     }
   };
 
-  uint64_t live = keys_of(0);
+  // a tile's mask is loaded two turns ahead and looked at when the tile before it has landed
+  uint64_t live = __ballot(key_on(0) != 0), next;
+  int on = key_on(1);
   issue(0, live);
   fetch(0, live);
   for (int t = 0; t < turns; ++t) {
-    const uint64_t next = keys_of(t + 1);
     const uint8_t* tile = mine + (Q4 ? 0 : (t & 1) * 2 * TILE);
     if constexpr (Q4) {
       attn_settle<(WM > 1)>();  // the tile before is read
       unpack4();
       attn_settle<(WM > 1)>();
+      next = __ballot(on != 0);
+      on = key_on(t + 2);
       if (t + 1 < turns) fetch(t + 1, next);
     } else {
       attn_settle<(WM > 1)>();  // tile t is there, and the one before is read
+      next = __ballot(on != 0);
+      on = key_on(t + 2);
       if (t + 1 < turns) issue(t + 1, next);
     }
     if (live != 0) {
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
     const float lg = none ? kNegInf : m[n] + __builtin_amdgcn_logf(l[n]);
     const int64_t at = token[n] * a.Hq + head[n];
     if (!valid[n]) continue;
-    if (a.splits > 1) {
+    if (parts > 1) {
       float* part = a.part + ((int64_t)split * a.Tq * a.Hq + at) * a.D;
       store_row<float, DT>(part, acc[n], inv, a.D, half);
       if (half == 0) a.part_l[(int64_t)split * a.Tq * a.Hq + at] = lg;
@@ -366,35 +373,49 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
   }
 }
 
-// The splits' results of a query, joined by their sums: 16 lanes a row, 8 elements each.
+// The splits' results of a query (at most 64), joined by their sums.  A wave has one query: its
+// lanes find the splits' weights, then four groups of 16 lanes take every fourth split, 8
+// elements a lane.
 template <typename XT>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), rows = a.Tq * a.Hq;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), rows = a.Tq * a.Hq;
   if (row >= rows) return;
+  const int lane = threadIdx.x & 63, mine = lane >> 4;
   const int64_t t = row / a.Hq;
-  const int h = (int)(row - t * a.Hq), d = 8 * (threadIdx.x & 15);
+  const int h = (int)(row - t * a.Hq), d = 8 * (lane & 15);
   if (a.qo && (t < attn_offset(a.qo, 0, a.Tq) || t >= attn_offset(a.qo, a.G, a.Tq))) return;
-  float top = kNegInf;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_l[s * rows + row]);
+  const int parts = attn_parts(a, attn_keys(a, a.qo ? attn_owner(a.qo, a.G, t) : 0));
+  if (parts == 1) return;
+  const float l = lane < parts ? a.part_l[lane * rows + row] : kNegInf;
+  float top = l;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
   const float off = top == kNegInf ? 0.0f : top;
-  float sum = 0.0f, v[8] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float l = a.part_l[s * rows + row], w = __builtin_amdgcn_exp2f(l - off);
-    sum += l == l ? w : l;  // a NaN is the row's
-    if (d < a.D && w != 0.0f) {
+  const float w = l == l ? __builtin_amdgcn_exp2f(l - off) : l;  // a NaN is the row's
+  float sum = w;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
+  float v[8] = {};
+  for (int s = mine; s < parts; s += 4) {
+    const float ws = __shfl(w, s);
+    if (d < a.D && ws != 0.0f) {
       const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part + (s * rows + row) * a.D + d);
       const f32x4_t x = p[0], y = p[1];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = __builtin_fmaf(x[e], w, v[e]);
-        v[4 + e] = __builtin_fmaf(y[e], w, v[4 + e]);
+        v[e] = __builtin_fmaf(x[e], ws, v[e]);
+        v[4 + e] = __builtin_fmaf(y[e], ws, v[4 + e]);
       }
     }
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] += __shfl_xor(v[e], 16);
+    v[e] += __shfl_xor(v[e], 32);
+  }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if ((threadIdx.x & 15) == 0 && a.lse)
-    a.lse[row] = sum == 0.0f ? kNegInf : (off + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (d >= a.D) return;
+  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (off + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (mine || d >= a.D) return;
   XT* o = static_cast<XT*>(a.o) + t * a.ot + h * a.oh + d;
   if constexpr (sizeof(XT) == 2) {
     *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16x2_rne(v[0] * inv, v[1] * inv), bf16x2_rne(v[2] * inv, v[3] * inv),
@@ -407,37 +428,18 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a) {
 
 // -------------------------------------------------------------------- host
 
-// The form of a call, by sizes alone.  wide: four waves of different rows share the tiles of
-// keys; else a workgroup has 32 rows and its waves share the keys.
-struct Plan {
-  bool wide;
-  int tile;  // rows of a workgroup
-  int slots, splits;
-};
-
-Plan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t G, bool ragged) {
-  Plan p;
-  const int64_t rows = Tq * (Hq / Hk);
-  p.wide = attn_slots(rows, 128, 1, false) * Hk >= 256;
-  p.tile = p.wide ? 128 : 32;
-  p.slots = (int)attn_slots(rows, p.tile, G, ragged);
-  // workgroups without splits, ragged ones counted as if each sequence had its share
-  const int64_t blocks = std::max<int64_t>(1, (rows + p.tile - 1) / p.tile) * Hk;
-  const int64_t tiles = (Tk / G + 127) / 128;  // rounds of the four waves
-  int64_t splits = 1;
-  if (!p.wide && blocks < 256) splits = std::min<int64_t>((511 + blocks) / blocks, tiles / 2);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
-  return p;
+AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t G, bool ragged) {
+  return attn_plan(Tq * (Hq / Hk), Tk, Hk, G, ragged);
 }
 
-size_t part_bytes(const Plan& p, int64_t Tq, int32_t Hq, int32_t D) {
+size_t part_bytes(const AttnPlan& p, int64_t Tq, int32_t Hq, int32_t D) {
   return p.splits > 1 ? up256((size_t)p.splits * Tq * Hq * (D + 1) * 4) : 0;
 }
 
 template <typename XT, int DT, int NQ, int WM, int WK, int KT, bool Q4>
 int32_t launch(const AttnArgs& a, hipStream_t st) {
   using F = Forward<XT, DT, NQ, WM, WK, KT, Q4>;
-  const int64_t blocks = (int64_t)a.slots * a.splits * a.Hk;
+  const int64_t blocks = attn_grid(a, a.qo != nullptr);
   ASP_TRY(check_attn_grid(blocks, F::THREADS));
   k_attn<XT, DT, NQ, WM, WK, KT, Q4><<<dim3((unsigned)blocks), F::THREADS, 0, st>>>(a);
   return launch_status("attention");
@@ -455,7 +457,7 @@ template <typename XT, bool Q4>
 int32_t launch_attn(const AttnArgs& a, bool wide, hipStream_t st) {
   ASP_TRY((a.D <= 64 ? launch_form<XT, 2, Q4>(a, wide, st) : launch_form<XT, 4, Q4>(a, wide, st)));
   if (a.splits == 1) return ASP_OK;
-  const int64_t blocks = (a.Tq * a.Hq + 15) / 16;
+  const int64_t blocks = (a.Tq * a.Hq + 3) / 4;
   ASP_TRY(check_attn_grid(blocks, 256));
   k_attn_join<XT><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
   return launch_status("attention join");
@@ -463,7 +465,7 @@ int32_t launch_attn(const AttnArgs& a, bool wide, hipStream_t st) {
 
 int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t workspace_bytes,
                  hipStream_t st) {
-  const Plan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.G, a.qo != nullptr);
+  const AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.G, a.qo != nullptr);
   const size_t need = part_bytes(p, a.Tq, a.Hq, a.D);
   if (need) ASP_TRY(check_ptr(workspace, "workspace", true));
   if (workspace_bytes < need)
@@ -472,6 +474,7 @@ int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t wo
   a.group = a.Hq / a.Hk;
   a.slots = p.slots;
   a.splits = p.splits;
+  a.chunk = p.chunk;
   a.part = static_cast<float*>(workspace);
   a.part_l = a.part + (size_t)p.splits * a.Tq * a.Hq * a.D;
   if (dtype == ASP_BF16)

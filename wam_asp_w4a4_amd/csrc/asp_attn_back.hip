@@ -103,7 +103,8 @@ struct BackQ {
 // dq of 32 WM rows (a token's shared heads follow one another); WK columns of waves take
 // every WK-th tile of 32 KT keys.  Also writes each row's logarithm and delta for k_attn_dkv.
 template <typename XT, int DT, int WM, int WK, int KT>
-__global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS)) k_attn_dq(const AttnArgs a) {
+__global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(XT) == 2 && WM > 1 ? 2 : 1))
+    k_attn_dq(const AttnArgs a) {
   using B = BackQ<XT, DT, WM, WK, KT>;
   using P = typename B::P;
   using R = typename B::R;
@@ -112,16 +113,19 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS)) k_attn_d
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave % WM, wk = wave / WM;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x);
-  const int slot = (int)(run % a.slots), split = (int)(run / a.slots % a.splits);
-  const int hk = (int)(run / a.slots / a.splits);
+  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.qo != nullptr);
+  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
+  // the later parts, which shorter sequences do not have, come last
+  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
+  const int split = (int)(run / a.slots / a.Hk);
   const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
   if (a.zero & 1 && a.qo && split == 0)
     attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
       zero_heads<XT>(a.dq, t, a.dqt, a.dqh, hk * a.group, a.group, a.D, B::THREADS);
     });
   const int64_t row0 = seq.tile * BM, rows = seq.rows * a.group;
-  if (!seq.any || row0 >= rows) return;
+  const int parts = attn_parts(a, seq.keys);
+  if (!seq.any || row0 >= rows || split >= parts) return;
 
   const int64_t r = row0 + 32 * wm + l32;
   const bool valid = r < rows;
@@ -151,15 +155,14 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS)) k_attn_d
     for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
 
   const int64_t tiles = (seq.keys + BN - 1) / BN;
-  const int64_t first = tiles * split / a.splits, last = tiles * (split + 1) / a.splits;
+  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
   const int turns = (int)((last - first + WK - 1) / WK);
   uint8_t* mine = smem + wk * B::GROUP;
   auto key0 = [&](int t) { return (first + (int64_t)t * WK + wk) * BN; };
-  auto keys_of = [&](int t) -> uint64_t {
+  auto key_on = [&](int t) -> int {
     const int64_t k = key0(t) + lane;
-    bool on = lane < BN && t < turns && first + (int64_t)t * WK + wk < last && k < seq.keys;
-    if (on && a.mask) on = a.mask[seq.k0 + k] != 0;
-    return __ballot(on);
+    const bool on = lane < BN && t < turns && first + (int64_t)t * WK + wk < last && k < seq.keys;
+    return on ? (a.mask ? a.mask[seq.k0 + k] : 1) : 0;
   };
   constexpr int COPIES = TILE / 1024 / WM;
   static_assert(TILE % (1024 * WM) == 0, "whole copies for each wave");
@@ -186,49 +189,46 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS)) k_attn_d
     }
   };
 
-  uint64_t live = keys_of(0);
+  uint64_t live = __ballot(key_on(0) != 0);
+  int on = key_on(1);
   issue(0, live);
   for (int t = 0; t < turns; ++t) {
-    const uint64_t next = keys_of(t + 1);
     const uint8_t* tile = mine + (t & 1) * 2 * TILE;
     attn_settle<(WM > 1)>();
+    const uint64_t next = __ballot(on != 0);
+    on = key_on(t + 2);
     if (t + 1 < turns) issue(t + 1, next);
     if (live != 0) {
-      f32x16_t s[KT], d[KT];
+      constexpr uint64_t ALL = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
+        f32x16_t s, d;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) s[k][v] = d[k][v] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < QS; ++i)
-          piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * k * R::BYTES, i, half, l32), qf[i], s[k]);
+        for (int v = 0; v < 16; ++v) s[v] = d[v] = 0.0f;
 #pragma unroll
         for (int i = 0; i < QS; ++i)
-          piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * k * R::BYTES, i, half, l32), df[i], d[k]);
+          piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * k * R::BYTES, i, half, l32), qf[i], s);
+#pragma unroll
+        for (int i = 0; i < QS; ++i)
+          piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * k * R::BYTES, i, half, l32), df[i], d);
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          d[k][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][v], c, -lg)) * (d[k][v] - delta);
-      }
-      constexpr uint64_t ALL = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
-      if (live != ALL)
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
+          d[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], c, -lg)) * (d[v] - delta);
+        if (live != ALL) {
           const uint32_t bits = (uint32_t)(live >> (32 * k)) >> (4 * half);
 #pragma unroll
           for (int v = 0; v < 16; ++v)
-            if (!(bits >> (8 * (v >> 2) + (v & 3)) & 1)) d[k][v] = 0.0f;
+            if (!(bits >> (8 * (v >> 2) + (v & 3)) & 1)) d[v] = 0.0f;
         }
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
         Weights<P> w;
-        w.set(d[k]);
+        w.set(d);
         columns_mfma<P, DT>(tile + 32 * k * R::BYTES, w, acc, lane);
       }
     }
     live = next;
   }
   if (!join_columns<WK, WM>(smem, wk, wm, lane, acc) || !valid) return;
-  if (a.splits > 1)
+  if (parts > 1)
     store_row<float, DT>(a.part_dq + ((int64_t)split * a.Tq * a.Hq + at) * a.D, acc, a.scale, a.D, half);
   else
     store_row<XT, DT>(static_cast<XT*>(a.dq) + token * a.dqt + head * a.dqh, acc, a.scale, a.D, half);
@@ -269,7 +269,8 @@ struct BackKV {
 // dk and dv of 32 WN keys of one head; WQ columns of waves take every WQ-th tile of 32 QT
 // queries, head by head of those that share the keys.
 template <typename XT, int DT, int WN, int WQ, int QT>
-__global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_dkv(const AttnArgs a) {
+__global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
+    k_attn_dkv(const AttnArgs a) {
   using B = BackKV<XT, DT, WN, WQ, QT>;
   using P = typename B::P;
   using R = typename B::R;
@@ -278,9 +279,11 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wn = wave % WN, wq = wave / WN;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x);
-  const int slot = (int)(run % a.slots), split = (int)(run / a.slots % a.splits);
-  const int hk = (int)(run / a.slots / a.splits);
+  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.ko != nullptr);
+  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
+  // the later parts, which shorter sequences do not have, come last
+  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
+  const int split = (int)(run / a.slots / a.Hk);
   const AttnSeq seq = attn_seq(a, a.ko, a.Tk, 1, BN, slot);
   if (a.zero & 6 && a.ko && split == 0)
     attn_outside(a.ko, a.G, a.Tk, slot, a.slots, [&](int64_t t) {
@@ -288,7 +291,8 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
       if (a.zero & 4) zero_heads<XT>(a.dv, t, a.dvt, a.dvh, hk, 1, a.D, B::THREADS);
     });
   const int64_t key0 = seq.tile * BN;
-  if (!seq.any || key0 >= seq.all) return;
+  const int parts = attn_parts(a, seq.rows * a.group);
+  if (!seq.any || key0 >= seq.all || split >= parts) return;
 
   const int64_t key = key0 + 32 * wn + l32, krow = seq.k0 + key;
   const bool stored = key < seq.all;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
   const int64_t per_head = (seq.rows + BQ - 1) / BQ;
   // a workgroup without a key that counts has nothing to sum
   const int64_t tiles = key0 < seq.keys ? per_head * a.group : 0;
-  const int64_t first = tiles * split / a.splits, last = tiles * (split + 1) / a.splits;
+  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
   const int turns = (int)((last - first + WQ - 1) / WQ);
   uint8_t* mine = smem + wq * B::GROUP;
   float* row_log2 = reinterpret_cast<float*>(mine + 4 * TILE);  // [buffer][BQ], then the deltas
@@ -366,7 +370,8 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
         piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * j * R::BYTES, i, half, l32), kf[i], s);
 #pragma unroll
       for (int i = 0; i < QS; ++i)
-        piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * j * R::BYTES, i, half, l32), vf[i], d);
+        piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * j * R::BYTES, i, half, l32),
+                      vf[i], d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = b * BQ + 32 * j + 8 * i + 4 * half;
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
   const int64_t at = krow * a.Hk + hk;
-  if (a.splits > 1) {
+  if (parts > 1) {
     const int64_t part = ((int64_t)split * a.Tk * a.Hk + at) * a.D;
     if (a.dv) store_row<float, DT>(a.part_dv + part, dv, 1.0f, a.D, half);
     if (a.dk) store_row<float, DT>(a.part_dk + part, dk, a.scale, a.D, half);
@@ -404,76 +409,73 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS)) k_attn_
   }
 }
 
-// The splits' sums of one or two tensors (blockIdx.y) of T x H heads, in order; 16 lanes a head
+// The parts' sums of dq, or of dk and dv (blockIdx.y), in order.  A wave has one token, its groups of 16
+// lanes a head each, 8 elements a lane.
 struct SumArgs {
+  AttnArgs a;
   const float* part[2];
   void* out[2];
-  int64_t st[2], sh[2];
-  const int32_t* offsets;
-  int64_t T;
-  int H, D, G, splits;
+  int64_t st[2], sh[2], T;
+  int H;
+  bool keys;  // dk and dv
 };
 
 template <typename XT>
-__global__ void __launch_bounds__(256) k_attn_sum(const SumArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4), rows = a.T * a.H;
-  const int d = 8 * (threadIdx.x & 15), which = blockIdx.y;
-  if (row >= rows || d >= a.D || !a.out[which]) return;
-  const int64_t t = row / a.H, h = row - t * a.H;
-  if (a.offsets && (t < attn_offset(a.offsets, 0, a.T) || t >= attn_offset(a.offsets, a.G, a.T))) return;
-  float v[8] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part[which] + (s * rows + row) * a.D + d);
-    const f32x4_t x = p[0], y = p[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += x[e];
-      v[4 + e] += y[e];
-    }
+__global__ void __launch_bounds__(256) k_attn_sum(const SumArgs s) {
+  const AttnArgs& a = s.a;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, which = blockIdx.y, d = 8 * (lane & 15);
+  if (t >= s.T || !s.out[which]) return;
+  const int32_t* offsets = s.keys ? a.ko : a.qo;
+  int g = 0;
+  if (offsets) {
+    if (t < attn_offset(offsets, 0, s.T) || t >= attn_offset(offsets, a.G, s.T)) return;
+    g = attn_owner(offsets, a.G, t);
   }
-  XT* o = static_cast<XT*>(a.out[which]) + t * a.st[which] + h * a.sh[which] + d;
-  if constexpr (sizeof(XT) == 2) {
-    *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
-                                             bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+  int64_t passed;
+  if (!s.keys) {
+    passed = attn_keys(a, g);
   } else {
-    *reinterpret_cast<f32x4_t*>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    const int64_t rows = a.qo ? attn_offset(a.qo, g + 1, a.Tq) - attn_offset(a.qo, g, a.Tq) : a.Tq;
+    passed = max(rows, (int64_t)0) * a.group;
+  }
+  const int parts = attn_parts(a, passed);
+  if (parts == 1 || d >= a.D) return;
+  for (int h = lane >> 4; h < s.H; h += 4) {
+    float v[8] = {};
+    for (int p = 0; p < parts; ++p) {
+      const f32x4_t* from =
+          reinterpret_cast<const f32x4_t*>(s.part[which] + ((p * s.T + t) * s.H + h) * a.D + d);
+      const f32x4_t x = from[0], y = from[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += x[e];
+        v[4 + e] += y[e];
+      }
+    }
+    XT* o = static_cast<XT*>(s.out[which]) + t * s.st[which] + h * s.sh[which] + d;
+    if constexpr (sizeof(XT) == 2) {
+      *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]),
+                                               bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])};
+    } else {
+      *reinterpret_cast<f32x4_t*>(o) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    }
   }
 }
 
 // -------------------------------------------------------------------- host
 
-// The form of one of the two passes, by sizes alone: `held` rows in registers (queries with their
-// shared heads, or keys) of Hk heads, `passed` rows in all that go by.  wide: four waves of
-// different rows share the tiles; else a workgroup has 32 rows and its waves share the tiles.
-struct Plan {
-  bool wide;
-  int slots, splits;
-};
-
-Plan plan_of(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged) {
-  Plan p;
-  p.wide = attn_slots(held, 128, 1, false) * Hk >= 256;
-  const int tile = p.wide ? 128 : 32;
-  p.slots = (int)attn_slots(held, tile, G, ragged);
-  const int64_t blocks = std::max<int64_t>(1, (held + tile - 1) / tile) * Hk;
-  const int64_t tiles = (passed / G + 127) / 128;
-  int64_t splits = 1;
-  if (!p.wide && blocks < 256) splits = std::min<int64_t>((511 + blocks) / blocks, tiles / 2);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64));
-  return p;
-}
-
 struct Sizes {
-  Plan q, kv;
+  AttnPlan q, kv;
   size_t rows, dq, dk;  // bytes of the parts of the workspace; dv's are dk's
 };
 
 Sizes sizes_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, int32_t G, bool rq, bool rk) {
   Sizes s;
   const int64_t group = Hq / Hk;
-  s.q = plan_of(Tq * group, Tk, Hk, G, rq);
-  s.kv = plan_of(Tk, Tq * group, Hk, G, rk);
+  s.q = attn_plan(Tq * group, Tk, Hk, G, rq);
+  s.kv = attn_plan(Tk, Tq * group, Hk, G, rk);
   s.rows = up256((size_t)Tq * Hq * 8);
   s.dq = s.q.splits > 1 ? up256((size_t)s.q.splits * Tq * Hq * D * 4) : 0;
   s.dk = s.kv.splits > 1 ? up256((size_t)s.kv.splits * Tk * Hk * D * 4) : 0;
@@ -483,7 +485,7 @@ Sizes sizes_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, int32_
 template <typename XT, int DT, int WM, int WK, int KT>
 int32_t launch_dq(const AttnArgs& a, hipStream_t st) {
   using B = BackQ<XT, DT, WM, WK, KT>;
-  const int64_t blocks = (int64_t)a.slots * a.splits * a.Hk;
+  const int64_t blocks = attn_grid(a, a.qo != nullptr);
   ASP_TRY(check_attn_grid(blocks, B::THREADS));
   k_attn_dq<XT, DT, WM, WK, KT><<<dim3((unsigned)blocks), B::THREADS, 0, st>>>(a);
   return launch_status("attention dq");
@@ -492,7 +494,7 @@ int32_t launch_dq(const AttnArgs& a, hipStream_t st) {
 template <typename XT, int DT, int WN, int WQ, int QT>
 int32_t launch_dkv(const AttnArgs& a, hipStream_t st) {
   using B = BackKV<XT, DT, WN, WQ, QT>;
-  const int64_t blocks = (int64_t)a.slots * a.splits * a.Hk;
+  const int64_t blocks = attn_grid(a, a.ko != nullptr);
   ASP_TRY(check_attn_grid(blocks, B::THREADS));
   k_attn_dkv<XT, DT, WN, WQ, QT><<<dim3((unsigned)blocks), B::THREADS, 0, st>>>(a);
   return launch_status("attention dk, dv");
@@ -500,7 +502,7 @@ int32_t launch_dkv(const AttnArgs& a, hipStream_t st) {
 
 template <typename XT>
 int32_t launch_sum(const SumArgs& s, int tensors, hipStream_t st) {
-  const int64_t blocks = (s.T * s.H + 15) / 16;
+  const int64_t blocks = (s.T + 3) / 4;
   ASP_TRY(check_attn_grid(blocks * tensors, 256));
   k_attn_sum<XT><<<dim3((unsigned)blocks, tensors), 256, 0, st>>>(s);
   return launch_status("attention sums");
@@ -514,11 +516,13 @@ int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
   if (a.Tq > 0 && a.dq) {
     a.slots = z.q.slots;
     a.splits = z.q.splits;
+    a.chunk = z.q.chunk;
     ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, COLUMNS, 1>(a, st)));
     if (a.splits > 1) {
       SumArgs s = {};
+      s.a = a;
       s.part[0] = a.part_dq; s.out[0] = a.dq; s.st[0] = a.dqt; s.sh[0] = a.dqh;
-      s.offsets = a.qo; s.T = a.Tq; s.H = a.Hq; s.D = a.D; s.G = a.G; s.splits = a.splits;
+      s.T = a.Tq; s.H = a.Hq;
       ASP_TRY(launch_sum<XT>(s, 1, st));
     }
   } else if (a.Tq > 0 && a.Tk > 0) {
@@ -530,12 +534,15 @@ int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
   if (a.Tk == 0 || (!a.dk && !a.dv)) return ASP_OK;
   a.slots = z.kv.slots;
   a.splits = z.kv.splits;
+  a.chunk = z.kv.chunk;
   ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, COLUMNS, 1>(a, st)));
   if (a.splits == 1) return ASP_OK;
   SumArgs s = {};
+  s.a = a;
+  s.keys = true;
   s.part[0] = a.part_dk; s.out[0] = a.dk; s.st[0] = a.dkt; s.sh[0] = a.dkh;
   s.part[1] = a.part_dv; s.out[1] = a.dv; s.st[1] = a.dvt; s.sh[1] = a.dvh;
-  s.offsets = a.ko; s.T = a.Tk; s.H = a.Hk; s.D = a.D; s.G = a.G; s.splits = a.splits;
+  s.T = a.Tk; s.H = a.Hk;
   return launch_sum<XT>(s, 2, st);
 }
 
