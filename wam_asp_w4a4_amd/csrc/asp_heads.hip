@@ -341,33 +341,40 @@ __global__ void __launch_bounds__(kThreads) k_head_norm_back(const HeadArgs a) {
     }
   }
   if (!s.part) return;
+  // each group's sums by element
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sums[(group * L + l) * 8 + j] = dw[j];
-  __syncthreads();
-  // element i of a lane's eight: L * 8 sums over the groups
-  for (int i = threadIdx.x; i < L * 8; i += kThreads) {
-    float sum = 0.0f;
-    for (int g = 0; g < kThreads / L; ++g) sum += sums[g * L * 8 + i];
-    const Where mine(i / 8, a.D, a.rot);
-    const int at = mine.at[(i & 7) / Where::RUN];
-    if (at >= 0) s.part[(int64_t)block * a.D + at + (i & 7) % Where::RUN] = sum;
+  for (int j = 0; j < 8; ++j) {
+    const int at = where.at[j / Where::RUN];
+    if (at >= 0) sums[group * L * 8 + at + j % Where::RUN] = dw[j];
   }
+  __syncthreads();
+  if ((int)threadIdx.x >= a.D) return;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int g = 0; g < kThreads / L; ++g) sum += sums[g * L * 8 + threadIdx.x];
+  s.part[(int64_t)block * a.D + threadIdx.x] = sum;
 }
 
-// dw = the sum of the blocks' rows: 16 columns a block, 64 threads a column
+// dw = the sum of the blocks' rows: 8 columns a workgroup, 128 threads a column
 __global__ void __launch_bounds__(1024) k_head_sums(const HeadArgs a) {
-  __shared__ float sums[64][17];
+  __shared__ float sums[8][129];
   const Side& s = a.side[blockIdx.y];
   if (!s.dw) return;
-  const int col = blockIdx.x * 16 + (threadIdx.x & 15), row = threadIdx.x >> 4;
+  const int col = blockIdx.x * 8 + (threadIdx.x & 7), row = threadIdx.x >> 3;
   float sum = 0.0f;
-  if (col < a.D)
-    for (int b = row; b < s.blocks; b += 64) sum += s.part[(int64_t)b * a.D + col];
-  sums[row][threadIdx.x & 15] = sum;
+  if (col < a.D) {
+#pragma unroll 8
+    for (int b = row; b < s.blocks; b += 128) sum += s.part[(int64_t)b * a.D + col];
+  }
+  sums[threadIdx.x & 7][row] = sum;
   __syncthreads();
-  if (row || col >= a.D) return;
-  for (int r = 1; r < 64; ++r) sum += sums[r][threadIdx.x & 15];
-  s.dw[col] = sum;
+  // a wave for each of the columns, two of the 128 sums a lane
+  const int c = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (c >= 8 || (int)(blockIdx.x * 8 + c) >= a.D) return;
+  sum = sums[c][lane] + sums[c][lane + 64];
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
+  if (lane == 0) s.dw[blockIdx.x * 8 + c] = sum;
 }
 
 // -------------------------------------------------------------------- host
@@ -615,7 +622,7 @@ int32_t asp_head_norm_backward(const void* dq, int64_t lddq, int64_t hsdq, const
   const hipStream_t st = (hipStream_t)stream;
   if (sq.blocks + sk.blocks) ASP_TRY(launch_heads<Backward>(a, dtype, d_dtype, layout, st));
   if (!sums) return ASP_OK;
-  k_head_sums<<<dim3((D + 15) / 16, 2), 1024, 0, st>>>(a);
+  k_head_sums<<<dim3((D + 7) / 8, 2), 1024, 0, st>>>(a);
   return launch_status("head norm sums");
 }
 

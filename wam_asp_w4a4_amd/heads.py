@@ -23,6 +23,13 @@ from .norm import KINDS
 LAYOUTS = {"pairs": B.ASP_ROTATE_PAIRS, "halves": B.ASP_ROTATE_HALVES}
 
 
+def _make(like, stream, shape, dtype):
+    """``_new`` on the device of `like`; the usual call in little host time."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+    return _new(stream, like.device, shape, dtype)
+
+
 class HeadNormGrads(NamedTuple):
     """Gradients of head_norm's inputs (None: not given, or not wanted)."""
     dq: torch.Tensor | None
@@ -34,6 +41,14 @@ class HeadNormGrads(NamedTuple):
 def _check_heads(t, name, shape, device, dtypes=_CODES):
     """t must be (T, H, D) with contiguous heads (None in `shape`: any number).  Returns its
     token and head strides."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device:
+        have, (T, H, D) = t.shape, shape
+        if len(have) == 3 and have[2] == D and (T is None or have[0] == T) \
+                and (H is None or have[1] == H):
+            st, sh, sd = t.stride()
+            if sd == 1 or D == 1:
+                # a dimension of one element has no stride to speak of
+                return st if have[0] > 1 else have[1] * D, sh if have[1] > 1 else D
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype not in dtypes:
@@ -44,11 +59,7 @@ def _check_heads(t, name, shape, device, dtypes=_CODES):
         raise ValueError(f"{name} must be ({want}), got {tuple(have)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    st, sh, sd = t.stride()
-    if sd != 1 and have[2] > 1:
-        raise ValueError(f"the heads of {name} must be contiguous, got strides {t.stride()}")
-    # a dimension of one element has no stride to speak of
-    return (st if have[0] > 1 else have[1] * have[2]), (sh if have[1] > 1 else have[2])
+    raise ValueError(f"the heads of {name} must be contiguous, got strides {t.stride()}")
 
 
 def _spec(T, D, device, has_k, norm, q_weight, k_weight, cos, sin, positions, layout):
@@ -71,6 +82,14 @@ def _spec(T, D, device, has_k, norm, q_weight, k_weight, cos, sin, positions, la
         if positions is not None:
             raise ValueError("positions without cos and sin")
         return KINDS[norm], LAYOUTS[layout], 0, 0
+    if isinstance(cos, torch.Tensor) and isinstance(sin, torch.Tensor) and positions is not None \
+            and cos.dtype is torch.float32 is sin.dtype and cos.shape == sin.shape \
+            and cos.device == device == sin.device and cos.is_contiguous() and sin.is_contiguous() \
+            and isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 \
+            and positions.shape == (T,) and positions.device == device and positions.is_contiguous():
+        have = cos.shape
+        if len(have) == 2 and have[0] > 0 and 0 < have[1] <= D // 2:
+            return KINDS[norm], LAYOUTS[layout], have[0], 2 * have[1]
     for t, name in ((cos, "cos"), (sin, "sin")):
         if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
             raise TypeError(f"{name} must be a float32 tensor")
@@ -108,43 +127,46 @@ def head_norm(q, k=None, *, norm="rms", q_weight=None, k_weight=None, cos=None, 
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D torch tensor, (T, H, D)")
     T, Hq, D = q.shape
-    dev = q.device
+    dev, x_dtype = q.device, q.dtype
     ldq, hsq = _check_heads(q, "q", (T, Hq, D), dev)
-    Hk, ldk, hsk = 0, 0, 0
+    Hk = ldk = hsk = ldko = hsko = 0
     if k is not None:
-        ldk, hsk = _check_heads(k, "k", (T, None, D), dev, (q.dtype,))
+        ldk, hsk = _check_heads(k, "k", (T, None, D), dev, (x_dtype,))
         Hk = k.shape[1]
     norm, layout, P, rot = _spec(T, D, dev, k is not None, norm, q_weight, k_weight, cos, sin,
                                  positions, layout)
-    given = [t for t in (q_out, k_out) if isinstance(t, torch.Tensor)]
-    if out is not None and out not in _Y_DTYPES:
-        raise ValueError(f"out must be 'f32' or 'bf16', not {out!r}")
-    dtype = _Y_DTYPES[out] if out is not None else given[0].dtype if given else q.dtype
+    if out is not None:
+        if out not in _Y_DTYPES:
+            raise ValueError(f"out must be 'f32' or 'bf16', not {out!r}")
+        dtype = _Y_DTYPES[out]
+    else:
+        given = [t.dtype for t in (q_out, k_out) if isinstance(t, torch.Tensor)]
+        dtype = given[0] if given else x_dtype
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    made, zero = [], 0   # bits of the outputs made here
-
-    def output(t, name, heads, bit):
-        nonlocal zero
-        if t is None:
-            t = _new(stream, dev, (T, heads, D), dtype)
-            made.append(t)
-            zero |= bit
-            return t, heads * D, D
-        return (t, *_check_heads(t, name, (T, heads, D), dev, (dtype,)))
-
-    q_out, ldqo, hsqo = output(q_out, "q_out", Hq, 1)
-    ldko = hsko = 0
-    if k is not None:
-        k_out, ldko, hsko = output(k_out, "k_out", Hk, 2)
-    at = B._at
     if dtype not in _CODES:
         raise TypeError(f"q_out must be float32 or bfloat16, not {dtype}")
+    made, zero = [], 0   # bits of the outputs made here
+    if q_out is None:
+        q_out, ldqo, hsqo, zero = _make(q, stream, (T, Hq, D), dtype), Hq * D, D, 1
+        made.append(q_out)
+    else:
+        ldqo, hsqo = _check_heads(q_out, "q_out", (T, Hq, D), dev, (dtype,))
+    if k is None:
+        pass
+    elif k_out is None:
+        k_out, ldko, hsko = _make(q, stream, (T, Hk, D), dtype), Hk * D, D
+        zero |= 2
+        made.append(k_out)
+    else:
+        ldko, hsko = _check_heads(k_out, "k_out", (T, Hk, D), dev, (dtype,))
+    at = B._at
     B.launch(dev, B.lib().asp_head_norm, q.data_ptr(), ldq, hsq, Hq, at(k), ldk, hsk, Hk,
-             _CODES[q.dtype], T, D, norm, at(q_weight), at(k_weight), eps, at(cos), at(sin), P, rot,
+             _CODES[x_dtype], T, D, norm, at(q_weight), at(k_weight), eps, at(cos), at(sin), P, rot,
              layout, at(positions), q_out.data_ptr(), ldqo, hsqo, at(k_out), ldko, hsko,
              _CODES[dtype], zero, B.stream_on(stream, dev))
-    _lend(stream, *made)
+    if stream is not None:
+        _lend(stream, *made)
     return q_out, k_out
 
 
@@ -168,59 +190,61 @@ def head_norm_backward(dq, dk, q, k=None, *, norm="rms", q_weight=None, k_weight
         Hk = k.shape[1]
     norm, layout, P, rot = _spec(T, D, dev, k is not None, norm, q_weight, k_weight, cos, sin,
                                  positions, layout)
-    wanted = HeadNormGrads(q, k, q_weight, k_weight)
+    want = (True, k is not None, q_weight is not None, k_weight is not None)
     if need is not None:
         need = tuple(need)
         for name in need:
-            if name not in HeadNormGrads._fields or getattr(wanted, name) is None:
+            if name not in HeadNormGrads._fields or not want[HeadNormGrads._fields.index(name)]:
                 raise ValueError(f"need names {name!r}: no gradient of a given input")
-        wanted = HeadNormGrads(*(t if name in need else None
-                                 for name, t in wanted._asdict().items()))
-    if dq_in is not None and wanted.dq is None or dk_in is not None and wanted.dk is None:
+        want = tuple(n in need for n in HeadNormGrads._fields)
+    want_q, want_k, want_qw, want_kw = want
+    if dq_in is not None and not want_q or dk_in is not None and not want_k:
         raise ValueError("a tensor for a gradient that is not wanted")
-    if all(t is None for t in wanted):
+    if not any(want):
         return HeadNormGrads(None, None, None, None)
-    lddq = hsdq = lddk = hsdk = 0
-    dtype, side_q, side_k = None, wanted.dq is not None or wanted.q_weight is not None, \
-        wanted.dk is not None or wanted.k_weight is not None
-    if side_q:
+    lddq = hsdq = lddk = hsdk = lddqi = hsdqi = lddki = hsdki = zero = 0
+    dtype, x_dtype, made = None, q.dtype, []
+    # the gradients of a side's result are read where one of its inputs' is wanted
+    pq = pk = d_qw = d_kw = None
+    if want_q or want_qw:
         lddq, hsdq = _check_heads(dq, "dq", (T, Hq, D), dev)
-        dtype = dq.dtype
-    if side_k:
+        dtype, pq = dq.dtype, dq.data_ptr()
+    if want_k or want_kw:
         lddk, hsdk = _check_heads(dk, "dk", (T, Hk, D), dev, _CODES if dtype is None else (dtype,))
-        dtype = dk.dtype
-    made, zero = [], 0
-
-    def new(shape, kind=torch.float32):
-        made.append(_new(stream, dev, shape, kind))
-        return made[-1]
-
-    def output(t, name, like, heads, bit):
-        nonlocal zero
-        if like is None:
-            return None, 0, 0
-        if t is None:
-            zero |= bit
-            return new((T, heads, D), q.dtype), heads * D, D
-        return (t, *_check_heads(t, name, (T, heads, D), dev, (q.dtype,)))
-
-    dq_in, lddqi, hsdqi = output(dq_in, "dq_in", wanted.dq, Hq, 1)
-    dk_in, lddki, hsdki = output(dk_in, "dk_in", wanted.dk, Hk, 2)
-    d_qw = None if wanted.q_weight is None else new(D)
-    d_kw = None if wanted.k_weight is None else new(D)
-    if d_qw is not None or d_kw is not None:
+        dtype, pk = dk.dtype, dk.data_ptr()
+    if dq_in is not None:
+        lddqi, hsdqi = _check_heads(dq_in, "dq_in", (T, Hq, D), dev, (x_dtype,))
+    elif want_q:
+        dq_in, lddqi, hsdqi, zero = _make(q, stream, (T, Hq, D), x_dtype), Hq * D, D, 1
+        made.append(dq_in)
+    if dk_in is not None:
+        lddki, hsdki = _check_heads(dk_in, "dk_in", (T, Hk, D), dev, (x_dtype,))
+    elif want_k:
+        dk_in, lddki, hsdki = _make(q, stream, (T, Hk, D), x_dtype), Hk * D, D
+        zero |= 2
+        made.append(dk_in)
+    if want_qw or want_kw:
+        if want_qw and want_kw:
+            both = _new(stream, dev, (2, D))    # one allocation
+            d_qw, d_kw = both.unbind(0)
+        elif want_qw:
+            d_qw = both = _new(stream, dev, D)
+        else:
+            d_kw = both = _new(stream, dev, D)
+        made.append(both)
         size = B.asp_head_norm_backward_workspace_bytes(T, Hq, Hk, D)
         if workspace is None:
             workspace = _new(stream, dev, max(size, 256), torch.uint8)
-        _check_ws(workspace, size, dev)
+        else:
+            _check_ws(workspace, size, dev)
     at = B._at
-    B.launch(dev, B.lib().asp_head_norm_backward, at(dq) if side_q else None, lddq, hsdq,
-             at(dk) if side_k else None, lddk, hsdk, _CODES[dtype], q.data_ptr(), ldq, hsq, Hq, at(k),
-             ldk, hsk, Hk, _CODES[q.dtype], T, D, norm, at(q_weight), at(k_weight), eps, at(cos),
-             at(sin), P, rot, layout, at(positions), at(dq_in), lddqi, hsdqi, at(dk_in), lddki, hsdki,
-             zero, at(d_qw), at(d_kw), at(workspace), 0 if workspace is None else workspace.numel(),
-             B.stream_on(stream, dev))
-    _lend(stream, *made)
+    B.launch(dev, B.lib().asp_head_norm_backward, pq, lddq, hsdq, pk, lddk, hsdk, _CODES[dtype],
+             q.data_ptr(), ldq, hsq, Hq, at(k), ldk, hsk, Hk, _CODES[x_dtype], T, D, norm,
+             at(q_weight), at(k_weight), eps, at(cos), at(sin), P, rot, layout, at(positions),
+             at(dq_in), lddqi, hsdqi, at(dk_in), lddki, hsdki, zero, at(d_qw), at(d_kw),
+             at(workspace), 0 if workspace is None else workspace.numel(), B.stream_on(stream, dev))
+    if stream is not None:
+        _lend(stream, *made)
     return HeadNormGrads(dq_in, dk_in, d_qw, d_kw)
 
 
