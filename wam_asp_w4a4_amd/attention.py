@@ -18,8 +18,8 @@ import torch
 
 from . import binding as B
 from .fp8 import _CODES, _no_capture, _no_forward_mode
-from .heads import _check_heads
-from .layer import _Y_DTYPES, _check_ws, _lend, _made_for, _new
+from .heads import _check_heads, _make
+from .layer import _Y_DTYPES, _check_ws, _lend, _new
 
 
 class AttentionGrads(NamedTuple):
@@ -38,21 +38,25 @@ def _check_ints(t, name, size, device):
                          f"got {tuple(t.shape)} on {t.device}")
 
 
-def _aligned(t, name, st, sh):
-    """The kernels read 16 bytes at a time."""
-    if (st | sh) * t.element_size() % 16 or t.data_ptr() % 16:
+def _matrix(t, name, shape, device, dtypes):
+    """(address, token stride, head stride) of a (T, H, D) tensor that the kernels read 16
+    bytes at a time."""
+    st, sh = _check_heads(t, name, shape, device, dtypes)
+    at = t.data_ptr()
+    if (st | sh) & (7 if t.dtype is torch.bfloat16 else 3) or at & 15:
         raise ValueError(f"{name} must be 16-byte aligned, its token and head strides too; got "
                          f"strides {t.stride()}")
-    if t.shape[0] > 1 and st < t.shape[2]:
+    if st < shape[2] and t.shape[0] > 1:
         raise ValueError(f"the tokens of {name} must not overlap, got strides {t.stride()}")
+    return at, st, sh
 
 
 def _check_pair(first, second, device):
     """Offsets of the two sides: both or neither, G."""
+    if first is None and second is None:
+        return 1
     if (first is None) != (second is None):
         raise ValueError("the offsets of both sides belong together")
-    if first is None:
-        return 1
     _check_ints(first, "q_offsets", 0, device)
     _check_ints(second, "kv_offsets", first.shape[0], device)
     return first.shape[0] - 1
@@ -97,7 +101,16 @@ class Nvfp4Cache:
 
     def check(self):
         """The four tensors belong together."""
-        kc = self.k_codes
+        kc, ks, vc, vs = self.k_codes, self.k_scales, self.v_codes, self.v_scales
+        if isinstance(kc, torch.Tensor) and isinstance(ks, torch.Tensor) \
+                and isinstance(vc, torch.Tensor) and isinstance(vs, torch.Tensor) \
+                and kc.dtype is ks.dtype is vc.dtype is vs.dtype is torch.uint8:
+            have = kc.shape
+            if len(have) == 3 and have[1] > 0 and have[2] & 7 == 0 and 8 <= have[2] <= 64 \
+                    and vc.shape == have and ks.shape == (have[0], have[1], have[2] >> 3) == vs.shape \
+                    and kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() \
+                    and vs.is_contiguous() and kc.device == ks.device == vc.device == vs.device:
+                return
         for t in (kc, self.k_scales, self.v_codes, self.v_scales):
             if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
                 raise TypeError("codes and scales must be uint8 tensors")
@@ -136,7 +149,8 @@ class Nvfp4Cache:
         offsets: one sequence of all tokens and rows.  The lengths are the caller's to
         advance (and then say ``attention`` how many keys count)."""
         self.check()
-        dev, Hk, D = self.device, self.heads, self.head_dim
+        rows, Hk, half = self.k_codes.shape
+        dev, D = self.k_codes.device, 2 * half
         ldk, hsk = _check_heads(k, "k", (None, Hk, D), dev)
         ldv, hsv = _check_heads(v, "v", (k.shape[0], Hk, D), dev, (k.dtype,))
         if (offsets is None) != (kv_offsets is None):
@@ -151,21 +165,21 @@ class Nvfp4Cache:
         at = B._at
         B.launch(dev, B.lib().asp_kv_store, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv,
                  _CODES[k.dtype], k.shape[0], Hk, D, G, at(offsets), at(kv_offsets), at(kv_lengths),
-                 self.rows, at(self.k_codes), at(self.k_scales), at(self.v_codes),
-                 at(self.v_scales), B.stream_on(stream, dev))
+                 rows, at(self.k_codes), at(self.k_scales), at(self.v_codes), at(self.v_scales),
+                 B.stream_on(stream, dev))
 
     def dequantize(self, dtype="f32", stream=None):
         """(k, v): the cache's values, (rows, Hk, D) float32 or bf16, which hold them exactly."""
         self.check()
         if dtype not in _Y_DTYPES:
             raise ValueError(f"dtype must be 'f32' or 'bf16', not {dtype!r}")
-        dev = self.device
-        k, v = (_new(stream, dev, (self.rows, self.heads, self.head_dim), _Y_DTYPES[dtype])
-                for _ in range(2))
+        rows, Hk, half = self.k_codes.shape
+        dev, shape = self.k_codes.device, (rows, Hk, 2 * half)
+        k, v = _new(stream, dev, shape, _Y_DTYPES[dtype]), _new(stream, dev, shape, _Y_DTYPES[dtype])
         at = B._at
         B.launch(dev, B.lib().asp_kv_load, at(self.k_codes), at(self.k_scales), at(self.v_codes),
-                 at(self.v_scales), self.rows, self.heads, self.head_dim, at(k), at(v),
-                 B.DTYPES[dtype], B.stream_on(stream, dev))
+                 at(self.v_scales), rows, Hk, 2 * half, at(k), at(v), B.DTYPES[dtype],
+                 B.stream_on(stream, dev))
         _lend(stream, k, v)
         return k, v
 
@@ -187,60 +201,60 @@ def attention(q, k, v=None, *, scale=None, q_offsets=None, kv_offsets=None, kv_l
         raise ValueError("q must be a 3-D torch tensor, (T, H, D)")
     Tq, Hq, D = q.shape
     dev = q.device
-    ldq, hsq = _check_heads(q, "q", (Tq, Hq, D), dev)
-    _aligned(q, "q", ldq, hsq)
+    dtype = q.dtype
+    pq = _matrix(q, "q", (Tq, Hq, D), dev, _CODES)
+    same = (dtype,)
     cached = isinstance(k, Nvfp4Cache)
     if cached:
         if v is not None:
             raise ValueError("v with a cache")
         k.check()
-        if k.device != dev or k.head_dim != D:
+        Tk, Hk, half = k.k_codes.shape
+        if k.k_codes.device != dev or 2 * half != D:
             raise ValueError(f"the cache has heads of {k.head_dim} on {k.device}, q of {D} on {dev}")
-        Tk, Hk = k.rows, k.heads
     else:
-        ldk, hsk = _check_heads(k, "k", (None, None, D), dev, (q.dtype,))
-        Tk, Hk = k.shape[:2]
-        ldv, hsv = _check_heads(v, "v", (Tk, Hk, D), dev, (q.dtype,))
-        _aligned(k, "k", ldk, hsk)
-        _aligned(v, "v", ldv, hsv)
+        pk = _matrix(k, "k", (None, None, D), dev, same)
+        Tk, Hk, _ = k.shape
+        pv = _matrix(v, "v", (Tk, Hk, D), dev, same)
     if Hk < 1 or Hq < 1 or Hq % Hk:
         raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
     G = _check_pair(q_offsets, kv_offsets, dev)
-    _check_keys(Tk, G, dev, kv_lengths, key_mask)
-    scale = _scale(scale, D)
+    if kv_lengths is not None or key_mask is not None:
+        _check_keys(Tk, G, dev, kv_lengths, key_mask)
+    scale = D ** -0.5 if scale is None else _scale(scale, D)
     made, zero = [], 0
     if o is None:
-        o = _new(stream, dev, (Tq, Hq, D), q.dtype)
+        o = _make(q, stream, (Tq, Hq, D), dtype)
         made.append(o)
-        zero, ldo, hso = 1, Hq * D, D
+        zero, po = 1, (o.data_ptr(), Hq * D, D)
     else:
-        ldo, hso = _check_heads(o, "o", (Tq, Hq, D), dev, (q.dtype,))
-        _aligned(o, "o", ldo, hso)
+        po = _matrix(o, "o", (Tq, Hq, D), dev, same)
     if lse is None:
-        lse = _new(stream, dev, (Tq, Hq))
+        lse = _make(q, stream, (Tq, Hq), torch.float32)
         made.append(lse)
         zero |= 2
     elif not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
         raise TypeError("lse must be a float32 tensor")
     elif lse.shape != (Tq, Hq) or lse.device != dev or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous ({Tq}, {Hq}) on {dev}")
-    need = B.asp_attention_workspace_bytes(Tq, Tk, Hq, Hk, D, G)
+    need, have, ws = B.asp_attention_workspace_bytes(Tq, Tk, Hq, Hk, D, G), 0, None
     if workspace is not None:
         _check_ws(workspace, need, dev)
+        have, ws = workspace.numel(), workspace.data_ptr()
     elif need:
         workspace = _new(stream, dev, need, torch.uint8)
+        have, ws = need, workspace.data_ptr()
     at = B._at
-    ws, have = at(workspace), 0 if workspace is None else workspace.numel()
-    tail = (at(q_offsets), at(kv_offsets), at(kv_lengths), at(key_mask), o.data_ptr(), ldo, hso,
-            lse.data_ptr(), zero, ws, have, B.stream_on(stream, dev))
+    tail = (at(q_offsets), at(kv_offsets), at(kv_lengths), at(key_mask), *po, lse.data_ptr(), zero,
+            ws, have, B.stream_on(stream, dev))
     if cached:
-        B.launch(dev, B.lib().asp_attention_cache, q.data_ptr(), ldq, hsq, _CODES[q.dtype],
-                 at(k.k_codes), at(k.k_scales), at(k.v_codes), at(k.v_scales), Tq, Tk, Hq, Hk, D,
-                 scale, G, *tail)
+        B.launch(dev, B.lib().asp_attention_cache, *pq, _CODES[dtype], at(k.k_codes), at(k.k_scales),
+                 at(k.v_codes), at(k.v_scales), Tq, Tk, Hq, Hk, D, scale, G, *tail)
     else:
-        B.launch(dev, B.lib().asp_attention, q.data_ptr(), ldq, hsq, k.data_ptr(), ldk, hsk,
-                 v.data_ptr(), ldv, hsv, _CODES[q.dtype], Tq, Tk, Hq, Hk, D, scale, G, *tail)
-    _lend(stream, *made)
+        B.launch(dev, B.lib().asp_attention, *pq, *pk, *pv, _CODES[dtype], Tq, Tk, Hq, Hk, D, scale,
+                 G, *tail)
+    if stream is not None:
+        _lend(stream, *made)
     return o, lse
 
 
@@ -258,17 +272,12 @@ def attention_backward(do, q, k, v, o, lse, *, scale=None, q_offsets=None, kv_of
     if isinstance(k, Nvfp4Cache):
         raise TypeError("a cache has no gradients")
 
-    def strides(t, name, shape, dtypes=same):
-        s = _check_heads(t, name, shape, dev, dtypes)
-        _aligned(t, name, *s)
-        return s
-
-    sq = strides(q, "q", (Tq, Hq, D), _CODES)
-    sk = strides(k, "k", (None, None, D))
-    Tk, Hk = k.shape[:2]
-    sv = strides(v, "v", (Tk, Hk, D))
-    so = strides(o, "o", (Tq, Hq, D))
-    sdo = strides(do, "do", (Tq, Hq, D))
+    pq = _matrix(q, "q", (Tq, Hq, D), dev, _CODES)
+    pk = _matrix(k, "k", (None, None, D), dev, same)
+    Tk, Hk, _ = k.shape
+    pv = _matrix(v, "v", (Tk, Hk, D), dev, same)
+    po = _matrix(o, "o", (Tq, Hq, D), dev, same)
+    pdo = _matrix(do, "do", (Tq, Hq, D), dev, same)
     if Hk < 1 or Hq < 1 or Hq % Hk:
         raise ValueError(f"{Hq} query heads are not a multiple of {Hk} key heads")
     if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32:
@@ -276,42 +285,50 @@ def attention_backward(do, q, k, v, o, lse, *, scale=None, q_offsets=None, kv_of
     if lse.shape != (Tq, Hq) or lse.device != dev or not lse.is_contiguous():
         raise ValueError(f"lse must be contiguous ({Tq}, {Hq}) on {dev}")
     G = _check_pair(q_offsets, kv_offsets, dev)
-    _check_keys(Tk, G, dev, kv_lengths, key_mask)
-    scale = _scale(scale, D)
-    names = AttentionGrads._fields
-    need = names if need is None else tuple(need)
-    for name in need:
-        if name not in names:
-            raise ValueError(f"need names {name!r}: no gradient")
-    given = dict(dq=dq, dk=dk, dv=dv)
-    for name, t in given.items():
-        if t is not None and name not in need:
+    if kv_lengths is not None or key_mask is not None:
+        _check_keys(Tk, G, dev, kv_lengths, key_mask)
+    scale = D ** -0.5 if scale is None else _scale(scale, D)
+    want_q = want_k = want_v = True
+    if need is not None:
+        need = tuple(need)
+        for name in need:
+            if name not in AttentionGrads._fields:
+                raise ValueError(f"need names {name!r}: no gradient")
+        want_q, want_k, want_v = (n in need for n in AttentionGrads._fields)
+        if dq is not None and not want_q or dk is not None and not want_k \
+                or dv is not None and not want_v:
             raise ValueError("a tensor for a gradient that need does not name")
-    if not need:
-        return AttentionGrads(None, None, None)
-    made, zero, out = [], 0, []
-    for bit, (name, shape) in enumerate(zip(names, ((Tq, Hq, D), (Tk, Hk, D), (Tk, Hk, D)))):
-        t = given[name]
-        if name not in need:
-            out += [None, 0, 0]
-        elif t is None:
-            given[name] = t = _new(stream, dev, shape, q.dtype)
-            made.append(t)
-            zero |= 1 << bit
-            out += [t.data_ptr(), shape[1] * D, D]
-        else:
-            out += [t.data_ptr(), *strides(t, name, shape)]
+        if not need:
+            return AttentionGrads(None, None, None)
+    made, zero, none = [], 0, (None, 0, 0)
+
+    def output(t, want, name, T, H, bit):
+        nonlocal zero
+        if t is not None:
+            return (t, *_matrix(t, name, (T, H, D), dev, same))
+        if not want:
+            return (None, *none)
+        t = _make(q, stream, (T, H, D), q.dtype)
+        made.append(t)
+        zero |= bit
+        return t, t.data_ptr(), H * D, D
+
+    dq, *pdq = output(dq, want_q, "dq", Tq, Hq, 1)
+    dk, *pdk = output(dk, want_k, "dk", Tk, Hk, 2)
+    dv, *pdv = output(dv, want_v, "dv", Tk, Hk, 4)
     size = B.asp_attention_backward_workspace_bytes(Tq, Tk, Hq, Hk, D, G)
     if workspace is None:
         workspace = _new(stream, dev, size, torch.uint8)
-    _check_ws(workspace, size, dev)
+    else:
+        _check_ws(workspace, size, dev)
     at = B._at
-    B.launch(dev, B.lib().asp_attention_backward, do.data_ptr(), *sdo, q.data_ptr(), *sq, k.data_ptr(),
-             *sk, v.data_ptr(), *sv, o.data_ptr(), *so, lse.data_ptr(), _CODES[q.dtype], Tq, Tk, Hq, Hk,
-             D, scale, G, at(q_offsets), at(kv_offsets), at(kv_lengths), at(key_mask), *out, zero,
-             workspace.data_ptr(), workspace.numel(), B.stream_on(stream, dev))
-    _lend(stream, *made)
-    return AttentionGrads(*given.values())
+    B.launch(dev, B.lib().asp_attention_backward, *pdo, *pq, *pk, *pv, *po, lse.data_ptr(),
+             _CODES[q.dtype], Tq, Tk, Hq, Hk, D, scale, G, at(q_offsets), at(kv_offsets),
+             at(kv_lengths), at(key_mask), *pdq, *pdk, *pdv, zero, workspace.data_ptr(),
+             workspace.numel(), B.stream_on(stream, dev))
+    if stream is not None:
+        _lend(stream, *made)
+    return AttentionGrads(dq, dk, dv)
 
 
 def _readable(t):

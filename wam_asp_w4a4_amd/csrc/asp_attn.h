@@ -42,8 +42,9 @@ struct AttnArgs {
   const uint8_t* mask;                     // [Tk]
   int64_t Tq, Tk;
   int Hq, Hk, group, D, G, slots, zero;
+  int heads;      // workgroups side by side: the key heads, or groups of them
   int splits;     // workgroups that may share one range of rows that go by,
-  int64_t chunk;  // which is split from so many on
+  uint32_t chunk; // which is split from so many on
   float scale;
   float* part;    // [splits][Tq][Hq][D]
   float* part_l;  // [splits][Tq][Hq]
@@ -61,10 +62,15 @@ struct AttnArgs {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_rows(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
-__device__ __forceinline__ void attn_copy(__amdgpu_buffer_rsrc_t r, int offset, void* lds_base) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds_base, 16,
+// 16 bytes a lane from the descriptor's bytes to LDS: lane l's land at `base` (uniform) + 16 l.  The
+// compiler waits for all copies in flight before a transposing read; the same copies in
+// assembly, without that wait, were no faster (8192 x 8192, 16 heads of 128: 546 us for
+// 541; dk and dv of 4096 x 4096 420 for 339, whose copies are then not moved between the products).
+__device__ __forceinline__ void attn_copy(__amdgpu_buffer_rsrc_t r, int offset, void* base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)base, 16,
                                            offset, 0, 0, 0);
 }
+
 // What takes a score to the exponent of 2.  It never becomes 0: minus infinity, a key that does not
 // count, has to stay that.
 constexpr float kLeast = 1.17549435e-38f;
@@ -86,10 +92,12 @@ __device__ __forceinline__ float both_halves(float x, F&& f) {
   return f(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 
-// A tile of rows in LDS: DT * 32 elements of ES bytes
+// A tile of rows in LDS: DT * 32 elements of ES bytes, USED pairs of pieces (three tiles of columns
+// lie in the room of four)
 template <int ES, int DT>
 struct Rows {
-  static constexpr int BYTES = DT * 32 * ES, PIECES = BYTES / 16;
+  static constexpr int BYTES = (DT == 3 ? 4 : DT) * 32 * ES, PIECES = BYTES / 16;
+  static constexpr int USED = DT * ES;
   static_assert(PIECES % 8 == 0, "the swizzle permutes eight or sixteen pieces");
   static __device__ __forceinline__ int swizzle(int row) {
     return PIECES == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : (row & 3) << 2 | (row >> 2 & 3);
@@ -271,6 +279,37 @@ __device__ __forceinline__ int64_t attn_offset(const int32_t* o, int g, int64_t 
   return min(max((int64_t)o[g], (int64_t)0), total);
 }
 
+// XCD-aware order: consecutive workgroups go to the 8 XCDs in turn.  Sequences of one length: each
+// XCD takes one contiguous run, so that the tiles of a head, which read the same keys, share an
+// L2.  Ragged ones: runs of kRaggedRun in turn, since the long sequences of a head would all be one
+// XCD's (the backward of 8192 queries in 4 sequences of 878 to 5506, 16 heads of 128, 4 of the
+// keys: 962 us, so 639).  The grid is then a multiple of 8 runs, and ids past the last
+// have no work.
+constexpr int kRaggedRun = 8;
+__device__ __forceinline__ uint32_t attn_run(uint32_t id, uint32_t total, bool ragged) {
+  const uint32_t xcd = id % 8, at = id / 8;
+  if (ragged) return (at / kRaggedRun * 8 + xcd) * kRaggedRun + at % kRaggedRun;
+  return xcd * (total / 8) + min(xcd, total % 8) + at;
+}
+
+// This workgroup's place: a tile of rows, a head of the keys and a part of what goes by.  The later
+// parts, which shorter sequences do not have, come last; heads_first: the heads of one tile follow
+// one another, else the tiles of one head.
+struct AttnPlace {
+  int slot, hk, split;
+};
+
+template <bool HEADS_FIRST = false>
+__device__ __forceinline__ bool attn_place(const AttnArgs& a, bool ragged, AttnPlace& p) {
+  const uint32_t run = attn_run(blockIdx.x, gridDim.x, ragged), slots = a.slots, heads = a.heads;
+  const uint32_t outer = HEADS_FIRST ? slots : heads, inner = HEADS_FIRST ? heads : slots;
+  const uint32_t by = run / inner, split = by / outer;
+  p.slot = (int)(HEADS_FIRST ? by - split * outer : run - by * inner);
+  p.hk = (int)(HEADS_FIRST ? run - by * inner : by - split * outer);
+  p.split = (int)split;
+  return split < (uint32_t)a.splits;
+}
+
 // Which sequence and tile a slot stands for.  Rows of `per` tiles: a sequence's first slot is
 // (its first row) / tile + g, which leaves each sequence enough slots and none to two.  The
 // wave searches 64 sequences at a time.  Offsets that are out of range or decrease give
@@ -283,7 +322,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* of
   s.any = true;
   if (offsets) {
     auto first = [&](int i) {
-      return (int64_t)((uint64_t)(attn_offset(offsets, i, total) * group) / (uint32_t)tile_rows) + i;
+      return (int64_t)((uint32_t)(attn_offset(offsets, i, total) * group) / (uint32_t)tile_rows) + i;
     };
     const int lane = threadIdx.x & 63;
     int n = a.G;
@@ -299,7 +338,9 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* of
       n = step > 1 ? min(step, n - (count - 1) * step) : 0;
     }
     g = __builtin_amdgcn_readfirstlane(g);
+    // (offsets that decrease may have led to a sequence whose first slot is behind this one)
     if (s.any) s.tile = slot - first(g);
+    if (s.tile < 0) s.any = false;
   }
   s.q0 = a.qo ? attn_offset(a.qo, g, a.Tq) : 0;
   s.rows = (a.qo ? attn_offset(a.qo, g + 1, a.Tq) : a.Tq) - s.q0;
@@ -312,7 +353,13 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* of
 
 // How many workgroups share `passed` rows
 __device__ __forceinline__ int attn_parts(const AttnArgs& a, int64_t passed) {
-  return a.splits == 1 ? 1 : (int)min(max((passed + a.chunk - 1) / a.chunk, (int64_t)1), (int64_t)a.splits);
+  return a.splits == 1 ? 1 : (int)min(max(((uint32_t)passed + a.chunk - 1) / a.chunk, 1u), (uint32_t)a.splits);
+}
+
+// The first of `tiles` that part `split` of `parts` has
+__device__ __forceinline__ int64_t attn_part(int64_t tiles, int split, int parts) {
+  const uint32_t each = (uint32_t)tiles / (uint32_t)parts, more = (uint32_t)tiles - each * parts;
+  return (int64_t)each * split + min((uint32_t)split, more);
 }
 
 // The sequence of a token inside the offsets: the last that begins at or before it.  A wave looks at
@@ -335,24 +382,11 @@ __device__ __forceinline__ int64_t attn_keys(const AttnArgs& a, int g) {
   return max(a.kl ? min(all, (int64_t)a.kl[g]) : all, (int64_t)0);
 }
 
-// XCD-aware order: consecutive workgroups go to the 8 XCDs in turn.  Sequences of one length: each
-// XCD takes one contiguous run, so that the tiles of a head, which read the same keys, share an
-// L2.  Ragged ones: runs of kRaggedRun in turn, since the long sequences of a head would all be one
-// XCD's (the backward of 8192 queries in 4 sequences of 878 to 5506, 16 heads of 128, 4 of the
-// keys: 962 us, so 639).  The grid is then a multiple of 8 runs, and ids past the last
-// have no work.
-constexpr int kRaggedRun = 8;
-__device__ __forceinline__ int64_t attn_run(uint32_t id, uint32_t total, bool ragged) {
-  const uint32_t xcd = id % 8, at = id / 8;
-  if (ragged) return ((int64_t)(at / kRaggedRun) * 8 + xcd) * kRaggedRun + at % kRaggedRun;
-  return (int64_t)xcd * (total / 8) + min(xcd, total % 8) + at;
-}
-
 // Rows of no sequence: f(token) for the tokens outside the offsets, a share for each slot
 template <typename F>
 __device__ __forceinline__ void attn_outside(const int32_t* offsets, int G, int64_t total, int slot,
                                              int slots, F&& f) {
-  const int64_t share = (total + slots - 1) / slots, t0 = slot * share, t1 = min(t0 + share, total);
+  const int64_t share = ((uint32_t)total + slots - 1u) / (uint32_t)slots, t0 = slot * share, t1 = min(t0 + share, total);
   const int64_t in0 = attn_offset(offsets, 0, total), in1 = attn_offset(offsets, G, total);
   for (int64_t t = t0; t < t1; ++t) {
     if (t >= in0 && t < in1)
@@ -400,6 +434,9 @@ inline int32_t check_attn(int32_t dtype, int64_t Tq, int64_t Tk, int32_t Hq, int
     return fail(ASP_ERR_SHAPE, "D=%d is not a multiple of 8 in [8, %d]", D, kMaxAttnD);
   if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
   if (!(scale > 0.0f) || !(scale < 3.0e38f)) return fail(ASP_ERR_ARG, "scale=%g", scale);
+  if (Tq * Hq > INT32_MAX || Tk * Hk > INT32_MAX)
+    return fail(ASP_ERR_SHAPE, "%lld x %d or %lld x %d heads are not below 2^31", (long long)Tq, Hq,
+                (long long)Tk, Hk);
   if ((!qo || !ko) && G != 1)
     return fail(ASP_ERR_ARG, "offsets are NULL with G=%d sequences", G);
   if ((uintptr_t)qo & 3 || (uintptr_t)ko & 3 || (uintptr_t)kl & 3)
@@ -415,7 +452,7 @@ inline int32_t check_attn_grid(int64_t blocks, int threads) {
 
 // workgroups of a launch: see attn_run
 inline int64_t attn_grid(const AttnArgs& a, bool ragged) {
-  const int64_t total = (int64_t)a.slots * a.splits * a.Hk, step = 8 * kRaggedRun;
+  const int64_t total = (int64_t)a.slots * a.splits * a.heads, step = 8 * kRaggedRun;
   return ragged ? (total + step - 1) / step * step : total;
 }
 
@@ -425,7 +462,7 @@ inline int64_t attn_grid(const AttnArgs& a, bool ragged) {
 struct AttnPlan {
   bool wide;
   int tile, slots, splits;
-  int64_t chunk;
+  uint32_t chunk;
 };
 
 inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged) {
@@ -439,12 +476,12 @@ inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, b
   // A range is split where that makes so many workgroups, and ragged sequences more, since the longest
   // would be alone at the end; but from `least` rows on only, since a part's result is written
   // and read again in float32.
-  const int64_t target = G > 1 ? 1024 : p.wide ? 0 : 512, least = p.wide ? 1024 : 256;
-  const int64_t most = p.wide ? 8 : std::min<int64_t>(64, 4 * target / blocks);
+  const int64_t target = G > 1 ? 1024 : p.wide ? 0 : 512, least = p.wide ? 1024 : 512;
+  const int64_t most = p.wide ? 8 : std::min<int64_t>(512, 4 * target / blocks);
   p.splits = 1;
-  p.chunk = passed + 1;
+  p.chunk = (uint32_t)passed + 1u;
   if (blocks < target && (p.wide || blocks < 256)) {
-    p.chunk = std::max(least, (by * blocks + target - 1) / target);
+    p.chunk = (uint32_t)std::max(least, (by * blocks + target - 1) / target);
     p.splits = (int)std::max<int64_t>(1, std::min((passed + p.chunk - 1) / p.chunk, most));
   }
   return p;

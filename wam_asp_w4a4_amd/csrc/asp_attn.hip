@@ -29,13 +29,149 @@ struct Forward {
   using R = Rows<P::ES, DT>;
   static constexpr int THREADS = 64 * WM * WK, BM = 32 * NQ * WM, BN = 32 * KT;
   static constexpr int TILE = BN * R::BYTES;                // K or V
-  static constexpr int BUFFERS = Q4 ? 1 : 2;
+  // one buffer where two would leave half of the columns: rows of 512 bytes
+  static constexpr int BUFFERS = Q4 || (WM == 1 && R::BYTES == 512) ? 1 : 2;
   static constexpr int GROUP = 2 * TILE * BUFFERS;          // of one of the WK columns
   static constexpr int STATE = 4 * 64 * (16 * DT + 2) * NQ;  // a wave's o, m and l
   static constexpr int JOIN = (WK - 1) * WM * STATE;
   static constexpr int LDS = WK * GROUP > JOIN ? WK * GROUP : JOIN;
   static_assert(LDS <= 160 * 1024, "a CU has 160 KB of LDS");
 };
+
+// Scores of KT tiles of 32 keys for the lane's query become the weights 2^(c s - m)
+template <int DT, int KT>
+__device__ __forceinline__ void softmax_step(f32x16_t (&s)[KT], float c, float& m, float& l,
+                                             f32x16_t (&acc)[DT]) {
+  float top = kNegInf;
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) top = fmaxf(top, s[k][v]);
+  top = both_halves(top, [](float x, float y) { return fmaxf(x, y); }) * c;
+  if (__any(top > m + kRaise)) {
+    const float up = fmaxf(m, top);
+    const float f = up == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+    m = up;
+    l *= f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[dt][v] *= f;
+  }
+  const float off = m == kNegInf ? 0.0f : m;
+#pragma unroll
+  for (int k = 0; k < KT; ++k)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      s[k][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][v], c, -off));
+      l += s[k][v];
+    }
+}
+
+// Joins the results of WK columns of waves in LDS, whose tiles are no longer needed: column 0 has
+// them (false: another's wave, which is done).
+template <int DT, int NQ, int WM, int WK>
+__device__ __forceinline__ bool join_columns(uint8_t* smem, int wk, int wm, int lane, float (&m)[NQ],
+                                             float (&l)[NQ], f32x16_t (&acc)[NQ][DT]) {
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) l[n] = both_halves(l[n], [](float x, float y) { return x + y; });
+  if constexpr (WK > 1) {
+    __syncthreads();
+    float* at = reinterpret_cast<float*>(smem) + lane;
+    constexpr int EACH = 16 * DT + 2;  // values of a lane for each of its NQ rows
+    if (wk > 0) {
+      float* to = at + ((wk - 1) * WM + wm) * NQ * EACH * 64;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) to[(n * EACH + 16 * dt + v) * 64] = acc[n][dt][v];
+        to[(n * EACH + 16 * DT) * 64] = m[n];
+        to[(n * EACH + 16 * DT + 1) * 64] = l[n];
+      }
+    }
+    __syncthreads();
+    if (wk > 0) return false;
+#pragma unroll
+    for (int w = 0; w < WK - 1; ++w) {
+      const float* from = at + (w * WM + wm) * NQ * EACH * 64;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float m2 = from[(n * EACH + 16 * DT) * 64], l2 = from[(n * EACH + 16 * DT + 1) * 64];
+        const float up = fmaxf(m[n], m2), off = up == kNegInf ? 0.0f : up;
+        const float f = __builtin_amdgcn_exp2f(m[n] - off), f2 = __builtin_amdgcn_exp2f(m2 - off);
+        l[n] = l[n] * f + l2 * f2;
+        m[n] = up;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            acc[n][dt][v] = __builtin_fmaf(acc[n][dt][v], f, from[(n * EACH + 16 * dt + v) * 64] * f2);
+      }
+    }
+  }
+  return true;
+}
+
+// A query's result, or its part's
+template <typename XT, int DT>
+__device__ __forceinline__ void store_result(const AttnArgs& a, int parts, int split, int64_t token,
+                                             int head, int half, float m, float l,
+                                             const f32x16_t (&acc)[DT]) {
+  const bool none = l == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / l;
+  // the logarithm to base 2 of the row's sum
+  const float lg = none ? kNegInf : m + __builtin_amdgcn_logf(l);
+  const int64_t at = token * a.Hq + head;
+  if (parts > 1) {
+    const int64_t rows = a.Tq * a.Hq;
+    store_row<float, DT>(a.part + (split * rows + at) * a.D, acc, inv, a.D, half);
+    if (half == 0) a.part_l[split * rows + at] = lg;
+  } else {
+    store_row<XT, DT>(static_cast<XT*>(a.o) + token * a.ot + head * a.oh, acc, inv, a.D, half);
+    if (half == 0 && a.lse) a.lse[at] = lg * kLn2;
+  }
+}
+
+// Rows of no sequence: zeros and -infinity where they are asked for
+template <typename XT>
+__device__ __forceinline__ void clear_outside(const AttnArgs& a, int slot, int hk) {
+  attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
+    const int pieces = a.D * (int)sizeof(XT) / 16;
+    for (int i = threadIdx.x; i < a.group * pieces; i += blockDim.x) {
+      const int h = hk * a.group + i / pieces;
+      if (a.zero & 1)
+        *reinterpret_cast<u32x4_t*>(static_cast<XT*>(a.o) + t * a.ot + h * a.oh +
+                                    i % pieces * (16 / sizeof(XT))) = u32x4_t{0, 0, 0, 0};
+      if (a.zero & 2 && i % pieces == 0) a.lse[t * a.Hq + h] = kNegInf;
+    }
+  });
+}
+
+// The lane's query in fp16, which has eleven bits but a short range: the row is scaled by a power of two
+// so that its largest finite element is 2^13 to 2^14 (what then falls below fp16's normal
+// range is 2^-27 of that, below what float32 sums keep), and the factor c of its scores back.
+template <int QS>
+__device__ __forceinline__ void query_half(u32x4_t (&qf)[QS], float& c) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < QS; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      top = max(top, max(finite_bits(bf16_lo(qf[s][e])), finite_bits(bf16_hi(qf[s][e]))));
+  // bits of finite magnitudes: as integers in the order of the values
+  const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+  top = max((uint32_t)both[0], (uint32_t)both[1]);
+  const int e2 = min(127 + 13 - (int)(top >> 23), 126);  // 2^e2 times the row
+  const float up = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
+  c = fmaxf(c * __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23), kLeast);
+#pragma unroll
+  for (int s = 0; s < QS; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      qf[s][e] = Half::pair(bf16_lo(qf[s][e]) * up, bf16_hi(qf[s][e]) * up);
+}
 
 // eight codes and their scale as 16-bit or 32-bit values
 __device__ __forceinline__ u32x4_t decode_half(uint32_t w, _Float16 s) {
@@ -49,29 +185,17 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
   using P = typename F::P;
   using R = typename F::R;
   constexpr int BM = F::BM, BN = F::BN, TILE = F::TILE;
-  constexpr int QS = R::PIECES / 2;             // pieces of a query in each half of the wave
+  constexpr int QS = R::USED;                   // pieces of a query in each half of the wave
   __shared__ __attribute__((aligned(16))) uint8_t smem[F::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave % WM, wk = wave / WM;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.qo != nullptr);
-  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
-  // the later parts, which shorter sequences do not have, come last
-  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
-  const int split = (int)(run / a.slots / a.Hk);
+  AttnPlace place;
+  if (!attn_place(a, a.qo != nullptr, place)) return;
+  const int slot = place.slot, hk = place.hk, split = place.split;
   const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
 
-  if (a.zero && a.qo && split == 0)
-    attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
-      const int pieces = a.D * (int)sizeof(XT) / 16;
-      for (int i = threadIdx.x; i < a.group * pieces; i += F::THREADS) {
-        const int h = hk * a.group + i / pieces;
-        if (a.zero & 1)
-          *reinterpret_cast<u32x4_t*>(static_cast<XT*>(a.o) + t * a.ot + h * a.oh +
-                                      i % pieces * (16 / sizeof(XT))) = u32x4_t{0, 0, 0, 0};
-        if (a.zero & 2 && i % pieces == 0) a.lse[t * a.Hq + h] = kNegInf;
-      }
-    });
+  if (a.zero && a.qo && split == 0) clear_outside<XT>(a, slot, hk);
   const int64_t row0 = seq.tile * BM, rows = seq.rows * a.group;
   const int parts = attn_parts(a, seq.keys);
   if (!seq.any || row0 >= rows || split >= parts) return;
@@ -86,7 +210,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
   for (int n = 0; n < NQ; ++n) {
     const int64_t r = row0 + 32 * (wm * NQ + n) + l32;
     valid[n] = r < rows;
-    const int64_t t = a.group == 1 ? r : r / a.group;
+    const int64_t t = a.group == 1 ? r : (uint32_t)r / (uint32_t)a.group;
     token[n] = seq.q0 + t;
     head[n] = hk * a.group + (int)(r - t * a.group);
     c[n] = attn_factor(a.scale);
@@ -96,29 +220,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
       const int d = (2 * s + half) * (16 / P::ES);
       qf[n][s] = valid[n] && d < a.D ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
     }
-    if constexpr (std::is_same_v<P, Half>) {
-      // fp16 has eleven bits but a short range: the row is scaled by a power of two so that its
-      // largest finite element is 2^13 to 2^14; what then falls below fp16's
-      // normal range is 2^-27 of that, below what float32 sums keep
-      uint32_t top = 0;
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = max(top, max(finite_bits(bf16_lo(qf[n][s][e])), finite_bits(bf16_hi(qf[n][s][e]))));
-      top = __builtin_bit_cast(uint32_t, both_halves(__builtin_bit_cast(float, top), [](float x, float y) {
-                                return __builtin_bit_cast(float, max(__builtin_bit_cast(uint32_t, x),
-                                                                     __builtin_bit_cast(uint32_t, y)));
-                              }));
-      const int e2 = min(127 + 13 - (int)(top >> 23), 126);  // 2^e2 times the row
-      const float up = __builtin_bit_cast(float, (uint32_t)(127 + e2) << 23);
-      c[n] = fmaxf(c[n] * __builtin_bit_cast(float, (uint32_t)(127 - e2) << 23), kLeast);
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          qf[n][s][e] = P::pair(bf16_lo(qf[n][s][e]) * up, bf16_hi(qf[n][s][e]) * up);
-    }
+    if constexpr (std::is_same_v<P, Half>) query_half(qf[n], c[n]);
   }
 
   f32x16_t acc[NQ][DT];
@@ -135,7 +237,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
 
   // this workgroup's tiles of keys; each of its WK columns makes `turns`
   const int64_t tiles = (seq.keys + BN - 1) / BN;
-  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
+  const int64_t first = attn_part(tiles, split, parts), last = attn_part(tiles, split + 1, parts);
   const int turns = (int)((last - first + WK - 1) / WK);
   uint8_t* mine = smem + wk * F::GROUP;
   const int64_t base_row = seq.k0;
@@ -160,7 +262,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
     }
   auto issue = [&](int t, uint64_t live) {
     if constexpr (!Q4) {
-      uint8_t* to = mine + (t & 1) * 2 * TILE;
+      uint8_t* to = mine + (t & (F::BUFFERS - 1)) * 2 * TILE;
       const int64_t at = base_row + key0(t);
       const int64_t n = min((int64_t)BN, seq.keys - key0(t));  // rows of the tile; may be none
       const XT* kp = static_cast<const XT*>(a.k) + (n > 0 ? at * a.kt + hk * a.kh : 0);
@@ -179,15 +281,16 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
     }
   };
   // ---- blocks of a 4-bit tile, through registers
-  constexpr int BLOCKS = BN * DT * 2 / (64 * WM);  // a lane's of K, and as many of V
-  static_assert(!Q4 || BN * DT * 2 % (64 * WM) == 0, "whole blocks for each lane");
+  constexpr int ROW_BLOCKS = R::PIECES * 8 / P::ES / 8;  // blocks of 16 in a row's room
+  constexpr int BLOCKS = BN * ROW_BLOCKS / (64 * WM);  // a lane's of K, and as many of V
+  static_assert(!Q4 || BN * ROW_BLOCKS % (64 * WM) == 0, "whole blocks for each lane");
   u32x2_t ck[Q4 ? BLOCKS : 1], cv[Q4 ? BLOCKS : 1];
   uint32_t sk[Q4 ? BLOCKS : 1], sv[Q4 ? BLOCKS : 1];
   auto fetch = [&](int t, uint64_t live) {
     if constexpr (Q4) {
 #pragma unroll
       for (int i = 0; i < BLOCKS; ++i) {
-        const int b = (i * WM + wm) * 64 + lane, row = b / (2 * DT), blk = b % (2 * DT);
+        const int b = (i * WM + wm) * 64 + lane, row = b / ROW_BLOCKS, blk = b % ROW_BLOCKS;
         ck[i] = cv[i] = u32x2_t{0, 0};
         sk[i] = sv[i] = 0;
         if ((live >> row & 1) && 16 * blk < a.D) {
@@ -204,7 +307,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
     if constexpr (Q4) {
 #pragma unroll
       for (int i = 0; i < BLOCKS; ++i) {
-        const int b = (i * WM + wm) * 64 + lane, row = b / (2 * DT), blk = b % (2 * DT);
+        const int b = (i * WM + wm) * 64 + lane, row = b / ROW_BLOCKS, blk = b % ROW_BLOCKS;
         auto put = [&](uint8_t* tile, u32x2_t w, uint32_t code) {
           const float s = __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
           uint8_t* to = tile + row * R::BYTES;
@@ -235,7 +338,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
   issue(0, live);
   fetch(0, live);
   for (int t = 0; t < turns; ++t) {
-    const uint8_t* tile = mine + (Q4 ? 0 : (t & 1) * 2 * TILE);
+    const uint8_t* tile = mine + (t & (F::BUFFERS - 1)) * 2 * TILE;
     if constexpr (Q4) {
       attn_settle<(WM > 1)>();  // the tile before is read
       unpack4();
@@ -247,7 +350,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
       attn_settle<(WM > 1)>();  // tile t is there, and the one before is read
       next = __ballot(on != 0);
       on = key_on(t + 2);
-      if (t + 1 < turns) issue(t + 1, next);
+      if (F::BUFFERS > 1 && t + 1 < turns) issue(t + 1, next);
     }
     if (live != 0) {
       f32x16_t s[NQ][KT];
@@ -276,32 +379,7 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
               for (int n = 0; n < NQ; ++n) s[n][k][v] = kNegInf;
         }
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float top = kNegInf;
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) top = fmaxf(top, s[n][k][v]);
-        top = both_halves(top, [](float x, float y) { return fmaxf(x, y); }) * c[n];
-        if (__any(top > m[n] + kRaise)) {
-          const float up = fmaxf(m[n], top);
-          const float f = up == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - up);
-          m[n] = up;
-          l[n] *= f;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[n][dt][v] *= f;
-        }
-        const float off = m[n] == kNegInf ? 0.0f : m[n];
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            s[n][k][v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][k][v], c[n], -off));
-            l[n] += s[n][k][v];
-          }
-      }
+      for (int n = 0; n < NQ; ++n) softmax_step<DT, KT>(s[n], c[n], m[n], l[n], acc[n]);
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
 #pragma unroll
@@ -312,110 +390,276 @@ __global__ void __launch_bounds__((Forward<XT, DT, NQ, WM, WK, KT, Q4>::THREADS)
         }
       }
     }
+    if constexpr (!Q4 && F::BUFFERS == 1) {
+      attn_settle<(WM > 1)>();  // the tile is read
+      if (t + 1 < turns) issue(t + 1, next);
+    }
     live = next;
   }
 
+  if (!join_columns<DT, NQ, WM, WK>(smem, wk, wm, lane, m, l, acc)) return;
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) l[n] = both_halves(l[n], [](float x, float y) { return x + y; });
-  if constexpr (WK > 1) {
-    __syncthreads();  // the tiles are read
-    float* at = reinterpret_cast<float*>(smem) + lane;
-    constexpr int EACH = 16 * DT + 2;  // values of a lane for each of its NQ rows
-    if (wk > 0) {
-      float* to = at + ((wk - 1) * WM + wm) * NQ * EACH * 64;
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) to[(n * EACH + 16 * dt + v) * 64] = acc[n][dt][v];
-        to[(n * EACH + 16 * DT) * 64] = m[n];
-        to[(n * EACH + 16 * DT + 1) * 64] = l[n];
-      }
-    }
-    __syncthreads();
-    if (wk > 0) return;
-#pragma unroll
-    for (int w = 0; w < WK - 1; ++w) {
-      const float* from = at + (w * WM + wm) * NQ * EACH * 64;
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        const float m2 = from[(n * EACH + 16 * DT) * 64], l2 = from[(n * EACH + 16 * DT + 1) * 64];
-        const float up = fmaxf(m[n], m2), off = up == kNegInf ? 0.0f : up;
-        const float f = __builtin_amdgcn_exp2f(m[n] - off), f2 = __builtin_amdgcn_exp2f(m2 - off);
-        l[n] = l[n] * f + l2 * f2;
-        m[n] = up;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int v = 0; v < 16; ++v)
-            acc[n][dt][v] = __builtin_fmaf(acc[n][dt][v], f, from[(n * EACH + 16 * dt + v) * 64] * f2);
-      }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const bool none = l[n] == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / l[n];
-    // the logarithm to base 2 of the row's sum
-    const float lg = none ? kNegInf : m[n] + __builtin_amdgcn_logf(l[n]);
-    const int64_t at = token[n] * a.Hq + head[n];
-    if (!valid[n]) continue;
-    if (parts > 1) {
-      float* part = a.part + ((int64_t)split * a.Tq * a.Hq + at) * a.D;
-      store_row<float, DT>(part, acc[n], inv, a.D, half);
-      if (half == 0) a.part_l[(int64_t)split * a.Tq * a.Hq + at] = lg;
-    } else {
-      XT* o = static_cast<XT*>(a.o) + token[n] * a.ot + head[n] * a.oh;
-      store_row<XT, DT>(o, acc[n], inv, a.D, half);
-      if (half == 0 && a.lse) a.lse[at] = lg * kLn2;
-    }
-  }
+  for (int n = 0; n < NQ; ++n)
+    if (valid[n]) store_result<XT, DT>(a, parts, split, token[n], head[n], half, m[n], l[n], acc[n]);
 }
 
-// The splits' results of a query (at most 64), joined by their sums.  A wave has one query: its
-// lanes find the splits' weights, then four groups of 16 lanes take every fourth split, 8
-// elements a lane.
-template <typename XT>
+// The same for few queries over a 4-bit cache with heads of 64 or 128: 32 rows of HW neighbouring
+// heads a workgroup, a wave for each head, or several that take the tiles of 32 keys in turn.  The
+// waves of neighbouring heads read the same cache lines (a row of a head is 32 or 64 bytes
+// of them; a workgroup's waves at the keys of one head: 431 us for 2^20 keys of 16 heads of
+// 64).  A tile's codes and scales go to LDS as they are, two tiles ahead, lanes next to each
+// other in a row (a lane with a row of its own: 442 us for 2^20 keys of 8 heads of 128,
+// then 301).  A lane then has one key's DT / 2 pieces of 32 values (16 bytes of codes, 2 of
+// scales), of k and of v: k's are decoded to the left operand where they are, since the
+// contraction may take a row's pieces in that order and the queries are loaded in it; v's go
+// back to LDS in fp16, to be transposed.
+template <int DT, int HW>
+struct Few4 {
+  static constexpr int WK = 4 / HW;  // waves of a head
+  using R = Rows<2, DT>;
+  static constexpr int D = 32 * DT, N = DT / 2, ROW = D / 2, PLACES = ROW / 16;
+  static constexpr int CODES = 32 * ROW, COPIES = CODES / 1024, SCALES = 256;
+  static constexpr int STAGE = 2 * (CODES + SCALES), LOADS = 2 * (COPIES + 1);
+  static constexpr int WAVE = 2 * STAGE + 32 * R::BYTES;
+  static constexpr int JOIN = (4 - HW) * 64 * 4 * (16 * DT + 2);
+  static constexpr int LDS = 4 * WAVE > JOIN ? 4 * WAVE : JOIN;
+  // piece p of a row lies at place p ^ key: 16 rows at one piece fall in distinct banks
+  static __device__ __forceinline__ int key(int row) { return PLACES == 4 ? row >> 2 & 3 : row >> 3 & 1; }
+};
+
+// A copy as attn_copy's, in assembly: for the builtin the compiler waits for all copies in flight
+// before each transposing read, which here would be the memory's whole latency for each tile
+// (2^20 keys of 8 heads of 128: 300 us).  No register is written but m0, which nothing else
+// in the kernel uses; the loop waits for its copies by their number.
+template <int BYTES>
+__device__ __forceinline__ void few4_copy(u32x4_t rows, int offset, void* base) {
+  // the low half of a flat address of LDS is the place in it
+  const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)base);
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 ::"v"(offset), "s"(rows), "s"(to) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 ::"v"(offset), "s"(rows), "s"(to) : "memory");
+}
+__device__ __forceinline__ u32x4_t few4_rows(const void* p, int64_t bytes) {
+  const uint64_t at = (uint64_t)p;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)at),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+
+// MASK: there is a key mask, whose loads the compiler waits for, and all copies with them
+template <int DT, int HW, bool MASK>
+__global__ void __launch_bounds__(256, 2) k_attn_few4(const AttnArgs a) {
+  using F = Few4<DT, HW>;
+  using R = typename F::R;
+  constexpr int N = F::N;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[F::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  // the heads of the same keys share cache lines: they go to one XCD
+  AttnPlace place;
+  if (!attn_place<true>(a, a.qo != nullptr, place)) return;
+  const int slot = place.slot, split = place.split, wk = wave / HW;
+  const int hk = place.hk * HW + wave % HW;
+  const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, 32, slot);
+  if (a.zero && a.qo && split == 0)
+    for (int i = 0; i < HW; ++i) clear_outside<uint16_t>(a, slot, place.hk * HW + i);
+  const int64_t row0 = seq.tile * 32, rows = seq.rows * a.group;
+  const int parts = attn_parts(a, seq.keys);
+  if (!seq.any || row0 >= rows || split >= parts) return;
+
+  const int64_t tiles = (seq.keys + 31) / 32;
+  const int64_t first = attn_part(tiles, split, parts) + wk, last = attn_part(tiles, split + 1, parts);
+  const int turns = (int)max((last - first + F::WK - 1) / F::WK, (int64_t)0);
+  uint8_t* mine = smem + wave * F::WAVE;
+  uint8_t* tile = mine + 2 * F::STAGE;
+  // does the lane's key of this wave's tile t count
+  auto key_on = [&](int t) -> int {
+    const int64_t key = (first + (int64_t)F::WK * t) * 32 + l32;
+    const bool on = t < turns && key < seq.keys;
+    return on ? (MASK ? a.mask[seq.k0 + key] : 1) : 0;
+  };
+  const int row_codes = a.Hk * F::ROW, row_scales = a.Hk * (F::D / 16);
+  int off[F::COPIES], row_of[F::COPIES];
+#pragma unroll
+  for (int i = 0; i < F::COPIES; ++i) {
+    row_of[i] = (64 * i + lane) / F::PLACES;
+    off[i] = row_of[i] * row_codes + 16 * ((64 * i + lane) % F::PLACES ^ F::key(row_of[i]));
+  }
+  // dwords of scales: D / 64 a row
+  const int scale_row = lane / N;
+  const int scale_off = scale_row < 32 ? scale_row * row_scales + 4 * (lane % N) : kFar;
+  auto issue = [&](int t, uint32_t live) {
+    uint8_t* to = mine + (t & 1) * F::STAGE;
+    const int64_t key = (first + (int64_t)F::WK * t) * 32, at = seq.k0 + key;
+    const int64_t n = t < turns ? min((int64_t)32, seq.keys - key) : 0;
+    const int64_t oc = n > 0 ? at * row_codes + hk * F::ROW : 0, nc = n > 0 ? (n - 1) * row_codes + F::ROW : 0;
+    const int64_t os = n > 0 ? at * row_scales + hk * (F::D / 16) : 0;
+    const int64_t ns = n > 0 ? (n - 1) * row_scales + F::D / 16 : 0;
+    const u32x4_t kc = few4_rows(a.kc + oc, nc), vc = few4_rows(a.vc + oc, nc);
+    const u32x4_t ks = few4_rows(a.ks + os, ns), vs = few4_rows(a.vs + os, ns);
+    // a masked key's values would meet a weight of 0, and make NaN of NaN
+    auto of = [&](int row, int offset) { return MASK && !(live >> (row & 31) & 1) ? kFar : offset; };
+#pragma unroll
+    for (int i = 0; i < F::COPIES; ++i) {
+      few4_copy<16>(kc, off[i], to + i * 1024);
+      few4_copy<16>(vc, of(row_of[i], off[i]), to + F::CODES + i * 1024);
+    }
+    few4_copy<4>(ks, scale_off, to + 2 * F::CODES);
+    few4_copy<4>(vs, of(scale_row, scale_off), to + 2 * F::CODES + F::SCALES);
+  };
+
+  int on = key_on(0), on1 = key_on(1);
+  uint32_t live[2];
+  live[0] = (uint32_t)__ballot(on != 0);
+  live[1] = (uint32_t)__ballot(on1 != 0);
+  issue(0, live[0]);
+  on = key_on(2);
+  issue(1, live[1]);
+
+  const int64_t r = row0 + l32, t_of = a.group == 1 ? r : (uint32_t)r / (uint32_t)a.group;
+  const bool valid = r < rows;
+  const int64_t token = seq.q0 + t_of;
+  const int head = hk * a.group + (int)(r - t_of * a.group);
+  const uint16_t* q = static_cast<const uint16_t*>(a.q) + token * a.qt + head * a.qh;
+  u32x4_t qf[4 * N];
+#pragma unroll
+  for (int s = 0; s < 4 * N; ++s)
+    qf[s] = valid ? *reinterpret_cast<const u32x4_t*>(q + 32 * (half * N + s / 4) + 8 * (s & 3))
+                  : u32x4_t{0, 0, 0, 0};
+  float c[1] = {attn_factor(a.scale)};
+  query_half(qf, c[0]);
+
+  f32x16_t acc[1][DT];
+  float m[1] = {kNegInf}, l[1] = {0.0f};
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[0][dt][v] = 0.0f;
+
+  auto block_scale = [](uint32_t two, int which) {
+    return (_Float16)(which ? __builtin_amdgcn_cvt_f32_fp8((int)two, 1) : __builtin_amdgcn_cvt_f32_fp8((int)two, 0));
+  };
+  for (int t = 0; t < turns; ++t) {
+    const uint8_t* from = mine + (t & 1) * F::STAGE;
+    // the copies of tile t + 1 are behind tile t's and the mask's load
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(F::LOADS) : "memory");
+    u32x4_t kc[N], vc[N];
+    uint32_t ks[N], vs[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = half * N + i, at = l32 * F::ROW + 16 * (p ^ F::key(l32));
+      kc[i] = *reinterpret_cast<const u32x4_t*>(from + at);
+      vc[i] = *reinterpret_cast<const u32x4_t*>(from + F::CODES + at);
+      ks[i] = *reinterpret_cast<const uint16_t*>(from + 2 * F::CODES + l32 * (F::D / 16) + 2 * p);
+      vs[i] = *reinterpret_cast<const uint16_t*>(from + 2 * F::CODES + F::SCALES + l32 * (F::D / 16) + 2 * p);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the next copies may overwrite them
+    const uint32_t now = live[t & 1], ahead = (uint32_t)__ballot(on != 0);
+    on = key_on(t + 3);
+    issue(t + 2, ahead);
+    live[t & 1] = ahead;
+    if (now == 0) continue;
+    f32x16_t s[1];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) s[0][v] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const _Float16 sk[2] = {block_scale(ks[i], 0), block_scale(ks[i], 1)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        s[0] = Half::mfma(__builtin_bit_cast(s16x8_t, decode8(kc[i][j], sk[j >> 1])),
+                          __builtin_bit_cast(s16x8_t, qf[4 * i + j]), s[0]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const _Float16 sv[2] = {block_scale(vs[i], 0), block_scale(vs[i], 1)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<half8_t*>(tile + l32 * R::BYTES +
+                                    16 * ((4 * (half * N + i) + j) ^ R::swizzle(l32))) =
+            decode8(vc[i][j], sv[j >> 1]);
+    }
+    if (now != ~0u) {
+      const uint32_t bits = now >> (4 * half);
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        if (!(bits >> (8 * (v >> 2) + (v & 3)) & 1)) s[0][v] = kNegInf;
+    }
+    softmax_step<DT, 1>(s, c[0], m[0], l[0], acc[0]);
+    Weights<Half> w;
+    w.set(s[0]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own rows are in LDS
+    columns_mfma<Half, DT>(tile, w, acc[0], lane);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no copy lands in what follows
+  if (!join_columns<DT, 1, HW, F::WK>(smem, wk, wave % HW, lane, m, l, acc) || !valid) return;
+  store_result<uint16_t, DT>(a, parts, split, token, head, half, m[0], l[0], acc[0]);
+}
+
+// The parts' results of a query, joined by their sums.  WAVES waves have one query: groups of 16 lanes,
+// 8 elements a lane, take the parts in turn, and are added in LDS.
+template <typename XT, int WAVES>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), rows = a.Tq * a.Hq;
-  if (row >= rows) return;
-  const int lane = threadIdx.x & 63, mine = lane >> 4;
-  const int64_t t = row / a.Hq;
+  constexpr int GROUPS = 4 * WAVES, ROWS = 4 / WAVES;  // of a query; queries of a workgroup
+  __shared__ float sums[256][9];
+  const int lane = threadIdx.x & 63, thread = threadIdx.x % (64 * WAVES);
+  const int64_t rows = a.Tq * a.Hq, row = (int64_t)blockIdx.x * ROWS + threadIdx.x / (64 * WAVES);
+  if (row >= rows && WAVES == 1) return;
+  const int64_t t = (uint32_t)row / (uint32_t)a.Hq;
   const int h = (int)(row - t * a.Hq), d = 8 * (lane & 15);
-  if (a.qo && (t < attn_offset(a.qo, 0, a.Tq) || t >= attn_offset(a.qo, a.G, a.Tq))) return;
-  const int parts = attn_parts(a, attn_keys(a, a.qo ? attn_owner(a.qo, a.G, t) : 0));
-  if (parts == 1) return;
-  const float l = lane < parts ? a.part_l[lane * rows + row] : kNegInf;
-  float top = l;
+  int parts = 0;
+  if (row < rows && !(a.qo && (t < attn_offset(a.qo, 0, a.Tq) || t >= attn_offset(a.qo, a.G, a.Tq))))
+    parts = attn_parts(a, attn_keys(a, a.qo ? attn_owner(a.qo, a.G, t) : 0));
+  if (parts <= 1) return;  // (all of a query's waves)
+  float top = kNegInf;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_l[s * rows + row]);
 #pragma unroll
   for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
   const float off = top == kNegInf ? 0.0f : top;
-  const float w = l == l ? __builtin_amdgcn_exp2f(l - off) : l;  // a NaN is the row's
-  float sum = w;
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
-  float v[8] = {};
-  for (int s = mine; s < parts; s += 4) {
-    const float ws = __shfl(w, s);
-    if (d < a.D && ws != 0.0f) {
+  float sum = 0.0f, v[8] = {};
+#pragma unroll 4
+  for (int s = thread >> 4; s < parts; s += GROUPS) {
+    const float l = a.part_l[s * rows + row];
+    const float w = l == l ? __builtin_amdgcn_exp2f(l - off) : l;  // a NaN is the row's
+    sum += w;
+    if (d < a.D) {
       const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part + (s * rows + row) * a.D + d);
       const f32x4_t x = p[0], y = p[1];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = __builtin_fmaf(x[e], ws, v[e]);
-        v[4 + e] = __builtin_fmaf(y[e], ws, v[4 + e]);
+        v[e] = __builtin_fmaf(x[e], w, v[e]);
+        v[4 + e] = __builtin_fmaf(y[e], w, v[4 + e]);
       }
     }
   }
+  auto add = [&](float& x) {
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+  };
+  add(sum);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] += __shfl_xor(v[e], 16);
-    v[e] += __shfl_xor(v[e], 32);
+  for (int e = 0; e < 8; ++e) add(v[e]);
+  if constexpr (WAVES > 1) {
+    float* mine = sums[threadIdx.x];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine[e] = v[e];
+    mine[8] = sum;
+    __syncthreads();
+    if (threadIdx.x >= 16) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      const float* other = sums[threadIdx.x + 64 * w];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += other[e];
+      sum += other[8];
+    }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (off + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (mine || d >= a.D) return;
+  if (thread == 0 && a.lse) a.lse[row] = sum == 0.0f ? kNegInf : (off + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (lane >= 16 || d >= a.D) return;
   XT* o = static_cast<XT*>(a.o) + t * a.ot + h * a.oh + d;
   if constexpr (sizeof(XT) == 2) {
     *reinterpret_cast<u32x4_t*>(o) = u32x4_t{bf16x2_rne(v[0] * inv, v[1] * inv), bf16x2_rne(v[2] * inv, v[3] * inv),
@@ -428,8 +672,15 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a) {
 
 // -------------------------------------------------------------------- host
 
-AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t G, bool ragged) {
-  return attn_plan(Tq * (Hq / Hk), Tk, Hk, G, ragged);
+AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t heads, int32_t Hk, int32_t G, bool ragged) {
+  return attn_plan(Tq * (Hq / Hk), Tk, heads, G, ragged);
+}
+
+// Heads that a workgroup of k_attn_few4 has (0: the call is none of its).  Several where a
+// sequence's rows of a head are one tile, as in a serving step: with more tiles the parts' results
+// cost more than the cache lines (256 rows over 4096 keys, 16 heads of 64: 32 us for 24).
+int few4_heads(int64_t held, int32_t G, int32_t Hk, int32_t D) {
+  return D % 64 ? 0 : held > 32 * (int64_t)G ? 1 : Hk % 4 == 0 ? 4 : Hk % 2 == 0 ? 2 : 1;
 }
 
 size_t part_bytes(const AttnPlan& p, int64_t Tq, int32_t Hq, int32_t D) {
@@ -447,25 +698,56 @@ int32_t launch(const AttnArgs& a, hipStream_t st) {
 
 template <typename XT, int DT, bool Q4>
 int32_t launch_form(const AttnArgs& a, bool wide, hipStream_t st) {
-  // rows of 512 bytes: half the tile, and two columns of waves, for LDS's sake
-  constexpr bool LONG = sizeof(XT) == 4 && DT == 4;
-  return wide ? launch<XT, DT, 1, 4, 1, LONG ? 1 : 2, Q4>(a, st)
-              : launch<XT, DT, 1, 1, LONG ? 2 : 4, 1, Q4>(a, st);
+  // rows of 512 bytes: half the tile, for LDS's sake
+  constexpr bool LONG = sizeof(XT) == 4 && DT > 2;
+  return wide ? launch<XT, DT, 1, 4, 1, LONG ? 1 : 2, Q4>(a, st) : launch<XT, DT, 1, 1, 4, 1, Q4>(a, st);
+}
+
+template <int DT, int HW>
+int32_t launch_few4(const AttnArgs& a, hipStream_t st) {
+  const int64_t blocks = attn_grid(a, a.qo != nullptr);
+  ASP_TRY(check_attn_grid(blocks, 256));
+  if (a.mask) k_attn_few4<DT, HW, true><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  else k_attn_few4<DT, HW, false><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  return launch_status("attention");
+}
+
+template <int DT>
+int32_t launch_few4(const AttnArgs& a, hipStream_t st) {
+  switch (a.Hk / a.heads) {
+    case 4: return launch_few4<DT, 4>(a, st);
+    case 2: return launch_few4<DT, 2>(a, st);
+    default: return launch_few4<DT, 1>(a, st);
+  }
 }
 
 template <typename XT, bool Q4>
-int32_t launch_attn(const AttnArgs& a, bool wide, hipStream_t st) {
-  ASP_TRY((a.D <= 64 ? launch_form<XT, 2, Q4>(a, wide, st) : launch_form<XT, 4, Q4>(a, wide, st)));
+int32_t launch_attn(const AttnArgs& a, bool wide, bool few4, hipStream_t st) {
+  if (few4)
+    ASP_TRY(a.D <= 64 ? launch_few4<2>(a, st) : launch_few4<4>(a, st));
+  else
+    ASP_TRY((a.D <= 64   ? launch_form<XT, 2, Q4>(a, wide, st)
+             : a.D <= 96 ? launch_form<XT, 3, Q4>(a, wide, st)
+                         : launch_form<XT, 4, Q4>(a, wide, st)));
   if (a.splits == 1) return ASP_OK;
-  const int64_t blocks = (a.Tq * a.Hq + 3) / 4;
+  // from so many parts on a workgroup for each query
+  const bool many = a.splits > 8;
+  const int64_t blocks = many ? a.Tq * a.Hq : (a.Tq * a.Hq + 3) / 4;
   ASP_TRY(check_attn_grid(blocks, 256));
-  k_attn_join<XT><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  if (many) k_attn_join<XT, 4><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
+  else k_attn_join<XT, 1><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
   return launch_status("attention join");
 }
 
 int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t workspace_bytes,
                  hipStream_t st) {
-  const AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.G, a.qo != nullptr);
+  AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.Hk, a.G, a.qo != nullptr);
+  a.heads = a.Hk;
+  const int few = q4 && dtype == ASP_BF16 && !p.wide ? few4_heads(a.Tq * (a.Hq / a.Hk), a.G, a.Hk, a.D) : 0;
+  if (few) {
+    a.heads = a.Hk / few;
+    p = plan_of(a.Tq, a.Tk, a.Hq, a.heads, a.Hk, a.G, a.qo != nullptr);
+  }
   const size_t need = part_bytes(p, a.Tq, a.Hq, a.D);
   if (need) ASP_TRY(check_ptr(workspace, "workspace", true));
   if (workspace_bytes < need)
@@ -478,8 +760,9 @@ int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t wo
   a.part = static_cast<float*>(workspace);
   a.part_l = a.part + (size_t)p.splits * a.Tq * a.Hq * a.D;
   if (dtype == ASP_BF16)
-    return q4 ? launch_attn<uint16_t, true>(a, p.wide, st) : launch_attn<uint16_t, false>(a, p.wide, st);
-  return q4 ? launch_attn<float, true>(a, p.wide, st) : launch_attn<float, false>(a, p.wide, st);
+    return q4 ? launch_attn<uint16_t, true>(a, p.wide, few != 0, st)
+              : launch_attn<uint16_t, false>(a, p.wide, false, st);
+  return q4 ? launch_attn<float, true>(a, p.wide, false, st) : launch_attn<float, false>(a, p.wide, false, st);
 }
 
 }  // namespace
@@ -495,7 +778,11 @@ int32_t asp_attention_workspace_bytes(int64_t Tq, int64_t Tk, int32_t Hq, int32_
   const int32_t some = 0;
   ASP_TRY(check_attn(ASP_F32, Tq, Tk, Hq, Hk, D, G, 1.0f, &some, &some, nullptr));
   if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
-  *bytes = part_bytes(plan_of(Tq, Tk, Hq, Hk, G, true), Tq, Hq, D);
+  const AttnPlan p = plan_of(Tq, Tk, Hq, Hk, Hk, G, true);
+  *bytes = part_bytes(p, Tq, Hq, D);
+  // a cache's, which may have more parts
+  if (const int few = p.wide ? 0 : few4_heads(Tq * (Hq / Hk), G, Hk, D))
+    *bytes = std::max(*bytes, part_bytes(plan_of(Tq, Tk, Hq, Hk / few, Hk, G, true), Tq, Hq, D));
   return ASP_OK;
 }
 

@@ -94,7 +94,9 @@ struct BackQ {
   using P = Product<XT>;
   using R = Rows<P::ES, DT>;
   static constexpr int THREADS = 64 * WM * WK, BM = 32 * WM, BN = 32 * KT;
-  static constexpr int TILE = BN * R::BYTES, GROUP = 4 * TILE;
+  // one buffer where two would leave half of the columns: rows of 512 bytes
+  static constexpr int BUFFERS = WM == 1 && R::BYTES == 512 ? 1 : 2;
+  static constexpr int TILE = BN * R::BYTES, GROUP = 2 * BUFFERS * TILE;
   static constexpr int JOIN = (WK - 1) * WM * DT * 16 * 64 * 4;
   static constexpr int LDS = WK * GROUP > JOIN ? WK * GROUP : JOIN;
   static_assert(LDS <= 160 * 1024, "a CU has 160 KB of LDS");
@@ -108,16 +110,14 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
   using B = BackQ<XT, DT, WM, WK, KT>;
   using P = typename B::P;
   using R = typename B::R;
-  constexpr int BM = B::BM, BN = B::BN, TILE = B::TILE, QS = R::PIECES / 2;
+  constexpr int BM = B::BM, BN = B::BN, TILE = B::TILE, QS = R::USED;
   __shared__ __attribute__((aligned(16))) uint8_t smem[B::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave % WM, wk = wave / WM;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.qo != nullptr);
-  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
-  // the later parts, which shorter sequences do not have, come last
-  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
-  const int split = (int)(run / a.slots / a.Hk);
+  AttnPlace place;
+  if (!attn_place(a, a.qo != nullptr, place)) return;
+  const int slot = place.slot, hk = place.hk, split = place.split;
   const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
   if (a.zero & 1 && a.qo && split == 0)
     attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
 
   const int64_t r = row0 + 32 * wm + l32;
   const bool valid = r < rows;
-  const int64_t t_of = a.group == 1 ? r : r / a.group;
+  const int64_t t_of = a.group == 1 ? r : (uint32_t)r / (uint32_t)a.group;
   const int64_t token = seq.q0 + t_of;
   const int head = hk * a.group + (int)(r - t_of * a.group);
   const int64_t at = token * a.Hq + head;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
     for (int v = 0; v < 16; ++v) acc[dt][v] = 0.0f;
 
   const int64_t tiles = (seq.keys + BN - 1) / BN;
-  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
+  const int64_t first = attn_part(tiles, split, parts), last = attn_part(tiles, split + 1, parts);
   const int turns = (int)((last - first + WK - 1) / WK);
   uint8_t* mine = smem + wk * B::GROUP;
   auto key0 = [&](int t) { return (first + (int64_t)t * WK + wk) * BN; };
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
     offv[i] = d < a.D ? (row * (int)a.vt + d) * P::ES : kFar;
   }
   auto issue = [&](int t, uint64_t live) {
-    uint8_t* to = mine + (t & 1) * 2 * TILE;
+    uint8_t* to = mine + (t & (B::BUFFERS - 1)) * 2 * TILE;
     const int64_t k = seq.k0 + key0(t), n = min((int64_t)BN, seq.keys - key0(t));
     const auto rk = attn_rows(static_cast<const XT*>(a.k) + (n > 0 ? k * a.kt + hk * a.kh : 0),
                               n > 0 ? ((n - 1) * a.kt + a.D) * P::ES : 0);
@@ -193,11 +193,11 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
   int on = key_on(1);
   issue(0, live);
   for (int t = 0; t < turns; ++t) {
-    const uint8_t* tile = mine + (t & 1) * 2 * TILE;
+    const uint8_t* tile = mine + (t & (B::BUFFERS - 1)) * 2 * TILE;
     attn_settle<(WM > 1)>();
     const uint64_t next = __ballot(on != 0);
     on = key_on(t + 2);
-    if (t + 1 < turns) issue(t + 1, next);
+    if (B::BUFFERS > 1 && t + 1 < turns) issue(t + 1, next);
     if (live != 0) {
       constexpr uint64_t ALL = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
 #pragma unroll
@@ -225,6 +225,10 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
         columns_mfma<P, DT>(tile + 32 * k * R::BYTES, w, acc, lane);
       }
     }
+    if constexpr (B::BUFFERS == 1) {
+      attn_settle<(WM > 1)>();  // the tile is read
+      if (t + 1 < turns) issue(t + 1, next);
+    }
     live = next;
   }
   if (!join_columns<WK, WM>(smem, wk, wm, lane, acc) || !valid) return;
@@ -240,7 +244,7 @@ template <typename XT>
 __global__ void __launch_bounds__(256) k_attn_rows(const AttnArgs a) {
   const int64_t row = (int64_t)blockIdx.x * 128 + (threadIdx.x >> 1);
   if (row >= a.Tq * a.Hq) return;
-  const int64_t t = row / a.Hq;
+  const int64_t t = (uint32_t)row / (uint32_t)a.Hq;
   const int h = (int)(row - t * a.Hq);
   if (a.qo && (t < attn_offset(a.qo, 0, a.Tq) || t >= attn_offset(a.qo, a.G, a.Tq))) return;
   const XT* g = static_cast<const XT*>(a.dout) + t * a.gt + h * a.gh;
@@ -260,7 +264,9 @@ struct BackKV {
   using R = Rows<P::ES, DT>;
   static constexpr int THREADS = 64 * WN * WQ, BN = 32 * WN, BQ = 32 * QT;
   static constexpr int TILE = BQ * R::BYTES;                 // queries or do
-  static constexpr int GROUP = 4 * TILE + 2 * 2 * BQ * 4;    // two buffers, and two of the rows' two values
+  // one buffer where two would leave half of the columns: rows of 512 bytes
+  static constexpr int BUFFERS = WN == 1 && R::BYTES == 512 ? 1 : 2;
+  static constexpr int GROUP = 2 * BUFFERS * TILE + 2 * 2 * BQ * 4;  // and two of the rows' two values
   static constexpr int JOIN = (WQ - 1) * WN * 2 * DT * 16 * 64 * 4;
   static constexpr int LDS = WQ * GROUP > JOIN ? WQ * GROUP : JOIN;
   static_assert(LDS <= 160 * 1024, "a CU has 160 KB of LDS");
@@ -274,16 +280,14 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   using B = BackKV<XT, DT, WN, WQ, QT>;
   using P = typename B::P;
   using R = typename B::R;
-  constexpr int BN = B::BN, BQ = B::BQ, TILE = B::TILE, QS = R::PIECES / 2;
+  constexpr int BN = B::BN, BQ = B::BQ, TILE = B::TILE, QS = R::USED;
   __shared__ __attribute__((aligned(16))) uint8_t smem[B::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   const int wn = wave % WN, wq = wave / WN;
-  const int64_t run = attn_run(blockIdx.x, gridDim.x, a.ko != nullptr);
-  if (run >= (int64_t)a.slots * a.splits * a.Hk) return;
-  // the later parts, which shorter sequences do not have, come last
-  const int slot = (int)(run % a.slots), hk = (int)(run / a.slots % a.Hk);
-  const int split = (int)(run / a.slots / a.Hk);
+  AttnPlace place;
+  if (!attn_place(a, a.ko != nullptr, place)) return;
+  const int slot = place.slot, hk = place.hk, split = place.split;
   const AttnSeq seq = attn_seq(a, a.ko, a.Tk, 1, BN, slot);
   if (a.zero & 6 && a.ko && split == 0)
     attn_outside(a.ko, a.G, a.Tk, slot, a.slots, [&](int64_t t) {
@@ -314,10 +318,10 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   const int64_t per_head = (seq.rows + BQ - 1) / BQ;
   // a workgroup without a key that counts has nothing to sum
   const int64_t tiles = key0 < seq.keys ? per_head * a.group : 0;
-  const int64_t first = tiles * split / parts, last = tiles * (split + 1) / parts;
+  const int64_t first = attn_part(tiles, split, parts), last = attn_part(tiles, split + 1, parts);
   const int turns = (int)((last - first + WQ - 1) / WQ);
   uint8_t* mine = smem + wq * B::GROUP;
-  float* row_log2 = reinterpret_cast<float*>(mine + 4 * TILE);  // [buffer][BQ], then the deltas
+  float* row_log2 = reinterpret_cast<float*>(mine + 2 * B::BUFFERS * TILE);  // [turn % 2][BQ], then the deltas
   float* row_delta = row_log2 + 2 * BQ;
   constexpr int COPIES = TILE / 1024 / WN;
   static_assert(TILE % (1024 * WN) == 0, "whole copies for each wave");
@@ -330,9 +334,9 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   }
   float2 mine_row = make_float2(0.0f, 0.0f);
   auto issue = [&](int t) {
-    uint8_t* to = mine + (t & 1) * 2 * TILE;
+    uint8_t* to = mine + (t & (B::BUFFERS - 1)) * 2 * TILE;
     const int64_t tile = first + (int64_t)t * WQ + wq;
-    const int64_t h = per_head ? tile / per_head : 0, row = (tile - h * per_head) * BQ;
+    const int64_t h = per_head ? (uint32_t)tile / (uint32_t)per_head : 0, row = (tile - h * per_head) * BQ;
     const int64_t n = tile < last ? min((int64_t)BQ, seq.rows - row) : 0;
     const int head = hk * a.group + (int)h;
     const int64_t q = seq.q0 + row;
@@ -353,13 +357,13 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   if (turns > 0) issue(0);
   for (int t = 0; t < turns; ++t) {
     const int b = t & 1;
-    const uint8_t* tile = mine + b * 2 * TILE;
+    const uint8_t* tile = mine + (t & (B::BUFFERS - 1)) * 2 * TILE;
     if (wn == 0 && lane < BQ) {
       row_log2[b * BQ + lane] = mine_row.x;
       row_delta[b * BQ + lane] = mine_row.y;
     }
     attn_settle<(WN > 1)>();
-    if (t + 1 < turns) issue(t + 1);
+    if (B::BUFFERS > 1 && t + 1 < turns) issue(t + 1);
 #pragma unroll
     for (int j = 0; j < QT; ++j) {
       f32x16_t s, d;
@@ -370,8 +374,7 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
         piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * j * R::BYTES, i, half, l32), kf[i], s);
 #pragma unroll
       for (int i = 0; i < QS; ++i)
-        piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * j * R::BYTES, i, half, l32),
-                      vf[i], d);
+        piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * j * R::BYTES, i, half, l32), vf[i], d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = b * BQ + 32 * j + 8 * i + 4 * half;
@@ -389,6 +392,10 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
       ws.set(d);
       columns_mfma<P, DT>(tile + TILE + 32 * j * R::BYTES, wp, dv, lane);
       columns_mfma<P, DT>(tile + 32 * j * R::BYTES, ws, dk, lane);
+    }
+    if constexpr (B::BUFFERS == 1) {
+      attn_settle<(WN > 1)>();  // the tile is read
+      if (t + 1 < turns) issue(t + 1);
     }
   }
   if (!join_columns<WQ, WN>(smem, wq, wn, lane, acc) || !stored) return;
@@ -510,14 +517,13 @@ int32_t launch_sum(const SumArgs& s, int tensors, hipStream_t st) {
 
 template <typename XT, int DT>
 int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
-  // rows of 512 bytes: half the tile, and two columns of waves, for LDS's sake
-  constexpr bool LONG = sizeof(XT) == 4 && DT == 4;
-  constexpr int COLUMNS = LONG ? 2 : 4, DEEP = LONG ? 1 : 2;
+  // rows of 512 bytes: half the tile, for LDS's sake
+  constexpr int DEEP = sizeof(XT) == 4 && DT > 2 ? 1 : 2;
   if (a.Tq > 0 && a.dq) {
     a.slots = z.q.slots;
     a.splits = z.q.splits;
     a.chunk = z.q.chunk;
-    ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, COLUMNS, 1>(a, st)));
+    ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, 4, 1>(a, st)));
     if (a.splits > 1) {
       SumArgs s = {};
       s.a = a;
@@ -535,7 +541,7 @@ int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
   a.slots = z.kv.slots;
   a.splits = z.kv.splits;
   a.chunk = z.kv.chunk;
-  ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, COLUMNS, 1>(a, st)));
+  ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, 4, 1>(a, st)));
   if (a.splits == 1) return ASP_OK;
   SumArgs s = {};
   s.a = a;
@@ -604,7 +610,7 @@ int32_t asp_attention_backward(const void* dout, int64_t lddo, int64_t hsdo, con
   a.q = q; a.k = k; a.v = v; a.o = const_cast<void*>(o); a.lse = const_cast<float*>(lse);
   a.qt = ldq; a.qh = hsq; a.kt = ldk; a.kh = hsk; a.vt = ldv; a.vh = hsv; a.ot = ldo; a.oh = hso;
   a.qo = q_offsets; a.ko = kv_offsets; a.kl = kv_lengths; a.mask = key_mask;
-  a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hk = Hk; a.group = Hq / Hk; a.D = D; a.G = G;
+  a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hk = Hk; a.heads = Hk; a.group = Hq / Hk; a.D = D; a.G = G;
   a.zero = zero; a.scale = scale;
   a.dout = dout; a.gt = lddo; a.gh = hsdo;
   a.dq = dq; a.dqt = lddq; a.dqh = hsdq; a.dk = dk; a.dkt = lddk; a.dkh = hsdk;
@@ -616,8 +622,10 @@ int32_t asp_attention_backward(const void* dout, int64_t lddo, int64_t hsdo, con
   a.part_dv = reinterpret_cast<float*>(w + z.rows + z.dq + z.dk);
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == ASP_BF16)
-    return D <= 64 ? run_back<uint16_t, 2>(a, z, st) : run_back<uint16_t, 4>(a, z, st);
-  return D <= 64 ? run_back<float, 2>(a, z, st) : run_back<float, 4>(a, z, st);
+    return D <= 64   ? run_back<uint16_t, 2>(a, z, st)
+           : D <= 96 ? run_back<uint16_t, 3>(a, z, st)
+                     : run_back<uint16_t, 4>(a, z, st);
+  return D <= 64 ? run_back<float, 2>(a, z, st) : D <= 96 ? run_back<float, 3>(a, z, st) : run_back<float, 4>(a, z, st);
 }
 
 }  // extern "C"

@@ -20,13 +20,19 @@ struct StoreArgs {
 
 template <typename XT>
 __global__ void __launch_bounds__(256) k_kv_store(const StoreArgs a) {
-  const int64_t each = a.T * a.H * a.per;
-  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t each = (uint32_t)(a.T * a.H * a.per);
+  uint32_t i = blockIdx.x * 256 + threadIdx.x;
   const int which = i >= each;
   if (which) i -= each;
   if (i >= each) return;
-  const int64_t head_of = i / a.per, t = head_of / a.H;
-  const int blk = (int)(i - head_of * a.per), h = (int)(head_of - t * a.H);
+  const uint32_t head_of = i / (uint32_t)a.per;
+  const int64_t t = head_of / (uint32_t)a.H;
+  const int blk = (int)(i - head_of * a.per), h = (int)(head_of - (uint32_t)t * a.H);
+  // the elements are on their way while the token's row is looked up
+  Raw<XT> raw[2];
+  const XT* x = static_cast<const XT*>(a.x[which]) + t * a.xt[which] + h * a.xh[which] + 16 * blk;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) raw_load<false>(x + 8 * p, 0, 8, raw[p]);
   // the token's sequence: the last that begins at or before it
   int g = 0;
   int64_t t0 = 0;
@@ -47,12 +53,11 @@ __global__ void __launch_bounds__(256) k_kv_store(const StoreArgs a) {
   if (row < k0 || row >= k1) return;  // no room in the sequence's rows
 
   float v[16];
-  const XT* x = static_cast<const XT*>(a.x[which]) + t * a.xt[which] + h * a.xh[which] + 16 * blk;
   uint32_t bad = 0;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     float u[8];
-    load8(x + 8 * p, 0, 8, u);
+    unpack(raw[p], u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[8 * p + e] = u[e];
@@ -149,7 +154,7 @@ int32_t asp_kv_store(const void* k, int64_t ldk, int64_t hsk, const void* v, int
   a.offsets = offsets; a.ko = kv_offsets; a.kl = kv_lengths;
   a.T = T; a.rows = rows; a.H = Hk; a.per = D / 16; a.G = G;
   const int64_t blocks = (2 * T * Hk * a.per + 255) / 256;
-  ASP_TRY(check_attn_grid(blocks, 256));
+  ASP_TRY(check_attn_grid(blocks, 256));  // and so the lanes have 32-bit numbers
   const hipStream_t st = (hipStream_t)stream;
   if (dtype == ASP_BF16) k_kv_store<uint16_t><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
   else k_kv_store<float><<<dim3((unsigned)blocks), 256, 0, st>>>(a);
