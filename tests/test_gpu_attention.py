@@ -198,6 +198,29 @@ def test_ragged(Hq, Hk, D, which, mask, dtype):
     assert not host(g.dk)[dead].any() and not host(g.dv)[dead].any() and not host(g.dq)[~case.owned].any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G, D", [(64, 64), (70, 64), (65, 128)])
+def test_more_sequences_than_a_wave_has_lanes(G, D, dtype):
+    """In both forms, with the longest sequence in the middle and some empty."""
+    for Hq, Hk in ((128, 128), (4, 2)):
+        lengths = [(7 * i) % 5 for i in range(G)]
+        keys = [(3 * i) % 8 for i in range(G)]
+        lengths[G // 2], keys[G // 2], keys[3] = 75, 90, 0
+        qo, ko = [0, *np.cumsum(lengths).tolist()], [2, *(2 + np.cumsum(keys)).tolist()]
+        case = Case(qo[-1] + 1, ko[-1] + 3, Hq, Hk, D, dtype, qo, ko, mask=0.9)
+        case.check_forward()
+        case.check_backward()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, qo, ko", [(1060, 2500, [0, 150, 1056], [0, 2300, 2400]), (2500, 1060, [0, 2300, 2400], [4, 150, 1056])])
+def test_long_ragged_sequences(Tq, Tk, qo, ko, dtype):
+    """Parts of a long sequence beside a short one that has none."""
+    case = Case(Tq, Tk, 32, 32, 40, dtype, qo, ko)
+    case.check_forward()
+    case.check_backward()
+
+
 @pytest.mark.parametrize("layout", ["heads", "padded"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strides(layout, dtype):

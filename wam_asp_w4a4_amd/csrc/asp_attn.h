@@ -293,62 +293,22 @@ __device__ __forceinline__ uint32_t attn_run(uint32_t id, uint32_t total, bool r
 }
 
 // This workgroup's place: a tile of rows, a head of the keys and a part of what goes by.  The later
-// parts, which shorter sequences do not have, come last; heads_first: the heads of one tile follow
-// one another, else the tiles of one head.
+// parts, which shorter sequences do not have, come last.  The tiles of a head follow one
+// another; or, heads_first, the heads of a tile, as for ragged sequences, whose longest are then
+// begun in all heads before the shorter ones (607 and 542 us of that backward).
 struct AttnPlace {
   int slot, hk, split;
 };
 
-template <bool HEADS_FIRST = false>
-__device__ __forceinline__ bool attn_place(const AttnArgs& a, bool ragged, AttnPlace& p) {
+__device__ __forceinline__ bool attn_place(const AttnArgs& a, bool ragged, bool heads_first,
+                                           AttnPlace& p) {
   const uint32_t run = attn_run(blockIdx.x, gridDim.x, ragged), slots = a.slots, heads = a.heads;
-  const uint32_t outer = HEADS_FIRST ? slots : heads, inner = HEADS_FIRST ? heads : slots;
+  const uint32_t outer = heads_first ? slots : heads, inner = heads_first ? heads : slots;
   const uint32_t by = run / inner, split = by / outer;
-  p.slot = (int)(HEADS_FIRST ? by - split * outer : run - by * inner);
-  p.hk = (int)(HEADS_FIRST ? run - by * inner : by - split * outer);
+  p.slot = (int)(heads_first ? by - split * outer : run - by * inner);
+  p.hk = (int)(heads_first ? run - by * inner : by - split * outer);
   p.split = (int)split;
   return split < (uint32_t)a.splits;
-}
-
-// Which sequence and tile a slot stands for.  Rows of `per` tiles: a sequence's first slot is
-// (its first row) / tile + g, which leaves each sequence enough slots and none to two.  The
-// wave searches 64 sequences at a time.  Offsets that are out of range or decrease give
-// sequences inside the tensors all the same.
-__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, const int32_t* offsets, int64_t total,
-                                            int group, int tile_rows, int slot) {
-  AttnSeq s = {};
-  int g = 0;
-  s.tile = slot;
-  s.any = true;
-  if (offsets) {
-    auto first = [&](int i) {
-      return (int64_t)((uint32_t)(attn_offset(offsets, i, total) * group) / (uint32_t)tile_rows) + i;
-    };
-    const int lane = threadIdx.x & 63;
-    int n = a.G;
-    while (n > 0) {
-      const int step = (n + 63) / 64, i = g + lane * step;
-      const bool before = lane * step < n && first(i) <= slot;
-      const int count = __builtin_popcountll(__ballot(before));
-      if (count == 0) {
-        s.any = false;
-        break;
-      }
-      g += (count - 1) * step;
-      n = step > 1 ? min(step, n - (count - 1) * step) : 0;
-    }
-    g = __builtin_amdgcn_readfirstlane(g);
-    // (offsets that decrease may have led to a sequence whose first slot is behind this one)
-    if (s.any) s.tile = slot - first(g);
-    if (s.tile < 0) s.any = false;
-  }
-  s.q0 = a.qo ? attn_offset(a.qo, g, a.Tq) : 0;
-  s.rows = (a.qo ? attn_offset(a.qo, g + 1, a.Tq) : a.Tq) - s.q0;
-  s.k0 = a.ko ? attn_offset(a.ko, g, a.Tk) : 0;
-  s.all = max((a.ko ? attn_offset(a.ko, g + 1, a.Tk) : a.Tk) - s.k0, (int64_t)0);
-  s.keys = a.kl ? min(s.all, max((int64_t)a.kl[g], (int64_t)0)) : s.all;
-  s.rows = max(s.rows, (int64_t)0);
-  return s;
 }
 
 // How many workgroups share `passed` rows
@@ -380,6 +340,71 @@ __device__ __forceinline__ int attn_owner(const int32_t* offsets, int G, int64_t
 __device__ __forceinline__ int64_t attn_keys(const AttnArgs& a, int g) {
   const int64_t all = a.ko ? attn_offset(a.ko, g + 1, a.Tk) - attn_offset(a.ko, g, a.Tk) : a.Tk;
   return max(a.kl ? min(all, (int64_t)a.kl[g]) : all, (int64_t)0);
+}
+
+// Which sequence and tile a slot stands for, where tiles are of queries (by a.qo, each with `group`
+// rows) or of keys (KEYS: by a.ko).  Up to 64 sequences: a lane has each, and those whose tiles
+// take the longest (by the rows that go by) have the first slots, so that no long one is left
+// to the end.  More: a sequence's first slot is (its first row) / tile + g, which leaves each
+// sequence enough slots and none to two, and the wave searches 64 sequences at a time.
+// Offsets that are out of range or decrease give sequences inside the tensors all the same.
+template <bool KEYS>
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int tile_rows, int slot) {
+  const int32_t* offsets = KEYS ? a.ko : a.qo;
+  const int64_t total = KEYS ? a.Tk : a.Tq;
+  const int group = KEYS ? 1 : a.group, lane = threadIdx.x & 63;
+  AttnSeq s = {};
+  int g = 0;
+  s.tile = slot;
+  s.any = true;
+  auto span = [](const int32_t* o, int i, int64_t all) {
+    return max((int32_t)(attn_offset(o, i + 1, all) - attn_offset(o, i, all)), 0);
+  };
+  if (offsets && a.G <= 64) {
+    int32_t tiles = 0, cost = -1;
+    if (lane < a.G) {
+      tiles = (int32_t)(((uint32_t)(span(offsets, lane, total) * group) + tile_rows - 1) / (uint32_t)tile_rows);
+      cost = KEYS ? (a.qo ? span(a.qo, lane, a.Tq) : (int32_t)a.Tq) : (int32_t)attn_keys(a, lane);
+    }
+    int32_t before = 0;
+    for (int j = 0; j < a.G; ++j) {
+      const int32_t other = __builtin_amdgcn_readlane(cost, j), has = __builtin_amdgcn_readlane(tiles, j);
+      if (other > cost || (other == cost && j < lane)) before += has;
+    }
+    const uint64_t mine = __ballot(slot >= before && slot - before < tiles);
+    s.any = mine != 0;
+    if (s.any) {
+      g = __builtin_ctzll(mine);
+      s.tile = slot - __builtin_amdgcn_readlane(before, g);
+    }
+  } else if (offsets) {
+    auto first = [&](int i) {
+      return (int64_t)((uint32_t)(attn_offset(offsets, i, total) * group) / (uint32_t)tile_rows) + i;
+    };
+    int n = a.G;
+    while (n > 0) {
+      const int step = (n + 63) / 64, i = g + lane * step;
+      const bool before = lane * step < n && first(i) <= slot;
+      const int count = __builtin_popcountll(__ballot(before));
+      if (count == 0) {
+        s.any = false;
+        break;
+      }
+      g += (count - 1) * step;
+      n = step > 1 ? min(step, n - (count - 1) * step) : 0;
+    }
+    // (offsets that decrease may have led to a sequence whose first slot is behind this one)
+    if (s.any) s.tile = slot - first(g);
+    if (s.tile < 0) s.any = false;
+  }
+  g = __builtin_amdgcn_readfirstlane(g);
+  s.q0 = a.qo ? attn_offset(a.qo, g, a.Tq) : 0;
+  s.rows = (a.qo ? attn_offset(a.qo, g + 1, a.Tq) : a.Tq) - s.q0;
+  s.k0 = a.ko ? attn_offset(a.ko, g, a.Tk) : 0;
+  s.all = max((a.ko ? attn_offset(a.ko, g + 1, a.Tk) : a.Tk) - s.k0, (int64_t)0);
+  s.keys = a.kl ? min(s.all, max((int64_t)a.kl[g], (int64_t)0)) : s.all;
+  s.rows = max(s.rows, (int64_t)0);
+  return s;
 }
 
 // Rows of no sequence: f(token) for the tokens outside the offsets, a share for each slot

@@ -116,9 +116,9 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
   const int half = lane >> 5, l32 = lane & 31;
   const int wm = wave % WM, wk = wave / WM;
   AttnPlace place;
-  if (!attn_place(a, a.qo != nullptr, place)) return;
+  if (!attn_place(a, a.qo != nullptr, a.qo != nullptr, place)) return;
   const int slot = place.slot, hk = place.hk, split = place.split;
-  const AttnSeq seq = attn_seq(a, a.qo, a.Tq, a.group, BM, slot);
+  const AttnSeq seq = attn_seq<false>(a, BM, slot);
   if (a.zero & 1 && a.qo && split == 0)
     attn_outside(a.qo, a.G, a.Tq, slot, a.slots, [&](int64_t t) {
       zero_heads<XT>(a.dq, t, a.dqt, a.dqh, hk * a.group, a.group, a.D, B::THREADS);
@@ -202,15 +202,18 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
       constexpr uint64_t ALL = BN == 64 ? ~0ull : (1ull << (BN & 63)) - 1;
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
+        // the wave that has products goes first (4096 x 4096, 16 heads of 128: 215 us without, 208 with)
         f32x16_t s, d;
 #pragma unroll
         for (int v = 0; v < 16; ++v) s[v] = d[v] = 0.0f;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < QS; ++i)
           piece_mfma<P>(row_frag<P::ES, DT>(tile + 32 * k * R::BYTES, i, half, l32), qf[i], s);
 #pragma unroll
         for (int i = 0; i < QS; ++i)
           piece_mfma<P>(row_frag<P::ES, DT>(tile + TILE + 32 * k * R::BYTES, i, half, l32), df[i], d);
+        __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           d[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[v], c, -lg)) * (d[v] - delta);
@@ -222,7 +225,9 @@ __global__ void __launch_bounds__((BackQ<XT, DT, WM, WK, KT>::THREADS), (sizeof(
         }
         Weights<P> w;
         w.set(d);
+        __builtin_amdgcn_s_setprio(1);
         columns_mfma<P, DT>(tile + 32 * k * R::BYTES, w, acc, lane);
+        __builtin_amdgcn_s_setprio(0);
       }
     }
     if constexpr (B::BUFFERS == 1) {
@@ -286,9 +291,9 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   const int half = lane >> 5, l32 = lane & 31;
   const int wn = wave % WN, wq = wave / WN;
   AttnPlace place;
-  if (!attn_place(a, a.ko != nullptr, place)) return;
+  if (!attn_place(a, a.ko != nullptr, a.ko != nullptr, place)) return;
   const int slot = place.slot, hk = place.hk, split = place.split;
-  const AttnSeq seq = attn_seq(a, a.ko, a.Tk, 1, BN, slot);
+  const AttnSeq seq = attn_seq<true>(a, BN, slot);
   if (a.zero & 6 && a.ko && split == 0)
     attn_outside(a.ko, a.G, a.Tk, slot, a.slots, [&](int64_t t) {
       if (a.zero & 2) zero_heads<XT>(a.dk, t, a.dkt, a.dkh, hk, 1, a.D, B::THREADS);
