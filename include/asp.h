@@ -731,7 +731,7 @@ int32_t asp_head_norm_backward(const void* dq, int64_t lddq, int64_t hsdq, const
  *   key_mask   device, Tk bytes, or NULL: a key whose byte is 0 does not count; its
  *              elements reach no result, whatever they are
  *   lse        device out float32 Tq x Hq, or NULL
- *   D a multiple of 8, 8..128; Hq, Hk up to 65535
+ *   D a multiple of 8, 8..128; Hq, Hk, G up to 65535; Tq Hq and Tk Hk below 2^31
  * Inputs need not be finite: a NaN reaches the queries that read it.  bf16: products
  * of bf16 with float32 sums; exp(s - lse) is rounded to bf16 for its product with v.
  * float32: float32 throughout.  The same bits on every call.

@@ -212,6 +212,30 @@ def test_more_sequences_than_a_wave_has_lanes(G, D, dtype):
         case.check_backward()
 
 
+def test_thousands_of_sequences():
+    G = 5000
+    qo = [i + (i > 2500) * 20 for i in range(G + 1)]
+    ko = [i + (i > 4000) * 60 for i in range(G + 1)]
+    case = Case(qo[-1], ko[-1], 2, 1, 8, "f32", qo, ko)
+    case.check_forward()
+    case.check_backward()
+
+
+@pytest.mark.parametrize("cache", [False, True])
+def test_parts_among_many_sequences(cache):
+    """One of a hundred sequences is long enough to be split."""
+    qo = list(range(101))
+    ko = [3 * i + (i > 60) * 1500 for i in range(101)]
+    case = Case(100, ko[-1], 4, 1, 64, "bf16", qo, ko, cache=cache)
+    case.check_forward()
+    if not cache:
+        case.check_backward()
+        # and a long one of queries
+        case = Case(ko[-1], 100, 4, 1, 64, "bf16", ko, qo)
+        case.check_forward()
+        case.check_backward()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq, Tk, qo, ko", [(1060, 2500, [0, 150, 1056], [0, 2300, 2400]), (2500, 1060, [0, 2300, 2400], [4, 150, 1056])])
 def test_long_ragged_sequences(Tq, Tk, qo, ko, dtype):
