@@ -167,7 +167,8 @@ def test_parity(Tq, Tk, Hq, Hk, D, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq, Tk, Hq, Hk, D", [(129, 200, 128, 128, 64), (130, 131, 256, 64, 128), (520, 330, 64, 64, 32), (1, 190, 512, 256, 96),
-                                               (150, 600, 128, 128, 64), (70, 520, 128, 128, 128), (100, 700, 160, 80, 96)])
+                                               (150, 600, 128, 128, 64), (70, 520, 128, 128, 128), (100, 700, 160, 80, 96),
+                                               (520, 70, 128, 128, 128), (300, 100, 160, 80, 72)])
 def test_many_heads(Tq, Tk, Hq, Hk, D, dtype):
     """Enough rows for the forms whose waves have rows of their own."""
     print(f"attention {Tq} {Tk} {Hq} {Hk} {D} {dtype}", flush=True)

@@ -514,4 +514,17 @@ inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, b
   return p;
 }
 
+// Workgroups of 128 rows with eight waves, two columns of four that share the keys, for bf16 where they
+// fill the CUs once: two waves a SIMD (2048 x 2048, 16 heads of 64: 28 us, 36 by four waves; from
+// 257 workgroups on four waves, 3000 x 3000 and 16 heads of 128: 97 us for 120).  Below, 32 rows
+// a workgroup while those run all at once, one a CU or, with heads up to 64, two (1024 x 1024,
+// 8 heads of 128: 16 us for 23; 16 heads of 64: 12 for 16; but 2048 x 2048, 8 heads of 128: 46
+// for 39; 1100 x 1024, 16 heads of 64: 20 for 16).  Short or ragged keys leave a column idle
+// (2048 x 64: 10 us for 8; 2048 x 2048 in five sequences: 52 for 43).
+inline bool attn_deep(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, bool ragged) {
+  const int64_t rows = Tq * (Hq / Hk);
+  return !ragged && Tk >= 512 && (rows + 127) / 128 * Hk <= 256 &&
+         (rows + 31) / 32 * Hk > (D <= 64 ? 512 : 256);
+}
+
 }  // namespace asp

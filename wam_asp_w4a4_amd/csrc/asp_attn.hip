@@ -682,19 +682,6 @@ AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t heads, int32_t Hk, 
   return attn_plan(Tq * (Hq / Hk), Tk, heads, G, ragged);
 }
 
-// Workgroups of 128 rows with eight waves, two columns of four that share the keys, for bf16 where they
-// fill the CUs once: two waves a SIMD (2048 x 2048, 16 heads of 64: 28 us, 36 by four waves; from
-// 257 workgroups on four waves, 3000 x 3000 and 16 heads of 128: 97 us for 120).  Below, 32 rows
-// a workgroup while those run all at once, one a CU or, with heads up to 64, two (1024 x 1024,
-// 8 heads of 128: 16 us for 23; 16 heads of 64: 12 for 16; but 2048 x 2048, 8 heads of 128: 46
-// for 39; 1100 x 1024, 16 heads of 64: 20 for 16).  Short or ragged keys leave a column idle
-// (2048 x 64: 10 us for 8; 2048 x 2048 in five sequences: 52 for 43).
-bool is_deep(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t D, bool ragged) {
-  const int64_t rows = Tq * (Hq / Hk);
-  return !ragged && Tk >= 512 && (rows + 127) / 128 * Hk <= 256 &&
-         (rows + 31) / 32 * Hk > (D <= 64 ? 512 : 256);
-}
-
 // Heads that a workgroup of k_attn_few4 has (0: the call is none of its).  Several where a
 // sequence's rows of a head are one tile, as in a serving step: with more tiles the parts' results
 // cost more than the cache lines (256 rows over 4096 keys, 16 heads of 64: 32 us for 24).
@@ -763,7 +750,7 @@ int32_t launch_attn(const AttnArgs& a, bool wide, bool deep, bool few4, hipStrea
 int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t workspace_bytes,
                  hipStream_t st) {
   AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.Hk, a.G, a.qo != nullptr);
-  const bool deep = dtype == ASP_BF16 && !q4 && is_deep(a.Tq, a.Tk, a.Hq, a.Hk, a.D, a.qo != nullptr);
+  const bool deep = dtype == ASP_BF16 && !q4 && attn_deep(a.Tq, a.Tk, a.Hq, a.Hk, a.D, a.qo != nullptr);
   if (deep) {
     p.splits = 1;
     p.slots = (int)attn_slots(a.Tq * (a.Hq / a.Hk), 128, 1, false);

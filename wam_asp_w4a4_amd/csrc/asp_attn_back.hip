@@ -528,7 +528,15 @@ int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
     a.slots = z.q.slots;
     a.splits = z.q.splits;
     a.chunk = z.q.chunk;
-    ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, 4, 1>(a, st)));
+    bool deep = false;
+    if constexpr (sizeof(XT) == 2) deep = attn_deep(a.Tq, a.Tk, a.Hq, a.Hk, a.D, a.qo != nullptr);
+    if (deep) {
+      a.splits = 1;
+      a.slots = (int)attn_slots(a.Tq * a.group, 128, 1, false);
+      if constexpr (sizeof(XT) == 2) ASP_TRY((launch_dq<XT, DT, 4, 2, 2>(a, st)));
+    } else {
+      ASP_TRY((z.q.wide ? launch_dq<XT, DT, 4, 1, DEEP>(a, st) : launch_dq<XT, DT, 1, 4, 1>(a, st)));
+    }
     if (a.splits > 1) {
       SumArgs s = {};
       s.a = a;
@@ -546,7 +554,20 @@ int32_t run_back(AttnArgs a, const Sizes& z, hipStream_t st) {
   a.slots = z.kv.slots;
   a.splits = z.kv.splits;
   a.chunk = z.kv.chunk;
-  ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, 4, 1>(a, st)));
+  // Heads above 64 leave room for one workgroup a CU: where those of 32 keys would need a second round
+  // and those of 64 do not, two columns of two waves (1024 x 1024, 16 heads of 128: the backward in
+  // 60 us for 71; heads of 64, 4096 x 512 and 32 of them: 99 for 92)
+  bool pairs = false;
+  if constexpr (sizeof(XT) == 2 && DT > 2)
+    pairs = !z.kv.wide && !a.ko && a.Tq * a.group >= 512 && (a.Tk + 63) / 64 * a.Hk <= 256 &&
+            (a.Tk + 31) / 32 * a.Hk > 256;
+  if (pairs) {
+    a.splits = 1;
+    a.slots = (int)attn_slots(a.Tk, 64, 1, false);
+    if constexpr (sizeof(XT) == 2 && DT > 2) ASP_TRY((launch_dkv<XT, DT, 2, 2, 2>(a, st)));
+  } else {
+    ASP_TRY((z.kv.wide ? launch_dkv<XT, DT, 4, 1, DEEP>(a, st) : launch_dkv<XT, DT, 1, 4, 1>(a, st)));
+  }
   if (a.splits == 1) return ASP_OK;
   SumArgs s = {};
   s.a = a;
