@@ -282,7 +282,7 @@ __device__ __forceinline__ int64_t attn_offset(const int32_t* o, int g, int64_t 
 // XCD-aware order: consecutive workgroups go to the 8 XCDs in turn.  Sequences of one length: each
 // XCD takes one contiguous run, so that the tiles of a head, which read the same keys, share an
 // L2.  Ragged ones: runs of kRaggedRun in turn, since the long sequences of a head would all be one
-// XCD's (the backward of 8192 queries in 4 sequences of 878 to 5506, 16 heads of 128, 4 of the
+// XCD's (the backward of 8192 queries in 4 sequences of 878 to 4628, 16 heads of 128, 4 of the
 // keys: 962 us, so 639).  The grid is then a multiple of 8 runs, and ids past the last
 // have no work.
 constexpr int kRaggedRun = 8;
@@ -295,7 +295,8 @@ __device__ __forceinline__ uint32_t attn_run(uint32_t id, uint32_t total, bool r
 // This workgroup's place: a tile of rows, a head of the keys and a part of what goes by.  The later
 // parts, which shorter sequences do not have, come last.  The tiles of a head follow one
 // another; or, heads_first, the heads of a tile, as for ragged sequences, whose longest are then
-// begun in all heads before the shorter ones (607 and 542 us of that backward).
+// begun in all heads before the shorter ones (that backward with its other steps: 607 us before,
+// 542 so).
 struct AttnPlace {
   int slot, hk, split;
 };

@@ -6,9 +6,15 @@
 // s = k q^T of a tile of keys, p = 2^(c s - m) with c = scale log2(e), l += p, o += v^T p.
 // When a tile's maximum exceeds m by more than 2^8, m is raised and l and o are scaled down;
 // until then p stays below 2^8, which costs float32 sums nothing.  Scores, sums
-// and o are float32.  bf16: p is rounded to bf16 for its product (as v is: half a step
-// is 2^-9 of each p, with signs that average out over the keys).  A row without a key has
-// l = 0: o is 0 and its logarithm -infinity.
+// and o are float32.  bf16: p is rounded to bf16 for its product, whose rate is nine times
+// float32's (half a step, at most 2^-8 of each p, with signs that average out over the
+// keys).  A row without a key has l = 0: o is 0 and its logarithm -infinity.
+//
+// Long calls are bound by the products, in whose gaps the exponentials have to fit: 8192 x 8192,
+// 16 heads of 128, 512 us, 1070 TFLOP/s (a library product: 1370), the matrix units busy
+// for 58 % of the time.  Few queries over a long cache are bound by its bytes and their decoding:
+// 131072 keys of 8 heads of 128, 54 us and 7 to join, 2.8 TB/s.  Short calls are one
+// tile's latency after another's: 256 x 512, 16 heads of 64, 7.5 us.
 #include "asp_attn.h"
 
 namespace asp {
@@ -435,18 +441,18 @@ struct Few4 {
 
 // A copy as attn_copy's, in assembly: for the builtin the compiler waits for all copies in flight
 // before each transposing read, which here would be the memory's whole latency for each tile
-// (2^20 keys of 8 heads of 128: 300 us).  No register is written but m0, which nothing else
-// in the kernel uses; the loop waits for its copies by their number.
+// (2^20 keys of 8 heads of 128: 300 us).  No register is written but m0; the loop waits for its
+// copies by their number.
 template <int BYTES>
 __device__ __forceinline__ void few4_copy(u32x4_t rows, int offset, void* base) {
   // the low half of a flat address of LDS is the place in it
   const uint32_t to = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)base);
   if constexpr (BYTES == 16)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 ::"v"(offset), "s"(rows), "s"(to) : "memory");
+                 ::"v"(offset), "s"(rows), "s"(to) : "m0", "memory");
   else
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 ::"v"(offset), "s"(rows), "s"(to) : "memory");
+                 ::"v"(offset), "s"(rows), "s"(to) : "m0", "memory");
 }
 __device__ __forceinline__ u32x4_t few4_rows(const void* p, int64_t bytes) {
   const uint64_t at = (uint64_t)p;

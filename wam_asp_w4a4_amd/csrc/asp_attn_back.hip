@@ -11,6 +11,11 @@
 // keys.  asp_attn.h has the layouts: as in the forward, the accumulators of p and ds are,
 // rounded to bf16 (half a step each, signs averaging out over the sums), the right
 // operands of the products that contract over them.
+//
+// Bound by the products and by what a wave's registers hold beside its sums: 4096 x 4096, 16 heads
+// of 128, dq in 206 us (1000 TFLOP/s of its three products; two waves a SIMD), dk and dv in 323
+// (850 of its four; their sums leave room for one wave a SIMD, and values kept in LDS for a
+// second wave spilled or took 341 us at best).
 #include "asp_attn.h"
 
 namespace asp {
