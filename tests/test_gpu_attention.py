@@ -595,6 +595,17 @@ def test_cache_parity(Tq, Tk, Hq, Hk, D, dtype):
     Case(Tq, Tk, Hq, Hk, D, dtype, qo, ko, [Tk // 4, Tk], 0.7, cache=True).check_forward()
 
 
+@pytest.mark.parametrize("mask", [None, 0.6])
+@pytest.mark.parametrize("Hq, Hk, D", [(32, 8, 128), (12, 4, 64), (4, 2, 64), (2, 2, 128)])
+def test_cache_heads_side_by_side_over_short_parts(Hq, Hk, D, mask):
+    """A serving step's sequences, from no key to many parts of four tiles."""
+    for n in (127, 128, 129, 700):
+        Case(1, n, Hq, Hk, D, "bf16", mask=mask, cache=True).check_forward()
+    lengths = [0, 1, 128, 300, 1030, 2000]
+    ko = [int(x) for x in np.cumsum([0] + lengths)]
+    Case(8, ko[-1] + 5, Hq, Hk, D, "bf16", [0, 1, 2, 3, 5, 6, 7], ko, [0, 1, 128, 257, 1030, 1999], mask, cache=True).check_forward()
+
+
 def test_cache_queries_of_any_size():
     """fp16 products: queries far outside its range are scaled."""
     for f in (1e-30, 1e-6, 1.0, 3e4, 1e30):

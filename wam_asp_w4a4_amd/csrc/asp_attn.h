@@ -493,7 +493,8 @@ struct AttnPlan {
   uint32_t chunk;
 };
 
-inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged) {
+inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, bool ragged,
+                          int waves = 4) {
   AttnPlan p;
   p.wide = attn_slots(held, 128, 1, false) * Hk >= 256;
   p.tile = p.wide ? 128 : 32;
@@ -510,6 +511,11 @@ inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, b
   p.chunk = (uint32_t)passed + 1u;
   if (blocks < target && (p.wide || blocks < 256)) {
     p.chunk = (uint32_t)std::max(least, (by * blocks + target - 1) / target);
+    // A head's `waves` of k_attn_few4, where fewer than four, have that many fewer rows until a workgroup
+    // a CU has some (one token over 2048 keys of 8 heads of 128: 15.5 us for 27.7; down to 64
+    // rows a wave, eight over 1024: 18.7 for 16.6; for 1024 workgroups, eight over 8192: 45 for 38)
+    if (waves < 4)
+      p.chunk = (uint32_t)std::max<int64_t>(128 * waves, std::min<int64_t>(p.chunk, by * blocks / 256));
     p.splits = (int)std::max<int64_t>(1, std::min((passed + p.chunk - 1) / p.chunk, most));
   }
   return p;

@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a) {
 
 // -------------------------------------------------------------------- host
 
-AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t heads, int32_t Hk, int32_t G, bool ragged) {
-  return attn_plan(Tq * (Hq / Hk), Tk, heads, G, ragged);
+AttnPlan plan_of(int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hk, int32_t G, bool ragged, int few = 1) {
+  return attn_plan(Tq * (Hq / Hk), Tk, Hk / few, G, ragged, 4 / few);
 }
 
 // Heads that a workgroup of k_attn_few4 has (0: the call is none of its).  Several where a
@@ -755,7 +755,7 @@ int32_t launch_attn(const AttnArgs& a, bool wide, bool deep, bool few4, hipStrea
 
 int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t workspace_bytes,
                  hipStream_t st) {
-  AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.Hk, a.G, a.qo != nullptr);
+  AttnPlan p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.G, a.qo != nullptr);
   const bool deep = dtype == ASP_BF16 && !q4 && attn_deep(a.Tq, a.Tk, a.Hq, a.Hk, a.D, a.qo != nullptr);
   if (deep) {
     p.splits = 1;
@@ -765,7 +765,7 @@ int32_t run_attn(AttnArgs& a, int32_t dtype, bool q4, void* workspace, size_t wo
   const int few = q4 && dtype == ASP_BF16 && !p.wide ? few4_heads(a.Tq * (a.Hq / a.Hk), a.G, a.Hk, a.D) : 0;
   if (few) {
     a.heads = a.Hk / few;
-    p = plan_of(a.Tq, a.Tk, a.Hq, a.heads, a.Hk, a.G, a.qo != nullptr);
+    p = plan_of(a.Tq, a.Tk, a.Hq, a.Hk, a.G, a.qo != nullptr, few);
   }
   const size_t need = part_bytes(p, a.Tq, a.Hq, a.D);
   if (need) ASP_TRY(check_ptr(workspace, "workspace", true));
@@ -798,11 +798,11 @@ int32_t asp_attention_workspace_bytes(int64_t Tq, int64_t Tk, int32_t Hq, int32_
   const int32_t some = 0;
   ASP_TRY(check_attn(ASP_F32, Tq, Tk, Hq, Hk, D, G, 1.0f, &some, &some, nullptr));
   if (!bytes) return fail(ASP_ERR_ARG, "null output pointer");
-  const AttnPlan p = plan_of(Tq, Tk, Hq, Hk, Hk, G, true);
+  const AttnPlan p = plan_of(Tq, Tk, Hq, Hk, G, true);
   *bytes = part_bytes(p, Tq, Hq, D);
   // a cache's, which may have more parts
   if (const int few = p.wide ? 0 : few4_heads(Tq * (Hq / Hk), G, Hk, D))
-    *bytes = std::max(*bytes, part_bytes(plan_of(Tq, Tk, Hq, Hk / few, Hk, G, true), Tq, Hq, D));
+    *bytes = std::max(*bytes, part_bytes(plan_of(Tq, Tk, Hq, Hk, G, true, few), Tq, Hq, D));
   return ASP_OK;
 }
 
