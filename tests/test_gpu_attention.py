@@ -346,6 +346,22 @@ def test_large_and_small_scores(dtype):
     assert o.isnan().all() and lse.isnan().all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, H", [(4, 3, 1), (40, 70, 256), (600, 600, 25)])
+def test_a_key_at_minus_infinity_has_no_gradients(Tq, Tk, H, dtype):
+    """Its weights are 0, in full tiles of queries and in the last one."""
+    case = Case(Tq, Tk, H, H, 72, dtype)
+    case.q.copy_(case.q.abs() + 1.0)
+    case.k[1] = -torch.inf
+    o, lse = attention(case.q, case.k, case.v)
+    g = attention_backward(case.do, case.q, case.k, case.v, o, lse, need=["dk", "dv"])
+    keys = torch.ones(Tk, dtype=torch.bool, device=DEV)
+    keys[1] = False
+    want = attention_backward(case.do, case.q, case.k, case.v, o, lse, key_mask=keys, need=["dk", "dv"])
+    assert not g.dk[1].any() and not g.dv[1].any()
+    assert torch.equal(g.dk, want.dk) and torch.equal(g.dv, want.dv) and g.dk.isfinite().all()
+
+
 def test_a_nan_query_stays_in_its_row():
     for Hq, Tk in ((4, 100), (2, 3000), (128, 100)):
         case = Case(70, Tk, Hq, Hq, 64, "bf16")

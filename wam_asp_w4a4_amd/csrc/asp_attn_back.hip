@@ -335,33 +335,37 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
   float* row_delta = row_log2 + 2 * BQ;
   constexpr int COPIES = TILE / 1024 / WN;
   static_assert(TILE % (1024 * WN) == 0, "whole copies for each wave");
-  int offq[COPIES], offd[COPIES];
+  // Rows past the end repeat the last one: with weights of 0 (zeros for a row would make NaN of a key at
+  // infinity, which has no weight in any row)
+  int row_of[COPIES], off[COPIES];
 #pragma unroll
   for (int i = 0; i < COPIES; ++i) {
-    const int row = R::row_of(wn * COPIES + i, lane), d = R::piece_of(wn * COPIES + i, lane) * (16 / P::ES);
-    offq[i] = d < a.D ? (row * (int)a.qt + d) * P::ES : kFar;
-    offd[i] = d < a.D ? (row * (int)a.gt + d) * P::ES : kFar;
+    const int d = R::piece_of(wn * COPIES + i, lane) * (16 / P::ES);
+    row_of[i] = R::row_of(wn * COPIES + i, lane);
+    off[i] = d < a.D ? d * P::ES : 1 << 30;  // past 64 rows' end, and below 2^31 with a row's offset
   }
+  const int stepq = (int)a.qt * P::ES, stepd = (int)a.gt * P::ES;
   float2 mine_row = make_float2(0.0f, 0.0f);
   auto issue = [&](int t) {
     uint8_t* to = mine + (t & (B::BUFFERS - 1)) * 2 * TILE;
-    const int64_t tile = first + (int64_t)t * WQ + wq;
-    const int64_t h = per_head ? (uint32_t)tile / (uint32_t)per_head : 0, row = (tile - h * per_head) * BQ;
-    const int64_t n = tile < last ? min((int64_t)BQ, seq.rows - row) : 0;
+    const int64_t at = first + (int64_t)t * WQ + wq, tile = min(at, last - 1);
+    const int64_t h = (uint32_t)tile / (uint32_t)per_head, row = (tile - h * per_head) * BQ;
+    const int n = (int)min((int64_t)BQ, seq.rows - row);
     const int head = hk * a.group + (int)h;
     const int64_t q = seq.q0 + row;
-    const auto rq = attn_rows(static_cast<const XT*>(a.q) + (n > 0 ? q * a.qt + head * a.qh : 0),
-                              n > 0 ? ((n - 1) * a.qt + a.D) * P::ES : 0);
-    const auto rd = attn_rows(static_cast<const XT*>(a.dout) + (n > 0 ? q * a.gt + head * a.gh : 0),
-                              n > 0 ? ((n - 1) * a.gt + a.D) * P::ES : 0);
+    const auto rq = attn_rows(static_cast<const XT*>(a.q) + q * a.qt + head * a.qh,
+                              ((n - 1) * a.qt + a.D) * P::ES);
+    const auto rd = attn_rows(static_cast<const XT*>(a.dout) + q * a.gt + head * a.gh,
+                              ((n - 1) * a.gt + a.D) * P::ES);
 #pragma unroll
     for (int i = 0; i < COPIES; ++i) {
-      attn_copy(rq, offq[i], to + (wn * COPIES + i) * 1024);
-      attn_copy(rd, offd[i], to + TILE + (wn * COPIES + i) * 1024);
+      const int r = min(row_of[i], n - 1);
+      attn_copy(rq, r * stepq + off[i], to + (wn * COPIES + i) * 1024);
+      attn_copy(rd, r * stepd + off[i], to + TILE + (wn * COPIES + i) * 1024);
     }
-    // rows past the end: weights of 0
+    // rows past the end, and a column's tile past the last: weights of 0
     mine_row = make_float2(-kNegInf, 0.0f);
-    if (wn == 0 && lane < n) mine_row = a.rows[(q + lane) * a.Hq + head];
+    if (wn == 0 && lane < n && at < last) mine_row = a.rows[(q + lane) * a.Hq + head];
   };
 
   if (turns > 0) issue(0);
