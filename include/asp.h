@@ -719,7 +719,7 @@ int32_t asp_head_norm_backward(const void* dq, int64_t lddq, int64_t hsdq, const
  *   q, o       device, Tq x Hq x D of `dtype`; k, v: Tk x Hk x D.  Heads are
  *              contiguous; token strides (ld, D to 2^22 elements) and head strides
  *              (hs) are multiples of 16 bytes.  o may be q itself (same strides)
- *   scale      above 0
+ *   scale      above 0, at most 1e38
  *   q_offsets, kv_offsets   device int32, G + 1 entries, not decreasing: sequence g
  *              has the queries q_offsets[g] .. q_offsets[g + 1] - 1 and the keys
  *              kv_offsets[g] .. (either may be none).  NULL (G = 1): all of them.

@@ -85,6 +85,15 @@ def test_attention_arguments(kw, want):
     status(lambda: attend(**kw), want)
 
 
+def test_scale_has_a_finite_factor():
+    """Past 2.3e38 the exponents' factor scale log2(e) would be infinite, and a score of 0 NaN."""
+    for scale in (2.0e38, 3.4e38):
+        status(lambda: attend(scale=scale), ARG)
+        with pytest.raises(ValueError, match="scale"):
+            Attention(scale)
+    assert Attention(1.0e38).scale == 1.0e38
+
+
 def cached(**kw):
     a = dict(q=P, ldq=128, hsq=64, dtype=1, k_codes=P, k_scales=P, v_codes=P, v_scales=P, Tq=4, Tk=5, Hq=2, Hk=2, D=64,
              scale=0.125, G=1, q_offsets=None, kv_offsets=None, kv_lengths=None, key_mask=None, o=P, ldo=128, hso=64,

@@ -74,8 +74,8 @@ def _check_keys(Tk, G, device, kv_lengths, key_mask):
 
 def _scale(scale, D):
     scale = D ** -0.5 if scale is None else float(scale)
-    if not 0.0 < scale < 3.0e38:
-        raise ValueError(f"scale must be above 0, not {scale}")
+    if not 0.0 < scale <= 1.0e38:
+        raise ValueError(f"scale must be above 0 and at most 1e38, not {scale}")
     return scale
 
 

@@ -459,7 +459,8 @@ inline int32_t check_attn(int32_t dtype, int64_t Tq, int64_t Tk, int32_t Hq, int
   if (D < 8 || D > kMaxAttnD || D % 8)
     return fail(ASP_ERR_SHAPE, "D=%d is not a multiple of 8 in [8, %d]", D, kMaxAttnD);
   if (G < 1 || G > 65535) return fail(ASP_ERR_SHAPE, "G=%d outside [1, 65535]", G);
-  if (!(scale > 0.0f) || !(scale < 3.0e38f)) return fail(ASP_ERR_ARG, "scale=%g", scale);
+  // (times log2(e) it has to be finite: a score of 0 stays 0)
+  if (!(scale > 0.0f) || !(scale <= 1.0e38f)) return fail(ASP_ERR_ARG, "scale=%g", scale);
   if (Tq * Hq > INT32_MAX || Tk * Hk > INT32_MAX)
     return fail(ASP_ERR_SHAPE, "%lld x %d or %lld x %d heads are not below 2^31", (long long)Tq, Hq,
                 (long long)Tk, Hk);
