@@ -223,6 +223,15 @@ def test_thousands_of_sequences():
     case.check_backward()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq, Tk, Hq, Hk, D", [(3, 2100, 6, 2, 40), (2, 1500, 30, 10, 72), (1500, 3, 5, 5, 64), (700, 1100, 7, 1, 128)])
+def test_parts_of_odd_head_counts(Tq, Tk, Hq, Hk, D, dtype):
+    """Few tokens' parts are summed by several waves a token."""
+    case = Case(Tq, Tk, Hq, Hk, D, dtype, mask=0.8)
+    case.check_forward()
+    case.check_backward()
+
+
 @pytest.mark.parametrize("cache", [False, True])
 def test_parts_among_many_sequences(cache):
     """One of a hundred sequences is long enough to be split."""

@@ -512,6 +512,10 @@ inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, b
   p.chunk = (uint32_t)passed + 1u;
   if (blocks < target && (p.wide || blocks < 256)) {
     p.chunk = (uint32_t)std::max(least, (by * blocks + target - 1) / target);
+    // one sequence: never a few workgroups more than the target, which would be a round of their own
+    // (777 x 1234, 8 heads of 64 over 2, 392 workgroups: 16 us, 588: 21; dk and dv, 468 and 546: 23
+    // and 30; 8 heads of 80 in float32: 57 and 70)
+    if (G == 1) p.chunk = (uint32_t)std::max<int64_t>(p.chunk, (passed + target / blocks - 1) / (target / blocks));
     // A head's `waves` of k_attn_few4, where fewer than four, have that many fewer rows until a workgroup
     // a CU has some (one token over 2048 keys of 8 heads of 128: 15.5 us for 27.7; down to 64
     // rows a wave, eight over 1024: 18.7 for 16.6; for 1024 workgroups, eight over 8192: 45 for 38)

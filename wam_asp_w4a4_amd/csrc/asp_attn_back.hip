@@ -431,7 +431,7 @@ __global__ void __launch_bounds__((BackKV<XT, DT, WN, WQ, QT>::THREADS))
 }
 
 // The parts' sums of dq, or of dk and dv (blockIdx.y), in order.  A wave has one token, its groups of 16
-// lanes a head each, 8 elements a lane.
+// lanes a head each, 8 elements a lane; few tokens have several waves (blockIdx.z) for their heads.
 struct SumArgs {
   AttnArgs a;
   const float* part[2];
@@ -462,8 +462,9 @@ __global__ void __launch_bounds__(256) k_attn_sum(const SumArgs s) {
   }
   const int parts = attn_parts(a, passed);
   if (parts == 1 || d >= a.D) return;
-  for (int h = lane >> 4; h < s.H; h += 4) {
+  for (int h = 4 * blockIdx.z + (lane >> 4); h < s.H; h += 4 * gridDim.z) {
     float v[8] = {};
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
       const f32x4_t* from =
           reinterpret_cast<const f32x4_t*>(s.part[which] + ((p * s.T + t) * s.H + h) * a.D + d);
@@ -524,8 +525,9 @@ int32_t launch_dkv(const AttnArgs& a, hipStream_t st) {
 template <typename XT>
 int32_t launch_sum(const SumArgs& s, int tensors, hipStream_t st) {
   const int64_t blocks = (s.T + 3) / 4;
-  ASP_TRY(check_attn_grid(blocks * tensors, 256));
-  k_attn_sum<XT><<<dim3((unsigned)blocks, tensors), 256, 0, st>>>(s);
+  const int heads = (int)std::min<int64_t>((s.H + 3) / 4, std::max<int64_t>(1, 2048 / blocks));
+  ASP_TRY(check_attn_grid(blocks * tensors * heads, 256));
+  k_attn_sum<XT><<<dim3((unsigned)blocks, tensors, heads), 256, 0, st>>>(s);
   return launch_status("attention sums");
 }
 
