@@ -13,7 +13,7 @@
 // operands of the products that contract over them.
 //
 // Bound by the products and by what a wave's registers hold beside its sums: 4096 x 4096, 16 heads
-// of 128, dq in 206 us (1000 TFLOP/s of its three products; two waves a SIMD), dk and dv in 323
+// of 128, dq in 206 us (1000 TFLOP/s of its three products; two waves a SIMD), dk and dv in 320
 // (850 of its four; their sums leave room for one wave a SIMD, and values kept in LDS for a
 // second wave spilled or took 341 us at best).
 #include "asp_attn.h"
