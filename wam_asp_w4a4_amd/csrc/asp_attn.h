@@ -505,7 +505,8 @@ inline AttnPlan attn_plan(int64_t held, int64_t passed, int32_t Hk, int32_t G, b
   const int64_t by = std::max<int64_t>(1, passed / G);
   // A range is split where that makes so many workgroups, and ragged sequences more, since the longest
   // would be alone at the end; but from `least` rows on only, since a part's result is written
-  // and read again in float32.
+  // and read again in float32.  (Ragged, 512 workgroups for 1024: 4096 x 4096 in five sequences, 16
+  // heads of 64, dq in 74 us for 49; 1536: 8192 x 8192 in four, 16 heads of 128, forward 227 for 160.)
   const int64_t target = G > 1 ? 1024 : p.wide ? 0 : 512, least = p.wide ? 1024 : 512;
   const int64_t most = p.wide ? 8 : std::min<int64_t>(512, 4 * target / blocks);
   p.splits = 1;
